@@ -305,6 +305,99 @@ mla_status mla_decode_v_up(mla_dtype dtype, mla_tensor out, float* lse_out, mla_
 size_t mla_decode_v_up_workspace_size(int32_t batch, int32_t num_heads, int32_t kv_lora_rank,
                                       int32_t num_splits);
 
+/* Step 3, ds_mla cache - the cache write into the fp8 ds_mla entries that
+ * mla_decode_sparse_fp8 reads ([vllm] concat_and_cache_mla into an fp8 ds_mla cache; the
+ * page gives the entry's layout, the quantisation rule is this library's).
+ *   cache [num_blocks, page, 656] byte view (strides in bytes, any stride(0) and storage
+ *   offset), data and strides 16-byte aligned; kv_c [T,512] and k_pe [T,64] in src_dtype,
+ *   any row stride; slot_mapping: device int64 [num_tokens].
+ *   For token i with s = slot_mapping[i] >= 0, entry s becomes
+ *     scale g    = max(max |kv_c[i, 128g .. 128g+127]| / 448, 2^-126)   (float32)
+ *     code c     = e4m3(kv_c[i,c] / scale[c / 128])   (the division correctly rounded in
+ *                  float32, the code to nearest with ties to even, saturating)
+ *     rope       = k_pe[i] (bf16, rounded to nearest even from float32).
+ *   An infinity counts as the largest float32 in the maximum and becomes a code of +-448;
+ *   a NaN does not count and becomes the NaN code. Padding slots, out-of-range slots, the
+ *   untouched entries and duplicate slots: as mla_cache_write. */
+mla_status mla_cache_write_ds_mla(mla_dtype src_dtype, mla_tensor cache, mla_tensor kv_c,
+                                  mla_tensor k_pe, const int64_t* slot_mapping, int64_t num_tokens,
+                                  void* stream);
+
+/* Read-back - rows of a paged cache gathered into contiguous rows [c_kv | k_pe], the
+ * inverse of the cache writes (what a chunk of prefill over a quantised or shared prefix
+ * begins with: the rows read back are a cache for mla_prefill and mla_prefill_window). The
+ * source pages have no counterpart of these calls.
+ *   out [T,W] (written; any row stride), W values a row; cache as in the writes;
+ *   block_table: device int32 [batch, max_blocks] with row stride block_table_stride;
+ *   cu_seqlens: device int32 [batch+1], ascending; seq_starts: device int32 [batch] or NULL
+ *   (all zero).
+ *   Row i of out with cu_seqlens[b] <= i < cu_seqlens[b+1] becomes row
+ *   seq_starts[b] + i - cu_seqlens[b] of sequence b (block block_table[b, row / page],
+ *   offset row % page). Rows of out before cu_seqlens[0], at or behind cu_seqlens[batch]
+ *   are left as they were. A row whose position or block id lies outside the table or the
+ *   cache is left as it was and reported by mla_device_error (MLA_ERR_DEVICE_DATA). out must
+ *   not overlap the cache.
+ *   mla_cache_read: a cache of `dtype` [num_blocks, page, W], bits unchanged.
+ *   mla_cache_read_fp8: e4m3 codes [num_blocks, page, W] (strides in bytes); a value is its
+ *   code's value times *scale (device float [1]) in float32, rounded once to dst_dtype.
+ *   mla_cache_read_ds_mla: W = 576; latent values are code * scale[column / 128] in float32,
+ *   rounded once to dst_dtype, rope values the stored ones; cache as in
+ *   mla_cache_write_ds_mla. */
+mla_status mla_cache_read(mla_dtype dtype, mla_tensor out, mla_tensor cache,
+                          const int32_t* block_table, int64_t block_table_stride,
+                          int32_t max_blocks, const int32_t* cu_seqlens, const int32_t* seq_starts,
+                          int32_t batch, void* stream);
+mla_status mla_cache_read_fp8(mla_dtype dst_dtype, mla_tensor out, mla_tensor cache,
+                              const int32_t* block_table, int64_t block_table_stride,
+                              int32_t max_blocks, const int32_t* cu_seqlens,
+                              const int32_t* seq_starts, int32_t batch, const float* scale,
+                              void* stream);
+mla_status mla_cache_read_ds_mla(mla_dtype dst_dtype, mla_tensor out, mla_tensor cache,
+                                 const int32_t* block_table, int64_t block_table_stride,
+                                 int32_t max_blocks, const int32_t* cu_seqlens,
+                                 const int32_t* seq_starts, int32_t batch, void* stream);
+
+/* Step 4, windowed - the decode limited to a sliding window and attention sinks. The source
+ * pages have no counterpart of this call.
+ *   Arguments, results and errors as mla_decode, except: the query of sequence b, at position
+ *   p = seq_lens[b] - 1, attends the rows t <= p with t < sinks or t > p - window (window >= 1
+ *   rows ending with its own, and the sequence's first `sinks` >= 0 rows). Rows outside are
+ *   never used, whatever they hold, and the block ids of pages without an attended row are not
+ *   read: such pages may have been freed.
+ *   workspace: at least mla_decode_window_workspace_size(...) bytes, 256-byte aligned,
+ *   caller-owned, not used by concurrent calls. */
+mla_status mla_decode_window(mla_dtype dtype, mla_tensor o_lat_out, float* lse_out,
+                             mla_tensor q_cat, mla_tensor cache, const int32_t* block_table,
+                             int64_t block_table_stride, int32_t max_blocks,
+                             const int32_t* seq_lens, int32_t kv_lora_rank, int32_t rope_dim,
+                             float softmax_scale, int32_t window, int32_t sinks,
+                             int32_t num_splits, void* workspace, size_t workspace_bytes,
+                             void* stream);
+size_t mla_decode_window_workspace_size(int32_t batch, int32_t num_heads, int32_t kv_lora_rank,
+                                        int32_t num_splits);
+
+/* Step 4, prefill, windowed - causal attention of a chunk of tokens per sequence over the
+ * paged cache, limited to a sliding window and attention sinks. The source pages have no
+ * counterpart of this call.
+ *   Arguments and results as mla_prefill (without max_q_len), except: a query at position p
+ *   attends the rows t <= p with t < sinks or t > p - window. A query at a negative position
+ *   (a chunk longer than its cache) attends nothing: o = 0, lse = -inf. Rows of q_cat outside
+ *   every sequence (before cu_seqlens_q[0], at or behind cu_seqlens_q[batch]) leave their rows
+ *   of o_lat_out and lse_out as they were. Rows that no query of the chunk attends are never
+ *   used, whatever they hold, and the block ids of pages without an attended row are not read;
+ *   a row that some query of the chunk attends must hold finite values.
+ *   workspace: at least mla_prefill_window_workspace_size(tokens, ...) bytes (tokens = rows of
+ *   q_cat), 256-byte aligned, caller-owned, not used by concurrent calls. */
+mla_status mla_prefill_window(mla_dtype dtype, mla_tensor o_lat_out, float* lse_out,
+                              mla_tensor q_cat, mla_tensor cache, const int32_t* block_table,
+                              int64_t block_table_stride, int32_t max_blocks,
+                              const int32_t* cu_seqlens_q, const int32_t* seq_lens_kv,
+                              int32_t batch, int32_t kv_lora_rank, int32_t rope_dim,
+                              float softmax_scale, int32_t window, int32_t sinks,
+                              void* workspace, size_t workspace_bytes, void* stream);
+size_t mla_prefill_window_workspace_size(int32_t tokens, int32_t batch, int32_t num_heads,
+                                         int32_t kv_lora_rank);
+
 /* Bytes of the static scratch behind mla_decode_noalloc (40 MiB). */
 #define MLA_DECODE_NOALLOC_SCRATCH_BYTES (40u * 1024u * 1024u)
 

@@ -73,6 +73,16 @@ def lib() -> ctypes.CDLL:
             "mla_decode_v_up": ([ctypes.c_int, T, P, T, T, P, I64, I32, P, I32, I32, F32, T, I32, P, SZ, P],
                                 ctypes.c_int),
             "mla_decode_v_up_workspace_size": ([I32, I32, I32, I32], SZ),
+            "mla_cache_write_ds_mla": ([ctypes.c_int, T, T, T, P, I64, P], ctypes.c_int),
+            "mla_cache_read": ([ctypes.c_int, T, T, P, I64, I32, P, P, I32, P], ctypes.c_int),
+            "mla_cache_read_fp8": ([ctypes.c_int, T, T, P, I64, I32, P, P, I32, P, P], ctypes.c_int),
+            "mla_cache_read_ds_mla": ([ctypes.c_int, T, T, P, I64, I32, P, P, I32, P], ctypes.c_int),
+            "mla_decode_window": ([ctypes.c_int, T, P, T, T, P, I64, I32, P, I32, I32, F32, I32, I32, I32, P, SZ, P],
+                                  ctypes.c_int),
+            "mla_decode_window_workspace_size": ([I32, I32, I32, I32], SZ),
+            "mla_prefill_window": ([ctypes.c_int, T, P, T, T, P, I64, I32, P, P, I32, I32, I32, F32, I32, I32, P, SZ,
+                                    P], ctypes.c_int),
+            "mla_prefill_window_workspace_size": ([I32, I32, I32, I32], SZ),
             "mla_device_error": ([P], ctypes.c_int),
             "mla_check_bounded_wait": ([ctypes.c_uint32, P], ctypes.c_int),
         }
@@ -379,6 +389,165 @@ def mla_decode_noalloc(o_lat_out, q_cat, cache, block_table, seq_lens, kv_lora_r
                                     block_table.data_ptr(), block_table.stride(0), block_table.shape[1],
                                     seq_lens.data_ptr(), kv_lora_rank, rope_dim, softmax_scale,
                                     num_splits, _stream(stream)))
+
+
+def _check_device(*tensors) -> None:
+    """Every tensor on one CUDA device, and that the current one: the library launches there."""
+    import torch
+    devices = {t.device for t in tensors if t is not None}
+    if len(devices) != 1 or next(iter(devices)).type != "cuda":
+        raise MlaError(MLA_ERR_INVALID_ARG, f"tensors must share one CUDA device: {sorted(map(str, devices))}")
+    device = devices.pop()
+    if device.index != torch.cuda.current_device():
+        raise MlaError(MLA_ERR_INVALID_ARG, f"tensors are on {device}, the current device is "
+                                            f"cuda:{torch.cuda.current_device()}")
+
+
+def _check_slots(slot_mapping) -> None:
+    import torch
+    if slot_mapping.dtype != torch.int64 or slot_mapping.dim() != 1:
+        raise MlaError(MLA_ERR_INVALID_ARG, "slot_mapping must be int64 [T]")
+    if slot_mapping.numel() and not slot_mapping.is_contiguous():
+        raise MlaError(MLA_ERR_INVALID_ARG, "slot_mapping must be contiguous")
+
+
+def _check_counts(t, n: int, name: str) -> None:
+    import torch
+    if t.dtype != torch.int32 or t.dim() != 1 or t.numel() != n or not t.is_contiguous():
+        raise MlaError(MLA_ERR_INVALID_ARG, f"{name} must be contiguous int32 [{n}]")
+
+
+def _check_table(block_table, batch: int) -> None:
+    import torch
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != batch:
+        raise MlaError(MLA_ERR_INVALID_ARG, f"block_table must be int32 [{batch}, max_blocks]")
+    if block_table.numel() and block_table.stride(1) != 1:
+        raise MlaError(MLA_ERR_INVALID_ARG, "block_table must have unit column stride")
+
+
+def _table_stride(block_table) -> int:
+    """Row stride of a block table (a single row's stride is arbitrary in torch: its width serves)."""
+    return block_table.stride(0) if block_table.shape[0] > 1 else block_table.shape[1]
+
+
+def _check_lse(lse_out, q_cat) -> None:
+    import torch
+    if lse_out is not None and (lse_out.dtype != torch.float32 or not lse_out.is_contiguous() or
+                                tuple(lse_out.shape) != tuple(q_cat.shape[:2])):
+        raise MlaError(MLA_ERR_INVALID_ARG, "lse_out must be contiguous float32 with q_cat's rows and heads")
+
+
+def _scratch(workspace, need: int, like, stream):
+    """The caller's workspace, or one allocated on the stream the call runs on (so that its memory
+    is reused only behind the call's work)."""
+    import torch
+    if workspace is not None:
+        _check_device(workspace, like)
+        if not workspace.is_contiguous():
+            raise MlaError(MLA_ERR_INVALID_ARG, "workspace must be contiguous")
+        return workspace
+    if stream is None:
+        return torch.empty(need, dtype=torch.uint8, device=like.device)
+    on = torch.cuda.ExternalStream(_stream(stream), device=like.device)
+    with torch.cuda.stream(on):
+        return torch.empty(need, dtype=torch.uint8, device=like.device)
+
+
+def _ds_mla_cache(cache):
+    import torch
+    if cache.dtype != torch.uint8:
+        raise MlaError(MLA_ERR_INVALID_ARG, "a ds_mla cache is uint8 bytes")
+    return cache[:, :, 0] if cache.dim() == 4 and cache.shape[2] == 1 else cache
+
+
+def mla_cache_write_ds_mla(cache, kv_c, k_pe, slot_mapping, stream=None) -> None:
+    """Step 3 into fp8 ds_mla entries: entry s of a uint8 [num_blocks, page, 656] (or
+    [num_blocks, page, 1, 656]) cache = kv_c[i] as e4m3 codes with a float32 scale per 128
+    columns, and k_pe[i] as bf16, for s = slot_mapping[i] >= 0; kv_c [T,512], k_pe [T,64]."""
+    cache = _ds_mla_cache(cache)
+    _check_slots(slot_mapping)
+    _check_device(cache, kv_c, k_pe, slot_mapping)
+    _check(lib().mla_cache_write_ds_mla(_dtype_code(kv_c, k_pe), as_mla_tensor(cache), as_mla_tensor(kv_c),
+                                        as_mla_tensor(k_pe), _ptr(slot_mapping), slot_mapping.numel(),
+                                        _stream(stream)))
+
+
+def _read_args(out, cache, block_table, cu_seqlens, seq_starts):
+    batch = block_table.shape[0]
+    _check_table(block_table, batch)
+    _check_counts(cu_seqlens, batch + 1, "cu_seqlens")
+    if seq_starts is not None:
+        _check_counts(seq_starts, batch, "seq_starts")
+    _check_device(out, cache, block_table, cu_seqlens, seq_starts)
+    return (as_mla_tensor(out), as_mla_tensor(cache), _ptr(block_table), _table_stride(block_table),
+            block_table.shape[1], _ptr(cu_seqlens), _ptr(seq_starts), batch)
+
+
+def mla_cache_read(out, cache, block_table, cu_seqlens, seq_starts=None, stream=None) -> None:
+    """Read-back of a plain cache: out[i] = row seq_starts[b] + i - cu_seqlens[b] of sequence b for
+    cu_seqlens[b] <= i < cu_seqlens[b+1]; out [T,W], bits unchanged, other rows left as they were."""
+    args = _read_args(out, cache, block_table, cu_seqlens, seq_starts)
+    _check(lib().mla_cache_read(_dtype_code(out, cache), *args, _stream(stream)))
+
+
+def mla_cache_read_fp8(out, cache, block_table, cu_seqlens, scale, seq_starts=None, stream=None) -> None:
+    """Read-back of an e4m3 cache: as mla_cache_read, a value = its code's value * scale, in out's dtype."""
+    cache = _fp8_cache(cache)
+    args = _read_args(out, cache, block_table, cu_seqlens, seq_starts)
+    _check_device(out, scale)
+    _check(lib().mla_cache_read_fp8(_dtype_code(out), *args, _f32_scalar(scale, "scale"), _stream(stream)))
+
+
+def mla_cache_read_ds_mla(out, cache, block_table, cu_seqlens, seq_starts=None, stream=None) -> None:
+    """Read-back of a ds_mla cache: as mla_cache_read with 576 values a row, [code * scale | rope]."""
+    cache = _ds_mla_cache(cache)
+    args = _read_args(out, cache, block_table, cu_seqlens, seq_starts)
+    _check(lib().mla_cache_read_ds_mla(_dtype_code(out), *args, _stream(stream)))
+
+
+def mla_decode_window_workspace_size(batch: int, num_heads: int, kv_lora_rank: int, num_splits: int = 0) -> int:
+    return int(lib().mla_decode_window_workspace_size(batch, num_heads, kv_lora_rank, num_splits))
+
+
+def mla_decode_window(o_lat_out, q_cat, cache, block_table, seq_lens, kv_lora_rank: int, rope_dim: int,
+                      softmax_scale: float, window: int, sinks: int = 0, lse_out=None, num_splits: int = 0,
+                      workspace=None, stream=None) -> None:
+    """Step 4, windowed: mla_decode over the last `window` rows of each sequence and its first `sinks` rows."""
+    B, H = q_cat.shape[0], q_cat.shape[1]
+    _check_table(block_table, B)
+    _check_counts(seq_lens, B, "seq_lens")
+    _check_lse(lse_out, q_cat)
+    _check_device(o_lat_out, q_cat, cache, block_table, seq_lens, lse_out)
+    workspace = _scratch(workspace, mla_decode_window_workspace_size(B, H, kv_lora_rank, num_splits), q_cat, stream)
+    _check(lib().mla_decode_window(_dtype_code(o_lat_out, q_cat, cache), as_mla_tensor(o_lat_out), _ptr(lse_out),
+                                   as_mla_tensor(q_cat), as_mla_tensor(cache), _ptr(block_table),
+                                   _table_stride(block_table), block_table.shape[1], _ptr(seq_lens), kv_lora_rank,
+                                   rope_dim, softmax_scale, window, sinks, num_splits, workspace.data_ptr(),
+                                   workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def mla_prefill_window_workspace_size(tokens: int, batch: int, num_heads: int, kv_lora_rank: int) -> int:
+    return int(lib().mla_prefill_window_workspace_size(tokens, batch, num_heads, kv_lora_rank))
+
+
+def mla_prefill_window(o_lat_out, q_cat, cache, block_table, cu_seqlens_q, seq_lens_kv, kv_lora_rank: int,
+                       rope_dim: int, softmax_scale: float, window: int, sinks: int = 0, lse_out=None,
+                       workspace=None, stream=None) -> None:
+    """Step 4 (prefill), windowed: each query attends the last `window` rows up to its own and its
+    sequence's first `sinks` rows."""
+    batch, T, H = seq_lens_kv.numel(), q_cat.shape[0], q_cat.shape[1]
+    _check_table(block_table, batch)
+    _check_counts(seq_lens_kv, batch, "seq_lens_kv")
+    _check_counts(cu_seqlens_q, batch + 1, "cu_seqlens_q")
+    _check_lse(lse_out, q_cat)
+    _check_device(o_lat_out, q_cat, cache, block_table, cu_seqlens_q, seq_lens_kv, lse_out)
+    workspace = _scratch(workspace, mla_prefill_window_workspace_size(T, batch, H, kv_lora_rank), q_cat, stream)
+    _check(lib().mla_prefill_window(_dtype_code(o_lat_out, q_cat, cache), as_mla_tensor(o_lat_out), _ptr(lse_out),
+                                    as_mla_tensor(q_cat), as_mla_tensor(cache), _ptr(block_table),
+                                    _table_stride(block_table), block_table.shape[1], _ptr(cu_seqlens_q),
+                                    _ptr(seq_lens_kv), batch, kv_lora_rank, rope_dim, softmax_scale, window, sinks,
+                                    workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                    _stream(stream)))
 
 
 def mla_check_bounded_wait(limit_us: int, stream=None) -> None:

@@ -705,6 +705,199 @@ mla_status mla_prefill(mla_dtype dtype, mla_tensor o_lat_out, float* lse_out, ml
                      "mla_prefill");
 }
 
+// ---- the ds_mla cache write and the read-backs --------------------------------------------
+
+namespace {
+// A ds_mla cache view: 656-byte entries, 16-byte aligned data and strides.
+mla_status check_ds_mla_cache(const mla_tensor& cache) {
+  MLA_TRY(check_cache(cache, kDsMlaEntry, "cache"));
+  if (reinterpret_cast<uintptr_t>(cache.data) % 16 != 0 || cache.stride[0] % 16 != 0 || cache.stride[1] % 16 != 0)
+    return fail(MLA_ERR_INVALID_ARG, "cache: data and strides must be 16-byte aligned");
+  return MLA_OK;
+}
+
+// The checks shared by the three read-backs, `width` values a row; *r is complete but for an
+// empty read (*empty).
+mla_status plan_read(mla_dtype dtype, const mla_tensor& out, int64_t width, const mla_tensor& cache,
+                     const int32_t* block_table, int64_t block_table_stride, int32_t max_blocks,
+                     const int32_t* cu_seqlens, const int32_t* seq_starts, int32_t batch, CacheRead* r, bool* empty) {
+  MLA_TRY(check_dtype(dtype));
+  MLA_TRY(check_view(out, 2, "out"));
+  if (out.shape[1] != width)
+    return fail(MLA_ERR_INVALID_ARG, "out width %lld, a cache row holds %lld values", (long long)out.shape[1],
+                (long long)width);
+  if (batch < 0) return fail(MLA_ERR_INVALID_ARG, "batch < 0");
+  if (cache.shape[2] > INT32_MAX) return fail(MLA_ERR_UNSUPPORTED, "cache: entry too wide");
+  *empty = numel(out) == 0 || batch == 0;
+  if (*empty) return MLA_OK;
+  if (out.shape[0] > INT32_MAX) return fail(MLA_ERR_UNSUPPORTED, "more rows than cu_seqlens can count");
+  if (block_table == nullptr || cu_seqlens == nullptr)
+    return fail(MLA_ERR_INVALID_ARG, "block_table and cu_seqlens must be non-null");
+  if (max_blocks <= 0 || block_table_stride < max_blocks)
+    return fail(MLA_ERR_INVALID_ARG, "need 0 < max_blocks <= block_table_stride");
+  *r = CacheRead{out.data, out.stride[0], out.shape[0],
+                 CacheView{cache.data, cache.stride[0], cache.stride[1], (int32_t)cache.shape[0],
+                           (int32_t)cache.shape[1], (int32_t)cache.shape[2]},
+                 block_table, block_table_stride, max_blocks, cu_seqlens, seq_starts, batch};
+  return MLA_OK;
+}
+}  // namespace
+
+mla_status mla_cache_write_ds_mla(mla_dtype src_dtype, mla_tensor cache, mla_tensor kv_c, mla_tensor k_pe,
+                                  const int64_t* slot_mapping, int64_t num_tokens, void* stream) {
+  g_msg[0] = 0;
+  MLA_TRY(check_dtype(src_dtype));
+  if (num_tokens < 0) return fail(MLA_ERR_INVALID_ARG, "num_tokens < 0");
+  MLA_TRY(check_view(kv_c, 2, "kv_c"));
+  MLA_TRY(check_view(k_pe, 2, "k_pe"));
+  if (kv_c.shape[1] != kDsMlaLatent || k_pe.shape[1] != kDsMlaRope)
+    return fail(MLA_ERR_INVALID_ARG, "a ds_mla entry takes kv_c [T,512] and k_pe [T,64], got widths %lld and %lld",
+                (long long)kv_c.shape[1], (long long)k_pe.shape[1]);
+  MLA_TRY(check_ds_mla_cache(cache));
+  if (kv_c.shape[0] != num_tokens || k_pe.shape[0] != num_tokens)
+    return fail(MLA_ERR_INVALID_ARG, "kv_c/k_pe rows (%lld/%lld) != num_tokens %lld",
+                (long long)kv_c.shape[0], (long long)k_pe.shape[0], (long long)num_tokens);
+  if (num_tokens == 0) return MLA_OK;
+  if (slot_mapping == nullptr) return fail(MLA_ERR_INVALID_ARG, "slot_mapping is null");
+  const View3 kc{kv_c.data, kv_c.shape[0], 1, kv_c.shape[1], kv_c.stride[0], 0, 1};
+  const View3 kp{k_pe.data, k_pe.shape[0], 1, k_pe.shape[1], k_pe.stride[0], 0, 1};
+  return cuda_status(launch_cache_write_ds_mla(src_dtype, view3(cache), kc, kp, slot_mapping, num_tokens,
+                                               (cudaStream_t)stream),
+                     "mla_cache_write_ds_mla");
+}
+
+mla_status mla_cache_read(mla_dtype dtype, mla_tensor out, mla_tensor cache, const int32_t* block_table,
+                          int64_t block_table_stride, int32_t max_blocks, const int32_t* cu_seqlens,
+                          const int32_t* seq_starts, int32_t batch, void* stream) {
+  g_msg[0] = 0;
+  MLA_TRY(check_cache(cache, out.rank == 2 ? out.shape[1] : 0, "cache"));
+  CacheRead r;
+  bool empty;
+  MLA_TRY(plan_read(dtype, out, cache.shape[2], cache, block_table, block_table_stride, max_blocks, cu_seqlens,
+                    seq_starts, batch, &r, &empty));
+  if (empty) return MLA_OK;
+  return cuda_status(launch_cache_read(dtype, r, (cudaStream_t)stream), "mla_cache_read");
+}
+
+mla_status mla_cache_read_fp8(mla_dtype dst_dtype, mla_tensor out, mla_tensor cache, const int32_t* block_table,
+                              int64_t block_table_stride, int32_t max_blocks, const int32_t* cu_seqlens,
+                              const int32_t* seq_starts, int32_t batch, const float* scale, void* stream) {
+  g_msg[0] = 0;
+  MLA_TRY(check_cache(cache, out.rank == 2 ? out.shape[1] : 0, "cache"));
+  CacheRead r;
+  bool empty;
+  MLA_TRY(plan_read(dst_dtype, out, cache.shape[2], cache, block_table, block_table_stride, max_blocks, cu_seqlens,
+                    seq_starts, batch, &r, &empty));
+  if (empty) return MLA_OK;
+  if (scale == nullptr) return fail(MLA_ERR_INVALID_ARG, "scale is null");
+  return cuda_status(launch_cache_read_fp8(dst_dtype, r, scale, (cudaStream_t)stream), "mla_cache_read_fp8");
+}
+
+mla_status mla_cache_read_ds_mla(mla_dtype dst_dtype, mla_tensor out, mla_tensor cache, const int32_t* block_table,
+                                 int64_t block_table_stride, int32_t max_blocks, const int32_t* cu_seqlens,
+                                 const int32_t* seq_starts, int32_t batch, void* stream) {
+  g_msg[0] = 0;
+  MLA_TRY(check_ds_mla_cache(cache));
+  CacheRead r;
+  bool empty;
+  MLA_TRY(plan_read(dst_dtype, out, kDsMlaLatent + kDsMlaRope, cache, block_table, block_table_stride, max_blocks,
+                    cu_seqlens, seq_starts, batch, &r, &empty));
+  if (empty) return MLA_OK;
+  return cuda_status(launch_cache_read_ds_mla(dst_dtype, r, (cudaStream_t)stream), "mla_cache_read_ds_mla");
+}
+
+// ---- attention limited to a window and sinks -----------------------------------------------
+
+namespace {
+mla_status check_window(int32_t window, int32_t sinks) {
+  if (window <= 0) return fail(MLA_ERR_INVALID_ARG, "window must be > 0, got %d", window);
+  if (sinks < 0) return fail(MLA_ERR_INVALID_ARG, "sinks must be >= 0, got %d", sinks);
+  return MLA_OK;
+}
+
+mla_status check_workspace(const void* workspace, size_t have, size_t need) {
+  if (workspace == nullptr || have < need)
+    return fail(MLA_ERR_INVALID_ARG, "workspace too small: %zu bytes, need %zu", have, need);
+  if (reinterpret_cast<uintptr_t>(workspace) % 256 != 0)
+    return fail(MLA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  return MLA_OK;
+}
+
+// mla_decode_window's workspace: mla_decode's layout, then the visible lengths [B].
+struct WindowWs {
+  DecodeWsLayout lay;
+  size_t off_visible, total;
+};
+WindowWs window_ws(int64_t B, int64_t H, int64_t L, int32_t units) {
+  WindowWs w;
+  w.lay = decode_ws_layout(B, H, L, units);
+  auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+  w.off_visible = up(w.lay.total);
+  w.total = up(w.off_visible + (size_t)B * sizeof(int32_t));
+  return w;
+}
+}  // namespace
+
+size_t mla_decode_window_workspace_size(int32_t batch, int32_t num_heads, int32_t kv_lora_rank, int32_t num_splits) {
+  if (batch < 0 || num_heads < 0 || kv_lora_rank < 0 || num_splits < 0) return 0;
+  return window_ws(batch, num_heads, kv_lora_rank, decode_units(num_splits)).total;
+}
+
+mla_status mla_decode_window(mla_dtype dtype, mla_tensor o_lat_out, float* lse_out, mla_tensor q_cat,
+                             mla_tensor cache, const int32_t* block_table, int64_t block_table_stride,
+                             int32_t max_blocks, const int32_t* seq_lens, int32_t kv_lora_rank, int32_t rope_dim,
+                             float softmax_scale, int32_t window, int32_t sinks, int32_t num_splits, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  g_msg[0] = 0;
+  DecodeCall dc;
+  MLA_TRY(check_window(window, sinks));
+  MLA_TRY(check_decode_args(dtype, o_lat_out, q_cat, cache, block_table, block_table_stride, max_blocks,
+                            seq_lens, kv_lora_rank, rope_dim, softmax_scale, num_splits, &dc));
+  if (dc.empty) return MLA_OK;
+  const WindowWs ws = window_ws(dc.B, dc.H, dc.L, decode_units(num_splits));
+  MLA_TRY(check_workspace(workspace, workspace_bytes, ws.total));
+  const cudaStream_t st = (cudaStream_t)stream;
+  const int32_t B = (int32_t)dc.B, H = (int32_t)dc.H, L = (int32_t)dc.L, R = (int32_t)dc.R;
+  const WindowArgs w{window, sinks};
+  // each sequence's visible rows, then the split-KV decode over that many
+  int32_t* visible = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + ws.off_visible);
+  const DecodeSched s = decode_sched_from_ws(workspace, ws.lay, B, decode_units(num_splits));
+  MLA_TRY(cuda_status(launch_window_lens(seq_lens, B, max_blocks, dc.cv.page, w, visible, st),
+                      "mla_decode_window lengths"));
+  MLA_TRY(cuda_status(launch_decode_schedule(visible, B, max_blocks, dc.cv.page, s, st), "mla_decode_window schedule"));
+  MLA_TRY(cuda_status(launch_decode_window_simt(dtype, dc.ov, lse_out, dc.qv, dc.cv, block_table, block_table_stride,
+                                                max_blocks, seq_lens, visible, B, H, L, R, softmax_scale, w, s, st),
+                      "mla_decode_window split kernel"));
+  return cuda_status(launch_decode_combine(dtype, dc.ov, lse_out, visible, B, H, L, s, st), "mla_decode_window combine");
+}
+
+size_t mla_prefill_window_workspace_size(int32_t tokens, int32_t batch, int32_t num_heads, int32_t kv_lora_rank) {
+  if (tokens < 0 || batch < 0 || num_heads < 0 || kv_lora_rank < 0) return 0;
+  return 256;
+}
+
+mla_status mla_prefill_window(mla_dtype dtype, mla_tensor o_lat_out, float* lse_out, mla_tensor q_cat,
+                              mla_tensor cache, const int32_t* block_table, int64_t block_table_stride,
+                              int32_t max_blocks, const int32_t* cu_seqlens_q, const int32_t* seq_lens_kv,
+                              int32_t batch, int32_t kv_lora_rank, int32_t rope_dim, float softmax_scale,
+                              int32_t window, int32_t sinks, void* workspace, size_t workspace_bytes, void* stream) {
+  g_msg[0] = 0;
+  MLA_TRY(check_window(window, sinks));
+  if (batch < 0) return fail(MLA_ERR_INVALID_ARG, "batch < 0");
+  // the views and tables are a decode's, with one query row a token
+  DecodeCall dc;
+  MLA_TRY(check_decode_args(dtype, o_lat_out, q_cat, cache, block_table, block_table_stride, max_blocks,
+                            seq_lens_kv, kv_lora_rank, rope_dim, softmax_scale, 0, &dc));
+  if (dc.empty || batch == 0) return MLA_OK;
+  if (cu_seqlens_q == nullptr) return fail(MLA_ERR_INVALID_ARG, "cu_seqlens_q must be non-null");
+  const int32_t T = (int32_t)dc.B, H = (int32_t)dc.H, L = (int32_t)dc.L, R = (int32_t)dc.R;
+  MLA_TRY(check_workspace(workspace, workspace_bytes, mla_prefill_window_workspace_size(T, batch, H, L)));
+  return cuda_status(launch_prefill_window_simt(dtype, dc.ov, lse_out, dc.qv, dc.cv, block_table, block_table_stride,
+                                                max_blocks, cu_seqlens_q, seq_lens_kv, batch, T, H, L, R,
+                                                softmax_scale, WindowArgs{window, sinks}, (cudaStream_t)stream),
+                     "mla_prefill_window");
+}
+
 mla_status mla_check_bounded_wait(uint32_t limit_us, void* stream) {
   g_msg[0] = 0;
   if (limit_us == 0 || limit_us > 1000000u)
@@ -716,7 +909,7 @@ mla_status mla_device_error(void* stream) {
   g_msg[0] = 0;
   cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_status(e, "mla_device_error: stream synchronize");
-  unsigned bits = copy_errors_read_clear() | attn_simt_errors_read_clear() | attn_tc_errors_read_clear() |
+  unsigned bits = copy_errors_read_clear() | cache_io_errors_read_clear() | attn_simt_errors_read_clear() | attn_tc_errors_read_clear() |
                   bmm_tc_errors_read_clear() | combine_vup_errors_read_clear();
   if (bits & kErrTimeout) return fail(MLA_ERR_TIMEOUT, "a bounded device-side wait gave up");
   if (bits & kErrDeviceData)

@@ -177,6 +177,46 @@ cudaError_t launch_decode_tc_dsmla(const View3& o_lat, float* lse, const View3& 
 cudaError_t launch_cache_write_fp8(mla_dtype src_dt, const View3& cache, const View3& kv_c, const View3& k_pe,
                                    int64_t L, int64_t R, const int64_t* slots, int64_t T, const float* scale,
                                    cudaStream_t st);
+// ds_mla cache write (cache_io.cu): kv_c [T, 512] and k_pe [T, 64] of src_dt into 656-byte
+// entries of a 16-byte aligned cache view (strides in bytes).
+cudaError_t launch_cache_write_ds_mla(mla_dtype src_dt, const View3& cache, const View3& kv_c, const View3& k_pe,
+                                      const int64_t* slots, int64_t tokens, cudaStream_t st);
+// A read-back of cache rows (cache_io.cu): out row i, cu_seqlens[b] <= i < cu_seqlens[b + 1], is
+// row seq_starts[b] + i - cu_seqlens[b] of sequence b (null starts: 0). The cache's strides and
+// entry count its own elements.
+struct CacheRead {
+  void* out;
+  int64_t out_s0, rows;
+  CacheView cache;
+  const int32_t* block_table;
+  int64_t bt_stride;
+  int32_t max_blocks;
+  const int32_t *cu_seqlens, *seq_starts;
+  int32_t batch;
+};
+cudaError_t launch_cache_read(mla_dtype dt, const CacheRead& r, cudaStream_t st);
+cudaError_t launch_cache_read_fp8(mla_dtype dst_dt, const CacheRead& r, const float* scale, cudaStream_t st);
+cudaError_t launch_cache_read_ds_mla(mla_dtype dst_dt, const CacheRead& r, cudaStream_t st);
+
+// Attention limited to a window and sinks on the CUDA cores (attn_simt.cu). A query at position p
+// of a sequence attends rows t <= p with t < sinks or t > p - window.
+struct WindowArgs {
+  int32_t window, sinks;
+};
+// visible[b] = rows the query at seq_lens[b] - 1 attends: the lengths of the split-KV schedule.
+cudaError_t launch_window_lens(const int32_t* seq_lens, int32_t B, int32_t max_blocks, int32_t page,
+                               const WindowArgs& w, int32_t* visible, cudaStream_t st);
+cudaError_t launch_decode_window_simt(mla_dtype dt, const View3& o_lat, float* lse, const View3& q,
+                                      const CacheView& cache, const int32_t* block_table, int64_t bt_stride,
+                                      int32_t max_blocks, const int32_t* seq_lens, const int32_t* visible, int32_t B,
+                                      int32_t H, int32_t L, int32_t R, float scale, const WindowArgs& w,
+                                      const DecodeSched& s, cudaStream_t st);
+cudaError_t launch_prefill_window_simt(mla_dtype dt, const View3& o_lat, float* lse, const View3& q,
+                                       const CacheView& cache, const int32_t* block_table, int64_t bt_stride,
+                                       int32_t max_blocks, const int32_t* cu_q, const int32_t* kv_lens, int32_t B,
+                                       int32_t T, int32_t H, int32_t L, int32_t R, float scale, const WindowArgs& w,
+                                       cudaStream_t st);
+
 cudaError_t launch_decode_combine(mla_dtype dt, const View3& o_lat, float* lse,
                                   const int32_t* seq_lens, int32_t B, int32_t H, int32_t L,
                                   const DecodeSched& s, cudaStream_t st);
@@ -256,6 +296,7 @@ mla_status report_status(mla_status st, const char* fmt, ...);
 
 // Per-module error words: read and clear (after the stream was synchronised).
 unsigned copy_errors_read_clear();
+unsigned cache_io_errors_read_clear();
 unsigned attn_simt_errors_read_clear();
 unsigned attn_tc_errors_read_clear();
 unsigned combine_vup_errors_read_clear();
