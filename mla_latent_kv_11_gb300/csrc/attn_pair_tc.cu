@@ -1,0 +1,1003 @@
+// Windowed attention on the tensor cores (tcgen05 + TMEM + TMA): split-KV decode and
+// causal prefill limited to a sliding window and sinks, bf16, kv_lora_rank 512, rope 64
+// or 0, up to 128 heads.
+//
+// Mathematics. A query at position p attends the rows t <= p with t < sinks or
+// t > p - window. Rows come in blocks of 64; a row tile's visible blocks are those of
+// the sinks and those of the window, listed one behind the other and taken two at a time.
+// One pass with the running maximum and sum of a softmax: m the reference maximum (raised
+// only when a tile's maximum exceeds it by more than 8 in base 2, so P stays below 2^8),
+// l = sum of the float32 weights, O += bf16(P) V in float32. The weights' rounding to bf16
+// is the only rounding between the inputs and the output's own.
+//
+// Tile. 128 query rows (heads of one token, or several tokens' heads) x 128 keys, by a
+// cluster of two CTAs. The rows are split: each CTA owns 64 of them, so that its output
+// accumulator, 64 x 512 float32, takes half its tensor memory and every row's scores lie
+// whole in one CTA (nothing is exchanged between the two). Each MMA is a
+// cta_group::2 MMA with M = 128: it takes its A rows from both CTAs and half of B from
+// each, at the full rate of both SMs (measured: 32 cycles for N = 128, K = 16, 64 for
+// N = 256; with 64-key tiles, N = 64, shared memory bounds it to 26 instead of 16).
+// Tensor memory per CTA (row r in lanes r and r + 64):
+//   O  [0, 256): lane r columns 0..255 of the row, lane r + 64 columns 256..511
+//   S  [256, 320) and [320, 384), of even and odd tiles: lane r keys 0..63, lane r + 64 keys 64..127
+//
+// Shared memory per CTA: Q 64 x 576 (72 KB), P 64 x 128 (16 KB), two key tiles of 64 KB and
+// one rope box of 8 KB. Q K^T needs, in each CTA, its 64 keys' whole rows (boxes H0: latent
+// columns 0..255, H1: 256..511, R: rope); P V needs all 128 keys' columns of its half. CTA r
+// keeps H_r of its keys for both; the other half is done with after Q K^T, and the other
+// CTA's keys' columns (box W) are loaded into its place. So a cache row crosses HBM once and
+// L2 1.44 times, and keys 64k .. 64k + 63 sit in H_k of both CTAs when P V runs.
+//
+// Order on the tensor pipe: QK(g+1), PV(g), so the softmax of tile g runs under QK(g+1);
+// at a row tile's end PV comes first. 256 threads: warp 0 loads (TMA), warp 1 of the first CTA
+// issues every MMA, warp 2 owns the tensor memory, warps 4..7 run the softmax, the rescaling
+// of O and the epilogue, one thread a lane.
+//
+// Every wait is bounded; one that gives up winds both CTAs down and is reported.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <math_constants.h>
+
+#include <algorithm>
+#include <mutex>
+#include <vector>
+
+#include "mla_internal.h"
+#include "sm100_ptx.cuh"
+
+namespace mla {
+namespace {
+
+using namespace ptx;
+
+__device__ unsigned g_pair_err = 0;
+
+constexpr int kBlk = 64;                     // cache rows per block: the keys of one CTA
+constexpr int kTileKeys = 2 * kBlk;          // keys per tile
+constexpr int kBox = kBlk * 128;             // 64 rows x 64 bf16 columns, 128-byte swizzle
+constexpr int kThreads = 256;
+constexpr int kSoftmaxWarp0 = 4;
+constexpr int kSoftmaxBar = 1;
+constexpr float kLazyRescale = 8.f;
+constexpr uint32_t kTmemS = 256, kTmemCols = 512;
+constexpr int kSegCost = 1;                  // cost of starting a row tile, in tiles
+constexpr int kSplitItems = 1024;            // row tiles up to which the schedule splits them
+
+template <int kRope>
+struct PairCfg {
+  static constexpr int kQBoxes = 8 + (kRope ? 1 : 0);
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffP = kQBoxes * kBox;
+  static constexpr int kOffKV = kOffP + 2 * kBox;          // [2 tiles][H0, H1][4 boxes]
+  static constexpr int kOffR = kOffKV + 2 * 8 * kBox;
+  static constexpr int kOffMisc = kOffR + (kRope ? kBox : 0);
+  static constexpr int kMiscBytes = 2048;
+  static constexpr int kSmemAlloc = kOffMisc + kMiscBytes + 1024;   // slack for 1 KB alignment
+};
+
+struct PairShared {
+  uint64_t full_k[2][2];   // first CTA: boxes 0, 1 / 2, 3 of H0 and H1 of both CTAs have landed
+  uint64_t full_r, full_q; // first CTA: the rope box, the queries, of both CTAs
+  uint64_t full_w[2];      // own W boxes
+  uint64_t s_full[2];      // scores of a tile are in tensor memory (and its Q, R and short half are read)
+  uint64_t pv_half[2];     // boxes 0, 1 of a tile's values are read
+  uint64_t pv_done[2];     // the tile's values and P are read, O is updated
+  uint64_t p_full;         // first CTA: P of both CTAs is written, O rescaled
+  uint64_t fin;
+  uint32_t tmem_base;
+  int abort_flag;
+  float smax[2][128];
+  float lsum[128];
+};
+static_assert(sizeof(PairShared) <= 2048, "barrier block overflows its slot");
+
+// The work of a unit: segments [t0, t1) of row tiles ("items").
+struct Seg {
+  int tok0, ntok, pos0, b;   // first token's row, tokens, its position, sequence
+  int lo, hi;                // first window row and last row any token attends
+  int nsb, wb, nblk;         // sink blocks, first window block behind them, blocks in all
+  int t0, t1, slot;          // tile range; partial slot or -1
+};
+
+struct PairParams {
+  int H, tpt, tptc;          // heads, tokens per row tile, tokens per CTA (heads split when H > 64: tptc 0)
+  int window, sinks;
+  float scale_log2;
+  __nv_bfloat16* o_lat;
+  int64_t o_s0, o_s1;
+  float* lse;
+  int page, num_blocks;
+  const int32_t* block_table;
+  int64_t bt_stride;
+  const int4* items;         // {first token row, tokens, its position, sequence} of each row tile
+  const int32_t* total;      // row tiles
+  const int2* unit_start;    // split: {row tile, tile} of each unit's first; null: whole row tiles dealt out
+  float* part_o;             // [2 * units][128][512]
+  float* part_lse;           // [2 * units][128]
+};
+
+__host__ __device__ inline int row_tiles(int nblk) { return nblk > 0 ? (nblk + 1) / 2 : 1; }
+
+// The visible blocks of a row tile whose tokens sit at pos0 .. pos0 + ntok - 1.
+__device__ __forceinline__ void visible_blocks(int pos0, int ntok, int window, int sinks, int& lo, int& hi, int& nsb,
+                                               int& wb, int& nblk) {
+  hi = pos0 + ntok - 1;
+  lo = max(0, pos0 - window + 1);
+  nsb = wb = nblk = 0;
+  if (hi < 0) return;
+  nsb = (min(sinks, hi + 1) + kBlk - 1) / kBlk;
+  wb = max(lo / kBlk, nsb);
+  nblk = nsb + max(0, hi / kBlk + 1 - wb);
+}
+
+struct Walker {
+  int unit, units, item, step, end_item, end_tile, tile;
+  int4 next_desc;
+
+  __device__ void init(const PairParams& p, int unit_, int units_) {
+    unit = unit_;
+    units = units_;
+    const int total = *p.total;
+    if (p.unit_start != nullptr) {
+      const int2 a = p.unit_start[unit], e = p.unit_start[unit + 1];
+      item = a.x;
+      tile = a.y;
+      end_item = e.x;
+      end_tile = e.y;
+      step = 1;
+    } else {   // the longest (latest) row tiles first
+      item = total - 1 - unit;
+      tile = 0;
+      step = -units;
+      end_item = -1;
+      end_tile = 0;
+    }
+    if (more()) next_desc = p.items[item];
+  }
+  __device__ bool more() const {
+    return step > 0 ? (item < end_item || (item == end_item && tile < end_tile)) : item >= 0;
+  }
+  // The next segment; the description of the one behind it is loaded meanwhile.
+  __device__ bool next(const PairParams& p, Seg& s) {
+    if (!more()) return false;
+    const int4 d = next_desc;
+    s.tok0 = d.x;
+    s.ntok = d.y;
+    s.pos0 = d.z;
+    s.b = d.w;
+    visible_blocks(s.pos0, s.ntok, p.window, p.sinks, s.lo, s.hi, s.nsb, s.wb, s.nblk);
+    const int nt = row_tiles(s.nblk);
+    s.t0 = tile;
+    s.t1 = step > 0 && item == end_item ? min(nt, end_tile) : nt;
+    s.slot = s.t0 == 0 && s.t1 == nt ? -1 : 2 * unit + (s.t0 == 0 ? 1 : 0);
+    item += step;
+    tile = 0;
+    if (more()) next_desc = p.items[item];
+    return true;
+  }
+};
+
+// First row of block j of a segment's list; -1 behind its end.
+__device__ __forceinline__ int block_row(const Seg& s, int j) {
+  return j >= s.nblk ? -1 : kBlk * (j < s.nsb ? j : s.wb + (j - s.nsb));
+}
+
+__device__ __forceinline__ void alloc_pair(uint32_t* dst, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+
+// One MMA of the pair, issued by the first CTA's converged warp (an elected lane).
+__device__ __forceinline__ void umma_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n .reg .b32 r;\n elect.sync r|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrive on `bar` of both CTAs once every MMA issued so far is complete.
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred e;\n .reg .b32 r;\n elect.sync r|e, 0xffffffff;\n"
+      " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}\n" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+// TMA load into this CTA whose bytes are counted on `bar`, a shared::cluster address (the first
+// CTA's barrier).
+__device__ __forceinline__ void tma_load_pair(void* dst, const void* map, uint32_t bar, int32_t c0, int32_t c1,
+                                              int32_t c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+template <int kRope>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    window_attn_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_constant__ CUtensorMap qmap,
+                       const PairParams p) {
+  using C = PairCfg<kRope>;
+  static_assert(C::kSmemAlloc <= 232448, "shared memory beyond the 227 KB a CTA may hold");
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem =
+      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  PairShared& sh = *reinterpret_cast<PairShared*>(smem + C::kOffMisc);
+  unsigned char *sQ = smem + C::kOffQ, *sP = smem + C::kOffP, *sKV = smem + C::kOffKV, *sR = smem + C::kOffR;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int unit = (int)cluster_id_x(), units = (int)nclusters_x();
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.full_k[i][0], 1);
+      mbar_init(&sh.full_k[i][1], 1);
+      mbar_init(&sh.full_w[i], 1);
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.pv_half[i], 1);
+      mbar_init(&sh.pv_done[i], 1);
+    }
+    mbar_init(&sh.full_r, 1);
+    mbar_init(&sh.full_q, 1);
+    mbar_init(&sh.p_full, 8);   // four warps of each CTA
+    mbar_init(&sh.fin, 1);
+    sh.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 2) alloc_pair(&sh.tmem_base, kTmemCols);
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&kvmap);
+    tma_prefetch_desc(&qmap);
+  }
+  tc_fence_before();
+  cluster_sync();   // both CTAs' barriers initialised, both tensor memories allocated
+  tc_fence_after();
+  pdl_enter();      // queries, cache and schedule come from the kernels before
+  const uint32_t tmem = sh.tmem_base;
+  volatile int* abort = &sh.abort_flag;
+  auto give_up = [&]() {   // tell both CTAs
+    sh.abort_flag = 1;
+    const uint32_t remote = map_to_rank(&sh.abort_flag, rank ^ 1u);
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(remote), "r"(1) : "memory");
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ loads, in both CTAs. The whole
+    // warp walks the tiles: lanes 0..15 look up the block ids of a tile (lane 8h + i: box i of
+    // its block h; blocks are one box of 64 rows, or several pages), lane 0 waits and issues.
+    const int rows_box = min(p.page, kBlk), subs = kBlk / rows_box;
+    const uint32_t bar_k0 = map_to_rank(&sh.full_k[0][0], 0), bar_r = map_to_rank(&sh.full_r, 0),
+                   bar_q = map_to_rank(&sh.full_q, 0);
+    Walker wk;
+    wk.init(p, unit, units);
+    Seg sg;
+    // the tile after the current one: its block ids (this lane's), the rows of its blocks within
+    // their pages, and whether it starts a segment
+    struct Tile {
+      int id, row0, row1;   // this lane's block id; page rows of blocks 0 and 1 (pages of 64 rows or more)
+      bool first;
+      int tok0;
+    };
+    bool have = wk.next(p, sg);
+    int j = have ? sg.t0 : 0;
+    auto fetch = [&](Tile& t) -> bool {
+      if (!have) return false;
+      const int h = (lane >> 3) & 1, i = lane & 7;
+      const int base = block_row(sg, 2 * j + h);
+      const int key = base + i * rows_box;
+      t.id = p.num_blocks;   // outside the tensor map: the box is filled with zeros
+      // rows of the box that some token attends
+      const bool seen = lane < 16 && i < subs && base >= 0 && key <= sg.hi && (key < p.sinks || key + rows_box > sg.lo);
+      if (seen) {
+        const int id = p.block_table[(int64_t)sg.b * p.bt_stride + key / p.page];
+        if (id >= 0 && id < p.num_blocks)
+          t.id = id;
+        else
+          atomicOr(&g_pair_err, kErrDeviceData);
+      }
+      const int in_page = base >= 0 && subs == 1 ? base % p.page : 0;
+      t.row0 = __shfl_sync(0xffffffffu, in_page, 0);
+      t.row1 = __shfl_sync(0xffffffffu, in_page, 8);
+      t.first = j == sg.t0;
+      t.tok0 = sg.tok0;
+      if (++j == sg.t1) {
+        have = wk.next(p, sg);
+        j = have ? sg.t0 : 0;
+      }
+      return true;
+    };
+    bool ok = true;
+    // boxes of block h of a tile (columns 64c .. 64c + 63 for c in [c0, c1)) into dst
+    auto load_block = [&](const Tile& t, int h, int c0, int c1, unsigned char* dst, uint32_t bar, bool pair) {
+      for (int i = 0; i < subs; ++i) {
+        const int id = __shfl_sync(0xffffffffu, t.id, 8 * h + i);
+        if (lane == 0) {
+          for (int c = c0; c < c1; ++c) {
+            unsigned char* d = dst + (c - c0) * kBox + i * rows_box * 128;
+            if (pair)
+              tma_load_pair(d, &kvmap, bar, 64 * c, h ? t.row1 : t.row0, id);
+            else
+              asm volatile(
+                  "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                  " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(d)),
+                  "l"(&kvmap), "r"(bar), "r"(64 * c), "r"(h ? t.row1 : t.row0), "r"(id)
+                  : "memory");
+          }
+        }
+      }
+    };
+    auto wait = [&](uint64_t* bar, int parity) {
+      if (lane == 0 && ok) ok = mbar_wait(bar, parity, abort);
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+    };
+    auto load_keys = [&](const Tile& t, int g, int part) {   // boxes 2 * part, 2 * part + 1 of H0 and H1
+      const int b = g & 1;
+      if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&sh.full_k[b][part], 2 * 4 * kBox);
+      unsigned char* d = sKV + b * 8 * kBox;
+      const uint32_t bar = bar_k0 + (2 * b + part) * 8;
+      load_block(t, (int)rank, 2 * part, 2 * part + 2, d + 2 * part * kBox, bar, true);
+      load_block(t, (int)rank, 4 + 2 * part, 4 + 2 * part + 2, d + (4 + 2 * part) * kBox, bar, true);
+    };
+    auto load_rope = [&](const Tile& t) {
+      if (kRope == 0) return;
+      if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&sh.full_r, 2 * kBox);
+      load_block(t, (int)rank, 8, 9, sR, bar_r, true);
+    };
+    auto load_q = [&](const Tile& t) {
+      if (lane != 0) return;
+      const int hb = min(p.H, 64), toks = max(p.tptc, 1);
+      if (rank == 0) mbar_arrive_expect_tx(&sh.full_q, 2u * C::kQBoxes * hb * toks * 128);
+      for (int c = 0; c < C::kQBoxes; ++c)
+        tma_load_pair(sQ + c * kBox, &qmap, bar_q, 64 * c, p.tptc ? 0 : 64 * (int)rank, t.tok0 + p.tptc * (int)rank);
+    };
+    Tile cur, nxt;
+    bool have_cur = fetch(cur);
+    if (have_cur) {
+      load_q(cur);
+      load_rope(cur);
+      load_keys(cur, 0, 0);
+      load_keys(cur, 0, 1);
+    }
+    for (int g = 0; ok && have_cur; ++g) {
+      const int b = g & 1, ph = (g >> 1) & 1;
+      const bool have_nxt = fetch(nxt);
+      // the next tile's keys: their buffer is free once PV(g - 1) has read it
+      auto load_next = [&]() {
+        if (!have_nxt) return;
+        for (int part = 0; ok && part < 2; ++part) {
+          if (g > 0) wait(part ? &sh.pv_done[b ^ 1] : &sh.pv_half[b ^ 1], ((g - 1) >> 1) & 1);
+          if (ok) load_keys(nxt, g + 1, part);
+        }
+      };
+      // PV(g - 1) comes before QK(g) at a segment's start, behind it else
+      const bool early = cur.first;
+      if (early) load_next();
+      if (ok) wait(&sh.s_full[b], ph);
+      if (!ok) break;
+      // QK(g) is done: the other CTA's keys' columns of this CTA's half take the place of the
+      // half that only QK(g) needed
+      if (lane == 0) mbar_arrive_expect_tx(&sh.full_w[b], 4 * kBox);
+      load_block(cur, 1 - (int)rank, 4 * (int)rank, 4 * (int)rank + 4, sKV + (b * 8 + 4 * (1 - (int)rank)) * kBox,
+                 smem_u32(&sh.full_w[b]), false);
+      if (have_nxt) {
+        load_rope(nxt);
+        if (nxt.first) load_q(nxt);
+      }
+      if (!early) load_next();
+      cur = nxt;
+      have_cur = have_nxt;
+    }
+    if (!ok) {
+      // copies in flight land within microseconds: wait well beyond that before the CTA ends
+      if (lane == 0) {
+        give_up();
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 2000000ull) {
+        }
+      }
+      __syncwarp();
+    }
+  } else if (warp == 1 && rank == 0) {
+    // ------------------------------------------------------------ MMA issuer of the pair
+    constexpr uint32_t id_qk = idesc_bf16(128, kTileKeys, false, false);
+    constexpr uint32_t id_pv = idesc_bf16(128, 256, false, true);
+    const uint32_t q0 = smem_u32(sQ), p0 = smem_u32(sP), kv0 = smem_u32(sKV), r0 = smem_u32(sR);
+    Walker wk;
+    wk.init(p, unit, units);
+    Seg sg;
+    int g = 0, seg_i = 0;
+    bool ok = true, pv_first = true;   // pv_first: the pending PV starts its segment's O
+    auto wait = [&](uint64_t* bar, int parity) {
+      ok = ok && __all_sync(0xffffffffu, mbar_wait<true>(bar, parity, abort));
+      return ok;
+    };
+    auto issue_pv = [&](int x) {
+      const int b = x & 1;
+      if (!wait(&sh.p_full, x & 1)) return;
+      tc_fence_after();
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          umma_pair(tmem + 128 * i, sdesc_sw128(p0 + (kk >> 2) * kBox + (kk & 3) * 32, 16, 1024),
+                    sdesc_sw128(kv0 + (b * 8 + (kk >> 2) * 4 + 2 * i) * kBox + (kk & 3) * 2048, kBox, 1024), id_pv,
+                    !(pv_first && kk == 0));
+        commit_pair(i ? &sh.pv_done[b] : &sh.pv_half[b]);
+      }
+    };
+    while (ok && wk.next(p, sg)) {
+      for (int j = sg.t0; ok && j < sg.t1; ++j, ++g) {
+        const int b = g & 1, ph = (g >> 1) & 1;
+        const uint32_t kb = kv0 + b * 8 * kBox, d = tmem + kTmemS + 64 * b;
+        if (j == sg.t0) {
+          if (g > 0) issue_pv(g - 1);
+          if (!ok || !wait(&sh.full_q, seg_i & 1)) break;
+        }
+        if (kRope) {
+          if (!wait(&sh.full_r, g & 1)) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_pair(d, sdesc_sw128(q0 + 8 * kBox + kk * 32, 16, 1024), sdesc_sw128(r0 + kk * 32, 16, 1024), id_qk,
+                      kk > 0);
+        }
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+          if (!wait(&sh.full_k[b][part], ph)) break;
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int box = 2 * part + (c & 1) + 4 * (c >> 1);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_pair(d, sdesc_sw128(q0 + box * kBox + kk * 32, 16, 1024),
+                        sdesc_sw128(kb + box * kBox + kk * 32, 16, 1024), id_qk, kRope || part || c || kk);
+          }
+        }
+        if (!ok) break;
+        commit_pair(&sh.s_full[b]);
+        if (j > sg.t0) {
+          issue_pv(g - 1);
+          pv_first = false;
+        }
+        if (j == sg.t0) pv_first = true;
+      }
+      ++seg_i;
+    }
+    if (ok && g > 0) issue_pv(g - 1);
+    if (!ok && lane == 0) give_up();
+    __syncwarp();
+    commit_pair(&sh.fin);
+  } else if (warp >= kSoftmaxWarp0) {
+    // ------------------------------------------------------------ softmax, rescaling, epilogue
+    const int ln = tid - kSoftmaxWarp0 * 32;            // tensor memory lane
+    const int row = ln & 63, half = ln >> 6;            // this CTA's row; keys (S) and columns (O) of this lane
+    const uint32_t lane_addr = (uint32_t)((warp - kSoftmaxWarp0) * 32) << 16;
+    const uint32_t bar_p = map_to_rank(&sh.p_full, 0);
+    // the row's token within the tile and its head
+    const int tok = p.tptc ? p.tptc * (int)rank + row / p.H : 0;
+    const int head = p.tptc ? row % p.H : 64 * (int)rank + row;
+    const bool real = p.tptc ? row < p.tptc * p.H : head < p.H;
+    auto group_all = [](bool v) { return named_bar_and(kSoftmaxBar, 128, v); };
+    Walker wk;
+    wk.init(p, unit, units);
+    Seg sg;
+    int g = 0;
+    bool ok = true, mine = true;   // ok: the group's decision; mine: this thread's waits so far
+    while (ok && wk.next(p, sg)) {
+      const bool valid = real && tok < sg.ntok;
+      const int pos = valid ? sg.pos0 + tok : -1;       // -1 attends nothing
+      float m = -CUDART_INF_F, l = 0.f;
+      for (int j = sg.t0; j < sg.t1; ++j, ++g) {
+        const int b = g & 1, ph = (g >> 1) & 1;
+        mine = mine && mbar_wait(&sh.s_full[b], ph, abort);
+        tc_fence_after();
+        float sv[64];
+        tmem_ld32(tmem + lane_addr + kTmemS + 64 * b, *reinterpret_cast<float(*)[32]>(sv));
+        tmem_ld32(tmem + lane_addr + kTmemS + 64 * b + 32, *reinterpret_cast<float(*)[32]>(sv + 32));
+        tmem_ld_wait();
+        const int kb = block_row(sg, 2 * j + half);
+        const bool whole = kb >= 0 && kb + kBlk - 1 <= pos && (kb + kBlk <= p.sinks || kb > pos - p.window);
+        if (!__all_sync(0xffffffffu, whole)) {
+#pragma unroll
+          for (int k = 0; k < 64; ++k) {
+            const int t = kb + k;
+            const bool seen = kb >= 0 && t <= pos && (t < p.sinks || t > pos - p.window);
+            sv[k] = seen ? sv[k] : -CUDART_INF_F;
+          }
+        }
+        float mx[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mx[k] = sv[k];
+#pragma unroll
+        for (int k = 8; k < 64; ++k) mx[k & 7] = fmaxf(mx[k & 7], sv[k]);
+        const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                                fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
+        sh.smax[g & 1][ln] = top;
+        ok = group_all(mine);   // the one group decision of a tile; the maxima of both halves
+        if (!ok) break;
+        const float mt = fmaxf(top, sh.smax[g & 1][ln ^ 64]) * p.scale_log2;
+        float alpha = 1.f;
+        if (mt > m + kLazyRescale || (m == -CUDART_INF_F && mt > -CUDART_INF_F)) {
+          alpha = m == -CUDART_INF_F ? 0.f : ex2_approx(m - mt);
+          m = mt;
+        }
+        const float ref = m == -CUDART_INF_F ? 0.f : -m;
+        l *= alpha;
+        uint32_t pk[32];
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < 64; k += 2) {
+          const float e0 = ex2_approx(fmaf(sv[k], p.scale_log2, ref));
+          const float e1 = ex2_approx(fmaf(sv[k + 1], p.scale_log2, ref));
+          sum[(k >> 1) & 3] += e0 + e1;
+          const __nv_bfloat162 h = __floats2bfloat162_rn(e0, e1);
+          pk[k >> 1] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        // P(g) takes P(g - 1)'s place and O is rescaled once PV(g - 1) is done
+        if (g > 0) mine = mine && mbar_wait(&sh.pv_done[b ^ 1], ((g - 1) >> 1) & 1, abort);
+        tc_fence_after();
+        if (__any_sync(0xffffffffu, alpha != 1.f && j > sg.t0)) {
+          for (int c = 0; c < 256; c += 32) {
+            float v[32];
+            tmem_ld32(tmem + lane_addr + c, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] *= alpha;
+            tmem_st32(tmem + lane_addr + c, v);
+          }
+          tmem_st_wait();
+        }
+#pragma unroll
+        for (int ch = 0; ch < 8; ++ch)
+          *reinterpret_cast<uint4*>(sP + half * kBox + row * 128 + ((ch ^ (row & 7)) << 4)) =
+              make_uint4(pk[4 * ch], pk[4 * ch + 1], pk[4 * ch + 2], pk[4 * ch + 3]);
+        // the other CTA's keys' values are here (the issuer does not wait for them itself)
+        mine = mine && mbar_wait(&sh.full_w[b], ph, abort);
+        // rows that no token attends: their weights are zero, and so must their values be,
+        // whatever the cache holds there
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int base = block_row(sg, 2 * j + h);
+          if (base < 0 || (base + kBlk - 1 <= sg.hi && (base + kBlk <= p.sinks || base >= sg.lo))) continue;
+          const int t = base + row;
+          if (!(t <= sg.hi && (t < p.sinks || t >= sg.lo))) {
+            unsigned char* v = sKV + (b * 8 + 4 * h + 2 * half) * kBox + row * 128;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              *reinterpret_cast<uint4*>(v + (i >> 3) * kBox + (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
+        asm volatile("fence.proxy.async.shared::cluster;" ::: "memory");
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(bar_p);
+      }
+      if (!ok) break;
+      // ---- O / l
+      const int last = g - 1;
+      mine = mine && mbar_wait(&sh.pv_done[last & 1], (last >> 1) & 1, abort);
+      sh.lsum[ln] = l;
+      ok = group_all(mine);
+      if (!ok) break;
+      tc_fence_after();
+      l += sh.lsum[ln ^ 64];
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      __nv_bfloat16* o = p.o_lat + (int64_t)(sg.tok0 + tok) * p.o_s0 + (int64_t)head * p.o_s1 + 256 * half;
+      const int64_t prow = (int64_t)sg.slot * 128 + tok * p.H + head;
+#pragma unroll 1
+      for (int c = 0; c < 256; c += 32) {
+        float v[32];
+        tmem_ld32(tmem + lane_addr + c, v);
+        tmem_ld_wait();
+        if (valid && sg.slot < 0) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) {
+            uint4 w;
+            __nv_bfloat162* h2 = reinterpret_cast<__nv_bfloat162*>(&w);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) h2[k] = __floats2bfloat162_rn(v[i + 2 * k] * inv, v[i + 2 * k + 1] * inv);
+            *reinterpret_cast<uint4*>(o + c + i) = w;
+          }
+        } else if (valid) {
+          float* q = p.part_o + prow * 512 + 256 * half + c;
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<float4*>(q + i) =
+                make_float4(v[i] * inv, v[i + 1] * inv, v[i + 2] * inv, v[i + 3] * inv);
+        }
+        __syncwarp();
+      }
+      if (valid && half == 0) {
+        const float lse = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -CUDART_INF_F;
+        if (sg.slot >= 0)
+          p.part_lse[prow] = lse;
+        else if (p.lse != nullptr)
+          p.lse[(int64_t)(sg.tok0 + tok) * p.H + head] = lse;
+      }
+    }
+    if (!ok) give_up();
+  }
+  // ---------------------------------------------------------------- teardown
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0) {
+    volatile int dummy = 0;
+    if (!mbar_wait(&sh.fin, 0, &dummy) || sh.abort_flag) atomicOr(&g_pair_err, kErrTimeout);
+  }
+  __syncthreads();
+  cluster_sync();   // neither CTA frees or leaves while the other's MMAs or copies may touch it
+  if (warp == 2) {
+    tc_fence_after();
+    dealloc_pair(tmem, kTmemCols);
+  }
+  cluster_sync();
+}
+
+// ------------------------------------------------------------------ schedule
+struct PairSched {
+  const int32_t* cu_q;     // null: a decode, one token a sequence
+  const int32_t* kv_lens;
+  int B, T, cap, tpt, window, sinks, units;
+  int4* items;
+  int32_t* total;
+  int2* unit_start;
+  int32_t* prefix;         // [B + 1] row tiles before each sequence (many row tiles only)
+};
+
+__device__ __forceinline__ int kv_len(const PairSched& s, int b) {
+  int n = s.kv_lens[b];
+  if (n < 0 || n > s.cap) {
+    atomicOr(&g_pair_err, kErrDeviceData);
+    n = n < 0 ? 0 : s.cap;
+  }
+  return n;
+}
+
+// Query tokens of sequence b; 0 (and reported) where cu_q leaves [0, T] or decreases.
+__device__ __forceinline__ int q_len(const PairSched& s, int b, int& q0) {
+  if (s.cu_q == nullptr) {
+    q0 = b;
+    return 1;
+  }
+  q0 = s.cu_q[b];
+  const int q1 = s.cu_q[b + 1];
+  if (q0 < 0 || q1 > s.T || q1 < q0) {
+    atomicOr(&g_pair_err, kErrDeviceData);
+    return 0;
+  }
+  return q1 - q0;
+}
+
+// Exclusive block scan of one int a thread (blockDim.x a multiple of 32).
+__device__ int scan_block(int v, int* warp_tot, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) warp_tot[warp] = x;
+  __syncthreads();
+  int before = 0, all = 0;
+  for (int w = 0; w < warps; ++w) {
+    if (w < warp) before += warp_tot[w];
+    all += warp_tot[w];
+  }
+  *total = all;
+  return before + x - v;
+}
+
+// Up to kSplitItems row tiles: their descriptions, and the units' starts: contiguous ranges of
+// tiles of equal cost, a row tile costing its tiles plus kSegCost. One block; a thread a
+// sequence, then a thread a row tile, then a thread a unit.
+__global__ void __launch_bounds__(1024) pair_split_kernel(PairSched s) {
+  __shared__ int warp_tot[32], first[kSplitItems + 1], q_begin[kSplitItems], q_count[kSplitItems], len[kSplitItems],
+      cost[kSplitItems + 1], tiles[kSplitItems];
+  pdl_enter();
+  const int i = threadIdx.x;
+  int n = 0, q0 = 0, total;
+  if (i < s.B) {
+    const int k = q_len(s, i, q0);
+    n = (k + s.tpt - 1) / s.tpt;
+    q_begin[i] = q0;
+    q_count[i] = k;
+    len[i] = kv_len(s, i);
+  }
+  const int ex = scan_block(n, warp_tot, &total);
+  if (i < s.B) first[i] = ex;
+  __syncthreads();
+  int nt = 0;
+  if (i < total) {
+    int lo = 0, hi = s.B - 1;   // the last sequence with first <= i: it has row tiles
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (first[mid] <= i) lo = mid; else hi = mid - 1;
+    }
+    const int t0 = (i - first[lo]) * s.tpt, ntok = min(s.tpt, q_count[lo] - t0);
+    const int pos0 = len[lo] - q_count[lo] + t0;
+    s.items[i] = make_int4(q_begin[lo] + t0, ntok, pos0, lo);
+    int a, b, c, d, nblk;
+    visible_blocks(pos0, ntok, s.window, s.sinks, a, b, c, d, nblk);
+    nt = row_tiles(nblk);
+  }
+  int all;
+  const int at = scan_block(i < total ? nt + kSegCost : 0, warp_tot, &all);
+  if (i < total) {
+    cost[i] = at;
+    tiles[i] = nt;
+  }
+  if (i == 0) *s.total = total;
+  __syncthreads();
+  // unit u starts at cost u * all / active: units beyond the tiles there are get nothing
+  const int active = max(1, min(s.units, all - kSegCost * total));
+  for (int u = i; u <= s.units; u += blockDim.x) {
+    int2 start = make_int2(total, 0);
+    if (u < active && total > 0) {
+      const int x = (int)((long long)u * all / active);
+      int lo = 0, hi = total - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (cost[mid] <= x) lo = mid; else hi = mid - 1;
+      }
+      const int into = max(0, x - cost[lo] - kSegCost);
+      start = into >= tiles[lo] ? make_int2(lo + 1, 0) : make_int2(lo, into);
+    }
+    s.unit_start[u] = start;
+  }
+}
+
+// More row tiles: how many lie before each sequence (one block), then a thread a row tile.
+__global__ void __launch_bounds__(1024) pair_prefix_kernel(PairSched s) {
+  __shared__ int warp_tot[32];
+  pdl_enter();
+  int carry = 0;
+  for (int base = 0; base < s.B; base += blockDim.x) {
+    const int b = base + threadIdx.x;
+    int q0, tot;
+    const int n = b < s.B ? (q_len(s, b, q0) + s.tpt - 1) / s.tpt : 0;
+    if (b < s.B) kv_len(s, b);   // reports a bad length
+    const int ex = scan_block(n, warp_tot, &tot);
+    if (b < s.B) s.prefix[b] = carry + ex;
+    carry += tot;
+  }
+  if (threadIdx.x == 0) {
+    s.prefix[s.B] = carry;
+    *s.total = carry;
+  }
+}
+
+__global__ void __launch_bounds__(256) pair_items_kernel(PairSched s) {
+  pdl_enter();
+  const int i = blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= s.prefix[s.B]) return;
+  int lo = 0, hi = s.B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (s.prefix[mid] <= i) lo = mid; else hi = mid - 1;
+  }
+  int q0 = lo, q1 = lo + 1;
+  if (s.cu_q != nullptr) {
+    q0 = s.cu_q[lo];
+    q1 = s.cu_q[lo + 1];
+  }
+  const int t0 = (i - s.prefix[lo]) * s.tpt;
+  const int kv = min(max(s.kv_lens[lo], 0), s.cap);
+  s.items[i] = make_int4(q0 + t0, min(s.tpt, q1 - q0 - t0), kv - (q1 - q0) + t0, lo);
+}
+
+// Row tiles cut across units: their pieces merged by log-sum-exp. Block (u, .) handles the row
+// tile that unit u + 1 is the first to start inside of; one warp a row.
+__global__ void __launch_bounds__(128) pair_combine_kernel(PairParams p, int units) {
+  pdl_enter();
+  const int u = blockIdx.x + 1;
+  const int2 at = p.unit_start[u], before = p.unit_start[u - 1];
+  if (at.x >= *p.total || at.y == 0 || (before.x == at.x && before.y > 0)) return;
+  const int4 d = p.items[at.x];
+  const int row = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int t = row / p.H, h = row - t * p.H;
+  if (t >= d.y) return;
+  // pieces: the head in unit u - 1 (slot 2 (u - 1) + 1), then units u, u + 1, ... (slots 2 v)
+  int np = 1;
+  while (u + np <= units) {
+    const int2 v = p.unit_start[u + np];
+    if (v.x != at.x || v.y == 0) break;
+    ++np;
+  }
+  auto slot = [&](int i) { return (int64_t)(i == 0 ? 2 * u - 1 : 2 * (u + i - 1)); };
+  float m = -CUDART_INF_F;
+  for (int i = 0; i <= np; ++i) m = fmaxf(m, p.part_lse[slot(i) * 128 + row]);
+  float4 acc[4] = {};
+  float tot = 0.f;
+  for (int i = 0; i <= np; ++i) {
+    const float li = p.part_lse[slot(i) * 128 + row];
+    const float w = li == -CUDART_INF_F ? 0.f : __expf(li - m);
+    tot += w;
+    const float* src = p.part_o + (slot(i) * 128 + row) * 512 + lane * 4;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float4 v = *reinterpret_cast<const float4*>(src + 128 * k);
+      acc[k].x = fmaf(w, v.x, acc[k].x);
+      acc[k].y = fmaf(w, v.y, acc[k].y);
+      acc[k].z = fmaf(w, v.z, acc[k].z);
+      acc[k].w = fmaf(w, v.w, acc[k].w);
+    }
+  }
+  const float inv = tot > 0.f ? 1.f / tot : 0.f;
+  __nv_bfloat16* o = p.o_lat + (int64_t)(d.x + t) * p.o_s0 + (int64_t)h * p.o_s1 + lane * 4;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(acc[k].x * inv, acc[k].y * inv);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(acc[k].z * inv, acc[k].w * inv);
+    *reinterpret_cast<uint2*>(o + 128 * k) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  }
+  if (lane == 0 && p.lse != nullptr)
+    p.lse[(int64_t)(d.x + t) * p.H + h] = tot > 0.f ? m + logf(tot) : -CUDART_INF_F;
+}
+
+template <int kRope>
+int max_pairs() {
+  static std::mutex mu;
+  static std::vector<int> cache;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  std::lock_guard<std::mutex> g(mu);
+  if ((int)cache.size() <= dev) cache.resize(dev + 1, 0);
+  if (cache[dev] == 0) {
+    using C = PairCfg<kRope>;
+    cudaFuncSetAttribute(window_attn_kernel<kRope>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemAlloc);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * device_sm_count(), 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = C::kSmemAlloc;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, window_attn_kernel<kRope>, &cfg) != cudaSuccess || n <= 0)
+      n = device_sm_count() / 2;
+    cudaGetLastError();
+    cache[dev] = n;
+  }
+  return cache[dev];
+}
+
+template <int kRope>
+cudaError_t launch_attn(const PairParams& p, const CUtensorMap& km, const CUtensorMap& qm, int units, cudaStream_t st) {
+  using C = PairCfg<kRope>;
+  const cudaError_t e = cudaFuncSetAttribute(window_attn_kernel<kRope>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             C::kSmemAlloc);
+  if (e != cudaSuccess) return e;
+  return launch_k(window_attn_kernel<kRope>, dim3(2 * units), dim3(kThreads), C::kSmemAlloc, st, km, qm, p);
+}
+
+int pair_tokens(int H) { return H > 64 ? 1 : 2 * (64 / H); }
+
+struct PairWs {
+  size_t off_total, off_items, off_starts, off_prefix, off_o, off_lse, total;
+};
+PairWs pair_ws(int64_t items, int64_t batch, int64_t units) {
+  auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+  PairWs w{};
+  w.off_total = 0;
+  w.off_items = 256;
+  w.off_starts = up(w.off_items + items * sizeof(int4));
+  w.off_prefix = up(w.off_starts + (units + 1) * sizeof(int2));
+  w.off_o = up(w.off_prefix + (batch + 1) * sizeof(int32_t));
+  // partial slots: two a unit where the schedule splits row tiles
+  w.off_lse = up(w.off_o + (items <= kSplitItems ? 2 * units * 128 * 512 * sizeof(float) : 0));
+  w.total = up(w.off_lse + (items <= kSplitItems ? 2 * units * 128 * sizeof(float) : 0));
+  return w;
+}
+
+// Row tiles of T tokens in B sequences, at most.
+int64_t most_items(int64_t T, int64_t B, int H, bool decode) {
+  if (decode) return B;
+  const int tpt = pair_tokens(H);
+  return tpt == 1 ? T : std::min<int64_t>(T, T / tpt + B);
+}
+
+bool pair_maps(const WindowCall& c, CUtensorMap* km, CUtensorMap* qm) {
+  const int E = c.L + c.R;
+  const uint32_t rows_box = c.cache.page < kBlk ? c.cache.page : kBlk;
+  const uint32_t hb = c.H < 64 ? c.H : 64, toks = c.H > 64 ? 1 : 64 / c.H;
+  return make_map3d(km, c.cache.data, E, c.cache.page, c.cache.num_blocks, (uint64_t)c.cache.s_row * 2,
+                    (uint64_t)c.cache.s_blk * 2, 64, rows_box, 1, CU_TENSOR_MAP_SWIZZLE_128B) &&
+         make_map3d(qm, c.q.data, E, c.H, c.q.n0, (uint64_t)c.q.s1 * 2, (uint64_t)c.q.s0 * 2, 64, hb, toks,
+                    CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+}  // namespace
+
+bool window_tc_supported(mla_dtype dt, const WindowCall& c) {
+  if (dt != MLA_BF16 || c.L != 512 || (c.R != 0 && c.R != 64) || c.H > 128 || !(c.scale > 0.f)) return false;
+  const int page = c.cache.page;
+  if (!(page % 64 == 0 || (64 % page == 0 && page % 8 == 0))) return false;
+  auto al16 = [](const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15) == 0; };
+  if (!al16(c.cache.data) || c.cache.s_blk % 8 || c.cache.s_row % 8) return false;
+  if (!al16(c.q.data) || c.q.s0 % 8 || c.q.s1 % 8) return false;
+  if (!al16(c.o.data) || c.o.s0 % 8 || c.o.s1 % 8) return false;
+  CUtensorMap km, qm;
+  return pair_maps(c, &km, &qm);
+}
+
+size_t window_tc_workspace(int64_t T, int64_t B, int H, bool decode, int num_splits) {
+  if (H <= 0 || H > 128) return 0;
+  return pair_ws(most_items(T, B, H, decode), B, num_splits > 0 ? num_splits : max_pairs<64>()).total;
+}
+
+cudaError_t launch_window_tc(const WindowCall& c, int num_splits, void* ws, cudaStream_t st) {
+  CUtensorMap km, qm;
+  if (!pair_maps(c, &km, &qm)) return cudaErrorInvalidValue;
+  const bool decode = c.cu_q == nullptr;
+  const int units = num_splits > 0 ? num_splits : max_pairs<64>();
+  const int64_t items = most_items(c.q.n0, c.B, c.H, decode);
+  const PairWs w = pair_ws(items, c.B, units);
+  char* base = static_cast<char*>(ws);
+  const bool split = items <= kSplitItems && c.B <= kSplitItems;
+  constexpr int kFar = 0x3fffffff;   // positions stay below this
+  const long long cap = (long long)c.max_blocks * c.cache.page;
+  PairSched s{c.cu_q, c.kv_lens, c.B, (int)c.q.n0, (int)std::min<long long>(cap, kFar), pair_tokens(c.H),
+              std::min(c.window.window, kFar), std::min(c.window.sinks, kFar), units,
+              reinterpret_cast<int4*>(base + w.off_items), reinterpret_cast<int32_t*>(base + w.off_total),
+              reinterpret_cast<int2*>(base + w.off_starts), reinterpret_cast<int32_t*>(base + w.off_prefix)};
+  cudaError_t e;
+  if (split) {
+    const int threads = (int)std::min<int64_t>(1024, (std::max<int64_t>({items, c.B, std::min(units + 1, 128)}) + 31) / 32 * 32);
+    e = launch_k(pair_split_kernel, 1, threads, 0, st, s);
+  } else {
+    e = launch_k(pair_prefix_kernel, 1, 1024, 0, st, s);
+    if (e == cudaSuccess) e = launch_k(pair_items_kernel, (unsigned)((items + 255) / 256), 256, 0, st, s);
+  }
+  if (e != cudaSuccess) return e;
+  PairParams p{};
+  p.H = c.H;
+  p.tpt = s.tpt;
+  p.tptc = c.H > 64 ? 0 : s.tpt / 2;
+  p.window = s.window;
+  p.sinks = s.sinks;
+  p.scale_log2 = c.scale * 1.4426950408889634f;
+  p.o_lat = static_cast<__nv_bfloat16*>(c.o.data);
+  p.o_s0 = c.o.s0;
+  p.o_s1 = c.o.s1;
+  p.lse = c.lse;
+  p.page = c.cache.page;
+  p.num_blocks = c.cache.num_blocks;
+  p.block_table = c.block_table;
+  p.bt_stride = c.bt_stride;
+  p.items = s.items;
+  p.total = s.total;
+  p.unit_start = split ? s.unit_start : nullptr;
+  p.part_o = reinterpret_cast<float*>(base + w.off_o);
+  p.part_lse = reinterpret_cast<float*>(base + w.off_lse);
+  e = c.R == 64 ? launch_attn<64>(p, km, qm, units, st) : launch_attn<0>(p, km, qm, units, st);
+  if (e != cudaSuccess || !split || units < 2) return e;
+  return launch_k(pair_combine_kernel, dim3(units - 1, (s.tpt * c.H + 3) / 4), 128, 0, st, p, units);
+}
+
+unsigned attn_pair_errors_read_clear() {
+  unsigned v = 0, zero = 0;
+  if (cudaMemcpyFromSymbol(&v, g_pair_err, sizeof(v)) != cudaSuccess) return 0;
+  cudaMemcpyToSymbol(g_pair_err, &zero, sizeof(zero));
+  return v;
+}
+
+}  // namespace mla

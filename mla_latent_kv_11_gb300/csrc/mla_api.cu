@@ -1,5 +1,6 @@
 // Host side of the C ABI: argument validation, dispatch, error reporting.
 // Nothing in this file touches device memory except through the launchers.
+#include <algorithm>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -823,24 +824,26 @@ mla_status check_workspace(const void* workspace, size_t have, size_t need) {
   return MLA_OK;
 }
 
-// mla_decode_window's workspace: mla_decode's layout, then the visible lengths [B].
+// mla_decode_window's workspace: on the CUDA cores mla_decode's layout, then the visible lengths
+// [B]; on the tensor cores a layout of its own. One size covers both.
 struct WindowWs {
   DecodeWsLayout lay;
   size_t off_visible, total;
 };
-WindowWs window_ws(int64_t B, int64_t H, int64_t L, int32_t units) {
+WindowWs window_ws(int64_t B, int64_t H, int64_t L, int32_t num_splits) {
   WindowWs w;
-  w.lay = decode_ws_layout(B, H, L, units);
+  w.lay = decode_ws_layout(B, H, L, decode_units(num_splits));
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   w.off_visible = up(w.lay.total);
   w.total = up(w.off_visible + (size_t)B * sizeof(int32_t));
+  if (L == 512) w.total = std::max(w.total, window_tc_workspace(B, B, (int)H, true, num_splits));
   return w;
 }
 }  // namespace
 
 size_t mla_decode_window_workspace_size(int32_t batch, int32_t num_heads, int32_t kv_lora_rank, int32_t num_splits) {
   if (batch < 0 || num_heads < 0 || kv_lora_rank < 0 || num_splits < 0) return 0;
-  return window_ws(batch, num_heads, kv_lora_rank, decode_units(num_splits)).total;
+  return window_ws(batch, num_heads, kv_lora_rank, num_splits).total;
 }
 
 mla_status mla_decode_window(mla_dtype dtype, mla_tensor o_lat_out, float* lse_out, mla_tensor q_cat,
@@ -854,11 +857,15 @@ mla_status mla_decode_window(mla_dtype dtype, mla_tensor o_lat_out, float* lse_o
   MLA_TRY(check_decode_args(dtype, o_lat_out, q_cat, cache, block_table, block_table_stride, max_blocks,
                             seq_lens, kv_lora_rank, rope_dim, softmax_scale, num_splits, &dc));
   if (dc.empty) return MLA_OK;
-  const WindowWs ws = window_ws(dc.B, dc.H, dc.L, decode_units(num_splits));
+  const WindowWs ws = window_ws(dc.B, dc.H, dc.L, num_splits);
   MLA_TRY(check_workspace(workspace, workspace_bytes, ws.total));
   const cudaStream_t st = (cudaStream_t)stream;
   const int32_t B = (int32_t)dc.B, H = (int32_t)dc.H, L = (int32_t)dc.L, R = (int32_t)dc.R;
   const WindowArgs w{window, sinks};
+  const WindowCall wc{dc.ov, dc.qv, lse_out, dc.cv, block_table, block_table_stride, max_blocks, nullptr, seq_lens,
+                      B, H, L, R, softmax_scale, w};
+  if (window_tc_supported(dtype, wc))
+    return cuda_status(launch_window_tc(wc, num_splits, workspace, st), "mla_decode_window (tensor cores)");
   // each sequence's visible rows, then the split-KV decode over that many
   int32_t* visible = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + ws.off_visible);
   const DecodeSched s = decode_sched_from_ws(workspace, ws.lay, B, decode_units(num_splits));
@@ -873,7 +880,7 @@ mla_status mla_decode_window(mla_dtype dtype, mla_tensor o_lat_out, float* lse_o
 
 size_t mla_prefill_window_workspace_size(int32_t tokens, int32_t batch, int32_t num_heads, int32_t kv_lora_rank) {
   if (tokens < 0 || batch < 0 || num_heads < 0 || kv_lora_rank < 0) return 0;
-  return 256;
+  return std::max<size_t>(256, kv_lora_rank == 512 ? window_tc_workspace(tokens, batch, num_heads, false, 0) : 0);
 }
 
 mla_status mla_prefill_window(mla_dtype dtype, mla_tensor o_lat_out, float* lse_out, mla_tensor q_cat,
@@ -892,6 +899,10 @@ mla_status mla_prefill_window(mla_dtype dtype, mla_tensor o_lat_out, float* lse_
   if (cu_seqlens_q == nullptr) return fail(MLA_ERR_INVALID_ARG, "cu_seqlens_q must be non-null");
   const int32_t T = (int32_t)dc.B, H = (int32_t)dc.H, L = (int32_t)dc.L, R = (int32_t)dc.R;
   MLA_TRY(check_workspace(workspace, workspace_bytes, mla_prefill_window_workspace_size(T, batch, H, L)));
+  const WindowCall wc{dc.ov, dc.qv, lse_out, dc.cv, block_table, block_table_stride, max_blocks, cu_seqlens_q,
+                      seq_lens_kv, batch, H, L, R, softmax_scale, WindowArgs{window, sinks}};
+  if (window_tc_supported(dtype, wc))
+    return cuda_status(launch_window_tc(wc, 0, workspace, (cudaStream_t)stream), "mla_prefill_window (tensor cores)");
   return cuda_status(launch_prefill_window_simt(dtype, dc.ov, lse_out, dc.qv, dc.cv, block_table, block_table_stride,
                                                 max_blocks, cu_seqlens_q, seq_lens_kv, batch, T, H, L, R,
                                                 softmax_scale, WindowArgs{window, sinks}, (cudaStream_t)stream),
@@ -909,7 +920,8 @@ mla_status mla_device_error(void* stream) {
   g_msg[0] = 0;
   cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_status(e, "mla_device_error: stream synchronize");
-  unsigned bits = copy_errors_read_clear() | cache_io_errors_read_clear() | attn_simt_errors_read_clear() | attn_tc_errors_read_clear() |
+  unsigned bits = copy_errors_read_clear() | cache_io_errors_read_clear() | attn_pair_errors_read_clear() |
+                  attn_simt_errors_read_clear() | attn_tc_errors_read_clear() |
                   bmm_tc_errors_read_clear() | combine_vup_errors_read_clear();
   if (bits & kErrTimeout) return fail(MLA_ERR_TIMEOUT, "a bounded device-side wait gave up");
   if (bits & kErrDeviceData)

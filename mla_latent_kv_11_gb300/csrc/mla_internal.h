@@ -203,6 +203,27 @@ cudaError_t launch_cache_read_ds_mla(mla_dtype dst_dt, const CacheRead& r, cudaS
 struct WindowArgs {
   int32_t window, sinks;
 };
+// A windowed call after validation: a prefill's queries (cu_q [B + 1]) or, with cu_q null, a
+// decode's, one token a sequence.
+struct WindowCall {
+  View3 o, q;
+  float* lse;
+  CacheView cache;
+  const int32_t* block_table;
+  int64_t bt_stride;
+  int32_t max_blocks;
+  const int32_t *cu_q, *kv_lens;
+  int32_t B, H, L, R;
+  float scale;
+  WindowArgs window;
+};
+// On the tensor cores (attn_pair_tc.cu): bf16, L = 512, R in {0, 64}, up to 128 heads, a positive
+// scale, pages of whole 64-row blocks or blocks of whole pages of 8 rows or more, 16-byte aligned
+// views.
+bool window_tc_supported(mla_dtype dt, const WindowCall& c);
+// Bytes of workspace for T query tokens of B sequences (0: H is not taken).
+size_t window_tc_workspace(int64_t T, int64_t B, int H, bool decode, int num_splits);
+cudaError_t launch_window_tc(const WindowCall& c, int num_splits, void* ws, cudaStream_t st);
 // visible[b] = rows the query at seq_lens[b] - 1 attends: the lengths of the split-KV schedule.
 cudaError_t launch_window_lens(const int32_t* seq_lens, int32_t B, int32_t max_blocks, int32_t page,
                                const WindowArgs& w, int32_t* visible, cudaStream_t st);
@@ -297,6 +318,7 @@ mla_status report_status(mla_status st, const char* fmt, ...);
 // Per-module error words: read and clear (after the stream was synchronised).
 unsigned copy_errors_read_clear();
 unsigned cache_io_errors_read_clear();
+unsigned attn_pair_errors_read_clear();
 unsigned attn_simt_errors_read_clear();
 unsigned attn_tc_errors_read_clear();
 unsigned combine_vup_errors_read_clear();
