@@ -55,8 +55,9 @@ __device__ unsigned g_pair_err = 0;
 constexpr int kBlk = 64;                     // cache rows per block: the keys of one CTA
 constexpr int kTileKeys = 2 * kBlk;          // keys per tile
 constexpr int kBox = kBlk * 128;             // 64 rows x 64 bf16 columns, 128-byte swizzle
-constexpr int kThreads = 256;
+constexpr int kThreads = 384;
 constexpr int kSoftmaxWarp0 = 4;
+constexpr int kSoftmaxThreads = 256;
 constexpr int kSoftmaxBar = 1;
 constexpr float kLazyRescale = 8.f;
 constexpr uint32_t kTmemS = 256, kTmemCols = 512;
@@ -71,25 +72,29 @@ struct PairCfg {
   static constexpr int kOffKV = kOffP + 2 * kBox;          // [2 tiles][H0, H1][4 boxes]
   static constexpr int kOffR = kOffKV + 2 * 8 * kBox;
   static constexpr int kOffMisc = kOffR + (kRope ? kBox : 0);
-  static constexpr int kMiscBytes = 2048;
-  static constexpr int kSmemAlloc = kOffMisc + kMiscBytes + 1024;   // slack for 1 KB alignment
+  static constexpr int kMiscBytes = 3072;
+  static constexpr int kSmemAlloc = kOffMisc + kMiscBytes;
 };
 
+// Offset of column group c (0..3) of half h of key tile b.
+__host__ __device__ constexpr int kv_box(int b, int h, int c) { return (b * 8 + h * 4 + c) * kBox; }
+
 struct PairShared {
-  uint64_t full_k[2][2];   // first CTA: boxes 0, 1 / 2, 3 of H0 and H1 of both CTAs have landed
+  uint64_t full_k[2][2];   // [tile][half] first CTA: H0 / H1 of both CTAs have landed
   uint64_t full_r, full_q; // first CTA: the rope box, the queries, of both CTAs
   uint64_t full_w[2];      // own W boxes
   uint64_t s_full[2];      // scores of a tile are in tensor memory (and its Q, R and short half are read)
-  uint64_t pv_half[2];     // boxes 0, 1 of a tile's values are read
+  uint64_t pv_half[2];     // the values of a tile's keys 0..63 (in the place of H0) are read
   uint64_t pv_done[2];     // the tile's values and P are read, O is updated
   uint64_t p_full;         // first CTA: P of both CTAs is written, O rescaled
   uint64_t fin;
   uint32_t tmem_base;
   int abort_flag;
-  float smax[2][128];
-  float lsum[128];
+  // row maxima of a tile, [tile parity][columns 0..31 / 32..63 of S][lane]; at a segment's end the
+  // weights' sums
+  float red[2][2][128];
 };
-static_assert(sizeof(PairShared) <= 2048, "barrier block overflows its slot");
+static_assert(sizeof(PairShared) <= 3072, "barrier block overflows its slot");
 
 // The work of a unit: segments [t0, t1) of row tiles ("items").
 struct Seg {
@@ -112,8 +117,10 @@ struct PairParams {
   const int4* items;         // {first token row, tokens, its position, sequence} of each row tile
   const int32_t* total;      // row tiles
   const int2* unit_start;    // split: {row tile, tile} of each unit's first; null: whole row tiles dealt out
-  float* part_o;             // [2 * units][128][512]
+  float* part_o;             // [2 * units][128][512], row 64 * CTA + row
   float* part_lse;           // [2 * units][128]
+  int q_whole;               // the queries' column groups come in one load
+  int prefetch;              // bring the tile after the next into L2 (rows come from HBM, each read once)
 };
 
 __host__ __device__ inline int row_tiles(int nblk) { return nblk > 0 ? (nblk + 1) / 2 : 1; }
@@ -177,9 +184,28 @@ struct Walker {
   }
 };
 
+// The walker's next segment for a role that issues from a whole warp: its tiles [first, return
+// value), none (0, 0) behind the last. Values that come from memory are not uniform to the compiler,
+// and under a branch on them it forms every operand of the MMAs and loads in vector registers (an MMA
+// then took 75 cycles to issue, a load 300); the results of a reduction over the warp are.
+__device__ __forceinline__ int open_segment(Walker& wk, const PairParams& p, Seg& s, int& first) {
+  const bool any = wk.next(p, s);
+  first = __reduce_max_sync(0xffffffffu, any ? s.t0 : 0);
+  return __reduce_max_sync(0xffffffffu, any ? s.t1 : 0);
+}
+
 // First row of block j of a segment's list; -1 behind its end.
 __device__ __forceinline__ int block_row(const Seg& s, int j) {
   return j >= s.nblk ? -1 : kBlk * (j < s.nsb ? j : s.wb + (j - s.nsb));
+}
+
+// The wait behind a first look, kept out of line: the roles' loops have to stay in the instruction
+// cache together.
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return mbar_wait<true>(bar, parity, abort);
+}
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return mbar_test_cluster(bar, parity) || wait_slow(bar, parity, abort);
 }
 
 __device__ __forceinline__ void alloc_pair(uint32_t* dst, uint32_t ncols) {
@@ -191,13 +217,19 @@ __device__ __forceinline__ void dealloc_pair(uint32_t taddr, uint32_t ncols) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
-// One MMA of the pair, issued by the first CTA's converged warp (an elected lane).
-__device__ __forceinline__ void umma_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                          uint32_t accumulate) {
+// Four MMAs of the pair (K = 64), issued by the first CTA's converged warp (an elected lane); the
+// descriptors advance by `as` and `bs` 16-byte units. The first replaces D where `fresh`.
+__device__ __forceinline__ void umma_pair4(uint32_t d, uint64_t a, uint64_t b, uint32_t as, uint32_t bs, uint32_t idesc,
+                                           bool fresh) {
   asm volatile(
-      "{\n .reg .pred p, e;\n .reg .b32 r;\n elect.sync r|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
-      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred p, t, e;\n .reg .b32 r;\n .reg .b64 a, b, as, bs;\n"
+      " elect.sync r|e, 0xffffffff;\n setp.eq.b32 p, %6, 0;\n setp.eq.b32 t, 0, 0;\n"
+      " cvt.u64.u32 as, %3;\n cvt.u64.u32 bs, %4;\n mov.b64 a, %1;\n mov.b64 b, %2;\n"
+      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, p;\n add.u64 a, a, as;\n add.u64 b, b, bs;\n"
+      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, t;\n add.u64 a, a, as;\n add.u64 b, b, bs;\n"
+      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, t;\n add.u64 a, a, as;\n add.u64 b, b, bs;\n"
+      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, t;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(as), "r"(bs), "r"(idesc), "r"((uint32_t)fresh)
       : "memory");
 }
 // Arrive on `bar` of both CTAs once every MMA issued so far is complete.
@@ -209,34 +241,78 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar) {
       "h"((uint16_t)3)
       : "memory");
 }
-// TMA load into this CTA whose bytes are counted on `bar`, a shared::cluster address (the first
-// CTA's barrier).
-__device__ __forceinline__ void tma_load_pair(void* dst, const void* map, uint32_t bar, int32_t c0, int32_t c1,
-                                              int32_t c2) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
-      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(map), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
-      : "memory");
-}
-__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
+// The loader's operations, each run by its whole converged warp and issued by an elected lane:
+// the operands then stay warp-uniform and a TMA load issues in 28 cycles. Behind a branch on one
+// lane it takes 147 (measured), which made the loads the pair's bottleneck.
+#define MLA_ELECT "{\n .reg .pred e;\n .reg .b32 r;\n elect.sync r|e, 0xffffffff;\n @e "
 
-template <int kRope>
+__device__ __forceinline__ void expect_bytes(uint64_t* bar, uint32_t bytes) {
+  asm volatile(MLA_ELECT "mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n}\n" ::"r"(smem_u32(bar)), "r"(bytes)
+               : "memory");
+}
+// Loads into this CTA whose bytes are counted on `bar`, a shared::cluster address (the first CTA's
+// barrier).
+__device__ __forceinline__ void load_pair_3d(void* dst, const void* map, uint32_t bar, int32_t c0, int32_t c1,
+                                             int32_t c2) {
+  asm volatile(MLA_ELECT
+               "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+               " [%0], [%1, {%3, %4, %5}], [%2];\n}\n" ::"r"(smem_u32(dst)),
+               "l"(map), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
+__device__ __forceinline__ void load_pair_4d(void* dst, const void* map, uint32_t bar, int32_t c1, int32_t c2,
+                                             int32_t c3) {
+  asm volatile(MLA_ELECT
+               "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+               " [%0], [%1, {%3, %4, %5, %6}], [%2];\n}\n" ::"r"(smem_u32(dst)),
+               "l"(map), "r"(bar), "r"(0), "r"(c1), "r"(c2), "r"(c3)
+               : "memory");
+}
+// The same counted on a barrier of this CTA.
+__device__ __forceinline__ void load_own_3d(void* dst, const void* map, uint64_t* bar, int32_t c0, int32_t c1,
+                                            int32_t c2) {
+  asm volatile(MLA_ELECT
+               "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+               " [%0], [%1, {%3, %4, %5}], [%2];\n}\n" ::"r"(smem_u32(dst)),
+               "l"(map), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
+__device__ __forceinline__ void load_own_4d(void* dst, const void* map, uint64_t* bar, int32_t c1, int32_t c2,
+                                            int32_t c3) {
+  asm volatile(MLA_ELECT
+               "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+               " [%0], [%1, {%3, %4, %5, %6}], [%2];\n}\n" ::"r"(smem_u32(dst)),
+               "l"(map), "r"(smem_u32(bar)), "r"(0), "r"(c1), "r"(c2), "r"(c3)
+               : "memory");
+}
+// Bring a box into L2 without waiting.
+__device__ __forceinline__ void prefetch_3d(const void* map, int32_t c0, int32_t c1, int32_t c2) {
+  asm volatile(MLA_ELECT "cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];\n}\n" ::"l"(map),
+               "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
+__device__ __forceinline__ void prefetch_4d(const void* map, int32_t c1, int32_t c2, int32_t c3) {
+  asm volatile(MLA_ELECT "cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];\n}\n" ::"l"(map),
+               "r"(0), "r"(c1), "r"(c2), "r"(c3)
+               : "memory");
+}
+#undef MLA_ELECT
+
+// kSmall: pages of less than 64 rows.
+template <int kRope, bool kSmall>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    window_attn_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_constant__ CUtensorMap qmap,
+    window_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap kvmap, const __grid_constant__ CUtensorMap qmap,
                        const PairParams p) {
   using C = PairCfg<kRope>;
   static_assert(C::kSmemAlloc <= 232448, "shared memory beyond the 227 KB a CTA may hold");
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char* smem =
-      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* smem = smem_raw;
   PairShared& sh = *reinterpret_cast<PairShared*>(smem + C::kOffMisc);
   unsigned char *sQ = smem + C::kOffQ, *sP = smem + C::kOffP, *sKV = smem + C::kOffKV, *sR = smem + C::kOffR;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t rank = cluster_ctarank();
-  const int unit = (int)cluster_id_x(), units = (int)nclusters_x();
+  // clusters are pairs along x; unlike the cluster's own registers blockIdx is uniform to the compiler
+  const uint32_t rank = blockIdx.x & 1;
+  const int unit = blockIdx.x >> 1, units = gridDim.x >> 1;
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -249,13 +325,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     mbar_init(&sh.full_r, 1);
     mbar_init(&sh.full_q, 1);
-    mbar_init(&sh.p_full, 8);   // four warps of each CTA
+    mbar_init(&sh.p_full, 2 * kSoftmaxThreads / 32);   // the softmax warps of both CTAs
     mbar_init(&sh.fin, 1);
     sh.abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == 2) alloc_pair(&sh.tmem_base, kTmemCols);
   if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&kmap);
     tma_prefetch_desc(&kvmap);
     tma_prefetch_desc(&qmap);
   }
@@ -263,7 +340,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync();   // both CTAs' barriers initialised, both tensor memories allocated
   tc_fence_after();
   pdl_enter();      // queries, cache and schedule come from the kernels before
-  const uint32_t tmem = sh.tmem_base;
+  constexpr uint32_t tmem = 0;   // all 512 columns are allocated: they begin at 0
   volatile int* abort = &sh.abort_flag;
   auto give_up = [&]() {   // tell both CTAs
     sh.abort_flag = 1;
@@ -273,129 +350,166 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ loads, in both CTAs. The whole
-    // warp walks the tiles: lanes 0..15 look up the block ids of a tile (lane 8h + i: box i of
-    // its block h; blocks are one box of 64 rows, or several pages), lane 0 waits and issues.
-    const int rows_box = min(p.page, kBlk), subs = kBlk / rows_box;
+    // warp walks the tiles. Lane h looks up the block id of a tile's block h (small pages: lanes
+    // 8h .. 8h + 7 the ids of its pages).
+    const int rows_box = kSmall ? p.page : kBlk, subs = kBlk / rows_box;
     const uint32_t bar_k0 = map_to_rank(&sh.full_k[0][0], 0), bar_r = map_to_rank(&sh.full_r, 0),
                    bar_q = map_to_rank(&sh.full_q, 0);
     Walker wk;
     wk.init(p, unit, units);
     Seg sg;
-    // the tile after the current one: its block ids (this lane's), the rows of its blocks within
-    // their pages, and whether it starts a segment
+    bool ok = true;
+    int j = 0, nt = 0;   // next tile of the open segment, its end; both warp-uniform
+    bool fresh = true;
+    auto open = [&]() {
+      nt = open_segment(wk, p, sg, j);
+      fresh = true;
+    };
+    open();
+    // a tile to load: this lane's block id (and page row of its block), whether it starts a segment
     struct Tile {
-      int id, row0, row1;   // this lane's block id; page rows of blocks 0 and 1 (pages of 64 rows or more)
-      bool first;
+      int id, row;
+      bool seen, first;
       int tok0;
     };
-    bool have = wk.next(p, sg);
-    int j = have ? sg.t0 : 0;
+    // the next tile: its block id is asked for here and used a tile later (settle)
     auto fetch = [&](Tile& t) -> bool {
-      if (!have) return false;
-      const int h = (lane >> 3) & 1, i = lane & 7;
+      if (j >= nt) return false;
+      const int h = kSmall ? (lane >> 3) & 1 : lane & 1;
       const int base = block_row(sg, 2 * j + h);
-      const int key = base + i * rows_box;
-      t.id = p.num_blocks;   // outside the tensor map: the box is filled with zeros
-      // rows of the box that some token attends
-      const bool seen = lane < 16 && i < subs && base >= 0 && key <= sg.hi && (key < p.sinks || key + rows_box > sg.lo);
-      if (seen) {
-        const int id = p.block_table[(int64_t)sg.b * p.bt_stride + key / p.page];
-        if (id >= 0 && id < p.num_blocks)
-          t.id = id;
-        else
-          atomicOr(&g_pair_err, kErrDeviceData);
-      }
-      const int in_page = base >= 0 && subs == 1 ? base % p.page : 0;
-      t.row0 = __shfl_sync(0xffffffffu, in_page, 0);
-      t.row1 = __shfl_sync(0xffffffffu, in_page, 8);
-      t.first = j == sg.t0;
-      t.tok0 = sg.tok0;
-      if (++j == sg.t1) {
-        have = wk.next(p, sg);
-        j = have ? sg.t0 : 0;
-      }
-      return true;
-    };
-    bool ok = true;
-    // boxes of block h of a tile (columns 64c .. 64c + 63 for c in [c0, c1)) into dst
-    auto load_block = [&](const Tile& t, int h, int c0, int c1, unsigned char* dst, uint32_t bar, bool pair) {
-      for (int i = 0; i < subs; ++i) {
-        const int id = __shfl_sync(0xffffffffu, t.id, 8 * h + i);
-        if (lane == 0) {
-          for (int c = c0; c < c1; ++c) {
-            unsigned char* d = dst + (c - c0) * kBox + i * rows_box * 128;
-            if (pair)
-              tma_load_pair(d, &kvmap, bar, 64 * c, h ? t.row1 : t.row0, id);
-            else
-              asm volatile(
-                  "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-                  " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(d)),
-                  "l"(&kvmap), "r"(bar), "r"(64 * c), "r"(h ? t.row1 : t.row0), "r"(id)
-                  : "memory");
-          }
+      const int key = kSmall ? base + (lane & 7) * rows_box : base;
+      // a box with rows that some token attends (of a listed block of 64 rows: always)
+      t.seen = base >= 0 && lane < (kSmall ? 16 : 2) &&
+               (!kSmall || ((lane & 7) < subs && key <= sg.hi && (key < p.sinks || key + rows_box > sg.lo)));
+      int page = 0;
+      t.row = 0;
+      if (t.seen) {
+        page = key / kBlk;   // pages of 64 rows: the block itself
+        if (p.page != kBlk) {
+          page = key / p.page;
+          t.row = key - page * p.page;
         }
       }
+      t.id = t.seen ? p.block_table[(int64_t)sg.b * p.bt_stride + page] : -1;
+      t.first = fresh;
+      t.tok0 = sg.tok0;
+      fresh = false;
+      if (++j == nt) open();
+      return true;
     };
-    auto wait = [&](uint64_t* bar, int parity) {
-      if (lane == 0 && ok) ok = mbar_wait(bar, parity, abort);
-      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+    // an id outside the cache, and boxes nobody attends, load from outside the tensor map: zeros
+    auto settle = [&](Tile& t) {
+      if (t.id < 0 || t.id >= p.num_blocks) {
+        if (t.seen) atomicOr(&g_pair_err, kErrDeviceData);
+        t.id = p.num_blocks;
+      }
     };
-    auto load_keys = [&](const Tile& t, int g, int part) {   // boxes 2 * part, 2 * part + 1 of H0 and H1
-      const int b = g & 1;
-      if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&sh.full_k[b][part], 2 * 4 * kBox);
-      unsigned char* d = sKV + b * 8 * kBox;
-      const uint32_t bar = bar_k0 + (2 * b + part) * 8;
-      load_block(t, (int)rank, 2 * part, 2 * part + 2, d + 2 * part * kBox, bar, true);
-      load_block(t, (int)rank, 4 + 2 * part, 4 + 2 * part + 2, d + (4 + 2 * part) * kBox, bar, true);
+    auto wait = [&](uint64_t* bar, int parity) { ok = ok && __all_sync(0xffffffffu, wait_for(bar, parity, abort)); };
+    // block h of a tile, n column groups of 64 from group c on, one under the other from dst on;
+    // counted on the first CTA's barrier `pair`, or on `own`
+    auto load_block = [&](const Tile& t, int h, int c, int n, unsigned char* dst, uint32_t pair, uint64_t* own) {
+      if (kSmall) {
+        for (int i = 0; i < subs; ++i) {
+          const int id = __shfl_sync(0xffffffffu, t.id, 8 * h + i);
+          for (int k = 0; k < n; ++k) {
+            unsigned char* d = dst + k * kBox + i * rows_box * 128;
+            if (own != nullptr)
+              load_own_3d(d, &kvmap, own, 64 * (c + k), 0, id);
+            else
+              load_pair_3d(d, &kvmap, pair, 64 * (c + k), 0, id);
+          }
+        }
+        return;
+      }
+      const int id = __shfl_sync(0xffffffffu, t.id, h), r = __shfl_sync(0xffffffffu, t.row, h);
+      if (n == 1)
+        load_pair_3d(dst, &kvmap, pair, 64 * c, r, id);
+      else if (own != nullptr)
+        load_own_4d(dst, &kmap, own, r, c, id);
+      else
+        load_pair_4d(dst, &kmap, pair, r, c, id);
+    };
+    auto load_keys = [&](const Tile& t, int b, int half) {
+      if (rank == 0) expect_bytes(&sh.full_k[b][half], 2 * 4 * kBox);
+      load_block(t, (int)rank, 4 * half, 4, sKV + kv_box(b, half, 0), bar_k0 + (2 * b + half) * 8, nullptr);
+    };
+    // the other CTA's keys, columns of this CTA's half, in the place of its own keys' other half
+    auto load_values = [&](const Tile& t, int b) {
+      expect_bytes(&sh.full_w[b], 4 * kBox);
+      load_block(t, 1 - (int)rank, 4 * (int)rank, 4, sKV + kv_box(b, 1 - (int)rank, 0), 0, &sh.full_w[b]);
     };
     auto load_rope = [&](const Tile& t) {
       if (kRope == 0) return;
-      if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&sh.full_r, 2 * kBox);
-      load_block(t, (int)rank, 8, 9, sR, bar_r, true);
+      if (rank == 0) expect_bytes(&sh.full_r, 2 * kBox);
+      load_block(t, (int)rank, 8, 1, sR, bar_r, nullptr);
     };
     auto load_q = [&](const Tile& t) {
-      if (lane != 0) return;
-      const int hb = min(p.H, 64), toks = max(p.tptc, 1);
-      if (rank == 0) mbar_arrive_expect_tx(&sh.full_q, 2u * C::kQBoxes * hb * toks * 128);
-      for (int c = 0; c < C::kQBoxes; ++c)
-        tma_load_pair(sQ + c * kBox, &qmap, bar_q, 64 * c, p.tptc ? 0 : 64 * (int)rank, t.tok0 + p.tptc * (int)rank);
+      const int hb = min(p.H, 64), toks = max(p.tptc, 1), h0 = p.tptc ? 0 : 64 * (int)rank;
+      if (rank == 0) expect_bytes(&sh.full_q, 2u * C::kQBoxes * hb * toks * 128);
+      const int t0 = t.tok0 + p.tptc * (int)rank;
+      const int n = p.q_whole ? 1 : C::kQBoxes;
+#pragma unroll 1
+      for (int c = 0; c < n; ++c) load_pair_4d(sQ + c * kBox, &qmap, bar_q, h0, t0, c);
     };
-    Tile cur, nxt;
-    bool have_cur = fetch(cur);
+    // this CTA's keys into L2
+    auto prefetch_keys = [&](const Tile& t) {
+      if (kSmall) return;
+      const int id = __shfl_sync(0xffffffffu, t.id, (int)rank), r = __shfl_sync(0xffffffffu, t.row, (int)rank);
+#pragma unroll 1
+      for (int c = 0; c < 8; c += 4) prefetch_4d(&kmap, r, c, id);
+      if (kRope) prefetch_3d(&kvmap, 512, r, id);
+    };
+    // cur: the tile whose scores are awaited; t1: the next; t2: its id is on its way
+    Tile cur, t1, t2;
+    bool have_cur = fetch(cur), have1 = fetch(t1), have2 = fetch(t2);
     if (have_cur) {
+      settle(cur);
       load_q(cur);
-      load_rope(cur);
       load_keys(cur, 0, 0);
       load_keys(cur, 0, 1);
+      load_rope(cur);
     }
+    if (have1) {
+      settle(t1);
+      if (p.prefetch) prefetch_keys(t1);
+    }
+#pragma unroll 1
     for (int g = 0; ok && have_cur; ++g) {
       const int b = g & 1, ph = (g >> 1) & 1;
-      const bool have_nxt = fetch(nxt);
-      // the next tile's keys: their buffer is free once PV(g - 1) has read it
-      auto load_next = [&]() {
-        if (!have_nxt) return;
-        for (int part = 0; ok && part < 2; ++part) {
-          if (g > 0) wait(part ? &sh.pv_done[b ^ 1] : &sh.pv_half[b ^ 1], ((g - 1) >> 1) & 1);
-          if (ok) load_keys(nxt, g + 1, part);
+      // The next tile's keys: their buffer is free once PV(g - 1) has read it. PV(g - 1) comes before
+      // QK(g) at a segment's start, behind it else: two rounds, of which one waits for QK(g), in the
+      // order of the tensor pipe
+      const int first_round = cur.first ? 0 : 1;
+#pragma unroll 1
+      for (int round = 0; round < 2; ++round) {
+        if (round == first_round) {
+          if (have1) {
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+              if (g > 0) wait(half ? &sh.pv_done[b ^ 1] : &sh.pv_half[b ^ 1], ((g - 1) >> 1) & 1);
+              if (ok) load_keys(t1, b ^ 1, half);
+            }
+          }
+        } else {
+          wait(&sh.s_full[b], ph);
+          if (ok) {
+            load_values(cur, b);   // QK(g) is done with their place, the rope box and, at the end, Q
+            if (have1) {
+              load_rope(t1);
+              if (t1.first) load_q(t1);
+            }
+          }
         }
-      };
-      // PV(g - 1) comes before QK(g) at a segment's start, behind it else
-      const bool early = cur.first;
-      if (early) load_next();
-      if (ok) wait(&sh.s_full[b], ph);
-      if (!ok) break;
-      // QK(g) is done: the other CTA's keys' columns of this CTA's half take the place of the
-      // half that only QK(g) needed
-      if (lane == 0) mbar_arrive_expect_tx(&sh.full_w[b], 4 * kBox);
-      load_block(cur, 1 - (int)rank, 4 * (int)rank, 4 * (int)rank + 4, sKV + (b * 8 + 4 * (1 - (int)rank)) * kBox,
-                 smem_u32(&sh.full_w[b]), false);
-      if (have_nxt) {
-        load_rope(nxt);
-        if (nxt.first) load_q(nxt);
       }
-      if (!early) load_next();
-      cur = nxt;
-      have_cur = have_nxt;
+      cur = t1;
+      t1 = t2;
+      have_cur = have1;
+      have1 = have2;
+      if (have1) {
+        settle(t1);
+        if (p.prefetch) prefetch_keys(t1);
+      }
+      have2 = fetch(t2);
     }
     if (!ok) {
       // copies in flight land within microseconds: wait well beyond that before the CTA ends
@@ -408,87 +522,98 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       __syncwarp();
     }
   } else if (warp == 1 && rank == 0) {
-    // ------------------------------------------------------------ MMA issuer of the pair
+    // ------------------------------------------------------------ MMA issuer of the pair. Its loops
+    // stay loops (four MMAs a round, descriptors advanced by additions): unrolled over a tile they
+    // would not stay in the instruction cache beside the other warps' code
     constexpr uint32_t id_qk = idesc_bf16(128, kTileKeys, false, false);
     constexpr uint32_t id_pv = idesc_bf16(128, 256, false, true);
-    const uint32_t q0 = smem_u32(sQ), p0 = smem_u32(sP), kv0 = smem_u32(sKV), r0 = smem_u32(sR);
+    const uint64_t dq = sdesc_sw128(smem_u32(sQ), 16, 1024), dp = sdesc_sw128(smem_u32(sP), 16, 1024),
+                   dk = sdesc_sw128(smem_u32(sKV), 16, 1024), dv = sdesc_sw128(smem_u32(sKV), kBox, 1024),
+                   dr = sdesc_sw128(smem_u32(sR), 16, 1024);
+    constexpr int kStep = kBox / 16;   // one box, in a descriptor's 16-byte units
     Walker wk;
     wk.init(p, unit, units);
     Seg sg;
     int g = 0, seg_i = 0;
     bool ok = true, pv_first = true;   // pv_first: the pending PV starts its segment's O
     auto wait = [&](uint64_t* bar, int parity) {
-      ok = ok && __all_sync(0xffffffffu, mbar_wait<true>(bar, parity, abort));
+      ok = ok && __all_sync(0xffffffffu, wait_for(bar, parity, abort));
       return ok;
     };
-    auto issue_pv = [&](int x) {
+    auto qk = [&](int x) {
       const int b = x & 1;
-      if (!wait(&sh.p_full, x & 1)) return;
+      const uint32_t d = kTmemS + 64 * b;
+      uint64_t a = dq, k = dk + (uint64_t)(8 * b) * kStep;
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        if (!wait(&sh.full_k[b][half], (x >> 1) & 1)) return;
+        tc_fence_after();
+#pragma unroll
+        for (int i = 0; i < 4; ++i, a += kStep, k += kStep) umma_pair4(d, a, k, 2, 2, id_qk, half == 0 && i == 0);
+      }
+      if (kRope) {   // last: the one box that has no second buffer
+        if (!wait(&sh.full_r, x & 1)) return;
+        tc_fence_after();
+        umma_pair4(d, dq + 8 * kStep, dr, 2, 2, id_qk, false);
+      }
+      commit_pair(&sh.s_full[b]);
+    };
+    auto pv = [&](int x) {
+      const int b = x & 1;
+      if (!wait(&sh.p_full, b)) return;
       tc_fence_after();
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          umma_pair(tmem + 128 * i, sdesc_sw128(p0 + (kk >> 2) * kBox + (kk & 3) * 32, 16, 1024),
-                    sdesc_sw128(kv0 + (b * 8 + (kk >> 2) * 4 + 2 * i) * kBox + (kk & 3) * 2048, kBox, 1024), id_pv,
-                    !(pv_first && kk == 0));
-        commit_pair(i ? &sh.pv_done[b] : &sh.pv_half[b]);
+#pragma unroll 1
+      for (int i = 0; i < 4; ++i) {   // keys 64 (i / 2) .., columns 128 (i % 2) .. of each half
+        umma_pair4(128 * (i & 1), dp + (uint64_t)(i >> 1) * kStep, dv + (uint64_t)(8 * b + 4 * (i >> 1) + 2 * (i & 1)) * kStep,
+                   2, 128, id_pv, pv_first && i < 2);
+        if (i & 1) commit_pair(i == 1 ? &sh.pv_half[b] : &sh.pv_done[b]);
       }
     };
-    while (ok && wk.next(p, sg)) {
-      for (int j = sg.t0; ok && j < sg.t1; ++j, ++g) {
-        const int b = g & 1, ph = (g >> 1) & 1;
-        const uint32_t kb = kv0 + b * 8 * kBox, d = tmem + kTmemS + 64 * b;
-        if (j == sg.t0) {
-          if (g > 0) issue_pv(g - 1);
+    int t0 = 0, t1 = open_segment(wk, p, sg, t0);
+    while (ok && t0 < t1) {
+      for (int j = t0; ok && j < t1; ++j, ++g) {
+        if (j == t0) {
+          if (g > 0) pv(g - 1);
           if (!ok || !wait(&sh.full_q, seg_i & 1)) break;
-        }
-        if (kRope) {
-          if (!wait(&sh.full_r, g & 1)) break;
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_pair(d, sdesc_sw128(q0 + 8 * kBox + kk * 32, 16, 1024), sdesc_sw128(r0 + kk * 32, 16, 1024), id_qk,
-                      kk > 0);
-        }
-#pragma unroll
-        for (int part = 0; part < 2; ++part) {
-          if (!wait(&sh.full_k[b][part], ph)) break;
-          tc_fence_after();
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int box = 2 * part + (c & 1) + 4 * (c >> 1);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              umma_pair(d, sdesc_sw128(q0 + box * kBox + kk * 32, 16, 1024),
-                        sdesc_sw128(kb + box * kBox + kk * 32, 16, 1024), id_qk, kRope || part || c || kk);
-          }
-        }
-        if (!ok) break;
-        commit_pair(&sh.s_full[b]);
-        if (j > sg.t0) {
-          issue_pv(g - 1);
+          pv_first = true;
+          qk(g);
+        } else {
+          qk(g);
+          if (!ok) break;
+          pv(g - 1);
           pv_first = false;
         }
-        if (j == sg.t0) pv_first = true;
       }
       ++seg_i;
+      t1 = open_segment(wk, p, sg, t0);
     }
-    if (ok && g > 0) issue_pv(g - 1);
+    if (ok && g > 0) pv(g - 1);
     if (!ok && lane == 0) give_up();
     __syncwarp();
     commit_pair(&sh.fin);
   } else if (warp >= kSoftmaxWarp0) {
-    // ------------------------------------------------------------ softmax, rescaling, epilogue
-    const int ln = tid - kSoftmaxWarp0 * 32;            // tensor memory lane
+    // ------------------------------------------------------------ softmax, rescaling, epilogue: two
+    // threads a lane, each with half of the lane's columns
+    const int st = tid - kSoftmaxWarp0 * 32;
+    const int ln = st & 127, part = st >> 7;            // tensor memory lane; columns of this thread
     const int row = ln & 63, half = ln >> 6;            // this CTA's row; keys (S) and columns (O) of this lane
-    const uint32_t lane_addr = (uint32_t)((warp - kSoftmaxWarp0) * 32) << 16;
+    const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t bar_p = map_to_rank(&sh.p_full, 0);
     // the row's token within the tile and its head
     const int tok = p.tptc ? p.tptc * (int)rank + row / p.H : 0;
     const int head = p.tptc ? row % p.H : 64 * (int)rank + row;
     const bool real = p.tptc ? row < p.tptc * p.H : head < p.H;
-    auto group_all = [](bool v) { return named_bar_and(kSoftmaxBar, 128, v); };
+    auto group_all = [](bool v) { return named_bar_and(kSoftmaxBar, kSoftmaxThreads, v); };
+    // the two rows this thread stores in the epilogue: token (none: beyond every tile) and offset
+    int out_tok[2];
+    int64_t out_off[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int rr = (st >> 3) + 32 * k;
+      const int t = p.tptc ? p.tptc * (int)rank + rr / p.H : 0, h = p.tptc ? rr % p.H : 64 * (int)rank + rr;
+      out_tok[k] = (p.tptc ? rr < p.tptc * p.H : h < p.H) ? t : kTileKeys;
+      out_off[k] = t * p.o_s0 + h * p.o_s1;
+    }
     Walker wk;
     wk.init(p, unit, units);
     Seg sg;
@@ -500,33 +625,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       float m = -CUDART_INF_F, l = 0.f;
       for (int j = sg.t0; j < sg.t1; ++j, ++g) {
         const int b = g & 1, ph = (g >> 1) & 1;
-        mine = mine && mbar_wait(&sh.s_full[b], ph, abort);
+        mine = mine && wait_for(&sh.s_full[b], ph, abort);
         tc_fence_after();
-        float sv[64];
-        tmem_ld32(tmem + lane_addr + kTmemS + 64 * b, *reinterpret_cast<float(*)[32]>(sv));
-        tmem_ld32(tmem + lane_addr + kTmemS + 64 * b + 32, *reinterpret_cast<float(*)[32]>(sv + 32));
+        float sv[32];
+        tmem_ld32(tmem + lane_addr + kTmemS + 64 * b + 32 * part, sv);
         tmem_ld_wait();
-        const int kb = block_row(sg, 2 * j + half);
-        const bool whole = kb >= 0 && kb + kBlk - 1 <= pos && (kb + kBlk <= p.sinks || kb > pos - p.window);
+        const int blk = block_row(sg, 2 * j + half);
+        const int kb = blk + 32 * part;                 // this thread's first key
+        const bool whole = blk >= 0 && kb + 31 <= pos && (kb + 32 <= p.sinks || kb > pos - p.window);
         if (!__all_sync(0xffffffffu, whole)) {
 #pragma unroll
-          for (int k = 0; k < 64; ++k) {
+          for (int k = 0; k < 32; ++k) {
             const int t = kb + k;
-            const bool seen = kb >= 0 && t <= pos && (t < p.sinks || t > pos - p.window);
+            const bool seen = blk >= 0 && t <= pos && (t < p.sinks || t > pos - p.window);
             sv[k] = seen ? sv[k] : -CUDART_INF_F;
           }
         }
-        float mx[8];
+        float mx[4];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) mx[k] = sv[k];
+        for (int k = 0; k < 4; ++k) mx[k] = sv[k];
 #pragma unroll
-        for (int k = 8; k < 64; ++k) mx[k & 7] = fmaxf(mx[k & 7], sv[k]);
-        const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                                fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
-        sh.smax[g & 1][ln] = top;
-        ok = group_all(mine);   // the one group decision of a tile; the maxima of both halves
+        for (int k = 4; k < 32; ++k) mx[k & 3] = fmaxf(mx[k & 3], sv[k]);
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        sh.red[g & 1][part][ln] = top;
+        ok = group_all(mine);                // the one group decision of a tile; the row's four maxima
         if (!ok) break;
-        const float mt = fmaxf(top, sh.smax[g & 1][ln ^ 64]) * p.scale_log2;
+        const float mt = fmaxf(fmaxf(top, sh.red[g & 1][part ^ 1][ln]),
+                               fmaxf(sh.red[g & 1][0][ln ^ 64], sh.red[g & 1][1][ln ^ 64])) * p.scale_log2;
         float alpha = 1.f;
         if (mt > m + kLazyRescale || (m == -CUDART_INF_F && mt > -CUDART_INF_F)) {
           alpha = m == -CUDART_INF_F ? 0.f : ex2_approx(m - mt);
@@ -534,10 +659,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         const float ref = m == -CUDART_INF_F ? 0.f : -m;
         l *= alpha;
-        uint32_t pk[32];
+        uint32_t pk[16];
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int k = 0; k < 64; k += 2) {
+        for (int k = 0; k < 32; k += 2) {
           const float e0 = ex2_approx(fmaf(sv[k], p.scale_log2, ref));
           const float e1 = ex2_approx(fmaf(sv[k + 1], p.scale_log2, ref));
           sum[(k >> 1) & 3] += e0 + e1;
@@ -546,10 +671,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         // P(g) takes P(g - 1)'s place and O is rescaled once PV(g - 1) is done
-        if (g > 0) mine = mine && mbar_wait(&sh.pv_done[b ^ 1], ((g - 1) >> 1) & 1, abort);
+        if (g > 0) mine = mine && wait_for(&sh.pv_done[b ^ 1], ((g - 1) >> 1) & 1, abort);
         tc_fence_after();
         if (__any_sync(0xffffffffu, alpha != 1.f && j > sg.t0)) {
-          for (int c = 0; c < 256; c += 32) {
+          for (int c = 128 * part; c < 128 * part + 128; c += 32) {
             float v[32];
             tmem_ld32(tmem + lane_addr + c, v);
             tmem_ld_wait();
@@ -560,11 +685,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tmem_st_wait();
         }
 #pragma unroll
-        for (int ch = 0; ch < 8; ++ch)
-          *reinterpret_cast<uint4*>(sP + half * kBox + row * 128 + ((ch ^ (row & 7)) << 4)) =
+        for (int ch = 0; ch < 4; ++ch)
+          *reinterpret_cast<uint4*>(sP + half * kBox + row * 128 + (((4 * part + ch) ^ (row & 7)) << 4)) =
               make_uint4(pk[4 * ch], pk[4 * ch + 1], pk[4 * ch + 2], pk[4 * ch + 3]);
         // the other CTA's keys' values are here (the issuer does not wait for them itself)
-        mine = mine && mbar_wait(&sh.full_w[b], ph, abort);
+        mine = mine && wait_for(&sh.full_w[b], ph, abort);
         // rows that no token attends: their weights are zero, and so must their values be,
         // whatever the cache holds there
 #pragma unroll
@@ -573,53 +698,81 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (base < 0 || (base + kBlk - 1 <= sg.hi && (base + kBlk <= p.sinks || base >= sg.lo))) continue;
           const int t = base + row;
           if (!(t <= sg.hi && (t < p.sinks || t >= sg.lo))) {
-            unsigned char* v = sKV + (b * 8 + 4 * h + 2 * half) * kBox + row * 128;
+            unsigned char* v = sKV + kv_box(b, h, 2 * half + part) + row * 128;
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              *reinterpret_cast<uint4*>(v + (i >> 3) * kBox + (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(v + i * 16) = make_uint4(0u, 0u, 0u, 0u);
           }
         }
-        asm volatile("fence.proxy.async.shared::cluster;" ::: "memory");
+        fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_cluster(bar_p);
+        // the writes this answers for are complete (each lane's fence, then the warp's barrier): a
+        // relaxed arrive on the other CTA's barrier orders nothing more. A release at cluster scope
+        // waits for all the CTA's copies in flight: 2200 to 3500 cycles a tile
+        if (lane == 0) {
+          if (rank == 0)
+            mbar_arrive(&sh.p_full);
+          else
+            asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_p) : "memory");
+        }
       }
       if (!ok) break;
       // ---- O / l
       const int last = g - 1;
-      mine = mine && mbar_wait(&sh.pv_done[last & 1], (last >> 1) & 1, abort);
-      sh.lsum[ln] = l;
+      mine = mine && wait_for(&sh.pv_done[last & 1], (last >> 1) & 1, abort);
+      sh.red[g & 1][part][ln] = l;         // the parity of the tile before the last: nobody reads it
       ok = group_all(mine);
       if (!ok) break;
       tc_fence_after();
-      l += sh.lsum[ln ^ 64];
+      const float (&sums)[2][128] = sh.red[g & 1];
+      l = (sums[0][ln] + sums[1][ln]) + (sums[0][ln ^ 64] + sums[1][ln ^ 64]);
+      named_bar(kSoftmaxBar, kSoftmaxThreads);   // read before the next tile's maxima take its place
       const float inv = l > 0.f ? 1.f / l : 0.f;
-      __nv_bfloat16* o = p.o_lat + (int64_t)(sg.tok0 + tok) * p.o_s0 + (int64_t)head * p.o_s1 + 256 * half;
-      const int64_t prow = (int64_t)sg.slot * 128 + tok * p.H + head;
+      const int64_t prow = (int64_t)sg.slot * 128 + 64 * rank + row;
+      // through P's place, 128 bytes of every row of both halves a round (64 bf16 columns, or 32
+      // float32 ones of a partial), so that eight lanes store a whole line: straight from the lanes'
+      // rows a store would touch 32 lines
+      const int rounds = sg.slot < 0 ? 4 : 8;
+      unsigned char* put = sP + half * kBox + row * 128;
 #pragma unroll 1
-      for (int c = 0; c < 256; c += 32) {
-        float v[32];
-        tmem_ld32(tmem + lane_addr + c, v);
-        tmem_ld_wait();
-        if (valid && sg.slot < 0) {
+      for (int r = 0; r < rounds; ++r) {
+        if (sg.slot < 0) {
+          float v[32];
+          tmem_ld32(tmem + lane_addr + 64 * r + 32 * part, v);
+          tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 32; i += 8) {
+          for (int ch = 0; ch < 4; ++ch) {
             uint4 w;
             __nv_bfloat162* h2 = reinterpret_cast<__nv_bfloat162*>(&w);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) h2[k] = __floats2bfloat162_rn(v[i + 2 * k] * inv, v[i + 2 * k + 1] * inv);
-            *reinterpret_cast<uint4*>(o + c + i) = w;
+            for (int k = 0; k < 4; ++k) h2[k] = __floats2bfloat162_rn(v[8 * ch + 2 * k] * inv, v[8 * ch + 2 * k + 1] * inv);
+            *reinterpret_cast<uint4*>(put + (((4 * part + ch) ^ (row & 7)) << 4)) = w;
           }
-        } else if (valid) {
-          float* q = p.part_o + prow * 512 + 256 * half + c;
+        } else {
+          float v[16];
+          tmem_ld16(tmem + lane_addr + 32 * r + 16 * part, v);
+          tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<float4*>(q + i) =
-                make_float4(v[i] * inv, v[i + 1] * inv, v[i + 2] * inv, v[i + 3] * inv);
+          for (int ch = 0; ch < 4; ++ch)
+            *reinterpret_cast<float4*>(put + (((4 * part + ch) ^ (row & 7)) << 4)) =
+                make_float4(v[4 * ch] * inv, v[4 * ch + 1] * inv, v[4 * ch + 2] * inv, v[4 * ch + 3] * inv);
         }
-        __syncwarp();
+        named_bar(kSoftmaxBar, kSoftmaxThreads);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {   // rows (st >> 3) + 32 k of the two halves, chunk st & 7
+          const int rr = ((st >> 3) + 32 * k) & 63, hf = k >> 1;
+          if (out_tok[k & 1] >= sg.ntok) continue;
+          const uint4 w = *reinterpret_cast<const uint4*>(sP + hf * kBox + rr * 128 + (((st & 7) ^ (rr & 7)) << 4));
+          if (sg.slot < 0)
+            *reinterpret_cast<uint4*>(p.o_lat + (int64_t)sg.tok0 * p.o_s0 + out_off[k & 1] + 256 * hf + 64 * r +
+                                      8 * (st & 7)) = w;
+          else
+            *reinterpret_cast<uint4*>(p.part_o + ((int64_t)sg.slot * 128 + 64 * rank + rr) * 512 + 256 * hf + 32 * r +
+                                      4 * (st & 7)) = w;
+        }
+        named_bar(kSoftmaxBar, kSoftmaxThreads);   // read before the next round's, or the next tile's P
       }
-      if (valid && half == 0) {
+      if (valid && half == 0 && part == 0) {
         const float lse = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -CUDART_INF_F;
         if (sg.slot >= 0)
           p.part_lse[prow] = lse;
@@ -807,9 +960,12 @@ __global__ void __launch_bounds__(128) pair_combine_kernel(PairParams p, int uni
   const int2 at = p.unit_start[u], before = p.unit_start[u - 1];
   if (at.x >= *p.total || at.y == 0 || (before.x == at.x && before.y > 0)) return;
   const int4 d = p.items[at.x];
-  const int row = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int t = row / p.H, h = row - t * p.H;
-  if (t >= d.y) return;
+  const int lane = threadIdx.x & 31;
+  // row rr of CTA `rank` of the tile, its token and head
+  const int rank = blockIdx.y & 1, rr = (blockIdx.y >> 1) * 4 + (threadIdx.x >> 5);
+  const int t = p.tptc ? p.tptc * rank + rr / p.H : 0, h = p.tptc ? rr % p.H : 64 * rank + rr;
+  if ((p.tptc && rr >= p.tptc * p.H) || h >= p.H || t >= d.y) return;
+  const int row = 64 * rank + rr;
   // pieces: the head in unit u - 1 (slot 2 (u - 1) + 1), then units u, u + 1, ... (slots 2 v)
   int np = 1;
   while (u + np <= units) {
@@ -826,10 +982,9 @@ __global__ void __launch_bounds__(128) pair_combine_kernel(PairParams p, int uni
     const float li = p.part_lse[slot(i) * 128 + row];
     const float w = li == -CUDART_INF_F ? 0.f : __expf(li - m);
     tot += w;
-    const float* src = p.part_o + (slot(i) * 128 + row) * 512 + lane * 4;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float4 v = *reinterpret_cast<const float4*>(src + 128 * k);
+      const float4 v = *reinterpret_cast<const float4*>(p.part_o + (slot(i) * 128 + row) * 512 + 128 * k + 4 * lane);
       acc[k].x = fmaf(w, v.x, acc[k].x);
       acc[k].y = fmaf(w, v.y, acc[k].y);
       acc[k].z = fmaf(w, v.z, acc[k].z);
@@ -837,7 +992,7 @@ __global__ void __launch_bounds__(128) pair_combine_kernel(PairParams p, int uni
     }
   }
   const float inv = tot > 0.f ? 1.f / tot : 0.f;
-  __nv_bfloat16* o = p.o_lat + (int64_t)(d.x + t) * p.o_s0 + (int64_t)h * p.o_s1 + lane * 4;
+  __nv_bfloat16* o = p.o_lat + (int64_t)(d.x + t) * p.o_s0 + (int64_t)h * p.o_s1 + 4 * lane;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const __nv_bfloat162 a = __floats2bfloat162_rn(acc[k].x * inv, acc[k].y * inv);
@@ -849,7 +1004,7 @@ __global__ void __launch_bounds__(128) pair_combine_kernel(PairParams p, int uni
     p.lse[(int64_t)(d.x + t) * p.H + h] = tot > 0.f ? m + logf(tot) : -CUDART_INF_F;
 }
 
-template <int kRope>
+template <int kRope, bool kSmall>
 int max_pairs() {
   static std::mutex mu;
   static std::vector<int> cache;
@@ -859,7 +1014,7 @@ int max_pairs() {
   if ((int)cache.size() <= dev) cache.resize(dev + 1, 0);
   if (cache[dev] == 0) {
     using C = PairCfg<kRope>;
-    cudaFuncSetAttribute(window_attn_kernel<kRope>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemAlloc);
+    cudaFuncSetAttribute(window_attn_kernel<kRope, kSmall>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemAlloc);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * device_sm_count(), 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
@@ -872,7 +1027,7 @@ int max_pairs() {
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, window_attn_kernel<kRope>, &cfg) != cudaSuccess || n <= 0)
+    if (cudaOccupancyMaxActiveClusters(&n, window_attn_kernel<kRope, kSmall>, &cfg) != cudaSuccess || n <= 0)
       n = device_sm_count() / 2;
     cudaGetLastError();
     cache[dev] = n;
@@ -880,13 +1035,14 @@ int max_pairs() {
   return cache[dev];
 }
 
-template <int kRope>
-cudaError_t launch_attn(const PairParams& p, const CUtensorMap& km, const CUtensorMap& qm, int units, cudaStream_t st) {
+template <int kRope, bool kSmall>
+cudaError_t launch_attn(const PairParams& p, const CUtensorMap (&maps)[3], int units, cudaStream_t st) {
   using C = PairCfg<kRope>;
-  const cudaError_t e = cudaFuncSetAttribute(window_attn_kernel<kRope>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  const cudaError_t e = cudaFuncSetAttribute(window_attn_kernel<kRope, kSmall>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              C::kSmemAlloc);
   if (e != cudaSuccess) return e;
-  return launch_k(window_attn_kernel<kRope>, dim3(2 * units), dim3(kThreads), C::kSmemAlloc, st, km, qm, p);
+  return launch_k(window_attn_kernel<kRope, kSmall>, dim3(2 * units), dim3(kThreads), C::kSmemAlloc, st, maps[0], maps[1], maps[2],
+                  p);
 }
 
 int pair_tokens(int H) { return H > 64 ? 1 : 2 * (64 / H); }
@@ -915,14 +1071,23 @@ int64_t most_items(int64_t T, int64_t B, int H, bool decode) {
   return tpt == 1 ? T : std::min<int64_t>(T, T / tpt + B);
 }
 
-bool pair_maps(const WindowCall& c, CUtensorMap* km, CUtensorMap* qm) {
-  const int E = c.L + c.R;
-  const uint32_t rows_box = c.cache.page < kBlk ? c.cache.page : kBlk;
-  const uint32_t hb = c.H < 64 ? c.H : 64, toks = c.H > 64 ? 1 : 64 / c.H;
-  return make_map3d(km, c.cache.data, E, c.cache.page, c.cache.num_blocks, (uint64_t)c.cache.s_row * 2,
-                    (uint64_t)c.cache.s_blk * 2, 64, rows_box, 1, CU_TENSOR_MAP_SWIZZLE_128B) &&
-         make_map3d(qm, c.q.data, E, c.H, c.q.n0, (uint64_t)c.q.s1 * 2, (uint64_t)c.q.s0 * 2, 64, hb, toks,
-                    CU_TENSOR_MAP_SWIZZLE_128B);
+// Whether a CTA's queries fill its 64 rows, so that one load lays all their column groups out.
+bool q_whole(int H) { return H >= 64 || 64 % H == 0; }
+
+// Tensor maps: [0] four column groups of 64 of a block, for pages of 64 rows or more; [1] one group of
+// a block or a page; [2] queries.
+bool pair_maps(const WindowCall& c, CUtensorMap (&maps)[3]) {
+  const uint64_t row = (uint64_t)c.cache.s_row * 2, blk = (uint64_t)c.cache.s_blk * 2, page = c.cache.page,
+                 blocks = c.cache.num_blocks, groups = (c.L + c.R) / 64, H = c.H, T = c.q.n0;
+  const uint32_t rows = page < kBlk ? (uint32_t)page : kBlk, hb = H < 64 ? (uint32_t)H : 64, toks = H > 64 ? 1 : 64 / hb;
+  constexpr auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  const uint64_t kd[4] = {64, page, 8, blocks}, ks[3] = {row, 128, blk};
+  const uint32_t kb[4] = {64, rows, 4, 1};
+  const uint64_t qd[4] = {64, H, T, groups}, qs[3] = {(uint64_t)c.q.s1 * 2, (uint64_t)c.q.s0 * 2, 128};
+  const uint32_t qb[4] = {64, hb, toks, q_whole(c.H) ? (uint32_t)groups : 1};
+  return make_map(&maps[0], c.cache.data, 4, kd, ks, kb, sw) &&
+         make_map3d(&maps[1], c.cache.data, 64 * groups, page, blocks, row, blk, 64, rows, 1, sw) &&
+         make_map(&maps[2], c.q.data, 4, qd, qs, qb, sw);
 }
 
 }  // namespace
@@ -935,20 +1100,20 @@ bool window_tc_supported(mla_dtype dt, const WindowCall& c) {
   if (!al16(c.cache.data) || c.cache.s_blk % 8 || c.cache.s_row % 8) return false;
   if (!al16(c.q.data) || c.q.s0 % 8 || c.q.s1 % 8) return false;
   if (!al16(c.o.data) || c.o.s0 % 8 || c.o.s1 % 8) return false;
-  CUtensorMap km, qm;
-  return pair_maps(c, &km, &qm);
+  CUtensorMap maps[3];
+  return pair_maps(c, maps);
 }
 
 size_t window_tc_workspace(int64_t T, int64_t B, int H, bool decode, int num_splits) {
   if (H <= 0 || H > 128) return 0;
-  return pair_ws(most_items(T, B, H, decode), B, num_splits > 0 ? num_splits : max_pairs<64>()).total;
+  return pair_ws(most_items(T, B, H, decode), B, num_splits > 0 ? num_splits : max_pairs<64, false>()).total;
 }
 
 cudaError_t launch_window_tc(const WindowCall& c, int num_splits, void* ws, cudaStream_t st) {
-  CUtensorMap km, qm;
-  if (!pair_maps(c, &km, &qm)) return cudaErrorInvalidValue;
+  CUtensorMap maps[3];
+  if (!pair_maps(c, maps)) return cudaErrorInvalidValue;
   const bool decode = c.cu_q == nullptr;
-  const int units = num_splits > 0 ? num_splits : max_pairs<64>();
+  const int units = num_splits > 0 ? num_splits : max_pairs<64, false>();
   const int64_t items = most_items(c.q.n0, c.B, c.H, decode);
   const PairWs w = pair_ws(items, c.B, units);
   char* base = static_cast<char*>(ws);
@@ -988,9 +1153,14 @@ cudaError_t launch_window_tc(const WindowCall& c, int num_splits, void* ws, cuda
   p.unit_start = split ? s.unit_start : nullptr;
   p.part_o = reinterpret_cast<float*>(base + w.off_o);
   p.part_lse = reinterpret_cast<float*>(base + w.off_lse);
-  e = c.R == 64 ? launch_attn<64>(p, km, qm, units, st) : launch_attn<0>(p, km, qm, units, st);
+  p.prefetch = split;
+  p.q_whole = q_whole(c.H);
+  if (p.page < kBlk)
+    e = c.R == 64 ? launch_attn<64, true>(p, maps, units, st) : launch_attn<0, true>(p, maps, units, st);
+  else
+    e = c.R == 64 ? launch_attn<64, false>(p, maps, units, st) : launch_attn<0, false>(p, maps, units, st);
   if (e != cudaSuccess || !split || units < 2) return e;
-  return launch_k(pair_combine_kernel, dim3(units - 1, (s.tpt * c.H + 3) / 4), 128, 0, st, p, units);
+  return launch_k(pair_combine_kernel, dim3(units - 1, 32), 128, 0, st, p, units);
 }
 
 unsigned attn_pair_errors_read_clear() {
