@@ -80,12 +80,12 @@ struct PairCfg {
 __host__ __device__ constexpr int kv_box(int b, int h, int c) { return (b * 8 + h * 4 + c) * kBox; }
 
 struct PairShared {
-  uint64_t full_k[2][2];   // [tile][half] first CTA: H0 / H1 of both CTAs have landed
+  uint64_t full_k[2][4];   // [tile][quarter] first CTA: two boxes of H0 (quarters 0, 1) or H1 of both CTAs
   uint64_t full_r, full_q; // first CTA: the rope box, the queries, of both CTAs
   uint64_t full_w[2];      // own W boxes
   uint64_t s_full[2];      // scores of a tile are in tensor memory (and its Q, R and short half are read)
-  uint64_t pv_half[2];     // the values of a tile's keys 0..63 (in the place of H0) are read
-  uint64_t pv_done[2];     // the tile's values and P are read, O is updated
+  uint64_t pv_done[2][4];  // [tile][quarter] the values in the place of that quarter are read; the last:
+                           // and P is, O is updated
   uint64_t p_full;         // first CTA: P of both CTAs is written, O rescaled
   uint64_t fin;
   uint32_t tmem_base;
@@ -200,9 +200,22 @@ __device__ __forceinline__ int block_row(const Seg& s, int j) {
 }
 
 // The wait behind a first look, kept out of line: the roles' loops have to stay in the instruction
-// cache together.
+// cache together. The timer, slow to read, is read only every 256 looks.
 __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  return mbar_wait<true>(bar, parity, abort);
+  uint64_t since = 0;
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_test_cluster(bar, parity)) return true;
+    if ((i & 255u) == 0) {
+      if (*abort) return false;
+      const uint64_t now = globaltimer_ns();
+      if (since == 0) {
+        since = now;
+      } else if (now - since > kWaitLimitNs) {
+        *abort = 1;
+        return false;
+      }
+    }
+  }
 }
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort) {
   return mbar_test_cluster(bar, parity) || wait_slow(bar, parity, abort);
@@ -316,12 +329,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.full_k[i][0], 1);
-      mbar_init(&sh.full_k[i][1], 1);
+      for (int q = 0; q < 4; ++q) {
+        mbar_init(&sh.full_k[i][q], 1);
+        mbar_init(&sh.pv_done[i][q], 1);
+      }
       mbar_init(&sh.full_w[i], 1);
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.pv_half[i], 1);
-      mbar_init(&sh.pv_done[i], 1);
     }
     mbar_init(&sh.full_r, 1);
     mbar_init(&sh.full_q, 1);
@@ -348,13 +361,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(remote), "r"(1) : "memory");
   };
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ loads, in both CTAs. The whole
-    // warp walks the tiles. Lane h looks up the block id of a tile's block h (small pages: lanes
-    // 8h .. 8h + 7 the ids of its pages).
+  if (warp == 0 || warp == 3) {
+    // ------------------------------------------------------------ loads, in both CTAs: warp 0 the keys,
+    // which the tensor pipe waits for, warp 3 the rest. The whole warp walks the tiles. Lane h looks
+    // up the block id of a tile's block h (small pages: lanes 8h .. 8h + 7 the ids of its pages).
     const int rows_box = kSmall ? p.page : kBlk, subs = kBlk / rows_box;
-    const uint32_t bar_k0 = map_to_rank(&sh.full_k[0][0], 0), bar_r = map_to_rank(&sh.full_r, 0),
-                   bar_q = map_to_rank(&sh.full_q, 0);
     Walker wk;
     wk.init(p, unit, units);
     Seg sg;
@@ -405,111 +416,110 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     };
     auto wait = [&](uint64_t* bar, int parity) { ok = ok && __all_sync(0xffffffffu, wait_for(bar, parity, abort)); };
-    // block h of a tile, n column groups of 64 from group c on, one under the other from dst on;
-    // counted on the first CTA's barrier `pair`, or on `own`
-    auto load_block = [&](const Tile& t, int h, int c, int n, unsigned char* dst, uint32_t pair, uint64_t* own) {
-      if (kSmall) {
-        for (int i = 0; i < subs; ++i) {
-          const int id = __shfl_sync(0xffffffffu, t.id, 8 * h + i);
-          for (int k = 0; k < n; ++k) {
-            unsigned char* d = dst + k * kBox + i * rows_box * 128;
-            if (own != nullptr)
-              load_own_3d(d, &kvmap, own, 64 * (c + k), 0, id);
-            else
-              load_pair_3d(d, &kvmap, pair, 64 * (c + k), 0, id);
-          }
+    // column groups c .. c + n - 1 of 64 of block h of a tile, one under the other from dst on; counted
+    // on the first CTA's barrier `pair`, or on `own`. Small pages: box by box.
+    auto load_small = [&](const Tile& t, int h, int c, int n, unsigned char* dst, uint32_t pair, uint64_t* own) {
+#pragma unroll 1
+      for (int i = 0; i < subs; ++i) {
+        const int id = __shfl_sync(0xffffffffu, t.id, 8 * h + i);
+#pragma unroll 1
+        for (int k = 0; k < n; ++k) {
+          unsigned char* d = dst + k * kBox + i * rows_box * 128;
+          if (own != nullptr)
+            load_own_3d(d, &kvmap, own, 64 * (c + k), 0, id);
+          else
+            load_pair_3d(d, &kvmap, pair, 64 * (c + k), 0, id);
         }
-        return;
       }
-      const int id = __shfl_sync(0xffffffffu, t.id, h), r = __shfl_sync(0xffffffffu, t.row, h);
-      if (n == 1)
-        load_pair_3d(dst, &kvmap, pair, 64 * c, r, id);
-      else if (own != nullptr)
-        load_own_4d(dst, &kmap, own, r, c, id);
-      else
-        load_pair_4d(dst, &kmap, pair, r, c, id);
     };
-    auto load_keys = [&](const Tile& t, int b, int half) {
-      if (rank == 0) expect_bytes(&sh.full_k[b][half], 2 * 4 * kBox);
-      load_block(t, (int)rank, 4 * half, 4, sKV + kv_box(b, half, 0), bar_k0 + (2 * b + half) * 8, nullptr);
-    };
-    // the other CTA's keys, columns of this CTA's half, in the place of its own keys' other half
-    auto load_values = [&](const Tile& t, int b) {
-      expect_bytes(&sh.full_w[b], 4 * kBox);
-      load_block(t, 1 - (int)rank, 4 * (int)rank, 4, sKV + kv_box(b, 1 - (int)rank, 0), 0, &sh.full_w[b]);
-    };
-    auto load_rope = [&](const Tile& t) {
-      if (kRope == 0) return;
-      if (rank == 0) expect_bytes(&sh.full_r, 2 * kBox);
-      load_block(t, (int)rank, 8, 1, sR, bar_r, nullptr);
-    };
-    auto load_q = [&](const Tile& t) {
-      const int hb = min(p.H, 64), toks = max(p.tptc, 1), h0 = p.tptc ? 0 : 64 * (int)rank;
-      if (rank == 0) expect_bytes(&sh.full_q, 2u * C::kQBoxes * hb * toks * 128);
-      const int t0 = t.tok0 + p.tptc * (int)rank;
-      const int n = p.q_whole ? 1 : C::kQBoxes;
-#pragma unroll 1
-      for (int c = 0; c < n; ++c) load_pair_4d(sQ + c * kBox, &qmap, bar_q, h0, t0, c);
-    };
-    // this CTA's keys into L2
-    auto prefetch_keys = [&](const Tile& t) {
-      if (kSmall) return;
-      const int id = __shfl_sync(0xffffffffu, t.id, (int)rank), r = __shfl_sync(0xffffffffu, t.row, (int)rank);
-#pragma unroll 1
-      for (int c = 0; c < 8; c += 4) prefetch_4d(&kmap, r, c, id);
-      if (kRope) prefetch_3d(&kvmap, 512, r, id);
-    };
-    // cur: the tile whose scores are awaited; t1: the next; t2: its id is on its way
+    // a tile whose id is settled, the next, and one whose id is on its way
     Tile cur, t1, t2;
     bool have_cur = fetch(cur), have1 = fetch(t1), have2 = fetch(t2);
-    if (have_cur) {
-      settle(cur);
-      load_q(cur);
-      load_keys(cur, 0, 0);
-      load_keys(cur, 0, 1);
-      load_rope(cur);
-    }
-    if (have1) {
-      settle(t1);
-      if (p.prefetch) prefetch_keys(t1);
-    }
-#pragma unroll 1
-    for (int g = 0; ok && have_cur; ++g) {
-      const int b = g & 1, ph = (g >> 1) & 1;
-      // The next tile's keys: their buffer is free once PV(g - 1) has read it. PV(g - 1) comes before
-      // QK(g) at a segment's start, behind it else: two rounds, of which one waits for QK(g), in the
-      // order of the tensor pipe
-      const int first_round = cur.first ? 0 : 1;
-#pragma unroll 1
-      for (int round = 0; round < 2; ++round) {
-        if (round == first_round) {
-          if (have1) {
-#pragma unroll 1
-            for (int half = 0; half < 2; ++half) {
-              if (g > 0) wait(half ? &sh.pv_done[b ^ 1] : &sh.pv_half[b ^ 1], ((g - 1) >> 1) & 1);
-              if (ok) load_keys(t1, b ^ 1, half);
-            }
-          }
-        } else {
-          wait(&sh.s_full[b], ph);
-          if (ok) {
-            load_values(cur, b);   // QK(g) is done with their place, the rope box and, at the end, Q
-            if (have1) {
-              load_rope(t1);
-              if (t1.first) load_q(t1);
-            }
-          }
-        }
-      }
+    if (have_cur) settle(cur);
+    if (have1) settle(t1);
+    auto advance = [&]() {
       cur = t1;
       t1 = t2;
       have_cur = have1;
       have1 = have2;
-      if (have1) {
-        settle(t1);
-        if (p.prefetch) prefetch_keys(t1);
-      }
+      if (have1) settle(t1);
       have2 = fetch(t2);
+    };
+    if (warp == 0) {
+      const uint32_t bar0 = map_to_rank(&sh.full_k[0][0], 0);
+#pragma unroll 1
+      for (int g = 0; ok && have_cur; ++g) {
+        const int b = g & 1;
+        const int id = __shfl_sync(0xffffffffu, cur.id, (int)rank), r = __shfl_sync(0xffffffffu, cur.row, (int)rank);
+        // a quarter as soon as PV(g - 2) has read what lies there; QK(g) takes them in the same order
+#pragma unroll 1
+        for (int q = 0; ok && q < 4; ++q) {
+          if (g > 1) wait(&sh.pv_done[b][q], ((g >> 1) & 1) ^ 1);
+          if (!ok) break;
+          unsigned char* d = sKV + (8 * b + 2 * q) * kBox;
+          const uint32_t bar = bar0 + (4 * b + q) * 8;
+          if (kSmall)
+            load_small(cur, (int)rank, 2 * q, 2, d, bar, nullptr);
+          else
+            load_pair_4d(d, &kmap, bar, r, 2 * q, id);
+          if (rank == 0) expect_bytes(&sh.full_k[b][q], 2 * 2 * kBox);
+        }
+        advance();
+      }
+    } else {
+      const uint32_t bar_r = map_to_rank(&sh.full_r, 0), bar_q = map_to_rank(&sh.full_q, 0);
+      const int own_h = (int)rank, other = 1 - own_h;
+      auto load_rope = [&](const Tile& t) {
+        if (kRope == 0) return;
+        if (kSmall)
+          load_small(t, own_h, 8, 1, sR, bar_r, nullptr);
+        else
+          load_pair_3d(sR, &kvmap, bar_r, 512, __shfl_sync(0xffffffffu, t.row, own_h),
+                       __shfl_sync(0xffffffffu, t.id, own_h));
+        if (rank == 0) expect_bytes(&sh.full_r, 2 * kBox);
+      };
+      auto load_q = [&](const Tile& t) {
+        const int hb = min(p.H, 64), toks = max(p.tptc, 1), h0 = p.tptc ? 0 : 64 * (int)rank;
+        const int t0 = t.tok0 + p.tptc * (int)rank;
+        const int n = p.q_whole ? 1 : C::kQBoxes;
+#pragma unroll 1
+        for (int c = 0; c < n; ++c) load_pair_4d(sQ + c * kBox, &qmap, bar_q, h0, t0, c);
+        if (rank == 0) expect_bytes(&sh.full_q, 2u * C::kQBoxes * hb * toks * 128);
+      };
+      auto prefetch_keys = [&](const Tile& t) {   // this CTA's keys into L2
+        if (kSmall) return;
+        const int id = __shfl_sync(0xffffffffu, t.id, own_h), r = __shfl_sync(0xffffffffu, t.row, own_h);
+#pragma unroll 1
+        for (int c = 0; c < 8; c += 2) prefetch_4d(&kmap, r, c, id);
+        if (kRope) prefetch_3d(&kvmap, 512, r, id);
+      };
+      if (have_cur) {
+        load_q(cur);
+        load_rope(cur);
+      }
+      if (have1 && p.prefetch) prefetch_keys(t1);
+#pragma unroll 1
+      for (int g = 0; ok && have_cur; ++g) {
+        const int b = g & 1;
+        wait(&sh.s_full[b], (g >> 1) & 1);
+        if (!ok) break;
+        // QK(g) is done with the rope box, with Q at a segment's end, and with its keys' columns of the
+        // other CTA's half: the other CTA's keys' columns of this CTA's half take their place
+        if (have1) load_rope(t1);
+        unsigned char* d = sKV + kv_box(b, other, 0);
+        const int id = __shfl_sync(0xffffffffu, cur.id, other), r = __shfl_sync(0xffffffffu, cur.row, other);
+#pragma unroll 1
+        for (int c = 0; c < 4; c += 2) {
+          if (kSmall)
+            load_small(cur, other, 4 * own_h + c, 2, d + c * kBox, 0, &sh.full_w[b]);
+          else
+            load_own_4d(d + c * kBox, &kmap, &sh.full_w[b], r, 4 * own_h + c, id);
+        }
+        expect_bytes(&sh.full_w[b], 4 * kBox);
+        if (have1 && t1.first) load_q(t1);
+        advance();
+        if (have1 && p.prefetch) prefetch_keys(t1);
+      }
     }
     if (!ok) {
       // copies in flight land within microseconds: wait well beyond that before the CTA ends
@@ -545,11 +555,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t d = kTmemS + 64 * b;
       uint64_t a = dq, k = dk + (uint64_t)(8 * b) * kStep;
 #pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        if (!wait(&sh.full_k[b][half], (x >> 1) & 1)) return;
+      for (int q = 0; q < 4; ++q) {
+        if (!wait(&sh.full_k[b][q], (x >> 1) & 1)) return;
         tc_fence_after();
 #pragma unroll
-        for (int i = 0; i < 4; ++i, a += kStep, k += kStep) umma_pair4(d, a, k, 2, 2, id_qk, half == 0 && i == 0);
+        for (int i = 0; i < 2; ++i, a += kStep, k += kStep) umma_pair4(d, a, k, 2, 2, id_qk, q == 0 && i == 0);
       }
       if (kRope) {   // last: the one box that has no second buffer
         if (!wait(&sh.full_r, x & 1)) return;
@@ -566,7 +576,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int i = 0; i < 4; ++i) {   // keys 64 (i / 2) .., columns 128 (i % 2) .. of each half
         umma_pair4(128 * (i & 1), dp + (uint64_t)(i >> 1) * kStep, dv + (uint64_t)(8 * b + 4 * (i >> 1) + 2 * (i & 1)) * kStep,
                    2, 128, id_pv, pv_first && i < 2);
-        if (i & 1) commit_pair(i == 1 ? &sh.pv_half[b] : &sh.pv_done[b]);
+        commit_pair(&sh.pv_done[b][i]);
       }
     };
     int t0 = 0, t1 = open_segment(wk, p, sg, t0);
@@ -671,7 +681,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         // P(g) takes P(g - 1)'s place and O is rescaled once PV(g - 1) is done
-        if (g > 0) mine = mine && wait_for(&sh.pv_done[b ^ 1], ((g - 1) >> 1) & 1, abort);
+        if (g > 0) mine = mine && wait_for(&sh.pv_done[b ^ 1][3], ((g - 1) >> 1) & 1, abort);
         tc_fence_after();
         if (__any_sync(0xffffffffu, alpha != 1.f && j > sg.t0)) {
           for (int c = 128 * part; c < 128 * part + 128; c += 32) {
@@ -719,7 +729,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (!ok) break;
       // ---- O / l
       const int last = g - 1;
-      mine = mine && wait_for(&sh.pv_done[last & 1], (last >> 1) & 1, abort);
+      mine = mine && wait_for(&sh.pv_done[last & 1][3], (last >> 1) & 1, abort);
       sh.red[g & 1][part][ln] = l;         // the parity of the tile before the last: nobody reads it
       ok = group_all(mine);
       if (!ok) break;
@@ -1074,7 +1084,7 @@ int64_t most_items(int64_t T, int64_t B, int H, bool decode) {
 // Whether a CTA's queries fill its 64 rows, so that one load lays all their column groups out.
 bool q_whole(int H) { return H >= 64 || 64 % H == 0; }
 
-// Tensor maps: [0] four column groups of 64 of a block, for pages of 64 rows or more; [1] one group of
+// Tensor maps: [0] two column groups of 64 of a block, for pages of 64 rows or more; [1] one group of
 // a block or a page; [2] queries.
 bool pair_maps(const WindowCall& c, CUtensorMap (&maps)[3]) {
   const uint64_t row = (uint64_t)c.cache.s_row * 2, blk = (uint64_t)c.cache.s_blk * 2, page = c.cache.page,
@@ -1082,7 +1092,7 @@ bool pair_maps(const WindowCall& c, CUtensorMap (&maps)[3]) {
   const uint32_t rows = page < kBlk ? (uint32_t)page : kBlk, hb = H < 64 ? (uint32_t)H : 64, toks = H > 64 ? 1 : 64 / hb;
   constexpr auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
   const uint64_t kd[4] = {64, page, 8, blocks}, ks[3] = {row, 128, blk};
-  const uint32_t kb[4] = {64, rows, 4, 1};
+  const uint32_t kb[4] = {64, rows, 2, 1};
   const uint64_t qd[4] = {64, H, T, groups}, qs[3] = {(uint64_t)c.q.s1 * 2, (uint64_t)c.q.s0 * 2, 128};
   const uint32_t qb[4] = {64, hb, toks, q_whole(c.H) ? (uint32_t)groups : 1};
   return make_map(&maps[0], c.cache.data, 4, kd, ks, kb, sw) &&
