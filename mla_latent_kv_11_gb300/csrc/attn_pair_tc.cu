@@ -230,20 +230,30 @@ __device__ __forceinline__ void dealloc_pair(uint32_t taddr, uint32_t ncols) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
-// Four MMAs of the pair (K = 64), issued by the first CTA's converged warp (an elected lane); the
-// descriptors advance by `as` and `bs` 16-byte units. The first replaces D where `fresh`.
-__device__ __forceinline__ void umma_pair4(uint32_t d, uint64_t a, uint64_t b, uint32_t as, uint32_t bs, uint32_t idesc,
-                                           bool fresh) {
+// Four MMAs of the pair (K = 64), issued by the first CTA's converged warp (an elected lane). The
+// operands' descriptors are given by their low words, which advance by kAs and kBs 16-byte units; the
+// high words (stride 1024, 128-byte swizzle) are constant, so that a descriptor costs one move into
+// the uniform registers instead of two. The first MMA replaces D where `fresh`.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+template <uint32_t kAs, uint32_t kBs, uint32_t kIdesc>
+__device__ __forceinline__ void umma_pair4(uint32_t d, uint32_t a, uint32_t b, bool fresh) {
   asm volatile(
-      "{\n .reg .pred p, t, e;\n .reg .b32 r;\n .reg .b64 a, b, as, bs;\n"
-      " elect.sync r|e, 0xffffffff;\n setp.eq.b32 p, %6, 0;\n setp.eq.b32 t, 0, 0;\n"
-      " cvt.u64.u32 as, %3;\n cvt.u64.u32 bs, %4;\n mov.b64 a, %1;\n mov.b64 b, %2;\n"
-      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, p;\n add.u64 a, a, as;\n add.u64 b, b, bs;\n"
-      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, t;\n add.u64 a, a, as;\n add.u64 b, b, bs;\n"
-      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, t;\n add.u64 a, a, as;\n add.u64 b, b, bs;\n"
-      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, t;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(as), "r"(bs), "r"(idesc), "r"((uint32_t)fresh)
+      "{\n .reg .pred p, t, e;\n .reg .b32 r, x, y;\n .reg .b64 a, b;\n"
+      " elect.sync r|e, 0xffffffff;\n setp.eq.b32 p, %3, 0;\n setp.eq.b32 t, 0, 0;\n"
+      " mov.b64 a, {%1, %7};\n mov.b64 b, {%2, %7};\n"
+      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %6, p;\n"
+      " add.u32 x, %1, %4;\n add.u32 y, %2, %5;\n mov.b64 a, {x, %7};\n mov.b64 b, {y, %7};\n"
+      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %6, t;\n"
+      " add.u32 x, x, %4;\n add.u32 y, y, %5;\n mov.b64 a, {x, %7};\n mov.b64 b, {y, %7};\n"
+      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %6, t;\n"
+      " add.u32 x, x, %4;\n add.u32 y, y, %5;\n mov.b64 a, {x, %7};\n mov.b64 b, {y, %7};\n"
+      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %6, t;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"((uint32_t)fresh), "n"(kAs), "n"(kBs), "n"(kIdesc), "n"(kDescHi)
       : "memory");
+}
+// Low word of a descriptor: address and leading-dimension offset in 16-byte units.
+__device__ __forceinline__ uint32_t desc_lo(const void* p, uint32_t lbo) {
+  return (smem_u32(p) >> 4) | ((lbo >> 4) << 16);
 }
 // Arrive on `bar` of both CTAs once every MMA issued so far is complete.
 __device__ __forceinline__ void commit_pair(uint64_t* bar) {
@@ -361,9 +371,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(remote), "r"(1) : "memory");
   };
 
-  if (warp == 0 || warp == 3) {
-    // ------------------------------------------------------------ loads, in both CTAs: warp 0 the keys,
-    // which the tensor pipe waits for, warp 3 the rest. The whole warp walks the tiles. Lane h looks
+  if (warp == 0 || warp == 2 || warp == 3) {
+    // ------------------------------------------------------------ loads, in both CTAs: warps 0 and 2 the
+    // keys, which the tensor pipe waits for (two quarters of a tile each), warp 3 the rest. The whole warp walks the tiles. Lane h looks
     // up the block id of a tile's block h (small pages: lanes 8h .. 8h + 7 the ids of its pages).
     const int rows_box = kSmall ? p.page : kBlk, subs = kBlk / rows_box;
     Walker wk;
@@ -445,7 +455,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (have1) settle(t1);
       have2 = fetch(t2);
     };
-    if (warp == 0) {
+    if (warp != 3) {
       const uint32_t bar0 = map_to_rank(&sh.full_k[0][0], 0);
 #pragma unroll 1
       for (int g = 0; ok && have_cur; ++g) {
@@ -453,7 +463,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int id = __shfl_sync(0xffffffffu, cur.id, (int)rank), r = __shfl_sync(0xffffffffu, cur.row, (int)rank);
         // a quarter as soon as PV(g - 2) has read what lies there; QK(g) takes them in the same order
 #pragma unroll 1
-        for (int q = 0; ok && q < 4; ++q) {
+        for (int q = warp >> 1; ok && q < 4; q += 2) {
           if (g > 1) wait(&sh.pv_done[b][q], ((g >> 1) & 1) ^ 1);
           if (!ok) break;
           unsigned char* d = sKV + (8 * b + 2 * q) * kBox;
@@ -537,9 +547,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // would not stay in the instruction cache beside the other warps' code
     constexpr uint32_t id_qk = idesc_bf16(128, kTileKeys, false, false);
     constexpr uint32_t id_pv = idesc_bf16(128, 256, false, true);
-    const uint64_t dq = sdesc_sw128(smem_u32(sQ), 16, 1024), dp = sdesc_sw128(smem_u32(sP), 16, 1024),
-                   dk = sdesc_sw128(smem_u32(sKV), 16, 1024), dv = sdesc_sw128(smem_u32(sKV), kBox, 1024),
-                   dr = sdesc_sw128(smem_u32(sR), 16, 1024);
+    const uint32_t dq = desc_lo(sQ, 16), dp = desc_lo(sP, 16), dk = desc_lo(sKV, 16), dv = desc_lo(sKV, kBox),
+                   dr = desc_lo(sR, 16);
     constexpr int kStep = kBox / 16;   // one box, in a descriptor's 16-byte units
     Walker wk;
     wk.init(p, unit, units);
@@ -552,19 +561,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     };
     auto qk = [&](int x) {
       const int b = x & 1;
-      const uint32_t d = kTmemS + 64 * b;
-      uint64_t a = dq, k = dk + (uint64_t)(8 * b) * kStep;
+      const uint32_t d = __reduce_max_sync(0xffffffffu, kTmemS + 64 * b);
+      uint32_t a = dq, k = __reduce_max_sync(0xffffffffu, dk + 8 * b * kStep);
 #pragma unroll 1
       for (int q = 0; q < 4; ++q) {
         if (!wait(&sh.full_k[b][q], (x >> 1) & 1)) return;
         tc_fence_after();
 #pragma unroll
-        for (int i = 0; i < 2; ++i, a += kStep, k += kStep) umma_pair4(d, a, k, 2, 2, id_qk, q == 0 && i == 0);
+        for (int i = 0; i < 2; ++i, a += kStep, k += kStep) umma_pair4<2, 2, id_qk>(d, a, k, q == 0 && i == 0);
       }
       if (kRope) {   // last: the one box that has no second buffer
         if (!wait(&sh.full_r, x & 1)) return;
         tc_fence_after();
-        umma_pair4(d, dq + 8 * kStep, dr, 2, 2, id_qk, false);
+        umma_pair4<2, 2, id_qk>(d, dq + 8 * kStep, dr, false);
       }
       commit_pair(&sh.s_full[b]);
     };
@@ -572,10 +581,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int b = x & 1;
       if (!wait(&sh.p_full, b)) return;
       tc_fence_after();
+      const uint32_t v = __reduce_max_sync(0xffffffffu, dv + 8 * b * kStep);
 #pragma unroll 1
       for (int i = 0; i < 4; ++i) {   // keys 64 (i / 2) .., columns 128 (i % 2) .. of each half
-        umma_pair4(128 * (i & 1), dp + (uint64_t)(i >> 1) * kStep, dv + (uint64_t)(8 * b + 4 * (i >> 1) + 2 * (i & 1)) * kStep,
-                   2, 128, id_pv, pv_first && i < 2);
+        umma_pair4<2, 128, id_pv>(128 * (i & 1), dp + (i >> 1) * kStep, v + 2 * i * kStep, pv_first && i < 2);
         commit_pair(&sh.pv_done[b][i]);
       }
     };
