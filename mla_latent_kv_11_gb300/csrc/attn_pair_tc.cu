@@ -555,18 +555,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     Seg sg;
     int g = 0, seg_i = 0;
     bool ok = true, pv_first = true;   // pv_first: the pending PV starts its segment's O
+    // A barrier is looked at before the MMAs that precede its wait are issued, so that the look's
+    // latency passes under them; looked at behind them it cost the tensor pipe 80 cycles each time
+    bool seen = false;
+    auto look = [&](uint64_t* bar, int parity) { seen = mbar_test_cluster(bar, parity); };
     auto wait = [&](uint64_t* bar, int parity) {
-      ok = ok && __all_sync(0xffffffffu, wait_for(bar, parity, abort));
+      ok = ok && (__all_sync(0xffffffffu, seen) || __all_sync(0xffffffffu, wait_slow(bar, parity, abort)));
       return ok;
     };
     auto qk = [&](int x) {
       const int b = x & 1;
       const uint32_t d = __reduce_max_sync(0xffffffffu, kTmemS + 64 * b);
       uint32_t a = dq, k = __reduce_max_sync(0xffffffffu, dk + 8 * b * kStep);
+      const int ph = (x >> 1) & 1;
+      look(&sh.full_k[b][0], ph);
 #pragma unroll 1
       for (int q = 0; q < 4; ++q) {
-        if (!wait(&sh.full_k[b][q], (x >> 1) & 1)) return;
+        if (!wait(&sh.full_k[b][q], ph)) return;
         tc_fence_after();
+        if (q < 3)
+          look(&sh.full_k[b][q + 1], ph);
+        else if (kRope)
+          look(&sh.full_r, x & 1);
 #pragma unroll
         for (int i = 0; i < 2; ++i, a += kStep, k += kStep) umma_pair4<2, 2, id_qk>(d, a, k, q == 0 && i == 0);
       }
@@ -579,9 +589,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     };
     auto pv = [&](int x) {
       const int b = x & 1;
+      look(&sh.p_full, b);
+      const uint32_t v = __reduce_max_sync(0xffffffffu, dv + 8 * b * kStep);
       if (!wait(&sh.p_full, b)) return;
       tc_fence_after();
-      const uint32_t v = __reduce_max_sync(0xffffffffu, dv + 8 * b * kStep);
 #pragma unroll 1
       for (int i = 0; i < 4; ++i) {   // keys 64 (i / 2) .., columns 128 (i % 2) .. of each half
         umma_pair4<2, 128, id_pv>(128 * (i & 1), dp + (i >> 1) * kStep, v + 2 * i * kStep, pv_first && i < 2);
@@ -593,6 +604,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int j = t0; ok && j < t1; ++j, ++g) {
         if (j == t0) {
           if (g > 0) pv(g - 1);
+          look(&sh.full_q, seg_i & 1);
           if (!ok || !wait(&sh.full_q, seg_i & 1)) break;
           pv_first = true;
           qk(g);
