@@ -566,10 +566,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     auto qk = [&](int x) {
       const int b = x & 1;
       const uint32_t d = __reduce_max_sync(0xffffffffu, kTmemS + 64 * b);
-      uint32_t a = dq, k = __reduce_max_sync(0xffffffffu, dk + 8 * b * kStep);
+      const uint32_t k = __reduce_max_sync(0xffffffffu, dk + 8 * b * kStep);
       const int ph = (x >> 1) & 1;
       look(&sh.full_k[b][0], ph);
-#pragma unroll 1
+#pragma unroll
       for (int q = 0; q < 4; ++q) {
         if (!wait(&sh.full_k[b][q], ph)) return;
         tc_fence_after();
@@ -578,7 +578,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         else if (kRope)
           look(&sh.full_r, x & 1);
 #pragma unroll
-        for (int i = 0; i < 2; ++i, a += kStep, k += kStep) umma_pair4<2, 2, id_qk>(d, a, k, q == 0 && i == 0);
+        for (int i = 2 * q; i < 2 * q + 2; ++i) umma_pair4<2, 2, id_qk>(d, dq + i * kStep, k + i * kStep, i == 0);
       }
       if (kRope) {   // last: the one box that has no second buffer
         if (!wait(&sh.full_r, x & 1)) return;
@@ -593,7 +593,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t v = __reduce_max_sync(0xffffffffu, dv + 8 * b * kStep);
       if (!wait(&sh.p_full, b)) return;
       tc_fence_after();
-#pragma unroll 1
+#pragma unroll
       for (int i = 0; i < 4; ++i) {   // keys 64 (i / 2) .., columns 128 (i % 2) .. of each half
         umma_pair4<2, 128, id_pv>(128 * (i & 1), dp + (i >> 1) * kStep, v + 2 * i * kStep, pv_first && i < 2);
         commit_pair(&sh.pv_done[b][i]);
