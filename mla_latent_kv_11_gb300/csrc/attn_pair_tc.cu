@@ -114,32 +114,43 @@ struct PairParams {
   int page, num_blocks;
   const int32_t* block_table;
   int64_t bt_stride;
-  const int4* items;         // {first token row, tokens, its position, sequence} of each row tile
+  const int4* items;         // two words a row tile (Item)
   const int32_t* total;      // row tiles
   const int2* unit_start;    // split: {row tile, tile} of each unit's first; null: whole row tiles dealt out
   float* part_o;             // [2 * units][128][512], row 64 * CTA + row
   float* part_lse;           // [2 * units][128]
+  int o_32B;                 // output rows lie on 32-byte boundaries: whole sectors a store
   int q_whole;               // the queries' column groups come in one load
   int prefetch;              // bring the tile after the next into L2 (rows come from HBM, each read once)
 };
 
 __host__ __device__ inline int row_tiles(int nblk) { return nblk > 0 ? (nblk + 1) / 2 : 1; }
 
-// The visible blocks of a row tile whose tokens sit at pos0 .. pos0 + ntok - 1.
-__device__ __forceinline__ void visible_blocks(int pos0, int ntok, int window, int sinks, int& lo, int& hi, int& nsb,
-                                               int& wb, int& nblk) {
-  hi = pos0 + ntok - 1;
-  lo = max(0, pos0 - window + 1);
-  nsb = wb = nblk = 0;
-  if (hi < 0) return;
-  nsb = (min(sinks, hi + 1) + kBlk - 1) / kBlk;
-  wb = max(lo / kBlk, nsb);
-  nblk = nsb + max(0, hi / kBlk + 1 - wb);
+// A row tile as the schedule describes it: {first token's row, tokens, its position, sequence} and
+// {first window row, sink blocks, first window block behind them, blocks in all}. Its tokens sit at
+// pos0 .. pos0 + ntok - 1.
+struct Item {
+  int4 a, b;
+};
+__device__ __forceinline__ Item make_item(int tok0, int ntok, int pos0, int seq, int window, int sinks) {
+  const int hi = pos0 + ntok - 1, lo = max(0, pos0 - window + 1);
+  int nsb = 0, wb = 0, nblk = 0;
+  if (hi >= 0) {
+    nsb = (min(sinks, hi + 1) + kBlk - 1) / kBlk;
+    wb = max(lo / kBlk, nsb);
+    nblk = nsb + max(0, hi / kBlk + 1 - wb);
+  }
+  return Item{make_int4(tok0, ntok, pos0, seq), make_int4(lo, nsb, wb, nblk)};
+}
+__device__ __forceinline__ Item load_item(const int4* items, int i) { return Item{items[2 * i], items[2 * i + 1]}; }
+__device__ __forceinline__ void store_item(int4* items, int i, const Item& it) {
+  items[2 * i] = it.a;
+  items[2 * i + 1] = it.b;
 }
 
 struct Walker {
   int unit, units, item, step, end_item, end_tile, tile;
-  int4 next_desc;
+  Item ahead;   // the next row tile, loaded while the one before it runs
 
   __device__ void init(const PairParams& p, int unit_, int units_) {
     unit = unit_;
@@ -159,7 +170,7 @@ struct Walker {
       end_item = -1;
       end_tile = 0;
     }
-    if (more()) next_desc = p.items[item];
+    if (more()) ahead = load_item(p.items, item);
   }
   __device__ bool more() const {
     return step > 0 ? (item < end_item || (item == end_item && tile < end_tile)) : item >= 0;
@@ -167,19 +178,22 @@ struct Walker {
   // The next segment; the description of the one behind it is loaded meanwhile.
   __device__ bool next(const PairParams& p, Seg& s) {
     if (!more()) return false;
-    const int4 d = next_desc;
-    s.tok0 = d.x;
-    s.ntok = d.y;
-    s.pos0 = d.z;
-    s.b = d.w;
-    visible_blocks(s.pos0, s.ntok, p.window, p.sinks, s.lo, s.hi, s.nsb, s.wb, s.nblk);
+    s.tok0 = ahead.a.x;
+    s.ntok = ahead.a.y;
+    s.pos0 = ahead.a.z;
+    s.b = ahead.a.w;
+    s.lo = ahead.b.x;
+    s.hi = s.pos0 + s.ntok - 1;
+    s.nsb = ahead.b.y;
+    s.wb = ahead.b.z;
+    s.nblk = ahead.b.w;
     const int nt = row_tiles(s.nblk);
     s.t0 = tile;
     s.t1 = step > 0 && item == end_item ? min(nt, end_tile) : nt;
     s.slot = s.t0 == 0 && s.t1 == nt ? -1 : 2 * unit + (s.t0 == 0 ? 1 : 0);
     item += step;
     tile = 0;
-    if (more()) next_desc = p.items[item];
+    if (more()) ahead = load_item(p.items, item);
     return true;
   }
 };
@@ -320,6 +334,13 @@ __device__ __forceinline__ void prefetch_4d(const void* map, int32_t c1, int32_t
                : "memory");
 }
 #undef MLA_ELECT
+
+// 32 bytes to a 32-byte aligned address in one store: a whole sector.
+__device__ __forceinline__ void st_global_32B(void* dst, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
 
 // kSmall: pages of less than 64 rows.
 template <int kRope, bool kSmall>
@@ -635,16 +656,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int head = p.tptc ? row % p.H : 64 * (int)rank + row;
     const bool real = p.tptc ? row < p.tptc * p.H : head < p.H;
     auto group_all = [](bool v) { return named_bar_and(kSoftmaxBar, kSoftmaxThreads, v); };
-    // the two rows this thread stores in the epilogue: token (none: beyond every tile) and offset
-    int out_tok[2];
-    int64_t out_off[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int rr = (st >> 3) + 32 * k;
-      const int t = p.tptc ? p.tptc * (int)rank + rr / p.H : 0, h = p.tptc ? rr % p.H : 64 * (int)rank + rr;
-      out_tok[k] = (p.tptc ? rr < p.tptc * p.H : h < p.H) ? t : kTileKeys;
-      out_off[k] = t * p.o_s0 + h * p.o_s1;
-    }
     Walker wk;
     wk.init(p, unit, units);
     Seg sg;
@@ -751,57 +762,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // ---- O / l
       const int last = g - 1;
       mine = mine && wait_for(&sh.pv_done[last & 1][3], (last >> 1) & 1, abort);
-      sh.red[g & 1][part][ln] = l;         // the parity of the tile before the last: nobody reads it
+      // in the place of the last tile's maxima: PV has its P, so every warp has read them; they are
+      // written again behind the next tile's barrier
+      float (&sums)[2][128] = sh.red[last & 1];
+      sums[part][ln] = l;
       ok = group_all(mine);
       if (!ok) break;
       tc_fence_after();
-      const float (&sums)[2][128] = sh.red[g & 1];
       l = (sums[0][ln] + sums[1][ln]) + (sums[0][ln ^ 64] + sums[1][ln ^ 64]);
-      named_bar(kSoftmaxBar, kSoftmaxThreads);   // read before the next tile's maxima take its place
       const float inv = l > 0.f ? 1.f / l : 0.f;
       const int64_t prow = (int64_t)sg.slot * 128 + 64 * rank + row;
-      // through P's place, 128 bytes of every row of both halves a round (64 bf16 columns, or 32
-      // float32 ones of a partial), so that eight lanes store a whole line: straight from the lanes'
-      // rows a store would touch 32 lines
-      const int rounds = sg.slot < 0 ? 4 : 8;
-      unsigned char* put = sP + half * kBox + row * 128;
+      if (sg.slot < 0) {
+        __nv_bfloat16* const o = p.o_lat + (int64_t)(sg.tok0 + tok) * p.o_s0 + (int64_t)head * p.o_s1 + 256 * half + 128 * part;
+        float v[32];
+        tmem_ld32(tmem + lane_addr + 128 * part, v);
 #pragma unroll 1
-      for (int r = 0; r < rounds; ++r) {
-        if (sg.slot < 0) {
-          float v[32];
-          tmem_ld32(tmem + lane_addr + 64 * r + 32 * part, v);
+        for (int r = 0; r < 4; ++r) {
+          uint32_t w[16];
           tmem_ld_wait();
 #pragma unroll
-          for (int ch = 0; ch < 4; ++ch) {
-            uint4 w;
-            __nv_bfloat162* h2 = reinterpret_cast<__nv_bfloat162*>(&w);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) h2[k] = __floats2bfloat162_rn(v[8 * ch + 2 * k] * inv, v[8 * ch + 2 * k + 1] * inv);
-            *reinterpret_cast<uint4*>(put + (((4 * part + ch) ^ (row & 7)) << 4)) = w;
+          for (int k = 0; k < 16; ++k) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * k] * inv, v[2 * k + 1] * inv);
+            w[k] = *reinterpret_cast<const uint32_t*>(&h);
           }
-        } else {
-          float v[16];
-          tmem_ld16(tmem + lane_addr + 32 * r + 16 * part, v);
+          if (r < 3) tmem_ld32(tmem + lane_addr + 128 * part + 32 * (r + 1), v);
+          if (valid) {
+            if (p.o_32B) {
+              st_global_32B(o + 32 * r, w);
+              st_global_32B(o + 32 * r + 16, w + 8);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                *reinterpret_cast<uint4*>(o + 32 * r + 8 * k) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+            }
+          }
+          __syncwarp();
+        }
+      } else {
+        float* const o = p.part_o + prow * 512 + 256 * half + 128 * part;
+        float v[16];
+        tmem_ld16(tmem + lane_addr + 128 * part, v);
+#pragma unroll 1
+        for (int r = 0; r < 8; ++r) {
+          uint32_t w[16];
           tmem_ld_wait();
 #pragma unroll
-          for (int ch = 0; ch < 4; ++ch)
-            *reinterpret_cast<float4*>(put + (((4 * part + ch) ^ (row & 7)) << 4)) =
-                make_float4(v[4 * ch] * inv, v[4 * ch + 1] * inv, v[4 * ch + 2] * inv, v[4 * ch + 3] * inv);
+          for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(v[k] * inv);
+          if (r < 7) tmem_ld16(tmem + lane_addr + 128 * part + 16 * (r + 1), v);
+          if (valid) {
+            st_global_32B(o + 16 * r, w);
+            st_global_32B(o + 16 * r + 8, w + 8);
+          }
+          __syncwarp();
         }
-        named_bar(kSoftmaxBar, kSoftmaxThreads);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {   // rows (st >> 3) + 32 k of the two halves, chunk st & 7
-          const int rr = ((st >> 3) + 32 * k) & 63, hf = k >> 1;
-          if (out_tok[k & 1] >= sg.ntok) continue;
-          const uint4 w = *reinterpret_cast<const uint4*>(sP + hf * kBox + rr * 128 + (((st & 7) ^ (rr & 7)) << 4));
-          if (sg.slot < 0)
-            *reinterpret_cast<uint4*>(p.o_lat + (int64_t)sg.tok0 * p.o_s0 + out_off[k & 1] + 256 * hf + 64 * r +
-                                      8 * (st & 7)) = w;
-          else
-            *reinterpret_cast<uint4*>(p.part_o + ((int64_t)sg.slot * 128 + 64 * rank + rr) * 512 + 256 * hf + 32 * r +
-                                      4 * (st & 7)) = w;
-        }
-        named_bar(kSoftmaxBar, kSoftmaxThreads);   // read before the next round's, or the next tile's P
       }
       if (valid && half == 0 && part == 0) {
         const float lse = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -CUDART_INF_F;
@@ -913,10 +926,9 @@ __global__ void __launch_bounds__(1024) pair_split_kernel(PairSched s) {
     }
     const int t0 = (i - first[lo]) * s.tpt, ntok = min(s.tpt, q_count[lo] - t0);
     const int pos0 = len[lo] - q_count[lo] + t0;
-    s.items[i] = make_int4(q_begin[lo] + t0, ntok, pos0, lo);
-    int a, b, c, d, nblk;
-    visible_blocks(pos0, ntok, s.window, s.sinks, a, b, c, d, nblk);
-    nt = row_tiles(nblk);
+    const Item it = make_item(q_begin[lo] + t0, ntok, pos0, lo, s.window, s.sinks);
+    store_item(s.items, i, it);
+    nt = row_tiles(it.b.w);
   }
   int all;
   const int at = scan_block(i < total ? nt + kSegCost : 0, warp_tot, &all);
@@ -980,7 +992,7 @@ __global__ void __launch_bounds__(256) pair_items_kernel(PairSched s) {
   }
   const int t0 = (i - s.prefix[lo]) * s.tpt;
   const int kv = min(max(s.kv_lens[lo], 0), s.cap);
-  s.items[i] = make_int4(q0 + t0, min(s.tpt, q1 - q0 - t0), kv - (q1 - q0) + t0, lo);
+  store_item(s.items, i, make_item(q0 + t0, min(s.tpt, q1 - q0 - t0), kv - (q1 - q0) + t0, lo, s.window, s.sinks));
 }
 
 // Row tiles cut across units: their pieces merged by log-sum-exp. Block (u, .) handles the row
@@ -990,7 +1002,7 @@ __global__ void __launch_bounds__(128) pair_combine_kernel(PairParams p, int uni
   const int u = blockIdx.x + 1;
   const int2 at = p.unit_start[u], before = p.unit_start[u - 1];
   if (at.x >= *p.total || at.y == 0 || (before.x == at.x && before.y > 0)) return;
-  const int4 d = p.items[at.x];
+  const int4 d = p.items[2 * at.x];
   const int lane = threadIdx.x & 31;
   // row rr of CTA `rank` of the tile, its token and head
   const int rank = blockIdx.y & 1, rr = (blockIdx.y >> 1) * 4 + (threadIdx.x >> 5);
@@ -1086,7 +1098,7 @@ PairWs pair_ws(int64_t items, int64_t batch, int64_t units) {
   PairWs w{};
   w.off_total = 0;
   w.off_items = 256;
-  w.off_starts = up(w.off_items + items * sizeof(int4));
+  w.off_starts = up(w.off_items + items * sizeof(Item));
   w.off_prefix = up(w.off_starts + (units + 1) * sizeof(int2));
   w.off_o = up(w.off_prefix + (batch + 1) * sizeof(int32_t));
   // partial slots: two a unit where the schedule splits row tiles
@@ -1186,6 +1198,7 @@ cudaError_t launch_window_tc(const WindowCall& c, int num_splits, void* ws, cuda
   p.part_lse = reinterpret_cast<float*>(base + w.off_lse);
   p.prefetch = split;
   p.q_whole = q_whole(c.H);
+  p.o_32B = reinterpret_cast<uintptr_t>(c.o.data) % 32 == 0 && c.o.s0 % 16 == 0 && c.o.s1 % 16 == 0;
   if (p.page < kBlk)
     e = c.R == 64 ? launch_attn<64, true>(p, maps, units, st) : launch_attn<0, true>(p, maps, units, st);
   else
