@@ -235,6 +235,11 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatil
   return mbar_test_cluster(bar, parity) || wait_slow(bar, parity, abort);
 }
 
+// The lowest n bits (none for n <= 0, all for n >= 32).
+__device__ __forceinline__ uint32_t bits_below(int n) {
+  return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+
 __device__ __forceinline__ void alloc_pair(uint32_t* dst, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(ncols)
                : "memory");
@@ -676,12 +681,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int kb = blk + 32 * part;                 // this thread's first key
         const bool whole = blk >= 0 && kb + 31 <= pos && (kb + 32 <= p.sinks || kb > pos - p.window);
         if (!__all_sync(0xffffffffu, whole)) {
+          // bit k: key kb + k is attended: [0, sinks) and (pos - window, ..) up to pos
+          const uint32_t m32 = blk < 0 ? 0u
+                                       : (bits_below(p.sinks - kb) | ~bits_below(pos - p.window + 1 - kb)) &
+                                             bits_below(pos + 1 - kb);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            const int t = kb + k;
-            const bool seen = blk >= 0 && t <= pos && (t < p.sinks || t > pos - p.window);
-            sv[k] = seen ? sv[k] : -CUDART_INF_F;
-          }
+          for (int k = 0; k < 32; ++k) sv[k] = (m32 >> k) & 1u ? sv[k] : -CUDART_INF_F;
         }
         float mx[4];
 #pragma unroll
@@ -742,7 +747,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (!(t <= sg.hi && (t < p.sinks || t >= sg.lo))) {
             unsigned char* v = sKV + kv_box(b, h, 2 * half + part) + row * 128;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(v + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+            for (int i = 0; i < 8; ++i)   // lanes in different banks
+              *reinterpret_cast<uint4*>(v + ((i ^ (row & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
           }
         }
         fence_proxy_async_smem();
