@@ -20,6 +20,7 @@
 // Tensor memory per CTA (row r in lanes r and r + 64):
 //   O  [0, 256): lane r columns 0..255 of the row, lane r + 64 columns 256..511
 //   S  [256, 320) and [320, 384), of even and odd tiles: lane r keys 0..63, lane r + 64 keys 64..127
+//   the finished output [384, 512): as O, bf16 pairs
 //
 // Shared memory per CTA: Q 64 x 576 (72 KB), P 64 x 128 (16 KB), two key tiles of 64 KB and
 // one rope box of 8 KB. Q K^T needs, in each CTA, its 64 keys' whole rows (boxes H0: latent
@@ -60,7 +61,7 @@ constexpr int kSoftmaxWarp0 = 4;
 constexpr int kSoftmaxThreads = 256;
 constexpr int kSoftmaxBar = 1;
 constexpr float kLazyRescale = 8.f;
-constexpr uint32_t kTmemS = 256, kTmemCols = 512;
+constexpr uint32_t kTmemS = 256, kTmemOut = 384, kTmemCols = 512;
 constexpr int kSegCost = 1;                  // cost of starting a row tile, in tiles
 constexpr int kSplitItems = 1024;            // row tiles up to which the schedule splits them
 
@@ -664,6 +665,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     Walker wk;
     wk.init(p, unit, units);
     Seg sg;
+    // the output that waits in tensor memory: quarters left of this thread's 128 columns, its row
+    int left = 0;
+    __nv_bfloat16* to = nullptr;
+    auto store_quarter = [&]() {
+      const int r = 4 - left--;
+      float v[16];
+      tmem_ld16(tmem + lane_addr + kTmemOut + 64 * part + 16 * r, v);
+      tmem_ld_wait();
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(v);
+      if (to != nullptr) {
+        if (p.o_32B) {
+          st_global_32B(to + 32 * r, w);
+          st_global_32B(to + 32 * r + 16, w + 8);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            *reinterpret_cast<uint4*>(to + 32 * r + 8 * k) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+        }
+      }
+      __syncwarp();
+    };
     int g = 0;
     bool ok = true, mine = true;   // ok: the group's decision; mine: this thread's waits so far
     while (ok && wk.next(p, sg)) {
@@ -763,6 +785,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           else
             asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_p) : "memory");
         }
+        if (left > 0) store_quarter();
       }
       if (!ok) break;
       // ---- O / l
@@ -779,7 +802,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const float inv = l > 0.f ? 1.f / l : 0.f;
       const int64_t prow = (int64_t)sg.slot * 128 + 64 * rank + row;
       if (sg.slot < 0) {
-        __nv_bfloat16* const o = p.o_lat + (int64_t)(sg.tok0 + tok) * p.o_s0 + (int64_t)head * p.o_s1 + 256 * half + 128 * part;
+        // A row tile's 64 KB of output leave an SM at 16 bytes a cycle, longer than a tile of keys takes.
+        // So O only becomes bf16 here, within tensor memory, and a quarter of it is stored behind each
+        // of the next tiles
+        while (left > 0) store_quarter();
         float v[32];
         tmem_ld32(tmem + lane_addr + 128 * part, v);
 #pragma unroll 1
@@ -792,18 +818,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             w[k] = *reinterpret_cast<const uint32_t*>(&h);
           }
           if (r < 3) tmem_ld32(tmem + lane_addr + 128 * part + 32 * (r + 1), v);
-          if (valid) {
-            if (p.o_32B) {
-              st_global_32B(o + 32 * r, w);
-              st_global_32B(o + 32 * r + 16, w + 8);
-            } else {
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                *reinterpret_cast<uint4*>(o + 32 * r + 8 * k) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
-            }
-          }
-          __syncwarp();
+          tmem_st16u(tmem + lane_addr + kTmemOut + 64 * part + 16 * r, w);
         }
+        tmem_st_wait();
+        left = 4;
+        // a lane whose row is not real stores nothing
+        to = valid ? p.o_lat + (int64_t)(sg.tok0 + tok) * p.o_s0 + (int64_t)head * p.o_s1 + 256 * half + 128 * part : nullptr;
       } else {
         float* const o = p.part_o + prow * 512 + 256 * half + 128 * part;
         float v[16];
@@ -830,6 +850,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           p.lse[(int64_t)(sg.tok0 + tok) * p.H + head] = lse;
       }
     }
+    while (left > 0) store_quarter();
     if (!ok) give_up();
   }
   // ---------------------------------------------------------------- teardown
