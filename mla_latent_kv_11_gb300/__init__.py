@@ -120,15 +120,10 @@ def _dtype_code(*tensors) -> int:
 
 def as_mla_tensor(t) -> MlaTensor:
     """Describe a torch tensor (any strides) as an mla_tensor view."""
-    if t.dim() > 4:
+    shape = t.shape
+    if len(shape) > 4:
         raise MlaError(MLA_ERR_INVALID_ARG, "rank > 4")
-    m = MlaTensor()
-    m.data = t.data_ptr() if t.numel() > 0 else None
-    m.rank = t.dim()
-    for i, (n, s) in enumerate(zip(t.shape, t.stride())):
-        m.shape[i] = n
-        m.stride[i] = s
-    return m
+    return MlaTensor(t.data_ptr() if t.numel() > 0 else None, len(shape), shape, t.stride())
 
 
 def _stream(stream) -> Optional[int]:
@@ -391,16 +386,22 @@ def mla_decode_noalloc(o_lat_out, q_cat, cache, block_table, seq_lens, kv_lora_r
                                     num_splits, _stream(stream)))
 
 
-def _check_device(*tensors) -> None:
-    """Every tensor on one CUDA device, and that the current one: the library launches there."""
+def _check_device(*tensors) -> int:
+    """Every tensor on one CUDA device, and that the current one: the library launches there. Its index."""
     import torch
-    devices = {t.device for t in tensors if t is not None}
-    if len(devices) != 1 or next(iter(devices)).type != "cuda":
-        raise MlaError(MLA_ERR_INVALID_ARG, f"tensors must share one CUDA device: {sorted(map(str, devices))}")
-    device = devices.pop()
-    if device.index != torch.cuda.current_device():
-        raise MlaError(MLA_ERR_INVALID_ARG, f"tensors are on {device}, the current device is "
-                                            f"cuda:{torch.cuda.current_device()}")
+    device = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise MlaError(MLA_ERR_INVALID_ARG, "tensors must lie on the current device, "
+                                                f"cuda:{device}; one is on {t.device}")
+    return device
+
+
+def _stream_on(stream, device: int) -> Optional[int]:
+    """The stream a call runs on; without one, the device's current stream (asked for directly: the
+    stream object costs more than the rest of a small call)."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
 
 
 def _check_slots(slot_mapping) -> None:
@@ -437,20 +438,20 @@ def _check_lse(lse_out, q_cat) -> None:
         raise MlaError(MLA_ERR_INVALID_ARG, "lse_out must be contiguous float32 with q_cat's rows and heads")
 
 
-def _scratch(workspace, need: int, like, stream):
-    """The caller's workspace, or one allocated on the stream the call runs on (so that its memory
-    is reused only behind the call's work)."""
+def _scratch(need: int, device: int, stream):
+    """A workspace allocated on the stream the call runs on, so that its memory is reused only behind
+    the call's work."""
     import torch
-    if workspace is not None:
-        _check_device(workspace, like)
-        if not workspace.is_contiguous():
-            raise MlaError(MLA_ERR_INVALID_ARG, "workspace must be contiguous")
-        return workspace
     if stream is None:
-        return torch.empty(need, dtype=torch.uint8, device=like.device)
-    on = torch.cuda.ExternalStream(_stream(stream), device=like.device)
-    with torch.cuda.stream(on):
-        return torch.empty(need, dtype=torch.uint8, device=like.device)
+        return torch.empty(need, dtype=torch.uint8, device=f"cuda:{device}")
+    with torch.cuda.stream(torch.cuda.ExternalStream(_stream(stream), device=device)):
+        return torch.empty(need, dtype=torch.uint8, device=f"cuda:{device}")
+
+
+def _workspace_args(workspace):
+    if not workspace.is_contiguous():
+        raise MlaError(MLA_ERR_INVALID_ARG, "workspace must be contiguous")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def _ds_mla_cache(cache):
@@ -466,10 +467,10 @@ def mla_cache_write_ds_mla(cache, kv_c, k_pe, slot_mapping, stream=None) -> None
     columns, and k_pe[i] as bf16, for s = slot_mapping[i] >= 0; kv_c [T,512], k_pe [T,64]."""
     cache = _ds_mla_cache(cache)
     _check_slots(slot_mapping)
-    _check_device(cache, kv_c, k_pe, slot_mapping)
+    device = _check_device(cache, kv_c, k_pe, slot_mapping)
     _check(lib().mla_cache_write_ds_mla(_dtype_code(kv_c, k_pe), as_mla_tensor(cache), as_mla_tensor(kv_c),
                                         as_mla_tensor(k_pe), _ptr(slot_mapping), slot_mapping.numel(),
-                                        _stream(stream)))
+                                        _stream_on(stream, device)))
 
 
 def _read_args(out, cache, block_table, cu_seqlens, seq_starts):
@@ -478,31 +479,31 @@ def _read_args(out, cache, block_table, cu_seqlens, seq_starts):
     _check_counts(cu_seqlens, batch + 1, "cu_seqlens")
     if seq_starts is not None:
         _check_counts(seq_starts, batch, "seq_starts")
-    _check_device(out, cache, block_table, cu_seqlens, seq_starts)
-    return (as_mla_tensor(out), as_mla_tensor(cache), _ptr(block_table), _table_stride(block_table),
-            block_table.shape[1], _ptr(cu_seqlens), _ptr(seq_starts), batch)
+    device = _check_device(out, cache, block_table, cu_seqlens, seq_starts)
+    return device, (as_mla_tensor(out), as_mla_tensor(cache), _ptr(block_table), _table_stride(block_table),
+                    block_table.shape[1], _ptr(cu_seqlens), _ptr(seq_starts), batch)
 
 
 def mla_cache_read(out, cache, block_table, cu_seqlens, seq_starts=None, stream=None) -> None:
     """Read-back of a plain cache: out[i] = row seq_starts[b] + i - cu_seqlens[b] of sequence b for
     cu_seqlens[b] <= i < cu_seqlens[b+1]; out [T,W], bits unchanged, other rows left as they were."""
-    args = _read_args(out, cache, block_table, cu_seqlens, seq_starts)
-    _check(lib().mla_cache_read(_dtype_code(out, cache), *args, _stream(stream)))
+    device, args = _read_args(out, cache, block_table, cu_seqlens, seq_starts)
+    _check(lib().mla_cache_read(_dtype_code(out, cache), *args, _stream_on(stream, device)))
 
 
 def mla_cache_read_fp8(out, cache, block_table, cu_seqlens, scale, seq_starts=None, stream=None) -> None:
     """Read-back of an e4m3 cache: as mla_cache_read, a value = its code's value * scale, in out's dtype."""
     cache = _fp8_cache(cache)
-    args = _read_args(out, cache, block_table, cu_seqlens, seq_starts)
-    _check_device(out, scale)
-    _check(lib().mla_cache_read_fp8(_dtype_code(out), *args, _f32_scalar(scale, "scale"), _stream(stream)))
+    device, args = _read_args(out, cache, block_table, cu_seqlens, seq_starts)
+    _check_device(scale)
+    _check(lib().mla_cache_read_fp8(_dtype_code(out), *args, _f32_scalar(scale, "scale"), _stream_on(stream, device)))
 
 
 def mla_cache_read_ds_mla(out, cache, block_table, cu_seqlens, seq_starts=None, stream=None) -> None:
     """Read-back of a ds_mla cache: as mla_cache_read with 576 values a row, [code * scale | rope]."""
     cache = _ds_mla_cache(cache)
-    args = _read_args(out, cache, block_table, cu_seqlens, seq_starts)
-    _check(lib().mla_cache_read_ds_mla(_dtype_code(out), *args, _stream(stream)))
+    device, args = _read_args(out, cache, block_table, cu_seqlens, seq_starts)
+    _check(lib().mla_cache_read_ds_mla(_dtype_code(out), *args, _stream_on(stream, device)))
 
 
 def mla_decode_window_workspace_size(batch: int, num_heads: int, kv_lora_rank: int, num_splits: int = 0) -> int:
@@ -517,13 +518,14 @@ def mla_decode_window(o_lat_out, q_cat, cache, block_table, seq_lens, kv_lora_ra
     _check_table(block_table, B)
     _check_counts(seq_lens, B, "seq_lens")
     _check_lse(lse_out, q_cat)
-    _check_device(o_lat_out, q_cat, cache, block_table, seq_lens, lse_out)
-    workspace = _scratch(workspace, mla_decode_window_workspace_size(B, H, kv_lora_rank, num_splits), q_cat, stream)
+    device = _check_device(o_lat_out, q_cat, cache, block_table, seq_lens, lse_out, workspace)
+    if workspace is None:
+        workspace = _scratch(mla_decode_window_workspace_size(B, H, kv_lora_rank, num_splits), device, stream)
     _check(lib().mla_decode_window(_dtype_code(o_lat_out, q_cat, cache), as_mla_tensor(o_lat_out), _ptr(lse_out),
                                    as_mla_tensor(q_cat), as_mla_tensor(cache), _ptr(block_table),
                                    _table_stride(block_table), block_table.shape[1], _ptr(seq_lens), kv_lora_rank,
-                                   rope_dim, softmax_scale, window, sinks, num_splits, workspace.data_ptr(),
-                                   workspace.numel() * workspace.element_size(), _stream(stream)))
+                                   rope_dim, softmax_scale, window, sinks, num_splits, *_workspace_args(workspace),
+                                   _stream_on(stream, device)))
 
 
 def mla_prefill_window_workspace_size(tokens: int, batch: int, num_heads: int, kv_lora_rank: int) -> int:
@@ -540,14 +542,14 @@ def mla_prefill_window(o_lat_out, q_cat, cache, block_table, cu_seqlens_q, seq_l
     _check_counts(seq_lens_kv, batch, "seq_lens_kv")
     _check_counts(cu_seqlens_q, batch + 1, "cu_seqlens_q")
     _check_lse(lse_out, q_cat)
-    _check_device(o_lat_out, q_cat, cache, block_table, cu_seqlens_q, seq_lens_kv, lse_out)
-    workspace = _scratch(workspace, mla_prefill_window_workspace_size(T, batch, H, kv_lora_rank), q_cat, stream)
+    device = _check_device(o_lat_out, q_cat, cache, block_table, cu_seqlens_q, seq_lens_kv, lse_out, workspace)
+    if workspace is None:
+        workspace = _scratch(mla_prefill_window_workspace_size(T, batch, H, kv_lora_rank), device, stream)
     _check(lib().mla_prefill_window(_dtype_code(o_lat_out, q_cat, cache), as_mla_tensor(o_lat_out), _ptr(lse_out),
                                     as_mla_tensor(q_cat), as_mla_tensor(cache), _ptr(block_table),
                                     _table_stride(block_table), block_table.shape[1], _ptr(cu_seqlens_q),
                                     _ptr(seq_lens_kv), batch, kv_lora_rank, rope_dim, softmax_scale, window, sinks,
-                                    workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                    _stream(stream)))
+                                    *_workspace_args(workspace), _stream_on(stream, device)))
 
 
 def mla_check_bounded_wait(limit_us: int, stream=None) -> None:

@@ -1106,13 +1106,13 @@ int max_pairs() {
 }
 
 template <int kRope, bool kSmall>
-cudaError_t launch_attn(const PairParams& p, const CUtensorMap (&maps)[3], int units, cudaStream_t st) {
+cudaError_t launch_attn(const PairParams& p, const WindowMaps& maps, int units, cudaStream_t st) {
   using C = PairCfg<kRope>;
   const cudaError_t e = cudaFuncSetAttribute(window_attn_kernel<kRope, kSmall>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              C::kSmemAlloc);
   if (e != cudaSuccess) return e;
-  return launch_k(window_attn_kernel<kRope, kSmall>, dim3(2 * units), dim3(kThreads), C::kSmemAlloc, st, maps[0], maps[1], maps[2],
-                  p);
+  return launch_k(window_attn_kernel<kRope, kSmall>, dim3(2 * units), dim3(kThreads), C::kSmemAlloc, st, maps.keys, maps.boxes,
+                  maps.q, p);
 }
 
 int pair_tokens(int H) { return H > 64 ? 1 : 2 * (64 / H); }
@@ -1144,9 +1144,9 @@ int64_t most_items(int64_t T, int64_t B, int H, bool decode) {
 // Whether a CTA's queries fill its 64 rows, so that one load lays all their column groups out.
 bool q_whole(int H) { return H >= 64 || 64 % H == 0; }
 
-// Tensor maps: [0] two column groups of 64 of a block, for pages of 64 rows or more; [1] one group of
-// a block or a page; [2] queries.
-bool pair_maps(const WindowCall& c, CUtensorMap (&maps)[3]) {
+// Tensor maps: two column groups of 64 of a block, for pages of 64 rows or more; one group of a block or
+// a page; queries.
+bool pair_maps(const WindowCall& c, WindowMaps* m) {
   const uint64_t row = (uint64_t)c.cache.s_row * 2, blk = (uint64_t)c.cache.s_blk * 2, page = c.cache.page,
                  blocks = c.cache.num_blocks, groups = (c.L + c.R) / 64, H = c.H, T = c.q.n0;
   const uint32_t rows = page < kBlk ? (uint32_t)page : kBlk, hb = H < 64 ? (uint32_t)H : 64, toks = H > 64 ? 1 : 64 / hb;
@@ -1155,14 +1155,14 @@ bool pair_maps(const WindowCall& c, CUtensorMap (&maps)[3]) {
   const uint32_t kb[4] = {64, rows, 2, 1};
   const uint64_t qd[4] = {64, H, T, groups}, qs[3] = {(uint64_t)c.q.s1 * 2, (uint64_t)c.q.s0 * 2, 128};
   const uint32_t qb[4] = {64, hb, toks, q_whole(c.H) ? (uint32_t)groups : 1};
-  return make_map(&maps[0], c.cache.data, 4, kd, ks, kb, sw) &&
-         make_map3d(&maps[1], c.cache.data, 64 * groups, page, blocks, row, blk, 64, rows, 1, sw) &&
-         make_map(&maps[2], c.q.data, 4, qd, qs, qb, sw);
+  return make_map(&m->keys, c.cache.data, 4, kd, ks, kb, sw) &&
+         make_map3d(&m->boxes, c.cache.data, 64 * groups, page, blocks, row, blk, 64, rows, 1, sw) &&
+         make_map(&m->q, c.q.data, 4, qd, qs, qb, sw);
 }
 
 }  // namespace
 
-bool window_tc_supported(mla_dtype dt, const WindowCall& c) {
+bool window_tc_supported(mla_dtype dt, const WindowCall& c, WindowMaps* maps) {
   if (dt != MLA_BF16 || c.L != 512 || (c.R != 0 && c.R != 64) || c.H > 128 || !(c.scale > 0.f)) return false;
   const int page = c.cache.page;
   if (!(page % 64 == 0 || (64 % page == 0 && page % 8 == 0))) return false;
@@ -1170,7 +1170,6 @@ bool window_tc_supported(mla_dtype dt, const WindowCall& c) {
   if (!al16(c.cache.data) || c.cache.s_blk % 8 || c.cache.s_row % 8) return false;
   if (!al16(c.q.data) || c.q.s0 % 8 || c.q.s1 % 8) return false;
   if (!al16(c.o.data) || c.o.s0 % 8 || c.o.s1 % 8) return false;
-  CUtensorMap maps[3];
   return pair_maps(c, maps);
 }
 
@@ -1179,9 +1178,7 @@ size_t window_tc_workspace(int64_t T, int64_t B, int H, bool decode, int num_spl
   return pair_ws(most_items(T, B, H, decode), B, num_splits > 0 ? num_splits : max_pairs<64, false>()).total;
 }
 
-cudaError_t launch_window_tc(const WindowCall& c, int num_splits, void* ws, cudaStream_t st) {
-  CUtensorMap maps[3];
-  if (!pair_maps(c, maps)) return cudaErrorInvalidValue;
+cudaError_t launch_window_tc(const WindowCall& c, const WindowMaps& maps, int num_splits, void* ws, cudaStream_t st) {
   const bool decode = c.cu_q == nullptr;
   const int units = num_splits > 0 ? num_splits : max_pairs<64, false>();
   const int64_t items = most_items(c.q.n0, c.B, c.H, decode);

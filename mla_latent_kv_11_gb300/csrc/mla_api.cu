@@ -864,8 +864,9 @@ mla_status mla_decode_window(mla_dtype dtype, mla_tensor o_lat_out, float* lse_o
   const WindowArgs w{window, sinks};
   const WindowCall wc{dc.ov, dc.qv, lse_out, dc.cv, block_table, block_table_stride, max_blocks, nullptr, seq_lens,
                       B, H, L, R, softmax_scale, w};
-  if (window_tc_supported(dtype, wc))
-    return cuda_status(launch_window_tc(wc, num_splits, workspace, st), "mla_decode_window (tensor cores)");
+  WindowMaps maps;
+  if (window_tc_supported(dtype, wc, &maps))
+    return cuda_status(launch_window_tc(wc, maps, num_splits, workspace, st), "mla_decode_window (tensor cores)");
   // each sequence's visible rows, then the split-KV decode over that many
   int32_t* visible = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + ws.off_visible);
   const DecodeSched s = decode_sched_from_ws(workspace, ws.lay, B, decode_units(num_splits));
@@ -901,8 +902,10 @@ mla_status mla_prefill_window(mla_dtype dtype, mla_tensor o_lat_out, float* lse_
   MLA_TRY(check_workspace(workspace, workspace_bytes, mla_prefill_window_workspace_size(T, batch, H, L)));
   const WindowCall wc{dc.ov, dc.qv, lse_out, dc.cv, block_table, block_table_stride, max_blocks, cu_seqlens_q,
                       seq_lens_kv, batch, H, L, R, softmax_scale, WindowArgs{window, sinks}};
-  if (window_tc_supported(dtype, wc))
-    return cuda_status(launch_window_tc(wc, 0, workspace, (cudaStream_t)stream), "mla_prefill_window (tensor cores)");
+  WindowMaps maps;
+  if (window_tc_supported(dtype, wc, &maps))
+    return cuda_status(launch_window_tc(wc, maps, 0, workspace, (cudaStream_t)stream),
+                       "mla_prefill_window (tensor cores)");
   return cuda_status(launch_prefill_window_simt(dtype, dc.ov, lse_out, dc.qv, dc.cv, block_table, block_table_stride,
                                                 max_blocks, cu_seqlens_q, seq_lens_kv, batch, T, H, L, R,
                                                 softmax_scale, WindowArgs{window, sinks}, (cudaStream_t)stream),

@@ -223,10 +223,14 @@ struct WindowCall {
 // On the tensor cores (attn_pair_tc.cu): bf16, L = 512, R in {0, 64}, up to 128 heads, a positive
 // scale, pages of whole 64-row blocks or blocks of whole pages of 8 rows or more, 16-byte aligned
 // views.
-bool window_tc_supported(mla_dtype dt, const WindowCall& c);
+// Fills the call's tensor maps where it is so.
+struct WindowMaps {
+  CUtensorMap keys, boxes, q;
+};
+bool window_tc_supported(mla_dtype dt, const WindowCall& c, WindowMaps* maps);
 // Bytes of workspace for T query tokens of B sequences (0: H is not taken).
 size_t window_tc_workspace(int64_t T, int64_t B, int H, bool decode, int num_splits);
-cudaError_t launch_window_tc(const WindowCall& c, int num_splits, void* ws, cudaStream_t st);
+cudaError_t launch_window_tc(const WindowCall& c, const WindowMaps& maps, int num_splits, void* ws, cudaStream_t st);
 // visible[b] = rows the query at seq_lens[b] - 1 attends: the lengths of the split-KV schedule.
 cudaError_t launch_window_lens(const int32_t* seq_lens, int32_t B, int32_t max_blocks, int32_t page,
                                const WindowArgs& w, int32_t* visible, cudaStream_t st);
