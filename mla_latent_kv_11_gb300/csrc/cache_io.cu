@@ -1,17 +1,20 @@
 // Rows into and out of a quantised paged cache: the write of 656-byte fp8 ds_mla
 // entries, and the read-back of plain, e4m3 and ds_mla rows into contiguous rows.
 //
-// Both are bound by HBM: every byte of a row crosses it once. One warp owns one
-// row at a time, a lane 16 consecutive latent values, so a 512-wide latent part
-// is one pass of the warp; a 128-column scale group is eight lanes, and its
-// maximum three exchanges.
+// Both are bound by HBM: every byte of a row crosses it once. A warp takes up to 32
+// consecutive rows (few where there are few, so that all SMs have some): its lanes look up
+// where a row each lies, at once, and then the warp moves the rows, four in flight. A lane
+// holds 16 consecutive latent values of a row, so a 512-wide latent part is one pass of the
+// warp; a 128-column scale group is eight lanes, and its maximum three exchanges.
 #include <cfloat>
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "mla_internal.h"
+#include "sm100_ptx.cuh"
 
 namespace mla {
 namespace {
@@ -25,32 +28,44 @@ __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float
 __device__ __forceinline__ void from_f(float* p, float v) { *p = v; }
 __device__ __forceinline__ void from_f(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-// N consecutive values as floats, 16 bytes a load.
-template <int N>
-__device__ __forceinline__ void load_n(const __nv_bfloat16* p, float (&x)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; i += 8) {
-    const uint4 w = *reinterpret_cast<const uint4*>(p + i);
-    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&w);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 f = __bfloat1622float2(h[k]);
-      x[i + 2 * k] = f.x;
-      x[i + 2 * k + 1] = f.y;
-    }
+// Consecutive rows a warp takes.
+constexpr int kMostRows = 32;
+constexpr int kInFlight = 4;
+
+// Sixteen consecutive values as floats: 32 bytes a load where `wide` (32-byte aligned), else 16.
+__device__ __forceinline__ void load_words(const void* p, uint32_t (&w)[8], bool wide) {
+  if (wide) {
+    ptx::ld_global_32B(p, w);
+  } else {
+    const uint4 a = reinterpret_cast<const uint4*>(p)[0], b = reinterpret_cast<const uint4*>(p)[1];
+    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
   }
 }
-template <int N>
-__device__ __forceinline__ void load_n(const float* p, float (&x)[N]) {
+__device__ __forceinline__ void load16(const __nv_bfloat16* p, float (&x)[16], bool wide) {
+  uint32_t w[8];
+  load_words(p, w, wide);
 #pragma unroll
-  for (int i = 0; i < N; i += 4) {
-    const float4 w = *reinterpret_cast<const float4*>(p + i);
-    x[i] = w.x;
-    x[i + 1] = w.y;
-    x[i + 2] = w.z;
-    x[i + 3] = w.w;
+  for (int i = 0; i < 8; ++i) {
+    const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
   }
 }
+__device__ __forceinline__ void load16(const float* p, float (&x)[16], bool wide) {
+  uint32_t w[8];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    load_words(p + 8 * h, w, wide);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[8 * h + i] = __uint_as_float(w[i]);
+  }
+}
+// Two consecutive values.
+__device__ __forceinline__ float2 load2(const __nv_bfloat16* p) {
+  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p));
+}
+__device__ __forceinline__ float2 load2(const float* p) { return *reinterpret_cast<const float2*>(p); }
 
 // N consecutive values, each rounded once to T, 16 bytes a store.
 template <int N>
@@ -70,6 +85,10 @@ __device__ __forceinline__ void store_n(float* p, const float (&x)[N]) {
   for (int i = 0; i < N; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
 }
 
+// Two consecutive values from bf16.
+__device__ __forceinline__ void store2(__nv_bfloat16* p, __nv_bfloat162 v) { *reinterpret_cast<__nv_bfloat162*>(p) = v; }
+__device__ __forceinline__ void store2(float* p, __nv_bfloat162 v) { *reinterpret_cast<float2*>(p) = __bfloat1622float2(v); }
+
 // Four codes of a 32-bit word as floats (exact: every e4m3 value is a half value).
 __device__ __forceinline__ void e4m3x4(uint32_t w, float* x) {
 #pragma unroll
@@ -79,69 +98,106 @@ __device__ __forceinline__ void e4m3x4(uint32_t w, float* x) {
     x[2 * k + 1] = __half2float(__ushort_as_half(h.y));
   }
 }
-__device__ __forceinline__ void e4m3x16(const uint4 w, float (&x)[16]) {
-  e4m3x4(w.x, x);
-  e4m3x4(w.y, x + 4);
-  e4m3x4(w.z, x + 8);
-  e4m3x4(w.w, x + 12);
-}
 __device__ __forceinline__ float e4m3(uint8_t c) {
   __nv_fp8_e4m3 v;
   v.__x = c;
   return static_cast<float>(v);
 }
 
+// x / s correctly rounded, r being 1 / s correctly rounded: Markstein's method (IBM J. Res. Dev. 34,
+// 1990). x * r is within two units in the last place; the remainder of a quotient q that near is
+// exact in one fused multiply-add, a first step makes q a neighbour of the quotient, and from a
+// neighbour the second gives it correctly rounded. No remainder may underflow: s is at least 2^-80
+// here (smaller scales divide). Infinities and NaNs come out as x * r would (the remainder of an
+// infinity is a NaN).
+__device__ __forceinline__ float divide(float x, float s, float r) {
+  const float q = x * r;
+  const float a = fmaf(fmaf(-q, s, x), r, q);
+  const float b = fmaf(fmaf(-a, s, x), r, a);
+  return fabsf(q) <= FLT_MAX ? b : q;
+}
+
+// The codes of two quotients: to nearest even, saturating.
+__device__ __forceinline__ uint32_t codes2(float a, float b) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+
 // ---------------------------------------------------------------------------
 // cache[s/page, s%page] = the ds_mla entry of [kv_c[i] | k_pe[i]] for every token i with slot
 // s >= 0. A group's scale is its largest magnitude / 448 (an infinity counts as the largest
 // float32, a NaN not at all), at least 2^-126 so that the division stays among normal numbers;
-// its codes are e4m3(x / scale), the division correctly rounded in float32 and the code rounded
-// to nearest even: a value is off by at most half an e4m3 step of its own size, 2^-4 of it, or
-// 2^-10 of the group's scale below the smallest normal code. vec: 16-byte aligned source rows.
+// its codes are e4m3(x / scale), the division correctly rounded in float32: a value is off by at
+// most half an e4m3 step of its own size, 2^-4 of it, or 2^-10 of the group's scale below the
+// smallest normal code. vec: 16-byte aligned source rows; wide: 32-byte aligned latent rows.
 template <typename T>
 __global__ void __launch_bounds__(256) write_ds_mla_kernel(
     uint8_t* __restrict__ cache, int64_t c_blk, int64_t c_row, int64_t num_rows, int32_t page,
     const T* __restrict__ kv_c, int64_t k_s0, const T* __restrict__ k_pe, int64_t p_s0,
-    const int64_t* __restrict__ slots, int64_t tokens, int vec) {
+    const int64_t* __restrict__ slots, int64_t tokens, int per_warp, int vec, int wide) {
   pdl_enter();
+  constexpr int kAhead = 2;   // tokens whose values are in registers
   const int lane = threadIdx.x & 31;
-  const int64_t step = ((int64_t)gridDim.x * blockDim.x) >> 5;
-  for (int64_t tok = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5; tok < tokens; tok += step) {
-    const int64_t s = slots[tok];
-    if (s < 0) continue;   // padding
-    if (s >= num_rows) {   // would land outside the view: skip and record
-      if (lane == 0) atomicOr(&g_io_err, kErrDeviceData);
-      continue;
+  const int64_t first = ((blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5) * per_warp;
+  if (first >= tokens) return;
+  const int n = (int)min((int64_t)per_warp, tokens - first);
+  // lane i: where token first + i goes (-1: padding, or outside the view: recorded)
+  int64_t off = -1;
+  if (lane < n) {
+    const int64_t s = slots[first + lane];
+    if (s >= num_rows) {
+      atomicOr(&g_io_err, kErrDeviceData);
+    } else if (s >= 0) {
+      const int64_t blk = s / page;
+      off = blk * c_blk + (s - blk * page) * c_row;
     }
-    const int64_t blk = s / page;
-    uint8_t* o = cache + blk * c_blk + (s - blk * page) * c_row;
-    const T* src = kv_c + tok * k_s0 + lane * 16;
-    float x[16], r[8] = {};
-    if (vec) {
-      load_n(src, x);
-      if (lane < 8) load_n(k_pe + tok * p_s0 + lane * 8, r);
-    } else {
+  }
+  __syncwarp();
+  for (int i = 0; i < n; i += kAhead) {
+    float x[kAhead][16];
+    float2 pe[kAhead];
+    int64_t to[kAhead];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = to_f(src[i]);
-      if (lane < 8) {
+    for (int u = 0; u < kAhead; ++u) {
+      to[u] = __shfl_sync(0xffffffffu, off, min(i + u, 31));
+      if (i + u >= n) to[u] = -1;
+      if (to[u] < 0) continue;
+      const int64_t tok = first + i + u;
+      const T* src = kv_c + tok * k_s0 + lane * 16;
+      const T* rope = k_pe + tok * p_s0 + lane * 2;
+      if (vec) {
+        load16(src, x[u], wide);
+        pe[u] = load2(rope);
+      } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) r[i] = to_f(k_pe[tok * p_s0 + lane * 8 + i]);
+        for (int k = 0; k < 16; ++k) x[u][k] = to_f(src[k]);
+        pe[u] = make_float2(to_f(rope[0]), to_f(rope[1]));
       }
     }
-    float top = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(x[i]));   // fmaxf passes a NaN over
-    top = fminf(top, FLT_MAX);
+    for (int u = 0; u < kAhead; ++u) {
+      if (to[u] < 0) continue;
+      uint8_t* o = cache + to[u];
+      float top = 0.f;
 #pragma unroll
-    for (int m = 1; m < 8; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-    const float scale = fmaxf(__fdiv_rn(top, kE4m3Max), FLT_MIN);
-    uint32_t w[4] = {};
+      for (int k = 0; k < 16; ++k) top = fmaxf(top, fabsf(x[u][k]));   // fmaxf passes a NaN over
+      top = fminf(top, FLT_MAX);
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      w[i >> 2] |= (uint32_t)__nv_cvt_float_to_fp8(__fdiv_rn(x[i], scale), __NV_SATFINITE, __NV_E4M3) << (8 * (i & 3));
-    *reinterpret_cast<uint4*>(o + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-    if ((lane & 7) == 0) *reinterpret_cast<float*>(o + kDsMlaLatent + 4 * (lane >> 3)) = scale;
-    if (lane < 8) store_n(reinterpret_cast<__nv_bfloat16*>(o + kDsMlaRopeByte) + lane * 8, r);
+      for (int m = 1; m < 8; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+      const float scale = fmaxf(__fdiv_rn(top, kE4m3Max), FLT_MIN);
+      uint32_t w[4] = {};
+      if (scale >= 0x1p-80f) {
+        const float inv = __frcp_rn(scale);
+#pragma unroll
+        for (int k = 0; k < 16; k += 2)
+          w[k >> 2] |= codes2(divide(x[u][k], scale, inv), divide(x[u][k + 1], scale, inv)) << (8 * (k & 2));
+      } else {
+        for (int k = 0; k < 16; k += 2)
+          w[k >> 2] |= codes2(__fdiv_rn(x[u][k], scale), __fdiv_rn(x[u][k + 1], scale)) << (8 * (k & 2));
+      }
+      *reinterpret_cast<uint4*>(o + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+      if ((lane & 7) == 0) *reinterpret_cast<float*>(o + kDsMlaLatent + 4 * (lane >> 3)) = scale;
+      reinterpret_cast<__nv_bfloat162*>(o + kDsMlaRopeByte)[lane] = __floats2bfloat162_rn(pe[u].x, pe[u].y);
+    }
   }
 }
 
@@ -160,7 +216,7 @@ struct ReadRows {
 
   // Element offset of out row i's cache row; -1: the row belongs to no sequence, or its block id
   // or position lies outside the table or the cache (recorded, the out row left as it was).
-  __device__ int64_t offset(int64_t i, int lane) const {
+  __device__ int64_t offset(int64_t i) const {
     int lo = 0, hi = batch - 1;   // the last b with cu[b] <= i
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -174,50 +230,108 @@ struct ReadRows {
       const int32_t blk = block_table[lo * bt_stride + pb];
       if (blk >= 0 && blk < num_blocks) return blk * s_blk + (p - pb * page) * s_row;
     }
-    if (lane == 0) atomicOr(&g_io_err, kErrDeviceData);
+    atomicOr(&g_io_err, kErrDeviceData);
     return -1;
+  }
+
+  // Calls row(u, out row, offset) for the rows of this warp, kInFlight at a time: first with
+  // load = true for each of them, then with load = false.
+  template <typename F>
+  __device__ __forceinline__ void each(int64_t total, int per_warp, F&& row) const {
+    const int lane = threadIdx.x & 31;
+    const int64_t first = ((blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5) * per_warp;
+    if (first >= total) return;
+    const int n = (int)min((int64_t)per_warp, total - first);
+    const int64_t mine = lane < n ? offset(first + lane) : -1;
+    __syncwarp();
+    for (int i = 0; i < n; i += kInFlight) {
+      int64_t off[kInFlight];
+#pragma unroll
+      for (int u = 0; u < kInFlight; ++u) {
+        off[u] = __shfl_sync(0xffffffffu, mine, min(i + u, 31));
+        if (i + u >= n) off[u] = -1;
+      }
+#pragma unroll
+      for (int u = 0; u < kInFlight; ++u)
+        if (off[u] >= 0) row(u, first + i + u, off[u], true);
+#pragma unroll
+      for (int u = 0; u < kInFlight; ++u)
+        if (off[u] >= 0) row(u, first + i + u, off[u], false);
+    }
   }
 };
 
-// A plain row: E words, bits unchanged.
-template <typename W>
+// A plain row: E words, bits unchanged; kWords words of each row in a lane at a time.
+template <typename W, int kWords>
 __global__ void __launch_bounds__(256) read_plain_kernel(W* __restrict__ out, int64_t o_s0, const W* __restrict__ cache,
-                                                         ReadRows rows, int64_t total, int32_t E) {
+                                                         ReadRows rows, int64_t total, int per_warp, int32_t E) {
   pdl_enter();
   const int lane = threadIdx.x & 31;
-  const int64_t step = ((int64_t)gridDim.x * blockDim.x) >> 5;
-  for (int64_t i = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5; i < total; i += step) {
-    const int64_t off = rows.offset(i, lane);
-    if (off < 0) continue;
-    for (int c = lane; c < E; c += 32) out[i * o_s0 + c] = cache[off + c];
+  for (int c0 = lane; c0 - lane < E; c0 += 32 * kWords) {
+    W v[kInFlight][kWords];
+    rows.each(total, per_warp, [&](int u, int64_t i, int64_t off, bool load) {
+#pragma unroll
+      for (int k = 0; k < kWords; ++k) {
+        const int c = c0 + 32 * k;
+        if (c >= E) continue;
+        if (load)
+          v[u][k] = cache[off + c];
+        else
+          out[i * o_s0 + c] = v[u][k];
+      }
+    });
   }
 }
 
-// A row of E e4m3 codes, each times *scale. vec: E and the strides multiples of 16 codes, 16-byte
-// aligned views.
+// Sixteen bytes of output: kN = 4 float32 or 8 bf16 values from as many codes, so that a warp's
+// stores cover whole lines (sixteen codes a lane, 32 or 64 bytes of output in steps of 16, wrote every
+// sector in parts: 29 us instead of 21 for 28K float32 rows).
+template <typename T>
+struct Chunk {
+  static constexpr int kN = 16 / sizeof(T);
+  using Codes = typename std::conditional<sizeof(T) == 4, uint32_t, uint2>::type;
+  static __device__ __forceinline__ void store(T* o, Codes c, float scale) {
+    float x[kN];
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&c);
+#pragma unroll
+    for (int i = 0; i < kN; i += 4) e4m3x4(w[i / 4], x + i);
+#pragma unroll
+    for (int i = 0; i < kN; ++i) x[i] *= scale;
+    store_n(o, x);
+  }
+};
+
+// A row of E e4m3 codes, each times *scale. vec: E and the strides multiples of 8 codes, 8-byte
+// aligned codes, 16-byte aligned output rows; kChunks chunks of each row in a lane at a time.
 template <typename T>
 __global__ void __launch_bounds__(256) read_fp8_kernel(T* __restrict__ out, int64_t o_s0, const uint8_t* __restrict__ cache,
-                                                       ReadRows rows, int64_t total, int32_t E,
+                                                       ReadRows rows, int64_t total, int per_warp, int32_t E,
                                                        const float* __restrict__ scale_p, int vec) {
   pdl_enter();
+  using C = Chunk<T>;
+  constexpr int kChunks = sizeof(T) == 4 ? 5 : 3;   // 640 values and 768: a row of 576 in one round
   const float scale = *scale_p;
   const int lane = threadIdx.x & 31;
-  const int64_t step = ((int64_t)gridDim.x * blockDim.x) >> 5;
-  for (int64_t i = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5; i < total; i += step) {
-    const int64_t off = rows.offset(i, lane);
-    if (off < 0) continue;
-    T* o = out + i * o_s0;
-    if (vec) {
-      for (int c = lane * 16; c < E; c += 512) {
-        float x[16];
-        e4m3x16(*reinterpret_cast<const uint4*>(cache + off + c), x);
+  if (vec) {
+    for (int c0 = 0; c0 < E; c0 += 32 * kChunks * C::kN) {
+      typename C::Codes v[kInFlight][kChunks];
+      rows.each(total, per_warp, [&](int u, int64_t i, int64_t off, bool load) {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) x[k] *= scale;
-        store_n(o + c, x);
-      }
-    } else {
-      for (int c = lane; c < E; c += 32) from_f(o + c, e4m3(cache[off + c]) * scale);
+        for (int k = 0; k < kChunks; ++k) {
+          const int c = c0 + (32 * k + lane) * C::kN;
+          if (c >= E) continue;
+          if (load)
+            v[u][k] = *reinterpret_cast<const typename C::Codes*>(cache + off + c);
+          else
+            C::store(out + i * o_s0 + c, v[u][k], scale);
+        }
+      });
     }
+  } else {
+    rows.each(total, per_warp, [&](int, int64_t i, int64_t off, bool load) {
+      if (load) return;
+      for (int c = lane; c < E; c += 32) from_f(out + i * o_s0 + c, e4m3(cache[off + c]) * scale);
+    });
   }
 }
 
@@ -226,56 +340,66 @@ __global__ void __launch_bounds__(256) read_fp8_kernel(T* __restrict__ out, int6
 template <typename T>
 __global__ void __launch_bounds__(256) read_ds_mla_kernel(T* __restrict__ out, int64_t o_s0,
                                                           const uint8_t* __restrict__ cache, ReadRows rows,
-                                                          int64_t total, int vec) {
+                                                          int64_t total, int per_warp, int vec) {
   pdl_enter();
+  using C = Chunk<T>;
+  constexpr int kChunks = kDsMlaLatent / (32 * C::kN);
   const int lane = threadIdx.x & 31;
-  const int64_t step = ((int64_t)gridDim.x * blockDim.x) >> 5;
-  for (int64_t i = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5; i < total; i += step) {
-    const int64_t off = rows.offset(i, lane);
-    if (off < 0) continue;
+  typename C::Codes codes[kInFlight][kChunks];
+  float scale[kInFlight][kChunks];
+  __nv_bfloat162 pe[kInFlight];
+  rows.each(total, per_warp, [&](int u, int64_t i, int64_t off, bool load) {
     const uint8_t* e = cache + off;
     T* o = out + i * o_s0;
-    const uint4 codes = *reinterpret_cast<const uint4*>(e + lane * 16);
-    const float scale = *reinterpret_cast<const float*>(e + kDsMlaLatent + 4 * (lane >> 3));
-    float x[16], r[8] = {};
-    if (lane < 8) load_n(reinterpret_cast<const __nv_bfloat16*>(e + kDsMlaRopeByte) + lane * 8, r);
-    e4m3x16(codes, x);
+    if (load) {
 #pragma unroll
-    for (int k = 0; k < 16; ++k) x[k] *= scale;
-    if (vec) {
-      store_n(o + lane * 16, x);
-      if (lane < 8) store_n(o + kDsMlaLatent + lane * 8, r);
+      for (int k = 0; k < kChunks; ++k) {
+        const int c = (32 * k + lane) * C::kN;
+        codes[u][k] = *reinterpret_cast<const typename C::Codes*>(e + c);
+        scale[u][k] = *reinterpret_cast<const float*>(e + kDsMlaLatent + 4 * (c / kDsMlaGroup));
+      }
+      pe[u] = reinterpret_cast<const __nv_bfloat162*>(e + kDsMlaRopeByte)[lane];
+    } else if (vec) {
+#pragma unroll
+      for (int k = 0; k < kChunks; ++k) C::store(o + (32 * k + lane) * C::kN, codes[u][k], scale[u][k]);
+      store2(o + kDsMlaLatent + 2 * lane, pe[u]);
     } else {
 #pragma unroll
-      for (int k = 0; k < 16; ++k) from_f(o + lane * 16 + k, x[k]);
-      if (lane < 8) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) from_f(o + kDsMlaLatent + lane * 8 + k, r[k]);
+      for (int k = 0; k < kChunks; ++k) {
+        const int c = (32 * k + lane) * C::kN;
+        for (int m = 0; m < C::kN; ++m)
+          from_f(o + c + m, e4m3(reinterpret_cast<const uint8_t*>(&codes[u][k])[m]) * scale[u][k]);
       }
+      const float2 f = __bfloat1622float2(pe[u]);
+      from_f(o + kDsMlaLatent + 2 * lane, f.x);
+      from_f(o + kDsMlaLatent + 2 * lane + 1, f.y);
     }
-  }
+  });
 }
 
 inline bool aligned(const void* p, int a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-// One warp a row, eight rows a block, at most 16 blocks an SM (the kernels stride over the rest).
-int row_grid(int64_t rows) {
-  const int64_t want = (rows + 7) / 8, cap = (int64_t)device_sm_count() * 16;
-  return (int)(want < cap ? want : cap);
+// Rows a warp takes, a multiple of kInFlight but for few rows: 32 where that leaves each SM 32 warps
+// or more, else fewer, down to one.
+int rows_per_warp(int64_t rows) {
+  const int64_t per = rows / ((int64_t)device_sm_count() * 32);
+  return per >= kMostRows ? kMostRows : per >= kInFlight ? (int)(per / kInFlight * kInFlight) : 1;
 }
+unsigned row_grid(int64_t rows, int per_warp) { return (unsigned)((rows + 8 * per_warp - 1) / (8 * per_warp)); }
 
 ReadRows read_rows(const CacheRead& r) {
   return ReadRows{r.block_table, r.bt_stride, r.max_blocks, r.cu_seqlens, r.seq_starts, r.batch,
                   r.cache.s_blk, r.cache.s_row, r.cache.num_blocks, r.cache.page};
 }
 
-template <typename W>
+template <typename W, int kWords>
 cudaError_t launch_plain(const CacheRead& r, int64_t per, cudaStream_t st) {
   ReadRows rows = read_rows(r);
   rows.s_blk /= per;
   rows.s_row /= per;
-  return launch_k(read_plain_kernel<W>, row_grid(r.rows), 256, 0, st, (W*)r.out, r.out_s0 / per, (const W*)r.cache.data,
-                  rows, r.rows, (int32_t)(r.cache.entry / per));
+  const int pw = rows_per_warp(r.rows);
+  return launch_k(read_plain_kernel<W, kWords>, row_grid(r.rows, pw), 256, 0, st, (W*)r.out, r.out_s0 / per,
+                  (const W*)r.cache.data, rows, r.rows, pw, (int32_t)(r.cache.entry / per));
 }
 
 }  // namespace
@@ -284,44 +408,49 @@ cudaError_t launch_cache_write_ds_mla(mla_dtype src_dt, const View3& cache, cons
                                       const int64_t* slots, int64_t tokens, cudaStream_t st) {
   const int64_t per = src_dt == MLA_F32 ? 4 : 8, rows = cache.n0 * cache.n1;
   const int vec = aligned(kv_c.data, 16) && aligned(k_pe.data, 16) && kv_c.s0 % per == 0 && k_pe.s0 % per == 0;
+  const int wide = aligned(kv_c.data, 32) && kv_c.s0 % (2 * per) == 0;
+  const int pw = rows_per_warp(tokens);
   if (src_dt == MLA_F32)
-    return launch_k(write_ds_mla_kernel<float>, row_grid(tokens), 256, 0, st, (uint8_t*)cache.data, cache.s0, cache.s1,
+    return launch_k(write_ds_mla_kernel<float>, row_grid(tokens, pw), 256, 0, st, (uint8_t*)cache.data, cache.s0, cache.s1,
                     rows, (int32_t)cache.n1, (const float*)kv_c.data, kv_c.s0, (const float*)k_pe.data, k_pe.s0, slots,
-                    tokens, vec);
-  return launch_k(write_ds_mla_kernel<__nv_bfloat16>, row_grid(tokens), 256, 0, st, (uint8_t*)cache.data, cache.s0,
+                    tokens, pw, vec, wide);
+  return launch_k(write_ds_mla_kernel<__nv_bfloat16>, row_grid(tokens, pw), 256, 0, st, (uint8_t*)cache.data, cache.s0,
                   cache.s1, rows, (int32_t)cache.n1, (const __nv_bfloat16*)kv_c.data, kv_c.s0,
-                  (const __nv_bfloat16*)k_pe.data, k_pe.s0, slots, tokens, vec);
+                  (const __nv_bfloat16*)k_pe.data, k_pe.s0, slots, tokens, pw, vec, wide);
 }
 
 cudaError_t launch_cache_read(mla_dtype dt, const CacheRead& r, cudaStream_t st) {
   const int64_t es = dt == MLA_F32 ? 4 : 2, per = 16 / es;
   if (aligned(r.out, 16) && aligned(r.cache.data, 16) && r.out_s0 % per == 0 && r.cache.s_blk % per == 0 &&
       r.cache.s_row % per == 0 && r.cache.entry % per == 0)
-    return launch_plain<uint4>(r, per, st);
-  return dt == MLA_F32 ? launch_plain<uint32_t>(r, 1, st) : launch_plain<uint16_t>(r, 1, st);
+    // 96 words hold a bf16 row of 576 values, 160 an fp32 one
+    return r.cache.entry / per <= 96 ? launch_plain<uint4, 3>(r, per, st) : launch_plain<uint4, 5>(r, per, st);
+  return dt == MLA_F32 ? launch_plain<uint32_t, 5>(r, 1, st) : launch_plain<uint16_t, 5>(r, 1, st);
 }
 
 cudaError_t launch_cache_read_fp8(mla_dtype dst_dt, const CacheRead& r, const float* scale, cudaStream_t st) {
   const int64_t per = dst_dt == MLA_F32 ? 4 : 8;
-  const int vec = aligned(r.out, 16) && r.out_s0 % per == 0 && aligned(r.cache.data, 16) && r.cache.s_blk % 16 == 0 &&
-                  r.cache.s_row % 16 == 0 && r.cache.entry % 16 == 0;
+  const int vec = aligned(r.out, 16) && r.out_s0 % per == 0 && aligned(r.cache.data, 8) && r.cache.s_blk % 8 == 0 &&
+                  r.cache.s_row % 8 == 0 && r.cache.entry % 8 == 0;
   const ReadRows rows = read_rows(r);
+  const int pw = rows_per_warp(r.rows);
   if (dst_dt == MLA_F32)
-    return launch_k(read_fp8_kernel<float>, row_grid(r.rows), 256, 0, st, (float*)r.out, r.out_s0,
-                    (const uint8_t*)r.cache.data, rows, r.rows, r.cache.entry, scale, vec);
-  return launch_k(read_fp8_kernel<__nv_bfloat16>, row_grid(r.rows), 256, 0, st, (__nv_bfloat16*)r.out, r.out_s0,
-                  (const uint8_t*)r.cache.data, rows, r.rows, r.cache.entry, scale, vec);
+    return launch_k(read_fp8_kernel<float>, row_grid(r.rows, pw), 256, 0, st, (float*)r.out, r.out_s0,
+                    (const uint8_t*)r.cache.data, rows, r.rows, pw, r.cache.entry, scale, vec);
+  return launch_k(read_fp8_kernel<__nv_bfloat16>, row_grid(r.rows, pw), 256, 0, st, (__nv_bfloat16*)r.out, r.out_s0,
+                  (const uint8_t*)r.cache.data, rows, r.rows, pw, r.cache.entry, scale, vec);
 }
 
 cudaError_t launch_cache_read_ds_mla(mla_dtype dst_dt, const CacheRead& r, cudaStream_t st) {
   const int64_t per = dst_dt == MLA_F32 ? 4 : 8;
   const int vec = aligned(r.out, 16) && r.out_s0 % per == 0;
   const ReadRows rows = read_rows(r);
+  const int pw = rows_per_warp(r.rows);
   if (dst_dt == MLA_F32)
-    return launch_k(read_ds_mla_kernel<float>, row_grid(r.rows), 256, 0, st, (float*)r.out, r.out_s0,
-                    (const uint8_t*)r.cache.data, rows, r.rows, vec);
-  return launch_k(read_ds_mla_kernel<__nv_bfloat16>, row_grid(r.rows), 256, 0, st, (__nv_bfloat16*)r.out, r.out_s0,
-                  (const uint8_t*)r.cache.data, rows, r.rows, vec);
+    return launch_k(read_ds_mla_kernel<float>, row_grid(r.rows, pw), 256, 0, st, (float*)r.out, r.out_s0,
+                    (const uint8_t*)r.cache.data, rows, r.rows, pw, vec);
+  return launch_k(read_ds_mla_kernel<__nv_bfloat16>, row_grid(r.rows, pw), 256, 0, st, (__nv_bfloat16*)r.out, r.out_s0,
+                  (const uint8_t*)r.cache.data, rows, r.rows, pw, vec);
 }
 
 unsigned cache_io_errors_read_clear() {
