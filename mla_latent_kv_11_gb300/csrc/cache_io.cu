@@ -1,9 +1,10 @@
 // Rows into and out of a quantised paged cache: the write of 656-byte fp8 ds_mla
 // entries, and the read-back of plain, e4m3 and ds_mla rows into contiguous rows.
 //
-// Both are bound by HBM: every byte of a row crosses it once. A warp takes up to 32
-// consecutive rows (few where there are few, so that all SMs have some): its lanes look up
-// where a row each lies, at once, and then the warp moves the rows, four in flight. A lane
+// Both are bound by HBM: every byte of a row crosses it once. A warp takes four consecutive
+// rows (one where there are few, so that every SM has some): a lane each looks up where they
+// lie, at once, and the warp then has all four in flight (eight or more rows a warp, taken
+// four by four, left too few warps at the end: 10 to 30% slower at 40000 rows). In the write a lane
 // holds 16 consecutive latent values of a row, so a 512-wide latent part is one pass of the
 // warp; a 128-column scale group is eight lanes, and its maximum three exchanges.
 #include <cfloat>
@@ -28,9 +29,7 @@ __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float
 __device__ __forceinline__ void from_f(float* p, float v) { *p = v; }
 __device__ __forceinline__ void from_f(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-// Consecutive rows a warp takes.
-constexpr int kMostRows = 32;
-constexpr int kInFlight = 4;
+constexpr int kInFlight = 4;   // rows a warp takes, at most
 
 // Sixteen consecutive values as floats: 32 bytes a load where `wide` (32-byte aligned), else 16.
 __device__ __forceinline__ void load_words(const void* p, uint32_t (&w)[8], bool wide) {
@@ -234,8 +233,8 @@ struct ReadRows {
     return -1;
   }
 
-  // Calls row(u, out row, offset) for the rows of this warp, kInFlight at a time: first with
-  // load = true for each of them, then with load = false.
+  // Calls row(u, out row, offset, load) for the rows of this warp: first with load = true for each of
+  // them, then with load = false.
   template <typename F>
   __device__ __forceinline__ void each(int64_t total, int per_warp, F&& row) const {
     const int lane = threadIdx.x & 31;
@@ -243,21 +242,15 @@ struct ReadRows {
     if (first >= total) return;
     const int n = (int)min((int64_t)per_warp, total - first);
     const int64_t mine = lane < n ? offset(first + lane) : -1;
-    __syncwarp();
-    for (int i = 0; i < n; i += kInFlight) {
-      int64_t off[kInFlight];
+    int64_t off[kInFlight];
 #pragma unroll
-      for (int u = 0; u < kInFlight; ++u) {
-        off[u] = __shfl_sync(0xffffffffu, mine, min(i + u, 31));
-        if (i + u >= n) off[u] = -1;
-      }
+    for (int u = 0; u < kInFlight; ++u) off[u] = __shfl_sync(0xffffffffu, mine, u);
 #pragma unroll
-      for (int u = 0; u < kInFlight; ++u)
-        if (off[u] >= 0) row(u, first + i + u, off[u], true);
+    for (int u = 0; u < kInFlight; ++u)
+      if (off[u] >= 0) row(u, first + u, off[u], true);
 #pragma unroll
-      for (int u = 0; u < kInFlight; ++u)
-        if (off[u] >= 0) row(u, first + i + u, off[u], false);
-    }
+    for (int u = 0; u < kInFlight; ++u)
+      if (off[u] >= 0) row(u, first + u, off[u], false);
   }
 };
 
@@ -379,12 +372,8 @@ __global__ void __launch_bounds__(256) read_ds_mla_kernel(T* __restrict__ out, i
 
 inline bool aligned(const void* p, int a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-// Rows a warp takes, a multiple of kInFlight but for few rows: 32 where that leaves each SM 32 warps
-// or more, else fewer, down to one.
-int rows_per_warp(int64_t rows) {
-  const int64_t per = rows / ((int64_t)device_sm_count() * 32);
-  return per >= kMostRows ? kMostRows : per >= kInFlight ? (int)(per / kInFlight * kInFlight) : 1;
-}
+// Rows a warp takes: four where that still gives each SM eight warps.
+int rows_per_warp(int64_t rows) { return rows >= (int64_t)device_sm_count() * 32 ? kInFlight : 1; }
 unsigned row_grid(int64_t rows, int per_warp) { return (unsigned)((rows + 8 * per_warp - 1) / (8 * per_warp)); }
 
 ReadRows read_rows(const CacheRead& r) {
