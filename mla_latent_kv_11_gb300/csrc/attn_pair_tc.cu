@@ -45,6 +45,7 @@
 
 #include "mla_internal.h"
 #include "sm100_ptx.cuh"
+#include "window_sched.cuh"
 
 namespace mla {
 namespace {
@@ -53,7 +54,7 @@ using namespace ptx;
 
 __device__ unsigned g_pair_err = 0;
 
-constexpr int kBlk = 64;                     // cache rows per block: the keys of one CTA
+// a block of 64 cache rows (kBlk): the keys of one CTA
 constexpr int kTileKeys = 2 * kBlk;          // keys per tile
 constexpr int kBox = kBlk * 128;             // 64 rows x 64 bf16 columns, 128-byte swizzle
 constexpr int kThreads = 384;
@@ -62,8 +63,6 @@ constexpr int kSoftmaxThreads = 256;
 constexpr int kSoftmaxBar = 1;
 constexpr float kLazyRescale = 8.f;
 constexpr uint32_t kTmemS = 256, kTmemOut = 384, kTmemCols = 512;
-constexpr int kSegCost = 1;                  // cost of starting a row tile, in tiles
-constexpr int kSplitItems = 1024;            // row tiles up to which the schedule splits them
 
 template <int kRope>
 struct PairCfg {
@@ -97,121 +96,29 @@ struct PairShared {
 };
 static_assert(sizeof(PairShared) <= 3072, "barrier block overflows its slot");
 
-// The work of a unit: segments [t0, t1) of row tiles ("items").
-struct Seg {
-  int tok0, ntok, pos0, b;   // first token's row, tokens, its position, sequence
-  int lo, hi;                // first window row and last row any token attends
-  int nsb, wb, nblk;         // sink blocks, first window block behind them, blocks in all
-  int t0, t1, slot;          // tile range; partial slot or -1
-};
-
 struct PairParams {
   int H, tpt, tptc;          // heads, tokens per row tile, tokens per CTA (heads split when H > 64: tptc 0)
   int window, sinks;
   float scale_log2;
-  __nv_bfloat16* o_lat;
-  int64_t o_s0, o_s1;
-  float* lse;
+  WindowSched sched;
+  WindowOut out;             // partial rows of a slot: 64 * CTA + row
   int page, num_blocks;
   const int32_t* block_table;
   int64_t bt_stride;
-  const int4* items;         // two words a row tile (Item)
-  const int32_t* total;      // row tiles
-  const int2* unit_start;    // split: {row tile, tile} of each unit's first; null: whole row tiles dealt out
-  float* part_o;             // [2 * units][128][512], row 64 * CTA + row
-  float* part_lse;           // [2 * units][128]
   int o_32B;                 // output rows lie on 32-byte boundaries: whole sectors a store
   int q_whole;               // the queries' column groups come in one load
   int prefetch;              // bring the tile after the next into L2 (rows come from HBM, each read once)
 };
 
-__host__ __device__ inline int row_tiles(int nblk) { return nblk > 0 ? (nblk + 1) / 2 : 1; }
-
-// A row tile as the schedule describes it: {first token's row, tokens, its position, sequence} and
-// {first window row, sink blocks, first window block behind them, blocks in all}. Its tokens sit at
-// pos0 .. pos0 + ntok - 1.
-struct Item {
-  int4 a, b;
-};
-__device__ __forceinline__ Item make_item(int tok0, int ntok, int pos0, int seq, int window, int sinks) {
-  const int hi = pos0 + ntok - 1, lo = max(0, pos0 - window + 1);
-  int nsb = 0, wb = 0, nblk = 0;
-  if (hi >= 0) {
-    nsb = (min(sinks, hi + 1) + kBlk - 1) / kBlk;
-    wb = max(lo / kBlk, nsb);
-    nblk = nsb + max(0, hi / kBlk + 1 - wb);
-  }
-  return Item{make_int4(tok0, ntok, pos0, seq), make_int4(lo, nsb, wb, nblk)};
-}
-__device__ __forceinline__ Item load_item(const int4* items, int i) { return Item{items[2 * i], items[2 * i + 1]}; }
-__device__ __forceinline__ void store_item(int4* items, int i, const Item& it) {
-  items[2 * i] = it.a;
-  items[2 * i + 1] = it.b;
-}
-
-struct Walker {
-  int unit, units, item, step, end_item, end_tile, tile;
-  Item ahead;   // the next row tile, loaded while the one before it runs
-
-  __device__ void init(const PairParams& p, int unit_, int units_) {
-    unit = unit_;
-    units = units_;
-    const int total = *p.total;
-    if (p.unit_start != nullptr) {
-      const int2 a = p.unit_start[unit], e = p.unit_start[unit + 1];
-      item = a.x;
-      tile = a.y;
-      end_item = e.x;
-      end_tile = e.y;
-      step = 1;
-    } else {   // the longest (latest) row tiles first
-      item = total - 1 - unit;
-      tile = 0;
-      step = -units;
-      end_item = -1;
-      end_tile = 0;
-    }
-    if (more()) ahead = load_item(p.items, item);
-  }
-  __device__ bool more() const {
-    return step > 0 ? (item < end_item || (item == end_item && tile < end_tile)) : item >= 0;
-  }
-  // The next segment; the description of the one behind it is loaded meanwhile.
-  __device__ bool next(const PairParams& p, Seg& s) {
-    if (!more()) return false;
-    s.tok0 = ahead.a.x;
-    s.ntok = ahead.a.y;
-    s.pos0 = ahead.a.z;
-    s.b = ahead.a.w;
-    s.lo = ahead.b.x;
-    s.hi = s.pos0 + s.ntok - 1;
-    s.nsb = ahead.b.y;
-    s.wb = ahead.b.z;
-    s.nblk = ahead.b.w;
-    const int nt = row_tiles(s.nblk);
-    s.t0 = tile;
-    s.t1 = step > 0 && item == end_item ? min(nt, end_tile) : nt;
-    s.slot = s.t0 == 0 && s.t1 == nt ? -1 : 2 * unit + (s.t0 == 0 ? 1 : 0);
-    item += step;
-    tile = 0;
-    if (more()) ahead = load_item(p.items, item);
-    return true;
-  }
-};
 
 // The walker's next segment for a role that issues from a whole warp: its tiles [first, return
 // value), none (0, 0) behind the last. Values that come from memory are not uniform to the compiler,
 // and under a branch on them it forms every operand of the MMAs and loads in vector registers (an MMA
 // then took 75 cycles to issue, a load 300); the results of a reduction over the warp are.
-__device__ __forceinline__ int open_segment(Walker& wk, const PairParams& p, Seg& s, int& first) {
-  const bool any = wk.next(p, s);
+__device__ __forceinline__ int open_segment(Walker<2>& wk, Seg& s, int& first) {
+  const bool any = wk.next(s);
   first = __reduce_max_sync(0xffffffffu, any ? s.t0 : 0);
   return __reduce_max_sync(0xffffffffu, any ? s.t1 : 0);
-}
-
-// First row of block j of a segment's list; -1 behind its end.
-__device__ __forceinline__ int block_row(const Seg& s, int j) {
-  return j >= s.nblk ? -1 : kBlk * (j < s.nsb ? j : s.wb + (j - s.nsb));
 }
 
 // The wait behind a first look, kept out of line: the roles' loops have to stay in the instruction
@@ -403,14 +310,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // keys, which the tensor pipe waits for (two quarters of a tile each), warp 3 the rest. The whole warp walks the tiles. Lane h looks
     // up the block id of a tile's block h (small pages: lanes 8h .. 8h + 7 the ids of its pages).
     const int rows_box = kSmall ? p.page : kBlk, subs = kBlk / rows_box;
-    Walker wk;
-    wk.init(p, unit, units);
+    Walker<2> wk;
+    wk.init(p.sched, unit, units);
     Seg sg;
     bool ok = true;
     int j = 0, nt = 0;   // next tile of the open segment, its end; both warp-uniform
     bool fresh = true;
     auto open = [&]() {
-      nt = open_segment(wk, p, sg, j);
+      nt = open_segment(wk, sg, j);
       fresh = true;
     };
     open();
@@ -577,8 +484,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t dq = desc_lo(sQ, 16), dp = desc_lo(sP, 16), dk = desc_lo(sKV, 16), dv = desc_lo(sKV, kBox),
                    dr = desc_lo(sR, 16);
     constexpr int kStep = kBox / 16;   // one box, in a descriptor's 16-byte units
-    Walker wk;
-    wk.init(p, unit, units);
+    Walker<2> wk;
+    wk.init(p.sched, unit, units);
     Seg sg;
     int g = 0, seg_i = 0;
     bool ok = true, pv_first = true;   // pv_first: the pending PV starts its segment's O
@@ -626,7 +533,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         commit_pair(&sh.pv_done[b][i]);
       }
     };
-    int t0 = 0, t1 = open_segment(wk, p, sg, t0);
+    int t0 = 0, t1 = open_segment(wk, sg, t0);
     while (ok && t0 < t1) {
       for (int j = t0; ok && j < t1; ++j, ++g) {
         if (j == t0) {
@@ -643,7 +550,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       ++seg_i;
-      t1 = open_segment(wk, p, sg, t0);
+      t1 = open_segment(wk, sg, t0);
     }
     if (ok && g > 0) pv(g - 1);
     if (!ok && lane == 0) give_up();
@@ -662,8 +569,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int head = p.tptc ? row % p.H : 64 * (int)rank + row;
     const bool real = p.tptc ? row < p.tptc * p.H : head < p.H;
     auto group_all = [](bool v) { return named_bar_and(kSoftmaxBar, kSoftmaxThreads, v); };
-    Walker wk;
-    wk.init(p, unit, units);
+    Walker<2> wk;
+    wk.init(p.sched, unit, units);
     Seg sg;
     // the output that waits in tensor memory: quarters left of this thread's 128 columns, its row
     int left = 0;
@@ -688,7 +595,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     };
     int g = 0;
     bool ok = true, mine = true;   // ok: the group's decision; mine: this thread's waits so far
-    while (ok && wk.next(p, sg)) {
+    while (ok && wk.next(sg)) {
       const bool valid = real && tok < sg.ntok;
       const int pos = valid ? sg.pos0 + tok : -1;       // -1 attends nothing
       float m = -CUDART_INF_F, l = 0.f;
@@ -823,9 +730,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tmem_st_wait();
         left = 4;
         // a lane whose row is not real stores nothing
-        to = valid ? p.o_lat + (int64_t)(sg.tok0 + tok) * p.o_s0 + (int64_t)head * p.o_s1 + 256 * half + 128 * part : nullptr;
+        to = valid ? static_cast<__nv_bfloat16*>(p.out.o) + (int64_t)(sg.tok0 + tok) * p.out.o_s0 + (int64_t)head * p.out.o_s1 +
+                         256 * half + 128 * part
+                   : nullptr;
       } else {
-        float* const o = p.part_o + prow * 512 + 256 * half + 128 * part;
+        float* const o = p.out.part_o + prow * 512 + 256 * half + 128 * part;
         float v[16];
         tmem_ld16(tmem + lane_addr + 128 * part, v);
 #pragma unroll 1
@@ -845,9 +754,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (valid && half == 0 && part == 0) {
         const float lse = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -CUDART_INF_F;
         if (sg.slot >= 0)
-          p.part_lse[prow] = lse;
-        else if (p.lse != nullptr)
-          p.lse[(int64_t)(sg.tok0 + tok) * p.H + head] = lse;
+          p.out.part_lse[prow] = lse;
+        else if (p.out.lse != nullptr)
+          p.out.lse[(int64_t)(sg.tok0 + tok) * p.H + head] = lse;
       }
     }
     while (left > 0) store_quarter();
@@ -867,211 +776,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     dealloc_pair(tmem, kTmemCols);
   }
   cluster_sync();
-}
-
-// ------------------------------------------------------------------ schedule
-struct PairSched {
-  const int32_t* cu_q;     // null: a decode, one token a sequence
-  const int32_t* kv_lens;
-  int B, T, cap, tpt, window, sinks, units;
-  int4* items;
-  int32_t* total;
-  int2* unit_start;
-  int32_t* prefix;         // [B + 1] row tiles before each sequence (many row tiles only)
-};
-
-__device__ __forceinline__ int kv_len(const PairSched& s, int b) {
-  int n = s.kv_lens[b];
-  if (n < 0 || n > s.cap) {
-    atomicOr(&g_pair_err, kErrDeviceData);
-    n = n < 0 ? 0 : s.cap;
-  }
-  return n;
-}
-
-// Query tokens of sequence b; 0 (and reported) where cu_q leaves [0, T] or decreases.
-__device__ __forceinline__ int q_len(const PairSched& s, int b, int& q0) {
-  if (s.cu_q == nullptr) {
-    q0 = b;
-    return 1;
-  }
-  q0 = s.cu_q[b];
-  const int q1 = s.cu_q[b + 1];
-  if (q0 < 0 || q1 > s.T || q1 < q0) {
-    atomicOr(&g_pair_err, kErrDeviceData);
-    return 0;
-  }
-  return q1 - q0;
-}
-
-// Exclusive block scan of one int a thread (blockDim.x a multiple of 32).
-__device__ int scan_block(int v, int* warp_tot, int* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  int x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  __syncthreads();
-  if (lane == 31) warp_tot[warp] = x;
-  __syncthreads();
-  int before = 0, all = 0;
-  for (int w = 0; w < warps; ++w) {
-    if (w < warp) before += warp_tot[w];
-    all += warp_tot[w];
-  }
-  *total = all;
-  return before + x - v;
-}
-
-// Up to kSplitItems row tiles: their descriptions, and the units' starts: contiguous ranges of
-// tiles of equal cost, a row tile costing its tiles plus kSegCost. One block; a thread a
-// sequence, then a thread a row tile, then a thread a unit.
-__global__ void __launch_bounds__(1024) pair_split_kernel(PairSched s) {
-  __shared__ int warp_tot[32], first[kSplitItems + 1], q_begin[kSplitItems], q_count[kSplitItems], len[kSplitItems],
-      cost[kSplitItems + 1], tiles[kSplitItems];
-  pdl_enter();
-  const int i = threadIdx.x;
-  int n = 0, q0 = 0, total;
-  if (i < s.B) {
-    const int k = q_len(s, i, q0);
-    n = (k + s.tpt - 1) / s.tpt;
-    q_begin[i] = q0;
-    q_count[i] = k;
-    len[i] = kv_len(s, i);
-  }
-  const int ex = scan_block(n, warp_tot, &total);
-  if (i < s.B) first[i] = ex;
-  __syncthreads();
-  int nt = 0;
-  if (i < total) {
-    int lo = 0, hi = s.B - 1;   // the last sequence with first <= i: it has row tiles
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (first[mid] <= i) lo = mid; else hi = mid - 1;
-    }
-    const int t0 = (i - first[lo]) * s.tpt, ntok = min(s.tpt, q_count[lo] - t0);
-    const int pos0 = len[lo] - q_count[lo] + t0;
-    const Item it = make_item(q_begin[lo] + t0, ntok, pos0, lo, s.window, s.sinks);
-    store_item(s.items, i, it);
-    nt = row_tiles(it.b.w);
-  }
-  int all;
-  const int at = scan_block(i < total ? nt + kSegCost : 0, warp_tot, &all);
-  if (i < total) {
-    cost[i] = at;
-    tiles[i] = nt;
-  }
-  if (i == 0) *s.total = total;
-  __syncthreads();
-  // unit u starts at cost u * all / active: units beyond the tiles there are get nothing
-  const int active = max(1, min(s.units, all - kSegCost * total));
-  for (int u = i; u <= s.units; u += blockDim.x) {
-    int2 start = make_int2(total, 0);
-    if (u < active && total > 0) {
-      const int x = (int)((long long)u * all / active);
-      int lo = 0, hi = total - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (cost[mid] <= x) lo = mid; else hi = mid - 1;
-      }
-      const int into = max(0, x - cost[lo] - kSegCost);
-      start = into >= tiles[lo] ? make_int2(lo + 1, 0) : make_int2(lo, into);
-    }
-    s.unit_start[u] = start;
-  }
-}
-
-// More row tiles: how many lie before each sequence (one block), then a thread a row tile.
-__global__ void __launch_bounds__(1024) pair_prefix_kernel(PairSched s) {
-  __shared__ int warp_tot[32];
-  pdl_enter();
-  int carry = 0;
-  for (int base = 0; base < s.B; base += blockDim.x) {
-    const int b = base + threadIdx.x;
-    int q0, tot;
-    const int n = b < s.B ? (q_len(s, b, q0) + s.tpt - 1) / s.tpt : 0;
-    if (b < s.B) kv_len(s, b);   // reports a bad length
-    const int ex = scan_block(n, warp_tot, &tot);
-    if (b < s.B) s.prefix[b] = carry + ex;
-    carry += tot;
-  }
-  if (threadIdx.x == 0) {
-    s.prefix[s.B] = carry;
-    *s.total = carry;
-  }
-}
-
-__global__ void __launch_bounds__(256) pair_items_kernel(PairSched s) {
-  pdl_enter();
-  const int i = blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= s.prefix[s.B]) return;
-  int lo = 0, hi = s.B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (s.prefix[mid] <= i) lo = mid; else hi = mid - 1;
-  }
-  int q0 = lo, q1 = lo + 1;
-  if (s.cu_q != nullptr) {
-    q0 = s.cu_q[lo];
-    q1 = s.cu_q[lo + 1];
-  }
-  const int t0 = (i - s.prefix[lo]) * s.tpt;
-  const int kv = min(max(s.kv_lens[lo], 0), s.cap);
-  store_item(s.items, i, make_item(q0 + t0, min(s.tpt, q1 - q0 - t0), kv - (q1 - q0) + t0, lo, s.window, s.sinks));
-}
-
-// Row tiles cut across units: their pieces merged by log-sum-exp. Block (u, .) handles the row
-// tile that unit u + 1 is the first to start inside of; one warp a row.
-__global__ void __launch_bounds__(128) pair_combine_kernel(PairParams p, int units) {
-  pdl_enter();
-  const int u = blockIdx.x + 1;
-  const int2 at = p.unit_start[u], before = p.unit_start[u - 1];
-  if (at.x >= *p.total || at.y == 0 || (before.x == at.x && before.y > 0)) return;
-  const int4 d = p.items[2 * at.x];
-  const int lane = threadIdx.x & 31;
-  // row rr of CTA `rank` of the tile, its token and head
-  const int rank = blockIdx.y & 1, rr = (blockIdx.y >> 1) * 4 + (threadIdx.x >> 5);
-  const int t = p.tptc ? p.tptc * rank + rr / p.H : 0, h = p.tptc ? rr % p.H : 64 * rank + rr;
-  if ((p.tptc && rr >= p.tptc * p.H) || h >= p.H || t >= d.y) return;
-  const int row = 64 * rank + rr;
-  // pieces: the head in unit u - 1 (slot 2 (u - 1) + 1), then units u, u + 1, ... (slots 2 v)
-  int np = 1;
-  while (u + np <= units) {
-    const int2 v = p.unit_start[u + np];
-    if (v.x != at.x || v.y == 0) break;
-    ++np;
-  }
-  auto slot = [&](int i) { return (int64_t)(i == 0 ? 2 * u - 1 : 2 * (u + i - 1)); };
-  float m = -CUDART_INF_F;
-  for (int i = 0; i <= np; ++i) m = fmaxf(m, p.part_lse[slot(i) * 128 + row]);
-  float4 acc[4] = {};
-  float tot = 0.f;
-  for (int i = 0; i <= np; ++i) {
-    const float li = p.part_lse[slot(i) * 128 + row];
-    const float w = li == -CUDART_INF_F ? 0.f : __expf(li - m);
-    tot += w;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float4 v = *reinterpret_cast<const float4*>(p.part_o + (slot(i) * 128 + row) * 512 + 128 * k + 4 * lane);
-      acc[k].x = fmaf(w, v.x, acc[k].x);
-      acc[k].y = fmaf(w, v.y, acc[k].y);
-      acc[k].z = fmaf(w, v.z, acc[k].z);
-      acc[k].w = fmaf(w, v.w, acc[k].w);
-    }
-  }
-  const float inv = tot > 0.f ? 1.f / tot : 0.f;
-  __nv_bfloat16* o = p.o_lat + (int64_t)(d.x + t) * p.o_s0 + (int64_t)h * p.o_s1 + 4 * lane;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(acc[k].x * inv, acc[k].y * inv);
-    const __nv_bfloat162 b = __floats2bfloat162_rn(acc[k].z * inv, acc[k].w * inv);
-    *reinterpret_cast<uint2*>(o + 128 * k) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-  }
-  if (lane == 0 && p.lse != nullptr)
-    p.lse[(int64_t)(d.x + t) * p.H + h] = tot > 0.f ? m + logf(tot) : -CUDART_INF_F;
 }
 
 template <int kRope, bool kSmall>
@@ -1117,30 +821,6 @@ cudaError_t launch_attn(const PairParams& p, const WindowMaps& maps, int units, 
 
 int pair_tokens(int H) { return H > 64 ? 1 : 2 * (64 / H); }
 
-struct PairWs {
-  size_t off_total, off_items, off_starts, off_prefix, off_o, off_lse, total;
-};
-PairWs pair_ws(int64_t items, int64_t batch, int64_t units) {
-  auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
-  PairWs w{};
-  w.off_total = 0;
-  w.off_items = 256;
-  w.off_starts = up(w.off_items + items * sizeof(Item));
-  w.off_prefix = up(w.off_starts + (units + 1) * sizeof(int2));
-  w.off_o = up(w.off_prefix + (batch + 1) * sizeof(int32_t));
-  // partial slots: two a unit where the schedule splits row tiles
-  w.off_lse = up(w.off_o + (items <= kSplitItems ? 2 * units * 128 * 512 * sizeof(float) : 0));
-  w.total = up(w.off_lse + (items <= kSplitItems ? 2 * units * 128 * sizeof(float) : 0));
-  return w;
-}
-
-// Row tiles of T tokens in B sequences, at most.
-int64_t most_items(int64_t T, int64_t B, int H, bool decode) {
-  if (decode) return B;
-  const int tpt = pair_tokens(H);
-  return tpt == 1 ? T : std::min<int64_t>(T, T / tpt + B);
-}
-
 // Whether a CTA's queries fill its 64 rows, so that one load lays all their column groups out.
 bool q_whole(int H) { return H >= 64 || 64 % H == 0; }
 
@@ -1175,60 +855,34 @@ bool window_tc_supported(mla_dtype dt, const WindowCall& c, WindowMaps* maps) {
 
 size_t window_tc_workspace(int64_t T, int64_t B, int H, bool decode, int num_splits) {
   if (H <= 0 || H > 128) return 0;
-  return pair_ws(most_items(T, B, H, decode), B, num_splits > 0 ? num_splits : max_pairs<64, false>()).total;
+  return window_workspace(T, B, decode, pair_tokens(H), num_splits > 0 ? num_splits : max_pairs<64, false>(), 128, 512);
 }
 
 cudaError_t launch_window_tc(const WindowCall& c, const WindowMaps& maps, int num_splits, void* ws, cudaStream_t st) {
-  const bool decode = c.cu_q == nullptr;
-  const int units = num_splits > 0 ? num_splits : max_pairs<64, false>();
-  const int64_t items = most_items(c.q.n0, c.B, c.H, decode);
-  const PairWs w = pair_ws(items, c.B, units);
-  char* base = static_cast<char*>(ws);
-  const bool split = items <= kSplitItems && c.B <= kSplitItems;
-  constexpr int kFar = 0x3fffffff;   // positions stay below this
-  const long long cap = (long long)c.max_blocks * c.cache.page;
-  PairSched s{c.cu_q, c.kv_lens, c.B, (int)c.q.n0, (int)std::min<long long>(cap, kFar), pair_tokens(c.H),
-              std::min(c.window.window, kFar), std::min(c.window.sinks, kFar), units,
-              reinterpret_cast<int4*>(base + w.off_items), reinterpret_cast<int32_t*>(base + w.off_total),
-              reinterpret_cast<int2*>(base + w.off_starts), reinterpret_cast<int32_t*>(base + w.off_prefix)};
-  cudaError_t e;
-  if (split) {
-    const int threads = (int)std::min<int64_t>(1024, (std::max<int64_t>({items, c.B, std::min(units + 1, 128)}) + 31) / 32 * 32);
-    e = launch_k(pair_split_kernel, 1, threads, 0, st, s);
-  } else {
-    e = launch_k(pair_prefix_kernel, 1, 1024, 0, st, s);
-    if (e == cudaSuccess) e = launch_k(pair_items_kernel, (unsigned)((items + 255) / 256), 256, 0, st, s);
-  }
-  if (e != cudaSuccess) return e;
+  const int units = num_splits > 0 ? num_splits : max_pairs<64, false>(), tpt = pair_tokens(c.H);
   PairParams p{};
+  cudaError_t e = launch_window_schedule(c, tpt, 2, units, 128, ws, &p.sched, &p.out, st);
+  if (e != cudaSuccess) return e;
   p.H = c.H;
-  p.tpt = s.tpt;
-  p.tptc = c.H > 64 ? 0 : s.tpt / 2;
-  p.window = s.window;
-  p.sinks = s.sinks;
+  p.tpt = tpt;
+  p.tptc = p.out.tptc = c.H > 64 ? 0 : tpt / 2;
+  constexpr int kFar = 0x3fffffff;   // positions stay below this
+  p.window = std::min(c.window.window, kFar);
+  p.sinks = std::min(c.window.sinks, kFar);
   p.scale_log2 = c.scale * 1.4426950408889634f;
-  p.o_lat = static_cast<__nv_bfloat16*>(c.o.data);
-  p.o_s0 = c.o.s0;
-  p.o_s1 = c.o.s1;
-  p.lse = c.lse;
   p.page = c.cache.page;
   p.num_blocks = c.cache.num_blocks;
   p.block_table = c.block_table;
   p.bt_stride = c.bt_stride;
-  p.items = s.items;
-  p.total = s.total;
-  p.unit_start = split ? s.unit_start : nullptr;
-  p.part_o = reinterpret_cast<float*>(base + w.off_o);
-  p.part_lse = reinterpret_cast<float*>(base + w.off_lse);
-  p.prefetch = split;
+  p.prefetch = p.sched.unit_start != nullptr;
   p.q_whole = q_whole(c.H);
   p.o_32B = reinterpret_cast<uintptr_t>(c.o.data) % 32 == 0 && c.o.s0 % 16 == 0 && c.o.s1 % 16 == 0;
   if (p.page < kBlk)
     e = c.R == 64 ? launch_attn<64, true>(p, maps, units, st) : launch_attn<0, true>(p, maps, units, st);
   else
     e = c.R == 64 ? launch_attn<64, false>(p, maps, units, st) : launch_attn<0, false>(p, maps, units, st);
-  if (e != cudaSuccess || !split || units < 2) return e;
-  return launch_k(pair_combine_kernel, dim3(units - 1, 32), 128, 0, st, p, units);
+  if (e != cudaSuccess) return e;
+  return launch_window_merge(MLA_BF16, p.sched, p.out, units, st);
 }
 
 unsigned attn_pair_errors_read_clear() {

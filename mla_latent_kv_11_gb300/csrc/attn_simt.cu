@@ -293,28 +293,6 @@ struct PagedRows {
   __device__ float at(int64_t base, int e) const { return ld(cache + base + e) * dk; }
 };
 
-// The rows a windowed query attends, counted 0 .. n - 1: its sequence's first `sinks` rows (those
-// before the window), then the window's rows from `lo` on.
-template <typename K>
-struct WindowRows {
-  PagedRows<K> paged;
-  int sinks, lo;
-  __device__ int64_t row(int j) const { return paged.row(j < sinks ? j : lo + (j - sinks)); }
-  __device__ float at(int64_t base, int e) const { return paged.at(base, e); }
-};
-
-// The window of a query at position p: rows [lo, p] and, before them, rows [0, sinks); returns how
-// many they are (0 for p < 0).
-__device__ __forceinline__ int window_rows(int p, const WindowArgs& w, int& sinks, int& lo) {
-  if (p < 0) {
-    sinks = lo = 0;
-    return 0;
-  }
-  lo = max(0, p - w.window + 1);   // window >= 1: no overflow
-  sinks = min(w.sinks, lo);
-  return sinks + (p + 1 - lo);
-}
-
 // The listed slots of a sparse query over a ds_mla cache (656-byte entries: 512 e4m3 latent
 // codes, four float32 scales each covering 128 latent columns, 64 bf16 rope values): row t is
 // slot idx_row[t] (block slot / page, row slot % page); negative slots are padding.
@@ -428,19 +406,6 @@ struct PagedSource {
   __device__ PagedRows<K> rows(int b) const {
     return PagedRows<K>{static_cast<const K*>(cv.data), cv, block_table + (int64_t)b * bt_stride,
                         descale_k != nullptr ? *descale_k : 1.f};
-  }
-};
-
-template <typename K>
-struct WindowSource {
-  PagedSource<K> paged;
-  const int32_t* seq_lens;
-  int cap;
-  WindowArgs w;
-  __device__ WindowRows<K> rows(int b) const {
-    WindowRows<K> r{paged.rows(b), 0, 0};
-    window_rows(min(max(seq_lens[b], 0), cap) - 1, w, r.sinks, r.lo);
-    return r;
   }
 };
 
@@ -714,55 +679,6 @@ __global__ void __launch_bounds__(kThreads) prefill_simt_kernel(
   }
 }
 
-// Windowed prefill: one CTA per (query row, head group), no split. Rows of q outside every
-// sequence (and of a sequence whose cu_q entries leave [0, T] or decrease) are left unwritten.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) prefill_window_simt_kernel(
-    T* __restrict__ o_lat, int64_t o_s0, int64_t o_s1, float* __restrict__ lse_out,
-    const T* __restrict__ q, int64_t q_s0, int64_t q_s1, CacheView cv,
-    const int32_t* __restrict__ block_table, int64_t bt_stride, int cap,
-    const int32_t* __restrict__ cu_q, const int32_t* __restrict__ kv_lens, int B, int H, int L,
-    int R, float scale, WindowArgs w) {
-  extern __shared__ __align__(16) unsigned char smem_raw[];
-  pdl_enter();
-  const SimtSmem sm = simt_smem(smem_raw, L + R);
-  const int r = blockIdx.x;
-  const int h0 = blockIdx.y * kHeads, hn = min(kHeads, H - h0);
-  int b = 0, hi = B - 1;   // the last b with cu_q[b] <= r
-  while (b < hi) {
-    const int mid = (b + hi + 1) >> 1;
-    if (cu_q[mid] <= r) b = mid; else hi = mid - 1;
-  }
-  const int q0 = cu_q[b], q1 = cu_q[b + 1];
-  if (r < q0 || r >= q1) return;
-  const int p = clamp_len(kv_lens, b, cap) - (q1 - q0) + (r - q0);
-  WindowRows<T> rows{PagedRows<T>{static_cast<const T*>(cv.data), cv, block_table + (int64_t)b * bt_stride, 1.f}, 0, 0};
-  const int n = window_rows(p, w, rows.sinks, rows.lo);
-  float acc[kHeads][2];
-  attend_rows(sm, q + (int64_t)r * q_s0, q_s1, h0, hn, L + R, L, rows, 0, n, scale, acc);
-  for (int h = 0; h < hn; ++h) {
-    const float l = sm.l[h];
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int col = threadIdx.x + c * kThreads;
-      if (col < L) st(o_lat + (int64_t)r * o_s0 + (int64_t)(h0 + h) * o_s1 + col, acc[h][c] * inv);
-    }
-    if (threadIdx.x == 0 && lse_out)
-      lse_out[(int64_t)r * H + h0 + h] = l > 0.f ? sm.m[h] + logf(l) : -CUDART_INF_F;
-  }
-}
-
-// Rows the newest query of each sequence attends.
-__global__ void __launch_bounds__(256) window_lens_kernel(const int32_t* __restrict__ seq_lens, int B, int cap,
-                                                          WindowArgs w, int32_t* __restrict__ visible) {
-  pdl_enter();
-  const int b = blockIdx.x * blockDim.x + threadIdx.x;
-  if (b >= B) return;
-  int sinks, lo;
-  visible[b] = window_rows(clamp_len(seq_lens, b, cap) - 1, w, sinks, lo);
-}
-
 // A sparse query's index list, compacted: its valid slots (0 <= slot < num_rows) in listed
 // order and their count; a slot past the cache is dropped and reported. One block a query:
 // each thread loads up to kPer consecutive entries at once, and a block-wide exclusive scan of
@@ -936,60 +852,6 @@ cudaError_t launch_prefill_simt(mla_dtype dt, const View3& o_lat, float* lse, co
         q.s1, cache, block_table, bt_stride, max_blocks, cu_q, kv_lens, B, H, L, R, scale);
   }
   return cudaGetLastError();
-}
-
-namespace {
-int table_rows(int32_t max_blocks, int32_t page) {
-  const long long cap = (long long)max_blocks * page;
-  return (int)(cap > INT32_MAX ? INT32_MAX : cap);
-}
-
-template <typename T>
-cudaError_t launch_prefill_window(const View3& o_lat, float* lse, const View3& q, const CacheView& cache,
-                                  const int32_t* block_table, int64_t bt_stride, int cap, const int32_t* cu_q,
-                                  const int32_t* kv_lens, int32_t B, int32_t T_, int32_t H, int32_t L, int32_t R,
-                                  float scale, const WindowArgs& w, cudaStream_t st) {
-  const dim3 grid(T_, (H + kHeads - 1) / kHeads);
-  const size_t sm = simt_smem_bytes(L + R);
-  allow_smem(prefill_window_simt_kernel<T>, sm);
-  return launch_k(prefill_window_simt_kernel<T>, grid, kThreads, sm, st, (T*)o_lat.data, o_lat.s0, o_lat.s1, lse,
-                  (const T*)q.data, q.s0, q.s1, cache, block_table, bt_stride, cap, cu_q, kv_lens, (int)B, (int)H,
-                  (int)L, (int)R, scale, w);
-}
-}  // namespace
-
-cudaError_t launch_window_lens(const int32_t* seq_lens, int32_t B, int32_t max_blocks, int32_t page,
-                               const WindowArgs& w, int32_t* visible, cudaStream_t st) {
-  return launch_k(window_lens_kernel, (B + 255) / 256, 256, 0, st, seq_lens, (int)B, table_rows(max_blocks, page), w,
-                  visible);
-}
-
-cudaError_t launch_decode_window_simt(mla_dtype dt, const View3& o_lat, float* lse, const View3& q,
-                                      const CacheView& cache, const int32_t* block_table, int64_t bt_stride,
-                                      int32_t max_blocks, const int32_t* seq_lens, const int32_t* visible, int32_t B,
-                                      int32_t H, int32_t L, int32_t R, float scale, const WindowArgs& w,
-                                      const DecodeSched& s, cudaStream_t st) {
-  const int cap = table_rows(max_blocks, cache.page);
-  if (dt == MLA_F32)
-    return launch_split_simt<float>(
-        o_lat, lse, q, WindowSource<float>{{cache, block_table, bt_stride, nullptr}, seq_lens, cap, w}, visible, cap, B,
-        H, L, R, scale, s, nullptr, st);
-  return launch_split_simt<__nv_bfloat16>(
-      o_lat, lse, q, WindowSource<__nv_bfloat16>{{cache, block_table, bt_stride, nullptr}, seq_lens, cap, w}, visible,
-      cap, B, H, L, R, scale, s, nullptr, st);
-}
-
-cudaError_t launch_prefill_window_simt(mla_dtype dt, const View3& o_lat, float* lse, const View3& q,
-                                       const CacheView& cache, const int32_t* block_table, int64_t bt_stride,
-                                       int32_t max_blocks, const int32_t* cu_q, const int32_t* kv_lens, int32_t B,
-                                       int32_t T, int32_t H, int32_t L, int32_t R, float scale, const WindowArgs& w,
-                                       cudaStream_t st) {
-  const int cap = table_rows(max_blocks, cache.page);
-  if (dt == MLA_F32)
-    return launch_prefill_window<float>(o_lat, lse, q, cache, block_table, bt_stride, cap, cu_q, kv_lens, B, T, H, L,
-                                        R, scale, w, st);
-  return launch_prefill_window<__nv_bfloat16>(o_lat, lse, q, cache, block_table, bt_stride, cap, cu_q, kv_lens, B, T,
-                                              H, L, R, scale, w, st);
 }
 
 cudaError_t launch_sparse_compact(const int32_t* indices, int64_t idx_stride, int32_t topk, int32_t B,

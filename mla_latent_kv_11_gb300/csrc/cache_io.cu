@@ -128,13 +128,15 @@ __device__ __forceinline__ uint32_t codes2(float a, float b) {
 // its codes are e4m3(x / scale), the division correctly rounded in float32: a value is off by at
 // most half an e4m3 step of its own size, 2^-4 of it, or 2^-10 of the group's scale below the
 // smallest normal code. vec: 16-byte aligned source rows; wide: 32-byte aligned latent rows.
+// Some 260 instructions a row keep the SM busy half of the time, so it wants warps more than rows in
+// flight: one row's values a warp in 48 registers (40 warps an SM) took 17 us for 40961 bf16 rows, two
+// rows' (24 warps) 21.
 template <typename T>
-__global__ void __launch_bounds__(256) write_ds_mla_kernel(
+__global__ void __launch_bounds__(256, 5) write_ds_mla_kernel(
     uint8_t* __restrict__ cache, int64_t c_blk, int64_t c_row, int64_t num_rows, int32_t page,
     const T* __restrict__ kv_c, int64_t k_s0, const T* __restrict__ k_pe, int64_t p_s0,
     const int64_t* __restrict__ slots, int64_t tokens, int per_warp, int vec, int wide) {
   pdl_enter();
-  constexpr int kAhead = 2;   // tokens whose values are in registers
   const int lane = threadIdx.x & 31;
   const int64_t first = ((blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5) * per_warp;
   if (first >= tokens) return;
@@ -151,52 +153,43 @@ __global__ void __launch_bounds__(256) write_ds_mla_kernel(
     }
   }
   __syncwarp();
-  for (int i = 0; i < n; i += kAhead) {
-    float x[kAhead][16];
-    float2 pe[kAhead];
-    int64_t to[kAhead];
+  for (int i = 0; i < n; ++i) {
+    const int64_t to = __shfl_sync(0xffffffffu, off, i);
+    if (to < 0) continue;
+    const int64_t tok = first + i;
+    const T* src = kv_c + tok * k_s0 + lane * 16;
+    const T* rope = k_pe + tok * p_s0 + lane * 2;
+    float x[16];
+    float2 pe;
+    if (vec) {
+      load16(src, x, wide);
+      pe = load2(rope);
+    } else {
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      to[u] = __shfl_sync(0xffffffffu, off, min(i + u, 31));
-      if (i + u >= n) to[u] = -1;
-      if (to[u] < 0) continue;
-      const int64_t tok = first + i + u;
-      const T* src = kv_c + tok * k_s0 + lane * 16;
-      const T* rope = k_pe + tok * p_s0 + lane * 2;
-      if (vec) {
-        load16(src, x[u], wide);
-        pe[u] = load2(rope);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 16; ++k) x[u][k] = to_f(src[k]);
-        pe[u] = make_float2(to_f(rope[0]), to_f(rope[1]));
-      }
+      for (int k = 0; k < 16; ++k) x[k] = to_f(src[k]);
+      pe = make_float2(to_f(rope[0]), to_f(rope[1]));
     }
+    uint8_t* o = cache + to;
+    float top = 0.f;
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      if (to[u] < 0) continue;
-      uint8_t* o = cache + to[u];
-      float top = 0.f;
+    for (int k = 0; k < 16; ++k) top = fmaxf(top, fabsf(x[k]));   // fmaxf passes a NaN over
+    top = fminf(top, FLT_MAX);
 #pragma unroll
-      for (int k = 0; k < 16; ++k) top = fmaxf(top, fabsf(x[u][k]));   // fmaxf passes a NaN over
-      top = fminf(top, FLT_MAX);
+    for (int m = 1; m < 8; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+    const float scale = fmaxf(__fdiv_rn(top, kE4m3Max), FLT_MIN);
+    uint32_t w[4] = {};
+    if (scale >= 0x1p-80f) {
+      const float inv = __frcp_rn(scale);
 #pragma unroll
-      for (int m = 1; m < 8; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-      const float scale = fmaxf(__fdiv_rn(top, kE4m3Max), FLT_MIN);
-      uint32_t w[4] = {};
-      if (scale >= 0x1p-80f) {
-        const float inv = __frcp_rn(scale);
-#pragma unroll
-        for (int k = 0; k < 16; k += 2)
-          w[k >> 2] |= codes2(divide(x[u][k], scale, inv), divide(x[u][k + 1], scale, inv)) << (8 * (k & 2));
-      } else {
-        for (int k = 0; k < 16; k += 2)
-          w[k >> 2] |= codes2(__fdiv_rn(x[u][k], scale), __fdiv_rn(x[u][k + 1], scale)) << (8 * (k & 2));
-      }
-      *reinterpret_cast<uint4*>(o + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-      if ((lane & 7) == 0) *reinterpret_cast<float*>(o + kDsMlaLatent + 4 * (lane >> 3)) = scale;
-      reinterpret_cast<__nv_bfloat162*>(o + kDsMlaRopeByte)[lane] = __floats2bfloat162_rn(pe[u].x, pe[u].y);
+      for (int k = 0; k < 16; k += 2)
+        w[k >> 2] |= codes2(divide(x[k], scale, inv), divide(x[k + 1], scale, inv)) << (8 * (k & 2));
+    } else {
+      for (int k = 0; k < 16; k += 2)
+        w[k >> 2] |= codes2(__fdiv_rn(x[k], scale), __fdiv_rn(x[k + 1], scale)) << (8 * (k & 2));
     }
+    *reinterpret_cast<uint4*>(o + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+    if ((lane & 7) == 0) *reinterpret_cast<float*>(o + kDsMlaLatent + 4 * (lane >> 3)) = scale;
+    reinterpret_cast<__nv_bfloat162*>(o + kDsMlaRopeByte)[lane] = __floats2bfloat162_rn(pe.x, pe.y);
   }
 }
 

@@ -824,26 +824,23 @@ mla_status check_workspace(const void* workspace, size_t have, size_t need) {
   return MLA_OK;
 }
 
-// mla_decode_window's workspace: on the CUDA cores mla_decode's layout, then the visible lengths
-// [B]; on the tensor cores a layout of its own. One size covers both.
-struct WindowWs {
-  DecodeWsLayout lay;
-  size_t off_visible, total;
-};
-WindowWs window_ws(int64_t B, int64_t H, int64_t L, int32_t num_splits) {
-  WindowWs w;
-  w.lay = decode_ws_layout(B, H, L, decode_units(num_splits));
-  auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
-  w.off_visible = up(w.lay.total);
-  w.total = up(w.off_visible + (size_t)B * sizeof(int32_t));
-  if (L == 512) w.total = std::max(w.total, window_tc_workspace(B, B, (int)H, true, num_splits));
-  return w;
+// A windowed call's workspace covers both of its paths.
+size_t window_bytes(int64_t T, int64_t B, int64_t H, int64_t L, bool decode, int32_t num_splits) {
+  const size_t tc = L == 512 ? window_tc_workspace(T, B, (int)H, decode, num_splits) : 0;
+  return std::max(tc, window_simt_workspace(T, B, H, L, decode, num_splits));
+}
+
+mla_status run_window(mla_dtype dtype, const WindowCall& c, int32_t num_splits, void* workspace, cudaStream_t st,
+                      const char* name) {
+  WindowMaps maps;
+  if (window_tc_supported(dtype, c, &maps)) return cuda_status(launch_window_tc(c, maps, num_splits, workspace, st), name);
+  return cuda_status(launch_window_simt(dtype, c, num_splits, workspace, st), name);
 }
 }  // namespace
 
 size_t mla_decode_window_workspace_size(int32_t batch, int32_t num_heads, int32_t kv_lora_rank, int32_t num_splits) {
   if (batch < 0 || num_heads < 0 || kv_lora_rank < 0 || num_splits < 0) return 0;
-  return window_ws(batch, num_heads, kv_lora_rank, num_splits).total;
+  return window_bytes(batch, batch, num_heads, kv_lora_rank, true, num_splits);
 }
 
 mla_status mla_decode_window(mla_dtype dtype, mla_tensor o_lat_out, float* lse_out, mla_tensor q_cat,
@@ -857,31 +854,15 @@ mla_status mla_decode_window(mla_dtype dtype, mla_tensor o_lat_out, float* lse_o
   MLA_TRY(check_decode_args(dtype, o_lat_out, q_cat, cache, block_table, block_table_stride, max_blocks,
                             seq_lens, kv_lora_rank, rope_dim, softmax_scale, num_splits, &dc));
   if (dc.empty) return MLA_OK;
-  const WindowWs ws = window_ws(dc.B, dc.H, dc.L, num_splits);
-  MLA_TRY(check_workspace(workspace, workspace_bytes, ws.total));
-  const cudaStream_t st = (cudaStream_t)stream;
-  const int32_t B = (int32_t)dc.B, H = (int32_t)dc.H, L = (int32_t)dc.L, R = (int32_t)dc.R;
-  const WindowArgs w{window, sinks};
-  const WindowCall wc{dc.ov, dc.qv, lse_out, dc.cv, block_table, block_table_stride, max_blocks, nullptr, seq_lens,
-                      B, H, L, R, softmax_scale, w};
-  WindowMaps maps;
-  if (window_tc_supported(dtype, wc, &maps))
-    return cuda_status(launch_window_tc(wc, maps, num_splits, workspace, st), "mla_decode_window (tensor cores)");
-  // each sequence's visible rows, then the split-KV decode over that many
-  int32_t* visible = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + ws.off_visible);
-  const DecodeSched s = decode_sched_from_ws(workspace, ws.lay, B, decode_units(num_splits));
-  MLA_TRY(cuda_status(launch_window_lens(seq_lens, B, max_blocks, dc.cv.page, w, visible, st),
-                      "mla_decode_window lengths"));
-  MLA_TRY(cuda_status(launch_decode_schedule(visible, B, max_blocks, dc.cv.page, s, st), "mla_decode_window schedule"));
-  MLA_TRY(cuda_status(launch_decode_window_simt(dtype, dc.ov, lse_out, dc.qv, dc.cv, block_table, block_table_stride,
-                                                max_blocks, seq_lens, visible, B, H, L, R, softmax_scale, w, s, st),
-                      "mla_decode_window split kernel"));
-  return cuda_status(launch_decode_combine(dtype, dc.ov, lse_out, visible, B, H, L, s, st), "mla_decode_window combine");
+  MLA_TRY(check_workspace(workspace, workspace_bytes, window_bytes(dc.B, dc.B, dc.H, dc.L, true, num_splits)));
+  const WindowCall c{dc.ov, dc.qv, lse_out, dc.cv, block_table, block_table_stride, max_blocks, nullptr, seq_lens,
+                     (int32_t)dc.B, (int32_t)dc.H, (int32_t)dc.L, (int32_t)dc.R, softmax_scale, {window, sinks}};
+  return run_window(dtype, c, num_splits, workspace, (cudaStream_t)stream, "mla_decode_window");
 }
 
 size_t mla_prefill_window_workspace_size(int32_t tokens, int32_t batch, int32_t num_heads, int32_t kv_lora_rank) {
   if (tokens < 0 || batch < 0 || num_heads < 0 || kv_lora_rank < 0) return 0;
-  return std::max<size_t>(256, kv_lora_rank == 512 ? window_tc_workspace(tokens, batch, num_heads, false, 0) : 0);
+  return window_bytes(tokens, batch, num_heads, kv_lora_rank, false, 0);
 }
 
 mla_status mla_prefill_window(mla_dtype dtype, mla_tensor o_lat_out, float* lse_out, mla_tensor q_cat,
@@ -898,18 +879,10 @@ mla_status mla_prefill_window(mla_dtype dtype, mla_tensor o_lat_out, float* lse_
                             seq_lens_kv, kv_lora_rank, rope_dim, softmax_scale, 0, &dc));
   if (dc.empty || batch == 0) return MLA_OK;
   if (cu_seqlens_q == nullptr) return fail(MLA_ERR_INVALID_ARG, "cu_seqlens_q must be non-null");
-  const int32_t T = (int32_t)dc.B, H = (int32_t)dc.H, L = (int32_t)dc.L, R = (int32_t)dc.R;
-  MLA_TRY(check_workspace(workspace, workspace_bytes, mla_prefill_window_workspace_size(T, batch, H, L)));
-  const WindowCall wc{dc.ov, dc.qv, lse_out, dc.cv, block_table, block_table_stride, max_blocks, cu_seqlens_q,
-                      seq_lens_kv, batch, H, L, R, softmax_scale, WindowArgs{window, sinks}};
-  WindowMaps maps;
-  if (window_tc_supported(dtype, wc, &maps))
-    return cuda_status(launch_window_tc(wc, maps, 0, workspace, (cudaStream_t)stream),
-                       "mla_prefill_window (tensor cores)");
-  return cuda_status(launch_prefill_window_simt(dtype, dc.ov, lse_out, dc.qv, dc.cv, block_table, block_table_stride,
-                                                max_blocks, cu_seqlens_q, seq_lens_kv, batch, T, H, L, R,
-                                                softmax_scale, WindowArgs{window, sinks}, (cudaStream_t)stream),
-                     "mla_prefill_window");
+  MLA_TRY(check_workspace(workspace, workspace_bytes, window_bytes(dc.B, batch, dc.H, dc.L, false, 0)));
+  const WindowCall c{dc.ov, dc.qv, lse_out, dc.cv, block_table, block_table_stride, max_blocks, cu_seqlens_q,
+                     seq_lens_kv, batch, (int32_t)dc.H, (int32_t)dc.L, (int32_t)dc.R, softmax_scale, {window, sinks}};
+  return run_window(dtype, c, 0, workspace, (cudaStream_t)stream, "mla_prefill_window");
 }
 
 mla_status mla_check_bounded_wait(uint32_t limit_us, void* stream) {
@@ -924,7 +897,7 @@ mla_status mla_device_error(void* stream) {
   cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_status(e, "mla_device_error: stream synchronize");
   unsigned bits = copy_errors_read_clear() | cache_io_errors_read_clear() | attn_pair_errors_read_clear() |
-                  attn_simt_errors_read_clear() | attn_tc_errors_read_clear() |
+                  window_sched_errors_read_clear() | window_simt_errors_read_clear() | attn_simt_errors_read_clear() | attn_tc_errors_read_clear() |
                   bmm_tc_errors_read_clear() | combine_vup_errors_read_clear();
   if (bits & kErrTimeout) return fail(MLA_ERR_TIMEOUT, "a bounded device-side wait gave up");
   if (bits & kErrDeviceData)

@@ -201,8 +201,8 @@ cudaError_t launch_cache_read(mla_dtype dt, const CacheRead& r, cudaStream_t st)
 cudaError_t launch_cache_read_fp8(mla_dtype dst_dt, const CacheRead& r, const float* scale, cudaStream_t st);
 cudaError_t launch_cache_read_ds_mla(mla_dtype dst_dt, const CacheRead& r, cudaStream_t st);
 
-// Attention limited to a window and sinks on the CUDA cores (attn_simt.cu). A query at position p
-// of a sequence attends rows t <= p with t < sinks or t > p - window.
+// Attention limited to a window and sinks. A query at position p of a sequence attends rows t <= p with
+// t < sinks or t > p - window.
 struct WindowArgs {
   int32_t window, sinks;
 };
@@ -220,10 +220,31 @@ struct WindowCall {
   float scale;
   WindowArgs window;
 };
+// The schedule in the workspace (window_sched.cu): the row tiles' descriptions, how many there are and,
+// where row tiles are cut, {row tile, tile} of each unit's first (null: whole row tiles dealt out).
+struct WindowSched {
+  int4* items;
+  int32_t* total;
+  int2* unit_start;
+};
+// Where results go: rows of the output, and the partial slots [2 * units][rows][L] of cut row tiles
+// with their log-sum-exps [2 * units][rows]. tptc 0: a slot's row is a head; else rows 64 r .. of a slot
+// are tptc tokens' heads each.
+struct WindowOut {
+  void* o;
+  int64_t o_s0, o_s1;
+  float *lse, *part_o, *part_lse;
+  int32_t rows, L, H, tptc;
+};
+// Row tiles of tpt tokens over `units` work units, tiles of blocks_per_tile 64-row blocks, slots of
+// `rows` rows.
+size_t window_workspace(int64_t T, int64_t B, bool decode, int tpt, int64_t units, int64_t rows, int64_t L);
+cudaError_t launch_window_schedule(const WindowCall& c, int tpt, int blocks_per_tile, int units, int rows, void* ws,
+                                   WindowSched* sched, WindowOut* out, cudaStream_t st);
+cudaError_t launch_window_merge(mla_dtype dt, const WindowSched& sched, const WindowOut& out, int units, cudaStream_t st);
 // On the tensor cores (attn_pair_tc.cu): bf16, L = 512, R in {0, 64}, up to 128 heads, a positive
 // scale, pages of whole 64-row blocks or blocks of whole pages of 8 rows or more, 16-byte aligned
-// views.
-// Fills the call's tensor maps where it is so.
+// views. Fills the call's tensor maps where it is so.
 struct WindowMaps {
   CUtensorMap keys, boxes, q;
 };
@@ -231,19 +252,9 @@ bool window_tc_supported(mla_dtype dt, const WindowCall& c, WindowMaps* maps);
 // Bytes of workspace for T query tokens of B sequences (0: H is not taken).
 size_t window_tc_workspace(int64_t T, int64_t B, int H, bool decode, int num_splits);
 cudaError_t launch_window_tc(const WindowCall& c, const WindowMaps& maps, int num_splits, void* ws, cudaStream_t st);
-// visible[b] = rows the query at seq_lens[b] - 1 attends: the lengths of the split-KV schedule.
-cudaError_t launch_window_lens(const int32_t* seq_lens, int32_t B, int32_t max_blocks, int32_t page,
-                               const WindowArgs& w, int32_t* visible, cudaStream_t st);
-cudaError_t launch_decode_window_simt(mla_dtype dt, const View3& o_lat, float* lse, const View3& q,
-                                      const CacheView& cache, const int32_t* block_table, int64_t bt_stride,
-                                      int32_t max_blocks, const int32_t* seq_lens, const int32_t* visible, int32_t B,
-                                      int32_t H, int32_t L, int32_t R, float scale, const WindowArgs& w,
-                                      const DecodeSched& s, cudaStream_t st);
-cudaError_t launch_prefill_window_simt(mla_dtype dt, const View3& o_lat, float* lse, const View3& q,
-                                       const CacheView& cache, const int32_t* block_table, int64_t bt_stride,
-                                       int32_t max_blocks, const int32_t* cu_q, const int32_t* kv_lens, int32_t B,
-                                       int32_t T, int32_t H, int32_t L, int32_t R, float scale, const WindowArgs& w,
-                                       cudaStream_t st);
+// On the CUDA cores (window_simt.cu): everything else.
+size_t window_simt_workspace(int64_t T, int64_t B, int64_t H, int64_t L, bool decode, int num_splits);
+cudaError_t launch_window_simt(mla_dtype dt, const WindowCall& c, int num_splits, void* ws, cudaStream_t st);
 
 cudaError_t launch_decode_combine(mla_dtype dt, const View3& o_lat, float* lse,
                                   const int32_t* seq_lens, int32_t B, int32_t H, int32_t L,
@@ -326,6 +337,8 @@ mla_status report_status(mla_status st, const char* fmt, ...);
 unsigned copy_errors_read_clear();
 unsigned cache_io_errors_read_clear();
 unsigned attn_pair_errors_read_clear();
+unsigned window_sched_errors_read_clear();
+unsigned window_simt_errors_read_clear();
 unsigned attn_simt_errors_read_clear();
 unsigned attn_tc_errors_read_clear();
 unsigned combine_vup_errors_read_clear();
