@@ -695,7 +695,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (left > 0) store_quarter();
       }
       if (!ok) break;
-      // ---- O / l
+      // ---- O / l. What is left of the output before goes out while the last PV runs
+      while (left > 0) store_quarter();
       const int last = g - 1;
       mine = mine && wait_for(&sh.pv_done[last & 1][3], (last >> 1) & 1, abort);
       // in the place of the last tile's maxima: PV has its P, so every warp has read them; they are
@@ -712,7 +713,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // A row tile's 64 KB of output leave an SM at 16 bytes a cycle, longer than a tile of keys takes.
         // So O only becomes bf16 here, within tensor memory, and a quarter of it is stored behind each
         // of the next tiles
-        while (left > 0) store_quarter();
         float v[32];
         tmem_ld32(tmem + lane_addr + 128 * part, v);
 #pragma unroll 1

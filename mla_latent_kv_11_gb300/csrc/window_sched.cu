@@ -1,11 +1,16 @@
 // The schedule of the windowed attention kernels, and the merge of row tiles cut across work units.
 //
-// A prefill's tokens form row tiles of `tpt` tokens, a decode's sequences one each. Up to kSplitItems
-// row tiles are cut: each work unit gets a contiguous range of tiles of equal cost (a row tile costing
-// its tiles plus kItemCost), so that few queries over a long axis keep every SM busy; a unit then
-// holds at most two cut row tiles, the end of one and the head of another, and two partial slots. More
-// row tiles balance by themselves and are dealt out whole. The schedule depends on the lengths
-// and the number of units alone: results repeat bit for bit.
+// A prefill's tokens form row tiles of `tpt` tokens, a decode's sequences one each. Few queries over a
+// long axis keep every SM busy by being cut:
+//   - no more row tiles than work units: each gets units of its own, as many as make the longest piece
+//     shortest, but one where cutting gains less than the float32 partials and their merge cost
+//     (cut_cost; 64 sequences of 33 tensor-core tiles on 76 units: 82 us cut, 71 whole);
+//   - up to kSplitItems row tiles: each unit gets a contiguous range of tiles of equal cost (a row
+//     tile costing its tiles plus kItemCost) and holds at most two cut row tiles, the end of one and the
+//     head of another;
+//   - more row tiles balance by themselves and are dealt out whole.
+// A unit has two partial slots. The schedule depends on the lengths and the number of units alone:
+// results repeat bit for bit.
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
@@ -81,7 +86,7 @@ __device__ int scan_block(int v, int* warp_tot, int* total) {
 template <int kPer>
 __global__ void __launch_bounds__(1024) window_split_kernel(SchedArgs s) {
   __shared__ int warp_tot[32], first[kSplitItems + 1], q_begin[kSplitItems], q_count[kSplitItems], len[kSplitItems],
-      cost[kSplitItems + 1], tiles[kSplitItems];
+      cost[kSplitItems + 1], tiles[kSplitItems], longest[32];
   pdl_enter();
   const int i = threadIdx.x;
   int n = 0, q0 = 0, total;
@@ -114,7 +119,30 @@ __global__ void __launch_bounds__(1024) window_split_kernel(SchedArgs s) {
     tiles[i] = nt;
   }
   if (i == 0) *s.total = total;
+  if (i < 32) longest[i] = 0;
   __syncthreads();
+  const int top = __reduce_max_sync(0xffffffffu, nt);
+  if ((i & 31) == 0) longest[i >> 5] = top;
+  __syncthreads();
+  if (total <= s.units) {
+    // what cutting adds to a unit's time, in tiles: a tensor-core tile takes 1.7 us, one on the CUDA
+    // cores ten times that
+    constexpr int cut_cost = kPer == 2 ? 5 : 0;
+    // pieces of at most `most` tiles: the least `most` whose pieces the units can take
+    int lo = 1, hi = 1, pieces;   // hi: the longest row tile
+    for (int w = 0; w < 32; ++w) hi = max(hi, longest[w]);
+    const int whole = hi;
+    while (lo < hi) {
+      const int most = (lo + hi) >> 1;
+      scan_block(i < total ? (nt + most - 1) / most : 0, warp_tot, &pieces);
+      if (pieces <= s.units) hi = most; else lo = most + 1;
+    }
+    const int k = i < total ? (lo + cut_cost < whole ? (nt + lo - 1) / lo : 1) : 0;
+    const int first_unit = scan_block(k, warp_tot, &pieces);
+    for (int j = 0; j < k; ++j) s.unit_start[first_unit + j] = make_int2(i, (int)((long long)nt * j / k));
+    for (int u = pieces + i; u <= s.units; u += blockDim.x) s.unit_start[u] = make_int2(total, 0);
+    return;
+  }
   // unit u starts at cost u * all / active: units beyond the tiles there are get nothing
   const int active = max(1, min(s.units, all - kItemCost * total));
   for (int u = i; u <= s.units; u += blockDim.x) {
@@ -189,7 +217,8 @@ __device__ __forceinline__ void store1(__nv_bfloat16* o, float v) { *o = __float
 constexpr int kMergeWarps = 8;
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(32 * kMergeWarps) window_merge_kernel(WindowSched s, WindowOut out, int units) {
-  pdl_enter();
+  // the schedule's words come from two launches back, complete before this kernel can start (the
+  // attention kernel between waits for them before it lets dependents launch): read before the wait
   const int u = blockIdx.x + 1, lane = threadIdx.x & 31;
   const int2 at = s.unit_start[u], before = s.unit_start[u - 1];
   if (at.x >= *s.total || at.y == 0 || (before.x == at.x && before.y > 0)) return;
@@ -212,6 +241,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) window_merge_kernel(WindowSc
     if (k < 32) break;
   }
   auto slot = [&](int i) { return (int64_t)(i == 0 ? 2 * u - 1 : 2 * (u + i - 1)); };
+  pdl_enter();
   float m = -CUDART_INF_F;
   for (int i = lane; i < n; i += 32) m = fmaxf(m, out.part_lse[slot(i) * out.rows + row]);
 #pragma unroll
