@@ -221,11 +221,13 @@ struct WindowCall {
   WindowArgs window;
 };
 // The schedule in the workspace (window_sched.cu): the row tiles' descriptions, how many there are and,
-// where row tiles are cut, {row tile, tile} of each unit's first (null: whole row tiles dealt out).
+// where row tiles may be cut, {row tile, tile} of each unit's first (null: whole row tiles dealt out);
+// cut: some may be, so their pieces have to be merged.
 struct WindowSched {
   int4* items;
   int32_t* total;
   int2* unit_start;
+  bool cut;
 };
 // Where results go: rows of the output, and the partial slots [2 * units][rows][L] of cut row tiles
 // with their log-sum-exps [2 * units][rows]. tptc 0: a slot's row is a head; else rows 64 r .. of a slot

@@ -4,7 +4,7 @@
 // long axis keep every SM busy by being cut:
 //   - no more row tiles than work units: each gets units of its own, as many as make the longest piece
 //     shortest, but one where cutting gains less than the float32 partials and their merge cost
-//     (cut_cost; 64 sequences of 33 tensor-core tiles on 76 units: 82 us cut, 71 whole);
+//     (kCutCost; 64 sequences of 33 tensor-core tiles on 76 units: 82 us cut, 71 whole);
 //   - up to kSplitItems row tiles: each unit gets a contiguous range of tiles of equal cost (a row
 //     tile costing its tiles plus kItemCost) and holds at most two cut row tiles, the end of one and the
 //     head of another;
@@ -23,7 +23,13 @@ namespace {
 
 __device__ unsigned g_window_err = 0;
 
-constexpr int kItemCost = 1;        // cost of starting a row tile, in tiles
+// In tiles, of kPer blocks each (measured: a tensor-core tile takes 1.7 us, one on the CUDA cores ten
+// times that): what a row tile costs beside its tiles (with 1 instead of 2, 880 row tiles of 3 tensor-core
+// tiles took 126 us instead of 113), and what cutting adds to a unit's time.
+template <int kPer>
+constexpr int kItemCost = kPer == 2 ? 2 : 1;
+template <int kPer>
+constexpr int kCutCost = kPer == 2 ? 5 : 0;
 constexpr int kSplitItems = 1024;   // row tiles up to which the schedule cuts them
 
 struct SchedArgs {
@@ -113,7 +119,7 @@ __global__ void __launch_bounds__(1024) window_split_kernel(SchedArgs s) {
     nt = item_tiles<kPer>(it.b.w);
   }
   int all;
-  const int at = scan_block(i < total ? nt + kItemCost : 0, warp_tot, &all);
+  const int at = scan_block(i < total ? nt + kItemCost<kPer> : 0, warp_tot, &all);
   if (i < total) {
     cost[i] = at;
     tiles[i] = nt;
@@ -125,9 +131,6 @@ __global__ void __launch_bounds__(1024) window_split_kernel(SchedArgs s) {
   if ((i & 31) == 0) longest[i >> 5] = top;
   __syncthreads();
   if (total <= s.units) {
-    // what cutting adds to a unit's time, in tiles: a tensor-core tile takes 1.7 us, one on the CUDA
-    // cores ten times that
-    constexpr int cut_cost = kPer == 2 ? 5 : 0;
     // pieces of at most `most` tiles: the least `most` whose pieces the units can take
     int lo = 1, hi = 1, pieces;   // hi: the longest row tile
     for (int w = 0; w < 32; ++w) hi = max(hi, longest[w]);
@@ -137,14 +140,14 @@ __global__ void __launch_bounds__(1024) window_split_kernel(SchedArgs s) {
       scan_block(i < total ? (nt + most - 1) / most : 0, warp_tot, &pieces);
       if (pieces <= s.units) hi = most; else lo = most + 1;
     }
-    const int k = i < total ? (lo + cut_cost < whole ? (nt + lo - 1) / lo : 1) : 0;
+    const int k = i < total ? (lo + kCutCost<kPer> < whole ? (nt + lo - 1) / lo : 1) : 0;
     const int first_unit = scan_block(k, warp_tot, &pieces);
     for (int j = 0; j < k; ++j) s.unit_start[first_unit + j] = make_int2(i, (int)((long long)nt * j / k));
     for (int u = pieces + i; u <= s.units; u += blockDim.x) s.unit_start[u] = make_int2(total, 0);
     return;
   }
   // unit u starts at cost u * all / active: units beyond the tiles there are get nothing
-  const int active = max(1, min(s.units, all - kItemCost * total));
+  const int active = max(1, min(s.units, all - kItemCost<kPer> * total));
   for (int u = i; u <= s.units; u += blockDim.x) {
     int2 start = make_int2(total, 0);
     if (u < active && total > 0) {
@@ -154,7 +157,7 @@ __global__ void __launch_bounds__(1024) window_split_kernel(SchedArgs s) {
         const int mid = (lo + hi + 1) >> 1;
         if (cost[mid] <= x) lo = mid; else hi = mid - 1;
       }
-      const int into = max(0, x - cost[lo] - kItemCost);
+      const int into = max(0, x - cost[lo] - kItemCost<kPer>);
       start = into >= tiles[lo] ? make_int2(lo + 1, 0) : make_int2(lo, into);
     }
     s.unit_start[u] = start;
@@ -262,7 +265,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) window_merge_kernel(WindowSc
         w[i] = __shfl_sync(0xffffffffu, mine, (i0 + i) & 31);
         if (i0 + i >= k) w[i] = 0.f;
         const float* src = out.part_o + (slot(base + min(i0 + i, k - 1)) * out.rows + row) * out.L;
-        if (kVec) {
+        if constexpr (kVec) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const int col = 128 * c + 4 * lane;
@@ -279,7 +282,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) window_merge_kernel(WindowSc
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         tot += w[i];
-        if (!kVec) continue;
+        if constexpr (kVec)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           acc[c].x = fmaf(w[i], v[i][c].x, acc[c].x);
@@ -292,7 +295,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) window_merge_kernel(WindowSc
   }
   const float inv = tot > 0.f ? 1.f / tot : 0.f;
   T* o = static_cast<T*>(out.o) + (int64_t)(d.x + t) * out.o_s0 + (int64_t)h * out.o_s1;
-  if (kVec) {
+  if constexpr (kVec) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const int col = 128 * c + 4 * lane;
@@ -353,7 +356,12 @@ cudaError_t launch_window_schedule(const WindowCall& c, int tpt, int blocks_per_
   // cut row tiles while their tiles can be counted in 32 bits
   const int64_t seen = std::min<int64_t>(cap, (int64_t)s.window + s.sinks) / kBlk + 4;
   const bool split = items <= kSplitItems && c.B <= kSplitItems && items * seen < (int64_t)1 << 30;
-  *sched = WindowSched{s.items, s.total, split ? s.unit_start : nullptr};
+  // tiles of a row tile at most; whether any can be cut
+  const int64_t tiles = (std::min<int64_t>(cap, (int64_t)s.window + tpt) / kBlk + 2 +
+                         std::min<int64_t>(cap, s.sinks) / kBlk + 1 + blocks_per_tile - 1) / blocks_per_tile;
+  const int cut_cost = blocks_per_tile == 2 ? kCutCost<2> : kCutCost<1>;
+  *sched = WindowSched{s.items, s.total, split ? s.unit_start : nullptr,
+                       split && units > 1 && tiles > 1 && (items > units || tiles > 1 + cut_cost)};
   *out = WindowOut{c.o.data, c.o.s0, c.o.s1, c.lse, reinterpret_cast<float*>(base + w.o),
                    reinterpret_cast<float*>(base + w.lse), rows, c.L, c.H, 0};
   if (split) {
@@ -367,7 +375,7 @@ cudaError_t launch_window_schedule(const WindowCall& c, int tpt, int blocks_per_
 }
 
 cudaError_t launch_window_merge(mla_dtype dt, const WindowSched& sched, const WindowOut& out, int units, cudaStream_t st) {
-  if (sched.unit_start == nullptr || units < 2) return cudaSuccess;
+  if (!sched.cut) return cudaSuccess;
   const dim3 grid(units - 1, (out.rows + kMergeWarps - 1) / kMergeWarps);
   const size_t es = dt == MLA_F32 ? 4 : 2;
   const bool vec = out.L % 4 == 0 && out.o_s0 % 4 == 0 && out.o_s1 % 4 == 0 &&
