@@ -313,8 +313,8 @@ size_t mla_decode_v_up_workspace_size(int32_t batch, int32_t num_heads, int32_t 
  *   any row stride; slot_mapping: device int64 [num_tokens].
  *   For token i with s = slot_mapping[i] >= 0, entry s becomes
  *     scale g    = max(max |kv_c[i, 128g .. 128g+127]| / 448, 2^-126)   (float32)
- *     code c     = e4m3(kv_c[i,c] / scale[c / 128])   (the division correctly rounded in
- *                  float32, the code to nearest with ties to even, saturating)
+ *     code c     = e4m3(kv_c[i,c] / scale[c / 128])   (the quotient rounded once, to the
+ *                  nearest code, ties to even, saturating)
  *     rope       = k_pe[i] (bf16, rounded to nearest even from float32).
  *   An infinity counts as the largest float32 in the maximum and becomes a code of +-448;
  *   a NaN does not count and becomes the NaN code. Padding slots, out-of-range slots, the

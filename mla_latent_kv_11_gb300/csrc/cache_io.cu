@@ -103,17 +103,35 @@ __device__ __forceinline__ float e4m3(uint8_t c) {
   return static_cast<float>(v);
 }
 
-// x / s correctly rounded, r being 1 / s correctly rounded: Markstein's method (IBM J. Res. Dev. 34,
-// 1990). x * r is within two units in the last place; the remainder of a quotient q that near is
-// exact in one fused multiply-add, a first step makes q a neighbour of the quotient, and from a
-// neighbour the second gives it correctly rounded. No remainder may underflow: s is at least 2^-80
-// here (smaller scales divide). Infinities and NaNs come out as x * r would (the remainder of an
-// infinity is a NaN).
-__device__ __forceinline__ float divide(float x, float s, float r) {
-  const float q = x * r;
-  const float a = fmaf(fmaf(-q, s, x), r, q);
-  const float b = fmaf(fmaf(-a, s, x), r, a);
-  return fabsf(q) <= FLT_MAX ? b : q;
+// x / s as a float32 that rounds to the same code as the quotient itself: rounded toward zero, with
+// the last bit set where that lost something. (Rounded to nearest it could land on the middle of two
+// codes, which a quotient beside it then rounds as: with bf16 values that is not rare, a 448 / top
+// times a short value being off a middle only by the rounding of the scale.) r is 1 / s correctly
+// rounded, and the steps Markstein's (IBM J. Res. Dev. 34, 1990): x * r is within two units in the
+// last place; the remainder of a quotient that near is exact in one fused multiply-add, a step with
+// it makes a neighbour of the quotient, and the neighbour's remainder says on which side that lies.
+// No remainder of a quotient near a middle (2^-10 and up) may underflow: s is at least 2^-80 here, x
+// finite or NaN. (An exact remainder needs no more: a code's middle has 5 bits, so a quotient that is
+// none is 2^-29 of itself away from it at least.)
+// Two quotients at a time, in paired instructions: ns and r hold -s and 1 / s twice.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  return (uint64_t)__float_as_uint(b) << 32 | __float_as_uint(a);
+}
+__device__ __forceinline__ float odd(uint32_t bits, uint32_t rem) {
+  asm("{\n\t.reg .pred p;\n\tsetp.neu.f32 p, %1, 0f00000000;\n\t@p or.b32 %0, %0, 1;\n\t}"
+      : "+r"(bits) : "f"(__uint_as_float(rem)));
+  return __uint_as_float(bits);
+}
+__device__ __forceinline__ void divide2(float x0, float x1, uint64_t ns, uint64_t r, float& y0, float& y1) {
+  const uint64_t x = pair(x0, x1);
+  uint64_t q, a, rem, t;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q) : "l"(x), "l"(r));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(a) : "l"(q), "l"(ns), "l"(x));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(a) : "l"(a), "l"(r), "l"(q));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(rem) : "l"(a), "l"(ns), "l"(x));
+  asm("fma.rz.f32x2 %0, %1, %2, %3;" : "=l"(t) : "l"(rem), "l"(r), "l"(a));
+  y0 = odd((uint32_t)t, (uint32_t)rem);
+  y1 = odd((uint32_t)(t >> 32), (uint32_t)(rem >> 32));
 }
 
 // The codes of two quotients: to nearest even, saturating.
@@ -125,12 +143,11 @@ __device__ __forceinline__ uint32_t codes2(float a, float b) {
 // cache[s/page, s%page] = the ds_mla entry of [kv_c[i] | k_pe[i]] for every token i with slot
 // s >= 0. A group's scale is its largest magnitude / 448 (an infinity counts as the largest
 // float32, a NaN not at all), at least 2^-126 so that the division stays among normal numbers;
-// its codes are e4m3(x / scale), the division correctly rounded in float32: a value is off by at
-// most half an e4m3 step of its own size, 2^-4 of it, or 2^-10 of the group's scale below the
+// its codes are e4m3(x / scale), rounded once: a value is off by at most half an e4m3 step of its own size, 2^-4 of it, or 2^-10 of the group's scale below the
 // smallest normal code. vec: 16-byte aligned source rows; wide: 32-byte aligned latent rows.
-// Some 260 instructions a row keep the SM busy half of the time, so it wants warps more than rows in
-// flight: one row's values a warp in 48 registers (40 warps an SM) took 17 us for 40961 bf16 rows, two
-// rows' (24 warps) 21.
+// Bounded by its instructions as much as by memory: it wants warps more than rows in flight. 40961
+// bf16 rows took 17 us with one row's values a warp (48 registers, 40 warps an SM), 21 with two rows'
+// (24 warps); 16.3 with the divisions paired, 4.6 TB/s (float32 rows 20.6 us, 5.9 TB/s).
 template <typename T>
 __global__ void __launch_bounds__(256, 5) write_ds_mla_kernel(
     uint8_t* __restrict__ cache, int64_t c_blk, int64_t c_row, int64_t num_rows, int32_t page,
@@ -173,19 +190,29 @@ __global__ void __launch_bounds__(256, 5) write_ds_mla_kernel(
     float top = 0.f;
 #pragma unroll
     for (int k = 0; k < 16; ++k) top = fmaxf(top, fabsf(x[k]));   // fmaxf passes a NaN over
+    const bool finite = top <= FLT_MAX;
     top = fminf(top, FLT_MAX);
 #pragma unroll
     for (int m = 1; m < 8; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
     const float scale = fmaxf(__fdiv_rn(top, kE4m3Max), FLT_MIN);
-    uint32_t w[4] = {};
-    if (scale >= 0x1p-80f) {
-      const float inv = __frcp_rn(scale);
+    float by = scale;
+    if (by < 0x1p-80f) {           // the same quotients, out of the way of underflow
+      by *= 0x1p64f;
 #pragma unroll
-      for (int k = 0; k < 16; k += 2)
-        w[k >> 2] |= codes2(divide(x[k], scale, inv), divide(x[k + 1], scale, inv)) << (8 * (k & 2));
-    } else {
-      for (int k = 0; k < 16; k += 2)
-        w[k >> 2] |= codes2(__fdiv_rn(x[k], scale), __fdiv_rn(x[k + 1], scale)) << (8 * (k & 2));
+      for (int k = 0; k < 16; ++k) x[k] *= 0x1p64f;
+    }
+    if (!finite) {                 // the scale is FLT_MAX / 448 then: a code of +-448
+#pragma unroll
+      for (int k = 0; k < 16; ++k) x[k] = fabsf(x[k]) > FLT_MAX ? copysignf(FLT_MAX, x[k]) : x[k];
+    }
+    uint32_t w[4] = {};
+    const float inv = __frcp_rn(by);
+    const uint64_t r = pair(inv, inv), ns = pair(-by, -by);
+#pragma unroll
+    for (int k = 0; k < 16; k += 2) {
+      float a, b;
+      divide2(x[k], x[k + 1], ns, r, a, b);
+      w[k >> 2] |= codes2(a, b) << (8 * (k & 2));
     }
     *reinterpret_cast<uint4*>(o + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
     if ((lane & 7) == 0) *reinterpret_cast<float*>(o + kDsMlaLatent + 4 * (lane >> 3)) = scale;

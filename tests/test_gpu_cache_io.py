@@ -11,12 +11,14 @@ E4M3 = torch.float8_e4m3fn
 
 
 def entry_of(kv_c, k_pe):
-    """The 656 bytes of each row, from the definition, on the CPU in float32."""
+    """The 656 bytes of each row, from the definition, on the CPU: the quotient in 64 bits, rounded once."""
     x = kv_c.float().cpu().view(-1, 4, 128)
     top = torch.where(x.isnan(), torch.zeros_like(x), x).abs().amax(-1).clamp_max(torch.finfo(torch.float32).max)
     scale = (top / 448).clamp_min(2.0 ** -126)
-    y = x / scale[..., None]
-    codes = torch.where(y.isnan(), y, y.clamp(-448, 448)).to(E4M3).view(-1, 512)
+    y = (x.double() / scale.double()[..., None]).clamp(-448, 448)                # clamp keeps a NaN
+    # e4m3: steps of 2^(exponent - 3), no exponent below -6; torch.round takes halves to even
+    step = torch.exp2(y.abs().clamp_min(2.0 ** -20).log2().floor().clamp_min(-6) - 3)
+    codes = (torch.round(y / step) * step).float().to(E4M3).view(-1, 512)
     pe = k_pe.cpu().to(torch.bfloat16)
     return torch.cat([codes.view(torch.uint8), scale.view(torch.uint8), pe.contiguous().view(torch.uint8)], 1)
 
@@ -54,6 +56,26 @@ def test_write_ds_mla(mla, dtype, tokens, page, layers):
     want[rows[keep].cuda() // page, layers - 1, rows[keep].cuda() % page] = entry_of(kv_c, k_pe)[keep].cuda()
     # a NaN of the rope may change its payload; every other byte is the definition's
     assert torch.equal(whole, want)
+
+
+def test_write_ds_mla_rounds_a_quotient_once(mla):
+    # short values and short maxima: many quotients near the middle of two codes, some of them where
+    # float32's nearest to the quotient is the middle itself (the last lines before the call show it)
+    m = torch.arange(128, 256)
+    x = torch.zeros(128, 4, 128)
+    for g in range(4):
+        x[:, g] = (torch.arange(128) + 128 * (g & 1)) * 2.0 ** -(g + 1)
+        x[:, g, 0] = m * 2.0 ** -(g // 2)
+    kv_c = x.view(128, 512).to(torch.bfloat16)
+    assert torch.equal(kv_c.float(), x.view(128, 512))
+    k_pe = torch.zeros(128, 64, dtype=torch.bfloat16)
+    want = entry_of(kv_c, k_pe)
+    top = x.abs().amax(-1, keepdim=True) / 448
+    assert not torch.equal((x / top).to(E4M3).view(128, 512).view(torch.uint8), want[:, :512])
+    cache = torch.zeros(2, 64, 656, dtype=torch.uint8, device="cuda")
+    mla.mla_cache_write_ds_mla(cache, kv_c.cuda(), k_pe.cuda(), torch.arange(128, device="cuda"))
+    mla.mla_device_error()
+    assert torch.equal(cache.view(128, 656).cpu(), want)
 
 
 def test_write_ds_mla_strided_rows_and_views(mla):
