@@ -363,7 +363,7 @@ mla_status mla_cache_read_ds_mla(mla_dtype dst_dtype, mla_tensor out, mla_tensor
  *   p = seq_lens[b] - 1, attends the rows t <= p with t < sinks or t > p - window (window >= 1
  *   rows ending with its own, and the sequence's first `sinks` >= 0 rows). Rows outside are
  *   never used, whatever they hold, and the block ids of pages without an attended row are not
- *   read: such pages may have been freed.
+ *   read: such pages may have been freed. num_splits beyond 4096 counts as 4096.
  *   workspace: at least mla_decode_window_workspace_size(...) bytes, 256-byte aligned,
  *   caller-owned, not used by concurrent calls. */
 mla_status mla_decode_window(mla_dtype dtype, mla_tensor o_lat_out, float* lse_out,
@@ -383,7 +383,8 @@ size_t mla_decode_window_workspace_size(int32_t batch, int32_t num_heads, int32_
  *   attends the rows t <= p with t < sinks or t > p - window. A query at a negative position
  *   (a chunk longer than its cache) attends nothing: o = 0, lse = -inf. Rows of q_cat outside
  *   every sequence (before cu_seqlens_q[0], at or behind cu_seqlens_q[batch]) leave their rows
- *   of o_lat_out and lse_out as they were. Rows that no query of the chunk attends are never
+ *   of o_lat_out and lse_out as they were; so do all rows where cu_seqlens_q decreases or
+ *   leaves [0, tokens], which mla_device_error reports (MLA_ERR_DEVICE_DATA). Rows that no query of the chunk attends are never
  *   used, whatever they hold, and the block ids of pages without an attended row are not read;
  *   a row that some query of the chunk attends must hold finite values.
  *   workspace: at least mla_prefill_window_workspace_size(tokens, ...) bytes (tokens = rows of

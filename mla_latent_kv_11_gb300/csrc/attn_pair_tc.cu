@@ -30,12 +30,28 @@
 // L2 1.44 times, and keys 64k .. 64k + 63 sit in H_k of both CTAs when P V runs.
 //
 // Order on the tensor pipe: QK(g+1), PV(g), so the softmax of tile g runs under QK(g+1);
-// at a row tile's end PV comes first. 256 threads: warp 0 loads (TMA), warp 1 of the first CTA
-// issues every MMA, warp 2 owns the tensor memory, warps 4..7 run the softmax, the rescaling
-// of O and the epilogue, one thread a lane.
+// at a row tile's end PV comes first. 384 threads: warps 0 and 2 load the keys, a quarter (two column
+// groups) a barrier, warp 3 the W boxes, rope and queries (TMA; with one warp for all, issuing the
+// loads took longer than the MMAs); warp 1 of the first CTA issues every MMA; warp 2 owns the tensor
+// memory; warps 4..11 run the softmax, the rescaling of O and the epilogue, two threads a lane. A row
+// tile's output is parked in tensor memory as bf16 and stored under the next tile's MMAs: a row's
+// stores leave an SM at 16 to 19 bytes a cycle, 3000 to 4000 cycles a row tile.
+//
+// Work. A row tile's key tiles are cut over the clusters where that shortens the longest one's list
+// (window_sched.cu); the pieces' float32 outputs and log-sum-exps are joined by a second kernel.
+//
+// What bounds it and what it measured (152 SMs, 76 clusters):
+//   prefill of 4 x 1024 tokens, 128 heads, window 2048: 1.43 ms, 1.57 PFLOP/s, 82% of a dense library
+//     product's rate. A tile takes 2100 cycles a cluster, its MMAs 1856 of them; shared memory moves
+//     363 KB a tile and CTA meanwhile.
+//   decode of 64 sequences of 1K to 16K rows, 128 heads, window 4096: 70 us, 4.2 TB/s; 5.9 TB/s between
+//     a start of 11 us (schedule, first loads) and a tail (cut rows' outputs and their merge).
+//   prefill of ragged prompts, 64 heads, window 777: 113 us for 82 GFLOP, bounded by what a row tile
+//     costs beside its 1 to 8 tiles (its queries' load, the pipeline's filling, its output).
 //
 // Every wait is bounded; one that gives up winds both CTAs down and is reported.
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
@@ -307,8 +323,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (warp == 0 || warp == 2 || warp == 3) {
     // ------------------------------------------------------------ loads, in both CTAs: warps 0 and 2 the
-    // keys, which the tensor pipe waits for (two quarters of a tile each), warp 3 the rest. The whole warp walks the tiles. Lane h looks
-    // up the block id of a tile's block h (small pages: lanes 8h .. 8h + 7 the ids of its pages).
+    // keys, which the tensor pipe waits for (two quarters of a tile each), warp 3 the rest. The whole
+    // warp walks the tiles. Lane h looks up the block id of a tile's block h (small pages: lanes
+    // 8h .. 8h + 7 the ids of its pages).
     const int rows_box = kSmall ? p.page : kBlk, subs = kBlk / rows_box;
     Walker<2> wk;
     wk.init(p.sched, unit, units);
@@ -707,7 +724,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (!ok) break;
       tc_fence_after();
       l = (sums[0][ln] + sums[1][ln]) + (sums[0][ln ^ 64] + sums[1][ln ^ 64]);
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float inv = l == 0.f ? 0.f : 1.f / l;   // a NaN stays one
       const int64_t prow = (int64_t)sg.slot * 128 + 64 * rank + row;
       if (sg.slot < 0) {
         // A row tile's 64 KB of output leave an SM at 16 bytes a cycle, longer than a tile of keys takes.
@@ -752,7 +769,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       if (valid && half == 0 && part == 0) {
-        const float lse = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -CUDART_INF_F;
+        const float lse = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.69314718055994531f;
         if (sg.slot >= 0)
           p.out.part_lse[prow] = lse;
         else if (p.out.lse != nullptr)
@@ -819,10 +836,38 @@ cudaError_t launch_attn(const PairParams& p, const WindowMaps& maps, int units, 
                   maps.q, p);
 }
 
+int pair_units(int num_splits) {
+  return num_splits > 0 ? std::min(num_splits, kMaxUnits) : max_pairs<64, false>();
+}
+
 int pair_tokens(int H) { return H > 64 ? 1 : 2 * (64 / H); }
 
 // Whether a CTA's queries fill its 64 rows, so that one load lays all their column groups out.
 bool q_whole(int H) { return H >= 64 || 64 % H == 0; }
+
+// A 4-D TMA map of bf16 (dims innermost first, strides of dims 1 to 3 in bytes), 128-byte swizzled.
+bool make_map4d(CUtensorMap* m, const void* base, const uint64_t (&dims)[4], const uint64_t (&strides)[3],
+                const uint32_t (&box)[4]) {
+  static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  if (!encode) return false;
+  cuuint64_t d[4], st[3];
+  cuuint32_t b[4], step[4] = {1, 1, 1, 1};
+  std::copy(dims, dims + 4, d);
+  std::copy(strides, strides + 3, st);
+  std::copy(box, box + 4, b);
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), d, st, b, step,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 // Tensor maps: two column groups of 64 of a block, for pages of 64 rows or more; one group of a block or
 // a page; queries.
@@ -830,14 +875,14 @@ bool pair_maps(const WindowCall& c, WindowMaps* m) {
   const uint64_t row = (uint64_t)c.cache.s_row * 2, blk = (uint64_t)c.cache.s_blk * 2, page = c.cache.page,
                  blocks = c.cache.num_blocks, groups = (c.L + c.R) / 64, H = c.H, T = c.q.n0;
   const uint32_t rows = page < kBlk ? (uint32_t)page : kBlk, hb = H < 64 ? (uint32_t)H : 64, toks = H > 64 ? 1 : 64 / hb;
-  constexpr auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
   const uint64_t kd[4] = {64, page, 8, blocks}, ks[3] = {row, 128, blk};
   const uint32_t kb[4] = {64, rows, 2, 1};
   const uint64_t qd[4] = {64, H, T, groups}, qs[3] = {(uint64_t)c.q.s1 * 2, (uint64_t)c.q.s0 * 2, 128};
   const uint32_t qb[4] = {64, hb, toks, q_whole(c.H) ? (uint32_t)groups : 1};
-  return make_map(&m->keys, c.cache.data, 4, kd, ks, kb, sw) &&
-         make_map3d(&m->boxes, c.cache.data, 64 * groups, page, blocks, row, blk, 64, rows, 1, sw) &&
-         make_map(&m->q, c.q.data, 4, qd, qs, qb, sw);
+  return make_map4d(&m->keys, c.cache.data, kd, ks, kb) &&
+         make_map3d(&m->boxes, c.cache.data, 64 * groups, page, blocks, row, blk, 64, rows, 1,
+                    CU_TENSOR_MAP_SWIZZLE_128B) &&
+         make_map4d(&m->q, c.q.data, qd, qs, qb);
 }
 
 }  // namespace
@@ -855,11 +900,11 @@ bool window_tc_supported(mla_dtype dt, const WindowCall& c, WindowMaps* maps) {
 
 size_t window_tc_workspace(int64_t T, int64_t B, int H, bool decode, int num_splits) {
   if (H <= 0 || H > 128) return 0;
-  return window_workspace(T, B, decode, pair_tokens(H), num_splits > 0 ? num_splits : max_pairs<64, false>(), 128, 512);
+  return window_workspace(T, B, decode, pair_tokens(H), pair_units(num_splits), 128, 512);
 }
 
 cudaError_t launch_window_tc(const WindowCall& c, const WindowMaps& maps, int num_splits, void* ws, cudaStream_t st) {
-  const int units = num_splits > 0 ? num_splits : max_pairs<64, false>(), tpt = pair_tokens(c.H);
+  const int units = pair_units(num_splits), tpt = pair_tokens(c.H);
   PairParams p{};
   cudaError_t e = launch_window_schedule(c, tpt, 2, units, 128, ws, &p.sched, &p.out, st);
   if (e != cudaSuccess) return e;

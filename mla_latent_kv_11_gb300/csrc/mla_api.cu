@@ -897,8 +897,8 @@ mla_status mla_device_error(void* stream) {
   cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_status(e, "mla_device_error: stream synchronize");
   unsigned bits = copy_errors_read_clear() | cache_io_errors_read_clear() | attn_pair_errors_read_clear() |
-                  window_sched_errors_read_clear() | window_simt_errors_read_clear() | attn_simt_errors_read_clear() | attn_tc_errors_read_clear() |
-                  bmm_tc_errors_read_clear() | combine_vup_errors_read_clear();
+                  window_sched_errors_read_clear() | window_simt_errors_read_clear() |
+                  attn_simt_errors_read_clear() | attn_tc_errors_read_clear() | bmm_tc_errors_read_clear() | combine_vup_errors_read_clear();
   if (bits & kErrTimeout) return fail(MLA_ERR_TIMEOUT, "a bounded device-side wait gave up");
   if (bits & kErrDeviceData)
     return fail(MLA_ERR_DEVICE_DATA, "a slot, block id or sequence length was out of range");

@@ -23,9 +23,9 @@ namespace {
 
 __device__ unsigned g_window_err = 0;
 
-// In tiles, of kPer blocks each (measured: a tensor-core tile takes 1.7 us, one on the CUDA cores ten
-// times that): what a row tile costs beside its tiles (with 1 instead of 2, 880 row tiles of 3 tensor-core
-// tiles took 126 us instead of 113), and what cutting adds to a unit's time.
+// In tiles, of kPer blocks each (a tensor-core tile takes 1.7 us, one on the CUDA cores ten times
+// that): what a row tile costs beside its tiles (a prefill of ragged prompts, 1 to 8 tensor-core tiles
+// a row tile, took 115 us with 2, 135 with 1), and what cutting adds to a unit's time.
 template <int kPer>
 constexpr int kItemCost = kPer == 2 ? 2 : 1;
 template <int kPer>
@@ -51,7 +51,8 @@ __device__ __forceinline__ int kv_len(const SchedArgs& s, int b) {
   return n;
 }
 
-// Query tokens of sequence b; 0 (and reported) where cu_q leaves [0, T] or decreases.
+// Query tokens of sequence b; -1 (and reported) where cu_q leaves [0, T] or decreases. Nothing is
+// computed then: only an ascending cu_q keeps the row tiles within the room for them.
 __device__ __forceinline__ int q_len(const SchedArgs& s, int b, int& q0) {
   if (s.cu_q == nullptr) {
     q0 = b;
@@ -61,7 +62,7 @@ __device__ __forceinline__ int q_len(const SchedArgs& s, int b, int& q0) {
   const int q1 = s.cu_q[b + 1];
   if (q0 < 0 || q1 > s.T || q1 < q0) {
     atomicOr(&g_window_err, kErrDeviceData);
-    return 0;
+    return -1;
   }
   return q1 - q0;
 }
@@ -95,9 +96,10 @@ __global__ void __launch_bounds__(1024) window_split_kernel(SchedArgs s) {
       cost[kSplitItems + 1], tiles[kSplitItems], longest[32];
   pdl_enter();
   const int i = threadIdx.x;
-  int n = 0, q0 = 0, total;
+  int n = 0, q0 = 0, k = 0, total;
+  if (i < s.B) k = q_len(s, i, q0);
+  if (__syncthreads_or(k < 0)) k = 0;
   if (i < s.B) {
-    const int k = q_len(s, i, q0);
     n = (k + s.tpt - 1) / s.tpt;
     q_begin[i] = q0;
     q_count[i] = k;
@@ -168,12 +170,17 @@ __global__ void __launch_bounds__(1024) window_split_kernel(SchedArgs s) {
 __global__ void __launch_bounds__(1024) window_prefix_kernel(SchedArgs s) {
   __shared__ int warp_tot[32];
   pdl_enter();
-  int carry = 0;
+  int carry = 0, q0;
+  bool bad = false;
+  for (int b = threadIdx.x; b < s.B; b += blockDim.x) {
+    bad |= q_len(s, b, q0) < 0;
+    kv_len(s, b);   // reports a bad length
+  }
+  bad = __syncthreads_or(bad);
   for (int base = 0; base < s.B; base += blockDim.x) {
     const int b = base + threadIdx.x;
-    int q0, tot;
-    const int n = b < s.B ? (q_len(s, b, q0) + s.tpt - 1) / s.tpt : 0;
-    if (b < s.B) kv_len(s, b);   // reports a bad length
+    int tot;
+    const int n = b < s.B && !bad ? (q_len(s, b, q0) + s.tpt - 1) / s.tpt : 0;
     const int ex = scan_block(n, warp_tot, &tot);
     if (b < s.B) s.prefix[b] = carry + ex;
     carry += tot;
@@ -224,15 +231,19 @@ __global__ void __launch_bounds__(32 * kMergeWarps) window_merge_kernel(WindowSc
   // attention kernel between waits for them before it lets dependents launch): read before the wait
   const int u = blockIdx.x + 1, lane = threadIdx.x & 31;
   const int2 at = s.unit_start[u], before = s.unit_start[u - 1];
-  if (at.x >= *s.total || at.y == 0 || (before.x == at.x && before.y > 0)) return;
+  // the first block waits for the attention kernel though it have nothing to merge: what follows this
+  // kernel waits for it alone
+  if (at.x >= *s.total || at.y == 0 || (before.x == at.x && before.y > 0)) {
+    if (blockIdx.x == 0 && blockIdx.y == 0) pdl_enter();
+    return;
+  }
   const int4 d = s.items[2 * at.x];
   // row `row` of a slot: its token and head (a CTA of the pair holds 64 rows: a half of the heads of
   // one token, or whole tokens)
   const int row = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
-  if (row >= out.rows) return;
   const int rank = row >> 6, rr = row & 63;
   const int t = out.tptc ? out.tptc * rank + rr / out.H : 0, h = out.tptc ? rr % out.H : row;
-  if ((out.tptc && rr >= out.tptc * out.H) || h >= out.H || t >= d.y) return;
+  if (row >= out.rows || (out.tptc && rr >= out.tptc * out.H) || h >= out.H || t >= d.y) return;
   // pieces: the head in unit u - 1 (slot 2 (u - 1) + 1), then units u, u + 1, ... (slots 2 v)
   int n = 1;
   for (int base = u;; base += 32) {
@@ -293,7 +304,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) window_merge_kernel(WindowSc
       }
     }
   }
-  const float inv = tot > 0.f ? 1.f / tot : 0.f;
+  const float inv = tot == 0.f ? 0.f : 1.f / tot;   // a NaN stays one
   T* o = static_cast<T*>(out.o) + (int64_t)(d.x + t) * out.o_s0 + (int64_t)h * out.o_s1;
   if constexpr (kVec) {
 #pragma unroll
@@ -309,7 +320,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) window_merge_kernel(WindowSc
     }
   }
   if (lane == 0 && out.lse != nullptr)
-    out.lse[(int64_t)(d.x + t) * out.H + h] = tot > 0.f ? m + logf(tot) : -CUDART_INF_F;
+    out.lse[(int64_t)(d.x + t) * out.H + h] = tot == 0.f ? -CUDART_INF_F : m + logf(tot);
 }
 
 // Row tiles at most: T tokens of B sequences, tpt a tile.

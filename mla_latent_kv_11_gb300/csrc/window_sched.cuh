@@ -6,7 +6,8 @@
 
 namespace mla {
 
-constexpr int kBlk = 64;   // cache rows per block
+constexpr int kBlk = 64;          // cache rows per block
+constexpr int kMaxUnits = 4096;   // work units at most, whatever a caller asks for
 
 // A row tile ("item") as the schedule describes it: {first token's row, tokens, its position, sequence}
 // and {first window row, sink blocks, first window block behind them, blocks in all}. Its tokens sit

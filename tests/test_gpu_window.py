@@ -279,6 +279,146 @@ def test_offsets_beyond_32_bits(mla):
     wr.check(o, l, c.want(), 1)
 
 
+@pytest.mark.parametrize("tokens,bounds", [(12, [0, 5, 3, 12]), (12, [0, 12, 0, 12]), (12, [-1, 4, 8, 12]),
+                                           (12, [0, 4, 8, 13]), (12, [0, 2 ** 31 - 1, 4, 12]),
+                                           (1100, [0, 1100, 0, 1100]), (1100, [0, 400, 300, 1101])])
+@pytest.mark.parametrize("geometry", ["v3", "lite_f32"])
+def test_bounds_that_decrease_or_leave_the_tokens_are_reported(mla, geometry, tokens, bounds):
+    c = prefill_case(geometry, [70, 70, 70], [tokens, 0, 0], 9, 0, seed=26)
+    cache, q, table, kv, _ = c.dev()
+    o, l = outputs(c)
+    cache = torch.zeros_like(cache)
+    table = torch.zeros_like(table)
+    cu = torch.tensor(bounds, dtype=torch.int32, device="cuda")
+    mla.mla_prefill_window(o, q, cache, table, cu, kv, 512, 64, c.scale, 9, lse_out=l)
+    with pytest.raises(mla.MlaError) as e:
+        mla.mla_device_error()
+    assert e.value.status == mla.MLA_ERR_DEVICE_DATA
+    assert (o == 7).all() and (l == 7).all()
+    # and the next call is right
+    c = prefill_case(geometry, [70, 33], [3, 2], 9, 0, seed=27)
+    wr.check(*prefill(mla, c), c.want(), 5)
+
+
+@pytest.mark.parametrize("geometry", ["h16", "lite_f32"])
+def test_decode_of_more_sequences_than_a_block_has_threads(mla, geometry):
+    c = decode_case(geometry, [(53 * i) % 90 for i in range(1100)], 40, 2, seed=28)
+    wr.check(*decode(mla, c), c.want(), 1100)
+
+
+@pytest.mark.parametrize("page", [32, 24, 192, 320])
+@pytest.mark.parametrize("geometry", ["v3", "h64"])
+def test_more_page_sizes(mla, geometry, page):
+    c = prefill_case(geometry, [420, 31], [4, 3], 170, 33, page=page, seed=29)
+    wr.check(*prefill(mla, c), c.want(), 7)
+
+
+def test_output_rows_on_16_byte_boundaries(mla):
+    c = prefill_case("h64", [300, 40], [5, 4], 100, 4, seed=30)
+    cache, q, table, kv, cu = c.dev()
+    wide = torch.full((9, 64, 536), 7.0, dtype=c.dt, device="cuda")
+    o = wide[..., 8:520]
+    assert o.data_ptr() % 32 == 16
+    mla.mla_prefill_window(o, q, cache, table, cu, kv, 512, 64, c.scale, 100, sinks=4)
+    mla.mla_device_error()
+    wr.check(o, None, c.want(), 9)
+    assert (wide[..., :8] == 7).all() and (wide[..., 520:] == 7).all()
+
+
+@pytest.mark.parametrize("geometry", ["v3", "lite_f32"])
+@pytest.mark.parametrize("scale", [0.0, -0.05])
+def test_scales_that_are_not_positive(mla, geometry, scale):
+    c = decode_case(geometry, [100, 0, 300], 120, 4, seed=31, scale=abs(scale))
+    want = c.want()
+    # the queries negated and the scale too: the same scores
+    if scale < 0:
+        c.qs, c.scale = -c.qs, scale
+    wr.check(*decode(mla, c), want, 3)
+
+
+def test_inputs_of_one_row_or_head_repeated(mla):
+    # strides of zero: every head, and every sequence, has the same query
+    c = decode_case("v3", [200, 90], 120, 4, seed=32)
+    c.qs = c.qs[:1, :1].expand(2, 128, -1)
+    cache, _, table, kv, _ = c.dev()
+    q = c.qs[:1, :1].contiguous().cuda().expand(2, 128, -1)
+    assert q.stride() == (0, 0, 1)
+    o, l = outputs(c)
+    mla.mla_decode_window(o, q, cache, table, kv, 512, 64, c.scale, 120, sinks=4, lse_out=l)
+    mla.mla_device_error()
+    wr.check(o, l, c.want(), 2)
+
+
+@pytest.mark.parametrize("geometry", ["v3", "h64", "lite_f32"])
+def test_a_nan_of_one_query_stays_in_its_row(mla, geometry):
+    c = prefill_case(geometry, [90, 700], [4, 1], 640, 4, seed=33)
+    want = c.want()
+    c.qs[1, 3, 7] = float("nan")
+    c.qs[4, 5, 9] = float("nan")     # a row that is cut over units and merged
+    o, l = prefill(mla, c)
+    for t, h in ((1, 3), (4, 5)):
+        assert o[t, h].isnan().all() and l[t, h].isnan()
+        o[t, h] = torch.from_numpy(want[0][t, h]).to(o)
+        l[t, h] = float(want[1][t, h])
+    # rounding `want` itself is within its bound
+    wr.check(o, l, want, 5)
+
+
+def test_more_splits_than_there_is_work(mla):
+    c = decode_case("lite_f32", [2000, 3, 0], 2000, 0, seed=34)
+    wr.check(*decode(mla, c, num_splits=2 ** 31 - 1), c.want(), 3)
+    assert mla.mla_decode_window_workspace_size(3, 16, 512, 2 ** 31 - 1) == \
+        mla.mla_decode_window_workspace_size(3, 16, 512, 4096)
+
+
+def test_two_graphs_share_a_workspace(mla):
+    cases = [prefill_case("v3", [700, 64], [9, 5], 500, 4, seed=35), prefill_case("h20", [100, 300], [40, 30], 77, 3, seed=36)]
+    need = max(mla.mla_prefill_window_workspace_size(sum(c.q_lens), len(c.kv), c.qs.shape[1], 512) for c in cases)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    graphs = []
+    for c in cases:
+        cache, q, table, kv, cu = c.dev()
+        o, l = outputs(c)
+
+        def call():
+            mla.mla_prefill_window(o, q, cache, table, cu, kv, 512, 64, c.scale, c.window, sinks=c.sinks, lse_out=l,
+                                   workspace=ws)
+        call()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        graphs.append((g, c, o, l, (cache, q, table, kv, cu)))
+    for _ in range(3):
+        for g, _, o, l, _ in graphs:
+            o.zero_()
+            l.zero_()
+            g.replay()
+    mla.mla_device_error()
+    for _, c, o, l, _ in graphs:
+        wr.check(o, l, c.want(), sum(c.q_lens))
+
+
+def test_results_are_there_for_the_next_kernel(mla):
+    # two sequences a unit (of 76), none cut: the merge has nothing to do, and what follows on the stream waits
+    # for the whole call all the same
+    c = decode_case("v3", [200] * 152, 200, 0, seed=37)
+    cache, q, table, kv, _ = c.dev()
+    want, _ = decode(mla, c)
+    o, _ = outputs(c)
+    wr.check(want, None, c.want(), 152)
+    for _ in range(50):
+        o.fill_(7.0)
+        mla.mla_decode_window(o, q, cache, table, kv, 512, 64, c.scale, 200)
+        copy = o.clone()
+        assert torch.equal(copy, want)
+
+
+def test_the_default_stream_by_number(mla):
+    c = decode_case("v3", [70, 200], 100, 4, seed=38)
+    wr.check(*decode(mla, c, stream=0), c.want(), 2)
+
+
 def test_refusals_of_the_binding(mla):
     c = decode_case("v3", [70], 20, 0, seed=25)
     cache, q, table, kv, cu = c.dev()
