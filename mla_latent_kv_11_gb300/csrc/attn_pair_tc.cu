@@ -106,8 +106,8 @@ struct PairShared {
   uint64_t fin;
   uint32_t tmem_base;
   int abort_flag;
-  // row maxima of a tile, [tile parity][columns 0..31 / 32..63 of S][lane]; at a segment's end the
-  // weights' sums
+  // exchanges between the four threads of a row, in turn in two places, [columns 0..31 / 32..63 of S]
+  // [lane]: the maxima of a tile, at a segment's end the weights' sums
   float red[2][2][128];
 };
 static_assert(sizeof(PairShared) <= 3072, "barrier block overflows its slot");
@@ -269,6 +269,17 @@ __device__ __forceinline__ void st_global_32B(void* dst, const uint32_t* w) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
                "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                : "memory");
+}
+
+// 16 lanes x 32 columns of tensor memory: w[4 k + 2 j + i] of lane t is row 8 j + t / 4, column
+// 8 k + 2 (t % 4) + i.
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t addr, uint32_t* w) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7]), "=r"(w[8]),
+        "=r"(w[9]), "=r"(w[10]), "=r"(w[11]), "=r"(w[12]), "=r"(w[13]), "=r"(w[14]), "=r"(w[15])
+      : "r"(addr));
 }
 
 // kSmall: pages of less than 64 rows.
@@ -589,30 +600,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     Walker<2> wk;
     wk.init(p.sched, unit, units);
     Seg sg;
-    // the output that waits in tensor memory: quarters left of this thread's 128 columns, its row
+    // The output that waits in tensor memory: quarters left of this warp's 32 rows x 128 columns, this
+    // lane's row. A quarter is 16 rows x 64 columns, whole lines of 128 bytes: an SM stores those at 31
+    // bytes a cycle, a sector of 32 a row at 17. The words are parked in the order that gives each lane
+    // 32 bytes of a row: lanes 4 a .. 4 a + 3 rows a and a + 8
     int left = 0;
     __nv_bfloat16* to = nullptr;
     auto store_quarter = [&]() {
-      const int r = 4 - left--;
-      float v[16];
-      tmem_ld16(tmem + lane_addr + kTmemOut + 64 * part + 16 * r, v);
+      const int r = 4 - left--, h = r & 1, c = r >> 1;
+      uint32_t w[16];
+      tmem_ld_16x32(tmem + lane_addr + ((16u * h) << 16) + kTmemOut + 64 * part + 32 * c, w);
       tmem_ld_wait();
-      const uint32_t* w = reinterpret_cast<const uint32_t*>(v);
-      if (to != nullptr) {
-        if (p.o_32B) {
-          st_global_32B(to + 32 * r, w);
-          st_global_32B(to + 32 * r + 16, w + 8);
-        } else {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            *reinterpret_cast<uint4*>(to + 32 * r + 8 * k) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+      for (int j = 0; j < 2; ++j) {
+        __nv_bfloat16* const o = reinterpret_cast<__nv_bfloat16*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), 16 * h + 8 * j + (lane >> 2)));
+        if (o == nullptr) continue;
+        uint32_t y[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) y[k] = w[4 * (k >> 1) + 2 * j + (k & 1)];
+        __nv_bfloat16* const d = o + 64 * c + 16 * (lane & 3);
+        if (p.o_32B) {
+          st_global_32B(d, y);
+        } else {
+          *reinterpret_cast<uint4*>(d) = make_uint4(y[0], y[1], y[2], y[3]);
+          *reinterpret_cast<uint4*>(d + 8) = make_uint4(y[4], y[5], y[6], y[7]);
         }
       }
       __syncwarp();
     };
-    int g = 0;
+    int g = 0, x = 0;              // x: which of the two places the next exchange between the rows' threads takes
     bool ok = true, mine = true;   // ok: the group's decision; mine: this thread's waits so far
-    while (ok && wk.next(sg)) {
+    bool more = wk.next(sg);
+    while (ok && more) {
       const bool valid = real && tok < sg.ntok;
       const int pos = valid ? sg.pos0 + tok : -1;       // -1 attends nothing
       float m = -CUDART_INF_F, l = 0.f;
@@ -640,11 +660,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int k = 4; k < 32; ++k) mx[k & 3] = fmaxf(mx[k & 3], sv[k]);
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        sh.red[g & 1][part][ln] = top;
+        sh.red[x][part][ln] = top;
         ok = group_all(mine);                // the one group decision of a tile; the row's four maxima
         if (!ok) break;
-        const float mt = fmaxf(fmaxf(top, sh.red[g & 1][part ^ 1][ln]),
-                               fmaxf(sh.red[g & 1][0][ln ^ 64], sh.red[g & 1][1][ln ^ 64])) * p.scale_log2;
+        const float mt = fmaxf(fmaxf(top, sh.red[x][part ^ 1][ln]),
+                               fmaxf(sh.red[x][0][ln ^ 64], sh.red[x][1][ln ^ 64])) * p.scale_log2;
+        x ^= 1;   // every thread is done with the place of the exchange before
         float alpha = 1.f;
         if (mt > m + kLazyRescale || (m == -CUDART_INF_F && mt > -CUDART_INF_F)) {
           alpha = m == -CUDART_INF_F ? 0.f : ex2_approx(m - mt);
@@ -712,43 +733,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (left > 0) store_quarter();
       }
       if (!ok) break;
-      // ---- O / l. What is left of the output before goes out while the last PV runs
-      while (left > 0) store_quarter();
-      const int last = g - 1;
-      mine = mine && wait_for(&sh.pv_done[last & 1][3], (last >> 1) & 1, abort);
-      // in the place of the last tile's maxima: PV has its P, so every warp has read them; they are
-      // written again behind the next tile's barrier
-      float (&sums)[2][128] = sh.red[last & 1];
+      // ---- O / l. The weights' sums are exchanged, what is left of the output before goes out and the
+      // next row tile is looked up while the last PV runs
+      float (&sums)[2][128] = sh.red[x];
       sums[part][ln] = l;
       ok = group_all(mine);
       if (!ok) break;
-      tc_fence_after();
       l = (sums[0][ln] + sums[1][ln]) + (sums[0][ln ^ 64] + sums[1][ln ^ 64]);
+      x ^= 1;
       const float inv = l == 0.f ? 0.f : 1.f / l;   // a NaN stays one
-      const int64_t prow = (int64_t)sg.slot * 128 + 64 * rank + row;
-      if (sg.slot < 0) {
-        // A row tile's 64 KB of output leave an SM at 16 bytes a cycle, longer than a tile of keys takes.
+      const int slot = sg.slot;
+      const int64_t prow = (int64_t)slot * 128 + 64 * rank + row, orow = sg.tok0 + tok;
+      if (valid && half == 0 && part == 0) {
+        const float lse = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.69314718055994531f;
+        if (slot >= 0)
+          p.out.part_lse[prow] = lse;
+        else if (p.out.lse != nullptr)
+          p.out.lse[orow * p.H + head] = lse;
+      }
+      while (left > 0) store_quarter();
+      more = wk.next(sg);
+      const int last = g - 1;
+      mine = mine && wait_for(&sh.pv_done[last & 1][3], (last >> 1) & 1, abort);
+      tc_fence_after();
+      if (slot < 0) {
+        // A row tile's 64 KB of output take an SM as long to store as a tile of keys takes.
         // So O only becomes bf16 here, within tensor memory, and a quarter of it is stored behind each
         // of the next tiles
-        float v[32];
-        tmem_ld32(tmem + lane_addr + 128 * part, v);
 #pragma unroll 1
-        for (int r = 0; r < 4; ++r) {
-          uint32_t w[16];
+        for (int r = 0; r < 2; ++r) {
+          float v[2][32];
+          tmem_ld32(tmem + lane_addr + 128 * part + 64 * r, v[0]);
+          tmem_ld32(tmem + lane_addr + 128 * part + 64 * r + 32, v[1]);
           tmem_ld_wait();
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * k] * inv, v[2 * k + 1] * inv);
-            w[k] = *reinterpret_cast<const uint32_t*>(&h);
+          for (int i = 0; i < 2; ++i) {
+            uint32_t w[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const int word = 8 * ((k >> 1) & 3) + 4 * i + 2 * (k >> 3) + (k & 1);   // of the 32
+              const float* const f = v[word >> 4] + 2 * (word & 15);
+              const __nv_bfloat162 h = __floats2bfloat162_rn(f[0] * inv, f[1] * inv);
+              w[k] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            tmem_st16u(tmem + lane_addr + kTmemOut + 64 * part + 32 * r + 16 * i, w);
           }
-          if (r < 3) tmem_ld32(tmem + lane_addr + 128 * part + 32 * (r + 1), v);
-          tmem_st16u(tmem + lane_addr + kTmemOut + 64 * part + 16 * r, w);
         }
         tmem_st_wait();
         left = 4;
         // a lane whose row is not real stores nothing
-        to = valid ? static_cast<__nv_bfloat16*>(p.out.o) + (int64_t)(sg.tok0 + tok) * p.out.o_s0 + (int64_t)head * p.out.o_s1 +
-                         256 * half + 128 * part
+        to = valid ? static_cast<__nv_bfloat16*>(p.out.o) + orow * p.out.o_s0 + (int64_t)head * p.out.o_s1 + 256 * half +
+                         128 * part
                    : nullptr;
       } else {
         float* const o = p.out.part_o + prow * 512 + 256 * half + 128 * part;
@@ -768,16 +803,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           __syncwarp();
         }
       }
-      if (valid && half == 0 && part == 0) {
-        const float lse = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.69314718055994531f;
-        if (sg.slot >= 0)
-          p.out.part_lse[prow] = lse;
-        else if (p.out.lse != nullptr)
-          p.out.lse[(int64_t)(sg.tok0 + tok) * p.H + head] = lse;
-      }
     }
     while (left > 0) store_quarter();
-    if (!ok) give_up();
+    if (!ok || !mine) give_up();
   }
   // ---------------------------------------------------------------- teardown
   tc_fence_before();
