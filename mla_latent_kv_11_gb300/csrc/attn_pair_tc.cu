@@ -786,19 +786,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                          128 * part
                    : nullptr;
       } else {
-        float* const o = p.out.part_o + prow * 512 + 256 * half + 128 * part;
-        float v[16];
-        tmem_ld16(tmem + lane_addr + 128 * part, v);
+        // float32, whole lines as above: 16 rows x 32 columns at a time, their columns in the order that
+        // tensor memory gives them out in (WindowOut: permuted)
+        const unsigned rows = __ballot_sync(0xffffffffu, valid);
+        float* const o = p.out.part_o + ((int64_t)slot * 128 + 64 * rank + 32 * (warp & 1)) * 512 + 256 * half + 128 * part +
+                         8 * (lane & 3);
+        uint32_t w[16];
+        tmem_ld_16x32(tmem + lane_addr + 128 * part, w);
 #pragma unroll 1
         for (int r = 0; r < 8; ++r) {
-          uint32_t w[16];
+          const int h = r & 1, c = r >> 1;
+          uint32_t y[2][8];
           tmem_ld_wait();
 #pragma unroll
-          for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(v[k] * inv);
-          if (r < 7) tmem_ld16(tmem + lane_addr + 128 * part + 16 * (r + 1), v);
-          if (valid) {
-            st_global_32B(o + 16 * r, w);
-            st_global_32B(o + 16 * r + 8, w + 8);
+          for (int i = 0; i < 2; ++i) {
+            const float by = __shfl_sync(0xffffffffu, inv, 16 * h + 8 * i + (lane >> 2));
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              y[i][k] = __float_as_uint(__uint_as_float(w[4 * (k >> 1) + 2 * i + (k & 1)]) * by);
+          }
+          if (r < 7)
+            tmem_ld_16x32(tmem + lane_addr + ((16u * ((r + 1) & 1)) << 16) + 128 * part + 32 * ((r + 1) >> 1), w);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int rw = 16 * h + 8 * i + (lane >> 2);
+            if ((rows >> rw) & 1u) st_global_32B(o + (int64_t)rw * 512 + 32 * c, y[i]);
           }
           __syncwarp();
         }
@@ -938,6 +950,7 @@ cudaError_t launch_window_tc(const WindowCall& c, const WindowMaps& maps, int nu
   if (e != cudaSuccess) return e;
   p.H = c.H;
   p.tpt = tpt;
+  p.out.permuted = true;
   p.tptc = p.out.tptc = c.H > 64 ? 0 : tpt / 2;
   constexpr int kFar = 0x3fffffff;   // positions stay below this
   p.window = std::min(c.window.window, kFar);

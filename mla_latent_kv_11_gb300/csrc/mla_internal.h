@@ -219,8 +219,9 @@ struct WindowCall {
 };
 // The schedule in the workspace (window_sched.cu): the row tiles' descriptions, how many there are and,
 // where row tiles may be cut, {row tile, tile} of each unit's first (null: whole row tiles dealt out);
-// cut: some may be, so their pieces have to be merged.
+// most: row tiles at most; cut: some may be cut, so their pieces have to be merged.
 struct WindowSched {
+  int64_t most;
   int4* items;
   int32_t* total;
   int2* unit_start;
@@ -228,12 +229,14 @@ struct WindowSched {
 };
 // Where results go: rows of the output, and the partial slots [2 * units][rows][L] of cut row tiles
 // with their log-sum-exps [2 * units][rows]. tptc 0: a slot's row is a head; else rows 64 r .. of a slot
-// are tptc tokens' heads each.
+// are tptc tokens' heads each. permuted: of each 32 columns of a partial row, place 8 b + 2 k + i holds
+// column 8 k + 2 b + i (b, k < 4, i < 2).
 struct WindowOut {
   void* o;
   int64_t o_s0, o_s1;
   float *lse, *part_o, *part_lse;
   int32_t rows, L, H, tptc;
+  bool permuted;
 };
 // Row tiles of tpt tokens over `units` work units, tiles of blocks_per_tile 64-row blocks, slots of
 // `rows` rows.

@@ -25,11 +25,12 @@ __device__ unsigned g_window_err = 0;
 
 // In tiles, of kPer blocks each (a tensor-core tile takes 1.7 us, one on the CUDA cores ten times
 // that): what a row tile costs beside its tiles (a prefill of ragged prompts, 1 to 8 tensor-core tiles
-// a row tile, took 115 us with 2, 135 with 1), and what cutting adds to a unit's time.
+// a row tile, took 115 us with 2, 135 with 1), and what cutting adds to a unit's time (one sequence of 5
+// tiles: 14.3 us cut, 17.1 whole; 24 of 3: 20.8 cut, 18.1 whole).
 template <int kPer>
 constexpr int kItemCost = kPer == 2 ? 2 : 1;
 template <int kPer>
-constexpr int kCutCost = kPer == 2 ? 5 : 0;
+constexpr int kCutCost = kPer == 2 ? 3 : 0;
 constexpr int kSplitItems = 1024;   // row tiles up to which the schedule cuts them
 
 struct SchedArgs {
@@ -120,8 +121,9 @@ __global__ void __launch_bounds__(1024) window_split_kernel(SchedArgs s) {
     store_item(s.items, i, it);
     nt = item_tiles<kPer>(it.b.w);
   }
-  int all;
+  int all;   // the tiles of all, and kItemCost each
   const int at = scan_block(i < total ? nt + kItemCost<kPer> : 0, warp_tot, &all);
+  const int sum = all - kItemCost<kPer> * total;
   if (i < total) {
     cost[i] = at;
     tiles[i] = nt;
@@ -133,23 +135,47 @@ __global__ void __launch_bounds__(1024) window_split_kernel(SchedArgs s) {
   if ((i & 31) == 0) longest[i >> 5] = top;
   __syncthreads();
   if (total <= s.units) {
-    // pieces of at most `most` tiles: the least `most` whose pieces the units can take
-    int lo = 1, hi = 1, pieces;   // hi: the longest row tile
-    for (int w = 0; w < 32; ++w) hi = max(hi, longest[w]);
-    const int whole = hi;
+    // pieces of at most `lo` tiles: the least `lo` whose pieces the units can take, between sum / units
+    // and sum / (units - total). Every warp tries one, evenly between the bounds
+    const int lane = i & 31, warp = i >> 5, warps = blockDim.x >> 5;
+    const int whole = max(1, __reduce_max_sync(0xffffffffu, longest[lane]));   // the longest row tile
+    int lo = min(whole, max(1, (sum + s.units - 1) / s.units)), hi = whole;
+    if (s.units > total) hi = max(lo, min(hi, (sum + s.units - total - 1) / (s.units - total)));
     while (lo < hi) {
-      const int most = (lo + hi) >> 1;
-      scan_block(i < total ? (nt + most - 1) / most : 0, warp_tot, &pieces);
-      if (pieces <= s.units) hi = most; else lo = most + 1;
+      const int step = max(1, (hi - lo) / warps), most = min(hi, lo + warp * step);
+      int pieces = 0;
+      for (int t = lane; t < total; t += 32) pieces += (tiles[t] + most - 1) / most;
+      pieces = __reduce_add_sync(0xffffffffu, pieces);
+      if (lane == 0) warp_tot[warp] = pieces <= s.units;
+      __syncthreads();
+      int fit = 0;   // the first warp whose pieces fit
+      while (fit < warps && !warp_tot[fit]) ++fit;
+      __syncthreads();
+      if (fit < warps) hi = min(hi, lo + fit * step);
+      if (fit > 0) lo = min(hi, lo + (fit - 1) * step + 1);
     }
-    const int k = i < total ? (lo + kCutCost<kPer> < whole ? (nt + lo - 1) / lo : 1) : 0;
-    const int first_unit = scan_block(k, warp_tot, &pieces);
-    for (int j = 0; j < k; ++j) s.unit_start[first_unit + j] = make_int2(i, (int)((long long)nt * j / k));
-    for (int u = pieces + i; u <= s.units; u += blockDim.x) s.unit_start[u] = make_int2(total, 0);
+    const int n = i < total ? (lo + kCutCost<kPer> < whole ? (nt + lo - 1) / lo : 1) : 0;
+    int pieces;
+    const int first_unit = scan_block(n, warp_tot, &pieces);
+    if (i < total) cost[i] = first_unit;
+    __syncthreads();
+    for (int u = i; u <= s.units; u += blockDim.x) {
+      int2 start = make_int2(total, 0);
+      if (u < pieces) {
+        int a = 0, b = total - 1;   // the last row tile with first unit <= u
+        while (a < b) {
+          const int mid = (a + b + 1) >> 1;
+          if (cost[mid] <= u) a = mid; else b = mid - 1;
+        }
+        const int k = (a + 1 < total ? cost[a + 1] : pieces) - cost[a];
+        start = make_int2(a, (int)((long long)tiles[a] * (u - cost[a]) / k));
+      }
+      s.unit_start[u] = start;
+    }
     return;
   }
   // unit u starts at cost u * all / active: units beyond the tiles there are get nothing
-  const int active = max(1, min(s.units, all - kItemCost<kPer> * total));
+  const int active = max(1, min(s.units, sum));
   for (int u = i; u <= s.units; u += blockDim.x) {
     int2 start = make_int2(total, 0);
     if (u < active && total > 0) {
@@ -211,116 +237,160 @@ __global__ void __launch_bounds__(256) window_items_kernel(SchedArgs s) {
 }
 
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void store4(float* o, float4 v) { *reinterpret_cast<float4*>(o) = v; }
-__device__ __forceinline__ void store4(__nv_bfloat16* o, float4 v) {
-  const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-  *reinterpret_cast<uint2*>(o) =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+__device__ __forceinline__ void store2(float* o, float a, float b) { *reinterpret_cast<float2*>(o) = make_float2(a, b); }
+__device__ __forceinline__ void store2(__nv_bfloat16* o, float a, float b) {
+  *reinterpret_cast<__nv_bfloat162*>(o) = __floats2bfloat162_rn(a, b);
 }
 __device__ __forceinline__ void store1(float* o, float v) { *o = v; }
 __device__ __forceinline__ void store1(__nv_bfloat16* o, float v) { *o = __float2bfloat16_rn(v); }
 
-// Row tiles cut across units: their pieces (normalised output and log-sum-exp) merged. Blocks (u, .)
-// handle the row tile that unit u + 1 is the first to start inside of; a warp a row. What bounds it
-// is latency: a lane a piece looks up how many there are and their sums at once, and the rows of
-// four pieces are in flight together.
+// Row tiles cut across units: their pieces (normalised output and log-sum-exp) merged. Blocks (i, .)
+// handle row tile i, or, with fewer units than row tiles, the one that unit i + 1 is the first to start
+// inside of; a warp 128 kC columns of a row. What bounds it is latency: the pieces are looked up 128 at
+// once, and sixteen loads of their values are in flight together, of as many pieces (kC 1: few row
+// tiles, each of many pieces) or of four (kC 4: enough rows to keep every SM busy). One row tile of 63
+// pieces: 23 us with the attention; 43 when a warp took a whole row and looked up its pieces first.
 constexpr int kMergeWarps = 8;
-template <typename T, bool kVec>
-__global__ void __launch_bounds__(32 * kMergeWarps) window_merge_kernel(WindowSched s, WindowOut out, int units) {
+template <typename T, bool kVec, int kC>
+__global__ void __launch_bounds__(32 * kMergeWarps) window_merge_kernel(WindowSched s, WindowOut out, int units,
+                                                                        bool by_item) {
   // the schedule's words come from two launches back, complete before this kernel can start (the
   // attention kernel between waits for them before it lets dependents launch): read before the wait
-  const int u = blockIdx.x + 1, lane = threadIdx.x & 31;
-  const int2 at = s.unit_start[u], before = s.unit_start[u - 1];
+  const int lane = threadIdx.x & 31;
+  int u = blockIdx.x + 1, item = blockIdx.x, n = 1;   // the first unit that starts inside, the row tile, its pieces
+  bool found = false;
+  if (!by_item) {
+    const int2 at = s.unit_start[u], before = s.unit_start[u - 1];
+    item = at.x;
+    found = at.y > 0 && !(before.x == at.x && before.y > 0);
+  }
+  if (by_item || found) {
+    for (int base = u = found ? u : 1; base < units; base += 128) {
+      int2 w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int v = base + 32 * i + lane;
+        w[i] = v < units ? s.unit_start[v] : make_int2(-1, 0);
+      }
+      unsigned in = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        in = __ballot_sync(0xffffffffu, w[i].x == item && w[i].y > 0);
+        if (in != 0 && !found) {
+          u = base + 32 * i + __ffs(in) - 1;
+          found = true;
+        }
+        n += __popc(in);
+      }
+      if (found && !(in >> 31)) break;   // the units inside a row tile follow one another
+    }
+  }
   // the first block waits for the attention kernel though it have nothing to merge: what follows this
   // kernel waits for it alone
-  if (at.x >= *s.total || at.y == 0 || (before.x == at.x && before.y > 0)) {
+  if (n == 1 || item >= *s.total) {
     if (blockIdx.x == 0 && blockIdx.y == 0) pdl_enter();
     return;
   }
-  const int4 d = s.items[2 * at.x];
+  const int4 d = s.items[2 * item];
+  const int tok0 = d.x, ntok = d.y;
   // row `row` of a slot: its token and head (a CTA of the pair holds 64 rows: a half of the heads of
   // one token, or whole tokens)
-  const int row = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
+  constexpr int kCols = 128 * kC;
+  const int cols = (out.L + kCols - 1) / kCols, job = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
+  const int row = job / cols, c0 = (job - row * cols) * kCols;
   const int rank = row >> 6, rr = row & 63;
   const int t = out.tptc ? out.tptc * rank + rr / out.H : 0, h = out.tptc ? rr % out.H : row;
-  if (row >= out.rows || (out.tptc && rr >= out.tptc * out.H) || h >= out.H || t >= d.y) return;
+  if (row >= out.rows || (out.tptc && rr >= out.tptc * out.H) || h >= out.H || t >= ntok) return;
   // pieces: the head in unit u - 1 (slot 2 (u - 1) + 1), then units u, u + 1, ... (slots 2 v)
-  int n = 1;
-  for (int base = u;; base += 32) {
-    const int v = base + lane;
-    const int2 w = v <= units ? s.unit_start[v] : make_int2(-1, 0);
-    const unsigned more = __ballot_sync(0xffffffffu, w.x == at.x && w.y > 0);
-    const int k = more == 0xffffffffu ? 32 : __ffs(~more) - 1;
-    n += k;
-    if (k < 32) break;
-  }
   auto slot = [&](int i) { return (int64_t)(i == 0 ? 2 * u - 1 : 2 * (u + i - 1)); };
   pdl_enter();
-  float m = -CUDART_INF_F;
-  for (int i = lane; i < n; i += 32) m = fmaxf(m, out.part_lse[slot(i) * out.rows + row]);
+  constexpr int kPieces = 16 / kC;   // in flight
+  float m = -CUDART_INF_F, tot = 0.f;
+  float4 acc[kC] = {};
+  for (int base = 0; base < n; base += kPieces) {
+    const float li = lane < kPieces && base + lane < n ? out.part_lse[slot(base + lane) * out.rows + row] : -CUDART_INF_F;
+    float4 v[kPieces][kC];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float tot = 0.f;
-  constexpr int kCols = kVec ? 4 : 16;   // float4s, or floats, of a row of up to 512 columns in a lane
-  float4 acc[4] = {};
-  float one[16] = {};
-  for (int base = 0; base < n; base += 32) {
-    const float li = base + lane < n ? out.part_lse[slot(base + lane) * out.rows + row] : -CUDART_INF_F;
-    const float mine = li == -CUDART_INF_F ? 0.f : __expf(li - m);
-    const int k = min(32, n - base);
-    for (int i0 = 0; i0 < k; i0 += 4) {
-      float4 v[4][4];
-      float w[4];
+    for (int i = 0; i < kPieces; ++i) {
+      const float* src = out.part_o + (slot(min(base + i, n - 1)) * out.rows + row) * out.L;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        w[i] = __shfl_sync(0xffffffffu, mine, (i0 + i) & 31);
-        if (i0 + i >= k) w[i] = 0.f;
-        const float* src = out.part_o + (slot(base + min(i0 + i, k - 1)) * out.rows + row) * out.L;
+      for (int c = 0; c < kC; ++c) {
+        const int a = c0 + 128 * c;
+        v[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (base + i >= n) continue;
         if constexpr (kVec) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int col = 128 * c + 4 * lane;
-            v[i][c] = col < out.L ? *reinterpret_cast<const float4*>(src + col) : make_float4(0.f, 0.f, 0.f, 0.f);
-          }
+          if (a + 4 * lane < out.L) v[i][c] = *reinterpret_cast<const float4*>(src + a + 4 * lane);
         } else {
-#pragma unroll
-          for (int c = 0; c < kCols; ++c) {
-            const int col = 32 * c + lane;
-            if (col < out.L) one[c] = fmaf(w[i], src[col], one[c]);
-          }
+          if (a + lane < out.L) v[i][c].x = src[a + lane];
+          if (a + 32 + lane < out.L) v[i][c].y = src[a + 32 + lane];
+          if (a + 64 + lane < out.L) v[i][c].z = src[a + 64 + lane];
+          if (a + 96 + lane < out.L) v[i][c].w = src[a + 96 + lane];
         }
       }
+    }
+    float top = li;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        tot += w[i];
-        if constexpr (kVec)
+    for (int o = kPieces / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    top = fmaxf(m, __shfl_sync(0xffffffffu, top, 0));
+    const float by = m == -CUDART_INF_F ? 0.f : __expf(m - top);
+    const float mine = li == -CUDART_INF_F ? 0.f : __expf(li - top);
+    m = top;
+    tot *= by;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          acc[c].x = fmaf(w[i], v[i][c].x, acc[c].x);
-          acc[c].y = fmaf(w[i], v[i][c].y, acc[c].y);
-          acc[c].z = fmaf(w[i], v[i][c].z, acc[c].z);
-          acc[c].w = fmaf(w[i], v[i][c].w, acc[c].w);
-        }
+    for (int c = 0; c < kC; ++c) acc[c] = make_float4(acc[c].x * by, acc[c].y * by, acc[c].z * by, acc[c].w * by);
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const float w = __shfl_sync(0xffffffffu, mine, i);
+      tot += w;
+#pragma unroll
+      for (int c = 0; c < kC; ++c) {
+        acc[c].x = fmaf(w, v[i][c].x, acc[c].x);
+        acc[c].y = fmaf(w, v[i][c].y, acc[c].y);
+        acc[c].z = fmaf(w, v[i][c].z, acc[c].z);
+        acc[c].w = fmaf(w, v[i][c].w, acc[c].w);
       }
     }
   }
   const float inv = tot == 0.f ? 0.f : 1.f / tot;   // a NaN stays one
-  T* o = static_cast<T*>(out.o) + (int64_t)(d.x + t) * out.o_s0 + (int64_t)h * out.o_s1;
-  if constexpr (kVec) {
+  T* o = static_cast<T*>(out.o) + (int64_t)(tok0 + t) * out.o_s0 + (int64_t)h * out.o_s1;
+  // a lane's four columns of 128: two pairs at b0 and b1 (kVec; the partial's places 4 lane ..), or lane,
+  // 32 + lane, ..
+  const int l8 = lane & 7;
+  const int b0 = out.permuted ? 32 * (lane >> 3) + 16 * (l8 & 1) + 2 * (l8 >> 1) : 4 * lane;
+  const int b1 = b0 + (out.permuted ? 8 : 2);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int col = 128 * c + 4 * lane;
-      if (col < out.L) store4(o + col, make_float4(acc[c].x * inv, acc[c].y * inv, acc[c].z * inv, acc[c].w * inv));
-    }
-  } else {
-#pragma unroll
-    for (int c = 0; c < kCols; ++c) {
-      const int col = 32 * c + lane;
-      if (col < out.L) store1(o + col, one[c] * inv);
+  for (int c = 0; c < kC; ++c) {
+    const int a = c0 + 128 * c;
+    if constexpr (kVec) {
+      if (a + 4 * lane < out.L) {
+        store2(o + a + b0, acc[c].x * inv, acc[c].y * inv);
+        store2(o + a + b1, acc[c].z * inv, acc[c].w * inv);
+      }
+    } else {
+      if (a + lane < out.L) store1(o + a + lane, acc[c].x * inv);
+      if (a + 32 + lane < out.L) store1(o + a + 32 + lane, acc[c].y * inv);
+      if (a + 64 + lane < out.L) store1(o + a + 64 + lane, acc[c].z * inv);
+      if (a + 96 + lane < out.L) store1(o + a + 96 + lane, acc[c].w * inv);
     }
   }
-  if (lane == 0 && out.lse != nullptr)
-    out.lse[(int64_t)(d.x + t) * out.H + h] = tot == 0.f ? -CUDART_INF_F : m + logf(tot);
+  if (c0 == 0 && lane == 0 && out.lse != nullptr)
+    out.lse[(int64_t)(tok0 + t) * out.H + h] = tot == 0.f ? -CUDART_INF_F : m + logf(tot);
+}
+
+template <typename T>
+cudaError_t launch_merge(const WindowSched& sched, const WindowOut& out, int units, cudaStream_t st) {
+  const bool vec = out.L % 4 == 0 && out.o_s0 % 4 == 0 && out.o_s1 % 4 == 0 &&
+                   reinterpret_cast<uintptr_t>(out.o) % (4 * sizeof(T)) == 0;
+  const bool by_item = sched.most < units;
+  const int64_t tiles = by_item ? sched.most : units - 1;
+  // whole rows a warp where that gives every SM eight warps (24 row tiles of 16 tiles: 31 us, 34 with
+  // quarters; one of 63: quarters)
+  const bool wide = out.L > 128 && tiles * out.rows >= 8 * (int64_t)device_sm_count();
+  const int cols = wide ? (out.L + 511) / 512 : (out.L + 127) / 128;
+  const dim3 grid((unsigned)tiles, (out.rows * cols + kMergeWarps - 1) / kMergeWarps);
+  auto kernel = wide ? (vec ? window_merge_kernel<T, true, 4> : window_merge_kernel<T, false, 4>)
+                     : (vec ? window_merge_kernel<T, true, 1> : window_merge_kernel<T, false, 1>);
+  return launch_k(kernel, grid, 32 * kMergeWarps, 0, st, sched, out, units, by_item);
 }
 
 // Row tiles at most: T tokens of B sequences, tpt a tile.
@@ -371,12 +441,12 @@ cudaError_t launch_window_schedule(const WindowCall& c, int tpt, int blocks_per_
   const int64_t tiles = (std::min<int64_t>(cap, (int64_t)s.window + tpt) / kBlk + 2 +
                          std::min<int64_t>(cap, s.sinks) / kBlk + 1 + blocks_per_tile - 1) / blocks_per_tile;
   const int cut_cost = blocks_per_tile == 2 ? kCutCost<2> : kCutCost<1>;
-  *sched = WindowSched{s.items, s.total, split ? s.unit_start : nullptr,
+  *sched = WindowSched{items, s.items, s.total, split ? s.unit_start : nullptr,
                        split && units > 1 && tiles > 1 && (items > units || tiles > 1 + cut_cost)};
   *out = WindowOut{c.o.data, c.o.s0, c.o.s1, c.lse, reinterpret_cast<float*>(base + w.o),
-                   reinterpret_cast<float*>(base + w.lse), rows, c.L, c.H, 0};
+                   reinterpret_cast<float*>(base + w.lse), rows, c.L, c.H, 0, false};
   if (split) {
-    const int64_t need = std::max<int64_t>({items, c.B, std::min(units + 1, 128)});
+    const int64_t need = std::max<int64_t>({items, c.B, 128});
     const int threads = (int)std::min<int64_t>(1024, (need + 31) / 32 * 32);
     return launch_k(blocks_per_tile == 2 ? window_split_kernel<2> : window_split_kernel<1>, 1, threads, 0, st, s);
   }
@@ -387,15 +457,7 @@ cudaError_t launch_window_schedule(const WindowCall& c, int tpt, int blocks_per_
 
 cudaError_t launch_window_merge(mla_dtype dt, const WindowSched& sched, const WindowOut& out, int units, cudaStream_t st) {
   if (!sched.cut) return cudaSuccess;
-  const dim3 grid(units - 1, (out.rows + kMergeWarps - 1) / kMergeWarps);
-  const size_t es = dt == MLA_F32 ? 4 : 2;
-  const bool vec = out.L % 4 == 0 && out.o_s0 % 4 == 0 && out.o_s1 % 4 == 0 &&
-                   reinterpret_cast<uintptr_t>(out.o) % (4 * es) == 0;
-  if (dt == MLA_F32)
-    return launch_k(vec ? window_merge_kernel<float, true> : window_merge_kernel<float, false>, grid, 32 * kMergeWarps,
-                    0, st, sched, out, units);
-  return launch_k(vec ? window_merge_kernel<__nv_bfloat16, true> : window_merge_kernel<__nv_bfloat16, false>, grid,
-                  32 * kMergeWarps, 0, st, sched, out, units);
+  return dt == MLA_F32 ? launch_merge<float>(sched, out, units, st) : launch_merge<__nv_bfloat16>(sched, out, units, st);
 }
 
 unsigned window_sched_errors_read_clear() {

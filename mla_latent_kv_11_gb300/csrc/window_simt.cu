@@ -1,14 +1,16 @@
 // Windowed attention on the CUDA cores: any head count, any entry width, any page, fp32 or bf16
 // (what the tensor-core kernel of attn_pair_tc.cu does not take).
 //
-// A block of 256 threads holds the queries of up to 16 heads of one token in shared memory and streams
-// the attended rows in sub-tiles of 32, as fp32. Each step is laid out for latency, which bounds these
+// A block of 256 threads holds the queries of up to kHeads heads of one token in shared memory and
+// streams the attended rows in sub-tiles of 32, as fp32. Each step is laid out for latency, which bounds
 // small cases: a warp loads whole rows, consecutive lanes on consecutive values, all its loads in
-// flight at once; for the scores a warp takes four heads and half of a row's width, a lane a key, four
+// flight at once; for the scores a warp takes four heads and a part of a row's width, a lane a key, four
 // values a load; for the output a thread owns two latent columns of every head. One pass with the
-// running maximum and sum of a softmax, all in fp32. A sub-tile takes 9 us, whatever is in it: five
-// float32 sequences of up to 104 attended rows, 16 heads, a half block a unit, take 37 us with schedule
-// and merge.
+// running maximum and sum of a softmax, all in fp32.
+//
+// Eight heads a block balance the loads of rows (again for every block of heads) against the products;
+// with fewer blocks than the SMs can hold, four are faster. Measured, with 16, 8 and 4 heads (fp32, 16
+// heads): 5 sequences of up to 104 attended rows 36, 29 and 23 us; 64 of 512 rows 143, 114 and 180.
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
@@ -21,7 +23,7 @@ namespace {
 
 __device__ unsigned g_window_simt_err = 0;
 
-constexpr int kHeads = 16, kKeys = 32, kThreads = 256;
+constexpr int kKeys = 32, kThreads = 256;
 
 __device__ __forceinline__ float ld(const float* p) { return *p; }
 __device__ __forceinline__ float ld(const __nv_bfloat16* p) { return __bfloat162float(*p); }
@@ -43,8 +45,12 @@ struct SimtArgs {
 // Pitch of a staged row: its width rounded up to four, plus four (lanes reading 16 bytes of
 // consecutive rows then hit different banks).
 __host__ __device__ inline int row_pitch(int E) { return (E + 3) / 4 * 4 + 4; }
-inline size_t simt_bytes(int E) {
-  return sizeof(float) * ((size_t)(kHeads + kKeys) * row_pitch(E) + 3 * kHeads * kKeys + 3 * kHeads);
+// Parts of a row's width that different warps take, for the scores.
+__host__ __device__ constexpr int parts(int heads) { return kThreads / 32 / (heads / 4); }
+template <int kHeads>
+size_t simt_bytes(int E) {
+  constexpr int kParts = parts(kHeads);
+  return sizeof(float) * ((size_t)(kHeads + kKeys) * row_pitch(E) + (kParts + 1) * kHeads * kKeys + 3 * kHeads);
 }
 
 // A row of E values into shared memory by one warp (zeros up to the pitch; all zeros without a source).
@@ -54,16 +60,17 @@ __device__ __forceinline__ void stage_row(float* dst, const T* src, int E, int P
   for (int e = lane; e < P; e += 32) dst[e] = src != nullptr && e < E ? ld(src + e) : 0.f;
 }
 
-template <typename T>
+template <typename T, int kHeads>
 __global__ void __launch_bounds__(kThreads) window_simt_kernel(SimtArgs a) {
+  constexpr int kParts = parts(kHeads);
   extern __shared__ __align__(16) float sm[];
   pdl_enter();
   const int L = a.out.L, E = L + a.R, P = row_pitch(E), H = a.out.H;
   float* const q = sm;
   float* const k = q + kHeads * P;
   float(*const part)[kHeads][kKeys] = reinterpret_cast<float(*)[kHeads][kKeys]>(k + kKeys * P);
-  float(*const w)[kKeys] = part[2];
-  float* const m = reinterpret_cast<float*>(part + 3);
+  float(*const w)[kKeys] = part[kParts];
+  float* const m = reinterpret_cast<float*>(part + kParts + 1);
   float* const l = m + kHeads;
   float* const alpha = l + kHeads;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -107,8 +114,9 @@ __global__ void __launch_bounds__(kThreads) window_simt_kernel(SimtArgs a) {
       }
       __syncthreads();
       {
-        // scores: heads 4 (warp % 4) .., half warp / 4 of the row, key `lane`
-        const int hq = 4 * (warp & 3), n4 = P / 4 - 1, e0 = (warp >> 2) * (n4 / 2), e1 = warp >> 2 ? n4 : n4 / 2;
+        // scores: heads hq .. hq + 3, part w of the row, key `lane`
+        const int hq = 4 * (warp % (kHeads / 4)), w = warp / (kHeads / 4), n4 = P / 4 - 1, e0 = w * n4 / kParts,
+                  e1 = (w + 1) * n4 / kParts;
         const float4* kr = reinterpret_cast<const float4*>(k + lane * P);
         const float4* qr = reinterpret_cast<const float4*>(q + hq * P);
         float s[4] = {0.f, 0.f, 0.f, 0.f};
@@ -122,13 +130,15 @@ __global__ void __launch_bounds__(kThreads) window_simt_kernel(SimtArgs a) {
           }
         }
 #pragma unroll
-        for (int h = 0; h < 4; ++h) part[warp >> 2][hq + h][lane] = s[h];
+        for (int h = 0; h < 4; ++h) part[w][hq + h][lane] = s[h];
       }
       __syncthreads();
 #pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {   // softmax: heads 2 warp, 2 warp + 1, key `lane`
-        const int h = 2 * warp + hh;
-        const float s = off >= 0 ? (part[0][h][lane] + part[1][h][lane]) * a.scale : -CUDART_INF_F;
+      for (int h = warp; h < kHeads; h += kThreads / 32) {   // softmax, key `lane`
+        float s = part[0][h][lane];
+#pragma unroll
+        for (int i = 1; i < kParts; ++i) s += part[i][h][lane];
+        s = off >= 0 ? s * a.scale : -CUDART_INF_F;
         float top = s;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -189,6 +199,14 @@ __global__ void __launch_bounds__(kThreads) window_simt_kernel(SimtArgs a) {
   }
 }
 
+template <typename T, int kHeads>
+cudaError_t launch_simt(const SimtArgs& a, int units, cudaStream_t st) {
+  const size_t bytes = simt_bytes<kHeads>(a.out.L + a.R);
+  const cudaError_t e = cudaFuncSetAttribute(window_simt_kernel<T, kHeads>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e != cudaSuccess) return e;
+  return launch_k(window_simt_kernel<T, kHeads>, dim3(units, (a.out.H + kHeads - 1) / kHeads), kThreads, bytes, st, a);
+}
+
 int simt_units(int num_splits) { return num_splits > 0 ? std::min(num_splits, kMaxUnits) : device_sm_count(); }
 
 }  // namespace
@@ -212,12 +230,13 @@ cudaError_t launch_window_simt(mla_dtype dt, const WindowCall& c, int num_splits
   a.window = c.window.window < 0x3fffffff ? c.window.window : 0x3fffffff;
   a.sinks = c.window.sinks;
   a.scale = c.scale;
-  const dim3 grid(units, (c.H + kHeads - 1) / kHeads);
-  const size_t bytes = simt_bytes(c.L + c.R);
-  auto kernel = dt == MLA_F32 ? window_simt_kernel<float> : window_simt_kernel<__nv_bfloat16>;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (e != cudaSuccess) return e;
-  e = launch_k(kernel, grid, kThreads, bytes, st, a);
+  // blocks of four heads that have work, at most: fewer than three an SM
+  const int64_t tiles = std::min<int64_t>((int64_t)c.max_blocks * c.cache.page, (int64_t)a.window + a.sinks) / kBlk + 3;
+  const bool few = a.sched.most * tiles * ((c.H + 3) / 4) <= 3 * (int64_t)device_sm_count();
+  if (dt == MLA_F32)
+    e = few ? launch_simt<float, 4>(a, units, st) : launch_simt<float, 8>(a, units, st);
+  else
+    e = few ? launch_simt<__nv_bfloat16, 4>(a, units, st) : launch_simt<__nv_bfloat16, 8>(a, units, st);
   if (e != cudaSuccess) return e;
   return launch_window_merge(dt, a.sched, a.out, units, st);
 }
