@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -32,6 +33,10 @@ class MlaError(RuntimeError):
 class MlaTensor(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("rank", ctypes.c_int32),
                 ("shape", ctypes.c_int64 * 4), ("stride", ctypes.c_int64 * 4)]
+
+
+# an MlaTensor's bytes by rank: packing them costs half of what filling the fields does
+_PACKED = [struct.Struct(f"Qi4x{r}q{8 * (4 - r)}x{r}q{8 * (4 - r)}x") for r in range(5)]
 
 
 _lib_handle: Optional[ctypes.CDLL] = None
@@ -107,10 +112,11 @@ def _check(status: int) -> None:
 
 def _dtype_code(*tensors) -> int:
     import torch
-    dts = {t.dtype for t in tensors if t is not None}
-    if len(dts) != 1:
-        raise MlaError(MLA_ERR_INVALID_ARG, f"tensors disagree on dtype: {sorted(map(str, dts))}")
-    dt = dts.pop()
+    dt = next(t for t in tensors if t is not None).dtype
+    for t in tensors:
+        if t is not None and t.dtype != dt:
+            dts = {t.dtype for t in tensors if t is not None}
+            raise MlaError(MLA_ERR_INVALID_ARG, f"tensors disagree on dtype: {sorted(map(str, dts))}")
     if dt == torch.float32:
         return MLA_F32
     if dt == torch.bfloat16:
@@ -121,9 +127,10 @@ def _dtype_code(*tensors) -> int:
 def as_mla_tensor(t) -> MlaTensor:
     """Describe a torch tensor (any strides) as an mla_tensor view."""
     shape = t.shape
-    if len(shape) > 4:
+    rank = len(shape)
+    if rank > 4:
         raise MlaError(MLA_ERR_INVALID_ARG, "rank > 4")
-    return MlaTensor(t.data_ptr() if t.numel() > 0 else None, len(shape), shape, t.stride())
+    return MlaTensor.from_buffer_copy(_PACKED[rank].pack(t.data_ptr() if t.numel() > 0 else 0, rank, *shape, *t.stride()))
 
 
 def _stream(stream) -> Optional[int]:
@@ -434,7 +441,7 @@ def _table_stride(block_table) -> int:
 def _check_lse(lse_out, q_cat) -> None:
     import torch
     if lse_out is not None and (lse_out.dtype != torch.float32 or not lse_out.is_contiguous() or
-                                tuple(lse_out.shape) != tuple(q_cat.shape[:2])):
+                                lse_out.shape != q_cat.shape[:2]):
         raise MlaError(MLA_ERR_INVALID_ARG, "lse_out must be contiguous float32 with q_cat's rows and heads")
 
 
