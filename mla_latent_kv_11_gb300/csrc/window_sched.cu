@@ -3,8 +3,9 @@
 // A prefill's tokens form row tiles of `tpt` tokens, a decode's sequences one each. Few queries over a
 // long axis keep every SM busy by being cut:
 //   - no more row tiles than work units: each gets units of its own, as many as make the longest piece
-//     shortest, but one where cutting gains less than the float32 partials and their merge cost
-//     (kCutCost; 64 sequences of 33 tensor-core tiles on 76 units: 82 us cut, 71 whole);
+//     shortest, but one where cutting gains less than the float32 pieces and their merge cost (cut_cost).
+//     Ranges of equal cost, as below, took 79 us for 64 sequences of 33 tensor-core tiles on 76 units,
+//     64 of them a sequence each 69;
 //   - up to kSplitItems row tiles: each unit gets a contiguous range of tiles of equal cost (a row
 //     tile costing its tiles plus kItemCost) and holds at most two cut row tiles, the end of one and the
 //     head of another;
@@ -24,19 +25,25 @@ namespace {
 __device__ unsigned g_window_err = 0;
 
 // In tiles, of kPer blocks each (a tensor-core tile takes 1.7 us, one on the CUDA cores ten times
-// that): what a row tile costs beside its tiles (a prefill of ragged prompts, 1 to 8 tensor-core tiles
-// a row tile, took 115 us with 2, 135 with 1), and what cutting adds to a unit's time (one sequence of 5
-// tiles: 14.3 us cut, 17.1 whole; 24 of 3: 20.8 cut, 18.1 whole).
+// that): what a row tile costs beside its tiles. A prefill of ragged prompts, 1 to 8 tensor-core tiles
+// a row tile, took 115 us with 2, 135 with 1.
 template <int kPer>
 constexpr int kItemCost = kPer == 2 ? 2 : 1;
+// What cutting evenly adds to a unit's time, in tiles: the merge's launch, and the float32 pieces written
+// and read, 4 KB a row (128 heads: one sequence of 3 tiles 11.2 us cut, 13.0 whole; 24 of 6 tiles 20.8
+// cut, 18.1 whole). On the CUDA cores a tile takes longer than that.
+constexpr int kMergeCost = 1, kRowsPerTile = 2048;
 template <int kPer>
-constexpr int kCutCost = kPer == 2 ? 3 : 0;
+__device__ __forceinline__ int cut_cost(int pieces, int rows) {
+  return kPer == 2 ? kMergeCost + pieces * rows / kRowsPerTile : 0;
+}
 constexpr int kSplitItems = 1024;   // row tiles up to which the schedule cuts them
 
 struct SchedArgs {
   const int32_t* cu_q;     // null: a decode, one token a sequence
   const int32_t* kv_lens;
   int B, T, cap, tpt, window, sinks, units;
+  int rows;                // of a full row tile
   int4* items;
   int32_t* total;
   int2* unit_start;
@@ -69,7 +76,7 @@ __device__ __forceinline__ int q_len(const SchedArgs& s, int b, int& q0) {
 }
 
 // Exclusive block scan of one int a thread (blockDim.x a multiple of 32).
-__device__ int scan_block(int v, int* warp_tot, int* total) {
+__device__ __noinline__ int scan_block(int v, int* warp_tot, int* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   int x = v;
 #pragma unroll
@@ -89,6 +96,20 @@ __device__ int scan_block(int v, int* warp_tot, int* total) {
   return before + x - v;
 }
 
+// The last i < n with v[i] <= x.
+__device__ __noinline__ int last_at_most(const int* v, int n, int x) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (v[mid] <= x) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// What bounds it is the fetching of its instructions, none of which are cached when it starts: a
+// straight run of them takes 2 us for every 300. So a decode skips what it does not need, scans and
+// searches are functions, and pieces start at multiples of their length.
+//
 // Up to kSplitItems row tiles: their descriptions, and the units' starts. One block; a thread a
 // sequence, then a thread a row tile, then a thread a unit.
 template <int kPer>
@@ -97,27 +118,31 @@ __global__ void __launch_bounds__(1024) window_split_kernel(SchedArgs s) {
       cost[kSplitItems + 1], tiles[kSplitItems], longest[32];
   pdl_enter();
   const int i = threadIdx.x;
-  int n = 0, q0 = 0, k = 0, total;
-  if (i < s.B) k = q_len(s, i, q0);
-  if (__syncthreads_or(k < 0)) k = 0;
-  if (i < s.B) {
-    n = (k + s.tpt - 1) / s.tpt;
-    q_begin[i] = q0;
-    q_count[i] = k;
-    len[i] = kv_len(s, i);
-  }
-  const int ex = scan_block(n, warp_tot, &total);
-  if (i < s.B) first[i] = ex;
-  __syncthreads();
-  int nt = 0;
-  if (i < total) {
-    int lo = 0, hi = s.B - 1;   // the last sequence with first <= i: it has row tiles
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (first[mid] <= i) lo = mid; else hi = mid - 1;
+  int nt = 0, total;
+  Item it;
+  if (s.cu_q == nullptr) {
+    total = s.B;
+    if (i < total) it = make_item(i, 1, kv_len(s, i) - 1, i, s.window, s.sinks);
+  } else {
+    int n = 0, q0 = 0, k = 0;
+    if (i < s.B) k = q_len(s, i, q0);
+    if (__syncthreads_or(k < 0)) k = 0;
+    if (i < s.B) {
+      n = (k + s.tpt - 1) / s.tpt;
+      q_begin[i] = q0;
+      q_count[i] = k;
+      len[i] = kv_len(s, i);
     }
-    const int t0 = (i - first[lo]) * s.tpt, ntok = min(s.tpt, q_count[lo] - t0);
-    const Item it = make_item(q_begin[lo] + t0, ntok, len[lo] - q_count[lo] + t0, lo, s.window, s.sinks);
+    const int ex = scan_block(n, warp_tot, &total);
+    if (i < s.B) first[i] = ex;
+    __syncthreads();
+    if (i < total) {
+      const int b = last_at_most(first, s.B, i);   // it has row tiles
+      const int t0 = (i - first[b]) * s.tpt;
+      it = make_item(q_begin[b] + t0, min(s.tpt, q_count[b] - t0), len[b] - q_count[b] + t0, b, s.window, s.sinks);
+    }
+  }
+  if (i < total) {
     store_item(s.items, i, it);
     nt = item_tiles<kPer>(it.b.w);
   }
@@ -135,40 +160,41 @@ __global__ void __launch_bounds__(1024) window_split_kernel(SchedArgs s) {
   if ((i & 31) == 0) longest[i >> 5] = top;
   __syncthreads();
   if (total <= s.units) {
-    // pieces of at most `lo` tiles: the least `lo` whose pieces the units can take, between sum / units
-    // and sum / (units - total). Every warp tries one, evenly between the bounds
     const int lane = i & 31, warp = i >> 5, warps = blockDim.x >> 5;
-    const int whole = max(1, __reduce_max_sync(0xffffffffu, longest[lane]));   // the longest row tile
-    int lo = min(whole, max(1, (sum + s.units - 1) / s.units)), hi = whole;
-    if (s.units > total) hi = max(lo, min(hi, (sum + s.units - total - 1) / (s.units - total)));
-    while (lo < hi) {
-      const int step = max(1, (hi - lo) / warps), most = min(hi, lo + warp * step);
-      int pieces = 0;
-      for (int t = lane; t < total; t += 32) pieces += (tiles[t] + most - 1) / most;
-      pieces = __reduce_add_sync(0xffffffffu, pieces);
-      if (lane == 0) warp_tot[warp] = pieces <= s.units;
-      __syncthreads();
-      int fit = 0;   // the first warp whose pieces fit
-      while (fit < warps && !warp_tot[fit]) ++fit;
-      __syncthreads();
-      if (fit < warps) hi = min(hi, lo + fit * step);
-      if (fit > 0) lo = min(hi, lo + (fit - 1) * step + 1);
+    const int whole = __reduce_max_sync(0xffffffffu, longest[lane]);   // the longest row tile
+    int first_unit = i, pieces = total, piece = 0;
+    if (whole > 1 + cut_cost<kPer>(0, 0)) {
+      // pieces of at most `lo` tiles: the least `lo` whose pieces the units can take, between sum / units
+      // and sum / (units - total). Every warp tries one, evenly between the bounds
+      int lo = min(whole, (sum + s.units - 1) / s.units), hi = whole;
+      if (s.units > total) hi = max(lo, min(hi, (sum + s.units - total - 1) / (s.units - total)));
+      while (lo < hi) {
+        const int step = max(1, (hi - lo) / warps), most = min(hi, lo + warp * step);
+        int k = 0;
+        for (int t = lane; t < total; t += 32) k += (tiles[t] + most - 1) / most;
+        k = __reduce_add_sync(0xffffffffu, k);
+        if (lane == 0) warp_tot[warp] = k <= s.units;
+        __syncthreads();
+        int fit = 0;   // the first warp whose pieces fit
+        while (fit < warps && !warp_tot[fit]) ++fit;
+        __syncthreads();
+        if (fit < warps) hi = min(hi, lo + fit * step);
+        if (fit > 0) lo = min(hi, lo + (fit - 1) * step + 1);
+      }
+      piece = lo;
+      first_unit = scan_block(i < total ? (nt + lo - 1) / lo : 0, warp_tot, &pieces);
+      if (lo + cut_cost<kPer>(pieces, s.rows) >= whole) {
+        first_unit = i;
+        pieces = total;
+      }
     }
-    const int n = i < total ? (lo + kCutCost<kPer> < whole ? (nt + lo - 1) / lo : 1) : 0;
-    int pieces;
-    const int first_unit = scan_block(n, warp_tot, &pieces);
     if (i < total) cost[i] = first_unit;
     __syncthreads();
     for (int u = i; u <= s.units; u += blockDim.x) {
       int2 start = make_int2(total, 0);
       if (u < pieces) {
-        int a = 0, b = total - 1;   // the last row tile with first unit <= u
-        while (a < b) {
-          const int mid = (a + b + 1) >> 1;
-          if (cost[mid] <= u) a = mid; else b = mid - 1;
-        }
-        const int k = (a + 1 < total ? cost[a + 1] : pieces) - cost[a];
-        start = make_int2(a, (int)((long long)tiles[a] * (u - cost[a]) / k));
+        start.x = last_at_most(cost, total, u);
+        start.y = (u - cost[start.x]) * piece;
       }
       s.unit_start[u] = start;
     }
@@ -180,11 +206,7 @@ __global__ void __launch_bounds__(1024) window_split_kernel(SchedArgs s) {
     int2 start = make_int2(total, 0);
     if (u < active && total > 0) {
       const int x = (int)((long long)u * all / active);
-      int lo = 0, hi = total - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (cost[mid] <= x) lo = mid; else hi = mid - 1;
-      }
+      const int lo = last_at_most(cost, total, x);
       const int into = max(0, x - cost[lo] - kItemCost<kPer>);
       start = into >= tiles[lo] ? make_int2(lo + 1, 0) : make_int2(lo, into);
     }
@@ -431,7 +453,7 @@ cudaError_t launch_window_schedule(const WindowCall& c, int tpt, int blocks_per_
   constexpr int kFar = 0x3fffffff;   // positions stay below this
   const int cap = (int)std::min<int64_t>((int64_t)c.max_blocks * c.cache.page, kFar);
   SchedArgs s{c.cu_q, c.kv_lens, c.B, (int)c.q.n0, cap, tpt, std::min(c.window.window, kFar),
-              std::min(c.window.sinks, kFar), units, reinterpret_cast<int4*>(base + w.items),
+              std::min(c.window.sinks, kFar), units, c.H * tpt, reinterpret_cast<int4*>(base + w.items),
               reinterpret_cast<int32_t*>(base + w.total), reinterpret_cast<int2*>(base + w.starts),
               reinterpret_cast<int32_t*>(base + w.prefix)};
   // cut row tiles while their tiles can be counted in 32 bits
@@ -440,9 +462,8 @@ cudaError_t launch_window_schedule(const WindowCall& c, int tpt, int blocks_per_
   // tiles of a row tile at most; whether any can be cut
   const int64_t tiles = (std::min<int64_t>(cap, (int64_t)s.window + tpt) / kBlk + 2 +
                          std::min<int64_t>(cap, s.sinks) / kBlk + 1 + blocks_per_tile - 1) / blocks_per_tile;
-  const int cut_cost = blocks_per_tile == 2 ? kCutCost<2> : kCutCost<1>;
   *sched = WindowSched{items, s.items, s.total, split ? s.unit_start : nullptr,
-                       split && units > 1 && tiles > 1 && (items > units || tiles > 1 + cut_cost)};
+                       split && units > 1 && tiles > 1 && (items > units || tiles > 1 + (blocks_per_tile == 2 ? kMergeCost : 0))};
   *out = WindowOut{c.o.data, c.o.s0, c.o.s1, c.lse, reinterpret_cast<float*>(base + w.o),
                    reinterpret_cast<float*>(base + w.lse), rows, c.L, c.H, 0, false};
   if (split) {
