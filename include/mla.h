@@ -13,7 +13,9 @@
  * and mla_prefill is step 4 for many causal queries per sequence. Fused forms:
  * mla_concat_q_cache_write (steps 2 and 3 in one launch), mla_absorb_concat_cache_write
  * (steps 1 to 3 in one call, the copies alongside the absorb) and mla_decode_v_up (step 4
- * with step 5 in its combine).
+ * with step 5 in its combine). mla_decode_window and mla_prefill_window are step 4 limited to
+ * a sliding window and attention sinks; mla_cache_write_ds_mla is step 3 into quantised
+ * entries, and mla_cache_read, _fp8 and _ds_mla read cache rows back.
  *
  * Sources of the operations (web pages):
  *   [vt]    vllm.cpp, tests/vt/test_ops_mla_absorb.cpp (BatchedMatmul and

@@ -34,8 +34,8 @@
 // groups) a barrier, warp 3 the W boxes, rope and queries (TMA; with one warp for all, issuing the
 // loads took longer than the MMAs); warp 1 of the first CTA issues every MMA; warp 2 owns the tensor
 // memory; warps 4..11 run the softmax, the rescaling of O and the epilogue, two threads a lane. A row
-// tile's output is parked in tensor memory as bf16 and stored under the next tile's MMAs: a row's
-// stores leave an SM at 16 to 19 bytes a cycle, 3000 to 4000 cycles a row tile.
+// tile's output is parked in tensor memory as bf16 and stored under the next tiles' MMAs, in whole
+// lines: its 64 KB take an SM 2100 cycles at its 31 bytes a cycle.
 //
 // Work. A row tile's key tiles are cut over the clusters where that shortens the longest one's list
 // (window_sched.cu); the pieces' float32 outputs and log-sum-exps are joined by a second kernel.
@@ -44,10 +44,13 @@
 //   prefill of 4 x 1024 tokens, 128 heads, window 2048: 1.43 ms, 1.57 PFLOP/s, 82% of a dense library
 //     product's rate. A tile takes 2100 cycles a cluster, its MMAs 1856 of them; shared memory moves
 //     363 KB a tile and CTA meanwhile.
-//   decode of 64 sequences of 1K to 16K rows, 128 heads, window 4096: 70 us, 4.2 TB/s; 5.9 TB/s between
-//     a start of 11 us (schedule, first loads) and a tail (cut rows' outputs and their merge).
-//   prefill of ragged prompts, 64 heads, window 777: 113 us for 82 GFLOP, bounded by what a row tile
-//     costs beside its 1 to 8 tiles (its queries' load, the pipeline's filling, its output).
+//   decode of 64 sequences of 1K to 16K rows, 128 heads, window 4096: 69.5 us, 4.2 TB/s; 6 TB/s between
+//     a start of 11 us (schedule, first loads) and the last outputs.
+//   prefill of ragged prompts, 64 heads, window 777: 109 us for 82 GFLOP, bounded by what a row tile
+//     costs beside its 1 to 8 tiles (its queries' load, the pipeline's filling, its output: 4500 cycles
+//     against 2350 a tile).
+//   7 tokens over 16K rows, 128 heads: 40 us for 31 GFLOP: 11 to 12 tiles a cluster, the rest schedule,
+//     start, float32 pieces and their merge.
 //
 // Every wait is bounded; one that gives up winds both CTAs down and is reported.
 #include <cuda.h>
@@ -88,7 +91,7 @@ struct PairCfg {
   static constexpr int kOffKV = kOffP + 2 * kBox;          // [2 tiles][H0, H1][4 boxes]
   static constexpr int kOffR = kOffKV + 2 * 8 * kBox;
   static constexpr int kOffMisc = kOffR + (kRope ? kBox : 0);
-  static constexpr int kMiscBytes = 3072;
+  static constexpr int kMiscBytes = 3 * 1024;
   static constexpr int kSmemAlloc = kOffMisc + kMiscBytes;
 };
 
@@ -110,7 +113,7 @@ struct PairShared {
   // [lane]: the maxima of a tile, at a segment's end the weights' sums
   float red[2][2][128];
 };
-static_assert(sizeof(PairShared) <= 3072, "barrier block overflows its slot");
+static_assert(sizeof(PairShared) <= PairCfg<64>::kMiscBytes, "barrier block overflows its slot");
 
 struct PairParams {
   int H, tpt, tptc;          // heads, tokens per row tile, tokens per CTA (heads split when H > 64: tptc 0)
