@@ -274,6 +274,26 @@ __device__ __forceinline__ void st_global_32B(void* dst, const uint32_t* w) {
                : "memory");
 }
 
+// Two float32 in one register pair, and arithmetic on both at once.
+__device__ __forceinline__ uint64_t pair_f32(float a, float b) {
+  return (uint64_t)__float_as_uint(b) << 32 | __float_as_uint(a);
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // 16 lanes x 32 columns of tensor memory: w[4 k + 2 j + i] of lane t is row 8 j + t / 4, column
 // 8 k + 2 (t % 4) + i.
 __device__ __forceinline__ void tmem_ld_16x32(uint32_t addr, uint32_t* w) {
@@ -659,10 +679,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         float mx[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) mx[k] = sv[k];
+        for (int k = 0; k < 4; ++k) mx[k] = max3(sv[k], sv[4 + 2 * k], sv[5 + 2 * k]);
 #pragma unroll
-        for (int k = 4; k < 32; ++k) mx[k & 3] = fmaxf(mx[k & 3], sv[k]);
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        for (int k = 12; k < 28; k += 2) mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], sv[k], sv[k + 1]);
+        const float top = max3(max3(mx[0], mx[1], sv[28]), max3(mx[2], mx[3], sv[29]), fmaxf(sv[30], sv[31]));
         sh.red[x][part][ln] = top;
         ok = group_all(mine);                // the one group decision of a tile; the row's four maxima
         if (!ok) break;
@@ -677,16 +697,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const float ref = m == -CUDART_INF_F ? 0.f : -m;
         l *= alpha;
         uint32_t pk[16];
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint64_t by = pair_f32(p.scale_log2, p.scale_log2), from = pair_f32(ref, ref);
+        uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int k = 0; k < 32; k += 2) {
-          const float e0 = ex2_approx(fmaf(sv[k], p.scale_log2, ref));
-          const float e1 = ex2_approx(fmaf(sv[k + 1], p.scale_log2, ref));
-          sum[(k >> 1) & 3] += e0 + e1;
+          const uint64_t x = fma_pair(pair_f32(sv[k], sv[k + 1]), by, from);
+          const float e0 = ex2_approx(__uint_as_float((uint32_t)x)), e1 = ex2_approx(__uint_as_float((uint32_t)(x >> 32)));
+          sum[(k >> 1) & 3] = add_pair(sum[(k >> 1) & 3], pair_f32(e0, e1));
           const __nv_bfloat162 h = __floats2bfloat162_rn(e0, e1);
           pk[k >> 1] = *reinterpret_cast<const uint32_t*>(&h);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        const uint64_t all = add_pair(add_pair(sum[0], sum[1]), add_pair(sum[2], sum[3]));
+        l += __uint_as_float((uint32_t)all) + __uint_as_float((uint32_t)(all >> 32));
         // P(g) takes P(g - 1)'s place and O is rescaled once PV(g - 1) is done
         if (g > 0) mine = mine && wait_for(&sh.pv_done[b ^ 1][3], ((g - 1) >> 1) & 1, abort);
         tc_fence_after();
