@@ -134,8 +134,9 @@ struct PairParams {
 // value), none (0, 0) behind the last. Values that come from memory are not uniform to the compiler,
 // and under a branch on them it forms every operand of the MMAs and loads in vector registers (an MMA
 // then took 75 cycles to issue, a load 300); the results of a reduction over the warp are.
-__device__ __forceinline__ int open_segment(Walker<2>& wk, Seg& s, int& first) {
-  const bool any = wk.next(s);
+template <bool kDirect>
+__device__ __forceinline__ int open_segment(const WindowSched& sched, Walker<2, kDirect>& wk, Seg& s, int& first) {
+  const bool any = wk.next(sched, s, &g_pair_err);
   first = __reduce_max_sync(0xffffffffu, any ? s.t0 : 0);
   return __reduce_max_sync(0xffffffffu, any ? s.t1 : 0);
 }
@@ -305,8 +306,8 @@ __device__ __forceinline__ void tmem_ld_16x32(uint32_t addr, uint32_t* w) {
       : "r"(addr));
 }
 
-// kSmall: pages of less than 64 rows.
-template <int kRope, bool kSmall>
+// kSmall: pages of less than 64 rows. kDirect: a direct schedule.
+template <int kRope, bool kSmall, bool kDirect>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     window_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap kvmap, const __grid_constant__ CUtensorMap qmap,
                        const PairParams p) {
@@ -361,14 +362,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // warp walks the tiles. Lane h looks up the block id of a tile's block h (small pages: lanes
     // 8h .. 8h + 7 the ids of its pages).
     const int rows_box = kSmall ? p.page : kBlk, subs = kBlk / rows_box;
-    Walker<2> wk;
-    wk.init(p.sched, unit, units);
+    Walker<2, kDirect> wk;
+    wk.init(p.sched, unit, units, &g_pair_err);
     Seg sg;
     bool ok = true;
     int j = 0, nt = 0;   // next tile of the open segment, its end; both warp-uniform
     bool fresh = true;
     auto open = [&]() {
-      nt = open_segment(wk, sg, j);
+      nt = open_segment(p.sched, wk, sg, j);
       fresh = true;
     };
     open();
@@ -535,8 +536,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t dq = desc_lo(sQ, 16), dp = desc_lo(sP, 16), dk = desc_lo(sKV, 16), dv = desc_lo(sKV, kBox),
                    dr = desc_lo(sR, 16);
     constexpr int kStep = kBox / 16;   // one box, in a descriptor's 16-byte units
-    Walker<2> wk;
-    wk.init(p.sched, unit, units);
+    Walker<2, kDirect> wk;
+    wk.init(p.sched, unit, units, &g_pair_err);
     Seg sg;
     int g = 0, seg_i = 0;
     bool ok = true, pv_first = true;   // pv_first: the pending PV starts its segment's O
@@ -584,7 +585,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         commit_pair(&sh.pv_done[b][i]);
       }
     };
-    int t0 = 0, t1 = open_segment(wk, sg, t0);
+    int t0 = 0, t1 = open_segment(p.sched, wk, sg, t0);
     while (ok && t0 < t1) {
       for (int j = t0; ok && j < t1; ++j, ++g) {
         if (j == t0) {
@@ -601,7 +602,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       ++seg_i;
-      t1 = open_segment(wk, sg, t0);
+      t1 = open_segment(p.sched, wk, sg, t0);
     }
     if (ok && g > 0) pv(g - 1);
     if (!ok && lane == 0) give_up();
@@ -620,8 +621,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int head = p.tptc ? row % p.H : 64 * (int)rank + row;
     const bool real = p.tptc ? row < p.tptc * p.H : head < p.H;
     auto group_all = [](bool v) { return named_bar_and(kSoftmaxBar, kSoftmaxThreads, v); };
-    Walker<2> wk;
-    wk.init(p.sched, unit, units);
+    Walker<2, kDirect> wk;
+    wk.init(p.sched, unit, units, &g_pair_err);
     Seg sg;
     // The output that waits in tensor memory: quarters left of this warp's 32 rows x 128 columns, this
     // lane's row. A quarter is 16 rows x 64 columns, whole lines of 128 bytes: an SM stores those at 31
@@ -654,7 +655,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     };
     int g = 0, x = 0;              // x: which of the two places the next exchange between the rows' threads takes
     bool ok = true, mine = true;   // ok: the group's decision; mine: this thread's waits so far
-    bool more = wk.next(sg);
+    bool more = wk.next(p.sched, sg, &g_pair_err);
     while (ok && more) {
       const bool valid = real && tok < sg.ntok;
       const int pos = valid ? sg.pos0 + tok : -1;       // -1 attends nothing
@@ -777,7 +778,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           p.out.lse[orow * p.H + head] = lse;
       }
       while (left > 0) store_quarter();
-      more = wk.next(sg);
+      more = wk.next(p.sched, sg, &g_pair_err);
       const int last = g - 1;
       mine = mine && wait_for(&sh.pv_done[last & 1][3], (last >> 1) & 1, abort);
       tc_fence_after();
@@ -860,7 +861,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync();
 }
 
-template <int kRope, bool kSmall>
+template <int kRope, bool kSmall, bool kDirect>
 int max_pairs() {
   static std::mutex mu;
   static std::vector<int> cache;
@@ -870,7 +871,7 @@ int max_pairs() {
   if ((int)cache.size() <= dev) cache.resize(dev + 1, 0);
   if (cache[dev] == 0) {
     using C = PairCfg<kRope>;
-    cudaFuncSetAttribute(window_attn_kernel<kRope, kSmall>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemAlloc);
+    cudaFuncSetAttribute(window_attn_kernel<kRope, kSmall, kDirect>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemAlloc);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * device_sm_count(), 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
@@ -883,7 +884,7 @@ int max_pairs() {
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, window_attn_kernel<kRope, kSmall>, &cfg) != cudaSuccess || n <= 0)
+    if (cudaOccupancyMaxActiveClusters(&n, window_attn_kernel<kRope, kSmall, kDirect>, &cfg) != cudaSuccess || n <= 0)
       n = device_sm_count() / 2;
     cudaGetLastError();
     cache[dev] = n;
@@ -891,18 +892,24 @@ int max_pairs() {
   return cache[dev];
 }
 
-template <int kRope, bool kSmall>
+template <int kRope, bool kSmall, bool kDirect>
 cudaError_t launch_attn(const PairParams& p, const WindowMaps& maps, int units, cudaStream_t st) {
   using C = PairCfg<kRope>;
-  const cudaError_t e = cudaFuncSetAttribute(window_attn_kernel<kRope, kSmall>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  const cudaError_t e = cudaFuncSetAttribute(window_attn_kernel<kRope, kSmall, kDirect>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              C::kSmemAlloc);
   if (e != cudaSuccess) return e;
-  return launch_k(window_attn_kernel<kRope, kSmall>, dim3(2 * units), dim3(kThreads), C::kSmemAlloc, st, maps.keys, maps.boxes,
+  return launch_k(window_attn_kernel<kRope, kSmall, kDirect>, dim3(2 * units), dim3(kThreads), C::kSmemAlloc, st, maps.keys, maps.boxes,
                   maps.q, p);
 }
 
+template <int kRope, bool kSmall>
+cudaError_t launch_page(const PairParams& p, const WindowMaps& maps, int units, cudaStream_t st) {
+  return p.sched.direct ? launch_attn<kRope, kSmall, true>(p, maps, units, st)
+                        : launch_attn<kRope, kSmall, false>(p, maps, units, st);
+}
+
 int pair_units(int num_splits) {
-  return num_splits > 0 ? std::min(num_splits, kMaxUnits) : max_pairs<64, false>();
+  return num_splits > 0 ? std::min(num_splits, kMaxUnits) : max_pairs<64, false, false>();
 }
 
 int pair_tokens(int H) { return H > 64 ? 1 : 2 * (64 / H); }
@@ -985,13 +992,13 @@ cudaError_t launch_window_tc(const WindowCall& c, const WindowMaps& maps, int nu
   p.num_blocks = c.cache.num_blocks;
   p.block_table = c.block_table;
   p.bt_stride = c.bt_stride;
-  p.prefetch = p.sched.unit_start != nullptr;
+  p.prefetch = p.sched.direct || p.sched.unit_start != nullptr;
   p.q_whole = q_whole(c.H);
   p.o_32B = reinterpret_cast<uintptr_t>(c.o.data) % 32 == 0 && c.o.s0 % 16 == 0 && c.o.s1 % 16 == 0;
   if (p.page < kBlk)
-    e = c.R == 64 ? launch_attn<64, true>(p, maps, units, st) : launch_attn<0, true>(p, maps, units, st);
+    e = c.R == 64 ? launch_page<64, true>(p, maps, units, st) : launch_page<0, true>(p, maps, units, st);
   else
-    e = c.R == 64 ? launch_attn<64, false>(p, maps, units, st) : launch_attn<0, false>(p, maps, units, st);
+    e = c.R == 64 ? launch_page<64, false>(p, maps, units, st) : launch_page<0, false>(p, maps, units, st);
   if (e != cudaSuccess) return e;
   return launch_window_merge(MLA_BF16, p.sched, p.out, units, st);
 }

@@ -9,7 +9,8 @@
 //   - up to kSplitItems row tiles: each unit gets a contiguous range of tiles of equal cost (a row
 //     tile costing its tiles plus kItemCost) and holds at most two cut row tiles, the end of one and the
 //     head of another;
-//   - more row tiles balance by themselves and are dealt out whole.
+//   - more row tiles balance by themselves and are dealt out whole;
+//   - so are a decode's of so short a window that none would be cut, without a schedule.
 // A unit has two partial slots. The schedule depends on the lengths and the number of units alone:
 // results repeat bit for bit.
 #include <cuda_bf16.h>
@@ -50,14 +51,7 @@ struct SchedArgs {
   int32_t* prefix;         // [B + 1] row tiles before each sequence (many row tiles only)
 };
 
-__device__ __forceinline__ int kv_len(const SchedArgs& s, int b) {
-  int n = s.kv_lens[b];
-  if (n < 0 || n > s.cap) {
-    atomicOr(&g_window_err, kErrDeviceData);
-    n = n < 0 ? 0 : s.cap;
-  }
-  return n;
-}
+__device__ __forceinline__ int kv_len(const SchedArgs& s, int b) { return mla::kv_len(s.kv_lens, s.cap, b, &g_window_err); }
 
 // Query tokens of sequence b; -1 (and reported) where cu_q leaves [0, T] or decreases. Nothing is
 // computed then: only an ascending cu_q keeps the row tiles within the room for them.
@@ -459,13 +453,18 @@ cudaError_t launch_window_schedule(const WindowCall& c, int tpt, int blocks_per_
   // cut row tiles while their tiles can be counted in 32 bits
   const int64_t seen = std::min<int64_t>(cap, (int64_t)s.window + s.sinks) / kBlk + 4;
   const bool split = items <= kSplitItems && c.B <= kSplitItems && items * seen < (int64_t)1 << 30;
-  // tiles of a row tile at most; whether any can be cut
-  const int64_t tiles = (std::min<int64_t>(cap, (int64_t)s.window + tpt) / kBlk + 2 +
-                         std::min<int64_t>(cap, s.sinks) / kBlk + 1 + blocks_per_tile - 1) / blocks_per_tile;
+  // tiles of a row tile at most; whether any can be cut. A decode of which none would be, whatever its
+  // lengths, needs no schedule (one 64-row sequence: 9.2 us with one)
+  const int64_t blocks = std::min<int64_t>((cap + (int64_t)kBlk - 1) / kBlk,
+                                           ((int64_t)s.window + tpt + kBlk - 3) / kBlk + 1 + (s.sinks + (int64_t)kBlk - 1) / kBlk);
+  const int64_t tiles = (blocks + blocks_per_tile - 1) / blocks_per_tile, least = 1 + (blocks_per_tile == 2 ? kMergeCost : 0);
+  const bool direct = decode && blocks_per_tile == 2 && tiles <= least;
   *sched = WindowSched{items, s.items, s.total, split ? s.unit_start : nullptr,
-                       split && units > 1 && tiles > 1 && (items > units || tiles > 1 + (blocks_per_tile == 2 ? kMergeCost : 0))};
+                       split && !direct && units > 1 && tiles > 1 && (items > units || tiles > least), direct, c.kv_lens,
+                       c.B, cap, s.window, s.sinks};
   *out = WindowOut{c.o.data, c.o.s0, c.o.s1, c.lse, reinterpret_cast<float*>(base + w.o),
                    reinterpret_cast<float*>(base + w.lse), rows, c.L, c.H, 0, false};
+  if (direct) return cudaSuccess;
   if (split) {
     const int64_t need = std::max<int64_t>({items, c.B, 128});
     const int threads = (int)std::min<int64_t>(1024, (need + 31) / 32 * 32);

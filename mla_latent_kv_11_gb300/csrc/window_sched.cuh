@@ -40,6 +40,16 @@ __device__ __forceinline__ int item_tiles(int nblk) {
   return nblk > 0 ? (nblk + kPer - 1) / kPer : 1;
 }
 
+// Rows of sequence b in the cache; a length beyond the table is cut to it (and reported in *err).
+__device__ __forceinline__ int kv_len(const int32_t* lens, int cap, int b, unsigned* err) {
+  int n = lens[b];
+  if (n < 0 || n > cap) {
+    atomicOr(err, kErrDeviceData);
+    n = n < 0 ? 0 : cap;
+  }
+  return n;
+}
+
 // A part of a row tile: tiles [t0, t1).
 struct Seg {
   int tok0, ntok, pos0, b;   // first token's row, tokens, its position, sequence
@@ -53,17 +63,26 @@ __device__ __forceinline__ int block_row(const Seg& s, int j) {
   return j >= s.nblk ? -1 : kBlk * (j < s.nsb ? j : s.wb + (j - s.nsb));
 }
 
-// The segments of one work unit, in tiles of kPer blocks.
-template <int kPer>
+// The segments of one work unit, in tiles of kPer blocks. kDirect: the schedule is (an instance of the
+// kernels of its own: the more code in the roles' loops, the slower they fetch it).
+template <int kPer, bool kDirect>
 struct Walker {
-  const int4* items;
   int unit, item, step, end_item, end_tile, tile;
   Item ahead;   // the next row tile, loaded while the one before it runs
 
-  __device__ void init(const WindowSched& s, int unit_, int units) {
-    items = s.items;
+  __device__ Item load(const WindowSched& s, int i, unsigned* err) const {
+    if constexpr (kDirect) return make_item(i, 1, kv_len(s.kv_lens, s.cap, i, err) - 1, i, s.window, s.sinks);
+    return load_item(s.items, i);
+  }
+  __device__ void init(const WindowSched& s, int unit_, int units, unsigned* err) {
     unit = unit_;
-    if (s.unit_start != nullptr) {
+    if constexpr (kDirect) {
+      item = unit;
+      tile = 0;
+      end_item = s.B;
+      end_tile = 0;
+      step = units;
+    } else if (s.unit_start != nullptr) {
       const int2 a = s.unit_start[unit], e = s.unit_start[unit + 1];
       item = a.x;
       tile = a.y;
@@ -77,12 +96,12 @@ struct Walker {
       end_item = -1;
       end_tile = 0;
     }
-    if (more()) ahead = load_item(items, item);
+    if (more()) ahead = load(s, item, err);
   }
   __device__ bool more() const {
     return step > 0 ? (item < end_item || (item == end_item && tile < end_tile)) : item >= 0;
   }
-  __device__ bool next(Seg& s) {
+  __device__ bool next(const WindowSched& sched, Seg& s, unsigned* err) {
     if (!more()) return false;
     s.tok0 = ahead.a.x;
     s.ntok = ahead.a.y;
@@ -99,7 +118,7 @@ struct Walker {
     s.slot = s.t0 == 0 && s.t1 == nt ? -1 : 2 * unit + (s.t0 == 0 ? 1 : 0);
     item += step;
     tile = 0;
-    if (more()) ahead = load_item(items, item);
+    if (more()) ahead = load(sched, item, err);
     return true;
   }
 };

@@ -75,10 +75,10 @@ __global__ void __launch_bounds__(kThreads) window_simt_kernel(SimtArgs a) {
   float* const alpha = l + kHeads;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int h0 = blockIdx.y * kHeads, hn = min(kHeads, H - h0);
-  Walker<1> wk;
-  wk.init(a.sched, blockIdx.x, gridDim.x);
+  Walker<1, false> wk;
+  wk.init(a.sched, blockIdx.x, gridDim.x, &g_window_simt_err);
   Seg sg;
-  while (wk.next(sg)) {
+  while (wk.next(a.sched, sg, &g_window_simt_err)) {
     __syncthreads();   // the last segment's sums are read
     for (int h = warp; h < kHeads; h += kThreads / 32)
       stage_row(q + h * P,
