@@ -41,9 +41,10 @@
 // (window_sched.cu); the pieces' float32 outputs and log-sum-exps are joined by a second kernel.
 //
 // What bounds it and what it measured (152 SMs, 76 clusters):
-//   prefill of 4 x 1024 tokens, 128 heads, window 2048: 1.43 ms, 1.57 PFLOP/s, 82% of a dense library
-//     product's rate. A tile takes 2100 cycles a cluster, its MMAs 1856 of them; shared memory moves
-//     363 KB a tile and CTA meanwhile.
+//   prefill of 4 x 1024 tokens, 128 heads, window 2048: 1.40 to 1.44 ms, 1.6 PFLOP/s, 83% of a dense
+//     library product's rate. A tile takes some 3200 cycles a cluster, its MMAs 2176 of them. Shared
+//     memory holds two tiles of keys, so the next but one waits for PV to leave its place, for its load
+//     (1400 cycles: the 64 KB a CTA come at 50 bytes a cycle), for its QK, which PV then follows.
 //   decode of 64 sequences of 1K to 16K rows, 128 heads, window 4096: 69.5 us, 4.2 TB/s; 6 TB/s between
 //     a start of 11 us (schedule, first loads) and the last outputs.
 //   prefill of ragged prompts, 64 heads, window 777: 109 us for 82 GFLOP, bounded by what a row tile

@@ -419,6 +419,34 @@ def test_the_default_stream_by_number(mla):
     wr.check(*decode(mla, c, stream=0), c.want(), 2)
 
 
+@pytest.mark.parametrize("dtype,heads,latent,rope,batch", [("f32", 16, 501, 3, 90), ("f32", 16, 500, 8, 90),
+                                                           ("bf16", 3, 30, 5, 2), ("bf16", 7, 129, 0, 4),
+                                                           ("f32", 9, 512, 64, 3), ("bf16", 130, 512, 64, 12)])
+def test_cut_rows_of_odd_widths(mla, dtype, heads, latent, rope, batch):
+    # rows cut over work units and merged: whole rows or parts of them a warp, widths of any remainder
+    kv = [150 + (97 * i) % 300 for i in range(batch)]
+    c = wr.Case(seed=39, dtype=dtype, heads=heads, latent=latent, rope=rope, page=16, kv=kv, q=[1] * batch, window=400,
+                sinks=2)
+    wr.check(*decode(mla, c), c.want(), batch)
+
+
+@pytest.mark.parametrize("kv,window", [([8000], 8000), ([2000] * 24, 2000), ([1500, 20, 1100, 640, 0, 2], 1400)])
+@pytest.mark.parametrize("geometry", ["v3", "h16"])
+def test_cut_rows_of_few_and_many_pieces(mla, geometry, kv, window):
+    if geometry == "v3" and len(kv) > 10:
+        kv = kv[:20]
+    c = decode_case(geometry, kv, window, 4, seed=40)
+    wr.check(*decode(mla, c), c.want(), len(kv))
+
+
+def test_a_padded_batch_of_prompts(mla):
+    # many more rows of q than tokens, as a captured call pads them; long rows, so that the few there are get cut
+    c = prefill_case("v3", [2000, 900, 0], [3, 2, 0], 1900, 4, seed=41, tail=400)
+    o, l = prefill(mla, c)
+    wr.check(o, l, c.want(), 5)
+    assert (o[5:] == 7).all() and (l[5:] == 7).all()
+
+
 def test_refusals_of_the_binding(mla):
     c = decode_case("v3", [70], 20, 0, seed=25)
     cache, q, table, kv, cu = c.dev()
