@@ -112,9 +112,13 @@ def _check(status: int) -> None:
 
 def _dtype_code(*tensors) -> int:
     import torch
-    dt = next(t for t in tensors if t is not None).dtype
+    dt = None
     for t in tensors:
-        if t is not None and t.dtype != dt:
+        if t is None:
+            continue
+        if dt is None:
+            dt = t.dtype
+        elif t.dtype != dt:
             dts = {t.dtype for t in tensors if t is not None}
             raise MlaError(MLA_ERR_INVALID_ARG, f"tensors disagree on dtype: {sorted(map(str, dts))}")
     if dt == torch.float32:
@@ -396,7 +400,7 @@ def mla_decode_noalloc(o_lat_out, q_cat, cache, block_table, seq_lens, kv_lora_r
 def _check_device(*tensors) -> int:
     """Every tensor on one CUDA device, and that the current one: the library launches there. Its index."""
     import torch
-    device = torch.cuda.current_device()
+    device = torch._C._cuda_getDevice()   # the tensors have initialised CUDA
     for t in tensors:
         if t is not None and t.get_device() != device:
             raise MlaError(MLA_ERR_INVALID_ARG, "tensors must lie on the current device, "
@@ -427,21 +431,33 @@ def _check_counts(t, n: int, name: str) -> None:
 
 def _check_table(block_table, batch: int) -> None:
     import torch
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != batch:
+    shape = block_table.shape
+    if block_table.dtype != torch.int32 or len(shape) != 2 or shape[0] != batch:
         raise MlaError(MLA_ERR_INVALID_ARG, f"block_table must be int32 [{batch}, max_blocks]")
-    if block_table.numel() and block_table.stride(1) != 1:
+    if block_table.stride(1) != 1 and block_table.numel():
         raise MlaError(MLA_ERR_INVALID_ARG, "block_table must have unit column stride")
 
 
 def _table_stride(block_table) -> int:
     """Row stride of a block table (a single row's stride is arbitrary in torch: its width serves)."""
-    return block_table.stride(0) if block_table.shape[0] > 1 else block_table.shape[1]
+    shape = block_table.shape
+    return block_table.stride(0) if shape[0] > 1 else shape[1]
+
+
+def _rows_and_heads(q_cat):
+    shape = q_cat.shape
+    if len(shape) != 3:
+        raise MlaError(MLA_ERR_INVALID_ARG, "q_cat must be [rows, heads, kv_lora_rank + rope_dim]")
+    return shape[0], shape[1]
 
 
 def _check_lse(lse_out, q_cat) -> None:
     import torch
-    if lse_out is not None and (lse_out.dtype != torch.float32 or not lse_out.is_contiguous() or
-                                lse_out.shape != q_cat.shape[:2]):
+    if lse_out is None:
+        return
+    shape, rows = lse_out.shape, q_cat.shape
+    if (lse_out.dtype != torch.float32 or not lse_out.is_contiguous() or len(shape) != 2 or shape[0] != rows[0] or
+            shape[1] != rows[1]):
         raise MlaError(MLA_ERR_INVALID_ARG, "lse_out must be contiguous float32 with q_cat's rows and heads")
 
 
@@ -481,7 +497,7 @@ def mla_cache_write_ds_mla(cache, kv_c, k_pe, slot_mapping, stream=None) -> None
 
 
 def _read_args(out, cache, block_table, cu_seqlens, seq_starts):
-    batch = block_table.shape[0]
+    batch = cu_seqlens.numel() - 1
     _check_table(block_table, batch)
     _check_counts(cu_seqlens, batch + 1, "cu_seqlens")
     if seq_starts is not None:
@@ -521,7 +537,7 @@ def mla_decode_window(o_lat_out, q_cat, cache, block_table, seq_lens, kv_lora_ra
                       softmax_scale: float, window: int, sinks: int = 0, lse_out=None, num_splits: int = 0,
                       workspace=None, stream=None) -> None:
     """Step 4, windowed: mla_decode over the last `window` rows of each sequence and its first `sinks` rows."""
-    B, H = q_cat.shape[0], q_cat.shape[1]
+    B, H = _rows_and_heads(q_cat)
     _check_table(block_table, B)
     _check_counts(seq_lens, B, "seq_lens")
     _check_lse(lse_out, q_cat)
@@ -544,7 +560,7 @@ def mla_prefill_window(o_lat_out, q_cat, cache, block_table, cu_seqlens_q, seq_l
                        workspace=None, stream=None) -> None:
     """Step 4 (prefill), windowed: each query attends the last `window` rows up to its own and its
     sequence's first `sinks` rows."""
-    batch, T, H = seq_lens_kv.numel(), q_cat.shape[0], q_cat.shape[1]
+    batch, (T, H) = seq_lens_kv.numel(), _rows_and_heads(q_cat)
     _check_table(block_table, batch)
     _check_counts(seq_lens_kv, batch, "seq_lens_kv")
     _check_counts(cu_seqlens_q, batch + 1, "cu_seqlens_q")

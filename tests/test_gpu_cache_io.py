@@ -281,7 +281,8 @@ def test_refusals_of_the_binding(mla):
     cu = torch.tensor([0, 4], dtype=torch.int32, device="cuda")
     for args in ((out[:, :512], cache, table, cu), (out, cache, table, cu[:1]), (out, cache, table.long(), cu),
                  (out, cache, table, cu.long()), (out.half(), cache, table, cu), (out, cache.cpu(), table, cu),
-                 (out.t(), cache, table, cu)):
+                 (out.t(), cache, table, cu), (out, cache, table[0], cu), (out, cache, table[0, 0], cu),
+                 (out, cache, table, cu[0]), (out, cache[0], table, cu), (out[0], cache, table, cu)):
         with pytest.raises(mla.MlaError):
             mla.mla_cache_read_ds_mla(*args)
     with pytest.raises(mla.MlaError):

@@ -470,4 +470,10 @@ def test_refusals_of_the_binding(mla):
     refused(o=o.cpu())
     refused(o=o.transpose(1, 2))
     refused(table=table[:, :0])
+    refused(table=table[0])
+    refused(table=table[0, 0])
+    refused(q=q[0])
+    refused(q=q[0, 0, 0])
+    refused(kv=kv[0])
+    refused(cache=cache[0])
     assert (o == 7).all() and (l == 7).all()
