@@ -219,8 +219,8 @@ struct WindowCall {
 };
 // The schedule in the workspace (window_sched.cu): the row tiles' descriptions, how many there are and,
 // where row tiles may be cut, {row tile, tile} of each unit's first (null: whole row tiles dealt out);
-// most: row tiles at most; cut: some may be cut, so their pieces have to be merged; direct: a decode whose
-// row tiles nothing would cut, on the tensor cores, whose units take every units-th sequence and describe it themselves.
+// most: row tiles at most; cut: some may be cut, so their pieces have to be merged; direct: a decode on the
+// tensor cores without a schedule, whose units take every units-th sequence and describe it themselves.
 struct WindowSched {
   int64_t most;
   int4* items;

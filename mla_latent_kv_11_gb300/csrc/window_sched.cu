@@ -10,7 +10,7 @@
 //     tile costing its tiles plus kItemCost) and holds at most two cut row tiles, the end of one and the
 //     head of another;
 //   - more row tiles balance by themselves and are dealt out whole;
-//   - so are a decode's of so short a window that none would be cut, without a schedule.
+//   - so are a decode's of a short window, without a schedule (kDirectTiles).
 // A unit has two partial slots. The schedule depends on the lengths and the number of units alone:
 // results repeat bit for bit.
 #include <cuda_bf16.h>
@@ -31,9 +31,14 @@ __device__ unsigned g_window_err = 0;
 template <int kPer>
 constexpr int kItemCost = kPer == 2 ? 2 : 1;
 // What cutting evenly adds to a unit's time, in tiles: the merge's launch, and the float32 pieces written
-// and read, 4 KB a row (128 heads: one sequence of 3 tiles 11.2 us cut, 13.0 whole; 24 of 6 tiles 20.8
-// cut, 18.1 whole). On the CUDA cores a tile takes longer than that.
-constexpr int kMergeCost = 1, kRowsPerTile = 2048;
+// and read, 4 KB a row (128 heads: 24 sequences of 6 tiles 20.8 us cut, 17.5 whole; of 16 tiles 27.7 cut,
+// 31.9 whole). On the CUDA cores a tile takes longer than that.
+constexpr int kMergeCost = 2, kRowsPerTile = 2048;
+// Tiles of a decode's row tile up to which it goes without a schedule, whole. One sequence of 3 tiles
+// takes 9.7 us so, 12.8 scheduled and cut; of 5 tiles 13 either way, with one launch instead of three. With
+// so many sequences that cutting would make three pieces of each at most, up to 8 (48 sequences of 6
+// tiles: 16.3 us, 19.8 with a schedule that cuts none; 24 of 5: 13.9, 17.4).
+constexpr int kDirectTiles = 5, kDirectTilesOfMany = 8;
 template <int kPer>
 __device__ __forceinline__ int cut_cost(int pieces, int rows) {
   return kPer == 2 ? kMergeCost + pieces * rows / kRowsPerTile : 0;
@@ -453,12 +458,12 @@ cudaError_t launch_window_schedule(const WindowCall& c, int tpt, int blocks_per_
   // cut row tiles while their tiles can be counted in 32 bits
   const int64_t seen = std::min<int64_t>(cap, (int64_t)s.window + s.sinks) / kBlk + 4;
   const bool split = items <= kSplitItems && c.B <= kSplitItems && items * seen < (int64_t)1 << 30;
-  // tiles of a row tile at most; whether any can be cut. A decode of which none would be, whatever its
-  // lengths, needs no schedule (one 64-row sequence: 9.2 us with one)
+  // tiles of a row tile at most; whether any can be cut, or a decode needs no schedule (with more
+  // sequences than units, only where none would be cut)
   const int64_t blocks = std::min<int64_t>((cap + (int64_t)kBlk - 1) / kBlk,
                                            ((int64_t)s.window + tpt + kBlk - 3) / kBlk + 1 + (s.sinks + (int64_t)kBlk - 1) / kBlk);
   const int64_t tiles = (blocks + blocks_per_tile - 1) / blocks_per_tile, least = 1 + (blocks_per_tile == 2 ? kMergeCost : 0);
-  const bool direct = decode && blocks_per_tile == 2 && tiles <= least;
+  const bool direct = decode && blocks_per_tile == 2 && tiles <= (c.B > units ? least : 4 * (int64_t)c.B > units ? kDirectTilesOfMany : kDirectTiles);
   *sched = WindowSched{items, s.items, s.total, split ? s.unit_start : nullptr,
                        split && !direct && units > 1 && tiles > 1 && (items > units || tiles > least), direct, c.kv_lens,
                        c.B, cap, s.window, s.sinks};
