@@ -219,16 +219,16 @@ struct WindowCall {
 };
 // The schedule in the workspace (window_sched.cu): the row tiles' descriptions, how many there are and,
 // where row tiles may be cut, {row tile, tile} of each unit's first (null: whole row tiles dealt out);
-// most: row tiles at most; cut: some may be cut, so their pieces have to be merged; direct: a decode on the
-// tensor cores without a schedule, whose units take every units-th sequence and describe it themselves.
+// most: row tiles at most; cut: some may be cut, so their pieces have to be merged; direct: on the tensor
+// cores and without a schedule, units take every units-th row tile and describe it themselves.
 struct WindowSched {
   int64_t most;
   int4* items;
   int32_t* total;
   int2* unit_start;
   bool cut, direct;
-  const int32_t* kv_lens;
-  int32_t B, cap, window, sinks;
+  const int32_t *cu_q, *kv_lens;   // cu_q null: a decode, one token a sequence
+  int32_t B, T, cap, tpt, window, sinks;
 };
 // Where results go: rows of the output, and the partial slots [2 * units][rows][L] of cut row tiles
 // with their log-sum-exps [2 * units][rows]. tptc 0: a slot's row is a head; else rows 64 r .. of a slot

@@ -10,7 +10,7 @@
 //     tile costing its tiles plus kItemCost) and holds at most two cut row tiles, the end of one and the
 //     head of another;
 //   - more row tiles balance by themselves and are dealt out whole;
-//   - so are a decode's of a short window, without a schedule (kDirectTiles).
+//   - so are those of a short window, without a schedule (kDirectTiles).
 // A unit has two partial slots. The schedule depends on the lengths and the number of units alone:
 // results repeat bit for bit.
 #include <cuda_bf16.h>
@@ -34,10 +34,10 @@ constexpr int kItemCost = kPer == 2 ? 2 : 1;
 // and read, 4 KB a row (128 heads: 24 sequences of 6 tiles 20.8 us cut, 17.5 whole; of 16 tiles 27.7 cut,
 // 31.9 whole). On the CUDA cores a tile takes longer than that.
 constexpr int kMergeCost = 2, kRowsPerTile = 2048;
-// Tiles of a decode's row tile up to which it goes without a schedule, whole. One sequence of 3 tiles
-// takes 9.7 us so, 12.8 scheduled and cut; of 5 tiles 13 either way, with one launch instead of three. With
-// so many sequences that cutting would make three pieces of each at most, up to 8 (48 sequences of 6
-// tiles: 16.3 us, 19.8 with a schedule that cuts none; 24 of 5: 13.9, 17.4).
+// Tiles of a row tile up to which no more of them than units go without a schedule, whole. One sequence
+// of 3 tiles takes 9.7 us so, 12.8 scheduled and cut; of 5 tiles 13 either way, with one launch instead
+// of three. Where cutting would make three pieces of each at most, up to 8 (48 sequences of 6 tiles: 16.3
+// us, 19.8 with a schedule that cuts none; 24 of 5: 13.9, 17.4).
 constexpr int kDirectTiles = 5, kDirectTilesOfMany = 8;
 template <int kPer>
 __device__ __forceinline__ int cut_cost(int pieces, int rows) {
@@ -58,20 +58,10 @@ struct SchedArgs {
 
 __device__ __forceinline__ int kv_len(const SchedArgs& s, int b) { return mla::kv_len(s.kv_lens, s.cap, b, &g_window_err); }
 
-// Query tokens of sequence b; -1 (and reported) where cu_q leaves [0, T] or decreases. Nothing is
-// computed then: only an ascending cu_q keeps the row tiles within the room for them.
 __device__ __forceinline__ int q_len(const SchedArgs& s, int b, int& q0) {
-  if (s.cu_q == nullptr) {
-    q0 = b;
-    return 1;
-  }
-  q0 = s.cu_q[b];
-  const int q1 = s.cu_q[b + 1];
-  if (q0 < 0 || q1 > s.T || q1 < q0) {
-    atomicOr(&g_window_err, kErrDeviceData);
-    return -1;
-  }
-  return q1 - q0;
+  if (s.cu_q != nullptr) return mla::q_len(s.cu_q, s.T, b, q0, &g_window_err);
+  q0 = b;
+  return 1;
 }
 
 // Exclusive block scan of one int a thread (blockDim.x a multiple of 32).
@@ -458,15 +448,16 @@ cudaError_t launch_window_schedule(const WindowCall& c, int tpt, int blocks_per_
   // cut row tiles while their tiles can be counted in 32 bits
   const int64_t seen = std::min<int64_t>(cap, (int64_t)s.window + s.sinks) / kBlk + 4;
   const bool split = items <= kSplitItems && c.B <= kSplitItems && items * seen < (int64_t)1 << 30;
-  // tiles of a row tile at most; whether any can be cut, or a decode needs no schedule (with more
-  // sequences than units, only where none would be cut)
+  // tiles of a row tile at most; whether any can be cut, or the call needs no schedule (a decode of more
+  // sequences than units only where none would be cut)
   const int64_t blocks = std::min<int64_t>((cap + (int64_t)kBlk - 1) / kBlk,
                                            ((int64_t)s.window + tpt + kBlk - 3) / kBlk + 1 + (s.sinks + (int64_t)kBlk - 1) / kBlk);
   const int64_t tiles = (blocks + blocks_per_tile - 1) / blocks_per_tile, least = 1 + (blocks_per_tile == 2 ? kMergeCost : 0);
-  const bool direct = decode && blocks_per_tile == 2 && tiles <= (c.B > units ? least : 4 * (int64_t)c.B > units ? kDirectTilesOfMany : kDirectTiles);
+  const bool direct = blocks_per_tile == 2 && (decode || c.B <= 32) &&
+                      tiles <= (items > units ? (decode ? least : 0) : 4 * items > units ? kDirectTilesOfMany : kDirectTiles);
   *sched = WindowSched{items, s.items, s.total, split ? s.unit_start : nullptr,
-                       split && !direct && units > 1 && tiles > 1 && (items > units || tiles > least), direct, c.kv_lens,
-                       c.B, cap, s.window, s.sinks};
+                       split && !direct && units > 1 && tiles > 1 && (items > units || tiles > least), direct, c.cu_q,
+                       c.kv_lens, c.B, s.T, cap, tpt, s.window, s.sinks};
   *out = WindowOut{c.o.data, c.o.s0, c.o.s1, c.lse, reinterpret_cast<float*>(base + w.o),
                    reinterpret_cast<float*>(base + w.lse), rows, c.L, c.H, 0, false};
   if (direct) return cudaSuccess;

@@ -50,6 +50,18 @@ __device__ __forceinline__ int kv_len(const int32_t* lens, int cap, int b, unsig
   return n;
 }
 
+// Query tokens of sequence b of a prefill, from q0 on; -1 (and reported) where cu leaves [0, T] or
+// decreases. Nothing is computed then: only ascending bounds keep the row tiles within the room for them.
+__device__ __forceinline__ int q_len(const int32_t* cu, int T, int b, int& q0, unsigned* err) {
+  q0 = cu[b];
+  const int q1 = cu[b + 1];
+  if (q0 < 0 || q1 > T || q1 < q0) {
+    atomicOr(err, kErrDeviceData);
+    return -1;
+  }
+  return q1 - q0;
+}
+
 // A part of a row tile: tiles [t0, t1).
 struct Seg {
   int tok0, ntok, pos0, b;   // first token's row, tokens, its position, sequence
@@ -69,9 +81,18 @@ template <int kPer, bool kDirect>
 struct Walker {
   int unit, item, step, end_item, end_tile, tile;
   Item ahead;   // the next row tile, loaded while the one before it runs
+  int q0, count, len, first, tiles;   // kDirect: of lane b's sequence b, its tokens, cache rows and row tiles
+
+  // A direct schedule is worked out by whole warps, a lane a sequence: a prefill has at most 32.
 
   __device__ Item load(const WindowSched& s, int i, unsigned* err) const {
-    if constexpr (kDirect) return make_item(i, 1, kv_len(s.kv_lens, s.cap, i, err) - 1, i, s.window, s.sinks);
+    if constexpr (kDirect) {
+      if (s.cu_q == nullptr) return make_item(i, 1, kv_len(s.kv_lens, s.cap, i, err) - 1, i, s.window, s.sinks);
+      const int b = 31 - __clz(__ballot_sync(0xffffffffu, tiles > 0 && first <= i));
+      const int t0 = (i - __shfl_sync(0xffffffffu, first, b)) * s.tpt, k = __shfl_sync(0xffffffffu, count, b);
+      const int pos0 = __shfl_sync(0xffffffffu, len, b) - k + t0, tok0 = __shfl_sync(0xffffffffu, q0, b) + t0;
+      return make_item(tok0, min(s.tpt, k - t0), pos0, b, s.window, s.sinks);
+    }
     return load_item(s.items, i);
   }
   __device__ void init(const WindowSched& s, int unit_, int units, unsigned* err) {
@@ -82,6 +103,23 @@ struct Walker {
       end_item = s.B;
       end_tile = 0;
       step = units;
+      if (s.cu_q != nullptr) {
+        const int b = threadIdx.x & 31;
+        q0 = count = len = 0;
+        if (b < s.B) {
+          count = q_len(s.cu_q, s.T, b, q0, err);
+          len = kv_len(s.kv_lens, s.cap, b, err);
+        }
+        tiles = __any_sync(0xffffffffu, count < 0) ? 0 : (count + s.tpt - 1) / s.tpt;
+        int x = tiles;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, x, o);
+          if (b >= o) x += y;
+        }
+        first = x - tiles;
+        end_item = __shfl_sync(0xffffffffu, x, 31);
+      }
     } else if (s.unit_start != nullptr) {
       const int2 a = s.unit_start[unit], e = s.unit_start[unit + 1];
       item = a.x;
