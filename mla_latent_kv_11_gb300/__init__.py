@@ -175,12 +175,10 @@ def mla_cache_write(cache, kv_c, k_pe, slot_mapping, stream=None) -> None:
 
 
 def _fp8_cache(cache):
-    """An e4m3 cache as a byte view (torch.float8_e4m3fn or uint8 storage of the codes)."""
+    """An e4m3 cache: torch.float8_e4m3fn or uint8 storage of the codes, whose strides count bytes either way."""
     import torch
-    if cache.dtype == torch.uint8:
+    if cache.dtype == torch.uint8 or cache.dtype == getattr(torch, "float8_e4m3fn", None):
         return cache
-    if cache.dtype == getattr(torch, "float8_e4m3fn", None):
-        return cache.view(torch.uint8)
     raise MlaError(MLA_ERR_INVALID_ARG, "an fp8 cache must be float8_e4m3fn or uint8 codes")
 
 
@@ -496,13 +494,13 @@ def mla_cache_write_ds_mla(cache, kv_c, k_pe, slot_mapping, stream=None) -> None
                                         _stream_on(stream, device)))
 
 
-def _read_args(out, cache, block_table, cu_seqlens, seq_starts):
+def _read_args(out, cache, block_table, cu_seqlens, seq_starts, scale=None):
     batch = cu_seqlens.numel() - 1
     _check_table(block_table, batch)
     _check_counts(cu_seqlens, batch + 1, "cu_seqlens")
     if seq_starts is not None:
         _check_counts(seq_starts, batch, "seq_starts")
-    device = _check_device(out, cache, block_table, cu_seqlens, seq_starts)
+    device = _check_device(out, cache, block_table, cu_seqlens, seq_starts, scale)
     return device, (as_mla_tensor(out), as_mla_tensor(cache), _ptr(block_table), _table_stride(block_table),
                     block_table.shape[1], _ptr(cu_seqlens), _ptr(seq_starts), batch)
 
@@ -517,8 +515,7 @@ def mla_cache_read(out, cache, block_table, cu_seqlens, seq_starts=None, stream=
 def mla_cache_read_fp8(out, cache, block_table, cu_seqlens, scale, seq_starts=None, stream=None) -> None:
     """Read-back of an e4m3 cache: as mla_cache_read, a value = its code's value * scale, in out's dtype."""
     cache = _fp8_cache(cache)
-    device, args = _read_args(out, cache, block_table, cu_seqlens, seq_starts)
-    _check_device(scale)
+    device, args = _read_args(out, cache, block_table, cu_seqlens, seq_starts, scale)
     _check(lib().mla_cache_read_fp8(_dtype_code(out), *args, _f32_scalar(scale, "scale"), _stream_on(stream, device)))
 
 
