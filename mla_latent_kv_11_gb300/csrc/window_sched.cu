@@ -25,9 +25,9 @@ namespace {
 
 __device__ unsigned g_window_err = 0;
 
-// In tiles, of kPer blocks each (a tensor-core tile takes 1.7 us, one on the CUDA cores ten times
-// that): what a row tile costs beside its tiles. A prefill of ragged prompts, 1 to 8 tensor-core tiles
-// a row tile, took 115 us with 2, 135 with 1.
+// In tiles (a tensor-core tile takes 1.7 us, one on the CUDA cores four times that): what a row tile
+// costs beside its tiles. A prefill of ragged prompts, 1 to 8 tensor-core tiles a row tile, took 115 us
+// with 2, 135 with 1.
 template <int kPer>
 constexpr int kItemCost = kPer == 2 ? 2 : 1;
 // What cutting evenly adds to a unit's time, in tiles: the merge's launch, and the float32 pieces written
@@ -446,13 +446,13 @@ cudaError_t launch_window_schedule(const WindowCall& c, int tpt, int blocks_per_
               reinterpret_cast<int32_t*>(base + w.total), reinterpret_cast<int2*>(base + w.starts),
               reinterpret_cast<int32_t*>(base + w.prefix)};
   // cut row tiles while their tiles can be counted in 32 bits
-  const int64_t seen = std::min<int64_t>(cap, (int64_t)s.window + s.sinks) / kBlk + 4;
+  const int64_t seen = std::min<int64_t>(cap, (int64_t)s.window + s.sinks) / (kBlk / 2) + 8;
   const bool split = items <= kSplitItems && c.B <= kSplitItems && items * seen < (int64_t)1 << 30;
   // tiles of a row tile at most; whether any can be cut, or the call needs no schedule (a decode of more
   // sequences than units only where none would be cut)
   const int64_t blocks = std::min<int64_t>((cap + (int64_t)kBlk - 1) / kBlk,
                                            ((int64_t)s.window + tpt + kBlk - 3) / kBlk + 1 + (s.sinks + (int64_t)kBlk - 1) / kBlk);
-  const int64_t tiles = (blocks + blocks_per_tile - 1) / blocks_per_tile, least = 1 + (blocks_per_tile == 2 ? kMergeCost : 0);
+  const int64_t tiles = blocks_per_tile == 1 ? 2 * blocks : (blocks + blocks_per_tile - 1) / blocks_per_tile, least = 1 + (blocks_per_tile == 2 ? kMergeCost : 0);
   const bool direct = blocks_per_tile == 2 && (decode || c.B <= 32) &&
                       tiles <= (items > units ? (decode ? least : 0) : 4 * items > units ? kDirectTilesOfMany : kDirectTiles);
   *sched = WindowSched{items, s.items, s.total, split ? s.unit_start : nullptr,

@@ -33,11 +33,11 @@ __device__ __forceinline__ void store_item(int4* items, int i, const Item& it) {
   items[2 * i + 1] = it.b;
 }
 
-// Tiles of a row tile: one, with nothing attended, where there are no blocks, so that its rows are
-// written all the same.
+// Tiles of a row tile, of kPer blocks each or (kPer 1, the CUDA cores) half a block: one, with nothing
+// attended, where there are no blocks, so that its rows are written all the same.
 template <int kPer>
 __device__ __forceinline__ int item_tiles(int nblk) {
-  return nblk > 0 ? (nblk + kPer - 1) / kPer : 1;
+  return nblk > 0 ? (kPer == 1 ? 2 * nblk : (nblk + kPer - 1) / kPer) : 1;
 }
 
 // Rows of sequence b in the cache; a length beyond the table is cut to it (and reported in *err).

@@ -10,7 +10,9 @@
 //
 // Eight heads a block balance the loads of rows (again for every block of heads) against the products;
 // with fewer blocks than the SMs can hold, four are faster. Measured, with 16, 8 and 4 heads (fp32, 16
-// heads): 5 sequences of up to 104 attended rows 36, 29 and 23 us; 64 of 512 rows 143, 114 and 180.
+// heads): 5 sequences of up to 104 attended rows 36, 29 and 23 us; 64 of 512 rows 143, 114 and 180. The
+// schedule cuts rows to sub-tiles and no finer than the blocks that the SMs hold at once: the 5 sequences
+// 16 us, 23 with pieces of two sub-tiles; 64 of 1024 rows and 128 heads 1.32 ms, 1.52 with a unit an SM.
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
@@ -92,7 +94,7 @@ __global__ void __launch_bounds__(kThreads) window_simt_kernel(SimtArgs a) {
 #pragma unroll
     for (int h = 0; h < kHeads; ++h) acc[h][0] = acc[h][1] = 0.f;
     const int pos = sg.pos0;
-    for (int j = 2 * sg.t0; j < 2 * sg.t1; ++j) {   // halves of blocks
+    for (int j = sg.t0; j < sg.t1; ++j) {   // halves of blocks
       // lane i: cache row i of the half, attended or not, and where it lies (-1: nowhere)
       const int base = block_row(sg, j >> 1), t = base + kKeys * (j & 1) + lane;
       const bool seen = base >= 0 && t <= pos && (t < a.sinks || t > pos - a.window);
@@ -207,16 +209,26 @@ cudaError_t launch_simt(const SimtArgs& a, int units, cudaStream_t st) {
   return launch_k(window_simt_kernel<T, kHeads>, dim3(units, (a.out.H + kHeads - 1) / kHeads), kThreads, bytes, st, a);
 }
 
-int simt_units(int num_splits) { return num_splits > 0 ? std::min(num_splits, kMaxUnits) : device_sm_count(); }
+// Blocks that the SMs hold at once: two each.
+int resident() { return 2 * device_sm_count(); }
+// Work units: one of `heads` heads a block each, as many as run at once.
+int simt_units(int num_splits, int64_t H, int heads) {
+  if (num_splits > 0) return std::min(num_splits, kMaxUnits);
+  return (int)std::max<int64_t>(1, resident() / std::max<int64_t>(1, (H + heads - 1) / heads));
+}
 
 }  // namespace
 
 size_t window_simt_workspace(int64_t T, int64_t B, int64_t H, int64_t L, bool decode, int num_splits) {
-  return window_workspace(T, B, decode, 1, simt_units(num_splits), H, L);
+  return window_workspace(T, B, decode, 1, simt_units(num_splits, H, 8), H, L);   // the larger number of units
 }
 
 cudaError_t launch_window_simt(mla_dtype dt, const WindowCall& c, int num_splits, void* ws, cudaStream_t st) {
-  const int units = simt_units(num_splits);
+  // four heads a block where the SMs hold at once all the blocks that have work, at most
+  const int64_t rows = std::min<int64_t>((int64_t)c.max_blocks * c.cache.page, (int64_t)c.window.window + c.window.sinks);
+  const int64_t items = c.cu_q == nullptr ? c.B : c.q.n0, tiles = 2 * (rows / kBlk + 3);
+  const bool few = items * tiles * ((c.H + 3) / 4) <= resident();
+  const int units = simt_units(num_splits, c.H, few ? 4 : 8);
   SimtArgs a{};
   cudaError_t e = launch_window_schedule(c, 1, 1, units, c.H, ws, &a.sched, &a.out, st);
   if (e != cudaSuccess) return e;
@@ -230,9 +242,6 @@ cudaError_t launch_window_simt(mla_dtype dt, const WindowCall& c, int num_splits
   a.window = c.window.window < 0x3fffffff ? c.window.window : 0x3fffffff;
   a.sinks = c.window.sinks;
   a.scale = c.scale;
-  // blocks of four heads that have work, at most: fewer than three an SM
-  const int64_t tiles = std::min<int64_t>((int64_t)c.max_blocks * c.cache.page, (int64_t)a.window + a.sinks) / kBlk + 3;
-  const bool few = a.sched.most * tiles * ((c.H + 3) / 4) <= 3 * (int64_t)device_sm_count();
   if (dt == MLA_F32)
     e = few ? launch_simt<float, 4>(a, units, st) : launch_simt<float, 8>(a, units, st);
   else
