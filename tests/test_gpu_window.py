@@ -439,6 +439,29 @@ def test_cut_rows_of_few_and_many_pieces(mla, geometry, kv, window):
     wr.check(*decode(mla, c), c.want(), len(kv))
 
 
+@pytest.mark.parametrize("splits", [1, 2, 3, 300])
+def test_decode_splits_of_a_short_window(mla, splits):
+    c = decode_case("v3", [2000, 3, 0, 900, 1500], 90, 2, seed=42)
+    wr.check(*decode(mla, c, num_splits=splits), c.want(), 5)
+
+
+@pytest.mark.parametrize("heads", [600, 2500])
+def test_more_heads_than_blocks_run_at_once(mla, heads):
+    c = wr.Case(seed=43, dtype="f32", heads=heads, latent=16, rope=2, page=16, kv=[100, 0, 40, 333], q=[1] * 4, window=60,
+                sinks=3)
+    wr.check(*decode(mla, c), c.want(), 4)
+
+
+@pytest.mark.parametrize("geometry", ["v3", "h16", "h20", "nope64"])
+@pytest.mark.parametrize("batch", [1, 31, 33])
+def test_prompts_of_few_tokens_and_short_windows(mla, geometry, batch):
+    # row tiles described by the units themselves up to 32 sequences, scheduled beyond; some prompts are empty
+    q = [(5 * i) % 3 if batch > 1 else 7 for i in range(batch)]
+    kv = [max(k, (61 * i) % 400) for i, k in enumerate(q)]
+    c = prefill_case(geometry, kv, q, 120, 5, seed=44, tail=2)
+    wr.check(*prefill(mla, c), c.want(), sum(q))
+
+
 def test_a_padded_batch_of_prompts(mla):
     # many more rows of q than tokens, as a captured call pads them; long rows, so that the few there are get cut
     c = prefill_case("v3", [2000, 900, 0], [3, 2, 0], 1900, 4, seed=41, tail=400)
