@@ -748,14 +748,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        // the writes this answers for are complete (each lane's fence, then the warp's barrier): a
-        // relaxed arrive on the other CTA's barrier orders nothing more. A release at cluster scope
-        // waits for all the CTA's copies in flight: 2200 to 3500 cycles a tile
+        // The lanes' shared-memory writes (P, cleared values) are ordered before this arrive by the warp's
+        // barrier and a release; their tensor memory accesses by the fence before. Across the two CTAs the
+        // release is one of shared memory alone: one of everything (an arrive with .release.cluster) waits
+        // for the output's stores and the copies in flight too, 2200 to 3500 cycles a tile
         if (lane == 0) {
           if (rank == 0)
             mbar_arrive(&sh.p_full);
           else
-            asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_p) : "memory");
+            mbar_arrive_smem_released(bar_p);
         }
         if (left > 0) store_quarter();
       }

@@ -60,6 +60,17 @@ __device__ __forceinline__ void mbar_arrive_remote_relaxed(uint64_t* bar, uint32
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
 }
 
+// Arrive on another CTA's barrier (a shared::cluster address) with release at cluster scope for this
+// CTA's shared memory alone, by a fence restricted to it before a relaxed arrive: what a thread of the
+// other CTA reads, or lets an MMA read, of this CTA's shared memory behind its acquiring wait is what was
+// written before. Writes to global memory are not ordered by it.
+__device__ __forceinline__ void mbar_arrive_smem_released(uint32_t remote) {
+  asm volatile(
+      "fence.release.sync_restrict::shared::cta.cluster;\n"
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote)
+      : "memory");
+}
+
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
