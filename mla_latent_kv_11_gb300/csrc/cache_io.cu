@@ -113,6 +113,11 @@ __device__ __forceinline__ float e4m3(uint8_t c) {
 // No remainder of a quotient near a middle (2^-10 and up) may underflow: s is at least 2^-80 here, x
 // finite or NaN. (An exact remainder needs no more: a code's middle has 5 bits, so a quotient that is
 // none is 2^-29 of itself away from it at least.)
+// The remainders are rounded down. That changes none that is exact, but makes a remainder of zero -0: for
+// x = -0 each later sum then adds two zeros of its sign and the quotient is -0; for x = +0 it adds zeros of
+// different signs, which to nearest and toward zero is +0. (Rounded to nearest, -0 came out as +0.) Where
+// a remainder underflows, |x| is below 2^-125 and the quotient below 2^-45, whose code is a zero of x's
+// sign: the last step, with a remainder near x where the steps before cancelled, still gives that sign.
 // Two quotients at a time, in paired instructions: ns and r hold -s and 1 / s twice.
 __device__ __forceinline__ uint64_t pair(float a, float b) {
   return (uint64_t)__float_as_uint(b) << 32 | __float_as_uint(a);
@@ -126,9 +131,9 @@ __device__ __forceinline__ void divide2(float x0, float x1, uint64_t ns, uint64_
   const uint64_t x = pair(x0, x1);
   uint64_t q, a, rem, t;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q) : "l"(x), "l"(r));
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(a) : "l"(q), "l"(ns), "l"(x));
+  asm("fma.rm.f32x2 %0, %1, %2, %3;" : "=l"(a) : "l"(q), "l"(ns), "l"(x));
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(a) : "l"(a), "l"(r), "l"(q));
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(rem) : "l"(a), "l"(ns), "l"(x));
+  asm("fma.rm.f32x2 %0, %1, %2, %3;" : "=l"(rem) : "l"(a), "l"(ns), "l"(x));
   asm("fma.rz.f32x2 %0, %1, %2, %3;" : "=l"(t) : "l"(rem), "l"(r), "l"(a));
   y0 = odd((uint32_t)t, (uint32_t)rem);
   y1 = odd((uint32_t)(t >> 32), (uint32_t)(rem >> 32));
