@@ -398,11 +398,13 @@ def mla_decode_noalloc(o_lat_out, q_cat, cache, block_table, seq_lens, kv_lora_r
 def _check_device(*tensors) -> int:
     """Every tensor on one CUDA device, and that the current one: the library launches there. Its index."""
     import torch
-    device = torch._C._cuda_getDevice()   # the tensors have initialised CUDA
+    device = tensors[0].get_device()
     for t in tensors:
-        if t is not None and t.get_device() != device:
-            raise MlaError(MLA_ERR_INVALID_ARG, "tensors must lie on the current device, "
-                                                f"cuda:{device}; one is on {t.device}")
+        if t is not None and (t.get_device() != device or device < 0):
+            raise MlaError(MLA_ERR_INVALID_ARG, f"tensors must lie on one CUDA device; one is on {t.device}")
+    if torch.cuda.current_device() != device:
+        raise MlaError(MLA_ERR_INVALID_ARG, f"tensors must lie on the current device, cuda:{torch.cuda.current_device()}; "
+                                            f"they are on cuda:{device}")
     return device
 
 

@@ -1,0 +1,32 @@
+"""Refusals of the binding's newer calls that need no GPU: tensors that do not lie on one."""
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def mla():
+    from mla_latent_kv_11_gb300 import build
+    build.build()
+    import mla_latent_kv_11_gb300 as m
+    return m
+
+
+def calls(mla, **more):
+    z = torch.zeros
+    i32 = dict(dtype=torch.int32)
+    entries, rows, table, cu = z(2, 8, 656, dtype=torch.uint8), z(4, 576), z(1, 1, **i32), torch.tensor([0, 4], **i32)
+    q, o, cache, lens = z(1, 2, 576), z(1, 2, 512), z(1, 64, 576), z(1, **i32)
+    window = dict(window=8, sinks=1) | more
+    return [lambda: mla.mla_cache_write_ds_mla(entries, z(3, 512), z(3, 64), z(3, dtype=torch.int64)),
+            lambda: mla.mla_cache_read(rows, z(1, 8, 576), table, cu),
+            lambda: mla.mla_cache_read_fp8(rows, z(1, 8, 576, dtype=torch.uint8), table, cu, torch.ones(1)),
+            lambda: mla.mla_cache_read_ds_mla(rows, entries, table, cu),
+            lambda: mla.mla_decode_window(o, q, cache, table, lens, 512, 64, 0.1, **window),
+            lambda: mla.mla_prefill_window(o, q, cache, table, torch.tensor([0, 1], **i32), lens, 512, 64, 0.1, **window)]
+
+
+@pytest.mark.parametrize("which", range(6))
+def test_host_tensors_are_refused(mla, which):
+    with pytest.raises(mla.MlaError) as e:
+        calls(mla)[which]()
+    assert e.value.status == mla.MLA_ERR_INVALID_ARG and "device" in str(e.value)
