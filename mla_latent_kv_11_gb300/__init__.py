@@ -409,10 +409,13 @@ def _check_device(*tensors) -> int:
 
 
 def _stream_on(stream, device: int) -> Optional[int]:
-    """The stream a call runs on; without one, the device's current stream (asked for directly: the
-    stream object costs more than the rest of a small call)."""
+    """The stream a call runs on; without one, the device's current stream (asked for directly where torch
+    allows it: the stream object costs more than the rest of a small call)."""
     import torch
-    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
+    if stream is not None:
+        return _stream(stream)
+    direct = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return direct(device) if direct is not None else torch.cuda.current_stream(device).cuda_stream
 
 
 def _check_slots(slot_mapping) -> None:

@@ -30,3 +30,12 @@ def test_host_tensors_are_refused(mla, which):
     with pytest.raises(mla.MlaError) as e:
         calls(mla)[which]()
     assert e.value.status == mla.MLA_ERR_INVALID_ARG and "device" in str(e.value)
+
+
+def test_the_stream_without_the_direct_question(mla, monkeypatch):
+    # a torch release without the private call: the public stream object serves
+    class Stream:
+        cuda_stream = 77
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device: Stream)
+    assert mla._stream_on(None, 0) == 77 and mla._stream_on(5, 0) == 5
