@@ -447,6 +447,12 @@ def _table_stride(block_table) -> int:
     return block_table.stride(0) if shape[0] > 1 else shape[1]
 
 
+def _check_int32(value: int, name: str) -> None:
+    """A count that the library takes in 32 bits (ctypes drops the bits above them)."""
+    if not -2 ** 31 <= value < 2 ** 31:
+        raise MlaError(MLA_ERR_INVALID_ARG, f"{name} must fit 32 bits, got {value}")
+
+
 def _rows_and_heads(q_cat):
     shape = q_cat.shape
     if len(shape) != 3:
@@ -540,6 +546,9 @@ def mla_decode_window(o_lat_out, q_cat, cache, block_table, seq_lens, kv_lora_ra
                       workspace=None, stream=None) -> None:
     """Step 4, windowed: mla_decode over the last `window` rows of each sequence and its first `sinks` rows."""
     B, H = _rows_and_heads(q_cat)
+    _check_int32(window, "window")
+    _check_int32(sinks, "sinks")
+    _check_int32(num_splits, "num_splits")
     _check_table(block_table, B)
     _check_counts(seq_lens, B, "seq_lens")
     _check_lse(lse_out, q_cat)
@@ -563,6 +572,8 @@ def mla_prefill_window(o_lat_out, q_cat, cache, block_table, cu_seqlens_q, seq_l
     """Step 4 (prefill), windowed: each query attends the last `window` rows up to its own and its
     sequence's first `sinks` rows."""
     batch, (T, H) = seq_lens_kv.numel(), _rows_and_heads(q_cat)
+    _check_int32(window, "window")
+    _check_int32(sinks, "sinks")
     _check_table(block_table, batch)
     _check_counts(seq_lens_kv, batch, "seq_lens_kv")
     _check_counts(cu_seqlens_q, batch + 1, "cu_seqlens_q")

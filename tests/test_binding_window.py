@@ -39,3 +39,19 @@ def test_the_stream_without_the_direct_question(mla, monkeypatch):
     monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device: Stream)
     assert mla._stream_on(None, 0) == 77 and mla._stream_on(5, 0) == 5
+
+
+@pytest.mark.parametrize("more", [dict(window=2 ** 32 + 5), dict(window=2 ** 31), dict(window=2 ** 63 - 1),
+                                  dict(sinks=2 ** 32), dict(sinks=-2 ** 32 + 3)])
+@pytest.mark.parametrize("which", [4, 5])
+def test_counts_beyond_32_bits_are_refused(mla, which, more):
+    # passed on they would lose their upper bits: a window of 2^32 + 5 rows would be one of 5
+    with pytest.raises(mla.MlaError) as e:
+        calls(mla, **more)[which]()
+    assert e.value.status == mla.MLA_ERR_INVALID_ARG and next(iter(more)) in str(e.value)
+
+
+def test_splits_beyond_32_bits_are_refused(mla):
+    with pytest.raises(mla.MlaError) as e:
+        calls(mla, num_splits=2 ** 32 + 1)[4]()
+    assert "num_splits" in str(e.value)
