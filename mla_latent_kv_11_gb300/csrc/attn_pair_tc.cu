@@ -1005,11 +1005,8 @@ cudaError_t launch_window_tc(const WindowCall& c, const WindowMaps& maps, int nu
   return launch_window_merge(MLA_BF16, p.sched, p.out, units, st);
 }
 
-unsigned attn_pair_errors_read_clear() {
-  unsigned v = 0, zero = 0;
-  if (cudaMemcpyFromSymbol(&v, g_pair_err, sizeof(v)) != cudaSuccess) return 0;
-  cudaMemcpyToSymbol(g_pair_err, &zero, sizeof(zero));
-  return v;
+cudaError_t attn_pair_error_word(unsigned** word) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_pair_err);
 }
 
 }  // namespace mla

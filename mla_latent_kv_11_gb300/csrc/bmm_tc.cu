@@ -255,11 +255,8 @@ cudaError_t launch_wait_check(uint32_t limit_us, cudaStream_t st) {
   return launch_k(wait_check_kernel, 1, 32, 0, st, (uint64_t)limit_us * 1000ull);
 }
 
-unsigned bmm_tc_errors_read_clear() {
-  unsigned v = 0, zero = 0;
-  if (cudaMemcpyFromSymbol(&v, g_bmm_err, sizeof(v)) != cudaSuccess) return 0;
-  cudaMemcpyToSymbol(g_bmm_err, &zero, sizeof(zero));
-  return v;
+cudaError_t bmm_tc_error_word(unsigned** word) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_bmm_err);
 }
 
 }  // namespace mla

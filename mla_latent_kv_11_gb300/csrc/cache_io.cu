@@ -467,11 +467,8 @@ cudaError_t launch_cache_read_ds_mla(mla_dtype dst_dt, const CacheRead& r, cudaS
                   (const uint8_t*)r.cache.data, rows, r.rows, pw, vec);
 }
 
-unsigned cache_io_errors_read_clear() {
-  unsigned v = 0, zero = 0;
-  if (cudaMemcpyFromSymbol(&v, g_io_err, sizeof(v)) != cudaSuccess) return 0;
-  cudaMemcpyToSymbol(g_io_err, &zero, sizeof(zero));
-  return v;
+cudaError_t cache_io_error_word(unsigned** word) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_io_err);
 }
 
 }  // namespace mla

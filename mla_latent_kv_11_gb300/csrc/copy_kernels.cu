@@ -412,9 +412,22 @@ cudaError_t launch_concat_cache(mla_dtype dt, const View3& out, const View3& nop
   return launch_k(alongside ? concat_cache_kernel<true> : concat_cache_kernel<false>, qb + cb, 256, 0, st, a, c, qb);
 }
 
+namespace {
+__global__ void gather_errors_kernel(ErrorWords words) {
+  pdl_enter();
+  if (threadIdx.x >= ErrorWords::kCount) return;
+  const unsigned v = atomicExch(words.word[threadIdx.x], 0u);
+  if (v != 0) atomicOr(&g_copy_err, v);
+}
+}  // namespace
+
+cudaError_t launch_gather_errors(const ErrorWords& words, cudaStream_t st) {
+  return launch_k(gather_errors_kernel, 1, 32, 0, st, words);
+}
+
 unsigned copy_errors_read_clear() {
   unsigned v = 0, zero = 0;
-  if (cudaMemcpyFromSymbol(&v, g_copy_err, sizeof(v)) != cudaSuccess) return 0;
+  if (cudaMemcpyFromSymbol(&v, g_copy_err, sizeof(v)) != cudaSuccess || v == 0) return 0;
   cudaMemcpyToSymbol(g_copy_err, &zero, sizeof(zero));
   return v;
 }

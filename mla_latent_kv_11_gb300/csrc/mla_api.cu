@@ -896,9 +896,15 @@ mla_status mla_device_error(void* stream) {
   g_msg[0] = 0;
   cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_status(e, "mla_device_error: stream synchronize");
-  unsigned bits = copy_errors_read_clear() | cache_io_errors_read_clear() | attn_pair_errors_read_clear() |
-                  window_sched_errors_read_clear() | window_simt_errors_read_clear() |
-                  attn_simt_errors_read_clear() | attn_tc_errors_read_clear() | bmm_tc_errors_read_clear() | combine_vup_errors_read_clear();
+  ErrorWords words;
+  cudaError_t (*const word_of[ErrorWords::kCount])(unsigned**) = {
+      cache_io_error_word, attn_pair_error_word, window_sched_error_word, window_simt_error_word, bmm_tc_error_word};
+  for (int i = 0; i < ErrorWords::kCount && e == cudaSuccess; ++i) e = word_of[i](&words.word[i]);
+  // on the legacy stream, as the copies that follow
+  if (e == cudaSuccess) e = launch_gather_errors(words, nullptr);
+  if (e != cudaSuccess) return cuda_status(e, "mla_device_error: gathering the error words");
+  const unsigned bits = copy_errors_read_clear() | attn_simt_errors_read_clear() | attn_tc_errors_read_clear() |
+                        combine_vup_errors_read_clear();
   if (bits & kErrTimeout) return fail(MLA_ERR_TIMEOUT, "a bounded device-side wait gave up");
   if (bits & kErrDeviceData)
     return fail(MLA_ERR_DEVICE_DATA, "a slot, block id or sequence length was out of range");

@@ -338,16 +338,24 @@ mla_status run_decode(mla_dtype dtype, const DecodeCall& dc, float* lse_out, con
 // Set (or clear, with MLA_OK) the calling thread's mla_last_error() message.
 mla_status report_status(mla_status st, const char* fmt, ...);
 
-// Per-module error words: read and clear (after the stream was synchronised).
+// Per-module error words. Reading one is a blocking copy of 6 us and clearing it another, so most modules
+// give the word's address on the current device, and one kernel moves their errors into the copy module's
+// word, which is then read (mla_device_error 119 us with a copy and a clearing of each of nine words).
+struct ErrorWords {
+  static constexpr int kCount = 5;
+  unsigned* word[kCount];
+};
+cudaError_t cache_io_error_word(unsigned** word);
+cudaError_t attn_pair_error_word(unsigned** word);
+cudaError_t window_sched_error_word(unsigned** word);
+cudaError_t window_simt_error_word(unsigned** word);
+cudaError_t bmm_tc_error_word(unsigned** word);
+cudaError_t launch_gather_errors(const ErrorWords& words, cudaStream_t st);
+// Read and clear (after the stream was synchronised).
 unsigned copy_errors_read_clear();
-unsigned cache_io_errors_read_clear();
-unsigned attn_pair_errors_read_clear();
-unsigned window_sched_errors_read_clear();
-unsigned window_simt_errors_read_clear();
 unsigned attn_simt_errors_read_clear();
 unsigned attn_tc_errors_read_clear();
 unsigned combine_vup_errors_read_clear();
-unsigned bmm_tc_errors_read_clear();
 cudaError_t launch_wait_check(uint32_t limit_us, cudaStream_t st);
 
 }  // namespace mla

@@ -476,11 +476,8 @@ cudaError_t launch_window_merge(mla_dtype dt, const WindowSched& sched, const Wi
   return dt == MLA_F32 ? launch_merge<float>(sched, out, units, st) : launch_merge<__nv_bfloat16>(sched, out, units, st);
 }
 
-unsigned window_sched_errors_read_clear() {
-  unsigned v = 0, zero = 0;
-  if (cudaMemcpyFromSymbol(&v, g_window_err, sizeof(v)) != cudaSuccess) return 0;
-  cudaMemcpyToSymbol(g_window_err, &zero, sizeof(zero));
-  return v;
+cudaError_t window_sched_error_word(unsigned** word) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_window_err);
 }
 
 }  // namespace mla

@@ -250,11 +250,8 @@ cudaError_t launch_window_simt(mla_dtype dt, const WindowCall& c, int num_splits
   return launch_window_merge(dt, a.sched, a.out, units, st);
 }
 
-unsigned window_simt_errors_read_clear() {
-  unsigned v = 0, zero = 0;
-  if (cudaMemcpyFromSymbol(&v, g_window_simt_err, sizeof(v)) != cudaSuccess) return 0;
-  cudaMemcpyToSymbol(g_window_simt_err, &zero, sizeof(zero));
-  return v;
+cudaError_t window_simt_error_word(unsigned** word) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_window_simt_err);
 }
 
 }  // namespace mla
