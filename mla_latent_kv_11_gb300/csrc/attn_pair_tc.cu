@@ -117,7 +117,7 @@ struct PairShared {
 static_assert(sizeof(PairShared) <= PairCfg<64>::kMiscBytes, "barrier block overflows its slot");
 
 struct PairParams {
-  int H, tpt, tptc;          // heads, tokens per row tile, tokens per CTA (heads split when H > 64: tptc 0)
+  int H, tptc;               // heads, tokens of a row tile per CTA (heads split when H > 64: tptc 0)
   int window, sinks;
   float scale_log2;
   WindowSched sched;
@@ -983,7 +983,6 @@ cudaError_t launch_window_tc(const WindowCall& c, const WindowMaps& maps, int nu
   cudaError_t e = launch_window_schedule(c, tpt, 2, units, 128, ws, &p.sched, &p.out, st);
   if (e != cudaSuccess) return e;
   p.H = c.H;
-  p.tpt = tpt;
   p.out.permuted = true;
   p.tptc = p.out.tptc = c.H > 64 ? 0 : tpt / 2;
   constexpr int kFar = 0x3fffffff;   // positions stay below this

@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(1024) window_split_kernel(SchedArgs s) {
       const int x = (int)((long long)u * all / active);
       const int lo = last_at_most(cost, total, x);
       const int into = max(0, x - cost[lo] - kItemCost<kPer>);
-      start = into >= tiles[lo] ? make_int2(lo + 1, 0) : make_int2(lo, into);
+      start = make_int2(lo, into);   // x lies below the next row tile's cost, so into below its tiles
     }
     s.unit_start[u] = start;
   }
