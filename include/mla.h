@@ -319,8 +319,9 @@ size_t mla_decode_v_up_workspace_size(int32_t batch, int32_t num_heads, int32_t 
  *                  nearest code, ties to even, saturating)
  *     rope       = k_pe[i] (bf16, rounded to nearest even from float32).
  *   An infinity counts as the largest float32 in the maximum and becomes a code of +-448;
- *   a NaN does not count and becomes the NaN code. Padding slots, out-of-range slots, the
- *   untouched entries and duplicate slots: as mla_cache_write. */
+ *   a NaN does not count and becomes the NaN code. Padding slots, out-of-range slots and the
+ *   untouched entries: as mla_cache_write. Duplicate slots: the entry's bytes are
+ *   unspecified (codes of one token may stand beside a scale of another). */
 mla_status mla_cache_write_ds_mla(mla_dtype src_dtype, mla_tensor cache, mla_tensor kv_c,
                                   mla_tensor k_pe, const int64_t* slot_mapping, int64_t num_tokens,
                                   void* stream);
@@ -366,6 +367,13 @@ mla_status mla_cache_read_ds_mla(mla_dtype dst_dtype, mla_tensor out, mla_tensor
  *   rows ending with its own, and the sequence's first `sinks` >= 0 rows). Rows outside are
  *   never used, whatever they hold, and the block ids of pages without an attended row are not
  *   read: such pages may have been freed. num_splits beyond 4096 counts as 4096.
+ *   A query that attends a row whose block id lies outside the cache gets unspecified values,
+ *   and mla_device_error reports it; other queries are not affected.
+ *   The tensor cores take bf16 with kv_lora_rank 512, rope_dim 64 or 0, up to 128 heads, a
+ *   positive softmax_scale, pages of 8, 16 or 32 rows or a multiple of 64, and q_cat, o_lat_out
+ *   and cache with 16-byte aligned data and strides that are multiples of 8 elements. Any
+ *   other call runs on the CUDA cores, to the same definition and, where there is much to
+ *   compute, 20 to 150 times slower.
  *   workspace: at least mla_decode_window_workspace_size(...) bytes, 256-byte aligned,
  *   caller-owned, not used by concurrent calls. */
 mla_status mla_decode_window(mla_dtype dtype, mla_tensor o_lat_out, float* lse_out,
@@ -386,9 +394,11 @@ size_t mla_decode_window_workspace_size(int32_t batch, int32_t num_heads, int32_
  *   (a chunk longer than its cache) attends nothing: o = 0, lse = -inf. Rows of q_cat outside
  *   every sequence (before cu_seqlens_q[0], at or behind cu_seqlens_q[batch]) leave their rows
  *   of o_lat_out and lse_out as they were; so do all rows where cu_seqlens_q decreases or
- *   leaves [0, tokens], which mla_device_error reports (MLA_ERR_DEVICE_DATA). Rows that no query of the chunk attends are never
- *   used, whatever they hold, and the block ids of pages without an attended row are not read;
- *   a row that some query of the chunk attends must hold finite values.
+ *   leaves [0, tokens], which mla_device_error reports (MLA_ERR_DEVICE_DATA). Rows that no
+ *   query of the chunk attends are never used, whatever they hold, and the block ids of pages
+ *   without an attended row are not read; a row that some query of the chunk attends must hold
+ *   finite values. Block ids outside the cache, and what the tensor cores take: as
+ *   mla_decode_window.
  *   workspace: at least mla_prefill_window_workspace_size(tokens, ...) bytes (tokens = rows of
  *   q_cat), 256-byte aligned, caller-owned, not used by concurrent calls. */
 mla_status mla_prefill_window(mla_dtype dtype, mla_tensor o_lat_out, float* lse_out,

@@ -8,7 +8,10 @@
 // One pass with the running maximum and sum of a softmax: m the reference maximum (raised
 // only when a tile's maximum exceeds it by more than 8 in base 2, so P stays below 2^8),
 // l = sum of the float32 weights, O += bf16(P) V in float32. The weights' rounding to bf16
-// is the only rounding between the inputs and the output's own.
+// is the only rounding between the inputs and the output's own: the tensor cores take them
+// no wider. l sums them unrounded, so that the log-sum-exp is float32's; an output that one key
+// dominates is off by its weight's rounding then, up to 2^-8 of itself, which the sum of the
+// rounded weights would cancel there and carry into the log-sum-exp instead.
 //
 // Tile. 128 query rows (heads of one token, or several tokens' heads) x 128 keys, by a
 // cluster of two CTAs. The rows are split: each CTA owns 64 of them, so that its output
