@@ -43,17 +43,18 @@
 // Work. A row tile's key tiles are cut over the clusters where that shortens the longest one's list
 // (window_sched.cu); the pieces' float32 outputs and log-sum-exps are joined by a second kernel.
 //
-// What bounds it and what it measured (152 SMs, 76 clusters):
-//   prefill of 4 x 1024 tokens, 128 heads, window 2048: 1.40 to 1.44 ms, 1.6 PFLOP/s, 83% of a dense
-//     library product's rate. A tile takes some 3200 cycles a cluster, its MMAs 2176 of them. Shared
-//     memory holds two tiles of keys, so the next but one waits for PV to leave its place, for its load
-//     (1400 cycles: the 64 KB a CTA come at 50 bytes a cycle), for its QK, which PV then follows.
-//   decode of 64 sequences of 1K to 16K rows, 128 heads, window 4096: 69.5 us, 4.2 TB/s; 6 TB/s between
+// What bounds it and what it measured (152 SMs, 76 clusters; device times of replayed graphs):
+//   prefill of 4 x 1024 tokens, 128 heads, window 2048: 1.40 ms, 1.6 PFLOP/s, in a short run, 84% of a
+//     dense library product's rate; 1.5 ms a call, 1.45 PFLOP/s, under the power cap. A tile takes some
+//     3200 cycles a cluster, its MMAs 2176 of them. Shared memory holds two tiles of keys, so the next
+//     but one waits for PV to leave its place, for its load (1400 cycles: the 64 KB a CTA come at 50
+//     bytes a cycle), for its QK, which PV then follows.
+//   decode of 64 sequences of 1K to 16K rows, 128 heads, window 4096: 69.4 us, 4.2 TB/s; 6 TB/s between
 //     a start of 11 us (schedule, first loads) and the last outputs.
-//   prefill of ragged prompts, 64 heads, window 777: 109 us for 82 GFLOP, bounded by what a row tile
+//   prefill of ragged prompts, 64 heads, window 777: 106 us for 82 GFLOP, bounded by what a row tile
 //     costs beside its 1 to 8 tiles (its queries' load, the pipeline's filling, its output: 4500 cycles
 //     against 2350 a tile).
-//   7 tokens over 16K rows, 128 heads: 40 us for 31 GFLOP: 11 to 12 tiles a cluster, the rest schedule,
+//   7 tokens over 16K rows, 128 heads: 37 us for 31 GFLOP: 11 to 12 tiles a cluster, the rest schedule,
 //     start, float32 pieces and their merge.
 //
 // Every wait is bounded; one that gives up winds both CTAs down and is reported.

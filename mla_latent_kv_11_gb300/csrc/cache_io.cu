@@ -150,9 +150,9 @@ __device__ __forceinline__ uint32_t codes2(float a, float b) {
 // float32, a NaN not at all), at least 2^-126 so that the division stays among normal numbers;
 // its codes are e4m3(x / scale), rounded once: a value is off by at most half an e4m3 step of its own size, 2^-4 of it, or 2^-10 of the group's scale below the
 // smallest normal code. vec: 16-byte aligned source rows; wide: 32-byte aligned latent rows.
-// Bounded by its instructions as much as by memory: it wants warps more than rows in flight. 40961
-// bf16 rows took 17 us with one row's values a warp (48 registers, 40 warps an SM), 21 with two rows'
-// (24 warps); 16.3 with the divisions paired, 4.6 TB/s (float32 rows 20.6 us, 5.9 TB/s).
+// It wants warps more than rows in flight: 40961 bf16 rows from HBM took 17 us with one row's values a warp
+// (48 registers, 40 warps an SM), 21 with two rows' (24 warps); 16.4 with the divisions paired, 4.5 TB/s
+// (13.1 where the rows lie in L2; float32 rows 20.7 us, 5.8 TB/s, and 19.7).
 template <typename T>
 __global__ void __launch_bounds__(256, 5) write_ds_mla_kernel(
     uint8_t* __restrict__ cache, int64_t c_blk, int64_t c_row, int64_t num_rows, int32_t page,
