@@ -411,6 +411,134 @@ mla_status mla_prefill_window(mla_dtype dtype, mla_tensor o_lat_out, float* lse_
 size_t mla_prefill_window_workspace_size(int32_t tokens, int32_t batch, int32_t num_heads,
                                          int32_t kv_lora_rank);
 
+/* Before step 1 - norms and the position rotation of what a layer's projections give: queries
+ * as steps 1 and 2 take them, and rows [c_kv | k_pe] as step 3 writes them. The source pages
+ * name the rotation but give no formula, and have no counterpart of these calls.
+ *   Queries: q [T,H,P+R]; weight [H,P+R] or [1,P+R] (broadcast to every head), or rank 0 for no
+ *   norm. With x a head of q, y = x * weight / sqrt(mean(x^2) + eps), the mean over all P+R
+ *   columns (no norm: y = x);
+ *     q_nope_out [T,H,P] = y[0:P],  q_pe_out [T,H,R] = rot(y[P:P+R])   (both written)
+ *   q_pe_out is usually the last R columns of q_cat. Either output may be q's own columns (the
+ *   same data pointer and strides); without a norm such a q_nope_out is not touched. Any other
+ *   overlap is undefined.
+ *   Rows: kv [T,L+R], weight [L]; with c = kv[t,0:L], the row of token t is
+ *     [c * weight / sqrt(mean(c^2) + eps) | rot(kv[t,L:L+R])].
+ *   rot turns pairs (a, b) of the R columns into (a cos - b sin, b cos + a sin): pair i is columns
+ *   2i and 2i+1 where `interleaved` is not 0, else columns i and i + R/2. Its cosine is
+ *   cos_sin[p, i], its sine cos_sin[p, R/2 + i], p = positions[t]: cos_sin is a device float32
+ *   table [num_positions, R] with row stride cos_sin_stride, positions device int64 [T]. R is even;
+ *   with R = 0 both may be NULL.
+ *   Sums (of squares among them), norms and rotations are float32; a value is rounded once, as it
+ *   is stored. A token whose position lies outside the table leaves its outputs and its row as
+ *   they were and is reported by mla_device_error (MLA_ERR_DEVICE_DATA). Slots, padding and
+ *   out-of-range slots: as mla_cache_write; a padding token's queries are computed all the same. */
+mla_status mla_norm_rope_q(mla_dtype dtype, mla_tensor q_nope_out, mla_tensor q_pe_out, mla_tensor q,
+                           mla_tensor weight, float eps, const int64_t* positions,
+                           const float* cos_sin, int64_t cos_sin_stride, int64_t num_positions,
+                           int32_t interleaved, void* stream);
+/* The rows, into a cache of `dtype` [num_blocks, page, L+R]. */
+mla_status mla_norm_rope_cache_write(mla_dtype dtype, mla_tensor cache, mla_tensor kv,
+                                     mla_tensor weight, float eps, const int64_t* positions,
+                                     const float* cos_sin, int64_t cos_sin_stride,
+                                     int64_t num_positions, int32_t interleaved,
+                                     const int64_t* slot_mapping, int64_t num_tokens, void* stream);
+/* The rows, into an e4m3 cache: the float32 row becomes codes as in mla_cache_write_fp8. */
+mla_status mla_norm_rope_cache_write_fp8(mla_dtype src_dtype, mla_tensor cache, mla_tensor kv,
+                                         mla_tensor weight, float eps, const int64_t* positions,
+                                         const float* cos_sin, int64_t cos_sin_stride,
+                                         int64_t num_positions, int32_t interleaved,
+                                         const int64_t* slot_mapping, int64_t num_tokens,
+                                         const float* scale, void* stream);
+/* The rows (L 512, R 64), into ds_mla entries: the float32 row becomes an entry as in
+ * mla_cache_write_ds_mla. */
+mla_status mla_norm_rope_cache_write_ds_mla(mla_dtype src_dtype, mla_tensor cache, mla_tensor kv,
+                                            mla_tensor weight, float eps, const int64_t* positions,
+                                            const float* cos_sin, int64_t cos_sin_stride,
+                                            int64_t num_positions, int32_t interleaved,
+                                            const int64_t* slot_mapping, int64_t num_tokens,
+                                            void* stream);
+/* mla_norm_rope_q and mla_norm_rope_cache_write in one launch. */
+mla_status mla_norm_rope_q_cache_write(mla_dtype dtype, mla_tensor q_nope_out, mla_tensor q_pe_out,
+                                       mla_tensor q, mla_tensor q_weight, mla_tensor cache,
+                                       mla_tensor kv, mla_tensor kv_weight, float eps,
+                                       const int64_t* positions, const float* cos_sin,
+                                       int64_t cos_sin_stride, int64_t num_positions,
+                                       int32_t interleaved, const int64_t* slot_mapping,
+                                       int64_t num_tokens, void* stream);
+
+/* After step 4 - what the queries give each cached row: its attention weight, summed over the
+ * queries that attend it and their heads, added to the row's mass (which mla_cache_evict goes by).
+ * The source pages have no counterpart of these calls.
+ *   mass: device float [batch, mass_rows], row stride mass_stride; q_cat [T,H,E], cache
+ *   [num_blocks, page, E], block table and lengths as in mla_decode and mla_prefill (E = L + R);
+ *   lse: device float [T,H] contiguous, what that decode or prefill gave for these queries;
+ *   softmax_scale the same as there.
+ *   For every row t < seq_lens[b] of a sequence with a query in the call
+ *     mass[b,t] = decay * mass[b,t] + sum over queries i that attend t, and heads h, of
+ *                 e^(softmax_scale * q_cat[i,h] . cache row t - lse[i,h])
+ *   (decay 1 sums up; decay 0 never reads what was there). A decode's query attends every row, a
+ *   prefill's the rows up to its own position, as in mla_prefill. Sums are float32 and their order
+ *   does not change from run to run on a device. A query whose lse is -inf (it attended
+ *   nothing) gives nothing. Masses behind a sequence's rows, and those of sequences without a query
+ *   or without rows, are left as they were; so are masses of rows whose block id lies outside the
+ *   cache, and of sequences whose cu_seqlens_q decrease or leave [0, T], which mla_device_error
+ *   reports (MLA_ERR_DEVICE_DATA), as it does a length beyond the table or mass_rows (which counts
+ *   as the largest that they hold). Rows outside the sequences are never used, whatever they hold.
+ *   The tensor cores take bf16 with E a multiple of 64 up to 576, up to 128 heads, pages of 8, 16 or
+ *   32 rows or a multiple of 64, and q_cat and cache with 16-byte aligned data and strides that are
+ *   multiples of 8 elements; any other call runs on the CUDA cores.
+ *   workspace (prefill): at least mla_prefill_mass_workspace_size() bytes, 256-byte aligned,
+ *   caller-owned, not used by concurrent calls. */
+mla_status mla_decode_mass(mla_dtype dtype, float* mass, int64_t mass_stride, int32_t mass_rows,
+                           mla_tensor q_cat, mla_tensor cache, const int32_t* block_table,
+                           int64_t block_table_stride, int32_t max_blocks, const int32_t* seq_lens,
+                           const float* lse, float softmax_scale, float decay, void* stream);
+mla_status mla_prefill_mass(mla_dtype dtype, float* mass, int64_t mass_stride, int32_t mass_rows,
+                            mla_tensor q_cat, mla_tensor cache, const int32_t* block_table,
+                            int64_t block_table_stride, int32_t max_blocks,
+                            const int32_t* cu_seqlens_q, const int32_t* seq_lens_kv, int32_t batch,
+                            const float* lse, float softmax_scale, float decay, void* workspace,
+                            size_t workspace_bytes, void* stream);
+size_t mla_prefill_mass_workspace_size(void);
+
+/* Eviction - each sequence of a paged cache cut to its `budget` heaviest rows, which move
+ * together in their order. The source pages have no counterpart of this call.
+ *   cache [num_blocks, page, W] view of elements of element_bytes (1, 2 or 4) bytes: a plain, an
+ *   e4m3 or a ds_mla cache; rows move bit for bit. block_table: device int32 [batch, max_blocks],
+ *   row stride block_table_stride; seq_lens: device int32 [batch].
+ *   mass: device float [batch, mass_rows], row stride mass_stride (mla_decode_mass and
+ *   mla_prefill_mass add to it): mass[b, t] is row t's weight in sequence b.
+ *   With n = seq_lens[b] <= budget every row stays. Else the rows t < sinks, the rows
+ *   t >= n - recent (sinks + recent <= budget) and, of the others, the heaviest up to `budget` rows in
+ *   all stay; of equal masses the lowest row stays first, -0 equals 0, a NaN is the heaviest. The
+ *   rows that stay, in ascending order t_0 < t_1 < .., become rows 0, 1, ..:
+ *     row j of sequence b (block block_table_out[b, j / page], offset j % page) = row t_j
+ *     mass_out[b, j] = mass[b, t_j];  mass_out[b, j] = 0 for the j < n behind them
+ *     seq_lens_out[b] = their count;  kept_out[b, j] = t_j, and -1 behind them (device int32
+ *     [batch, budget], or NULL)
+ *   What lies in the cache behind the rows that stay is left as it was, and so is mass_out from
+ *   row n on. Rows keep the position they were rotated for: a row's place in the cache no longer
+ *   is its position.
+ *   block_table_out NULL: the rows move within their pages. Else each of its blocks is the one that
+ *   block_table names in the same place, or one that no row of the call lies in; a page that two
+ *   sequences share must not be written (give others). mass_out NULL (or mass, with its strides): in
+ *   place; else the two do not overlap. seq_lens_out may be seq_lens.
+ *   A row whose block id, old or new, lies outside the cache or the table is not moved and is
+ *   reported by mla_device_error (MLA_ERR_DEVICE_DATA); the ids of pages from which and to which no
+ *   row moves need not name a block of the cache. A length beyond the table or mass_rows is
+ *   reported and counts as the largest that they hold.
+ *   workspace: device scratch of at least mla_cache_evict_workspace_size(batch, mass_rows, budget)
+ *   bytes, 256-byte aligned, caller-owned, not used by concurrent calls. */
+mla_status mla_cache_evict(int32_t element_bytes, mla_tensor cache, float* mass, int64_t mass_stride,
+                           int32_t mass_rows, const int32_t* block_table,
+                           int64_t block_table_stride, int32_t max_blocks, const int32_t* seq_lens,
+                           int32_t batch, int32_t budget, int32_t sinks, int32_t recent,
+                           const int32_t* block_table_out, int64_t block_table_out_stride,
+                           int32_t max_blocks_out, float* mass_out, int64_t mass_out_stride,
+                           int32_t mass_out_rows, int32_t* seq_lens_out, int32_t* kept_out,
+                           void* workspace, size_t workspace_bytes, void* stream);
+size_t mla_cache_evict_workspace_size(int32_t batch, int32_t rows, int32_t budget);
+
 /* Bytes of the static scratch behind mla_decode_noalloc (40 MiB). */
 #define MLA_DECODE_NOALLOC_SCRATCH_BYTES (40u * 1024u * 1024u)
 

@@ -88,6 +88,21 @@ def lib() -> ctypes.CDLL:
             "mla_prefill_window": ([ctypes.c_int, T, P, T, T, P, I64, I32, P, P, I32, I32, I32, F32, I32, I32, P, SZ,
                                     P], ctypes.c_int),
             "mla_prefill_window_workspace_size": ([I32, I32, I32, I32], SZ),
+            "mla_norm_rope_q": ([ctypes.c_int, T, T, T, T, F32, P, P, I64, I64, I32, P], ctypes.c_int),
+            "mla_norm_rope_cache_write": ([ctypes.c_int, T, T, T, F32, P, P, I64, I64, I32, P, I64, P], ctypes.c_int),
+            "mla_norm_rope_cache_write_fp8": ([ctypes.c_int, T, T, T, F32, P, P, I64, I64, I32, P, I64, P, P],
+                                              ctypes.c_int),
+            "mla_norm_rope_cache_write_ds_mla": ([ctypes.c_int, T, T, T, F32, P, P, I64, I64, I32, P, I64, P],
+                                                 ctypes.c_int),
+            "mla_norm_rope_q_cache_write": ([ctypes.c_int, T, T, T, T, T, T, T, F32, P, P, I64, I64, I32, P, I64, P],
+                                            ctypes.c_int),
+            "mla_decode_mass": ([ctypes.c_int, P, I64, I32, T, T, P, I64, I32, P, P, F32, F32, P], ctypes.c_int),
+            "mla_prefill_mass": ([ctypes.c_int, P, I64, I32, T, T, P, I64, I32, P, P, I32, P, F32, F32, P, SZ, P],
+                                 ctypes.c_int),
+            "mla_prefill_mass_workspace_size": ([], SZ),
+            "mla_cache_evict": ([I32, T, P, I64, I32, P, I64, I32, P, I32, I32, I32, I32, P, I64, I32, P, I64, I32, P, P, P,
+                                 SZ, P], ctypes.c_int),
+            "mla_cache_evict_workspace_size": ([I32, I32, I32], SZ),
             "mla_device_error": ([P], ctypes.c_int),
             "mla_check_bounded_wait": ([ctypes.c_uint32, P], ctypes.c_int),
         }
@@ -586,6 +601,181 @@ def mla_prefill_window(o_lat_out, q_cat, cache, block_table, cu_seqlens_q, seq_l
                                     _table_stride(block_table), block_table.shape[1], _ptr(cu_seqlens_q),
                                     _ptr(seq_lens_kv), batch, kv_lora_rank, rope_dim, softmax_scale, window, sinks,
                                     *_workspace_args(workspace), _stream_on(stream, device)))
+
+
+def _angle_args(positions, cos_sin, tokens: int, eps: float):
+    """eps, positions, table, its row stride, its rows."""
+    import torch
+    if positions.dtype != torch.int64 or positions.dim() != 1 or positions.numel() != tokens or not positions.is_contiguous():
+        raise MlaError(MLA_ERR_INVALID_ARG, f"positions must be contiguous int64 [{tokens}]")
+    shape = cos_sin.shape
+    if cos_sin.dtype != torch.float32 or len(shape) != 2 or (cos_sin.numel() and cos_sin.stride(1) != 1):
+        raise MlaError(MLA_ERR_INVALID_ARG, "cos_sin must be float32 [positions, rope width] with unit column stride")
+    return eps, _ptr(positions), _ptr(cos_sin), _table_stride(cos_sin), shape[0]
+
+
+def _check_rope(cos_sin, rope: int) -> None:
+    if cos_sin.shape[1] != rope:
+        raise MlaError(MLA_ERR_INVALID_ARG, f"cos_sin holds {cos_sin.shape[1]} values a position, the rope is {rope} wide")
+
+
+def _head_weight(weight) -> MlaTensor:
+    """A norm's weight [H, W], or [W] for every head alike; None: no norm."""
+    if weight is None:
+        return MlaTensor()
+    return as_mla_tensor(weight.unsqueeze(0) if weight.dim() == 1 else weight)
+
+
+def _rows_of(t, rank: int, name: str) -> int:
+    if t.dim() != rank:
+        raise MlaError(MLA_ERR_INVALID_ARG, f"{name} must have {rank} dimensions")
+    return t.shape[0]
+
+
+def mla_norm_rope_q(q_nope_out, q_pe_out, q, weight, positions, cos_sin, eps: float = 1e-6, interleaved: bool = True,
+                    stream=None) -> None:
+    """Norm (weight [P+R], [H,P+R] or None for none) and rotation of query heads: q [T,H,P+R] becomes q_nope_out
+    [T,H,P] and q_pe_out [T,H,R] (usually q_cat's last columns); either may be q's own columns. positions int64 [T]
+    into cos_sin float32 [positions, R] (R/2 cosines, R/2 sines)."""
+    angles = _angle_args(positions, cos_sin, _rows_of(q, 3, "q"), eps)
+    _check_rope(cos_sin, q_pe_out.shape[-1])
+    device = _check_device(q, q_nope_out, q_pe_out, weight, positions, cos_sin)
+    _check(lib().mla_norm_rope_q(_dtype_code(q, q_nope_out, q_pe_out, weight), as_mla_tensor(q_nope_out),
+                                 as_mla_tensor(q_pe_out), as_mla_tensor(q), _head_weight(weight), *angles,
+                                 int(interleaved), _stream_on(stream, device)))
+
+
+def _norm_rows_args(cache, kv, weight, positions, cos_sin, slot_mapping, eps):
+    angles = _angle_args(positions, cos_sin, _rows_of(kv, 2, "kv"), eps)
+    _check_rope(cos_sin, kv.shape[1] - _rows_of(weight, 1, "weight"))
+    _check_slots(slot_mapping)
+    return (as_mla_tensor(cache), as_mla_tensor(kv), as_mla_tensor(weight), *angles), \
+        _check_device(cache, kv, weight, positions, cos_sin, slot_mapping)
+
+
+def mla_norm_rope_cache_write(cache, kv, weight, positions, cos_sin, slot_mapping, eps: float = 1e-6,
+                              interleaved: bool = True, stream=None) -> None:
+    """Step 3 from a projection's output: row s of the cache = [kv[i,:L] normalised by weight [L] | kv[i,L:] rotated]
+    for s = slot_mapping[i] >= 0; angles as mla_norm_rope_q."""
+    args, device = _norm_rows_args(cache, kv, weight, positions, cos_sin, slot_mapping, eps)
+    _check(lib().mla_norm_rope_cache_write(_dtype_code(cache, kv, weight), *args, int(interleaved), _ptr(slot_mapping),
+                                           slot_mapping.numel(), _stream_on(stream, device)))
+
+
+def mla_norm_rope_cache_write_fp8(cache, kv, weight, positions, cos_sin, slot_mapping, scale, eps: float = 1e-6,
+                                  interleaved: bool = True, stream=None) -> None:
+    """mla_norm_rope_cache_write into an e4m3 cache: row s = e4m3(the float32 row / scale)."""
+    cache = _fp8_cache(cache)
+    args, device = _norm_rows_args(cache, kv, weight, positions, cos_sin, slot_mapping, eps)
+    _check_device(kv, scale)
+    _check(lib().mla_norm_rope_cache_write_fp8(_dtype_code(kv, weight), *args, int(interleaved), _ptr(slot_mapping),
+                                               slot_mapping.numel(), _f32_scalar(scale, "scale"),
+                                               _stream_on(stream, device)))
+
+
+def mla_norm_rope_cache_write_ds_mla(cache, kv, weight, positions, cos_sin, slot_mapping, eps: float = 1e-6,
+                                     interleaved: bool = True, stream=None) -> None:
+    """mla_norm_rope_cache_write into fp8 ds_mla entries (kv [T,576], weight [512]), as mla_cache_write_ds_mla."""
+    cache = _ds_mla_cache(cache)
+    args, device = _norm_rows_args(cache, kv, weight, positions, cos_sin, slot_mapping, eps)
+    _check(lib().mla_norm_rope_cache_write_ds_mla(_dtype_code(kv, weight), *args, int(interleaved), _ptr(slot_mapping),
+                                                  slot_mapping.numel(), _stream_on(stream, device)))
+
+
+def mla_norm_rope_q_cache_write(q_nope_out, q_pe_out, q, q_weight, cache, kv, kv_weight, positions, cos_sin, slot_mapping,
+                                eps: float = 1e-6, interleaved: bool = True, stream=None) -> None:
+    """mla_norm_rope_q(q_nope_out, q_pe_out, q, q_weight, ..) and mla_norm_rope_cache_write(cache, kv, kv_weight, ..)
+    in one launch."""
+    args, device = _norm_rows_args(cache, kv, kv_weight, positions, cos_sin, slot_mapping, eps)
+    _check_device(kv, q, q_nope_out, q_pe_out, q_weight)
+    _check(lib().mla_norm_rope_q_cache_write(_dtype_code(q, q_nope_out, q_pe_out, q_weight, cache, kv, kv_weight),
+                                             as_mla_tensor(q_nope_out), as_mla_tensor(q_pe_out), as_mla_tensor(q),
+                                             _head_weight(q_weight), *args, int(interleaved), _ptr(slot_mapping),
+                                             slot_mapping.numel(), _stream_on(stream, device)))
+
+
+def _check_mass(mass, batch: int, name: str = "mass") -> None:
+    import torch
+    shape = mass.shape
+    if mass.dtype != torch.float32 or len(shape) != 2 or shape[0] != batch or (mass.stride(1) != 1 and mass.numel()):
+        raise MlaError(MLA_ERR_INVALID_ARG, f"{name} must be float32 [{batch}, rows] with unit row stride")
+
+
+def mla_decode_mass(mass, q_cat, cache, block_table, seq_lens, lse, softmax_scale: float, decay: float = 1.0,
+                    stream=None) -> None:
+    """What one query a sequence gives each row: mass[b,t] (float32 [B, rows]) = decay * mass[b,t] + its attention weight
+    summed over heads, from the decode's lse [B,H]; q_cat [B,H,L+R], cache, block_table, seq_lens as mla_decode."""
+    B, _ = _rows_and_heads(q_cat)
+    _check_table(block_table, B)
+    _check_counts(seq_lens, B, "seq_lens")
+    _check_mass(mass, B)
+    _check_lse(lse, q_cat)
+    device = _check_device(mass, q_cat, cache, block_table, seq_lens, lse)
+    _check(lib().mla_decode_mass(_dtype_code(q_cat, cache), _ptr(mass), _table_stride(mass), mass.shape[1],
+                                 as_mla_tensor(q_cat), as_mla_tensor(cache), _ptr(block_table), _table_stride(block_table),
+                                 block_table.shape[1], _ptr(seq_lens), _ptr(lse), softmax_scale, decay,
+                                 _stream_on(stream, device)))
+
+
+def mla_prefill_mass_workspace_size() -> int:
+    return int(lib().mla_prefill_mass_workspace_size())
+
+
+def mla_prefill_mass(mass, q_cat, cache, block_table, cu_seqlens_q, seq_lens_kv, lse, softmax_scale: float,
+                     decay: float = 1.0, workspace=None, stream=None) -> None:
+    """mla_decode_mass for a chunk of causal queries a sequence: q_cat and lse as mla_prefill had and gave them."""
+    batch = seq_lens_kv.numel()
+    _rows_and_heads(q_cat)
+    _check_table(block_table, batch)
+    _check_counts(seq_lens_kv, batch, "seq_lens_kv")
+    _check_counts(cu_seqlens_q, batch + 1, "cu_seqlens_q")
+    _check_mass(mass, batch)
+    _check_lse(lse, q_cat)
+    device = _check_device(mass, q_cat, cache, block_table, cu_seqlens_q, seq_lens_kv, lse, workspace)
+    if workspace is None:
+        workspace = _scratch(mla_prefill_mass_workspace_size(), device, stream)
+    _check(lib().mla_prefill_mass(_dtype_code(q_cat, cache), _ptr(mass), _table_stride(mass), mass.shape[1],
+                                  as_mla_tensor(q_cat), as_mla_tensor(cache), _ptr(block_table), _table_stride(block_table),
+                                  block_table.shape[1], _ptr(cu_seqlens_q), _ptr(seq_lens_kv), batch, _ptr(lse), softmax_scale,
+                                  decay, *_workspace_args(workspace), _stream_on(stream, device)))
+
+
+def mla_cache_evict_workspace_size(batch: int, rows: int, budget: int) -> int:
+    return int(lib().mla_cache_evict_workspace_size(batch, rows, budget))
+
+
+def mla_cache_evict(cache, mass, block_table, seq_lens, budget: int, seq_lens_out, sinks: int = 0, recent: int = 0,
+                    block_table_out=None, mass_out=None, kept_out=None, workspace=None, stream=None) -> None:
+    """Cut each sequence to its `budget` heaviest rows (the first `sinks` and the last `recent` stay in any case), which
+    become rows 0, 1, .. in their order, in their pages or in those of block_table_out; masses move along (mass_out, or
+    in place), seq_lens_out int32 [B] gets the lengths, kept_out int32 [B, budget] the old rows (-1 behind the last).
+    cache: a plain, an e4m3 or a ds_mla cache."""
+    batch = seq_lens.numel()
+    cache = cache[:, :, 0] if cache.dim() == 4 and cache.shape[2] == 1 else cache
+    for value, name in ((budget, "budget"), (sinks, "sinks"), (recent, "recent")):
+        _check_int32(value, name)
+    _check_table(block_table, batch)
+    _check_counts(seq_lens, batch, "seq_lens")
+    _check_counts(seq_lens_out, batch, "seq_lens_out")
+    _check_mass(mass, batch)
+    table_out, out = (None, 0, 0), (None, 0, 0)
+    if block_table_out is not None:
+        _check_table(block_table_out, batch)
+        if block_table_out.data_ptr() != block_table.data_ptr() or block_table_out.shape != block_table.shape or \
+                block_table_out.stride() != block_table.stride():
+            table_out = _ptr(block_table_out), _table_stride(block_table_out), block_table_out.shape[1]
+    if mass_out is not None:
+        _check_mass(mass_out, batch, "mass_out")
+        out = _ptr(mass_out), _table_stride(mass_out), mass_out.shape[1]
+    if kept_out is not None:
+        _check_counts(kept_out.reshape(-1) if kept_out.is_contiguous() else kept_out, batch * budget, "kept_out")
+    device = _check_device(cache, mass, block_table, seq_lens, seq_lens_out, block_table_out, mass_out, kept_out, workspace)
+    if workspace is None:
+        workspace = _scratch(mla_cache_evict_workspace_size(batch, mass.shape[1], budget), device, stream)
+    _check(lib().mla_cache_evict(cache.element_size(), as_mla_tensor(cache), _ptr(mass), _table_stride(mass), mass.shape[1],
+                                 _ptr(block_table), _table_stride(block_table), block_table.shape[1], _ptr(seq_lens), batch,
+                                 budget, sinks, recent, *table_out, *out, _ptr(seq_lens_out), _ptr(kept_out),
+                                 *_workspace_args(workspace), _stream_on(stream, device)))
 
 
 def mla_check_bounded_wait(limit_us: int, stream=None) -> None:

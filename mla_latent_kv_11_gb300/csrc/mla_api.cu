@@ -885,6 +885,272 @@ mla_status mla_prefill_window(mla_dtype dtype, mla_tensor o_lat_out, float* lse_
   return run_window(dtype, c, 0, workspace, (cudaStream_t)stream, "mla_prefill_window");
 }
 
+// ---- norms and rotations of new queries and rows -------------------------------------------
+
+namespace {
+// The angles' arguments, for `tokens` > 0 tokens.
+mla_status plan_angles(const int64_t* positions, const float* cos_sin, int64_t stride, int64_t count, float eps,
+                       int32_t interleaved, int64_t tokens, int64_t R, NormRopeCall* c) {
+  if (!(eps >= 0.f)) return fail(MLA_ERR_INVALID_ARG, "eps must be >= 0");
+  if (R % 2 != 0) return fail(MLA_ERR_INVALID_ARG, "rope width %lld is odd", (long long)R);
+  if (tokens > INT32_MAX || R > INT32_MAX) return fail(MLA_ERR_UNSUPPORTED, "too many tokens or rope columns");
+  if (tokens > 0 && R > 0) {
+    if (positions == nullptr || cos_sin == nullptr)
+      return fail(MLA_ERR_INVALID_ARG, "positions and cos_sin must be non-null");
+    if (count <= 0 || stride < R) return fail(MLA_ERR_INVALID_ARG, "cos_sin must be [num_positions > 0, rope width]");
+  }
+  c->tokens = tokens;
+  c->R = (int32_t)R;
+  c->eps = eps;
+  c->interleaved = interleaved != 0;
+  c->positions = positions;
+  c->cos_sin = cos_sin;
+  c->cos_sin_stride = stride;
+  c->num_positions = count;
+  return MLA_OK;
+}
+
+mla_status plan_norm_q(const mla_tensor& q_nope_out, const mla_tensor& q_pe_out, const mla_tensor& q,
+                       const mla_tensor& weight, NormRopeCall* c) {
+  MLA_TRY(check_view(q, 3, "q"));
+  MLA_TRY(check_view(q_nope_out, 3, "q_nope_out"));
+  MLA_TRY(check_view(q_pe_out, 3, "q_pe_out"));
+  const int64_t T = q.shape[0], H = q.shape[1], P = q_nope_out.shape[2], R = q_pe_out.shape[2];
+  if (q_nope_out.shape[0] != T || q_nope_out.shape[1] != H || q_pe_out.shape[0] != T || q_pe_out.shape[1] != H)
+    return fail(MLA_ERR_INVALID_ARG, "q_nope_out and q_pe_out must have q's tokens and heads, [%lld,%lld,.]", (long long)T,
+                (long long)H);
+  if (q.shape[2] != P + R)
+    return fail(MLA_ERR_INVALID_ARG, "q width %lld != P + R = %lld", (long long)q.shape[2], (long long)(P + R));
+  if (P + R > INT32_MAX) return fail(MLA_ERR_UNSUPPORTED, "q: heads too wide");
+  c->q_weight = nullptr;
+  if (weight.rank != 0) {
+    MLA_TRY(check_view(weight, 2, "q weight"));
+    if ((weight.shape[0] != H && weight.shape[0] != 1) || weight.shape[1] != P + R)
+      return fail(MLA_ERR_INVALID_ARG, "q weight must be [H,P+R] or [1,P+R], or have rank 0 for no norm");
+    c->q_weight = weight.data;
+    c->q_weight_s0 = weight.shape[0] == 1 ? 0 : weight.stride[0];
+  }
+  if (T > 0 && H > INT32_MAX / T) return fail(MLA_ERR_UNSUPPORTED, "too many query heads in one call");
+  c->H = (int32_t)(P + R > 0 ? H : 0);
+  c->P = (int32_t)P;
+  c->q = view3(q);
+  c->q_nope = view3(q_nope_out);
+  c->q_pe = view3(q_pe_out);
+  return MLA_OK;
+}
+
+// The rows' part: `width` is the cache's entry (0: L + R).
+mla_status plan_norm_rows(const mla_tensor& cache, bool ds_mla, const mla_tensor& kv, const mla_tensor& weight,
+                          const int64_t* slot_mapping, int64_t num_tokens, int64_t* R, NormRopeCall* c) {
+  if (num_tokens < 0) return fail(MLA_ERR_INVALID_ARG, "num_tokens < 0");
+  MLA_TRY(check_view(kv, 2, "kv"));
+  MLA_TRY(check_view(weight, 1, "kv weight"));
+  const int64_t L = weight.shape[0], E = kv.shape[1];
+  if (L <= 0 || L > E)
+    return fail(MLA_ERR_INVALID_ARG, "kv weight must be [L] with 0 < L <= kv width %lld, got %lld", (long long)E, (long long)L);
+  if (ds_mla) {
+    if (L != kDsMlaLatent || E != kDsMlaLatent + kDsMlaRope)
+      return fail(MLA_ERR_INVALID_ARG, "a ds_mla entry takes kv [T,576] and a weight of 512, got %lld and %lld", (long long)E,
+                  (long long)L);
+    MLA_TRY(check_ds_mla_cache(cache));
+  } else {
+    MLA_TRY(check_cache(cache, E, "cache"));
+  }
+  if (E > INT32_MAX) return fail(MLA_ERR_UNSUPPORTED, "kv: rows too wide");
+  if (kv.shape[0] != num_tokens)
+    return fail(MLA_ERR_INVALID_ARG, "kv rows (%lld) != num_tokens %lld", (long long)kv.shape[0], (long long)num_tokens);
+  if (num_tokens > 0 && slot_mapping == nullptr) return fail(MLA_ERR_INVALID_ARG, "slot_mapping is null");
+  *R = E - L;
+  c->L = (int32_t)L;
+  c->rows = true;
+  c->ds_mla = ds_mla;
+  c->cache = view3(cache);
+  c->kv = View3{kv.data, kv.shape[0], 1, kv.shape[1], kv.stride[0], 0, 1};
+  c->kv_weight = weight.data;
+  c->slots = slot_mapping;
+  return MLA_OK;
+}
+
+mla_status norm_rows(mla_dtype dtype, mla_tensor cache, bool ds_mla, bool fp8, mla_tensor kv, mla_tensor weight, float eps,
+                     const int64_t* positions, const float* cos_sin, int64_t cos_sin_stride, int64_t num_positions,
+                     int32_t interleaved, const int64_t* slot_mapping, int64_t num_tokens, const float* scale, void* stream,
+                     const char* name) {
+  g_msg[0] = 0;
+  NormRopeCall c{};
+  int64_t R = 0;
+  MLA_TRY(check_dtype(dtype));
+  MLA_TRY(plan_norm_rows(cache, ds_mla, kv, weight, slot_mapping, num_tokens, &R, &c));
+  MLA_TRY(plan_angles(positions, cos_sin, cos_sin_stride, num_positions, eps, interleaved, num_tokens, R, &c));
+  if (num_tokens == 0) return MLA_OK;
+  if (fp8 && scale == nullptr) return fail(MLA_ERR_INVALID_ARG, "scale is null");
+  c.scale = scale;
+  return cuda_status(launch_norm_rope(dtype, c, (cudaStream_t)stream), name);
+}
+}  // namespace
+
+mla_status mla_norm_rope_q(mla_dtype dtype, mla_tensor q_nope_out, mla_tensor q_pe_out, mla_tensor q, mla_tensor weight,
+                           float eps, const int64_t* positions, const float* cos_sin, int64_t cos_sin_stride,
+                           int64_t num_positions, int32_t interleaved, void* stream) {
+  g_msg[0] = 0;
+  NormRopeCall c{};
+  MLA_TRY(check_dtype(dtype));
+  MLA_TRY(plan_norm_q(q_nope_out, q_pe_out, q, weight, &c));
+  MLA_TRY(plan_angles(positions, cos_sin, cos_sin_stride, num_positions, eps, interleaved, q.shape[0], q_pe_out.shape[2], &c));
+  if (numel(q) == 0) return MLA_OK;
+  return cuda_status(launch_norm_rope(dtype, c, (cudaStream_t)stream), "mla_norm_rope_q");
+}
+
+mla_status mla_norm_rope_cache_write(mla_dtype dtype, mla_tensor cache, mla_tensor kv, mla_tensor weight, float eps,
+                                     const int64_t* positions, const float* cos_sin, int64_t cos_sin_stride,
+                                     int64_t num_positions, int32_t interleaved, const int64_t* slot_mapping,
+                                     int64_t num_tokens, void* stream) {
+  return norm_rows(dtype, cache, false, false, kv, weight, eps, positions, cos_sin, cos_sin_stride, num_positions, interleaved,
+                   slot_mapping, num_tokens, nullptr, stream, "mla_norm_rope_cache_write");
+}
+
+mla_status mla_norm_rope_cache_write_fp8(mla_dtype src_dtype, mla_tensor cache, mla_tensor kv, mla_tensor weight, float eps,
+                                         const int64_t* positions, const float* cos_sin, int64_t cos_sin_stride,
+                                         int64_t num_positions, int32_t interleaved, const int64_t* slot_mapping,
+                                         int64_t num_tokens, const float* scale, void* stream) {
+  return norm_rows(src_dtype, cache, false, true, kv, weight, eps, positions, cos_sin, cos_sin_stride, num_positions,
+                   interleaved, slot_mapping, num_tokens, scale, stream, "mla_norm_rope_cache_write_fp8");
+}
+
+mla_status mla_norm_rope_cache_write_ds_mla(mla_dtype src_dtype, mla_tensor cache, mla_tensor kv, mla_tensor weight, float eps,
+                                            const int64_t* positions, const float* cos_sin, int64_t cos_sin_stride,
+                                            int64_t num_positions, int32_t interleaved, const int64_t* slot_mapping,
+                                            int64_t num_tokens, void* stream) {
+  return norm_rows(src_dtype, cache, true, false, kv, weight, eps, positions, cos_sin, cos_sin_stride, num_positions,
+                   interleaved, slot_mapping, num_tokens, nullptr, stream, "mla_norm_rope_cache_write_ds_mla");
+}
+
+mla_status mla_norm_rope_q_cache_write(mla_dtype dtype, mla_tensor q_nope_out, mla_tensor q_pe_out, mla_tensor q,
+                                       mla_tensor q_weight, mla_tensor cache, mla_tensor kv, mla_tensor kv_weight, float eps,
+                                       const int64_t* positions, const float* cos_sin, int64_t cos_sin_stride,
+                                       int64_t num_positions, int32_t interleaved, const int64_t* slot_mapping,
+                                       int64_t num_tokens, void* stream) {
+  g_msg[0] = 0;
+  NormRopeCall c{};
+  int64_t R = 0;
+  MLA_TRY(check_dtype(dtype));
+  MLA_TRY(plan_norm_q(q_nope_out, q_pe_out, q, q_weight, &c));
+  MLA_TRY(plan_norm_rows(cache, false, kv, kv_weight, slot_mapping, num_tokens, &R, &c));
+  if (q.shape[0] != num_tokens)
+    return fail(MLA_ERR_INVALID_ARG, "q tokens (%lld) != num_tokens %lld", (long long)q.shape[0], (long long)num_tokens);
+  if (q_pe_out.shape[2] != R)
+    return fail(MLA_ERR_INVALID_ARG, "q rope width %lld, kv rope width %lld", (long long)q_pe_out.shape[2], (long long)R);
+  MLA_TRY(plan_angles(positions, cos_sin, cos_sin_stride, num_positions, eps, interleaved, num_tokens, R, &c));
+  if (num_tokens == 0) return MLA_OK;
+  return cuda_status(launch_norm_rope(dtype, c, (cudaStream_t)stream), "mla_norm_rope_q_cache_write");
+}
+
+// ---- what the queries give each row ---------------------------------------------------------
+
+namespace {
+mla_status mass_call(mla_dtype dtype, float* mass, int64_t mass_stride, int32_t mass_rows, const mla_tensor& q_cat,
+                     const mla_tensor& cache, const int32_t* block_table, int64_t block_table_stride, int32_t max_blocks,
+                     const int32_t* cu_seqlens_q, const int32_t* seq_lens, int64_t batch, bool decode, const float* lse,
+                     float softmax_scale, float decay, void* workspace, size_t workspace_bytes, void* stream,
+                     const char* name) {
+  g_msg[0] = 0;
+  MLA_TRY(check_dtype(dtype));
+  MLA_TRY(check_view(q_cat, 3, "q_cat"));
+  const int64_t T = q_cat.shape[0], H = q_cat.shape[1], E = q_cat.shape[2];
+  if (E <= 0) return fail(MLA_ERR_INVALID_ARG, "q_cat: rows of no values");
+  MLA_TRY(check_cache(cache, E, "cache"));
+  if (batch < 0) return fail(MLA_ERR_INVALID_ARG, "batch < 0");
+  if (!(softmax_scale - softmax_scale == 0.f) || !(decay - decay == 0.f))
+    return fail(MLA_ERR_INVALID_ARG, "softmax_scale and decay must be finite");
+  if (T == 0 || H == 0 || batch == 0) return MLA_OK;
+  if (T > INT32_MAX / 2 || H > 4096 || batch > 65535) return fail(MLA_ERR_UNSUPPORTED, "too many tokens, heads or sequences");
+  if (E > 1024) return fail(MLA_ERR_UNSUPPORTED, "entry width %lld > 1024", (long long)E);
+  if (mass == nullptr || lse == nullptr || block_table == nullptr || seq_lens == nullptr ||
+      (!decode && cu_seqlens_q == nullptr))
+    return fail(MLA_ERR_INVALID_ARG, "mass, lse, block_table and sequence lengths must be non-null");
+  if (max_blocks <= 0 || block_table_stride < max_blocks)
+    return fail(MLA_ERR_INVALID_ARG, "need 0 < max_blocks <= block_table_stride");
+  if (mass_rows <= 0 || mass_stride < mass_rows) return fail(MLA_ERR_INVALID_ARG, "need 0 < mass_rows <= mass_stride");
+  if (!decode) MLA_TRY(check_workspace(workspace, workspace_bytes, 256));
+  const MassCall c{mass, mass_stride, mass_rows, view3(q_cat),
+                   CacheView{cache.data, cache.stride[0], cache.stride[1], (int32_t)cache.shape[0], (int32_t)cache.shape[1],
+                             (int32_t)cache.shape[2]},
+                   block_table, block_table_stride, max_blocks, cu_seqlens_q, seq_lens, lse, (int32_t)batch, (int32_t)T,
+                   (int32_t)H, softmax_scale, decay};
+  return cuda_status(launch_mass_simt(dtype, c, (cudaStream_t)stream), name);
+}
+}  // namespace
+
+mla_status mla_decode_mass(mla_dtype dtype, float* mass, int64_t mass_stride, int32_t mass_rows, mla_tensor q_cat,
+                           mla_tensor cache, const int32_t* block_table, int64_t block_table_stride, int32_t max_blocks,
+                           const int32_t* seq_lens, const float* lse, float softmax_scale, float decay, void* stream) {
+  return mass_call(dtype, mass, mass_stride, mass_rows, q_cat, cache, block_table, block_table_stride, max_blocks, nullptr,
+                   seq_lens, q_cat.rank == 3 ? q_cat.shape[0] : 0, true, lse, softmax_scale, decay, nullptr, 0, stream,
+                   "mla_decode_mass");
+}
+
+size_t mla_prefill_mass_workspace_size(void) { return 256; }
+
+mla_status mla_prefill_mass(mla_dtype dtype, float* mass, int64_t mass_stride, int32_t mass_rows, mla_tensor q_cat,
+                            mla_tensor cache, const int32_t* block_table, int64_t block_table_stride, int32_t max_blocks,
+                            const int32_t* cu_seqlens_q, const int32_t* seq_lens_kv, int32_t batch, const float* lse,
+                            float softmax_scale, float decay, void* workspace, size_t workspace_bytes, void* stream) {
+  return mass_call(dtype, mass, mass_stride, mass_rows, q_cat, cache, block_table, block_table_stride, max_blocks, cu_seqlens_q,
+                   seq_lens_kv, batch, false, lse, softmax_scale, decay, workspace, workspace_bytes, stream,
+                   "mla_prefill_mass");
+}
+
+// ---- eviction ------------------------------------------------------------------------------
+
+size_t mla_cache_evict_workspace_size(int32_t batch, int32_t rows, int32_t budget) {
+  if (batch < 0 || rows < 0 || budget < 0) return 0;
+  return evict_workspace(batch, rows, budget);
+}
+
+mla_status mla_cache_evict(int32_t element_bytes, mla_tensor cache, float* mass, int64_t mass_stride, int32_t mass_rows,
+                           const int32_t* block_table, int64_t block_table_stride, int32_t max_blocks,
+                           const int32_t* seq_lens, int32_t batch, int32_t budget, int32_t sinks, int32_t recent,
+                           const int32_t* block_table_out, int64_t block_table_out_stride, int32_t max_blocks_out,
+                           float* mass_out, int64_t mass_out_stride, int32_t mass_out_rows, int32_t* seq_lens_out,
+                           int32_t* kept_out, void* workspace, size_t workspace_bytes, void* stream) {
+  g_msg[0] = 0;
+  if (element_bytes != 1 && element_bytes != 2 && element_bytes != 4)
+    return fail(MLA_ERR_INVALID_ARG, "element_bytes must be 1, 2 or 4, got %d", element_bytes);
+  MLA_TRY(check_cache(cache, cache.rank == 3 ? cache.shape[2] : 0, "cache"));
+  if (cache.shape[2] > INT32_MAX / 4) return fail(MLA_ERR_UNSUPPORTED, "cache: entry too wide");
+  if (budget < 1 || sinks < 0 || recent < 0) return fail(MLA_ERR_INVALID_ARG, "need budget >= 1, sinks >= 0, recent >= 0");
+  if ((int64_t)sinks + recent > budget)
+    return fail(MLA_ERR_INVALID_ARG, "sinks %d + recent %d rows do not fit the budget %d", sinks, recent, budget);
+  if (batch < 0) return fail(MLA_ERR_INVALID_ARG, "batch < 0");
+  if (batch > 65535) return fail(MLA_ERR_UNSUPPORTED, "more than 65535 sequences in one call");
+  if (batch == 0) return MLA_OK;
+  if (mass == nullptr || block_table == nullptr || seq_lens == nullptr || seq_lens_out == nullptr)
+    return fail(MLA_ERR_INVALID_ARG, "mass, block_table, seq_lens and seq_lens_out must be non-null");
+  if (max_blocks <= 0 || block_table_stride < max_blocks)
+    return fail(MLA_ERR_INVALID_ARG, "need 0 < max_blocks <= block_table_stride");
+  if (mass_rows <= 0 || mass_stride < mass_rows) return fail(MLA_ERR_INVALID_ARG, "need 0 < mass_rows <= mass_stride");
+  if (block_table_out == nullptr) {
+    block_table_out = block_table;
+    block_table_out_stride = block_table_stride;
+    max_blocks_out = max_blocks;
+  } else if (max_blocks_out <= 0 || block_table_out_stride < max_blocks_out) {
+    return fail(MLA_ERR_INVALID_ARG, "need 0 < max_blocks_out <= block_table_out_stride");
+  }
+  if (mass_out == nullptr) {
+    mass_out = mass;
+    mass_out_stride = mass_stride;
+    mass_out_rows = mass_rows;
+  } else if (mass_out_rows <= 0 || mass_out_stride < mass_out_rows) {
+    return fail(MLA_ERR_INVALID_ARG, "need 0 < mass_out_rows <= mass_out_stride");
+  }
+  MLA_TRY(check_workspace(workspace, workspace_bytes, evict_workspace(batch, mass_rows, budget)));
+  const int64_t es = element_bytes;
+  const EvictCall c{cache.data, cache.stride[0] * es, cache.stride[1] * es, cache.shape[2] * es, (int32_t)cache.shape[0],
+                    (int32_t)cache.shape[1], mass, mass_stride, mass_rows, block_table, block_table_stride, max_blocks,
+                    seq_lens, batch, budget, sinks, recent, block_table_out, block_table_out_stride, max_blocks_out, mass_out,
+                    mass_out_stride, mass_out_rows, seq_lens_out, kept_out};
+  return cuda_status(launch_evict(c, workspace, (cudaStream_t)stream), "mla_cache_evict");
+}
+
 mla_status mla_check_bounded_wait(uint32_t limit_us, void* stream) {
   g_msg[0] = 0;
   if (limit_us == 0 || limit_us > 1000000u)
@@ -898,7 +1164,8 @@ mla_status mla_device_error(void* stream) {
   if (e != cudaSuccess) return cuda_status(e, "mla_device_error: stream synchronize");
   ErrorWords words;
   cudaError_t (*const word_of[ErrorWords::kCount])(unsigned**) = {
-      cache_io_error_word, attn_pair_error_word, window_sched_error_word, window_simt_error_word, bmm_tc_error_word};
+      cache_io_error_word, attn_pair_error_word, window_sched_error_word, window_simt_error_word, bmm_tc_error_word,
+      norm_rope_error_word, evict_error_word, mass_simt_error_word};
   for (int i = 0; i < ErrorWords::kCount && e == cudaSuccess; ++i) e = word_of[i](&words.word[i]);
   // on the legacy stream, as the copies that follow
   if (e == cudaSuccess) e = launch_gather_errors(words, nullptr);

@@ -198,6 +198,69 @@ cudaError_t launch_cache_read(mla_dtype dt, const CacheRead& r, cudaStream_t st)
 cudaError_t launch_cache_read_fp8(mla_dtype dst_dt, const CacheRead& r, const float* scale, cudaStream_t st);
 cudaError_t launch_cache_read_ds_mla(mla_dtype dst_dt, const CacheRead& r, cudaStream_t st);
 
+// Norms and rotations of new queries and cache rows (norm_rope.cu) after validation. H 0: no queries;
+// rows false: no cache rows; scale: e4m3 rows; ds_mla: ds_mla entries; else rows of the call's dtype.
+struct NormRopeCall {
+  int64_t tokens;
+  int32_t H, P, R, L, interleaved;
+  float eps;
+  const int64_t* positions;
+  const float* cos_sin;
+  int64_t cos_sin_stride, num_positions;
+  View3 q, q_nope, q_pe;
+  const void* q_weight;      // null: no norm
+  int64_t q_weight_s0;
+  bool rows, ds_mla;
+  View3 cache, kv;
+  const void* kv_weight;
+  const int64_t* slots;
+  const float* scale;
+};
+cudaError_t launch_norm_rope(mla_dtype dt, const NormRopeCall& c, cudaStream_t st);
+
+// Eviction of the lightest rows (evict.cu) after validation; strides of the cache in bytes.
+struct EvictCall {
+  void* cache;
+  int64_t s_blk, s_row, row_bytes;
+  int32_t num_blocks, page;
+  float* mass;
+  int64_t mass_stride;
+  int32_t mass_rows;
+  const int32_t* block_table;
+  int64_t bt_stride;
+  int32_t max_blocks;
+  const int32_t* seq_lens;
+  int32_t batch, budget, sinks, recent;
+  const int32_t* block_table_out;
+  int64_t bto_stride;
+  int32_t max_blocks_out;
+  float* mass_out;
+  int64_t mass_out_stride;
+  int32_t mass_out_rows;
+  int32_t *seq_lens_out, *kept_out;
+};
+size_t evict_workspace(int64_t batch, int64_t rows, int64_t budget);
+cudaError_t launch_evict(const EvictCall& c, void* ws, cudaStream_t st);
+
+// Row masses after validation: what the queries of a prefill (cu_q [B + 1]) or, with cu_q null, of a
+// decode give each row.
+struct MassCall {
+  float* mass;
+  int64_t mass_stride;
+  int32_t mass_rows;
+  View3 q;                 // [T, H, E]
+  CacheView cache;
+  const int32_t* block_table;
+  int64_t bt_stride;
+  int32_t max_blocks;
+  const int32_t *cu_q, *kv_lens;
+  const float* lse;
+  int32_t B, T, H;
+  float scale, decay;
+};
+// On the CUDA cores (mass_simt.cu).
+cudaError_t launch_mass_simt(mla_dtype dt, const MassCall& c, cudaStream_t st);
+
 // Attention limited to a window and sinks. A query at position p of a sequence attends rows t <= p with
 // t < sinks or t > p - window.
 struct WindowArgs {
@@ -342,7 +405,7 @@ mla_status report_status(mla_status st, const char* fmt, ...);
 // give the word's address on the current device, and one kernel moves their errors into the copy module's
 // word, which is then read (mla_device_error 119 us with a copy and a clearing of each of nine words).
 struct ErrorWords {
-  static constexpr int kCount = 5;
+  static constexpr int kCount = 8;
   unsigned* word[kCount];
 };
 cudaError_t cache_io_error_word(unsigned** word);
@@ -350,6 +413,9 @@ cudaError_t attn_pair_error_word(unsigned** word);
 cudaError_t window_sched_error_word(unsigned** word);
 cudaError_t window_simt_error_word(unsigned** word);
 cudaError_t bmm_tc_error_word(unsigned** word);
+cudaError_t norm_rope_error_word(unsigned** word);
+cudaError_t evict_error_word(unsigned** word);
+cudaError_t mass_simt_error_word(unsigned** word);
 cudaError_t launch_gather_errors(const ErrorWords& words, cudaStream_t st);
 // Read and clear (after the stream was synchronised).
 unsigned copy_errors_read_clear();

@@ -1,0 +1,231 @@
+"""Norms and rotations of query heads and of cache rows against 64 bits, with derived bounds."""
+import pytest
+import torch
+
+import norm_rope_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+EPS = 1e-6
+BF16, F32 = torch.bfloat16, torch.float32
+POSITIONS = 300
+
+# heads, nope, rope, latent
+V3, LITE, NOPE, ODD, WIDE = (128, 128, 64, 512), (16, 128, 64, 512), (64, 256, 0, 512), (3, 7, 6, 20), (5, 1000, 64, 1000)
+
+
+def inputs(seed, tokens, dims, dtype, per_head=True, pad=0):
+    heads, nope, rope, latent = dims
+    g = torch.Generator().manual_seed(seed)
+
+    def draw(*shape):
+        return torch.randn(*shape, generator=g)
+
+    width = nope + rope
+    q = (draw(tokens, heads, width + pad) * torch.exp(draw(tokens, heads, 1))).to(dtype)
+    kv = (draw(tokens, latent + rope + pad) * torch.exp(2 * draw(tokens, 1))).to(dtype)
+    qw = (1 + draw(heads, width) / 4).to(dtype) if per_head else (1 + draw(width) / 4).to(dtype)
+    kw = (1 + draw(latent) / 4).to(dtype)
+    pos = torch.randint(0, POSITIONS, (tokens,), generator=g)
+    return q[..., :width], kv[:, :latent + rope], qw, kw, pos, ref.table(POSITIONS, rope)
+
+
+def slots_of(seed, tokens, rows):
+    order = torch.randperm(rows, generator=torch.Generator().manual_seed(seed))[:tokens]
+    order[::5] = -1
+    return order
+
+
+def gpu(t, offset):
+    """t on the GPU, its data `offset` elements behind an aligned address, its padded strides kept."""
+    flat = torch.full((t.untyped_storage().nbytes() // t.element_size() + offset,), float("nan"), dtype=t.dtype, device="cuda")
+    whole = flat[offset:].as_strided(t.shape, t.stride())
+    whole.copy_(t)
+    return whole
+
+
+@pytest.mark.parametrize("interleaved", [True, False])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("dims,tokens,offset,pad", [(V3, 1, 0, 0), (V3, 19, 0, 8), (LITE, 37, 0, 0), (NOPE, 9, 0, 0), (ODD, 5, 0, 0),
+                                                    (ODD, 33, 1, 3), (LITE, 6, 1, 0), (LITE, 7, 0, 1), (WIDE, 3, 0, 0)])
+@pytest.mark.parametrize("norm", ["none", "all", "per head"])
+def test_queries(mla, interleaved, dtype, dims, tokens, offset, pad, norm):
+    q, _, w, _, pos, cs = inputs(tokens, tokens, dims, dtype, norm == "per head", pad)
+    w = None if norm == "none" else w
+    heads, nope, rope, latent = dims
+    nope_out = torch.full((tokens, heads, nope), float("nan"), dtype=dtype, device="cuda")
+    q_cat = torch.full((tokens, heads, latent + rope), float("nan"), dtype=dtype, device="cuda")
+    dq, dw = gpu(q, offset), None if w is None else w.cuda()
+    mla.mla_norm_rope_q(nope_out, q_cat[..., latent:], dq, dw, pos.cuda(), cs.cuda(), eps=EPS, interleaved=interleaved)
+    mla.mla_device_error()
+    (n, en), (r, er) = ref.queries(q, w, nope, cs[pos], interleaved, EPS)
+    ref.check(nope_out, n, en, dtype, "nope")
+    ref.check(q_cat[..., latent:], r, er, dtype, "rope")
+    assert torch.isnan(q_cat[..., :latent]).all()
+    if norm == "none":
+        assert torch.equal(nope_out.cpu(), q[..., :nope])
+    # in place: the same bits
+    n2, r2 = dq[..., :nope], dq[..., nope:]
+    mla.mla_norm_rope_q(n2, r2, dq, dw, pos.cuda(), cs.cuda(), eps=EPS, interleaved=interleaved)
+    assert torch.equal(n2, nope_out) and torch.equal(r2, q_cat[..., latent:])
+
+
+@pytest.mark.parametrize("interleaved", [True, False])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("dims,tokens,offset,pad,page,layers", [
+    (V3, 1, 0, 0, 64, 1), (V3, 77, 0, 8, 16, 3), (NOPE, 30, 0, 0, 64, 1), (ODD, 41, 1, 3, 5, 2), (LITE, 11, 1, 0, 64, 1),
+    (LITE, 12, 0, 1, 1, 1), (WIDE, 9, 0, 0, 8, 1)])
+def test_rows(mla, interleaved, dtype, dims, tokens, offset, pad, page, layers):
+    _, kv, _, w, pos, cs = inputs(tokens, tokens, dims, dtype, pad=pad)
+    latent, rope = dims[3], dims[2]
+    blocks = -(-tokens // page) + 2
+    whole = torch.full((blocks, layers, page, latent + rope), 7.0, dtype=dtype, device="cuda")
+    slots = slots_of(tokens, tokens, blocks * page)
+    mla.mla_norm_rope_cache_write(whole[:, layers - 1], gpu(kv, offset), w.cuda(), pos.cuda(), cs.cuda(), slots.cuda(),
+                                  eps=EPS, interleaved=interleaved)
+    mla.mla_device_error()
+    want, err = ref.rows(kv, w, cs[pos], interleaved, EPS)
+    real = slots >= 0
+    got = whole[:, layers - 1].reshape(blocks * page, -1).cpu()
+    ref.check(got[slots[real]], want[real], err[real], dtype, "rows")
+    left = torch.ones(blocks * page, dtype=torch.bool)
+    left[slots[real]] = False
+    assert (got[left] == 7).all() and (layers == 1 or (whole[:, :layers - 1] == 7).all())
+
+
+@pytest.mark.parametrize("interleaved", [True, False])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("dims,tokens,offset,pad", [(V3, 1, 0, 0), (V3, 70, 0, 8), (NOPE, 30, 0, 0), (ODD, 41, 1, 3),
+                                                    (LITE, 11, 1, 0), (WIDE, 9, 0, 0)])
+def test_rows_e4m3(mla, interleaved, dtype, dims, tokens, offset, pad):
+    _, kv, _, w, pos, cs = inputs(tokens + 1, tokens, dims, dtype, pad=pad)
+    latent, rope, page = dims[3], dims[2], 16
+    blocks = -(-tokens // page) + 2
+    cache = torch.full((blocks, page, latent + rope), 0x55, dtype=torch.uint8, device="cuda")
+    slots, scale = slots_of(tokens, tokens, blocks * page), 0.0171
+    mla.mla_norm_rope_cache_write_fp8(cache, gpu(kv, offset), w.cuda(), pos.cuda(), cs.cuda(), slots.cuda(),
+                                      torch.tensor([scale], device="cuda"), eps=EPS, interleaved=interleaved)
+    mla.mla_device_error()
+    want, err = ref.rows(kv, w, cs[pos], interleaved, EPS)
+    y = want / torch.tensor(scale).double()
+    # the quotient is rounded to float32 before it becomes a code
+    err = err / scale + (y.abs() + err / scale) * 2.0 ** -24
+    real = slots >= 0
+    got = cache.view(blocks * page, -1).cpu()
+    ref.check_codes(got[slots[real]], y[real], err[real], "codes")
+    left = torch.ones(blocks * page, dtype=torch.bool)
+    left[slots[real]] = False
+    assert (got[left] == 0x55).all()
+
+
+@pytest.mark.parametrize("interleaved", [True, False])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("tokens,offset,pad,layers", [(1, 0, 0, 1), (130, 0, 8, 3), (9, 1, 0, 1), (10, 0, 1, 2)])
+def test_rows_ds_mla(mla, interleaved, dtype, tokens, offset, pad, layers):
+    _, kv, _, w, pos, cs = inputs(tokens + 2, tokens, V3, dtype, pad=pad)
+    if tokens > 9:
+        kv[3, :512] = 0                       # a row of zeros
+        kv[4, :512] = 0
+        kv[4, 5] = -1                         # one value in a row: three groups of zeros
+        kv[6, 128:256] = 2.0 ** -100          # next to nothing beside the rest
+    blocks, page = -(-tokens // 16) + 1, 16
+    whole = torch.full((blocks, layers, page, 656), 0x55, dtype=torch.uint8, device="cuda")
+    slots = slots_of(tokens, tokens, blocks * page)
+    mla.mla_norm_rope_cache_write_ds_mla(whole[:, layers - 1], gpu(kv, offset), w.cuda(), pos.cuda(), cs.cuda(), slots.cuda(),
+                                         eps=EPS, interleaved=interleaved)
+    mla.mla_device_error()
+    want, err = ref.rows(kv, w, cs[pos], interleaved, EPS)
+    real = slots >= 0
+    got = whole[:, layers - 1].reshape(blocks * page, 656).cpu()
+    e, want, err = got[slots[real]], want[real], err[real]
+    c, ec = want[:, :512].view(-1, 4, 128), err[:, :512].view(-1, 4, 128)
+    scale = (c.abs().amax(-1) / 448).clamp_min(2.0 ** -126)
+    es = ec.amax(-1) / 448 + scale * 2.0 ** -23
+    scales = e[:, 512:528].contiguous().view(F32).double()
+    assert ((scales - scale).abs() <= es).all(), "scales"
+    # codes by the scale as it is stored
+    y, ey = (c / scales[..., None]).flatten(1), (ec / scales[..., None]).flatten(1)
+    ref.check_codes(e[:, :512], y, ey + y.abs() * 2.0 ** -50, "codes")
+    ref.check(e[:, 528:].contiguous().view(BF16), want[:, 512:], err[:, 512:], BF16, "rope")
+    left = torch.ones(blocks * page, dtype=torch.bool)
+    left[slots[real]] = False
+    assert (got[left] == 0x55).all() and (layers == 1 or (whole[:, :layers - 1] == 0x55).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("dims,tokens,offset", [(V3, 1, 0), (V3, 65, 0), (NOPE, 5, 0), (ODD, 12, 0), (LITE, 4, 1)])
+@pytest.mark.parametrize("norm", [True, False])
+def test_both_in_one_launch(mla, dtype, dims, tokens, offset, norm):
+    # the two calls' results, bit for bit; without a norm the nope columns stay where they are
+    q, kv, qw, kw, pos, cs = inputs(tokens + 3, tokens, dims, dtype)
+    heads, nope, rope, latent = dims
+    q, kv, qw, kw, pos, cs = gpu(q, offset), gpu(kv, offset), qw.cuda() if norm else None, kw.cuda(), pos.cuda(), cs.cuda()
+    blocks, page = -(-tokens // 16) + 1, 16
+    slots = slots_of(tokens, tokens, blocks * page).cuda()
+    got = []
+    for together in (False, True):
+        nope_out = torch.zeros(tokens, heads, nope, dtype=dtype, device="cuda") if norm else q[..., :nope]
+        q_cat = torch.zeros(tokens, heads, latent + rope, dtype=dtype, device="cuda")
+        cache = torch.zeros(blocks, page, latent + rope, dtype=dtype, device="cuda")
+        if together:
+            mla.mla_norm_rope_q_cache_write(nope_out, q_cat[..., latent:], q, qw, cache, kv, kw, pos, cs, slots, eps=EPS)
+        else:
+            mla.mla_norm_rope_q(nope_out, q_cat[..., latent:], q, qw, pos, cs, eps=EPS)
+            mla.mla_norm_rope_cache_write(cache, kv, kw, pos, cs, slots, eps=EPS)
+        got.append((nope_out, q_cat, cache))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
+def test_positions_outside_the_table(mla):
+    q, kv, qw, kw, pos, cs = inputs(4, 6, LITE, BF16)
+    pos[1], pos[4] = POSITIONS, -1
+    nope = torch.full((6, 16, 128), 7.0, dtype=BF16, device="cuda")
+    pe, cache = nope[..., :64].clone(), torch.full((1, 8, 576), 7.0, dtype=BF16, device="cuda")
+    mla.mla_norm_rope_q_cache_write(nope, pe, q.cuda(), qw.cuda(), cache, kv.cuda(), kw.cuda(), pos.cuda(), cs.cuda(),
+                                    torch.tensor([0, 1, 2, 8, 4, 5], device="cuda"), eps=EPS)
+    with pytest.raises(mla.MlaError) as e:
+        mla.mla_device_error()
+    assert e.value.status == mla.MLA_ERR_DEVICE_DATA
+    good = [0, 2, 3, 5]
+    (n, en), (r, er) = ref.queries(q[good], qw, 128, cs[pos[good]], True, EPS)
+    ref.check(nope[good], n, en, BF16, "nope")
+    ref.check(pe[good], r, er, BF16, "rope")
+    assert (nope[[1, 4]] == 7).all() and (pe[[1, 4]] == 7).all()
+    want, err = ref.rows(kv, kw, cs[pos.clamp(0, POSITIONS - 1)], True, EPS)
+    ref.check(cache[0, [0, 2, 5]], want[[0, 2, 5]], err[[0, 2, 5]], BF16, "rows")
+    assert (cache[0, [1, 3, 4, 6, 7]] == 7).all()       # 1, 4: bad positions, 3: its slot lies outside
+    mla.mla_device_error()
+
+
+def test_no_tokens(mla):
+    z = torch.zeros
+    cs, none = ref.table(4, 64).cuda(), z(0, dtype=torch.int64, device="cuda")
+    q, kv = z(0, 16, 192, device="cuda"), z(0, 576, device="cuda")
+    mla.mla_norm_rope_q_cache_write(q[..., :128], q[..., 128:], q, None, z(1, 8, 576, device="cuda"), kv, z(512, device="cuda"),
+                                    none, cs, none)
+    mla.mla_device_error()
+
+
+def test_captured_and_on_another_stream(mla):
+    q, kv, qw, kw, pos, cs = (t.cuda() for t in inputs(5, 33, V3, BF16))
+    slots = torch.arange(33, device="cuda")
+    outs = [[torch.zeros(33, 128, 128, dtype=BF16, device="cuda"), torch.zeros(33, 128, 64, dtype=BF16, device="cuda"),
+             torch.zeros(1, 64, 576, dtype=BF16, device="cuda")] for _ in range(3)]
+
+    def call(o, **more):
+        mla.mla_norm_rope_q_cache_write(o[0], o[1], q, qw, o[2], kv, kw, pos, cs, slots, **more)
+
+    call(outs[0])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    call(outs[1], stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(outs[2])
+    graph.replay()
+    torch.cuda.synchronize()
+    for o in outs[1:]:
+        for a, b in zip(outs[0], o):
+            assert torch.equal(a, b)
