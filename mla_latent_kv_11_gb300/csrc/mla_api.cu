@@ -1070,12 +1070,14 @@ mla_status mass_call(mla_dtype dtype, float* mass, int64_t mass_stride, int32_t 
   if (max_blocks <= 0 || block_table_stride < max_blocks)
     return fail(MLA_ERR_INVALID_ARG, "need 0 < max_blocks <= block_table_stride");
   if (mass_rows <= 0 || mass_stride < mass_rows) return fail(MLA_ERR_INVALID_ARG, "need 0 < mass_rows <= mass_stride");
-  if (!decode) MLA_TRY(check_workspace(workspace, workspace_bytes, 256));
+  if (!decode) MLA_TRY(check_workspace(workspace, workspace_bytes, mass_tc_workspace()));
   const MassCall c{mass, mass_stride, mass_rows, view3(q_cat),
                    CacheView{cache.data, cache.stride[0], cache.stride[1], (int32_t)cache.shape[0], (int32_t)cache.shape[1],
                              (int32_t)cache.shape[2]},
                    block_table, block_table_stride, max_blocks, cu_seqlens_q, seq_lens, lse, (int32_t)batch, (int32_t)T,
                    (int32_t)H, softmax_scale, decay};
+  MassMaps maps;
+  if (mass_tc_supported(dtype, c, &maps)) return cuda_status(launch_mass_tc(c, maps, workspace, (cudaStream_t)stream), name);
   return cuda_status(launch_mass_simt(dtype, c, (cudaStream_t)stream), name);
 }
 }  // namespace
@@ -1088,7 +1090,7 @@ mla_status mla_decode_mass(mla_dtype dtype, float* mass, int64_t mass_stride, in
                    "mla_decode_mass");
 }
 
-size_t mla_prefill_mass_workspace_size(void) { return 256; }
+size_t mla_prefill_mass_workspace_size(void) { return mass_tc_workspace(); }
 
 mla_status mla_prefill_mass(mla_dtype dtype, float* mass, int64_t mass_stride, int32_t mass_rows, mla_tensor q_cat,
                             mla_tensor cache, const int32_t* block_table, int64_t block_table_stride, int32_t max_blocks,
@@ -1165,7 +1167,7 @@ mla_status mla_device_error(void* stream) {
   ErrorWords words;
   cudaError_t (*const word_of[ErrorWords::kCount])(unsigned**) = {
       cache_io_error_word, attn_pair_error_word, window_sched_error_word, window_simt_error_word, bmm_tc_error_word,
-      norm_rope_error_word, evict_error_word, mass_simt_error_word};
+      norm_rope_error_word, evict_error_word, mass_simt_error_word, mass_tc_error_word};
   for (int i = 0; i < ErrorWords::kCount && e == cudaSuccess; ++i) e = word_of[i](&words.word[i]);
   // on the legacy stream, as the copies that follow
   if (e == cudaSuccess) e = launch_gather_errors(words, nullptr);

@@ -258,7 +258,16 @@ struct MassCall {
   int32_t B, T, H;
   float scale, decay;
 };
-// On the CUDA cores (mass_simt.cu).
+// On the tensor cores (mass_tc.cu): bf16, rows of up to 576 values in whole groups of 64, up to 128 heads,
+// pages of whole 64-row blocks or blocks of whole pages of 8 rows or more, 16-byte aligned views. Fills the
+// call's tensor maps where it is so.
+struct MassMaps {
+  CUtensorMap keys, q;
+};
+bool mass_tc_supported(mla_dtype dt, const MassCall& c, MassMaps* maps);
+size_t mass_tc_workspace();   // of a prefill
+cudaError_t launch_mass_tc(const MassCall& c, const MassMaps& maps, void* ws, cudaStream_t st);
+// On the CUDA cores (mass_simt.cu): everything else.
 cudaError_t launch_mass_simt(mla_dtype dt, const MassCall& c, cudaStream_t st);
 
 // Attention limited to a window and sinks. A query at position p of a sequence attends rows t <= p with
@@ -405,7 +414,7 @@ mla_status report_status(mla_status st, const char* fmt, ...);
 // give the word's address on the current device, and one kernel moves their errors into the copy module's
 // word, which is then read (mla_device_error 119 us with a copy and a clearing of each of nine words).
 struct ErrorWords {
-  static constexpr int kCount = 8;
+  static constexpr int kCount = 9;
   unsigned* word[kCount];
 };
 cudaError_t cache_io_error_word(unsigned** word);
@@ -416,6 +425,7 @@ cudaError_t bmm_tc_error_word(unsigned** word);
 cudaError_t norm_rope_error_word(unsigned** word);
 cudaError_t evict_error_word(unsigned** word);
 cudaError_t mass_simt_error_word(unsigned** word);
+cudaError_t mass_tc_error_word(unsigned** word);
 cudaError_t launch_gather_errors(const ErrorWords& words, cudaStream_t st);
 // Read and clear (after the stream was synchronised).
 unsigned copy_errors_read_clear();
