@@ -9,9 +9,12 @@
 // Both parts are bound by HBM: every value crosses it once. A row stays in registers between its sum
 // and its stores, in 16-byte words: a query head in 8, 16 or 32 lanes of up to four words each (24
 // words of a 192-wide bf16 head are three a lane of eight, so that no lane idles), a cache row in one
-// warp. A word's partner half a rope away is loaded by the lane that needs it (the line is in L1
-// already) instead of being exchanged. Both parts share one launch: a decode step has 5 to 500 blocks
-// of work in all.
+// warp. A block takes heads of one token, several a warp one behind the other, so that the token's angles, the
+// addresses and a weight that all heads share are worked out once (a head a warp alone issued three times the
+// instructions: 4096 tokens of 128 heads 113 us). No lane has more than one word of the rope; its partner
+// half a rope away is loaded by the lane that needs it (the line is in L1 already) instead of being
+// exchanged. Both parts share one launch: a decode step has 5 to 500 blocks of work in all.
+#include <algorithm>
 #include <cfloat>
 
 #include "e4m3_codes.cuh"
@@ -52,6 +55,31 @@ struct Word {
     }
     return w;
   }
+  // x times by, and times the values of w.
+  static __device__ __forceinline__ void scale(float (&x)[kN], float by, const uint4& w) {
+    float y[kN];
+    open(w, y);
+    const uint64_t b = pair(by, by);
+#pragma unroll
+    for (int i = 0; i < kN; i += 2) {
+      uint64_t v = pair(x[i], x[i + 1]);
+      asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(v), "l"(b));
+      asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(v), "l"(pair(y[i], y[i + 1])));
+      x[i] = __uint_as_float((uint32_t)v);
+      x[i + 1] = __uint_as_float((uint32_t)(v >> 32));
+    }
+  }
+  static __device__ __forceinline__ float squares(const uint4& w) {
+    float x[kN];
+    open(w, x);
+    uint64_t sum = 0;
+#pragma unroll
+    for (int i = 0; i < kN; i += 2) {
+      const uint64_t v = pair(x[i], x[i + 1]);
+      asm("fma.rn.f32x2 %0, %1, %1, %0;" : "+l"(sum) : "l"(v));
+    }
+    return __uint_as_float((uint32_t)sum) + __uint_as_float((uint32_t)(sum >> 32));
+  }
   // The word at p, which need not be aligned where !vec.
   static __device__ __forceinline__ uint4 load(const T* p, bool vec) {
     if (vec) return *reinterpret_cast<const uint4*>(p);
@@ -79,15 +107,22 @@ struct Angles {
     }
     return table + p * stride;
   }
-  // N consecutive cosines or sines, 16 or 8 bytes a load where the table allows (`words`).
-  template <int N>
-  __device__ __forceinline__ void load(const float* p, float (&x)[N]) const {
+};
+
+// The angles of one word of a rope: columns d .. d + kN - 1. (The rotations are written in fused
+// multiply-adds, the same in every kernel, so that which one a call takes does not change a rotation's bits.)
+template <int kN, bool kInter>
+struct Turn {
+  static constexpr int kHas = kInter ? kN / 2 : kN;
+  float c[kHas], s[kHas];   // half a rope apart: the first half's sines negative, as its columns are the a's
+
+  static __device__ __forceinline__ void load(const float* p, bool words, float (&x)[kHas]) {
     if (!words) {
 #pragma unroll
-      for (int k = 0; k < N; ++k) x[k] = p[k];
-    } else if constexpr (N % 4 == 0) {
+      for (int k = 0; k < kHas; ++k) x[k] = p[k];
+    } else if constexpr (kHas % 4 == 0) {
 #pragma unroll
-      for (int k = 0; k < N; k += 4) {
+      for (int k = 0; k < kHas; k += 4) {
         const float4 v = *reinterpret_cast<const float4*>(p + k);
         x[k] = v.x; x[k + 1] = v.y; x[k + 2] = v.z; x[k + 3] = v.w;
       }
@@ -96,30 +131,28 @@ struct Angles {
       x[0] = v.x; x[1] = v.y;
     }
   }
-  // (The rotations are written in fused multiply-adds, the same in every kernel, so that which one a call
-  // takes does not change a rotation's bits.)
-  // The rope columns d .. d + N - 1, with their partners half a rope away in `with` (interleaved: unused).
-  template <int N>
-  __device__ __forceinline__ void turn(float (&x)[N], const float (&with)[N], const float* cs, int d) const {
-    const int half = R >> 1;
-    if (interleaved) {
-      float c[N / 2], s[N / 2];
-      load(cs + (d >> 1), c);
-      load(cs + half + (d >> 1), s);
+  // cs: the token's row of the table.
+  __device__ __forceinline__ void open(const float* cs, int d, int half, bool words) {
+    const int i = kInter ? d >> 1 : d < half ? d : d - half;
+    load(cs + i, words, c);
+    load(cs + half + i, words, s);
+    if (!kInter && d < half) {
 #pragma unroll
-      for (int k = 0; k < N; k += 2) {
+      for (int k = 0; k < kHas; ++k) s[k] = -s[k];
+    }
+  }
+  // with: the partners half a rope away (kInter: not used).
+  __device__ __forceinline__ void turn(float (&x)[kN], const float (&with)[kN]) const {
+    if constexpr (kInter) {
+#pragma unroll
+      for (int k = 0; k < kN; k += 2) {
         const float a = x[k], b = x[k + 1];
         x[k] = fmaf(a, c[k >> 1], -(b * s[k >> 1]));
         x[k + 1] = fmaf(b, c[k >> 1], a * s[k >> 1]);
       }
     } else {
-      const int i = d < half ? d : d - half;
-      const float sign = d < half ? -1.f : 1.f;
-      float c[N], s[N];
-      load(cs + i, c);
-      load(cs + half + i, s);
 #pragma unroll
-      for (int k = 0; k < N; ++k) x[k] = fmaf(x[k], c[k], sign * (with[k] * s[k]));
+      for (int k = 0; k < kN; ++k) x[k] = fmaf(x[k], c[k], with[k] * s[k]);
     }
   }
 };
@@ -135,7 +168,8 @@ struct QueryPart {
   int64_t w_s0;
   int32_t H, P, W;      // heads, columns before the rope, columns
   int32_t first;        // columns before it stay as they are (in place, without a norm)
-  int32_t rows;         // tokens * H
+  int32_t tokens;       // 0: no queries
+  int32_t parts;        // blocks of a token: block i takes heads from i * (H / parts, rounded up to whole passes) on
 };
 
 struct RowPart {
@@ -171,69 +205,84 @@ __device__ __forceinline__ float norm_factor(float sum, int n, float eps) {
   return t == t && y <= FLT_MAX ? fmaf(0.5f * y, t, y) : y;  // (v infinite or zero: as it is)
 }
 
-// Heads of queries, in words: kG lanes a row, kW words a lane.
-template <typename T, int kG, int kW>
+// Heads of queries, in words: kG lanes a head, kW words a lane, kPass heads a pass of the block. A block
+// takes `per` heads (whole passes) of one token.
+constexpr int kThreads = 256;
+template <int kG>
+constexpr int kPass = kThreads / kG;
+
+template <typename T, int kG, int kW, bool kInter>
 __device__ __forceinline__ void query_rows(const QueryPart& p, const Angles& ang, float eps, int block) {
   using V = Word<T>;
-  const int lane = threadIdx.x & 31, l = lane & (kG - 1);
-  const int64_t row = ((int64_t)block * (blockDim.x >> 5) + (threadIdx.x >> 5)) * (32 / kG) + lane / kG;
-  bool live = row < p.rows;
-  const int t = live ? (int)row / p.H : 0, h = live ? (int)row - t * p.H : 0;
-  const float* cs = live ? ang.of(t) : nullptr;
-  live = live && (ang.R == 0 || cs != nullptr);
-  const T* src = static_cast<const T*>(p.q) + t * p.q_s0 + h * p.q_s1;
-  const T* wgt = p.weight == nullptr ? nullptr : static_cast<const T*>(p.weight) + h * p.w_s0;
+  const int l = threadIdx.x & (kG - 1);
+  const int t = block / p.parts, part = block - t * p.parts;
+  const int per = ((p.H + p.parts - 1) / p.parts + kPass<kG> - 1) / kPass<kG> * kPass<kG>;
+  const int h_end = min(p.H, (part + 1) * per);
+  int h = part * per + threadIdx.x / kG;
+  const float* cs = ang.of(t);
+  if (ang.R != 0 && cs == nullptr) return;   // the whole block's token
   const int half = ang.R >> 1;
-  uint4 own[kW], with[kW];
-  float sum = 0.f;
+  // this lane's word of the rope, if it has one
+  int rope = -1;
 #pragma unroll
   for (int j = 0; j < kW; ++j) {
     const int c = p.first + (l + kG * j) * V::kN;
-    own[j] = with[j] = make_uint4(0u, 0u, 0u, 0u);
-    if (!live || c >= p.W) continue;
-    own[j] = V::load(src + c, true);
-    if (c >= p.P && !ang.interleaved) with[j] = V::load(src + (c < p.P + half ? c + half : c - half), true);
+    if (c >= p.P && c < p.W) rope = c;
   }
-  if (wgt != nullptr) {
+  const int partner = rope < p.P + half ? rope + half : rope - half;
+  Turn<V::kN, kInter> turn;
+  if (rope >= 0) turn.open(cs, rope - p.P, half, ang.words);
+  const T* src = static_cast<const T*>(p.q) + t * p.q_s0 + h * p.q_s1 + p.first + l * V::kN;
+  T* nope = static_cast<T*>(p.nope) + t * p.n_s0 + h * p.n_s1 + p.first + l * V::kN;
+  T* pe = static_cast<T*>(p.pe) + t * p.p_s0 + h * p.p_s1 + (rope - p.P);
+  const int64_t src_to_partner = partner - p.first - l * V::kN;
+  const bool norm = p.weight != nullptr;
+  const T* wgt = static_cast<const T*>(p.weight) + h * p.w_s0 + p.first + l * V::kN;
+  const int left = p.W - p.first - l * V::kN;      // columns from this lane's first on
+  for (; __any_sync(0xffffffffu, h < h_end); h += kPass<kG>) {
+    const bool live = h < h_end;
+    uint4 own[kW], with = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
     for (int j = 0; j < kW; ++j) {
-      float x[V::kN];
-      V::open(own[j], x);
-#pragma unroll
-      for (int k = 0; k < V::kN; ++k) sum += x[k] * x[k];
+      own[j] = make_uint4(0u, 0u, 0u, 0u);
+      if (live && kG * j * V::kN < left) own[j] = V::load(src + kG * j * V::kN, true);
     }
+    if (!kInter && live && rope >= 0) with = V::load(src + src_to_partner, true);
+    float by = 1.f;
+    if (norm) {
+      float sum = 0.f;
 #pragma unroll
-    for (int m = 1; m < kG; m <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-  }
-  __syncwarp();   // the outputs may be q's own columns: every load comes before any store
-  if (!live) return;
-  const float by = wgt != nullptr ? norm_factor(sum, p.W, eps) : 1.f;
+      for (int j = 0; j < kW; ++j) sum += V::squares(own[j]);
 #pragma unroll
-  for (int j = 0; j < kW; ++j) {
-    const int c = p.first + (l + kG * j) * V::kN;
-    if (c >= p.W) continue;
-    float x[V::kN];
-    V::open(own[j], x);
-    if (wgt != nullptr) {
-      float w[V::kN];
-      V::open(V::load(wgt + c, true), w);
-#pragma unroll
-      for (int k = 0; k < V::kN; ++k) x[k] = x[k] * by * w[k];
+      for (int m = 1; m < kG; m <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+      by = norm_factor(sum, p.W, eps);
     }
-    if (c < p.P) {
-      *reinterpret_cast<uint4*>(static_cast<T*>(p.nope) + t * p.n_s0 + h * p.n_s1 + c) = V::close(x);
-      continue;
-    }
-    float y[V::kN];
-    V::open(with[j], y);
-    if (wgt != nullptr && !ang.interleaved) {
-      float w[V::kN];
-      V::open(V::load(wgt + (c < p.P + half ? c + half : c - half), true), w);
+    __syncwarp();   // the outputs may be q's own columns: every load of a head comes before any store
+    if (live) {
 #pragma unroll
-      for (int k = 0; k < V::kN; ++k) y[k] = y[k] * by * w[k];
+      for (int j = 0; j < kW; ++j) {
+        if (kG * j * V::kN >= left) continue;
+        const int c = p.first + (l + kG * j) * V::kN;
+        float x[V::kN];
+        V::open(own[j], x);
+        if (norm) V::scale(x, by, V::load(wgt + kG * j * V::kN, true));
+        if (c < p.P) {
+          *reinterpret_cast<uint4*>(nope + kG * j * V::kN) = V::close(x);
+          continue;
+        }
+        float y[V::kN] = {};
+        if (!kInter) {
+          V::open(with, y);
+          if (norm) V::scale(y, by, V::load(wgt + src_to_partner, true));
+        }
+        turn.turn(x, y);
+        *reinterpret_cast<uint4*>(pe) = V::close(x);
+      }
     }
-    ang.turn(x, y, cs, c - p.P);
-    *reinterpret_cast<uint4*>(static_cast<T*>(p.pe) + t * p.p_s0 + h * p.p_s1 + (c - p.P)) = V::close(x);
+    src += kPass<kG> * p.q_s1;
+    nope += kPass<kG> * p.n_s1;
+    pe += kPass<kG> * p.p_s1;
+    wgt += kPass<kG> * p.w_s0;
   }
 }
 
@@ -272,37 +321,38 @@ __device__ __forceinline__ float quantise_group(float (&x)[kN], uint32_t (&w)[kN
   return scale;
 }
 
-// New cache rows, in words: a warp a row, up to kW words a lane. vec: the sources are aligned words.
-template <typename T, int kFmt, int kW>
+// New cache rows, in words: a warp a row, up to kW words a lane. vec: the sources are aligned words. The row is
+// asked for at once with its slot and its position.
+template <typename T, int kFmt, int kW, bool kInter>
 __device__ __forceinline__ void cache_rows(const RowPart& p, const Angles& ang, float eps, int block, bool vec) {
   using V = Word<T>;
   const int lane = threadIdx.x & 31;
-  const int64_t t = (int64_t)block * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  const int64_t t = (int64_t)block * (kThreads / 32) + (threadIdx.x >> 5);
   if (t >= p.tokens) return;
+  const T* src = static_cast<const T*>(p.kv) + t * p.k_s0 + lane * V::kN;
+  const T* wgt = static_cast<const T*>(p.weight) + lane * V::kN;
+  const int left = p.E - lane * V::kN, half = ang.R >> 1;
+  uint4 own[kW], with = make_uint4(0u, 0u, 0u, 0u);
+  int rope = -1;
+#pragma unroll
+  for (int j = 0; j < kW; ++j) {
+    own[j] = make_uint4(0u, 0u, 0u, 0u);
+    if (32 * j * V::kN < left) {
+      own[j] = V::load(src + 32 * j * V::kN, vec);
+      if ((lane + 32 * j) * V::kN >= p.L) rope = (lane + 32 * j) * V::kN - p.L;
+    }
+  }
+  if (!kInter && rope >= 0)
+    with = V::load(static_cast<const T*>(p.kv) + t * p.k_s0 + p.L + (rope < half ? rope + half : rope - half), vec);
   const int64_t off = row_offset(p, t, lane);
-  if (off < 0) return;
   const float* cs = ang.of(t);
-  if (ang.R != 0 && cs == nullptr) return;
-  const T* src = static_cast<const T*>(p.kv) + t * p.k_s0;
-  const T* wgt = static_cast<const T*>(p.weight);
-  const int half = ang.R >> 1;
-  uint4 own[kW], with[kW];
+  if (off < 0 || (ang.R != 0 && cs == nullptr)) return;
+  Turn<V::kN, kInter> turn;
+  if (rope >= 0) turn.open(cs, rope, half, ang.words);
   float sum = 0.f;
 #pragma unroll
   for (int j = 0; j < kW; ++j) {
-    const int c = (lane + 32 * j) * V::kN;
-    own[j] = with[j] = make_uint4(0u, 0u, 0u, 0u);
-    if (c >= p.E) continue;
-    own[j] = V::load(src + c, vec);
-    if (c >= p.L && !ang.interleaved) with[j] = V::load(src + (c < p.L + half ? c + half : c - half), vec);
-  }
-#pragma unroll
-  for (int j = 0; j < kW; ++j) {
-    float x[V::kN];
-    V::open(own[j], x);
-    float s = 0.f;
-#pragma unroll
-    for (int k = 0; k < V::kN; ++k) s += x[k] * x[k];
+    const float s = V::squares(own[j]);
     if ((lane + 32 * j) * V::kN < p.L) sum += s;
   }
 #pragma unroll
@@ -316,14 +366,11 @@ __device__ __forceinline__ void cache_rows(const RowPart& p, const Angles& ang, 
     float x[V::kN];
     V::open(own[j], x);
     if (c < p.L) {
-      float w[V::kN];
-      V::open(V::load(wgt + c, vec), w);
-#pragma unroll
-      for (int k = 0; k < V::kN; ++k) x[k] = x[k] * by * w[k];
+      V::scale(x, by, V::load(wgt + 32 * j * V::kN, vec));
     } else if (c < p.E) {
       float y[V::kN];
-      V::open(with[j], y);
-      ang.turn(x, y, cs, c - p.L);
+      V::open(with, y);
+      turn.turn(x, y);
     }
     if constexpr (kFmt == kPlain) {
       *reinterpret_cast<uint4*>(static_cast<T*>(p.cache) + off + c) = V::close(x);
@@ -356,17 +403,17 @@ __device__ __forceinline__ void cache_rows(const RowPart& p, const Angles& ang, 
 }
 
 // Blocks [0, q_blocks) take query heads, the others cache rows.
-template <typename T, int kFmt, int kG, int kW>
-__global__ void __launch_bounds__(256) norm_rope_kernel(const QueryPart q, const RowPart r, const Angles ang, float eps,
-                                                        int q_blocks, int vec) {
+template <typename T, int kFmt, int kG, int kW, bool kInter>
+__global__ void __launch_bounds__(kThreads, 4) norm_rope_kernel(const QueryPart q, const RowPart r, const Angles ang, float eps,
+                                                                int q_blocks, int vec) {
   pdl_enter();
   if constexpr (kW > 0) {
     if ((int)blockIdx.x < q_blocks) {
-      query_rows<T, kG, kW>(q, ang, eps, blockIdx.x);
+      query_rows<T, kG, kW, kInter>(q, ang, eps, blockIdx.x);
       return;
     }
   }
-  cache_rows<T, kFmt, sizeof(T) == 4 ? 5 : 3>(r, ang, eps, blockIdx.x - q_blocks, vec);   // 640 or 768 columns
+  cache_rows<T, kFmt, sizeof(T) == 4 ? 5 : 3, kInter>(r, ang, eps, blockIdx.x - q_blocks, vec);   // 640 or 768 columns
 }
 
 // ---------------------------------------------------------------------------
@@ -408,8 +455,8 @@ __global__ void __launch_bounds__(256) norm_rope_any_kernel(const QueryPart q, c
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if ((int)blockIdx.x < q_blocks) {
     const int64_t row = (int64_t)blockIdx.x * 8 + warp;
-    if (row >= q.rows) return;
-    const int t = (int)row / q.H, h = (int)row - t * q.H;
+    if (row >= (int64_t)q.tokens * q.H) return;
+    const int t = (int)(row / q.H), h = (int)(row - (int64_t)t * q.H);
     const float* cs = ang.of(t);
     if (ang.R != 0 && cs == nullptr) return;
     const T* src = static_cast<const T*>(q.q) + t * q.q_s0 + h * q.q_s1;
@@ -451,15 +498,15 @@ template <typename T>
 bool in_words(const QueryPart& q, const RowPart& r, int fmt, const Angles& a) {
   constexpr int per = Word<T>::kN;
   if (a.R % (2 * per) != 0) return false;   // halves of whole words
-  if (q.rows > 0) {
+  if (q.tokens > 0) {
     if (q.P % per || !aligned16(q.q) || !aligned16(q.nope) || !aligned16(q.pe) || q.q_s0 % per || q.q_s1 % per ||
         q.n_s0 % per || q.n_s1 % per || q.p_s0 % per || q.p_s1 % per)
       return false;
     if (q.weight != nullptr && (!aligned16(q.weight) || q.w_s0 % per)) return false;
-    if ((q.W - q.first) / per > 32 * 4) return false;
+    if ((q.W - q.first) / per > 32 * 4 || a.R / per > 32) return false;   // four words a lane, one of them the rope's
   }
   if (r.tokens > 0 && fmt != kDsMla) {
-    if (r.L % per || r.E > (sizeof(T) == 4 ? 5 : 3) * 32 * per || !aligned16(r.kv) || r.k_s0 % per || !aligned16(r.weight))
+    if (r.L % per || a.R / per > 32 || r.E > (sizeof(T) == 4 ? 5 : 3) * 32 * per || !aligned16(r.kv) || r.k_s0 % per || !aligned16(r.weight))
       return false;
     const int unit = fmt == kPlain ? per : 4;   // an e4m3 row is stored four codes at a time
     if (fmt == kPlain ? !aligned16(r.cache) : reinterpret_cast<uintptr_t>(r.cache) % 4 != 0) return false;
@@ -468,33 +515,45 @@ bool in_words(const QueryPart& q, const RowPart& r, int fmt, const Angles& a) {
   return true;
 }
 
-template <typename T, int kFmt>
-cudaError_t launch(const QueryPart& q, const RowPart& r, const Angles& ang, float eps, cudaStream_t st) {
-  const unsigned r_blocks = (unsigned)((r.tokens + 7) / 8);
-  if (!in_words<T>(q, r, kFmt, ang)) {
-    if constexpr (kFmt == kDsMla) {
-      return cudaErrorInvalidValue;   // its widths and cache are words by definition
-    } else {
-      const unsigned q_blocks = (unsigned)(((int64_t)q.rows + 7) / 8);
-      return launch_k(norm_rope_any_kernel<T, kFmt>, q_blocks + r_blocks, 256, 0, st, q, r, ang, eps, (int)q_blocks);
-    }
-  }
+template <typename T, int kFmt, bool kInter>
+cudaError_t launch_words(QueryPart q, const RowPart& r, const Angles& ang, float eps, cudaStream_t st) {
   constexpr int per = Word<T>::kN;
+  const unsigned r_blocks = (unsigned)((r.tokens + 7) / 8);
   const int vec = kFmt != kDsMla || (aligned16(r.kv) && r.k_s0 % per == 0 && aligned16(r.weight));
-  if (q.rows == 0) return launch_k(norm_rope_kernel<T, kFmt, 32, 0>, r_blocks, 256, 0, st, q, r, ang, eps, 0, vec);
+  if (q.tokens == 0) return launch_k(norm_rope_kernel<T, kFmt, 32, 0, kInter>, r_blocks, kThreads, 0, st, q, r, ang, eps, 0, vec);
   if constexpr (kFmt == kPlain) {
-    // the fewest lanes that hold a row in four words each, and no more words than it takes
-    const int words = (q.W - q.first) / per, lanes = words <= 32 ? 8 : words <= 64 ? 16 : 32, w = (words + lanes - 1) / lanes;
-    const unsigned q_blocks = (unsigned)(((int64_t)q.rows * lanes + 255) / 256), grid = q_blocks + r_blocks;
-    auto go = [&](auto kernel) { return launch_k(kernel, grid, 256, 0, st, q, r, ang, eps, (int)q_blocks, vec); };
+    // the fewest lanes that hold a head in four words each, the rope in one; and no more words than it takes
+    const int words = (q.W - q.first) / per, rope = ang.R / per;
+    const int lanes = words <= 32 && rope <= 8 ? 8 : words <= 64 && rope <= 16 ? 16 : 32, w = (words + lanes - 1) / lanes;
+    // a token's heads in one block, or in several while that leaves an SM without four
+    const int pass = kThreads / lanes, passes = (q.H + pass - 1) / pass;
+    q.parts = (int)std::min<int64_t>(passes, (4LL * device_sm_count() + q.tokens - 1) / q.tokens);
+    const int64_t q_blocks = (int64_t)q.tokens * q.parts;
+    if (q_blocks + r_blocks > INT32_MAX) return cudaErrorInvalidValue;
+    auto go = [&](auto kernel) {
+      return launch_k(kernel, (unsigned)(q_blocks + r_blocks), kThreads, 0, st, q, r, ang, eps, (int)q_blocks, vec);
+    };
     if (lanes == 8) {
-      if (w <= 1) return go(norm_rope_kernel<T, kFmt, 8, 1>);
-      return w <= 3 ? go(norm_rope_kernel<T, kFmt, 8, 3>) : go(norm_rope_kernel<T, kFmt, 8, 4>);
+      if (w <= 1) return go(norm_rope_kernel<T, kFmt, 8, 1, kInter>);
+      return w <= 3 ? go(norm_rope_kernel<T, kFmt, 8, 3, kInter>) : go(norm_rope_kernel<T, kFmt, 8, 4, kInter>);
     }
-    if (lanes == 16) return w <= 3 ? go(norm_rope_kernel<T, kFmt, 16, 3>) : go(norm_rope_kernel<T, kFmt, 16, 4>);
-    return go(norm_rope_kernel<T, kFmt, 32, 4>);
+    if (lanes == 16) return w <= 3 ? go(norm_rope_kernel<T, kFmt, 16, 3, kInter>) : go(norm_rope_kernel<T, kFmt, 16, 4, kInter>);
+    return go(norm_rope_kernel<T, kFmt, 32, 4, kInter>);
   }
   return cudaErrorInvalidValue;   // queries go with plain rows alone
+}
+
+template <typename T, int kFmt>
+cudaError_t launch(const QueryPart& q, const RowPart& r, const Angles& ang, float eps, cudaStream_t st) {
+  if (in_words<T>(q, r, kFmt, ang))
+    return ang.interleaved ? launch_words<T, kFmt, true>(q, r, ang, eps, st) : launch_words<T, kFmt, false>(q, r, ang, eps, st);
+  if constexpr (kFmt == kDsMla) {
+    return cudaErrorInvalidValue;     // its widths and cache are words by definition
+  } else {
+    const unsigned q_blocks = (unsigned)(((int64_t)q.tokens * q.H + 7) / 8);
+    return launch_k(norm_rope_any_kernel<T, kFmt>, q_blocks + (unsigned)((r.tokens + 7) / 8), kThreads, 0, st, q, r, ang, eps,
+                    (int)q_blocks);
+  }
 }
 
 }  // namespace
@@ -506,18 +565,18 @@ cudaError_t launch_norm_rope(mla_dtype dt, const NormRopeCall& c, cudaStream_t s
              aligned16(c.cos_sin) && c.cos_sin_stride % 4 == 0 && c.R % 8 == 0};
   if (c.tokens > 0 && c.H > 0) {
     q = QueryPart{c.q.data, c.q.s0, c.q.s1, c.q_nope.data, c.q_nope.s0, c.q_nope.s1, c.q_pe.data, c.q_pe.s0, c.q_pe.s1,
-                  c.q_weight, c.q_weight_s0, c.H, c.P, c.P + c.R, 0, (int32_t)(c.tokens * c.H)};
+                  c.q_weight, c.q_weight_s0, c.H, c.P, c.P + c.R, 0, (int32_t)c.tokens, 1};
     if (c.q_weight == nullptr && c.q_nope.data == c.q.data && c.q_nope.s0 == c.q.s0 && c.q_nope.s1 == c.q.s1) q.first = c.P;
     // empty outputs: any aligned place serves
     if (c.P == 0) q.nope = const_cast<void*>(q.q), q.n_s0 = q.n_s1 = 0;
     if (c.R == 0) q.pe = const_cast<void*>(q.q), q.p_s0 = q.p_s1 = 0;
-    if (q.first == q.W) q.rows = 0;
+    if (q.first == q.W) q.tokens = 0;
   }
   if (c.rows) {
     r = RowPart{c.kv.data, c.kv.s0, c.kv_weight, c.cache.data, c.cache.s0, c.cache.s1, c.cache.n0 * c.cache.n1,
                 (int32_t)c.cache.n1, c.L, c.L + c.R, c.slots, c.tokens, c.scale};
   }
-  if (q.rows == 0 && r.tokens == 0) return cudaSuccess;
+  if (q.tokens == 0 && r.tokens == 0) return cudaSuccess;
   const bool f32 = dt == MLA_F32;
   if (c.scale != nullptr) return f32 ? launch<float, kE4m3>(q, r, ang, c.eps, st) : launch<__nv_bfloat16, kE4m3>(q, r, ang, c.eps, st);
   if (c.ds_mla) return f32 ? launch<float, kDsMla>(q, r, ang, c.eps, st) : launch<__nv_bfloat16, kDsMla>(q, r, ang, c.eps, st);
