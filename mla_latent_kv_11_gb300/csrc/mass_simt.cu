@@ -1,10 +1,12 @@
 // Row masses on the CUDA cores: every type and shape that the tensor cores do not take.
 //
-// A block owns 64 rows of a sequence and goes over the query rows (tokens x heads) that attend any of
-// them, 64 at a time: their scores as a 64 x 64 float32 tile, four rows by four queries a thread, in
-// steps of 32 columns through shared memory; then the weights e^(s - lse), added to the thread's four
-// rows. At the end the sixteen threads of a row add up in a fixed order, so a result does not change
-// from run to run.
+// A block owns kTile rows of a sequence and goes over the query rows (tokens x heads) that attend any of
+// them, kTile at a time: their scores as a float32 tile, kTile / 16 rows by as many queries a thread, in
+// steps of columns through shared memory, the next step's values on their way in registers; then the weights
+// e^(s - lse), added to the thread's rows. At the end the sixteen threads of a row add up in a fixed order, so a
+// result does not change from run to run. Tiles of 64 compute most (1 load of shared memory for 2 products);
+// with few query rows a sequence (a decode of up to 32 heads) tiles of 16, as more blocks share the rows and
+// fewer queries are padding: 5 sequences of up to 256 float32 rows, 16 heads: 61 us with tiles of 64, 12 with 16.
 #include <math_constants.h>
 
 #include <cuda_bf16.h>
@@ -16,25 +18,26 @@ namespace {
 
 __device__ unsigned g_mass_simt_err = 0;
 
-constexpr int kTileRows = 64, kTileQ = 64, kStep = 32, kMassThreads = 256;
+constexpr int kMassThreads = 256;
 
 __device__ __forceinline__ float value(float v) { return v; }
 __device__ __forceinline__ float value(__nv_bfloat16 v) { return __bfloat162float(v); }
 
-template <typename T>
+template <typename T, int kTile>
 __global__ void __launch_bounds__(kMassThreads) mass_simt_kernel(const MassArgs a, const T* __restrict__ q, int64_t q_s0,
                                                                  int64_t q_s1, const T* __restrict__ cache, int64_t c_blk,
                                                                  int64_t c_row) {
   pdl_enter();
-  __shared__ float sk[kStep][kTileRows + 4], sq[kStep][kTileQ + 4];
-  __shared__ int64_t row_at[kTileRows], q_at[kTileQ];
-  __shared__ float q_lse[kTileQ];
-  __shared__ int q_pos[kTileQ];
+  constexpr int kStep = kTile == 64 ? 32 : 64, kMine = kTile / 16, kLoads = kTile * kStep / kMassThreads;
+  __shared__ float sk[kStep][kTile + 4], sq[kStep][kTile + 4];
+  __shared__ int64_t row_at[kTile], q_at[kTile];
+  __shared__ float q_lse[kTile];
+  __shared__ int q_pos[kTile];
   const int b = blockIdx.y, tid = threadIdx.x;
   const MassSeq s = mass_seq(a, b, &g_mass_simt_err);
-  const int t0 = blockIdx.x * kTileRows;
+  const int t0 = blockIdx.x * kTile;
   if (s.nq == 0 || t0 >= s.kv) return;
-  if (tid < kTileRows) {
+  if (tid < kTile) {
     const int t = t0 + tid;
     row_at[tid] = -1;
     if (t < s.kv) {
@@ -46,13 +49,15 @@ __global__ void __launch_bounds__(kMassThreads) mass_simt_kernel(const MassArgs 
     }
   }
   const int d = s.kv - s.nq;                          // position of the first query
-  const int tx = tid & 15, ty = tid >> 4;             // queries 4 tx .., rows 4 ty ..
-  float acc[4] = {};
+  const int tx = tid & 15, ty = tid >> 4;             // queries kMine tx .., rows kMine ty ..
+  const int le = tid % kStep, lr = tid / kStep;       // this thread's column and first row of a step's loads
+  constexpr int kLoadRows = kMassThreads / kStep;
+  float acc[kMine] = {};
   // 64-bit: tokens times heads may pass 32 bits
   const int64_t end = (int64_t)s.nq * a.H;
-  for (int64_t r0 = (int64_t)max(0, t0 - d) * a.H; r0 < end; r0 += kTileQ) {
+  for (int64_t r0 = (int64_t)max(0, t0 - d) * a.H; r0 < end; r0 += kTile) {
     __syncthreads();
-    if (tid < kTileQ) {
+    if (tid < kTile) {
       const int64_t r = r0 + tid;
       q_at[tid] = -1;
       q_lse[tid] = CUDART_INF_F;
@@ -66,58 +71,77 @@ __global__ void __launch_bounds__(kMassThreads) mass_simt_kernel(const MassArgs 
       }
     }
     __syncthreads();
-    float c[4][4] = {};
+    float c[kMine][kMine] = {}, nk[kLoads], nq[kLoads];
+    auto ask = [&](int e) {
+#pragma unroll
+      for (int k = 0; k < kLoads; ++k) {
+        const int r = lr + k * kLoadRows;
+        nk[k] = e < a.E && row_at[r] >= 0 ? value(cache[row_at[r] + e]) : 0.f;
+        nq[k] = e < a.E && q_at[r] >= 0 ? value(q[q_at[r] + e]) : 0.f;
+      }
+    };
+    ask(le);
     for (int e0 = 0; e0 < a.E; e0 += kStep) {
 #pragma unroll
-      for (int k = 0; k < kTileRows * kStep / kMassThreads; ++k) {
-        const int i = tid + k * kMassThreads, e = i & (kStep - 1), r = i / kStep;
-        const bool in = e0 + e < a.E;
-        sk[e][r] = in && row_at[r] >= 0 ? value(cache[row_at[r] + e0 + e]) : 0.f;
-        sq[e][r] = in && q_at[r] >= 0 ? value(q[q_at[r] + e0 + e]) : 0.f;
+      for (int k = 0; k < kLoads; ++k) {
+        sk[le][lr + k * kLoadRows] = nk[k];
+        sq[le][lr + k * kLoadRows] = nq[k];
       }
       __syncthreads();
+      if (e0 + kStep < a.E) ask(e0 + kStep + le);
 #pragma unroll 8
       for (int e = 0; e < kStep; ++e) {
-        const float4 x = *reinterpret_cast<const float4*>(&sk[e][4 * ty]), y = *reinterpret_cast<const float4*>(&sq[e][4 * tx]);
-        const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+        float xs[kMine], ys[kMine];
+        if constexpr (kMine == 4) {
+          const float4 x = *reinterpret_cast<const float4*>(&sk[e][4 * ty]), y = *reinterpret_cast<const float4*>(&sq[e][4 * tx]);
+          xs[0] = x.x; xs[1] = x.y; xs[2] = x.z; xs[3] = x.w;
+          ys[0] = y.x; ys[1] = y.y; ys[2] = y.z; ys[3] = y.w;
+        } else {
+          xs[0] = sk[e][ty];
+          ys[0] = sq[e][tx];
+        }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < kMine; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) c[i][j] = fmaf(xs[i], ys[j], c[i][j]);
+          for (int j = 0; j < kMine; ++j) c[i][j] = fmaf(xs[i], ys[j], c[i][j]);
       }
       __syncthreads();
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float l = q_lse[4 * tx + j];
-      const int p = q_pos[4 * tx + j];
+    for (int j = 0; j < kMine; ++j) {
+      const float l = q_lse[kMine * tx + j];
+      const int p = q_pos[kMine * tx + j];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (t0 + 4 * ty + i <= p) acc[i] += expf(fmaf(c[i][j], a.scale, -l));
+      for (int i = 0; i < kMine; ++i)
+        if (t0 + kMine * ty + i <= p) acc[i] += expf(fmaf(c[i][j], a.scale, -l));
     }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < kMine; ++i) {
 #pragma unroll
     for (int m = 1; m < 16; m <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], m);
-    const int t = t0 + 4 * ty + i;
-    if (tx == 0 && t < s.kv && row_at[4 * ty + i] >= 0) {
+    const int t = t0 + kMine * ty + i;
+    if (tx == 0 && t < s.kv && row_at[kMine * ty + i] >= 0) {
       float* const m = a.mass + b * a.mass_stride + t;
       *m = new_mass(a.decay == 0.f ? 0.f : *m, acc[i], a.decay);
     }
   }
 }
 
+template <typename T, int kTile>
+cudaError_t launch(const MassCall& c, const MassArgs& a, cudaStream_t st) {
+  const dim3 grid((unsigned)((a.cap + kTile - 1) / kTile), (unsigned)c.B);
+  return launch_k(mass_simt_kernel<T, kTile>, grid, kMassThreads, 0, st, a, (const T*)c.q.data, c.q.s0, c.q.s1,
+                  (const T*)c.cache.data, c.cache.s_blk, c.cache.s_row);
+}
+
 }  // namespace
 
 cudaError_t launch_mass_simt(mla_dtype dt, const MassCall& c, cudaStream_t st) {
   const MassArgs a = mass_args(c);
-  const dim3 grid((unsigned)((a.cap + kTileRows - 1) / kTileRows), (unsigned)c.B);
-  if (dt == MLA_F32)
-    return launch_k(mass_simt_kernel<float>, grid, kMassThreads, 0, st, a, (const float*)c.q.data, c.q.s0, c.q.s1,
-                    (const float*)c.cache.data, c.cache.s_blk, c.cache.s_row);
-  return launch_k(mass_simt_kernel<__nv_bfloat16>, grid, kMassThreads, 0, st, a, (const __nv_bfloat16*)c.q.data, c.q.s0,
-                  c.q.s1, (const __nv_bfloat16*)c.cache.data, c.cache.s_blk, c.cache.s_row);
+  const bool few = (int64_t)c.T * c.H <= 32 * (int64_t)c.B;   // query rows a sequence, on average
+  if (dt == MLA_F32) return few ? launch<float, 16>(c, a, st) : launch<float, 64>(c, a, st);
+  return few ? launch<__nv_bfloat16, 16>(c, a, st) : launch<__nv_bfloat16, 64>(c, a, st);
 }
 
 cudaError_t mass_simt_error_word(unsigned** word) {
