@@ -750,25 +750,27 @@ def mla_cache_evict(cache, mass, block_table, seq_lens, budget: int, seq_lens_ou
     become rows 0, 1, .. in their order, in their pages or in those of block_table_out; masses move along (mass_out, or
     in place), seq_lens_out int32 [B] gets the lengths, kept_out int32 [B, budget] the old rows (-1 behind the last).
     cache: a plain, an e4m3 or a ds_mla cache."""
+    import torch
     batch = seq_lens.numel()
-    cache = cache[:, :, 0] if cache.dim() == 4 and cache.shape[2] == 1 else cache
+    if cache.dim() == 4 and cache.shape[2] == 1:
+        cache = cache[:, :, 0]
     for value, name in ((budget, "budget"), (sinks, "sinks"), (recent, "recent")):
         _check_int32(value, name)
     _check_table(block_table, batch)
     _check_counts(seq_lens, batch, "seq_lens")
-    _check_counts(seq_lens_out, batch, "seq_lens_out")
+    if seq_lens_out is not seq_lens:
+        _check_counts(seq_lens_out, batch, "seq_lens_out")
     _check_mass(mass, batch)
-    table_out, out = (None, 0, 0), (None, 0, 0)
-    if block_table_out is not None:
+    table_out = out = (None, 0, 0)
+    if block_table_out is not None and block_table_out is not block_table:
         _check_table(block_table_out, batch)
-        if block_table_out.data_ptr() != block_table.data_ptr() or block_table_out.shape != block_table.shape or \
-                block_table_out.stride() != block_table.stride():
-            table_out = _ptr(block_table_out), _table_stride(block_table_out), block_table_out.shape[1]
-    if mass_out is not None:
+        table_out = _ptr(block_table_out), _table_stride(block_table_out), block_table_out.shape[1]
+    if mass_out is not None and mass_out is not mass:
         _check_mass(mass_out, batch, "mass_out")
         out = _ptr(mass_out), _table_stride(mass_out), mass_out.shape[1]
-    if kept_out is not None:
-        _check_counts(kept_out.reshape(-1) if kept_out.is_contiguous() else kept_out, batch * budget, "kept_out")
+    if kept_out is not None and (kept_out.dtype != torch.int32 or kept_out.numel() != batch * budget or
+                                 not kept_out.is_contiguous()):
+        raise MlaError(MLA_ERR_INVALID_ARG, f"kept_out must be contiguous int32 [{batch}, {budget}]")
     device = _check_device(cache, mass, block_table, seq_lens, seq_lens_out, block_table_out, mass_out, kept_out, workspace)
     if workspace is None:
         workspace = _scratch(mla_cache_evict_workspace_size(batch, mass.shape[1], budget), device, stream)

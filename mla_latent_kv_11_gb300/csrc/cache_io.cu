@@ -25,41 +25,6 @@ __device__ unsigned g_io_err = 0;
 
 constexpr int kInFlight = 4;   // rows a warp takes, at most
 
-// Sixteen consecutive values as floats: 32 bytes a load where `wide` (32-byte aligned), else 16.
-__device__ __forceinline__ void load_words(const void* p, uint32_t (&w)[8], bool wide) {
-  if (wide) {
-    ptx::ld_global_32B(p, w);
-  } else {
-    const uint4 a = reinterpret_cast<const uint4*>(p)[0], b = reinterpret_cast<const uint4*>(p)[1];
-    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
-  }
-}
-__device__ __forceinline__ void load16(const __nv_bfloat16* p, float (&x)[16], bool wide) {
-  uint32_t w[8];
-  load_words(p, w, wide);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
-  }
-}
-__device__ __forceinline__ void load16(const float* p, float (&x)[16], bool wide) {
-  uint32_t w[8];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    load_words(p + 8 * h, w, wide);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[8 * h + i] = __uint_as_float(w[i]);
-  }
-}
-// Two consecutive values.
-__device__ __forceinline__ float2 load2(const __nv_bfloat16* p) {
-  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p));
-}
-__device__ __forceinline__ float2 load2(const float* p) { return *reinterpret_cast<const float2*>(p); }
-
 // N consecutive values, each rounded once to T, 16 bytes a store.
 template <int N>
 __device__ __forceinline__ void store_n(__nv_bfloat16* p, const float (&x)[N]) {
@@ -145,33 +110,8 @@ __global__ void __launch_bounds__(256, 5) write_ds_mla_kernel(
       pe = make_float2(to_f(rope[0]), to_f(rope[1]));
     }
     uint8_t* o = cache + to;
-    float top = 0.f;
-#pragma unroll
-    for (int k = 0; k < 16; ++k) top = fmaxf(top, fabsf(x[k]));   // fmaxf passes a NaN over
-    const bool finite = top <= FLT_MAX;
-    top = fminf(top, FLT_MAX);
-#pragma unroll
-    for (int m = 1; m < 8; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-    const float scale = fmaxf(__fdiv_rn(top, kE4m3Max), FLT_MIN);
-    float by = scale;
-    if (by < 0x1p-80f) {           // the same quotients, out of the way of underflow
-      by *= 0x1p64f;
-#pragma unroll
-      for (int k = 0; k < 16; ++k) x[k] *= 0x1p64f;
-    }
-    if (!finite) {                 // the scale is FLT_MAX / 448 then: a code of +-448
-#pragma unroll
-      for (int k = 0; k < 16; ++k) x[k] = fabsf(x[k]) > FLT_MAX ? copysignf(FLT_MAX, x[k]) : x[k];
-    }
-    uint32_t w[4] = {};
-    const float inv = __frcp_rn(by);
-    const uint64_t r = pair(inv, inv), ns = pair(-by, -by);
-#pragma unroll
-    for (int k = 0; k < 16; k += 2) {
-      float a, b;
-      divide2(x[k], x[k + 1], ns, r, a, b);
-      w[k >> 2] |= codes2(a, b) << (8 * (k & 2));
-    }
+    uint32_t w[4];
+    const float scale = quantise_group(x, w);
     *reinterpret_cast<uint4*>(o + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
     if ((lane & 7) == 0) *reinterpret_cast<float*>(o + kDsMlaLatent + 4 * (lane >> 3)) = scale;
     reinterpret_cast<__nv_bfloat162*>(o + kDsMlaRopeByte)[lane] = __floats2bfloat162_rn(pe.x, pe.y);

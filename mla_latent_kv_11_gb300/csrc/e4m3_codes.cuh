@@ -2,10 +2,14 @@
 // that write quantised cache rows.
 #pragma once
 
+#include <cfloat>
+
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
 #include <cstdint>
+
+#include "sm100_ptx.cuh"
 
 namespace mla {
 namespace {
@@ -16,6 +20,41 @@ __device__ __forceinline__ float to_f(float v) { return v; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ void from_f(float* p, float v) { *p = v; }
 __device__ __forceinline__ void from_f(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+// Sixteen consecutive values as floats: 32 bytes a load where `wide` (32-byte aligned), else 16.
+__device__ __forceinline__ void load_words(const void* p, uint32_t (&w)[8], bool wide) {
+  if (wide) {
+    ptx::ld_global_32B(p, w);
+  } else {
+    const uint4 a = reinterpret_cast<const uint4*>(p)[0], b = reinterpret_cast<const uint4*>(p)[1];
+    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+  }
+}
+__device__ __forceinline__ void load16(const __nv_bfloat16* p, float (&x)[16], bool wide) {
+  uint32_t w[8];
+  load_words(p, w, wide);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+__device__ __forceinline__ void load16(const float* p, float (&x)[16], bool wide) {
+  uint32_t w[8];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    load_words(p + 8 * h, w, wide);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[8 * h + i] = __uint_as_float(w[i]);
+  }
+}
+// Two consecutive values.
+__device__ __forceinline__ float2 load2(const __nv_bfloat16* p) {
+  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p));
+}
+__device__ __forceinline__ float2 load2(const float* p) { return *reinterpret_cast<const float2*>(p); }
 
 // x / s as a float32 that rounds to the same code as the quotient itself: rounded toward zero, with
 // the last bit set where that lost something. (Rounded to nearest it could land on the middle of two
@@ -56,6 +95,41 @@ __device__ __forceinline__ void divide2(float x0, float x1, uint64_t ns, uint64_
 // The codes of two quotients: to nearest even, saturating.
 __device__ __forceinline__ uint32_t codes2(float a, float b) {
   return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+
+// A group of 128 values, sixteen in each of eight consecutive lanes: the codes of this lane's, and the group's
+// scale, its largest magnitude / 448 (an infinity counts as the largest float32, a NaN not at all), at least
+// 2^-126 so that the division stays among normal numbers.
+__device__ __forceinline__ float quantise_group(float (&x)[16], uint32_t (&w)[4]) {
+  float top = 0.f;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) top = fmaxf(top, fabsf(x[k]));   // fmaxf passes a NaN over
+  const bool finite = top <= FLT_MAX;
+  top = fminf(top, FLT_MAX);
+#pragma unroll
+  for (int m = 1; m < 8; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+  const float scale = fmaxf(__fdiv_rn(top, kE4m3Max), FLT_MIN);
+  float by = scale;
+  if (by < 0x1p-80f) {           // the same quotients, out of the way of underflow
+    by *= 0x1p64f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) x[k] *= 0x1p64f;
+  }
+  if (!finite) {                 // the scale is FLT_MAX / 448 then: a code of +-448
+#pragma unroll
+    for (int k = 0; k < 16; ++k) x[k] = fabsf(x[k]) > FLT_MAX ? copysignf(FLT_MAX, x[k]) : x[k];
+  }
+  const float inv = __frcp_rn(by);
+  const uint64_t r = pair(inv, inv), ns = pair(-by, -by);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) w[k] = 0;
+#pragma unroll
+  for (int k = 0; k < 16; k += 2) {
+    float a, b;
+    divide2(x[k], x[k + 1], ns, r, a, b);
+    w[k >> 2] |= codes2(a, b) << (8 * (k & 2));
+  }
+  return scale;
 }
 
 }  // namespace

@@ -76,7 +76,10 @@ struct TcArgs {
   int chunks, stages;        // of 64 columns; of the ring
   int n, half;               // query rows of a tile, and of one CTA
   int tpc;                   // prefill: tokens of a tile per CTA
+  // a prefill's pieces of rows that are cut, of each unit: those that end in its first tiles, and that begin in its
+  // last ones
   float* part;               // [unit][2][256]
+  int4* piece;               // [unit][2] {sequence (-1: none), tile of 256 rows, whether it is the last piece, rows}
 };
 
 // Sum over i < n of (a i + b) / m, rounded down each: the integer points under a line, counted by Euclid's
@@ -145,6 +148,31 @@ __device__ long long all_tiles(const TcArgs& a, long long* sh) {
   return sum;
 }
 
+// Tile x's place within the sequence that *found names.
+template <bool kPrefill>
+__device__ Place place_in(const TcArgs& a, long long x, Place* found) {
+  Place p = *found;
+  Tiles<kPrefill> t;
+  t.open(a, p.seq);
+  if constexpr (kPrefill) {
+    // the outer tile that holds x: the threads look at one each
+    for (int k = threadIdx.x; k < t.outer; k += kThreads) {
+      const long long lo = p.base + t.before(k);
+      const int n = t.inner - t.first(k);
+      if (lo <= x && x < lo + n) {
+        found->outer = k;
+        found->tile = t.first(k) + (int)(x - lo);
+      }
+    }
+    __syncthreads();
+    p = *found;
+  } else {
+    p.tile = (int)(x - p.base);
+  }
+  __syncthreads();
+  return p;
+}
+
 // Where tile x lies, x below the total.
 template <bool kPrefill>
 __device__ Place find_tile(const TcArgs& a, long long x, long long* sh, Place* found) {
@@ -178,33 +206,53 @@ __device__ Place find_tile(const TcArgs& a, long long x, long long* sh, Place* f
     base += all;
     if (x < base) break;     // the same for every thread
   }
-  Place p = *found;
-  Tiles<kPrefill> t;
-  t.open(a, p.seq);
-  if constexpr (kPrefill) {
-    // the outer tile that holds x: the threads look at one each
-    for (int k = threadIdx.x; k < t.outer; k += kThreads) {
-      const long long lo = p.base + t.before(k);
-      const int n = t.inner - t.first(k);
-      if (lo <= x && x < lo + n) {
-        found->outer = k;
-        found->tile = t.first(k) + (int)(x - lo);
-      }
-    }
-    __syncthreads();
-    p = *found;
-  } else {
-    p.tile = (int)(x - p.base);
+  return place_in<kPrefill>(a, x, found);
+}
+// This unit's tiles [x0, x1), and where x0 lies if there are any.
+template <bool kPrefill>
+__device__ Place my_tiles(const TcArgs& a, int unit, int units, long long& x0, long long& x1, long long* sh, Place* found) {
+  if (a.m.B > kThreads) {
+    const long long total = all_tiles<kPrefill>(a, sh);
+    x0 = total * unit / units;
+    x1 = total * (unit + 1) / units;
+    return x0 < x1 ? find_tile<kPrefill>(a, x0, sh, found) : Place{};
   }
+  // a thread a sequence: total and place from one sum over them
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = threadIdx.x;
+  Tiles<kPrefill> t;
+  long long mine = 0;
+  if (b < a.m.B) {
+    t.open(a, b);
+    mine = t.total();
+  }
+  long long upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += y;
+  }
+  if (lane == 31) sh[warp] = upto;
   __syncthreads();
-  return p;
+  long long total = 0, before = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w == warp) before = total;
+    total += sh[w];
+  }
+  x0 = total * unit / units;
+  x1 = total * (unit + 1) / units;
+  if (x0 >= x1) return Place{};   // the same for every thread
+  const long long at = before + upto - mine;
+  if (mine > 0 && at <= x0 && x0 < at + mine) *found = Place{b, 0, 0, at};
+  __syncthreads();
+  return place_in<kPrefill>(a, x0, found);
 }
 
 // The segments of a range of tiles: inner tiles [i0, i1) of an outer one.
 struct Seg {
   MassSeq s;
   int b, outer, i0, i1;
-  bool whole, begins;        // it is all of its outer tile; it holds the outer tile's first
+  bool whole, begins, ends;  // it is all of its outer tile; it holds the outer tile's first, and its last
 };
 template <bool kPrefill>
 struct Walker {
@@ -232,7 +280,8 @@ struct Walker {
     s.i0 = i;
     s.i1 = (int)min((long long)t.inner, i + left);
     s.begins = i == t.first(k);
-    s.whole = s.begins && s.i1 == t.inner;
+    s.ends = s.i1 == t.inner;
+    s.whole = s.begins && s.ends;
     left -= s.i1 - s.i0;
     ++k;
     i = k < t.outer ? t.first(k) : 0;
@@ -409,10 +458,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   };
 
   // this cluster's tiles [x0, x1): both CTAs work out the same
-  const long long total = all_tiles<kPrefill>(a, sh.wide);
-  const long long x0 = total * unit / units, x1 = total * (unit + 1) / units;
-  Place from{0, 0, 0, 0};
-  if (x0 < x1) from = find_tile<kPrefill>(a, x0, sh.wide, &sh.found);
+  long long x0, x1;
+  const Place from = my_tiles<kPrefill>(a, unit, units, x0, x1, sh.wide, &sh.found);
   Walker<kPrefill> wk;
   wk.init(a, from.seq, from.outer, from.tile, x1 - x0);
   Seg sg;
@@ -557,6 +604,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     };
     bool ok = true, mine = true;   // ok: the group's decision; mine: this thread's waits so far
     int x = 0, place = 0;
+    int4 pieces[2] = {make_int4(-1, 0, 0, 0), make_int4(-1, 0, 0, 0)};
     while (ok && wk.next(a, sg)) {
       const int d = sg.s.kv - sg.s.nq;
       auto row_of = [&](int k) { return kRows * k + kCtaRows * (int)rank + e; };
@@ -631,12 +679,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive_smem_released(d_empty + 8 * buf);
         }
         if (!ok) break;
-        if (!sg.whole)
+        if (sg.whole) {
+          if (to != nullptr) *to = new_mass(old, sum, a.m.decay);
+        } else {
           a.part[((int64_t)unit * 2 + (sg.begins ? 1 : 0)) * kRows + kCtaRows * rank + e] = sum;
-        else if (to != nullptr)
-          *to = new_mass(old, sum, a.m.decay);
+          pieces[sg.begins ? 1 : 0] = make_int4(sg.b, sg.outer, sg.ends, sg.s.kv);
+        }
       }
     }
+    if (kPrefill && rank == 0 && e < 2) a.piece[2 * unit + e] = pieces[e];
     if (!ok || !mine) give_up();
   }
   // ---------------------------------------------------------------- teardown
@@ -655,32 +706,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync();
 }
 
-// Block u - 1 looks at where unit u's range begins. If that cuts 256 rows, and no range before begins within
-// them, it adds up their pieces: unit u - 1's last and, from u on, each unit's first until they are through.
+// Block u - 1 looks at the rows that end in, or go on through, unit u's first tiles. If they begin in the unit
+// before (units without tiles aside), it adds up their pieces in order.
 __global__ void __launch_bounds__(kThreads) mass_merge_kernel(const TcArgs a, int units) {
   pdl_enter();
-  __shared__ long long wide[8];
-  __shared__ Place found;
+  __shared__ int4 piece[kMaxUnits][2];
   const int u = blockIdx.x + 1, e = threadIdx.x;
-  const long long total = all_tiles<true>(a, wide);
-  const long long x = total * u / units;
-  if (x >= total || x == total * (u - 1) / units) return;   // nothing begins here, or unit u - 1 is empty
-  const Place p = find_tile<true>(a, x, wide, &found);
-  Tiles<true> t;
-  t.open(a, p.seq);
-  const int first = t.first(p.outer);
-  if (p.tile == first) return;                              // not cut
-  const long long begin = x - (p.tile - first), end = begin + (t.inner - first);
-  if (total * (u - 1) / units > begin) return;              // an earlier cut of the same rows
-  float sum = a.part[((int64_t)(u - 1) * 2 + 1) * kRows + e];
-  for (int v = u; v < units && total * v / units < end; ++v)
-    if (total * v / units < total * (v + 1) / units) sum += a.part[(int64_t)v * 2 * kRows + e];
-  const int row = kRows * p.outer + e;
-  if (row >= t.s.kv) return;
-  const int id = a.m.block_table[p.seq * a.m.bt_stride + row / a.m.page];
-  if (id < 0 || id >= a.m.num_blocks) return;               // recorded by the kernel before
-  float* const to = a.m.mass + p.seq * a.m.mass_stride + row;
-  *to = new_mass(a.m.decay == 0.f ? 0.f : *to, sum, a.m.decay);
+  for (int i = e; i < 2 * units; i += kThreads) piece[i >> 1][i & 1] = a.piece[i];
+  __syncthreads();
+  const int4 p = piece[u][0];
+  if (p.x < 0) return;
+  int v = u - 1;
+  while (v > 0 && piece[v][0].x < 0 && piece[v][1].x < 0) --v;
+  if (piece[v][1].x != p.x || piece[v][1].y != p.y) return;   // an earlier piece of the same rows
+  const int row = kRows * p.y + e;
+  if (row >= p.w) return;
+  const int id = a.m.block_table[p.x * a.m.bt_stride + row / a.m.page];
+  float* const to = a.m.mass + p.x * a.m.mass_stride + row;
+  const float old = a.m.decay == 0.f ? 0.f : *to;
+  float sum = a.part[((int64_t)v * 2 + 1) * kRows + e];
+  for (v = u; v < units; ++v) {
+    if (piece[v][0].x < 0) continue;                          // without tiles
+    sum += a.part[(int64_t)v * 2 * kRows + e];
+    if (piece[v][0].z != 0) break;
+  }
+  if (id < 0 || id >= a.m.num_blocks) return;                 // recorded by the kernel before
+  *to = new_mass(old, sum, a.m.decay);
 }
 
 template <bool kPrefill>
@@ -744,7 +795,7 @@ bool mass_tc_supported(mla_dtype dt, const MassCall& c, MassMaps* maps) {
                     CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-size_t mass_tc_workspace() { return (size_t)max_pairs<true>() * 2 * kRows * sizeof(float); }
+size_t mass_tc_workspace() { return (size_t)max_pairs<true>() * 2 * (kRows * sizeof(float) + sizeof(int4)); }
 
 cudaError_t launch_mass_tc(const MassCall& c, const MassMaps& maps, void* ws, cudaStream_t st) {
   const bool decode = c.cu_q == nullptr;
@@ -755,9 +806,10 @@ cudaError_t launch_mass_tc(const MassCall& c, const MassMaps& maps, void* ws, cu
   a.n = decode ? decode_rows(c.H) : kRows;
   a.half = a.n / 2;
   a.stages = std::min(kMaxStages, (kArena - a.chunks * (decode ? a.half * 128 : kChunkBytes)) / kChunkBytes);
-  a.part = static_cast<float*>(ws);
   if (decode) return launch<false>(a, maps, max_pairs<false>(), st);
   const int units = max_pairs<true>();
+  a.part = static_cast<float*>(ws);
+  a.piece = reinterpret_cast<int4*>(a.part + (int64_t)units * 2 * kRows);
   const cudaError_t e = launch<true>(a, maps, units, st);
   if (e != cudaSuccess || units < 2) return e;
   return launch_k(mass_merge_kernel, dim3(units - 1), dim3(kThreads), 0, st, a, units);

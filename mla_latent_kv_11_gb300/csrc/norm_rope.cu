@@ -15,7 +15,6 @@
 // half a rope away is loaded by the lane that needs it (the line is in L1 already) instead of being
 // exchanged. Both parts share one launch: a decode step has 5 to 500 blocks of work in all.
 #include <algorithm>
-#include <cfloat>
 
 #include "e4m3_codes.cuh"
 #include "mla_internal.h"
@@ -25,7 +24,7 @@ namespace {
 
 __device__ unsigned g_norm_err = 0;
 
-enum Format { kPlain, kE4m3, kDsMla };
+enum Format { kPlain, kE4m3 };
 
 // A 16-byte word's values.
 template <typename T>
@@ -80,14 +79,7 @@ struct Word {
     }
     return __uint_as_float((uint32_t)sum) + __uint_as_float((uint32_t)(sum >> 32));
   }
-  // The word at p, which need not be aligned where !vec.
-  static __device__ __forceinline__ uint4 load(const T* p, bool vec) {
-    if (vec) return *reinterpret_cast<const uint4*>(p);
-    float x[kN];
-#pragma unroll
-    for (int i = 0; i < kN; ++i) x[i] = to_f(p[i]);
-    return close(x);   // exact: the values are T's
-  }
+  static __device__ __forceinline__ uint4 load(const T* p) { return *reinterpret_cast<const uint4*>(p); }
 };
 
 // Positions and the table of their cosines and sines, [count, R] float32: R / 2 cosines, then R / 2 sines.
@@ -126,7 +118,7 @@ struct Turn {
         const float4 v = *reinterpret_cast<const float4*>(p + k);
         x[k] = v.x; x[k + 1] = v.y; x[k + 2] = v.z; x[k + 3] = v.w;
       }
-    } else {
+    } else if constexpr (kHas == 2) {
       const float2 v = *reinterpret_cast<const float2*>(p);
       x[0] = v.x; x[1] = v.y;
     }
@@ -239,15 +231,23 @@ __device__ __forceinline__ void query_rows(const QueryPart& p, const Angles& ang
   const bool norm = p.weight != nullptr;
   const T* wgt = static_cast<const T*>(p.weight) + h * p.w_s0 + p.first + l * V::kN;
   const int left = p.W - p.first - l * V::kN;      // columns from this lane's first on
-  for (; __any_sync(0xffffffffu, h < h_end); h += kPass<kG>) {
-    const bool live = h < h_end;
-    uint4 own[kW], with = make_uint4(0u, 0u, 0u, 0u);
+  uint4 own[kW], with;
+  auto ask = [&](bool live, uint4 (&w)[kW], uint4& v) {
 #pragma unroll
     for (int j = 0; j < kW; ++j) {
-      own[j] = make_uint4(0u, 0u, 0u, 0u);
-      if (live && kG * j * V::kN < left) own[j] = V::load(src + kG * j * V::kN, true);
+      w[j] = make_uint4(0u, 0u, 0u, 0u);
+      if (live && kG * j * V::kN < left) w[j] = V::load(src + kG * j * V::kN);
     }
-    if (!kInter && live && rope >= 0) with = V::load(src + src_to_partner, true);
+    v = make_uint4(0u, 0u, 0u, 0u);
+    if (!kInter && live && rope >= 0) v = V::load(src + src_to_partner);
+  };
+  ask(h < h_end, own, with);
+  for (; __any_sync(0xffffffffu, h < h_end); h += kPass<kG>) {
+    const bool live = h < h_end;
+    // the next head is on its way while this one is worked on
+    uint4 next[kW], next_with;
+    src += kPass<kG> * p.q_s1;
+    ask(h + kPass<kG> < h_end, next, next_with);
     float by = 1.f;
     if (norm) {
       float sum = 0.f;
@@ -265,7 +265,7 @@ __device__ __forceinline__ void query_rows(const QueryPart& p, const Angles& ang
         const int c = p.first + (l + kG * j) * V::kN;
         float x[V::kN];
         V::open(own[j], x);
-        if (norm) V::scale(x, by, V::load(wgt + kG * j * V::kN, true));
+        if (norm) V::scale(x, by, V::load(wgt + kG * j * V::kN));
         if (c < p.P) {
           *reinterpret_cast<uint4*>(nope + kG * j * V::kN) = V::close(x);
           continue;
@@ -273,58 +273,25 @@ __device__ __forceinline__ void query_rows(const QueryPart& p, const Angles& ang
         float y[V::kN] = {};
         if (!kInter) {
           V::open(with, y);
-          if (norm) V::scale(y, by, V::load(wgt + src_to_partner, true));
+          if (norm) V::scale(y, by, V::load(wgt + src_to_partner));
         }
         turn.turn(x, y);
         *reinterpret_cast<uint4*>(pe) = V::close(x);
       }
     }
-    src += kPass<kG> * p.q_s1;
+#pragma unroll
+    for (int j = 0; j < kW; ++j) own[j] = next[j];
+    with = next_with;
     nope += kPass<kG> * p.n_s1;
     pe += kPass<kG> * p.p_s1;
     wgt += kPass<kG> * p.w_s0;
   }
 }
 
-// A group of 128 latents of a ds_mla entry, a word of it in each of its kLanes lanes: the codes of this
-// lane's word, and the scale. The quantisation is that of the ds_mla cache write.
-template <int kN, int kLanes>
-__device__ __forceinline__ float quantise_group(float (&x)[kN], uint32_t (&w)[kN / 4]) {
-  float top = 0.f;
-#pragma unroll
-  for (int k = 0; k < kN; ++k) top = fmaxf(top, fabsf(x[k]));   // fmaxf passes a NaN over
-  const bool finite = top <= FLT_MAX;
-  top = fminf(top, FLT_MAX);
-#pragma unroll
-  for (int m = 1; m < kLanes; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-  const float scale = fmaxf(__fdiv_rn(top, kE4m3Max), FLT_MIN);
-  float by = scale;
-  if (by < 0x1p-80f) {           // the same quotients, out of the way of underflow
-    by *= 0x1p64f;
-#pragma unroll
-    for (int k = 0; k < kN; ++k) x[k] *= 0x1p64f;
-  }
-  if (!finite) {                 // the scale is FLT_MAX / 448 then: a code of +-448
-#pragma unroll
-    for (int k = 0; k < kN; ++k) x[k] = fabsf(x[k]) > FLT_MAX ? copysignf(FLT_MAX, x[k]) : x[k];
-  }
-  const float inv = __frcp_rn(by);
-  const uint64_t r = pair(inv, inv), ns = pair(-by, -by);
-#pragma unroll
-  for (int k = 0; k < kN / 4; ++k) w[k] = 0;
-#pragma unroll
-  for (int k = 0; k < kN; k += 2) {
-    float a, b;
-    divide2(x[k], x[k + 1], ns, r, a, b);
-    w[k >> 2] |= codes2(a, b) << (8 * (k & 2));
-  }
-  return scale;
-}
-
-// New cache rows, in words: a warp a row, up to kW words a lane. vec: the sources are aligned words. The row is
-// asked for at once with its slot and its position.
+// New cache rows, plain or e4m3, in words: a warp a row, up to kW words a lane. The row is asked for at once with
+// its slot and its position.
 template <typename T, int kFmt, int kW, bool kInter>
-__device__ __forceinline__ void cache_rows(const RowPart& p, const Angles& ang, float eps, int block, bool vec) {
+__device__ __forceinline__ void cache_rows(const RowPart& p, const Angles& ang, float eps, int block) {
   using V = Word<T>;
   const int lane = threadIdx.x & 31;
   const int64_t t = (int64_t)block * (kThreads / 32) + (threadIdx.x >> 5);
@@ -338,12 +305,12 @@ __device__ __forceinline__ void cache_rows(const RowPart& p, const Angles& ang, 
   for (int j = 0; j < kW; ++j) {
     own[j] = make_uint4(0u, 0u, 0u, 0u);
     if (32 * j * V::kN < left) {
-      own[j] = V::load(src + 32 * j * V::kN, vec);
+      own[j] = V::load(src + 32 * j * V::kN);
       if ((lane + 32 * j) * V::kN >= p.L) rope = (lane + 32 * j) * V::kN - p.L;
     }
   }
   if (!kInter && rope >= 0)
-    with = V::load(static_cast<const T*>(p.kv) + t * p.k_s0 + p.L + (rope < half ? rope + half : rope - half), vec);
+    with = V::load(static_cast<const T*>(p.kv) + t * p.k_s0 + p.L + (rope < half ? rope + half : rope - half));
   const int64_t off = row_offset(p, t, lane);
   const float* cs = ang.of(t);
   if (off < 0 || (ang.R != 0 && cs == nullptr)) return;
@@ -362,50 +329,95 @@ __device__ __forceinline__ void cache_rows(const RowPart& p, const Angles& ang, 
 #pragma unroll
   for (int j = 0; j < kW; ++j) {
     const int c = (lane + 32 * j) * V::kN;
-    if (kFmt != kDsMla && c >= p.E) continue;   // a group's lanes stay together below
+    if (c >= p.E) continue;
     float x[V::kN];
     V::open(own[j], x);
     if (c < p.L) {
-      V::scale(x, by, V::load(wgt + 32 * j * V::kN, vec));
-    } else if (c < p.E) {
+      V::scale(x, by, V::load(wgt + 32 * j * V::kN));
+    } else {
       float y[V::kN];
       V::open(with, y);
       turn.turn(x, y);
     }
     if constexpr (kFmt == kPlain) {
       *reinterpret_cast<uint4*>(static_cast<T*>(p.cache) + off + c) = V::close(x);
-    } else if constexpr (kFmt == kE4m3) {
+    } else {
       uint32_t w[V::kN / 4] = {};
 #pragma unroll
       for (int k = 0; k < V::kN; k += 2) w[k >> 2] |= codes2(__fdiv_rn(x[k], scale), __fdiv_rn(x[k + 1], scale)) << (8 * (k & 2));
       uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.cache) + off + c);
 #pragma unroll
       for (int k = 0; k < V::kN / 4; ++k) o[k] = w[k];
-    } else {
-      uint8_t* o = static_cast<uint8_t*>(p.cache) + off;
-      constexpr int kLanes = kDsMlaGroup / V::kN;
-      if ((32 * j) * V::kN < kDsMlaLatent) {     // the word lies in a group: so do all of the warp's
-        uint32_t w[V::kN / 4];
-        const float s = quantise_group<V::kN, kLanes>(x, w);
-        uint32_t* d = reinterpret_cast<uint32_t*>(o + c);
-        if constexpr (V::kN == 8)
-          *reinterpret_cast<uint2*>(d) = make_uint2(w[0], w[1]);
-        else
-          *d = w[0];
-        if ((lane & (kLanes - 1)) == 0) *reinterpret_cast<float*>(o + kDsMlaLatent + 4 * (c / kDsMlaGroup)) = s;
-      } else if (c < p.E) {
-        __nv_bfloat162* d = reinterpret_cast<__nv_bfloat162*>(o + kDsMlaRopeByte + 2 * (c - kDsMlaLatent));
-#pragma unroll
-        for (int k = 0; k < V::kN; k += 2) d[k >> 1] = __floats2bfloat162_rn(x[k], x[k + 1]);
-      }
     }
   }
 }
 
+// New rows as ds_mla entries: a warp a row, sixteen latents and two rope columns a lane, so that a group of 128
+// is eight lanes and its scale worked out once a lane (with a 16-byte word a lane, four groups a lane of four
+// float32 values each: 25 us for 20011 rows instead of DS_US). vec: aligned 16-byte words; wide: 32-byte aligned.
+template <typename T, bool kInter>
+__device__ __forceinline__ void ds_mla_rows(const RowPart& p, const Angles& ang, float eps, int block, bool vec, bool wide) {
+  const int lane = threadIdx.x & 31;
+  const int64_t t = (int64_t)block * (kThreads / 32) + (threadIdx.x >> 5);
+  if (t >= p.tokens) return;
+  const T* const row = static_cast<const T*>(p.kv) + t * p.k_s0;
+  const T* const rope = row + kDsMlaLatent;
+  const T* const wgt = static_cast<const T*>(p.weight) + 16 * lane;
+  // columns 2 lane and 2 lane + 1; half a rope apart their partners lie 32 columns on or back
+  const int partner = 2 * lane ^ 32;
+  float x[16];
+  float2 pe, with = make_float2(0.f, 0.f);
+  if (vec) {
+    load16(row + 16 * lane, x, wide);
+    pe = load2(rope + 2 * lane);
+    if (!kInter) with = load2(rope + partner);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) x[k] = to_f(row[16 * lane + k]);
+    pe = make_float2(to_f(rope[2 * lane]), to_f(rope[2 * lane + 1]));
+    if (!kInter) with = make_float2(to_f(rope[partner]), to_f(rope[partner + 1]));
+  }
+  const int64_t off = row_offset(p, t, lane);
+  const float* cs = ang.of(t);
+  if (off < 0 || cs == nullptr) return;
+  Turn<2, kInter> turn;
+  turn.open(cs, 2 * lane, 32, false);
+  uint64_t sum2 = 0;
+#pragma unroll
+  for (int k = 0; k < 16; k += 2) {
+    const uint64_t v = pair(x[k], x[k + 1]);
+    asm("fma.rn.f32x2 %0, %1, %1, %0;" : "+l"(sum2) : "l"(v));
+  }
+  float sum = __uint_as_float((uint32_t)sum2) + __uint_as_float((uint32_t)(sum2 >> 32));
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+  const float by = norm_factor(sum, kDsMlaLatent, eps);
+  {
+    float w[16];   // from L1, all but the first time; held from the start they cost the block a fifth of its warps
+    if (vec) {
+      load16(wgt, w, false);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 16; ++k) w[k] = to_f(wgt[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < 16; ++k) x[k] = x[k] * by * w[k];
+  }
+  uint32_t codes[4];
+  const float scale = quantise_group(x, codes);
+  uint8_t* const o = static_cast<uint8_t*>(p.cache) + off;
+  *reinterpret_cast<uint4*>(o + 16 * lane) = make_uint4(codes[0], codes[1], codes[2], codes[3]);
+  if ((lane & 7) == 0) *reinterpret_cast<float*>(o + kDsMlaLatent + 4 * (lane >> 3)) = scale;
+  float y[2] = {pe.x, pe.y};
+  const float z[2] = {with.x, with.y};
+  turn.turn(y, z);
+  reinterpret_cast<__nv_bfloat162*>(o + kDsMlaRopeByte)[lane] = __floats2bfloat162_rn(y[0], y[1]);
+}
+
 // Blocks [0, q_blocks) take query heads, the others cache rows.
 template <typename T, int kFmt, int kG, int kW, bool kInter>
-__global__ void __launch_bounds__(kThreads, 4) norm_rope_kernel(const QueryPart q, const RowPart r, const Angles ang, float eps,
-                                                                int q_blocks, int vec) {
+__global__ void __launch_bounds__(kThreads, kInter || kW < 3 ? 4 : 3) norm_rope_kernel(const QueryPart q, const RowPart r, const Angles ang, float eps,
+                                                                int q_blocks) {
   pdl_enter();
   if constexpr (kW > 0) {
     if ((int)blockIdx.x < q_blocks) {
@@ -413,7 +425,14 @@ __global__ void __launch_bounds__(kThreads, 4) norm_rope_kernel(const QueryPart 
       return;
     }
   }
-  cache_rows<T, kFmt, sizeof(T) == 4 ? 5 : 3, kInter>(r, ang, eps, blockIdx.x - q_blocks, vec);   // 640 or 768 columns
+  cache_rows<T, kFmt, sizeof(T) == 4 ? 5 : 3, kInter>(r, ang, eps, blockIdx.x - q_blocks);   // 640 or 768 columns
+}
+
+template <typename T, bool kInter>
+__global__ void __launch_bounds__(kThreads, 5) norm_rope_ds_mla_kernel(const RowPart r, const Angles ang, float eps, int vec,
+                                                                       int wide) {
+  pdl_enter();
+  ds_mla_rows<T, kInter>(r, ang, eps, blockIdx.x, vec, wide);
 }
 
 // ---------------------------------------------------------------------------
@@ -505,7 +524,7 @@ bool in_words(const QueryPart& q, const RowPart& r, int fmt, const Angles& a) {
     if (q.weight != nullptr && (!aligned16(q.weight) || q.w_s0 % per)) return false;
     if ((q.W - q.first) / per > 32 * 4 || a.R / per > 32) return false;   // four words a lane, one of them the rope's
   }
-  if (r.tokens > 0 && fmt != kDsMla) {
+  if (r.tokens > 0) {
     if (r.L % per || a.R / per > 32 || r.E > (sizeof(T) == 4 ? 5 : 3) * 32 * per || !aligned16(r.kv) || r.k_s0 % per || !aligned16(r.weight))
       return false;
     const int unit = fmt == kPlain ? per : 4;   // an e4m3 row is stored four codes at a time
@@ -519,8 +538,7 @@ template <typename T, int kFmt, bool kInter>
 cudaError_t launch_words(QueryPart q, const RowPart& r, const Angles& ang, float eps, cudaStream_t st) {
   constexpr int per = Word<T>::kN;
   const unsigned r_blocks = (unsigned)((r.tokens + 7) / 8);
-  const int vec = kFmt != kDsMla || (aligned16(r.kv) && r.k_s0 % per == 0 && aligned16(r.weight));
-  if (q.tokens == 0) return launch_k(norm_rope_kernel<T, kFmt, 32, 0, kInter>, r_blocks, kThreads, 0, st, q, r, ang, eps, 0, vec);
+  if (q.tokens == 0) return launch_k(norm_rope_kernel<T, kFmt, 32, 0, kInter>, r_blocks, kThreads, 0, st, q, r, ang, eps, 0);
   if constexpr (kFmt == kPlain) {
     // the fewest lanes that hold a head in four words each, the rope in one; and no more words than it takes
     const int words = (q.W - q.first) / per, rope = ang.R / per;
@@ -531,7 +549,7 @@ cudaError_t launch_words(QueryPart q, const RowPart& r, const Angles& ang, float
     const int64_t q_blocks = (int64_t)q.tokens * q.parts;
     if (q_blocks + r_blocks > INT32_MAX) return cudaErrorInvalidValue;
     auto go = [&](auto kernel) {
-      return launch_k(kernel, (unsigned)(q_blocks + r_blocks), kThreads, 0, st, q, r, ang, eps, (int)q_blocks, vec);
+      return launch_k(kernel, (unsigned)(q_blocks + r_blocks), kThreads, 0, st, q, r, ang, eps, (int)q_blocks);
     };
     if (lanes == 8) {
       if (w <= 1) return go(norm_rope_kernel<T, kFmt, 8, 1, kInter>);
@@ -547,13 +565,18 @@ template <typename T, int kFmt>
 cudaError_t launch(const QueryPart& q, const RowPart& r, const Angles& ang, float eps, cudaStream_t st) {
   if (in_words<T>(q, r, kFmt, ang))
     return ang.interleaved ? launch_words<T, kFmt, true>(q, r, ang, eps, st) : launch_words<T, kFmt, false>(q, r, ang, eps, st);
-  if constexpr (kFmt == kDsMla) {
-    return cudaErrorInvalidValue;     // its widths and cache are words by definition
-  } else {
-    const unsigned q_blocks = (unsigned)(((int64_t)q.tokens * q.H + 7) / 8);
-    return launch_k(norm_rope_any_kernel<T, kFmt>, q_blocks + (unsigned)((r.tokens + 7) / 8), kThreads, 0, st, q, r, ang, eps,
-                    (int)q_blocks);
-  }
+  const unsigned q_blocks = (unsigned)(((int64_t)q.tokens * q.H + 7) / 8);
+  return launch_k(norm_rope_any_kernel<T, kFmt>, q_blocks + (unsigned)((r.tokens + 7) / 8), kThreads, 0, st, q, r, ang, eps,
+                  (int)q_blocks);
+}
+
+template <typename T>
+cudaError_t launch_ds_mla(const RowPart& r, const Angles& ang, float eps, cudaStream_t st) {
+  constexpr int per = Word<T>::kN;
+  const int vec = aligned16(r.kv) && r.k_s0 % per == 0 && aligned16(r.weight);
+  const int wide = reinterpret_cast<uintptr_t>(r.kv) % 32 == 0 && r.k_s0 % (2 * per) == 0;
+  return launch_k(ang.interleaved ? norm_rope_ds_mla_kernel<T, true> : norm_rope_ds_mla_kernel<T, false>,
+                  (unsigned)((r.tokens + 7) / 8), kThreads, 0, st, r, ang, eps, vec, wide);
 }
 
 }  // namespace
@@ -579,7 +602,7 @@ cudaError_t launch_norm_rope(mla_dtype dt, const NormRopeCall& c, cudaStream_t s
   if (q.tokens == 0 && r.tokens == 0) return cudaSuccess;
   const bool f32 = dt == MLA_F32;
   if (c.scale != nullptr) return f32 ? launch<float, kE4m3>(q, r, ang, c.eps, st) : launch<__nv_bfloat16, kE4m3>(q, r, ang, c.eps, st);
-  if (c.ds_mla) return f32 ? launch<float, kDsMla>(q, r, ang, c.eps, st) : launch<__nv_bfloat16, kDsMla>(q, r, ang, c.eps, st);
+  if (c.ds_mla) return f32 ? launch_ds_mla<float>(r, ang, c.eps, st) : launch_ds_mla<__nv_bfloat16>(r, ang, c.eps, st);
   return f32 ? launch<float, kPlain>(q, r, ang, c.eps, st) : launch<__nv_bfloat16, kPlain>(q, r, ang, c.eps, st);
 }
 

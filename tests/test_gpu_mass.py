@@ -174,3 +174,13 @@ def test_captured_and_on_another_stream(mla, prefill):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(mass, want)
+
+
+@pytest.mark.parametrize("prefill", [False, True])
+def test_more_sequences_than_a_block_has_threads(mla, prefill):
+    kv = [int(x) for x in torch.randint(0, 400, (300,), generator=torch.Generator().manual_seed(3))]
+    q = [min(n, i % 7) for i, n in enumerate(kv)] if prefill else None
+    c = Case(41, BF16, 16, 576, 64, kv, q)
+    got = c.run(mla, 0.5)
+    c.check(got, 0.5)
+    assert torch.equal(got, c.run(mla, 0.5))
