@@ -224,19 +224,6 @@ __global__ void __launch_bounds__(kMaxSelectThreads) evict_select_kernel(const S
   }
 }
 
-// Division of rows (below 2^31) by the page: (t * factor) >> shift with factor = 2^shift / page rounded up,
-// shift = 31 + log2(page) rounded up; factor is at most 2^32, the error below 2^31 / 2^shift < 1 / page.
-struct PageOf {
-  uint64_t factor;
-  int shift, page;
-  explicit PageOf(int p) : shift(31), page(p) {
-    while ((1ll << (shift - 31)) < p) ++shift;
-    // shift is 62 at most, and 2^62 fits
-    factor = ((1ull << shift) + (uint64_t)p - 1) / (uint64_t)p;
-  }
-  __device__ __forceinline__ int operator()(int t) const { return (int)(((uint64_t)(uint32_t)t * factor) >> shift); }
-};
-
 struct MoveArgs {
   void* cache;
   int64_t s_blk, s_row;                              // in words

@@ -79,6 +79,21 @@ inline View3 view3(const mla_tensor& t) {
   return View3{t.data, t.shape[0], t.shape[1], t.shape[2], t.stride[0], t.stride[1], t.stride[2]};
 }
 
+// Division of rows (below 2^31) by the page: (t * factor) >> shift with factor = 2^shift / page rounded up,
+// shift = 31 + log2(page) rounded up; factor is at most 2^32, the error below 2^31 / 2^shift < 1 / page.
+struct PageOf {
+  uint64_t factor;
+  int shift, page;
+  explicit PageOf(int p) : shift(31), page(p) {
+    while ((1ll << (shift - 31)) < p) ++shift;
+    // shift is 62 at most, and 2^62 fits
+    factor = ((1ull << shift) + (uint64_t)p - 1) / (uint64_t)p;
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ int operator()(int t) const { return (int)(((uint64_t)(uint32_t)t * factor) >> shift); }
+#endif
+};
+
 // The paged cache as the kernels see it.
 struct CacheView {
   const void* data;  // element (blk, row, e) at data + blk*s_blk + row*s_row + e

@@ -10,10 +10,9 @@
 // and its stores, in 16-byte words: a query head in 8, 16 or 32 lanes of up to four words each (24
 // words of a 192-wide bf16 head are three a lane of eight, so that no lane idles), a cache row in one
 // warp. A block takes heads of one token, several a warp one behind the other, so that the token's angles, the
-// addresses and a weight that all heads share are worked out once (a head a warp alone issued three times the
-// instructions: 4096 tokens of 128 heads 113 us). No lane has more than one word of the rope; its partner
-// half a rope away is loaded by the lane that needs it (the line is in L1 already) instead of being
-// exchanged. Both parts share one launch: a decode step has 5 to 500 blocks of work in all.
+// addresses are worked out once (a head a warp alone issued three times the instructions: 4096 tokens of 128
+// heads 113 us). No lane has more than one word of the rope; its partner half a rope away comes from its lane. Both
+// parts share one launch: a decode step has 5 to 500 blocks of work in all.
 #include <algorithm>
 
 #include "e4m3_codes.cuh"
@@ -89,15 +88,18 @@ struct Angles {
   int64_t stride, count;
   int32_t R, interleaved, words;
 
-  // Row of token t's angles; null where its position lies outside the table (recorded).
-  __device__ __forceinline__ const float* of(int64_t t) const {
+  // A position's row of angles; null where it lies outside the table (recorded).
+  __device__ __forceinline__ const float* row(int64_t p, int lane) const {
     if (R == 0) return table;   // nothing to rotate
-    const int64_t p = positions[t];
     if (p < 0 || p >= count) {
-      atomicOr(&g_norm_err, kErrDeviceData);
+      if (lane == 0) atomicOr(&g_norm_err, kErrDeviceData);
       return nullptr;
     }
     return table + p * stride;
+  }
+  // The same of token t.
+  __device__ __forceinline__ const float* of(int64_t t) const {
+    return R == 0 ? table : row(positions[t], (int)threadIdx.x & 31);
   }
 };
 
@@ -149,6 +151,12 @@ struct Turn {
   }
 };
 
+// The lane, modulo the lanes of a row, that holds the word half a rope away from the one at `rope`.
+template <int kN>
+__device__ __forceinline__ int partner_lane(int rope, int half, int lane) {
+  return rope < half ? lane + half / kN : lane - half / kN;
+}
+
 struct QueryPart {
   const void* q;
   int64_t q_s0, q_s1;
@@ -170,22 +178,23 @@ struct RowPart {
   const void* weight;
   void* cache;
   int64_t c_blk, c_row, num_rows;
-  int32_t page, L, E;
+  PageOf page_of;
+  int32_t L, E;
   const int64_t* slots;
   int64_t tokens;
   const float* scale;   // kE4m3
 };
 
-// Offset of token t's row in the cache; -1: padding, or outside the view (recorded).
-__device__ __forceinline__ int64_t row_offset(const RowPart& p, int64_t t, int lane) {
-  const int64_t s = p.slots[t];
+// Offset of slot s in the cache; -1: padding, or outside the view (recorded).
+__device__ __forceinline__ int64_t row_offset(const RowPart& p, int64_t s, int lane) {
   if (s < 0) return -1;
   if (s >= p.num_rows) {
     if (lane == 0) atomicOr(&g_norm_err, kErrDeviceData);
     return -1;
   }
-  const int64_t blk = s / p.page;
-  return blk * p.c_blk + (s - blk * p.page) * p.c_row;
+  // (a division of 64 bits takes as long as half of a row's arithmetic)
+  const int64_t blk = p.num_rows <= INT32_MAX ? p.page_of((int)s) : s / p.page_of.page;
+  return blk * p.c_blk + (s - blk * p.page_of.page) * p.c_row;
 }
 
 // 1 / sqrt(sum / n + eps), one Newton step behind the two roundings of a root and a division: it enters every
@@ -200,6 +209,7 @@ __device__ __forceinline__ float norm_factor(float sum, int n, float eps) {
 // Heads of queries, in words: kG lanes a head, kW words a lane, kPass heads a pass of the block. A block
 // takes `per` heads (whole passes) of one token.
 constexpr int kThreads = 256;
+constexpr int kRowBlocks = 3, kHeadBlocks = 4;   // blocks an SM holds: of rows alone, of heads (and rows)
 template <int kG>
 constexpr int kPass = kThreads / kG;
 
@@ -219,35 +229,32 @@ __device__ __forceinline__ void query_rows(const QueryPart& p, const Angles& ang
 #pragma unroll
   for (int j = 0; j < kW; ++j) {
     const int c = p.first + (l + kG * j) * V::kN;
-    if (c >= p.P && c < p.W) rope = c;
+    if (c >= p.P && c < p.W) rope = c - p.P;
   }
-  const int partner = rope < p.P + half ? rope + half : rope - half;
+  const int partner = partner_lane<V::kN>(rope, half, l) & (kG - 1);
   Turn<V::kN, kInter> turn;
-  if (rope >= 0) turn.open(cs, rope - p.P, half, ang.words);
+  if (rope >= 0) turn.open(cs, rope, half, ang.words);
   const T* src = static_cast<const T*>(p.q) + t * p.q_s0 + h * p.q_s1 + p.first + l * V::kN;
   T* nope = static_cast<T*>(p.nope) + t * p.n_s0 + h * p.n_s1 + p.first + l * V::kN;
-  T* pe = static_cast<T*>(p.pe) + t * p.p_s0 + h * p.p_s1 + (rope - p.P);
-  const int64_t src_to_partner = partner - p.first - l * V::kN;
+  T* pe = static_cast<T*>(p.pe) + t * p.p_s0 + h * p.p_s1 + rope;
   const bool norm = p.weight != nullptr;
   const T* wgt = static_cast<const T*>(p.weight) + h * p.w_s0 + p.first + l * V::kN;
   const int left = p.W - p.first - l * V::kN;      // columns from this lane's first on
-  uint4 own[kW], with;
-  auto ask = [&](bool live, uint4 (&w)[kW], uint4& v) {
+  uint4 own[kW];
+  auto ask = [&](bool live, uint4 (&w)[kW]) {
 #pragma unroll
     for (int j = 0; j < kW; ++j) {
       w[j] = make_uint4(0u, 0u, 0u, 0u);
       if (live && kG * j * V::kN < left) w[j] = V::load(src + kG * j * V::kN);
     }
-    v = make_uint4(0u, 0u, 0u, 0u);
-    if (!kInter && live && rope >= 0) v = V::load(src + src_to_partner);
   };
-  ask(h < h_end, own, with);
+  ask(h < h_end, own);
   for (; __any_sync(0xffffffffu, h < h_end); h += kPass<kG>) {
     const bool live = h < h_end;
     // the next head is on its way while this one is worked on
-    uint4 next[kW], next_with;
+    uint4 next[kW];
     src += kPass<kG> * p.q_s1;
-    ask(h + kPass<kG> < h_end, next, next_with);
+    ask(h + kPass<kG> < h_end, next);
     float by = 1.f;
     if (norm) {
       float sum = 0.f;
@@ -258,165 +265,243 @@ __device__ __forceinline__ void query_rows(const QueryPart& p, const Angles& ang
       by = norm_factor(sum, p.W, eps);
     }
     __syncwarp();   // the outputs may be q's own columns: every load of a head comes before any store
-    if (live) {
+    float r[V::kN] = {}, y[V::kN] = {};
 #pragma unroll
-      for (int j = 0; j < kW; ++j) {
-        if (kG * j * V::kN >= left) continue;
-        const int c = p.first + (l + kG * j) * V::kN;
-        float x[V::kN];
-        V::open(own[j], x);
-        if (norm) V::scale(x, by, V::load(wgt + kG * j * V::kN));
-        if (c < p.P) {
-          *reinterpret_cast<uint4*>(nope + kG * j * V::kN) = V::close(x);
-          continue;
-        }
-        float y[V::kN] = {};
-        if (!kInter) {
-          V::open(with, y);
-          if (norm) V::scale(y, by, V::load(wgt + src_to_partner));
-        }
-        turn.turn(x, y);
-        *reinterpret_cast<uint4*>(pe) = V::close(x);
+    for (int j = 0; j < kW; ++j) {
+      if (!live || kG * j * V::kN >= left) continue;
+      float x[V::kN];
+      V::open(own[j], x);
+      if (norm) V::scale(x, by, V::load(wgt + kG * j * V::kN));
+      if (p.first + (l + kG * j) * V::kN < p.P) {
+        *reinterpret_cast<uint4*>(nope + kG * j * V::kN) = V::close(x);
+      } else {
+#pragma unroll
+        for (int k = 0; k < V::kN; ++k) r[k] = x[k];
       }
+    }
+    if (!kInter) {
+#pragma unroll
+      for (int k = 0; k < V::kN; ++k) y[k] = __shfl_sync(0xffffffffu, r[k], partner, kG);
+    }
+    if (live && rope >= 0) {
+      turn.turn(r, y);
+      *reinterpret_cast<uint4*>(pe) = V::close(r);
     }
 #pragma unroll
     for (int j = 0; j < kW; ++j) own[j] = next[j];
-    with = next_with;
     nope += kPass<kG> * p.n_s1;
     pe += kPass<kG> * p.p_s1;
     wgt += kPass<kG> * p.w_s0;
   }
 }
 
-// New cache rows, plain or e4m3, in words: a warp a row, up to kW words a lane. The row is asked for at once with
-// its slot and its position.
-template <typename T, int kFmt, int kW, bool kInter>
-__device__ __forceinline__ void cache_rows(const RowPart& p, const Angles& ang, float eps, int block) {
+// Codes of x / scale, the quotient first rounded to the nearest float32. For scales of ordinary size by Markstein's
+// steps (divide2 with a last step to the nearest), two at a time: quotients beyond 1024 saturate, so
+// larger values are cut there, where no step overflows; what underflows in them has the code 0.
+struct Quotients {
+  float scale, most;
+  uint64_t ns, r;
+  bool plain;     // a scale so small or large that the steps could leave the range of normal numbers
+  __device__ __forceinline__ explicit Quotients(float s) : scale(s), most(1024.f * fabsf(s)), plain(!(fabsf(s) > 0x1p-60f && fabsf(s) < 0x1p60f)) {
+    const float inv = __frcp_rn(plain ? 1.f : s);
+    ns = pair(-s, -s);
+    r = pair(inv, inv);
+  }
+  __device__ __forceinline__ uint32_t codes(float x0, float x1) const {
+    if (plain) return codes2(__fdiv_rn(x0, scale), __fdiv_rn(x1, scale));
+    asm("min.NaN.f32 %0, %0, %2;\n\tmax.NaN.f32 %0, %0, %3;\n\tmin.NaN.f32 %1, %1, %2;\n\tmax.NaN.f32 %1, %1, %3;"
+        : "+f"(x0), "+f"(x1) : "f"(most), "f"(-most));
+    const uint64_t x = pair(x0, x1);
+    uint64_t q, rem;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q) : "l"(x), "l"(r));
+    asm("fma.rm.f32x2 %0, %1, %2, %3;" : "=l"(rem) : "l"(q), "l"(ns), "l"(x));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(q) : "l"(rem), "l"(r), "l"(q));
+    asm("fma.rm.f32x2 %0, %1, %2, %3;" : "=l"(rem) : "l"(q), "l"(ns), "l"(x));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(q) : "l"(rem), "l"(r), "l"(q));
+    return codes2(__uint_as_float((uint32_t)q), __uint_as_float((uint32_t)(q >> 32)));
+  }
+};
+
+// New cache rows, plain or e4m3, in words: a warp a row, up to kW words a lane. kLoop: rows from `first` on, every
+// `step`th, each asked for, with its slot and position, while the one before is worked on; else one row (beside
+// query heads, whose registers the second row would take).
+template <typename T, int kFmt, int kW, bool kInter, bool kLoop>
+__device__ __forceinline__ void cache_rows(const RowPart& p, const Angles& ang, float eps, int64_t first, int64_t step) {
   using V = Word<T>;
-  const int lane = threadIdx.x & 31;
-  const int64_t t = (int64_t)block * (kThreads / 32) + (threadIdx.x >> 5);
-  if (t >= p.tokens) return;
-  const T* src = static_cast<const T*>(p.kv) + t * p.k_s0 + lane * V::kN;
-  const T* wgt = static_cast<const T*>(p.weight) + lane * V::kN;
-  const int left = p.E - lane * V::kN, half = ang.R >> 1;
-  uint4 own[kW], with = make_uint4(0u, 0u, 0u, 0u);
+  const int lane = threadIdx.x & 31, left = p.E - lane * V::kN, half = ang.R >> 1;
   int rope = -1;
 #pragma unroll
-  for (int j = 0; j < kW; ++j) {
-    own[j] = make_uint4(0u, 0u, 0u, 0u);
-    if (32 * j * V::kN < left) {
-      own[j] = V::load(src + 32 * j * V::kN);
-      if ((lane + 32 * j) * V::kN >= p.L) rope = (lane + 32 * j) * V::kN - p.L;
+  for (int j = 0; j < kW; ++j)
+    if (32 * j * V::kN < left && (lane + 32 * j) * V::kN >= p.L) rope = (lane + 32 * j) * V::kN - p.L;
+  const int partner = partner_lane<V::kN>(rope, half, lane) & 31;
+  const T* const wgt = static_cast<const T*>(p.weight) + lane * V::kN;
+  struct Row {
+    uint4 own[kW];
+    int64_t slot, pos;
+  };
+  auto ask = [&](int64_t t, Row& r) {
+    const T* const src = static_cast<const T*>(p.kv) + t * p.k_s0 + lane * V::kN;
+#pragma unroll
+    for (int j = 0; j < kW; ++j) {
+      r.own[j] = make_uint4(0u, 0u, 0u, 0u);
+      if (t < p.tokens && 32 * j * V::kN < left) r.own[j] = V::load(src + 32 * j * V::kN);
     }
-  }
-  if (!kInter && rope >= 0)
-    with = V::load(static_cast<const T*>(p.kv) + t * p.k_s0 + p.L + (rope < half ? rope + half : rope - half));
-  const int64_t off = row_offset(p, t, lane);
-  const float* cs = ang.of(t);
-  if (off < 0 || (ang.R != 0 && cs == nullptr)) return;
-  Turn<V::kN, kInter> turn;
-  if (rope >= 0) turn.open(cs, rope, half, ang.words);
-  float sum = 0.f;
+    r.slot = t < p.tokens ? p.slots[t] : -1;
+    r.pos = t < p.tokens && ang.R != 0 ? ang.positions[t] : 0;
+  };
+  Row row;
+  ask(first, row);
+  const Quotients quotients(kFmt == kE4m3 ? *p.scale : 1.f);
+  for (int64_t t = first; t < p.tokens; t += step) {
+    Row next;
+    if (kLoop) ask(t + step, next);
+    const int64_t off = row_offset(p, row.slot, lane);
+    const float* cs = off < 0 ? nullptr : ang.row(row.pos, lane);
+    Turn<V::kN, kInter> turn;
+    if (rope >= 0 && cs != nullptr) turn.open(cs, rope, half, ang.words);
+    if (off >= 0 && (ang.R == 0 || cs != nullptr)) {   // the same for the whole warp
+      float sum = 0.f;
 #pragma unroll
-  for (int j = 0; j < kW; ++j) {
-    const float s = V::squares(own[j]);
-    if ((lane + 32 * j) * V::kN < p.L) sum += s;
-  }
+      for (int j = 0; j < kW; ++j) {
+        const float s = V::squares(row.own[j]);
+        if ((lane + 32 * j) * V::kN < p.L) sum += s;
+      }
 #pragma unroll
-  for (int m = 1; m < 32; m <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-  const float by = norm_factor(sum, p.L, eps);
-  const float scale = kFmt == kE4m3 ? *p.scale : 1.f;
+      for (int m = 1; m < 32; m <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+      const float by = norm_factor(sum, p.L, eps);
+      auto put = [&](int c, const float (&x)[V::kN]) {
+        if constexpr (kFmt == kPlain) {
+          *reinterpret_cast<uint4*>(static_cast<T*>(p.cache) + off + c) = V::close(x);
+        } else {
+          uint32_t w[V::kN / 4] = {};
 #pragma unroll
-  for (int j = 0; j < kW; ++j) {
-    const int c = (lane + 32 * j) * V::kN;
-    if (c >= p.E) continue;
-    float x[V::kN];
-    V::open(own[j], x);
-    if (c < p.L) {
-      V::scale(x, by, V::load(wgt + 32 * j * V::kN));
-    } else {
-      float y[V::kN];
-      V::open(with, y);
-      turn.turn(x, y);
+          for (int k = 0; k < V::kN; k += 2) w[k >> 2] |= quotients.codes(x[k], x[k + 1]) << (8 * (k & 2));
+          uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.cache) + off + c);
+#pragma unroll
+          for (int k = 0; k < V::kN / 4; ++k) o[k] = w[k];
+        }
+      };
+      float r[V::kN] = {}, y[V::kN] = {};
+#pragma unroll
+      for (int j = 0; j < kW; ++j) {
+        const int c = (lane + 32 * j) * V::kN;
+        if (c >= p.E) continue;
+        float x[V::kN];
+        V::open(row.own[j], x);
+        if (c < p.L) {
+          V::scale(x, by, V::load(wgt + 32 * j * V::kN));
+          put(c, x);
+        } else {
+#pragma unroll
+          for (int k = 0; k < V::kN; ++k) r[k] = x[k];
+        }
+      }
+      if (!kInter) {
+#pragma unroll
+        for (int k = 0; k < V::kN; ++k) y[k] = __shfl_sync(0xffffffffu, r[k], partner);
+      }
+      if (rope >= 0) {
+        turn.turn(r, y);
+        put(p.L + rope, r);
+      }
     }
-    if constexpr (kFmt == kPlain) {
-      *reinterpret_cast<uint4*>(static_cast<T*>(p.cache) + off + c) = V::close(x);
-    } else {
-      uint32_t w[V::kN / 4] = {};
-#pragma unroll
-      for (int k = 0; k < V::kN; k += 2) w[k >> 2] |= codes2(__fdiv_rn(x[k], scale), __fdiv_rn(x[k + 1], scale)) << (8 * (k & 2));
-      uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.cache) + off + c);
-#pragma unroll
-      for (int k = 0; k < V::kN / 4; ++k) o[k] = w[k];
-    }
+    if (!kLoop) break;
+    row = next;
   }
 }
 
 // New rows as ds_mla entries: a warp a row, sixteen latents and two rope columns a lane, so that a group of 128
 // is eight lanes and its scale worked out once a lane (with a 16-byte word a lane, four groups a lane of four
-// float32 values each: 25 us for 20011 rows instead of DS_US). vec: aligned 16-byte words; wide: 32-byte aligned.
+// float32 values each: 25 us for 20011 rows; 17 with one row a warp, 15 with the next row on its way). vec: aligned
+// 16-byte words; wide: 32-byte aligned rows.
 template <typename T, bool kInter>
-__device__ __forceinline__ void ds_mla_rows(const RowPart& p, const Angles& ang, float eps, int block, bool vec, bool wide) {
+__device__ __forceinline__ void ds_mla_rows(const RowPart& p, const Angles& ang, float eps, int64_t first, int64_t step,
+                                            bool vec, bool wide) {
   const int lane = threadIdx.x & 31;
-  const int64_t t = (int64_t)block * (kThreads / 32) + (threadIdx.x >> 5);
-  if (t >= p.tokens) return;
-  const T* const row = static_cast<const T*>(p.kv) + t * p.k_s0;
-  const T* const rope = row + kDsMlaLatent;
-  const T* const wgt = static_cast<const T*>(p.weight) + 16 * lane;
-  // columns 2 lane and 2 lane + 1; half a rope apart their partners lie 32 columns on or back
-  const int partner = 2 * lane ^ 32;
-  float x[16];
-  float2 pe, with = make_float2(0.f, 0.f);
-  if (vec) {
-    load16(row + 16 * lane, x, wide);
-    pe = load2(rope + 2 * lane);
-    if (!kInter) with = load2(rope + partner);
-  } else {
+  constexpr int kRaw = 16 * sizeof(T) / 4;           // 32-bit words of sixteen values
+  struct Row {
+    uint32_t x[kRaw];
+    float2 pe;
+    int64_t slot, pos;
+  };
+  auto ask = [&](int64_t t, Row& r) {
+    r.slot = r.pos = -1;
+    if (t >= p.tokens) return;
+    const T* const src = static_cast<const T*>(p.kv) + t * p.k_s0 + 16 * lane;
+    const T* const rope = static_cast<const T*>(p.kv) + t * p.k_s0 + kDsMlaLatent + 2 * lane;
+    if (vec) {
 #pragma unroll
-    for (int k = 0; k < 16; ++k) x[k] = to_f(row[16 * lane + k]);
-    pe = make_float2(to_f(rope[2 * lane]), to_f(rope[2 * lane + 1]));
-    if (!kInter) with = make_float2(to_f(rope[partner]), to_f(rope[partner + 1]));
-  }
-  const int64_t off = row_offset(p, t, lane);
-  const float* cs = ang.of(t);
-  if (off < 0 || cs == nullptr) return;
-  Turn<2, kInter> turn;
-  turn.open(cs, 2 * lane, 32, false);
-  uint64_t sum2 = 0;
+      for (int k = 0; k < kRaw; k += 8) load_words(src + k * (int)(4 / sizeof(T)), reinterpret_cast<uint32_t (&)[8]>(r.x[k]), wide);
+      r.pe = load2(rope);
+    } else {
+      T* const x = reinterpret_cast<T*>(r.x);
 #pragma unroll
-  for (int k = 0; k < 16; k += 2) {
-    const uint64_t v = pair(x[k], x[k + 1]);
-    asm("fma.rn.f32x2 %0, %1, %1, %0;" : "+l"(sum2) : "l"(v));
-  }
-  float sum = __uint_as_float((uint32_t)sum2) + __uint_as_float((uint32_t)(sum2 >> 32));
-#pragma unroll
-  for (int m = 1; m < 32; m <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-  const float by = norm_factor(sum, kDsMlaLatent, eps);
+      for (int k = 0; k < 16; ++k) x[k] = src[k];
+      r.pe = make_float2(to_f(rope[0]), to_f(rope[1]));
+    }
+    r.slot = p.slots[t];
+    r.pos = ang.positions[t];
+  };
+  Row row;
+  ask(first, row);
+  float w[16];
   {
-    float w[16];   // from L1, all but the first time; held from the start they cost the block a fifth of its warps
+    const T* const wgt = static_cast<const T*>(p.weight) + 16 * lane;
     if (vec) {
       load16(wgt, w, false);
     } else {
 #pragma unroll
       for (int k = 0; k < 16; ++k) w[k] = to_f(wgt[k]);
     }
-#pragma unroll
-    for (int k = 0; k < 16; ++k) x[k] = x[k] * by * w[k];
   }
-  uint32_t codes[4];
-  const float scale = quantise_group(x, codes);
-  uint8_t* const o = static_cast<uint8_t*>(p.cache) + off;
-  *reinterpret_cast<uint4*>(o + 16 * lane) = make_uint4(codes[0], codes[1], codes[2], codes[3]);
-  if ((lane & 7) == 0) *reinterpret_cast<float*>(o + kDsMlaLatent + 4 * (lane >> 3)) = scale;
-  float y[2] = {pe.x, pe.y};
-  const float z[2] = {with.x, with.y};
-  turn.turn(y, z);
-  reinterpret_cast<__nv_bfloat162*>(o + kDsMlaRopeByte)[lane] = __floats2bfloat162_rn(y[0], y[1]);
+  for (int64_t t = first; t < p.tokens; t += step) {
+    Row next;
+    ask(t + step, next);
+    const int64_t off = row_offset(p, row.slot, lane);
+    const float* cs = off < 0 ? nullptr : ang.row(row.pos, lane);
+    if (cs != nullptr) {                             // the same for the whole warp
+      Turn<2, kInter> turn;
+      turn.open(cs, 2 * lane, kDsMlaRope / 2, false);
+      float x[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        if constexpr (sizeof(T) == 4)
+          x[k] = __uint_as_float(row.x[k]);
+        else
+          x[k] = __uint_as_float(k & 1 ? row.x[k >> 1] & 0xffff0000u : row.x[k >> 1] << 16);
+      }
+      uint64_t sum2 = 0;
+#pragma unroll
+      for (int k = 0; k < 16; k += 2) {
+        const uint64_t v = pair(x[k], x[k + 1]);
+        asm("fma.rn.f32x2 %0, %1, %1, %0;" : "+l"(sum2) : "l"(v));
+      }
+      float sum = __uint_as_float((uint32_t)sum2) + __uint_as_float((uint32_t)(sum2 >> 32));
+#pragma unroll
+      for (int m = 1; m < 32; m <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+      const float by = norm_factor(sum, kDsMlaLatent, eps);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) x[k] = x[k] * by * w[k];
+      uint32_t codes[4];
+      const float scale = quantise_group(x, codes);
+      uint8_t* const o = static_cast<uint8_t*>(p.cache) + off;
+      *reinterpret_cast<uint4*>(o + 16 * lane) = make_uint4(codes[0], codes[1], codes[2], codes[3]);
+      if ((lane & 7) == 0) *reinterpret_cast<float*>(o + kDsMlaLatent + 4 * (lane >> 3)) = scale;
+      float y[2] = {row.pe.x, row.pe.y}, z[2] = {};
+      if (!kInter) {                                 // columns 2 lane and 2 lane + 1: their partners 32 columns on or back
+        z[0] = __shfl_xor_sync(0xffffffffu, y[0], 16);
+        z[1] = __shfl_xor_sync(0xffffffffu, y[1], 16);
+      }
+      turn.turn(y, z);
+      reinterpret_cast<__nv_bfloat162*>(o + kDsMlaRopeByte)[lane] = __floats2bfloat162_rn(y[0], y[1]);
+    }
+    row = next;
+  }
 }
 
 // Blocks [0, q_blocks) take query heads, the others cache rows.
 template <typename T, int kFmt, int kG, int kW, bool kInter>
-__global__ void __launch_bounds__(kThreads, kInter || kW < 3 ? 4 : 3) norm_rope_kernel(const QueryPart q, const RowPart r, const Angles ang, float eps,
+__global__ void __launch_bounds__(kThreads, kW == 0 ? kRowBlocks : kHeadBlocks) norm_rope_kernel(const QueryPart q, const RowPart r, const Angles ang, float eps,
                                                                 int q_blocks) {
   pdl_enter();
   if constexpr (kW > 0) {
@@ -425,14 +510,16 @@ __global__ void __launch_bounds__(kThreads, kInter || kW < 3 ? 4 : 3) norm_rope_
       return;
     }
   }
-  cache_rows<T, kFmt, sizeof(T) == 4 ? 5 : 3, kInter>(r, ang, eps, blockIdx.x - q_blocks);   // 640 or 768 columns
+  const int64_t first = (int64_t)(blockIdx.x - q_blocks) * (kThreads / 32) + (threadIdx.x >> 5);
+  cache_rows<T, kFmt, sizeof(T) == 4 ? 5 : 3, kInter, kW == 0>(r, ang, eps, first, (int64_t)(gridDim.x - q_blocks) * (kThreads / 32));   // 640 or 768 columns
 }
 
 template <typename T, bool kInter>
-__global__ void __launch_bounds__(kThreads, 5) norm_rope_ds_mla_kernel(const RowPart r, const Angles ang, float eps, int vec,
+__global__ void __launch_bounds__(kThreads, kRowBlocks) norm_rope_ds_mla_kernel(const RowPart r, const Angles ang, float eps, int vec,
                                                                        int wide) {
   pdl_enter();
-  ds_mla_rows<T, kInter>(r, ang, eps, blockIdx.x, vec, wide);
+  const int64_t first = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  ds_mla_rows<T, kInter>(r, ang, eps, first, (int64_t)gridDim.x * (kThreads / 32), vec, wide);
 }
 
 // ---------------------------------------------------------------------------
@@ -494,7 +581,7 @@ __global__ void __launch_bounds__(256) norm_rope_any_kernel(const QueryPart q, c
   }
   const int64_t t = (int64_t)(blockIdx.x - q_blocks) * 8 + warp;
   if (t >= r.tokens) return;
-  const int64_t off = row_offset(r, t, lane);
+  const int64_t off = row_offset(r, r.slots[t], lane);
   if (off < 0) return;
   const float* cs = ang.of(t);
   if (ang.R != 0 && cs == nullptr) return;
@@ -534,10 +621,15 @@ bool in_words(const QueryPart& q, const RowPart& r, int fmt, const Angles& a) {
   return true;
 }
 
+// Blocks for `tokens` rows, eight warps each: no more than run at once.
+unsigned row_blocks(int64_t tokens, int blocks_per_sm) {
+  return (unsigned)std::min<int64_t>((tokens + 7) / 8, (int64_t)blocks_per_sm * device_sm_count());
+}
+
 template <typename T, int kFmt, bool kInter>
 cudaError_t launch_words(QueryPart q, const RowPart& r, const Angles& ang, float eps, cudaStream_t st) {
   constexpr int per = Word<T>::kN;
-  const unsigned r_blocks = (unsigned)((r.tokens + 7) / 8);
+  const unsigned r_blocks = q.tokens == 0 ? row_blocks(r.tokens, kRowBlocks) : (unsigned)((r.tokens + 7) / 8);
   if (q.tokens == 0) return launch_k(norm_rope_kernel<T, kFmt, 32, 0, kInter>, r_blocks, kThreads, 0, st, q, r, ang, eps, 0);
   if constexpr (kFmt == kPlain) {
     // the fewest lanes that hold a head in four words each, the rope in one; and no more words than it takes
@@ -576,14 +668,14 @@ cudaError_t launch_ds_mla(const RowPart& r, const Angles& ang, float eps, cudaSt
   const int vec = aligned16(r.kv) && r.k_s0 % per == 0 && aligned16(r.weight);
   const int wide = reinterpret_cast<uintptr_t>(r.kv) % 32 == 0 && r.k_s0 % (2 * per) == 0;
   return launch_k(ang.interleaved ? norm_rope_ds_mla_kernel<T, true> : norm_rope_ds_mla_kernel<T, false>,
-                  (unsigned)((r.tokens + 7) / 8), kThreads, 0, st, r, ang, eps, vec, wide);
+                  row_blocks(r.tokens, kRowBlocks), kThreads, 0, st, r, ang, eps, vec, wide);
 }
 
 }  // namespace
 
 cudaError_t launch_norm_rope(mla_dtype dt, const NormRopeCall& c, cudaStream_t st) {
   QueryPart q{};
-  RowPart r{};
+  RowPart r{nullptr, 0, nullptr, nullptr, 0, 0, 0, PageOf(1), 0, 0, nullptr, 0, nullptr};
   Angles ang{c.positions, c.cos_sin, c.cos_sin_stride, c.num_positions, c.R, c.interleaved,
              aligned16(c.cos_sin) && c.cos_sin_stride % 4 == 0 && c.R % 8 == 0};
   if (c.tokens > 0 && c.H > 0) {
@@ -597,7 +689,7 @@ cudaError_t launch_norm_rope(mla_dtype dt, const NormRopeCall& c, cudaStream_t s
   }
   if (c.rows) {
     r = RowPart{c.kv.data, c.kv.s0, c.kv_weight, c.cache.data, c.cache.s0, c.cache.s1, c.cache.n0 * c.cache.n1,
-                (int32_t)c.cache.n1, c.L, c.L + c.R, c.slots, c.tokens, c.scale};
+                PageOf((int32_t)c.cache.n1), c.L, c.L + c.R, c.slots, c.tokens, c.scale};
   }
   if (q.tokens == 0 && r.tokens == 0) return cudaSuccess;
   const bool f32 = dt == MLA_F32;
