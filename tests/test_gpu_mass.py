@@ -184,3 +184,26 @@ def test_more_sequences_than_a_block_has_threads(mla, prefill):
     got = c.run(mla, 0.5)
     c.check(got, 0.5)
     assert torch.equal(got, c.run(mla, 0.5))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("prefill", [False, True])
+def test_masses_in_a_wider_buffer(mla, dtype, prefill):
+    c = Case(43, dtype, 16, 576, 64, [300, 90, 0, 129], [5, 6, 0, 129] if prefill else None)
+    wide = torch.full((4, c.rows + 9), 7.0, device="cuda")
+    mass = wide[:, 3:3 + c.rows]
+    mass.copy_(c.mass)
+    got = c.run(mla, 0.5, mass=mass)
+    c.check(got.contiguous(), 0.5)
+    assert (wide[:, :3] == 7).all() and (wide[:, 3 + c.rows:] == 7).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_more_rows_than_masses(mla, dtype):
+    # a length beyond the masses counts as the largest that they hold, and is reported
+    c = Case(47, dtype, 16, 576, 64, [300, 90])
+    whole = c.run(mla)
+    got = c.run(mla, mass=c.mass[:, :200].clone())
+    with pytest.raises(mla.MlaError):
+        mla.mla_device_error()
+    assert torch.equal(got, whole[:, :200])

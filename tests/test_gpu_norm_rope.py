@@ -229,3 +229,85 @@ def test_captured_and_on_another_stream(mla):
     for o in outs[1:]:
         for a, b in zip(outs[0], o):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("dims", [(16, 0, 64, 512), (16, 64, 0, 512), (2, 0, 2, 3), (4, 64, 512, 64), (4, 8, 24, 40)])
+def test_heads_of_rope_alone_and_of_none(mla, dtype, dims):
+    heads, nope, rope, latent = dims
+    for norm in (False, True):
+        for interleaved in (False, True):
+            q, kv, w, kw, pos, cs = inputs(7, 9, dims, dtype)
+            w = w if norm else None
+            n, r = torch.zeros(9, heads, nope, dtype=dtype, device="cuda"), torch.zeros(9, heads, rope, dtype=dtype, device="cuda")
+            cache, slots = torch.zeros(2, 8, latent + rope, dtype=dtype, device="cuda"), torch.arange(9)
+            mla.mla_norm_rope_q_cache_write(n, r, q.cuda(), None if w is None else w.cuda(), cache, kv.cuda(), kw.cuda(), pos.cuda(),
+                                            cs.cuda(), slots.cuda(), eps=EPS, interleaved=interleaved)
+            mla.mla_device_error()
+            (wn, en), (wr, er) = ref.queries(q, w, nope, cs[pos], interleaved, EPS)
+            ref.check(n, wn, en, dtype, "nope")
+            ref.check(r, wr, er, dtype, "rope")
+            want, err = ref.rows(kv, kw, cs[pos], interleaved, EPS)
+            ref.check(cache.view(16, -1)[:9], want, err, dtype, "rows")
+
+
+@pytest.mark.parametrize("form", ["", "_fp8", "_ds_mla"])
+@pytest.mark.parametrize("offset,pad", [(0, 4), (1, 0), (0, 3), (2, 2)])
+def test_tables_of_other_strides(mla, form, offset, pad):
+    # a table cut from a wider one, its rows on any 4-byte boundary: the results do not change
+    _, kv, _, w, pos, cs = inputs(9, 20, LITE, BF16)
+    wide = torch.full((POSITIONS * (64 + pad) + offset,), float("nan"), device="cuda")
+    other = wide[offset:].view(POSITIONS, 64 + pad)[:, :64]
+    other.copy_(cs)
+    got = []
+    for table in (cs.cuda(), other):
+        cache = torch.zeros(3, 8, 656 if form == "_ds_mla" else 576, dtype=torch.uint8 if form else BF16, device="cuda")
+        more = [torch.tensor([0.01], device="cuda")] if form == "_fp8" else []
+        for interleaved in (False, True):
+            getattr(mla, "mla_norm_rope_cache_write" + form)(cache, kv.cuda(), w.cuda(), pos.cuda(), table, torch.arange(20).cuda(), *more,
+                                                             eps=EPS, interleaved=interleaved)
+            got.append(cache.clone())
+    assert torch.equal(got[0], got[2]) and torch.equal(got[1], got[3])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("scale", [0.0171, 1.0, 2.0 ** -70, 3e25, 1e-30, 2.0 ** 60, -0.5])
+def test_e4m3_quotients_are_the_cache_writes(mla, dtype, scale):
+    # at position 0 the rotation leaves every value as it is, so the rope columns' codes are those that
+    # mla_cache_write_fp8 gives the same values: infinities, NaN, zeros of both signs and values near the middle of codes too
+    g = torch.Generator().manual_seed(5)
+    rows, rope, latent = 300, 256, 16
+    x = torch.randn(rows, rope, generator=g) * torch.exp(6 * torch.randn(rows, 1, generator=g)) * abs(scale)
+    x[:20] = (torch.arange(20 * rope).view(20, rope) % 2048 - 1024) / 8 * scale          # codes, middles of codes
+    x[20:24] = torch.tensor([0.0, -0.0, float("inf"), -float("inf"), float("nan"), 3e38, -3e38, 1e-45]).repeat(4, rope // 8)
+    x = x.to(dtype).cuda()
+    kv = torch.cat([torch.ones(rows, latent, dtype=dtype, device="cuda"), x], 1)
+    cs = torch.cat([torch.ones(1, rope // 2), torch.zeros(1, rope // 2)], 1).cuda()
+    slots, zero = torch.arange(rows, device="cuda"), torch.zeros(rows, dtype=torch.int64, device="cuda")
+    s = torch.tensor([scale], device="cuda")
+    a, b = (torch.zeros(5, 64, latent + rope, dtype=torch.uint8, device="cuda") for _ in range(2))
+    finite = torch.isfinite(x).all(1).cpu()
+    for interleaved in (False, True):
+        mla.mla_norm_rope_cache_write_fp8(a, kv, torch.ones(latent, dtype=dtype, device="cuda"), zero, cs, slots, s, interleaved=interleaved)
+        mla.mla_cache_write_fp8(b, kv[:, :latent], x, slots, s)
+        mla.mla_device_error()
+        u, v = (t.view(320, -1)[:rows, latent:].cpu()[finite] for t in (a, b))
+        # x c - y 0 and y c + x 0 are x and y, but for the sign of a zero
+        zero_sign = (u ^ v) == 0x80
+        assert ((u == v) | (zero_sign & (u & 0x7F == 0))).all()
+
+
+def test_many_rows_one_behind_the_other(mla):
+    # more rows than warps run at once, so that a warp takes several
+    for form, dtype in (("", BF16), ("", F32), ("_fp8", BF16), ("_ds_mla", F32), ("_ds_mla", BF16)):
+        _, kv, _, w, pos, cs = inputs(17, 9001, LITE, dtype)
+        slots = slots_of(3, 9001, 9100)
+        cache = torch.zeros(91, 100, 656 if form == "_ds_mla" else 576, dtype=torch.uint8 if form else dtype, device="cuda")
+        one = torch.zeros_like(cache)
+        more = [torch.tensor([0.01], device="cuda")] if form == "_fp8" else []
+        call = getattr(mla, "mla_norm_rope_cache_write" + form)
+        kv, w, pos, cs, slots = kv.cuda(), w.cuda(), pos.cuda(), cs.cuda(), slots.cuda()
+        call(cache, kv, w, pos, cs, slots, *more, eps=EPS)
+        for i in range(0, 9001, 1500):                # few enough for a warp each
+            call(one, kv[i:i + 1500], w, pos[i:i + 1500], cs, slots[i:i + 1500], *more, eps=EPS)
+        assert torch.equal(cache, one)
