@@ -13,10 +13,17 @@
 //   decode:  a sequence's queries stay (N = its heads, rounded up to 32), its rows stream: each
 //            crosses HBM and L2 once;
 //   prefill: 256 rows stay, the tokens' queries stream (N = 256): each byte of them loaded by a CTA serves
-//            512 x 64 multiplications, so that L2 feeds the tensor pipe at 32 bytes a cycle.
+//            512 x 64 multiplications, so that L2 feeds the tensor pipe at 32 bytes a cycle. (With N = 128 the operands'
+//            reads of shared memory bound the products: 910 us for the 4 x 512 prefill below instead of 700.)
 // Resident chunks are released one by one by the last tile that reads them, and the next ones loaded under it.
-// Tensor memory holds two accumulators of 256 columns; the four epilogue warps sum one while the next is
-// computed.
+//
+// Sums. The tensor cores' additions into an accumulator round toward zero, so that a score's error grows with the
+// length of the chain and does not average out over queries: with one accumulator for the 36 steps of a 576-wide
+// row, masses came out 1.4e-6 of themselves too small. So the first half of the chunks goes to one accumulator and
+// the rest to another, which the epilogue adds: 0.65e-6. A decode's two fit into tensor memory twice, so that
+// one tile is summed while the next is computed. A prefill's fill it (2 x 256 columns): there the epilogue's eight warps
+// take the first into registers (128 a thread, lent by the other warps) while the second is computed, and the second
+// while the next tile's first is: 6% slower than one accumulator in two places (12% at 32 tokens over 16K rows).
 //
 // Work. Tiles (256 rows x N queries) are numbered through all sequences and dealt out in equal consecutive
 // ranges, one a cluster; where a range begins is worked out by each cluster from the lengths. A prefill's
@@ -29,6 +36,7 @@
 #include <math_constants.h>
 
 #include <algorithm>
+#include <atomic>
 #include <mutex>
 #include <vector>
 
@@ -45,11 +53,20 @@ __device__ unsigned g_mass_tc_err = 0;
 constexpr int kRows = 256, kCtaRows = 128;         // cache rows of a tile, and of one CTA of the pair
 constexpr int kChunkBytes = kCtaRows * 128;        // 128 rows x 64 bf16 columns, 128-byte swizzle
 constexpr int kMaxChunks = 9, kMaxStages = 12;
-constexpr int kThreads = 256;
-constexpr int kEpiWarp0 = 4, kEpiThreads = 128, kEpiBar = 1;
+constexpr int kEpiWarp0 = 4, kEpiBar = 1;
+template <bool kPrefill>
+constexpr int kEpiThreads = kPrefill ? 256 : 128;
+template <bool kPrefill>
+constexpr int kThreads = 128 + kEpiThreads<kPrefill>;
+// registers of a thread of a prefill: at launch (what 384 threads may have), of the first four warps, of the others
+constexpr int kLaunchRegs = 168, kRoleRegs = 72, kEpiRegs = 216;
+static_assert(kRoleRegs * 128 + kEpiRegs * 256 <= kLaunchRegs * 384, "the shares draw on the launch's registers");
 constexpr int kMiscBytes = 3 * 1024;
 constexpr int kArena = 232448 - kMiscBytes;        // shared memory for operands: 224 KB
 constexpr int kMaxUnits = 256;
+// tensor memory columns from a tile's first accumulator to its second
+template <bool kPrefill>
+constexpr uint32_t kSecond = kPrefill ? 256 : 128;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Where a tile lies: inner tile `tile` of outer tile `outer` of sequence seq; base: tiles before the sequence.
@@ -61,19 +78,21 @@ struct Place {
 struct Shared {
   uint64_t ring_full[kMaxStages], ring_empty[kMaxStages];   // full: first CTA, bytes of both
   uint64_t res_full[kMaxChunks], res_empty[kMaxChunks];
-  uint64_t d_full[2], d_empty[2];                           // d_empty: first CTA, epilogue warps of both
+  // decode: of even and odd tiles; prefill: of a tile's two accumulators. d_empty: first CTA, epilogue warps of both
+  uint64_t d_full[2], d_empty[2];
   uint64_t fin;
   uint32_t tmem_base;
   int abort_flag;
   Place found;
-  long long wide[8];
+  long long wide[12];
   float neg_lse[2][256];     // -lse * log2(e) of a tile's columns, in turn in two places
 };
 static_assert(sizeof(Shared) <= kMiscBytes, "barrier block overflows its slot");
 
 struct TcArgs {
   MassArgs m;
-  int chunks, stages;        // of 64 columns; of the ring
+  int chunks, split;         // of 64 columns; those before `split` are summed apart from the others
+  int stages;                // of the ring
   int n, half;               // query rows of a tile, and of one CTA
   int tpc;                   // prefill: tokens of a tile per CTA
   // a prefill's pieces of rows that are cut, of each unit: those that end in its first tiles, and that begin in its
@@ -126,13 +145,13 @@ struct Tiles {
   __device__ long long total() const { return outer == 0 ? 0 : before(outer); }
 };
 
-// Tiles of the whole call. All threads of the block (256) take part here and in find_tile, and every one gets
+// Tiles of the whole call. All threads of the block take part here and in find_tile, and every one gets
 // the answer.
 template <bool kPrefill>
 __device__ long long all_tiles(const TcArgs& a, long long* sh) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   long long sum = 0;
-  for (int b = threadIdx.x; b < a.m.B; b += kThreads) {
+  for (int b = threadIdx.x; b < a.m.B; b += kThreads<kPrefill>) {
     Tiles<kPrefill> t;
     t.open(a, b);
     sum += t.total();
@@ -143,7 +162,7 @@ __device__ long long all_tiles(const TcArgs& a, long long* sh) {
   __syncthreads();
   sum = 0;
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) sum += sh[w];
+  for (int w = 0; w < kThreads<kPrefill> / 32; ++w) sum += sh[w];
   __syncthreads();
   return sum;
 }
@@ -156,7 +175,7 @@ __device__ Place place_in(const TcArgs& a, long long x, Place* found) {
   t.open(a, p.seq);
   if constexpr (kPrefill) {
     // the outer tile that holds x: the threads look at one each
-    for (int k = threadIdx.x; k < t.outer; k += kThreads) {
+    for (int k = threadIdx.x; k < t.outer; k += kThreads<kPrefill>) {
       const long long lo = p.base + t.before(k);
       const int n = t.inner - t.first(k);
       if (lo <= x && x < lo + n) {
@@ -178,7 +197,7 @@ template <bool kPrefill>
 __device__ Place find_tile(const TcArgs& a, long long x, long long* sh, Place* found) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   long long base = 0;
-  for (int b0 = 0; b0 < a.m.B; b0 += kThreads) {
+  for (int b0 = 0; b0 < a.m.B; b0 += kThreads<kPrefill>) {
     const int b = b0 + threadIdx.x;
     Tiles<kPrefill> t;
     long long mine = 0;
@@ -196,7 +215,7 @@ __device__ Place find_tile(const TcArgs& a, long long x, long long* sh, Place* f
     __syncthreads();
     long long all = 0, before = base;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
+    for (int w = 0; w < kThreads<kPrefill> / 32; ++w) {
       if (w == warp) before = base + all;
       all += sh[w];
     }
@@ -211,7 +230,7 @@ __device__ Place find_tile(const TcArgs& a, long long x, long long* sh, Place* f
 // This unit's tiles [x0, x1), and where x0 lies if there are any.
 template <bool kPrefill>
 __device__ Place my_tiles(const TcArgs& a, int unit, int units, long long& x0, long long& x1, long long* sh, Place* found) {
-  if (a.m.B > kThreads) {
+  if (a.m.B > kThreads<kPrefill>) {
     const long long total = all_tiles<kPrefill>(a, sh);
     x0 = total * unit / units;
     x1 = total * (unit + 1) / units;
@@ -235,7 +254,7 @@ __device__ Place my_tiles(const TcArgs& a, int unit, int units, long long& x0, l
   __syncthreads();
   long long total = 0, before = 0;
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
+  for (int w = 0; w < kThreads<kPrefill> / 32; ++w) {
     if (w == warp) before = total;
     total += sh[w];
   }
@@ -289,8 +308,8 @@ struct Walker {
   }
 };
 
-// The wait behind a first look, out of line; the timer is read only every 256 looks.
-__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort) {
+// The wait behind a first look (in line: registers cannot move between warps around a call); the timer is read only every 256 looks.
+__device__ __forceinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort) {
   uint64_t since = 0;
   for (uint32_t i = 1;; ++i) {
     if (mbar_test_cluster(bar, parity)) return true;
@@ -383,11 +402,8 @@ __device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
   return d;
 }
 
-// 32 columns of this lane's scores from tensor memory: e^(scale s - lse) summed, of columns [lo, hi) of them.
-__device__ __forceinline__ float sum_weights(uint32_t taddr, const float* neg_lse, float scale_log2, int lo, int hi) {
-  float v[32];
-  tmem_ld32(taddr, v);
-  tmem_ld_wait();
+// e^(scale s - lse) summed over columns [lo, hi) of 32 scores.
+__device__ __forceinline__ float sum_weights(const float (&v)[32], const float* neg_lse, float scale_log2, int lo, int hi) {
   const uint64_t by = pair_f32(scale_log2, scale_log2);
   uint64_t sum[2] = {0, 0};
   if (__all_sync(0xffffffffu, lo <= 0 && hi >= 32)) {
@@ -410,9 +426,39 @@ __device__ __forceinline__ float sum_weights(uint32_t taddr, const float* neg_ls
   const uint64_t all = add_pair(sum[0], sum[1]);
   return low(all) + high(all);
 }
+// What tensor memory loads asked for, usable behind a wait: arithmetic on the registers, which to the compiler
+// have their values from the load on, stays behind this.
+__device__ __forceinline__ void loaded(float (&w)[16]) {
+  asm volatile(""
+               : "+f"(w[0]), "+f"(w[1]), "+f"(w[2]), "+f"(w[3]), "+f"(w[4]), "+f"(w[5]), "+f"(w[6]), "+f"(w[7]),
+                 "+f"(w[8]), "+f"(w[9]), "+f"(w[10]), "+f"(w[11]), "+f"(w[12]), "+f"(w[13]), "+f"(w[14]), "+f"(w[15]));
+}
+__device__ __forceinline__ void loaded(float (&w)[32]) {
+  asm volatile(""
+               : "+f"(w[0]), "+f"(w[1]), "+f"(w[2]), "+f"(w[3]), "+f"(w[4]), "+f"(w[5]), "+f"(w[6]), "+f"(w[7]),
+                 "+f"(w[8]), "+f"(w[9]), "+f"(w[10]), "+f"(w[11]), "+f"(w[12]), "+f"(w[13]), "+f"(w[14]), "+f"(w[15]),
+                 "+f"(w[16]), "+f"(w[17]), "+f"(w[18]), "+f"(w[19]), "+f"(w[20]), "+f"(w[21]), "+f"(w[22]), "+f"(w[23]),
+                 "+f"(w[24]), "+f"(w[25]), "+f"(w[26]), "+f"(w[27]), "+f"(w[28]), "+f"(w[29]), "+f"(w[30]), "+f"(w[31]));
+}
+// The second accumulator's 32 columns added to the first's (in halves: 32 more registers would be spilled).
+__device__ __forceinline__ void add_second(uint32_t taddr, float (&v)[32]) {
+#pragma unroll
+  for (int h = 0; h < 32; h += 16) {
+    float w[16];
+    tmem_ld16(taddr + h, w);
+    tmem_ld_wait();
+    loaded(w);
+#pragma unroll
+    for (int k = 0; k < 16; k += 2) {
+      const uint64_t x = add_pair(pair_f32(v[h + k], v[h + k + 1]), pair_f32(w[k], w[k + 1]));
+      v[h + k] = low(x);
+      v[h + k + 1] = high(x);
+    }
+  }
+}
 
 template <bool kPrefill>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kPrefill>, 1)
     mass_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap qmap, const TcArgs a) {
   extern __shared__ __align__(1024) unsigned char smem[];
   Shared& sh = *reinterpret_cast<Shared*>(smem + kArena);
@@ -434,7 +480,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.d_full[i], 1);
-      mbar_init(&sh.d_empty[i], 2 * kEpiThreads / 32);   // the epilogue warps of both CTAs
+      mbar_init(&sh.d_empty[i], 2 * kEpiThreads<kPrefill> / 32);   // the epilogue warps of both CTAs
     }
     mbar_init(&sh.fin, 1);
     sh.abort_flag = 0;
@@ -464,147 +510,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   wk.init(a, from.seq, from.outer, from.tile, x1 - x0);
   Seg sg;
 
-  if (warp == 0 || warp == 3) {
-    // ------------------------------------------------------------ loads, in both CTAs: warp 0 the ring,
-    // warp 3 the resident operand; keys are looked up by lanes, one a box
-    const bool ring_role = warp == 0;
-    const int rows_box = min(a.m.page, 64), boxes = kCtaRows / rows_box;
-    bool ok = true;
-    auto wait = [&](uint64_t* bar, int parity) { ok = ok && __all_sync(0xffffffffu, wait_for(bar, parity, abort)); };
-    // this lane's box of the CTA's rows of tile k: its block (outside the cache: none, loads zeros) and row
-    auto look_up = [&](const Seg& s, int k, int& id, int& row) {
-      const int t = kRows * k + kCtaRows * (int)rank + lane * rows_box;
-      id = a.m.num_blocks;
-      row = 0;
-      if (lane < boxes && t < s.s.kv) {
-        const int page = t / a.m.page, got = a.m.block_table[s.b * a.m.bt_stride + page];
-        if (got >= 0 && got < a.m.num_blocks) {
-          id = got;
-          row = t - page * a.m.page;
-        }
-      }
-    };
-    auto load_keys = [&](unsigned char* dst, uint64_t* bar, int c, int id, int row) {
-      const uint32_t to = map_to_rank(bar, 0);
-#pragma unroll 1
-      for (int i = 0; i < boxes; ++i)
-        load_pair_3d(dst + i * rows_box * 128, &kmap, to, 64 * c, __shfl_sync(0xffffffffu, row, i),
-                     __shfl_sync(0xffffffffu, id, i));
-      if (rank == 0) expect_bytes(bar, 2 * kChunkBytes);
-    };
-    auto load_queries = [&](unsigned char* dst, uint64_t* bar, int c, int h0, int tok) {
-      load_pair_3d(dst, &qmap, map_to_rank(bar, 0), 64 * c, h0, tok);
-      const int rows = kPrefill ? a.m.H * a.tpc : a.half;
-      if (rank == 0) expect_bytes(bar, 2u * rows * 128);
-    };
-    if (ring_role) {
-      int stage = 0, round = 0;
-      auto take = [&](auto&& load) {   // every chunk of a tile through the ring
-#pragma unroll 1
-        for (int c = 0; ok && c < a.chunks; ++c) {
-          if (round > 0) wait(&sh.ring_empty[stage], (round & 1) ^ 1);
-          if (!ok) break;
-          load(ring + stage * kChunkBytes, &sh.ring_full[stage], c);
-          if (++stage == a.stages) {
-            stage = 0;
-            ++round;
-          }
-        }
-      };
-      while (ok && wk.next(a, sg)) {
-        if (kPrefill) {
-          for (int i = sg.i0; ok && i < sg.i1; ++i) {
-            const int tok = sg.s.q0 + (2 * i + (int)rank) * a.tpc;
-            take([&](unsigned char* dst, uint64_t* bar, int c) { load_queries(dst, bar, c, 0, tok); });
-          }
-        } else {
-          int id, row;
-          look_up(sg, sg.i0, id, row);
-          for (int i = sg.i0; ok && i < sg.i1; ++i) {
-            int id1 = 0, row1 = 0;   // the next tile's: asked for under this one's loads
-            if (i + 1 < sg.i1) look_up(sg, i + 1, id1, row1);
-            take([&](unsigned char* dst, uint64_t* bar, int c) { load_keys(dst, bar, c, id, row); });
-            id = id1;
-            row = row1;
-          }
-        }
-      }
-    } else {
-      for (int g = 0; ok && wk.next(a, sg); ++g) {
-        int id = 0, row = 0;
-        if (kPrefill) look_up(sg, sg.outer, id, row);
-#pragma unroll 1
-        for (int c = 0; ok && c < a.chunks; ++c) {
-          if (g > 0) wait(&sh.res_empty[c], (g & 1) ^ 1);
-          if (!ok) break;
-          if (kPrefill)
-            load_keys(smem + c * res_bytes, &sh.res_full[c], c, id, row);
-          else
-            load_queries(smem + c * res_bytes, &sh.res_full[c], c, (int)rank * a.half, sg.s.q0);
-        }
-      }
-    }
-    if (!ok) {
-      // copies in flight land within microseconds: wait well beyond that before the CTA ends
-      if (lane == 0) {
-        give_up();
-        const uint64_t t0 = globaltimer_ns();
-        while (globaltimer_ns() - t0 < 2000000ull) {
-        }
-      }
-      __syncwarp();
-    }
-  } else if (warp == 1 && rank == 0) {
-    // ------------------------------------------------------------ MMA issuer of the pair
-    const uint32_t idesc = __reduce_max_sync(0xffffffffu, idesc_bf16(kRows, 0, false, false) | (uint32_t)(a.n >> 3) << 17);
-    const uint32_t res_lo = desc_lo(smem), ring_lo = desc_lo(ring);
-    bool ok = true;
-    auto wait = [&](uint64_t* bar, int parity) {
-      ok = ok && __all_sync(0xffffffffu, wait_for(bar, parity, abort));
-      return ok;
-    };
-    int stage = 0, round = 0, x = 0;
-    for (int g = 0; ok && wk.next(a, sg); ++g) {
-      const int i0 = __reduce_max_sync(0xffffffffu, sg.i0), i1 = __reduce_max_sync(0xffffffffu, sg.i1);
-      for (int i = i0; ok && i < i1; ++i, ++x) {
-        const int buf = x & 1;
-        if (x > 1 && !wait(&sh.d_empty[buf], ((x >> 1) & 1) ^ 1)) break;
-        const uint32_t d = __reduce_max_sync(0xffffffffu, 256u * buf);
-#pragma unroll 1
-        for (int c = 0; c < a.chunks; ++c) {
-          if (i == i0 && !wait(&sh.res_full[c], g & 1)) break;
-          if (!wait(&sh.ring_full[stage], round & 1)) break;
-          tc_fence_after();
-          const uint32_t r = __reduce_max_sync(0xffffffffu, res_lo + c * (res_bytes >> 4));
-          const uint32_t s = __reduce_max_sync(0xffffffffu, ring_lo + stage * (kChunkBytes >> 4));
-          umma_pair4(d, kPrefill ? r : s, kPrefill ? s : r, idesc, c == 0);
-          commit_pair(&sh.ring_empty[stage]);
-          if (i + 1 == i1) commit_pair(&sh.res_empty[c]);
-          if (++stage == a.stages) {
-            stage = 0;
-            ++round;
-          }
-        }
-        if (ok) commit_pair(&sh.d_full[buf]);
-      }
-    }
-    if (!ok && lane == 0) give_up();
-    __syncwarp();
-    commit_pair(&sh.fin);
-  } else if (warp >= kEpiWarp0) {
-    // ------------------------------------------------------------ weights and sums: a thread a cache row
-    const int e = tid - kEpiWarp0 * 32;                 // tensor memory lane, the CTA's row
+  // (a prefill's registers move by whole warpgroups: warps 0 to 3 give, 4 to 11 take)
+  if (warp >= kEpiWarp0) {
+    if constexpr (kPrefill) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
+    // ------------------------------------------------------------ weights and sums: a thread a cache row (two in a
+    // prefill, half of the columns each)
+    const int et = tid - kEpiWarp0 * 32, e = et & 127;  // tensor memory lane: the CTA's row
     const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
     const float scale_log2 = a.m.scale * kLog2e;
+    const bool two = a.chunks > 1;
     const uint32_t d_empty = map_to_rank(&sh.d_empty[0], 0);
     // -lse log2(e) of head h of token tok; a query that attended nothing (lse -inf) gives e^-inf
-    auto neg_lse = [&](int tok, int h) {
-      const float l = a.m.lse[(int64_t)tok * a.m.H + h];
-      return l == -CUDART_INF_F ? l : -l * kLog2e;
-    };
+    auto neg_lse = [&](float lse) { return lse == -CUDART_INF_F ? lse : -lse * kLog2e; };
     bool ok = true, mine = true;   // ok: the group's decision; mine: this thread's waits so far
     int x = 0, place = 0;
-    int4 pieces[2] = {make_int4(-1, 0, 0, 0), make_int4(-1, 0, 0, 0)};
+    int4 ending = make_int4(-1, 0, 0, 0), beginning = ending;   // this unit's pieces of rows that are cut
     while (ok && wk.next(a, sg)) {
       const int d = sg.s.kv - sg.s.nq;
       auto row_of = [&](int k) { return kRows * k + kCtaRows * (int)rank + e; };
@@ -619,19 +539,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         return a.m.mass + sg.b * a.m.mass_stride + t;
       };
       if (!kPrefill) {
-        sh.neg_lse[place][e] = e < a.m.H ? neg_lse(sg.s.q0, e) : 0.f;
+        sh.neg_lse[place][e] = e < a.m.H ? neg_lse(a.m.lse[(int64_t)sg.s.q0 * a.m.H + e]) : 0.f;
         for (int i = sg.i0; i < sg.i1; ++i, ++x) {
           const int buf = x & 1;
           float* const to = row_mass(row_of(i));
           const float old = to != nullptr && a.m.decay != 0.f ? *to : 0.f;
           mine = mine && wait_for(&sh.d_full[buf], (x >> 1) & 1, abort);
-          ok = named_bar_and(kEpiBar, kEpiThreads, mine);
+          ok = named_bar_and(kEpiBar, kEpiThreads<kPrefill>, mine);
           if (!ok) break;
           tc_fence_after();
           float sum = 0.f;
 #pragma unroll 1
-          for (int c = 0; c < a.m.H; c += 32)
-            sum += sum_weights(tmem + lane_addr + 256 * buf + c, &sh.neg_lse[place][c], scale_log2, 0, a.m.H - c);
+          for (int c = 0; c < a.m.H; c += 32) {
+            float v[32];
+            tmem_ld32(tmem + lane_addr + 256 * buf + c, v);
+            tmem_ld_wait();
+            loaded(v);
+            if (two) add_second(tmem + lane_addr + 256 * buf + kSecond<kPrefill> + c, v);
+            sum += sum_weights(v, &sh.neg_lse[place][c], scale_log2, 0, a.m.H - c);
+          }
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_smem_released(d_empty + 8 * buf);
@@ -639,56 +565,212 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         place ^= 1;
       } else {
-        const int t = row_of(sg.outer), H = a.m.H, tpt = 2 * a.tpc;
-        float* const to = row_mass(t);
+        const int t = row_of(sg.outer), H = a.m.H, half = et >> 7;
+        float* const to = half == 0 ? row_mass(t) : nullptr;
         const float old = to != nullptr && sg.whole && a.m.decay != 0.f ? *to : 0.f;
-        // this thread's columns of a tile: token e / H of each CTA's, head e % H
+        // the columns of this thread's half: head c % H of token c / H of its CTA's; its own of them is column e
         const int tok = e / H, head = e - tok * H;
-        float l[2];
+        float l;
         auto ask = [&](int i) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int q = (2 * i + h) * a.tpc + tok;
-            l[h] = tok < a.tpc && q < sg.s.nq ? neg_lse(sg.s.q0 + q, head) : 0.f;
-          }
+          const int q = (2 * i + half) * a.tpc + tok;
+          l = tok < a.tpc && q < sg.s.nq ? a.m.lse[(int64_t)(sg.s.q0 + q) * H + head] : 0.f;
         };
         ask(sg.i0);
         float sum = 0.f;
         for (int i = sg.i0; i < sg.i1; ++i, ++x, place ^= 1) {
-          const int buf = x & 1;
-          sh.neg_lse[place][e] = l[0];
-          sh.neg_lse[place][128 + e] = l[1];
-          if (i + 1 < sg.i1) ask(i + 1);
-          mine = mine && wait_for(&sh.d_full[buf], (x >> 1) & 1, abort);
-          ok = named_bar_and(kEpiBar, kEpiThreads, mine);
+          sh.neg_lse[place][et] = neg_lse(l);
+          if (i + 1 < sg.i1) ask(i + 1);   // used a tile later
+          mine = mine && wait_for(&sh.d_full[0], x & 1, abort);
+          ok = named_bar_and(kEpiBar, kEpiThreads<kPrefill>, mine);
           if (!ok) break;
           tc_fence_after();
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            // of this half's columns, tokens [seen, there) count: those at or behind the row's position
-            const int q0 = i * tpt + h * a.tpc;
-            const int there = min(max(sg.s.nq - q0, 0), a.tpc) * H, seen = min(max(t - d - q0, 0), a.tpc) * H;
-            const int last = __reduce_max_sync(0xffffffffu, there), first = __reduce_min_sync(0xffffffffu, seen) & ~31;
-#pragma unroll 1
-            for (int c = first; c < last; c += 32)
-              sum += sum_weights(tmem + lane_addr + 256 * buf + 128 * h + c, &sh.neg_lse[place][128 * h + c], scale_log2,
-                                 seen - c, there - c);
-          }
+          // of the half's columns, tokens [seen, there) count: those at or behind the row's position
+          const int q0 = (2 * i + half) * a.tpc;
+          const int there = min(max(sg.s.nq - q0, 0), a.tpc) * H, seen = min(max(t - d - q0, 0), a.tpc) * H;
+          const int last = __reduce_max_sync(0xffffffffu, there), first = __reduce_min_sync(0xffffffffu, seen);
+          auto counts = [&](int c) { return 32 * c < last && 32 * c + 32 > first; };   // some of columns 32 c .. may
+          float v[4][32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (counts(c)) tmem_ld32(tmem + lane_addr + 128 * half + 32 * c, v[c]);
+          tmem_ld_wait();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) loaded(v[c]);
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_smem_released(d_empty + 8 * buf);
+          if (lane == 0) mbar_arrive_smem_released(d_empty);
+          if (two) {
+            mine = mine && wait_for(&sh.d_full[1], x & 1, abort);
+            __syncwarp();
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if (counts(c)) add_second(tmem + lane_addr + kSecond<kPrefill> + 128 * half + 32 * c, v[c]);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_smem_released(d_empty + 8);
+          }
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (counts(c))
+              sum += sum_weights(v[c], &sh.neg_lse[place][128 * half + 32 * c], scale_log2, seen - 32 * c, there - 32 * c);
         }
         if (!ok) break;
+        // the row's two sums, by way of the place that the next tile's -lse take: its thread there is the one that
+        // reads the sum
+        if (half == 1) sh.neg_lse[place][e] = sum;
+        ok = named_bar_and(kEpiBar, kEpiThreads<kPrefill>, mine);
+        if (!ok) break;
+        if (half == 1) continue;
+        sum += sh.neg_lse[place][e];
         if (sg.whole) {
           if (to != nullptr) *to = new_mass(old, sum, a.m.decay);
         } else {
           a.part[((int64_t)unit * 2 + (sg.begins ? 1 : 0)) * kRows + kCtaRows * rank + e] = sum;
-          pieces[sg.begins ? 1 : 0] = make_int4(sg.b, sg.outer, sg.ends, sg.s.kv);
+          (sg.begins ? beginning : ending) = make_int4(sg.b, sg.outer, sg.ends, sg.s.kv);
         }
       }
     }
-    if (kPrefill && rank == 0 && e < 2) a.piece[2 * unit + e] = pieces[e];
+    if (kPrefill && rank == 0 && et == 0) {
+      a.piece[2 * unit] = ending;
+      a.piece[2 * unit + 1] = beginning;
+    }
     if (!ok || !mine) give_up();
+  } else {
+    if constexpr (kPrefill) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRoleRegs));
+    if (warp == 0 || warp == 3) {
+      // ------------------------------------------------------------ loads, in both CTAs: warp 0 the ring,
+      // warp 3 the resident operand; keys are looked up by lanes, one a box
+      const bool ring_role = warp == 0;
+      const int rows_box = min(a.m.page, 64), boxes = kCtaRows / rows_box;
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, int parity) { ok = ok && __all_sync(0xffffffffu, wait_for(bar, parity, abort)); };
+      // this lane's box of the CTA's rows of tile k: its block (outside the cache: none, loads zeros) and row
+      auto look_up = [&](const Seg& s, int k, int& id, int& row) {
+        const int t = kRows * k + kCtaRows * (int)rank + lane * rows_box;
+        id = a.m.num_blocks;
+        row = 0;
+        if (lane < boxes && t < s.s.kv) {
+          const int page = t / a.m.page, got = a.m.block_table[s.b * a.m.bt_stride + page];
+          if (got >= 0 && got < a.m.num_blocks) {
+            id = got;
+            row = t - page * a.m.page;
+          }
+        }
+      };
+      auto load_keys = [&](unsigned char* dst, uint64_t* bar, int c, int id, int row) {
+        const uint32_t to = map_to_rank(bar, 0);
+  #pragma unroll 1
+        for (int i = 0; i < boxes; ++i)
+          load_pair_3d(dst + i * rows_box * 128, &kmap, to, 64 * c, __shfl_sync(0xffffffffu, row, i),
+                       __shfl_sync(0xffffffffu, id, i));
+        if (rank == 0) expect_bytes(bar, 2 * kChunkBytes);
+      };
+      auto load_queries = [&](unsigned char* dst, uint64_t* bar, int c, int h0, int tok) {
+        load_pair_3d(dst, &qmap, map_to_rank(bar, 0), 64 * c, h0, tok);
+        const int rows = kPrefill ? a.m.H * a.tpc : a.half;
+        if (rank == 0) expect_bytes(bar, 2u * rows * 128);
+      };
+      if (ring_role) {
+        int stage = 0, round = 0;
+        auto take = [&](auto&& load) {   // every chunk of a tile through the ring
+  #pragma unroll 1
+          for (int c = 0; ok && c < a.chunks; ++c) {
+            if (round > 0) wait(&sh.ring_empty[stage], (round & 1) ^ 1);
+            if (!ok) break;
+            load(ring + stage * kChunkBytes, &sh.ring_full[stage], c);
+            if (++stage == a.stages) {
+              stage = 0;
+              ++round;
+            }
+          }
+        };
+        while (ok && wk.next(a, sg)) {
+          if (kPrefill) {
+            for (int i = sg.i0; ok && i < sg.i1; ++i) {
+              const int tok = sg.s.q0 + (2 * i + (int)rank) * a.tpc;
+              take([&](unsigned char* dst, uint64_t* bar, int c) { load_queries(dst, bar, c, 0, tok); });
+            }
+          } else {
+            int id, row;
+            look_up(sg, sg.i0, id, row);
+            for (int i = sg.i0; ok && i < sg.i1; ++i) {
+              int id1 = 0, row1 = 0;   // the next tile's: asked for under this one's loads
+              if (i + 1 < sg.i1) look_up(sg, i + 1, id1, row1);
+              take([&](unsigned char* dst, uint64_t* bar, int c) { load_keys(dst, bar, c, id, row); });
+              id = id1;
+              row = row1;
+            }
+          }
+        }
+      } else {
+        for (int g = 0; ok && wk.next(a, sg); ++g) {
+          int id = 0, row = 0;
+          if (kPrefill) look_up(sg, sg.outer, id, row);
+  #pragma unroll 1
+          for (int c = 0; ok && c < a.chunks; ++c) {
+            if (g > 0) wait(&sh.res_empty[c], (g & 1) ^ 1);
+            if (!ok) break;
+            if (kPrefill)
+              load_keys(smem + c * res_bytes, &sh.res_full[c], c, id, row);
+            else
+              load_queries(smem + c * res_bytes, &sh.res_full[c], c, (int)rank * a.half, sg.s.q0);
+          }
+        }
+      }
+      if (!ok) {
+        // copies in flight land within microseconds: wait well beyond that before the CTA ends
+        if (lane == 0) {
+          give_up();
+          const uint64_t t0 = globaltimer_ns();
+          while (globaltimer_ns() - t0 < 2000000ull) {
+          }
+        }
+        __syncwarp();
+      }
+    } else if (warp == 1 && rank == 0) {
+      // ------------------------------------------------------------ MMA issuer of the pair
+      const uint32_t idesc = __reduce_max_sync(0xffffffffu, idesc_bf16(kRows, 0, false, false) | (uint32_t)(a.n >> 3) << 17);
+      const uint32_t res_lo = desc_lo(smem), ring_lo = desc_lo(ring);
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, int parity) {
+        ok = ok && __all_sync(0xffffffffu, wait_for(bar, parity, abort));
+        return ok;
+      };
+      int stage = 0, round = 0, x = 0;
+      for (int g = 0; ok && wk.next(a, sg); ++g) {
+        const int i0 = __reduce_max_sync(0xffffffffu, sg.i0), i1 = __reduce_max_sync(0xffffffffu, sg.i1);
+        for (int i = i0; ok && i < i1; ++i, ++x) {
+          // decode: both accumulators of a tile, in turn in two places; prefill: one behind the other
+          const int buf = kPrefill ? 0 : x & 1;
+          if (kPrefill ? x > 0 && !wait(&sh.d_empty[0], (x & 1) ^ 1) : x > 1 && !wait(&sh.d_empty[buf], ((x >> 1) & 1) ^ 1)) break;
+  #pragma unroll 1
+          for (int c = 0; c < a.chunks; ++c) {
+            if (kPrefill && c == a.split) {
+              commit_pair(&sh.d_full[0]);
+              if (x > 0 && !wait(&sh.d_empty[1], (x & 1) ^ 1)) break;
+            }
+            if (i == i0 && !wait(&sh.res_full[c], g & 1)) break;
+            if (!wait(&sh.ring_full[stage], round & 1)) break;
+            tc_fence_after();
+            const uint32_t d = __reduce_max_sync(0xffffffffu, 256u * buf + (c < a.split ? 0u : kSecond<kPrefill>));
+            const uint32_t r = __reduce_max_sync(0xffffffffu, res_lo + c * (res_bytes >> 4));
+            const uint32_t s = __reduce_max_sync(0xffffffffu, ring_lo + stage * (kChunkBytes >> 4));
+            umma_pair4(d, kPrefill ? r : s, kPrefill ? s : r, idesc, c == 0 || c == a.split);
+            commit_pair(&sh.ring_empty[stage]);
+            if (i + 1 == i1) commit_pair(&sh.res_empty[c]);
+            if (++stage == a.stages) {
+              stage = 0;
+              ++round;
+            }
+          }
+          if (ok) commit_pair(&sh.d_full[kPrefill ? (a.chunks > 1 ? 1 : 0) : buf]);
+        }
+      }
+      if (!ok && lane == 0) give_up();
+      __syncwarp();
+      commit_pair(&sh.fin);
+    }
   }
   // ---------------------------------------------------------------- teardown
   tc_fence_before();
@@ -708,11 +790,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 // Block u - 1 looks at the rows that end in, or go on through, unit u's first tiles. If they begin in the unit
 // before (units without tiles aside), it adds up their pieces in order.
-__global__ void __launch_bounds__(kThreads) mass_merge_kernel(const TcArgs a, int units) {
+__global__ void __launch_bounds__(kRows) mass_merge_kernel(const TcArgs a, int units) {
   pdl_enter();
   __shared__ int4 piece[kMaxUnits][2];
   const int u = blockIdx.x + 1, e = threadIdx.x;
-  for (int i = e; i < 2 * units; i += kThreads) piece[i >> 1][i & 1] = a.piece[i];
+  for (int i = e; i < 2 * units; i += kRows) piece[i >> 1][i & 1] = a.piece[i];
   __syncthreads();
   const int4 p = piece[u][0];
   if (p.x < 0) return;
@@ -749,7 +831,7 @@ int max_pairs() {
     cudaFuncSetAttribute(mass_tc_kernel<kPrefill>, cudaFuncAttributeMaxDynamicSharedMemorySize, kArena + kMiscBytes);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * device_sm_count(), 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.blockDim = dim3(kThreads<kPrefill>, 1, 1);
     cfg.dynamicSmemBytes = kArena + kMiscBytes;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -771,7 +853,18 @@ cudaError_t launch(const TcArgs& a, const MassMaps& maps, int units, cudaStream_
   const cudaError_t e = cudaFuncSetAttribute(mass_tc_kernel<kPrefill>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              kArena + kMiscBytes);
   if (e != cudaSuccess) return e;
-  return launch_k(mass_tc_kernel<kPrefill>, dim3(2 * units), dim3(kThreads), kArena + kMiscBytes, st, maps.keys, maps.q, a);
+  if (kPrefill) {
+    // the shares of setmaxnreg draw on what the kernel was compiled for: with less they would wait for ever
+    static std::atomic<int> regs{0};
+    if (regs.load() == 0) {
+      cudaFuncAttributes attr;
+      const cudaError_t f = cudaFuncGetAttributes(&attr, mass_tc_kernel<kPrefill>);
+      if (f != cudaSuccess) return f;
+      regs.store(attr.numRegs);
+    }
+    if (regs.load() != kLaunchRegs) return cudaErrorInvalidKernelImage;
+  }
+  return launch_k(mass_tc_kernel<kPrefill>, dim3(2 * units), dim3(kThreads<kPrefill>), kArena + kMiscBytes, st, maps.keys, maps.q, a);
 }
 
 int tokens_per_cta(int H) { return std::max(1, kCtaRows / H); }
@@ -802,6 +895,7 @@ cudaError_t launch_mass_tc(const MassCall& c, const MassMaps& maps, void* ws, cu
   TcArgs a{};
   a.m = mass_args(c);
   a.chunks = c.cache.entry / 64;
+  a.split = (a.chunks + 1) / 2;
   a.tpc = tokens_per_cta(c.H);
   a.n = decode ? decode_rows(c.H) : kRows;
   a.half = a.n / 2;
@@ -812,7 +906,7 @@ cudaError_t launch_mass_tc(const MassCall& c, const MassMaps& maps, void* ws, cu
   a.piece = reinterpret_cast<int4*>(a.part + (int64_t)units * 2 * kRows);
   const cudaError_t e = launch<true>(a, maps, units, st);
   if (e != cudaSuccess || units < 2) return e;
-  return launch_k(mass_merge_kernel, dim3(units - 1), dim3(kThreads), 0, st, a, units);
+  return launch_k(mass_merge_kernel, dim3(units - 1), dim3(kRows), 0, st, a, units);
 }
 
 cudaError_t mass_tc_error_word(unsigned** word) {
