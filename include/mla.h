@@ -15,7 +15,10 @@
  * (steps 1 to 3 in one call, the copies alongside the absorb) and mla_decode_v_up (step 4
  * with step 5 in its combine). mla_decode_window and mla_prefill_window are step 4 limited to
  * a sliding window and attention sinks; mla_cache_write_ds_mla is step 3 into quantised
- * entries, and mla_cache_read, _fp8 and _ds_mla read cache rows back.
+ * entries, and mla_cache_read, _fp8 and _ds_mla read cache rows back. mla_norm_rope_q and the
+ * mla_norm_rope_cache_write calls make the queries and rows of steps 1 to 3 from a layer's
+ * projections; mla_decode_mass and mla_prefill_mass weigh the cached rows by the attention they
+ * receive, and mla_cache_evict keeps the heaviest.
  *
  * Sources of the operations (web pages):
  *   [vt]    vllm.cpp, tests/vt/test_ops_mla_absorb.cpp (BatchedMatmul and

@@ -7,7 +7,7 @@
 // those bits in shared memory (sums, whatever their order), then the digit where the wanted count is reached;
 // fewer passes where it is reached exactly. A block (256 to 1024 threads, by the rows that the table and the masses
 // have room for) holds sixteen keys a thread in registers, and reads longer sequences again. Two bits a round
-// by counting keys above three limits took 20.8 us for 64 sequences of 1K to 8K rows instead of SELECT_US.
+// by counting keys above three limits took 20.8 us for 64 sequences of 1K to 8K rows instead of 14.
 // Of the rows with the smallest key that stays the lowest stay.
 //
 // Moving. Row kept[j] becomes row j <= kept[j], in place: what a step writes, rows j .. , no later step
@@ -16,7 +16,7 @@
 // earlier ones. Columns do not touch one another: a sequence is cut into slices of columns, a block each, and
 // every block takes all rows of its slice. Rows pass through shared memory (asynchronous copies, three
 // steps in flight, each thread its own words): held in registers, one step at a time, 64 sequences of 1K to 8K
-// rows took 58 us to move instead of MOVE_US.
+// rows took 58 us to move instead of 38 (5.7 TB/s).
 #include <algorithm>
 #include <climits>
 

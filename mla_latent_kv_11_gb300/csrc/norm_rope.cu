@@ -9,10 +9,15 @@
 // Both parts are bound by HBM: every value crosses it once. A row stays in registers between its sum
 // and its stores, in 16-byte words: a query head in 8, 16 or 32 lanes of up to four words each (24
 // words of a 192-wide bf16 head are three a lane of eight, so that no lane idles), a cache row in one
-// warp. A block takes heads of one token, several a warp one behind the other, so that the token's angles, the
+// warp. A block takes heads of one token, several a warp one behind the other, so that the token's angles and the
 // addresses are worked out once (a head a warp alone issued three times the instructions: 4096 tokens of 128
 // heads 113 us). No lane has more than one word of the rope; its partner half a rope away comes from its lane. Both
 // parts share one launch: a decode step has 5 to 500 blocks of work in all.
+//
+// What it measured (device times): 4096 tokens of 128 normed heads of 192 and their rows, bf16: 73 us for 413 MB,
+// 5.6 TB/s, 0.83 of a copy's rate (halves rotated 81 us: a word's partner through eight exchanges); queries without a norm
+// 38 us for 145 MB: a rope's 128 bytes a head are read and written in separate lines. 20011 float32 rows into ds_mla entries
+// 15 us, 4.4 TB/s; 40000 bf16 rows plain 22 us, e4m3 30. A step of 64 tokens 3.6 us, of one 2.1.
 #include <algorithm>
 
 #include "e4m3_codes.cuh"
