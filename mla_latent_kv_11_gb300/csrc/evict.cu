@@ -14,7 +14,7 @@
 // reads (their sources lie at or behind their targets), so a block that takes rows in ascending order,
 // all loads of a step before its stores, needs no second copy, and may load later steps before it stores
 // earlier ones. Columns do not touch one another: a sequence is cut into slices of columns, a block each, and
-// every block takes all rows of its slice. Rows pass through shared memory (asynchronous copies, three
+// every block takes all rows of its slice. Rows pass through shared memory (asynchronous copies, two
 // steps in flight, each thread its own words): held in registers, one step at a time, 64 sequences of 1K to 8K
 // rows took 58 us to move instead of 38 (5.7 TB/s).
 #include <algorithm>

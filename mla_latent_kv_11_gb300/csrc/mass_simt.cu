@@ -11,6 +11,8 @@
 
 #include <cuda_bf16.h>
 
+#include <algorithm>
+
 #include "mass.cuh"
 
 namespace mla {
@@ -35,102 +37,106 @@ __global__ void __launch_bounds__(kMassThreads) mass_simt_kernel(const MassArgs 
   __shared__ int q_pos[kTile];
   const int b = blockIdx.y, tid = threadIdx.x;
   const MassSeq s = mass_seq(a, b, &g_mass_simt_err);
-  const int t0 = blockIdx.x * kTile;
-  if (s.nq == 0 || t0 >= s.kv) return;
-  if (tid < kTile) {
-    const int t = t0 + tid;
-    row_at[tid] = -1;
-    if (t < s.kv) {
-      const int pb = t / a.page, blk = a.block_table[b * a.bt_stride + pb];
-      if (blk >= 0 && blk < a.num_blocks)
-        row_at[tid] = blk * c_blk + (t - pb * a.page) * c_row;
-      else
-        atomicOr(&g_mass_simt_err, kErrDeviceData);
-    }
-  }
+  if (s.nq == 0) return;
   const int d = s.kv - s.nq;                          // position of the first query
   const int tx = tid & 15, ty = tid >> 4;             // queries kMine tx .., rows kMine ty ..
   const int le = tid % kStep, lr = tid / kStep;       // this thread's column and first row of a step's loads
   constexpr int kLoadRows = kMassThreads / kStep;
-  float acc[kMine] = {};
   // 64-bit: tokens times heads may pass 32 bits
   const int64_t end = (int64_t)s.nq * a.H;
-  for (int64_t r0 = (int64_t)max(0, t0 - d) * a.H; r0 < end; r0 += kTile) {
-    __syncthreads();
+  for (int t0 = blockIdx.x * kTile; t0 < s.kv; t0 += gridDim.x * kTile) {
+    __syncthreads();   // the tile before is done with row_at
     if (tid < kTile) {
-      const int64_t r = r0 + tid;
-      q_at[tid] = -1;
-      q_lse[tid] = CUDART_INF_F;
-      q_pos[tid] = -1;                                // attends nothing
-      if (r < end) {
-        const int i = (int)(r / a.H), h = (int)(r - (int64_t)i * a.H);
-        q_at[tid] = (int64_t)(s.q0 + i) * q_s0 + h * q_s1;
-        const float l = a.lse[(int64_t)(s.q0 + i) * a.H + h];
-        q_lse[tid] = l;
-        if (l != -CUDART_INF_F) q_pos[tid] = d + i;   // a query that attended nothing gives nothing
+      const int t = t0 + tid;
+      row_at[tid] = -1;
+      if (t < s.kv) {
+        const int pb = t / a.page, blk = a.block_table[b * a.bt_stride + pb];
+        if (blk >= 0 && blk < a.num_blocks)
+          row_at[tid] = blk * c_blk + (t - pb * a.page) * c_row;
+        else
+          atomicOr(&g_mass_simt_err, kErrDeviceData);
       }
     }
-    __syncthreads();
-    float c[kMine][kMine] = {}, nk[kLoads], nq[kLoads];
-    auto ask = [&](int e) {
-#pragma unroll
-      for (int k = 0; k < kLoads; ++k) {
-        const int r = lr + k * kLoadRows;
-        nk[k] = e < a.E && row_at[r] >= 0 ? value(cache[row_at[r] + e]) : 0.f;
-        nq[k] = e < a.E && q_at[r] >= 0 ? value(q[q_at[r] + e]) : 0.f;
-      }
-    };
-    ask(le);
-    for (int e0 = 0; e0 < a.E; e0 += kStep) {
-#pragma unroll
-      for (int k = 0; k < kLoads; ++k) {
-        sk[le][lr + k * kLoadRows] = nk[k];
-        sq[le][lr + k * kLoadRows] = nq[k];
+    float acc[kMine] = {};
+    for (int64_t r0 = (int64_t)max(0, t0 - d) * a.H; r0 < end; r0 += kTile) {
+      __syncthreads();
+      if (tid < kTile) {
+        const int64_t r = r0 + tid;
+        q_at[tid] = -1;
+        q_lse[tid] = CUDART_INF_F;
+        q_pos[tid] = -1;                                // attends nothing
+        if (r < end) {
+          const int i = (int)(r / a.H), h = (int)(r - (int64_t)i * a.H);
+          q_at[tid] = (int64_t)(s.q0 + i) * q_s0 + h * q_s1;
+          const float l = a.lse[(int64_t)(s.q0 + i) * a.H + h];
+          q_lse[tid] = l;
+          if (l != -CUDART_INF_F) q_pos[tid] = d + i;   // a query that attended nothing gives nothing
+        }
       }
       __syncthreads();
-      if (e0 + kStep < a.E) ask(e0 + kStep + le);
-#pragma unroll 8
-      for (int e = 0; e < kStep; ++e) {
-        float xs[kMine], ys[kMine];
-        if constexpr (kMine == 4) {
-          const float4 x = *reinterpret_cast<const float4*>(&sk[e][4 * ty]), y = *reinterpret_cast<const float4*>(&sq[e][4 * tx]);
-          xs[0] = x.x; xs[1] = x.y; xs[2] = x.z; xs[3] = x.w;
-          ys[0] = y.x; ys[1] = y.y; ys[2] = y.z; ys[3] = y.w;
-        } else {
-          xs[0] = sk[e][ty];
-          ys[0] = sq[e][tx];
+      float c[kMine][kMine] = {}, nk[kLoads], nq[kLoads];
+      auto ask = [&](int e) {
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k) {
+          const int r = lr + k * kLoadRows;
+          nk[k] = e < a.E && row_at[r] >= 0 ? value(cache[row_at[r] + e]) : 0.f;
+          nq[k] = e < a.E && q_at[r] >= 0 ? value(q[q_at[r] + e]) : 0.f;
         }
+      };
+      ask(le);
+      for (int e0 = 0; e0 < a.E; e0 += kStep) {
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k) {
+          sk[le][lr + k * kLoadRows] = nk[k];
+          sq[le][lr + k * kLoadRows] = nq[k];
+        }
+        __syncthreads();
+        if (e0 + kStep < a.E) ask(e0 + kStep + le);
+#pragma unroll 8
+        for (int e = 0; e < kStep; ++e) {
+          float xs[kMine], ys[kMine];
+          if constexpr (kMine == 4) {
+            const float4 x = *reinterpret_cast<const float4*>(&sk[e][4 * ty]), y = *reinterpret_cast<const float4*>(&sq[e][4 * tx]);
+            xs[0] = x.x; xs[1] = x.y; xs[2] = x.z; xs[3] = x.w;
+            ys[0] = y.x; ys[1] = y.y; ys[2] = y.z; ys[3] = y.w;
+          } else {
+            xs[0] = sk[e][ty];
+            ys[0] = sq[e][tx];
+          }
+#pragma unroll
+          for (int i = 0; i < kMine; ++i)
+#pragma unroll
+            for (int j = 0; j < kMine; ++j) c[i][j] = fmaf(xs[i], ys[j], c[i][j]);
+        }
+        __syncthreads();
+      }
+#pragma unroll
+      for (int j = 0; j < kMine; ++j) {
+        const float l = q_lse[kMine * tx + j];
+        const int p = q_pos[kMine * tx + j];
 #pragma unroll
         for (int i = 0; i < kMine; ++i)
-#pragma unroll
-          for (int j = 0; j < kMine; ++j) c[i][j] = fmaf(xs[i], ys[j], c[i][j]);
+          if (t0 + kMine * ty + i <= p) acc[i] += expf(fmaf(c[i][j], a.scale, -l));
       }
-      __syncthreads();
     }
 #pragma unroll
-    for (int j = 0; j < kMine; ++j) {
-      const float l = q_lse[kMine * tx + j];
-      const int p = q_pos[kMine * tx + j];
+    for (int i = 0; i < kMine; ++i) {
 #pragma unroll
-      for (int i = 0; i < kMine; ++i)
-        if (t0 + kMine * ty + i <= p) acc[i] += expf(fmaf(c[i][j], a.scale, -l));
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < kMine; ++i) {
-#pragma unroll
-    for (int m = 1; m < 16; m <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], m);
-    const int t = t0 + kMine * ty + i;
-    if (tx == 0 && t < s.kv && row_at[kMine * ty + i] >= 0) {
-      float* const m = a.mass + b * a.mass_stride + t;
-      *m = new_mass(a.decay == 0.f ? 0.f : *m, acc[i], a.decay);
+      for (int m = 1; m < 16; m <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], m);
+      const int t = t0 + kMine * ty + i;
+      if (tx == 0 && t < s.kv && row_at[kMine * ty + i] >= 0) {
+        float* const m = a.mass + b * a.mass_stride + t;
+        *m = new_mass(a.decay == 0.f ? 0.f : *m, acc[i], a.decay);
+      }
     }
   }
 }
 
 template <typename T, int kTile>
 cudaError_t launch(const MassCall& c, const MassArgs& a, cudaStream_t st) {
-  const dim3 grid((unsigned)((a.cap + kTile - 1) / kTile), (unsigned)c.B);
+  // tables are often far longer than their sequences: no more blocks a sequence than fill the SMs a few times
+  const int most = std::max(1, 16 * device_sm_count() / c.B);
+  const dim3 grid((unsigned)std::min((a.cap + kTile - 1) / kTile, most), (unsigned)c.B);
   return launch_k(mass_simt_kernel<T, kTile>, grid, kMassThreads, 0, st, a, (const T*)c.q.data, c.q.s0, c.q.s1,
                   (const T*)c.cache.data, c.cache.s_blk, c.cache.s_row);
 }
