@@ -15,9 +15,9 @@
 // parts share one launch: a decode step has 5 to 500 blocks of work in all.
 //
 // What it measured (device times): 4096 tokens of 128 normed heads of 192 and their rows, bf16: 73 us for 413 MB,
-// 5.6 TB/s, 0.83 of a copy's rate (halves rotated 81 us: a word's partner through eight exchanges); queries without a norm
+// 5.6 TB/s, 0.83 of a copy's rate (halves rotated 79 us: a word's partner through eight exchanges); queries without a norm
 // 38 us for 145 MB: a rope's 128 bytes a head are read and written in separate lines. 20011 float32 rows into ds_mla entries
-// 15 us, 4.4 TB/s; 40000 bf16 rows plain 22 us, e4m3 30. A step of 64 tokens 3.6 us, of one 2.1.
+// 15 us, 4.4 TB/s; 40000 bf16 rows plain 22 us, e4m3 28. A step of 64 tokens 3.5 us, of one 2.1.
 #include <algorithm>
 
 #include "e4m3_codes.cuh"
@@ -202,13 +202,16 @@ __device__ __forceinline__ int64_t row_offset(const RowPart& p, int64_t s, int l
   return blk * p.c_blk + (s - blk * p.page_of.page) * p.c_row;
 }
 
-// 1 / sqrt(sum / n + eps), one Newton step behind the two roundings of a root and a division: it enters every
-// value of the row, and a quantised value next to the middle of two codes tells its last bit.
-__device__ __forceinline__ float norm_factor(float sum, int n, float eps) {
-  const float v = sum / (float)n + eps, y = 1.f / sqrtf(v);
+// 1 / sqrt(sum / n + eps), inv = 1 / n: a quotient and a root each mended by a step with its remainder (a division,
+// a root and another division took a head a fifth of its instructions). It enters every value of the row, and a
+// quantised value next to the middle of two codes tells its last bit.
+__device__ __forceinline__ float norm_factor(float sum, float n, float inv, float eps) {
+  float v = sum * inv;
+  v = fmaf(fmaf(-v, n, sum), inv, v) + eps;
+  const float y = rsqrtf(v);
   const float p = v * y, low = fmaf(v, y, -p);               // v y = p + low
   const float t = fmaf(-low, y, fmaf(-p, y, 1.f));           // 1 - v y^2
-  return t == t && y <= FLT_MAX ? fmaf(0.5f * y, t, y) : y;  // (v infinite or zero: as it is)
+  return t == t && y <= FLT_MAX ? fmaf(0.5f * y, t, y) : y;  // (v infinite, zero or NaN: as it is)
 }
 
 // Heads of queries, in words: kG lanes a head, kW words a lane, kPass heads a pass of the block. A block
@@ -243,6 +246,7 @@ __device__ __forceinline__ void query_rows(const QueryPart& p, const Angles& ang
   T* nope = static_cast<T*>(p.nope) + t * p.n_s0 + h * p.n_s1 + p.first + l * V::kN;
   T* pe = static_cast<T*>(p.pe) + t * p.p_s0 + h * p.p_s1 + rope;
   const bool norm = p.weight != nullptr;
+  const float inv = 1.f / (float)p.W;
   const T* wgt = static_cast<const T*>(p.weight) + h * p.w_s0 + p.first + l * V::kN;
   const int left = p.W - p.first - l * V::kN;      // columns from this lane's first on
   uint4 own[kW];
@@ -267,7 +271,7 @@ __device__ __forceinline__ void query_rows(const QueryPart& p, const Angles& ang
       for (int j = 0; j < kW; ++j) sum += V::squares(own[j]);
 #pragma unroll
       for (int m = 1; m < kG; m <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-      by = norm_factor(sum, p.W, eps);
+      by = norm_factor(sum, (float)p.W, inv, eps);
     }
     __syncwarp();   // the outputs may be q's own columns: every load of a head comes before any store
     float r[V::kN] = {}, y[V::kN] = {};
@@ -357,6 +361,7 @@ __device__ __forceinline__ void cache_rows(const RowPart& p, const Angles& ang, 
   Row row;
   ask(first, row);
   const Quotients quotients(kFmt == kE4m3 ? *p.scale : 1.f);
+  const float inv = 1.f / (float)p.L;
   for (int64_t t = first; t < p.tokens; t += step) {
     Row next;
     if (kLoop) ask(t + step, next);
@@ -373,7 +378,7 @@ __device__ __forceinline__ void cache_rows(const RowPart& p, const Angles& ang, 
       }
 #pragma unroll
       for (int m = 1; m < 32; m <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-      const float by = norm_factor(sum, p.L, eps);
+      const float by = norm_factor(sum, (float)p.L, inv, eps);
       auto put = [&](int c, const float (&x)[V::kN]) {
         if constexpr (kFmt == kPlain) {
           *reinterpret_cast<uint4*>(static_cast<T*>(p.cache) + off + c) = V::close(x);
@@ -484,7 +489,7 @@ __device__ __forceinline__ void ds_mla_rows(const RowPart& p, const Angles& ang,
       float sum = __uint_as_float((uint32_t)sum2) + __uint_as_float((uint32_t)(sum2 >> 32));
 #pragma unroll
       for (int m = 1; m < 32; m <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-      const float by = norm_factor(sum, kDsMlaLatent, eps);
+      const float by = norm_factor(sum, kDsMlaLatent, 1.f / kDsMlaLatent, eps);
 #pragma unroll
       for (int k = 0; k < 16; ++k) x[k] = x[k] * by * w[k];
       uint32_t codes[4];
@@ -572,7 +577,7 @@ __global__ void __launch_bounds__(256) norm_rope_any_kernel(const QueryPart q, c
     if (ang.R != 0 && cs == nullptr) return;
     const T* src = static_cast<const T*>(q.q) + t * q.q_s0 + h * q.q_s1;
     const T* wgt = q.weight == nullptr ? nullptr : static_cast<const T*>(q.weight) + h * q.w_s0;
-    const float by = wgt != nullptr ? norm_factor(row_sum(src, q.W, lane), q.W, eps) : 1.f;
+    const float by = wgt != nullptr ? norm_factor(row_sum(src, q.W, lane), (float)q.W, 1.f / (float)q.W, eps) : 1.f;
     T* nope = static_cast<T*>(q.nope) + t * q.n_s0 + h * q.n_s1;
     T* pe = static_cast<T*>(q.pe) + t * q.p_s0 + h * q.p_s1;
     __syncwarp();   // sums are done with columns that the stores may overwrite
@@ -591,7 +596,7 @@ __global__ void __launch_bounds__(256) norm_rope_any_kernel(const QueryPart q, c
   const float* cs = ang.of(t);
   if (ang.R != 0 && cs == nullptr) return;
   const T* src = static_cast<const T*>(r.kv) + t * r.k_s0;
-  const float by = norm_factor(row_sum(src, r.L, lane), r.L, eps);
+  const float by = norm_factor(row_sum(src, r.L, lane), (float)r.L, 1.f / (float)r.L, eps);
   const float scale = kFmt == kE4m3 ? *r.scale : 1.f;
   each_column(src, static_cast<const T*>(r.weight), r.L, 0, r.L, ang, cs, by, lane, [&](int c, float v) {
     if constexpr (kFmt == kPlain)
