@@ -214,3 +214,18 @@ def test_captured_graphs_and_streams(mla):
     torch.cuda.synchronize()
     for c, want, out, lens_out in outs:
         assert lens_out.tolist() == want[2] and torch.equal(out.cpu(), want[1]) and torch.equal(bits(c.whole), bits(want[0]))
+
+
+@pytest.mark.parametrize("lens,budget", [([140001], 70000), ([131073, 0, 1, 5, 9001], 131000), ([20000, 700, 16385, 8192, 2], 600)])
+@pytest.mark.parametrize("masses", ["spread", "few", "odd", "same"])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_several_blocks_a_sequence(mla, lens, budget, masses, in_place):
+    # sequences of all lengths in calls whose tables have room for long ones; the first more than eight blocks hold
+    run(mla, Case(len(lens) + budget, lens, 64, 24, torch.bfloat16, masses, extra=3), budget, 3, 65, in_place)
+
+
+def test_several_blocks_a_slice(mla):
+    # wide rows, one to nine sequences: a slice's rows are dealt over eight blocks down to one
+    for lens in ([5000], [4000, 3000], [2500] * 3 + [17], [1500, 2600] * 4 + [900]):
+        for dtype, width in ((torch.bfloat16, 576), (torch.float32, 576), (torch.uint8, 656)):
+            run(mla, Case(len(lens) + width, lens, 64, width, dtype), 1300, 4, 64)
