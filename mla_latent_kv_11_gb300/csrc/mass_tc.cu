@@ -415,6 +415,15 @@ __device__ __forceinline__ void load_pair_3d(void* dst, const void* map, uint32_
       : "memory");
 }
 
+// The same by every lane that comes here.
+__device__ __forceinline__ void load_pair_3d_lane(void* dst, const void* map, uint32_t bar, int32_t c0, int32_t c1, int32_t c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
 __device__ __forceinline__ uint64_t pair_f32(float a, float b) {
   return (uint64_t)__float_as_uint(b) << 32 | __float_as_uint(a);
 }
@@ -688,11 +697,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kPrefill>, 
         }
       };
       auto load_keys = [&](unsigned char* dst, uint64_t* bar, int c, int id, int row) {
-        const uint32_t to = map_to_rank(bar, 0);
-  #pragma unroll 1
-        for (int i = 0; i < boxes; ++i)
-          load_pair_3d(dst + i * rows_box * 128, &kmap, to, 64 * c, __shfl_sync(0xffffffffu, row, i),
-                       __shfl_sync(0xffffffffu, id, i));
+        // each lane its own box: handed to one lane, boxes of 16 rows took the 64-sequence decode 170 us, not 134
+        if (lane < boxes) load_pair_3d_lane(dst + lane * rows_box * 128, &kmap, map_to_rank(bar, 0), 64 * c, row, id);
+        __syncwarp();
         if (rank == 0) expect_bytes(bar, 2 * kChunkBytes);
       };
       auto load_queries = [&](unsigned char* dst, uint64_t* bar, int c, int h0, int tok) {
