@@ -9,7 +9,7 @@
 // Both parts are bound by HBM: every value crosses it once. A row stays in registers between its sum
 // and its stores, in 16-byte words: a query head in 8, 16 or 32 lanes of up to four words each (24
 // words of a 192-wide bf16 head are three a lane of eight, so that no lane idles), a cache row in one
-// warp. A block takes heads of one token, several a warp one behind the other, so that the token's angles and the
+// warp or half of one. A block takes heads of one token, several a warp one behind the other, so that the token's angles and the
 // addresses are worked out once (a head a warp alone issued three times the instructions: 4096 tokens of 128
 // heads 113 us). No lane has more than one word of the rope; its partner half a rope away comes from its lane. Both
 // parts share one launch: a decode step has 5 to 500 blocks of work in all.
@@ -17,7 +17,7 @@
 // What it measured (device times): 4096 tokens of 128 normed heads of 192 and their rows, bf16: 73 us for 413 MB,
 // 5.6 TB/s, 0.83 of a copy's rate (halves rotated 79 us: a word's partner through eight exchanges); queries without a norm
 // 38 us for 145 MB: a rope's 128 bytes a head are read and written in separate lines. 20011 float32 rows into ds_mla entries
-// 15 us, 4.4 TB/s; 40000 bf16 rows plain 22 us, e4m3 28. A step of 64 tokens 3.5 us, of one 2.1.
+// 15 us, 4.4 TB/s; 40000 bf16 rows plain 24 us, e4m3 29 (pairs side by side 21 and 23). A step of 64 tokens 3.5 us, of one 2.1.
 #include <algorithm>
 
 #include "e4m3_codes.cuh"
@@ -188,6 +188,7 @@ struct RowPart {
   const int64_t* slots;
   int64_t tokens;
   const float* scale;   // kE4m3
+  int32_t eights;       // kE4m3: rows are eight bytes aligned
 };
 
 // Offset of slot s in the cache; -1: padding, or outside the view (recorded).
@@ -217,7 +218,7 @@ __device__ __forceinline__ float norm_factor(float sum, float n, float inv, floa
 // Heads of queries, in words: kG lanes a head, kW words a lane, kPass heads a pass of the block. A block
 // takes `per` heads (whole passes) of one token.
 constexpr int kThreads = 256;
-constexpr int kRowBlocks = 3, kHeadBlocks = 4;   // blocks an SM holds: of rows alone, of heads (and rows)
+constexpr int kRowBlocks = 3, kHalfBlocks = 2, kHeadBlocks = 4;   // blocks an SM holds: of rows alone (of half a warp), of heads (and rows)
 template <int kG>
 constexpr int kPass = kThreads / kG;
 
@@ -318,8 +319,9 @@ struct Quotients {
   }
   __device__ __forceinline__ uint32_t codes(float x0, float x1) const {
     if (plain) return codes2(__fdiv_rn(x0, scale), __fdiv_rn(x1, scale));
-    asm("min.NaN.f32 %0, %0, %2;\n\tmax.NaN.f32 %0, %0, %3;\n\tmin.NaN.f32 %1, %1, %2;\n\tmax.NaN.f32 %1, %1, %3;"
-        : "+f"(x0), "+f"(x1) : "f"(most), "f"(-most));
+    // the smaller magnitude, with x's sign
+    asm("min.NaN.xorsign.abs.f32 %0, %0, %1;" : "+f"(x0) : "f"(most));
+    asm("min.NaN.xorsign.abs.f32 %0, %0, %1;" : "+f"(x1) : "f"(most));
     const uint64_t x = pair(x0, x1);
     uint64_t q, rem;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q) : "l"(x), "l"(r));
@@ -331,19 +333,18 @@ struct Quotients {
   }
 };
 
-// New cache rows, plain or e4m3, in words: a warp a row, up to kW words a lane. kLoop: rows from `first` on, every
+// New cache rows, plain or e4m3, in words: kG lanes a row, up to kW words a lane. kLoop: rows from `first` on, every
 // `step`th, each asked for, with its slot and position, while the one before is worked on; else one row (beside
 // query heads, whose registers the second row would take).
-template <typename T, int kFmt, int kW, bool kInter, bool kLoop>
+template <typename T, int kFmt, int kG, int kW, bool kInter, bool kLoop>
 __device__ __forceinline__ void cache_rows(const RowPart& p, const Angles& ang, float eps, int64_t first, int64_t step) {
   using V = Word<T>;
-  const int lane = threadIdx.x & 31, left = p.E - lane * V::kN, half = ang.R >> 1;
+  const int lane = threadIdx.x & (kG - 1), left = p.E - lane * V::kN, half = ang.R >> 1;
   int rope = -1;
 #pragma unroll
   for (int j = 0; j < kW; ++j)
-    if (32 * j * V::kN < left && (lane + 32 * j) * V::kN >= p.L) rope = (lane + 32 * j) * V::kN - p.L;
-  const int partner = partner_lane<V::kN>(rope, half, lane) & 31;
-  const T* const wgt = static_cast<const T*>(p.weight) + lane * V::kN;
+    if (kG * j * V::kN < left && (lane + kG * j) * V::kN >= p.L) rope = (lane + kG * j) * V::kN - p.L;
+  const int partner = partner_lane<V::kN>(rope, half, lane) & (kG - 1);
   struct Row {
     uint4 own[kW];
     int64_t slot, pos;
@@ -353,32 +354,40 @@ __device__ __forceinline__ void cache_rows(const RowPart& p, const Angles& ang, 
 #pragma unroll
     for (int j = 0; j < kW; ++j) {
       r.own[j] = make_uint4(0u, 0u, 0u, 0u);
-      if (t < p.tokens && 32 * j * V::kN < left) r.own[j] = V::load(src + 32 * j * V::kN);
+      if (t < p.tokens && kG * j * V::kN < left) r.own[j] = V::load(src + kG * j * V::kN);
     }
     r.slot = t < p.tokens ? p.slots[t] : -1;
     r.pos = t < p.tokens && ang.R != 0 ? ang.positions[t] : 0;
   };
   Row row;
   ask(first, row);
+  const T* const wgt = static_cast<const T*>(p.weight) + lane * V::kN;
   const Quotients quotients(kFmt == kE4m3 ? *p.scale : 1.f);
   const float inv = 1.f / (float)p.L;
-  for (int64_t t = first; t < p.tokens; t += step) {
+  for (int64_t t = first; kG == 32 ? t < p.tokens : __any_sync(0xffffffffu, t < p.tokens); t += step) {
     Row next;
     if (kLoop) ask(t + step, next);
     const int64_t off = row_offset(p, row.slot, lane);
     const float* cs = off < 0 ? nullptr : ang.row(row.pos, lane);
+    const bool live = off >= 0 && (ang.R == 0 || cs != nullptr);   // the same for all lanes of a row
     Turn<V::kN, kInter> turn;
-    if (rope >= 0 && cs != nullptr) turn.open(cs, rope, half, ang.words);
-    if (off >= 0 && (ang.R == 0 || cs != nullptr)) {   // the same for the whole warp
-      float sum = 0.f;
+    if (rope >= 0 && live) turn.open(cs, rope, half, ang.words);
+    if (kG < 32 || live) {                           // (of half a warp the other row may be live)
+      const bool mine = kG == 32 || live;
+      // the sums that 32 lanes would have, added in their order: a row's bits do not depend on the call's other rows
+      constexpr int kSums = 32 / kG;
+      float sum[kSums] = {};
 #pragma unroll
       for (int j = 0; j < kW; ++j) {
         const float s = V::squares(row.own[j]);
-        if ((lane + 32 * j) * V::kN < p.L) sum += s;
+        if ((lane + kG * j) * V::kN < p.L) sum[j % kSums] += s;
       }
 #pragma unroll
-      for (int m = 1; m < 32; m <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-      const float by = norm_factor(sum, (float)p.L, inv, eps);
+      for (int m = 1; m < kG; m <<= 1) {
+#pragma unroll
+        for (int i = 0; i < kSums; ++i) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], m);
+      }
+      const float by = norm_factor(kSums == 1 ? sum[0] : sum[0] + sum[kSums - 1], (float)p.L, inv, eps);
       auto put = [&](int c, const float (&x)[V::kN]) {
         if constexpr (kFmt == kPlain) {
           *reinterpret_cast<uint4*>(static_cast<T*>(p.cache) + off + c) = V::close(x);
@@ -387,32 +396,43 @@ __device__ __forceinline__ void cache_rows(const RowPart& p, const Angles& ang, 
 #pragma unroll
           for (int k = 0; k < V::kN; k += 2) w[k >> 2] |= quotients.codes(x[k], x[k + 1]) << (8 * (k & 2));
           uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.cache) + off + c);
+          if constexpr (V::kN == 8) {
+            if (p.eights) {
+              *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[1]);
+              return;
+            }
+          }
 #pragma unroll
           for (int k = 0; k < V::kN / 4; ++k) o[k] = w[k];
         }
       };
-      float r[V::kN] = {}, y[V::kN] = {};
+      uint4 turned = make_uint4(0u, 0u, 0u, 0u);     // the lane's word of the rope, as read
 #pragma unroll
       for (int j = 0; j < kW; ++j) {
-        const int c = (lane + 32 * j) * V::kN;
-        if (c >= p.E) continue;
-        float x[V::kN];
-        V::open(row.own[j], x);
+        const int c = (lane + kG * j) * V::kN;
+        if (c >= p.E || !mine) continue;
         if (c < p.L) {
-          V::scale(x, by, V::load(wgt + 32 * j * V::kN));
+          float x[V::kN];
+          V::open(row.own[j], x);
+          V::scale(x, by, V::load(wgt + kG * j * V::kN));
           put(c, x);
         } else {
-#pragma unroll
-          for (int k = 0; k < V::kN; ++k) r[k] = x[k];
+          turned = row.own[j];
         }
       }
+      uint4 with = turned;
       if (!kInter) {
-#pragma unroll
-        for (int k = 0; k < V::kN; ++k) y[k] = __shfl_sync(0xffffffffu, r[k], partner);
+        with.x = __shfl_sync(0xffffffffu, turned.x, partner, kG);
+        with.y = __shfl_sync(0xffffffffu, turned.y, partner, kG);
+        with.z = __shfl_sync(0xffffffffu, turned.z, partner, kG);
+        with.w = __shfl_sync(0xffffffffu, turned.w, partner, kG);
       }
-      if (rope >= 0) {
-        turn.turn(r, y);
-        put(p.L + rope, r);
+      if (rope >= 0 && mine) {
+        float x[V::kN], y[V::kN];
+        V::open(turned, x);
+        V::open(with, y);
+        turn.turn(x, y);
+        put(p.L + rope, x);
       }
     }
     if (!kLoop) break;
@@ -511,7 +531,7 @@ __device__ __forceinline__ void ds_mla_rows(const RowPart& p, const Angles& ang,
 
 // Blocks [0, q_blocks) take query heads, the others cache rows.
 template <typename T, int kFmt, int kG, int kW, bool kInter>
-__global__ void __launch_bounds__(kThreads, kW == 0 ? kRowBlocks : kHeadBlocks) norm_rope_kernel(const QueryPart q, const RowPart r, const Angles ang, float eps,
+__global__ void __launch_bounds__(kThreads, kW == 0 ? (kG == 16 ? kHalfBlocks : kRowBlocks) : kHeadBlocks) norm_rope_kernel(const QueryPart q, const RowPart r, const Angles ang, float eps,
                                                                 int q_blocks) {
   pdl_enter();
   if constexpr (kW > 0) {
@@ -520,8 +540,11 @@ __global__ void __launch_bounds__(kThreads, kW == 0 ? kRowBlocks : kHeadBlocks) 
       return;
     }
   }
-  const int64_t first = (int64_t)(blockIdx.x - q_blocks) * (kThreads / 32) + (threadIdx.x >> 5);
-  cache_rows<T, kFmt, sizeof(T) == 4 ? 5 : 3, kInter, kW == 0>(r, ang, eps, first, (int64_t)(gridDim.x - q_blocks) * (kThreads / 32));   // 640 or 768 columns
+  // rows alone: kG lanes a row; beside heads a warp
+  constexpr int kLanes = kW == 0 ? kG : 32, kRows = kThreads / kLanes;
+  const int64_t first = (int64_t)(blockIdx.x - q_blocks) * kRows + threadIdx.x / kLanes;
+  cache_rows<T, kFmt, kLanes, kLanes == 16 || sizeof(T) == 4 ? 5 : 3, kInter, kW == 0>(   // 640 or 768 columns
+      r, ang, eps, first, (int64_t)(gridDim.x - q_blocks) * kRows);
 }
 
 template <typename T, bool kInter>
@@ -631,16 +654,25 @@ bool in_words(const QueryPart& q, const RowPart& r, int fmt, const Angles& a) {
   return true;
 }
 
-// Blocks for `tokens` rows, eight warps each: no more than run at once.
-unsigned row_blocks(int64_t tokens, int blocks_per_sm) {
-  return (unsigned)std::min<int64_t>((tokens + 7) / 8, (int64_t)blocks_per_sm * device_sm_count());
+// Blocks for `tokens` rows, `rows` at a time in each: no more than run at once.
+unsigned row_blocks(int64_t tokens, int rows, int per_sm) {
+  return (unsigned)std::min<int64_t>((tokens + rows - 1) / rows, (int64_t)per_sm * device_sm_count());
 }
 
 template <typename T, int kFmt, bool kInter>
 cudaError_t launch_words(QueryPart q, const RowPart& r, const Angles& ang, float eps, cudaStream_t st) {
   constexpr int per = Word<T>::kN;
-  const unsigned r_blocks = q.tokens == 0 ? row_blocks(r.tokens, kRowBlocks) : (unsigned)((r.tokens + 7) / 8);
-  if (q.tokens == 0) return launch_k(norm_rope_kernel<T, kFmt, 32, 0, kInter>, r_blocks, kThreads, 0, st, q, r, ang, eps, 0);
+  if (q.tokens == 0) {
+    // Half a warp a row where five words a lane hold it and there are more rows than half warps: a row's sum, factor
+    // and places are worked out for two at once, and no third of the lanes idles (bf16, us: 40000 rows
+    // e4m3 33.6 with a warp a row, 28.6 with half; plain 28.4, 24.1; 2500 rows e4m3 3.8, 3.9, plain 3.0, 3.3).
+    if constexpr (per == 8) {
+      if (r.E <= 5 * 16 * per && ang.R <= 16 * per && r.tokens > 16 * kHalfBlocks * device_sm_count())
+        return launch_k(norm_rope_kernel<T, kFmt, 16, 0, kInter>, row_blocks(r.tokens, 16, kHalfBlocks), kThreads, 0, st, q, r, ang, eps, 0);
+    }
+    return launch_k(norm_rope_kernel<T, kFmt, 32, 0, kInter>, row_blocks(r.tokens, 8, kRowBlocks), kThreads, 0, st, q, r, ang, eps, 0);
+  }
+  const unsigned r_blocks = (unsigned)((r.tokens + 7) / 8);
   if constexpr (kFmt == kPlain) {
     // the fewest lanes that hold a head in four words each, the rope in one; and no more words than it takes
     const int words = (q.W - q.first) / per, rope = ang.R / per;
@@ -678,14 +710,14 @@ cudaError_t launch_ds_mla(const RowPart& r, const Angles& ang, float eps, cudaSt
   const int vec = aligned16(r.kv) && r.k_s0 % per == 0 && aligned16(r.weight);
   const int wide = reinterpret_cast<uintptr_t>(r.kv) % 32 == 0 && r.k_s0 % (2 * per) == 0;
   return launch_k(ang.interleaved ? norm_rope_ds_mla_kernel<T, true> : norm_rope_ds_mla_kernel<T, false>,
-                  row_blocks(r.tokens, kRowBlocks), kThreads, 0, st, r, ang, eps, vec, wide);
+                  row_blocks(r.tokens, 8, kRowBlocks), kThreads, 0, st, r, ang, eps, vec, wide);
 }
 
 }  // namespace
 
 cudaError_t launch_norm_rope(mla_dtype dt, const NormRopeCall& c, cudaStream_t st) {
   QueryPart q{};
-  RowPart r{nullptr, 0, nullptr, nullptr, 0, 0, 0, PageOf(1), 0, 0, nullptr, 0, nullptr};
+  RowPart r{nullptr, 0, nullptr, nullptr, 0, 0, 0, PageOf(1), 0, 0, nullptr, 0, nullptr, 0};
   Angles ang{c.positions, c.cos_sin, c.cos_sin_stride, c.num_positions, c.R, c.interleaved,
              aligned16(c.cos_sin) && c.cos_sin_stride % 4 == 0 && c.R % 8 == 0};
   if (c.tokens > 0 && c.H > 0) {
@@ -699,7 +731,8 @@ cudaError_t launch_norm_rope(mla_dtype dt, const NormRopeCall& c, cudaStream_t s
   }
   if (c.rows) {
     r = RowPart{c.kv.data, c.kv.s0, c.kv_weight, c.cache.data, c.cache.s0, c.cache.s1, c.cache.n0 * c.cache.n1,
-                PageOf((int32_t)c.cache.n1), c.L, c.L + c.R, c.slots, c.tokens, c.scale};
+                PageOf((int32_t)c.cache.n1), c.L, c.L + c.R, c.slots, c.tokens, c.scale, 0};
+    r.eights = (reinterpret_cast<uintptr_t>(r.cache) | r.c_blk | r.c_row) % 8 == 0;
   }
   if (q.tokens == 0 && r.tokens == 0) return cudaSuccess;
   const bool f32 = dt == MLA_F32;
