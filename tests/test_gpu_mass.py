@@ -207,3 +207,29 @@ def test_more_rows_than_masses(mla, dtype):
     with pytest.raises(mla.MlaError):
         mla.mla_device_error()
     assert torch.equal(got, whole[:, :200])
+
+
+@pytest.mark.parametrize("dtype,page,pad", [(F32, 64, 0), (BF16, 48, 0), (F32, 16, 1), (BF16, 5, 4)])
+@pytest.mark.parametrize("heads,width", [(16, 576), (20, 100), (64, 330), (128, 576), (7, 33)])
+@pytest.mark.parametrize("prefill", [False, True])
+def test_wide_tiles_on_the_cuda_cores(mla, dtype, page, pad, heads, width, prefill):
+    # enough rows for tiles of 128, with 16 to 128 queries each; widths that end inside a step or a word, rows that
+    # are not 16-byte aligned
+    r = torch.Generator().manual_seed(heads + page)
+    kv = [0, 1, 127, 128, 129] + [int(x) for x in torch.randint(0, 600, (40,), generator=r)]
+    q = [min(n + 1, 1 + i % 3) for i, n in enumerate(kv)] if prefill else None
+    c = Case(heads + width, dtype, heads, width, page, kv, q, pad=pad)
+    got = c.run(mla, 0.5)
+    c.check(got, 0.5)
+    assert torch.equal(got, c.run(mla, 0.5))
+    mla.mla_device_error()
+
+
+@pytest.mark.parametrize("dtype,heads", [(F32, 16), (F32, 128), (BF16, 130)])
+@pytest.mark.parametrize("kv,q", [([700], [300]), ([130, 0, 400, 65], [130, 2, 37, 1]), ([5000, 3], [20, 3])])
+def test_queries_over_the_blocks_of_a_cluster(mla, dtype, heads, kv, q):
+    c = Case(heads, dtype, heads, 192, 64, kv, q, tail=1)
+    got = c.run(mla, 0.5)
+    c.check(got, 0.5)
+    assert torch.equal(got, c.run(mla, 0.5))
+    mla.mla_device_error()
