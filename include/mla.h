@@ -490,6 +490,8 @@ mla_status mla_norm_rope_q_cache_write(mla_dtype dtype, mla_tensor q_nope_out, m
  *   The tensor cores take bf16 with E a multiple of 64 up to 576, up to 128 heads, pages of 8, 16 or
  *   32 rows or a multiple of 64, and q_cat and cache with 16-byte aligned data and strides that are
  *   multiples of 8 elements; any other call runs on the CUDA cores.
+ *   The lse of a windowed call does not fit: it leaves out rows that are weighed here. Quantised
+ *   caches are not taken: read their rows back (mla_cache_read_fp8, mla_cache_read_ds_mla).
  *   workspace (prefill): at least mla_prefill_mass_workspace_size() bytes, 256-byte aligned,
  *   caller-owned, not used by concurrent calls. */
 mla_status mla_decode_mass(mla_dtype dtype, float* mass, int64_t mass_stride, int32_t mass_rows,

@@ -510,8 +510,15 @@ __device__ __forceinline__ void ds_mla_rows(const RowPart& p, const Angles& ang,
 #pragma unroll
       for (int m = 1; m < 32; m <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
       const float by = norm_factor(sum, kDsMlaLatent, 1.f / kDsMlaLatent, eps);
+      const uint64_t by2 = pair(by, by);
 #pragma unroll
-      for (int k = 0; k < 16; ++k) x[k] = x[k] * by * w[k];
+      for (int k = 0; k < 16; k += 2) {
+        uint64_t v = pair(x[k], x[k + 1]);
+        asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(v), "l"(by2));
+        asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(v), "l"(pair(w[k], w[k + 1])));
+        x[k] = __uint_as_float((uint32_t)v);
+        x[k + 1] = __uint_as_float((uint32_t)(v >> 32));
+      }
       uint32_t codes[4];
       const float scale = quantise_group(x, codes);
       uint8_t* const o = static_cast<uint8_t*>(p.cache) + off;
