@@ -311,3 +311,38 @@ def test_many_rows_one_behind_the_other(mla):
         for i in range(0, 9001, 1500):                # few enough for a warp each
             call(one, kv[i:i + 1500], w, pos[i:i + 1500], cs, slots[i:i + 1500], *more, eps=EPS)
         assert torch.equal(cache, one)
+
+
+@pytest.mark.parametrize("form", ["", "_fp8"])
+@pytest.mark.parametrize("interleaved", [True, False])
+@pytest.mark.parametrize("rope,latent,pad", [(64, 512, 0), (64, 512, 4), (0, 640, 0), (128, 512, 0), (256, 16, 0), (64, 264, 0), (16, 8, 0), (64, 640, 0)])
+def test_many_rows_side_by_side(mla, form, interleaved, rope, latent, pad):
+    # two rows a warp: rows that are padding, lie outside the cache or have no angles beside rows that are written,
+    # entries of 4-byte alignment (pad), and the same bits as in calls of few rows
+    T = 7001
+    _, kv, _, w, pos, cs = inputs(23, T, (1, 8, rope, latent), BF16)
+    slots = slots_of(4, T, 7200)
+    slots[7::10] = 7200 + 5
+    if rope:
+        pos[3::11], pos[9::17] = POSITIONS, -1
+    kind = torch.uint8 if form else BF16
+    step = pad if form else 2 * pad
+    whole, other = (torch.full((72, 100, latent + rope + step), 7, dtype=kind, device="cuda") for _ in range(2))
+    cache, one = whole[..., :latent + rope], other[..., :latent + rope]
+    more = [torch.tensor([0.01], device="cuda")] if form else []
+    call = getattr(mla, "mla_norm_rope_cache_write" + form)
+    kv, w, pos, cs, slots = kv.cuda(), w.cuda(), pos.cuda(), cs.cuda(), slots.cuda()
+    call(cache, kv, w, pos, cs, slots, *more, eps=EPS, interleaved=interleaved)
+    with pytest.raises(mla.MlaError):
+        mla.mla_device_error()
+    for i in range(0, T, 1000):
+        call(one, kv[i:i + 1000], w, pos[i:i + 1000], cs, slots[i:i + 1000], *more, eps=EPS, interleaved=interleaved)
+    with pytest.raises(mla.MlaError):
+        mla.mla_device_error()
+    assert torch.equal(whole, other)
+    fine = (slots >= 0) & (slots < 7200) & (((pos >= 0) & (pos < POSITIONS)) | (rope == 0))
+    written = torch.zeros(7200, dtype=torch.bool, device="cuda")
+    written[slots[fine]] = True
+    flat = whole.view(7200, -1)
+    assert (flat[~written] == 7).all() and (flat[:, latent + rope:] == 7).all()
+    assert (flat[written] != 7).any(1).all()
