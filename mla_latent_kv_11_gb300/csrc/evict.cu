@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kMaxSelectThreads) evict_select_kernel(const S
       key[i] = t >= lo && t < hi ? key_of(val[i]) : 0u;
     }
   };
-  if constexpr (kClusters) {                                  // no block writes to another that is not there yet
+  if constexpr (kClusters) {                         // no block writes to another that is not there yet
     for (int i = tid; i < kBins; i += threads) sums[0][i] = 0;
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   }
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kMaxSelectThreads) evict_select_kernel(const S
       }
       __syncthreads();
       int* const sum = kClusters ? sums[shift == 10] : hist;
-      if constexpr (kClusters) {                              // most bins are empty
+      if constexpr (kClusters) {                     // most bins are empty
         for (int i = tid; i < kBins; i += threads) {
           const int v = i < bins ? hist[i] : 0;
           for (int r = 0; v != 0 && r < blocks; ++r) add_rank(sum + i, r, v);
@@ -290,6 +290,7 @@ struct MoveArgs {
   void* cache;
   int64_t s_blk, s_row;                              // in words
   int32_t num_blocks, words;                         // words of a row
+  int32_t blocks;                                    // of a slice
   PageOf page_of;
   const int32_t *table, *table_out;
   int64_t bt_stride, bto_stride;
@@ -319,8 +320,9 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const MoveArgs
   extern __shared__ __align__(16) unsigned char smem[];
   W (*const buf)[kInStep][kWords][kMoveThreads] = reinterpret_cast<W (*)[kInStep][kWords][kMoveThreads]>(smem);
   // this thread's words are `word` and, where the row has it, the one 2^kShift behind
-  const int b = blockIdx.z, tid = threadIdx.x, word = ((int)blockIdx.y * kWords << kShift) + (tid & ((1 << kShift) - 1));
-  const int sub = (kClusters ? blockIdx.x * kStep : 0) + (tid >> kShift), step = kClusters ? gridDim.x * kStep : kStep;
+  const int blocks = kClusters ? a.blocks : 1, slice = blockIdx.x / blocks, rank = blockIdx.x - slice * blocks;
+  const int b = blockIdx.y, tid = threadIdx.x, word = (slice * kWords << kShift) + (tid & ((1 << kShift) - 1));
+  const int sub = rank * kStep + (tid >> kShift), step = blocks * kStep;
   const int2 m = a.moved[b];
   const int32_t* const list = a.list + (int64_t)b * a.list_stride;
   const int32_t *const table = a.table + b * a.bt_stride, *const table_out = a.table_out + b * a.bto_stride;
@@ -404,13 +406,14 @@ cudaError_t launch_move(MoveArgs a, int64_t row_bytes, int32_t batch, int32_t ro
   const int64_t sms = device_sm_count(), wide = (int64_t)slices(2) * batch;
   int blocks = 1;
   while (blocks < kMaxCluster && 2 * blocks * wide <= 2 * sms && blocks * (kMoveThreads >> 2) * kInStep * 2 < rows) blocks *= 2;
+  a.blocks = blocks;
   constexpr int kBytes = kStages * kInStep * kWords * kMoveThreads * (int)sizeof(W);
   auto go = [&](auto kernel, int shift) {
     if (kBytes > 48 * 1024) {
       const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
       if (e != cudaSuccess) return e;
     }
-    return launch_clusters(kernel, blocks, dim3(blocks, slices(shift), batch), kMoveThreads, kBytes, st, a);
+    return launch_clusters(kernel, blocks, dim3((unsigned)blocks * slices(shift), batch), kMoveThreads, kBytes, st, a);
   };
   const int shift = 2 * blocks * wide >= sms ? 2 : 2 * blocks * slices(1) * batch >= sms ? 1 : 0;
   if (blocks == 1) {
@@ -449,7 +452,7 @@ cudaError_t launch_evict(const EvictCall& c, void* ws, cudaStream_t st) {
       blocks *= 2;
   const cudaError_t e = launch_clusters(blocks > 1 ? evict_select_kernel<true> : evict_select_kernel<false>, blocks, dim3(blocks, c.batch), threads, 0, st, s);
   if (e != cudaSuccess) return e;
-  const MoveArgs m{c.cache, c.s_blk, c.s_row, c.num_blocks, 0, PageOf(c.page), c.block_table, c.block_table_out, c.bt_stride,
+  const MoveArgs m{c.cache, c.s_blk, c.s_row, c.num_blocks, 0, 1, PageOf(c.page), c.block_table, c.block_table_out, c.bt_stride,
                    c.bto_stride, c.max_blocks_out, list, list_stride, moved};
   const int64_t all = (int64_t)reinterpret_cast<uintptr_t>(c.cache) | c.s_blk | c.s_row | c.row_bytes;
   if (all % 16 == 0) return launch_move<uint4>(m, c.row_bytes, c.batch, list_stride, st);

@@ -229,3 +229,8 @@ def test_several_blocks_a_slice(mla):
     for lens in ([5000], [4000, 3000], [2500] * 3 + [17], [1500, 2600] * 4 + [900]):
         for dtype, width in ((torch.bfloat16, 576), (torch.float32, 576), (torch.uint8, 656)):
             run(mla, Case(len(lens) + width, lens, 64, width, dtype), 1300, 4, 64)
+
+
+def test_very_wide_rows(mla):
+    # more slices of columns than a grid has rows
+    run(mla, Case(31, [5, 9], 2, 300001, torch.uint8), 4, 1, 1)
