@@ -234,3 +234,37 @@ def test_several_blocks_a_slice(mla):
 def test_very_wide_rows(mla):
     # more slices of columns than a grid has rows
     run(mla, Case(31, [5, 9], 2, 300001, torch.uint8), 4, 1, 1)
+
+
+@pytest.mark.parametrize("several", [False, True])
+def test_clusters_captured_with_lengths_in_place(mla, several):
+    # one long sequence beside short ones, captured once and replayed twice: the second replay finds nothing to drop
+    lens = [20000, 3, 0, 12000] if several else [20000]
+    c = Case(41, lens, 64, 64, torch.bfloat16)
+    mass, table = c.mass.cuda(), torch.from_numpy(c.table).cuda()
+    budget, n = 5000, torch.tensor(lens, dtype=torch.int32, device="cuda")
+    kept = torch.full((len(lens), budget), 5, dtype=torch.int32, device="cuda")
+    want = c.want(budget, 4, 64, c.mass.clone(), kept.cpu().clone())
+    before = c.whole.clone(), c.mass.clone(), n.clone()
+    ws = torch.empty(mla.mla_cache_evict_workspace_size(len(lens), mass.shape[1], budget), dtype=torch.uint8, device="cuda")
+
+    def call():
+        mla.mla_cache_evict(c.cache, mass, table, n, budget, n, sinks=4, recent=64, block_table_out=table, kept_out=kept, workspace=ws)
+
+    call()
+    torch.cuda.synchronize()
+    c.whole.copy_(before[0])
+    mass.copy_(before[1])
+    n.copy_(before[2])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert n.tolist() == want[2] and torch.equal(kept.cpu(), want[3])
+    assert torch.equal(bits(mass), bits(want[1])) and torch.equal(bits(c.whole), bits(want[0]))
+    graph.replay()
+    mla.mla_device_error()
+    assert n.tolist() == want[2]
+    assert torch.equal(kept.cpu(), torch.where(torch.arange(budget) < torch.tensor(want[2])[:, None], torch.arange(budget), -1).int())
+    assert torch.equal(bits(mass), bits(want[1])) and torch.equal(bits(c.whole), bits(want[0]))
