@@ -65,7 +65,7 @@ constexpr int kEpiWarp0 = 4, kEpiBar = 1;
 template <bool kPrefill>
 constexpr int kEpiThreads = kPrefill ? 256 : 128;
 template <bool kPrefill>
-constexpr int kThreads = 128 + kEpiThreads<kPrefill>;
+constexpr int kThreads = 128 + kEpiThreads<kPrefill> + (kPrefill ? 0 : 64);   // a decode's: two more warps that load
 // registers of a thread of a prefill: at launch (what 384 threads may have), of the first four warps, of the others
 constexpr int kLaunchRegs = 168, kRoleRegs = 72, kEpiRegs = 216;
 static_assert(kRoleRegs * 128 + kEpiRegs * 256 <= kLaunchRegs * 384, "the shares draw on the launch's registers");
@@ -549,7 +549,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kPrefill>, 
   Seg sg;
 
   // (a prefill's registers move by whole warpgroups: warps 0 to 3 give, 4 to 11 take)
-  if (warp >= kEpiWarp0) {
+  if (warp >= kEpiWarp0 && (kPrefill || warp < 8)) {
     if constexpr (kPrefill) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
     // ------------------------------------------------------------ weights and sums: a thread a cache row (two in a
     // prefill, half of the columns each)
@@ -676,10 +676,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kPrefill>, 
     if (!ok || !mine) give_up();
   } else {
     if constexpr (kPrefill) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRoleRegs));
-    if (warp == 0 || warp == 3) {
+    if (warp == 0 || warp == 3 || (!kPrefill && warp != 1)) {
       // ------------------------------------------------------------ loads, in both CTAs: warp 0 the ring,
-      // warp 3 the resident operand; keys are looked up by lanes, one a box
-      const bool ring_role = warp == 0;
+      // warp 3 the resident operand; keys are looked up by lanes, one a box. A warp hands over a box every 50 to 70
+      // ns, so four warps (2 is free behind the allocation) share a decode's ring, every fourth box each (pages of 16 rows, 64 sequences of 1K-16K: 134 us
+      // with one, 115 with two, 111 with four; of 8 rows 200, 149, 120; of 64, two boxes a tile, 106 to 109 with each)
+      const bool ring_role = warp != 3;
       const int rows_box = min(a.m.page, 64), boxes = kCtaRows / rows_box;
       bool ok = true;
       auto wait = [&](uint64_t* bar, int parity) { ok = ok && __all_sync(0xffffffffu, wait_for(bar, parity, abort)); };
@@ -697,10 +699,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kPrefill>, 
         }
       };
       auto load_keys = [&](unsigned char* dst, uint64_t* bar, int c, int id, int row) {
-        // each lane its own box: handed to one lane, boxes of 16 rows took the 64-sequence decode 170 us, not 134
-        if (lane < boxes) load_pair_3d_lane(dst + lane * rows_box * 128, &kmap, map_to_rank(bar, 0), 64 * c, row, id);
+        // each lane its own: handed to one lane, boxes of 16 rows took 170 us
+        if (lane < boxes && (kPrefill || (lane & 3) == (warp < 8 ? warp >> 1 : warp - 6))) load_pair_3d_lane(dst + lane * rows_box * 128, &kmap, map_to_rank(bar, 0), 64 * c, row, id);
         __syncwarp();
-        if (rank == 0) expect_bytes(bar, 2 * kChunkBytes);
+        if (rank == 0 && (kPrefill || warp == 0)) expect_bytes(bar, 2 * kChunkBytes);
       };
       auto load_queries = [&](unsigned char* dst, uint64_t* bar, int c, int h0, int tok) {
         load_pair_3d(dst, &qmap, map_to_rank(bar, 0), 64 * c, h0, tok);
