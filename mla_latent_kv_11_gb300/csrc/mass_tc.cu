@@ -676,13 +676,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kPrefill>, 
     if (!ok || !mine) give_up();
   } else {
     if constexpr (kPrefill) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRoleRegs));
-    if (warp == 0 || warp == 3 || (!kPrefill && warp != 1)) {
+    // a tile's boxes of keys in a CTA. A decode's loaders are warps 0, 2 (free behind the allocation), 8 and 9, as far
+    // as there is a box for each: one without would hold up nobody, could fall two rounds of the ring behind and then
+    // wait for a phase that is over.
+    const int rows_box = min(a.m.page, 64), boxes = kCtaRows / rows_box, loader = warp < 8 ? warp >> 1 : warp - 6;
+    if (kPrefill ? warp == 0 || warp == 3 : warp == 3 || (warp != 1 && loader < boxes)) {
       // ------------------------------------------------------------ loads, in both CTAs: warp 0 the ring,
       // warp 3 the resident operand; keys are looked up by lanes, one a box. A warp hands over a box every 50 to 70
-      // ns, so four warps (2 is free behind the allocation) share a decode's ring, every fourth box each (pages of 16 rows, 64 sequences of 1K-16K: 134 us
-      // with one, 115 with two, 111 with four; of 8 rows 200, 149, 120; of 64, two boxes a tile, 106 to 109 with each)
+      // ns, so up to four warps share a decode's ring (64 sequences of 1K-16K, pages of 16 rows: 134 us with one, 115 with
+      // two, 111 with four; of 8 rows 200, 149, 120; of 64 rows 106 to 109 with each).
       const bool ring_role = warp != 3;
-      const int rows_box = min(a.m.page, 64), boxes = kCtaRows / rows_box;
       bool ok = true;
       auto wait = [&](uint64_t* bar, int parity) { ok = ok && __all_sync(0xffffffffu, wait_for(bar, parity, abort)); };
       // this lane's box of the CTA's rows of tile k: its block (outside the cache: none, loads zeros) and row
@@ -700,7 +703,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kPrefill>, 
       };
       auto load_keys = [&](unsigned char* dst, uint64_t* bar, int c, int id, int row) {
         // each lane its own: handed to one lane, boxes of 16 rows took 170 us
-        if (lane < boxes && (kPrefill || (lane & 3) == (warp < 8 ? warp >> 1 : warp - 6))) load_pair_3d_lane(dst + lane * rows_box * 128, &kmap, map_to_rank(bar, 0), 64 * c, row, id);
+        if (lane < boxes && (kPrefill || (lane & 3) == loader))
+          load_pair_3d_lane(dst + lane * rows_box * 128, &kmap, map_to_rank(bar, 0), 64 * c, row, id);
         __syncwarp();
         if (rank == 0 && (kPrefill || warp == 0)) expect_bytes(bar, 2 * kChunkBytes);
       };
