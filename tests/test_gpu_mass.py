@@ -233,3 +233,19 @@ def test_queries_over_the_blocks_of_a_cluster(mla, dtype, heads, kv, q):
     c.check(got, 0.5)
     assert torch.equal(got, c.run(mla, 0.5))
     mla.mla_device_error()
+
+
+@pytest.mark.parametrize("batch", [385, 900])
+@pytest.mark.parametrize("prefill", [False, True])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_far_more_sequences_than_a_block_has_threads(mla, batch, prefill, dtype):
+    r = torch.Generator().manual_seed(batch)
+    kv = [int(x) for x in torch.randint(0, 300, (batch,), generator=r)]
+    kv[:330] = [n if i % 3 == 0 else 0 for i, n in enumerate(kv[:330])]   # long runs of sequences without rows
+    kv[40:200] = [0] * 160
+    q = [min(n, i % 5) for i, n in enumerate(kv)] if prefill else None
+    c = Case(batch, dtype, 16, 128, 64, kv, q)
+    got = c.run(mla, 0.5)
+    c.check(got, 0.5)
+    assert torch.equal(got, c.run(mla, 0.5))
+    mla.mla_device_error()
