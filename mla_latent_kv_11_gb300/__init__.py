@@ -15,6 +15,11 @@ import os
 import struct
 from typing import Optional
 
+try:
+    import torch   # once: an import statement in each helper took a call of several tensors 1 us of 12
+except ImportError:   # (the build needs none)
+    torch = None
+
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmla.so")
 
@@ -126,7 +131,6 @@ def _check(status: int) -> None:
 
 
 def _dtype_code(*tensors) -> int:
-    import torch
     dt = None
     for t in tensors:
         if t is None:
@@ -153,7 +157,6 @@ def as_mla_tensor(t) -> MlaTensor:
 
 
 def _stream(stream) -> Optional[int]:
-    import torch
     if stream is None:
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
@@ -179,7 +182,6 @@ def mla_concat_q(q_cat_out, nope, rope, stream=None) -> None:
 
 def mla_cache_write(cache, kv_c, k_pe, slot_mapping, stream=None) -> None:
     """Step 3: cache[s // page, s % page, :] = [kv_c[i] | k_pe[i]] for s = slot_mapping[i] >= 0."""
-    import torch
     if slot_mapping.dtype != torch.int64:
         raise MlaError(MLA_ERR_INVALID_ARG, "slot_mapping must be int64")
     if slot_mapping.numel() and not slot_mapping.is_contiguous():
@@ -191,14 +193,12 @@ def mla_cache_write(cache, kv_c, k_pe, slot_mapping, stream=None) -> None:
 
 def _fp8_cache(cache):
     """An e4m3 cache: torch.float8_e4m3fn or uint8 storage of the codes, whose strides count bytes either way."""
-    import torch
     if cache.dtype == torch.uint8 or cache.dtype == getattr(torch, "float8_e4m3fn", None):
         return cache
     raise MlaError(MLA_ERR_INVALID_ARG, "an fp8 cache must be float8_e4m3fn or uint8 codes")
 
 
 def _f32_scalar(t, name):
-    import torch
     if t is None:
         return None
     if t.dtype != torch.float32 or t.numel() != 1 or not t.is_cuda:
@@ -208,7 +208,6 @@ def _f32_scalar(t, name):
 
 def mla_cache_write_fp8(cache, kv_c, k_pe, slot_mapping, scale, stream=None) -> None:
     """Step 3 into an e4m3 cache: row s = e4m3([kv_c[i] | k_pe[i]] / scale) for s = slot_mapping[i] >= 0."""
-    import torch
     if slot_mapping.dtype != torch.int64:
         raise MlaError(MLA_ERR_INVALID_ARG, "slot_mapping must be int64")
     if slot_mapping.numel() and not slot_mapping.is_contiguous():
@@ -224,7 +223,6 @@ def mla_cache_write_fp8(cache, kv_c, k_pe, slot_mapping, scale, stream=None) -> 
 def mla_concat_q_cache_write(q_cat_out, nope, rope, cache, kv_c, k_pe, slot_mapping, stream=None) -> None:
     """Steps 2 and 3 in one launch: mla_concat_q(q_cat_out, nope, rope) and
     mla_cache_write(cache, kv_c, k_pe, slot_mapping)."""
-    import torch
     if slot_mapping.dtype != torch.int64:
         raise MlaError(MLA_ERR_INVALID_ARG, "slot_mapping must be int64")
     if slot_mapping.numel() and not slot_mapping.is_contiguous():
@@ -239,7 +237,6 @@ def mla_absorb_concat_cache_write(q_cat, q_nope, w_uk, q_pe, cache, kv_c, k_pe, 
     """Steps 1 to 3 in one call: mla_absorb_q into q_cat's first L columns (q_nope [H,T,P],
     w_uk [H,P,L]), then the rope columns of q_cat and the cache write of the new rows, the
     copies running alongside the absorb."""
-    import torch
     if slot_mapping.dtype != torch.int64:
         raise MlaError(MLA_ERR_INVALID_ARG, "slot_mapping must be int64")
     if slot_mapping.numel() and not slot_mapping.is_contiguous():
@@ -256,7 +253,6 @@ def mla_decode_workspace_size(batch: int, num_heads: int, kv_lora_rank: int, num
 
 
 def _check_int32_table(block_table, seq_lens):
-    import torch
     if block_table.dtype != torch.int32 or seq_lens.dtype != torch.int32:
         raise MlaError(MLA_ERR_INVALID_ARG, "block_table and sequence lengths must be int32")
     if block_table.dim() != 2 or block_table.stride(1) != 1:
@@ -269,7 +265,6 @@ def mla_decode(o_lat_out, q_cat, cache, block_table, seq_lens, kv_lora_rank: int
                softmax_scale: float, lse_out=None, num_splits: int = 0, workspace=None,
                stream=None) -> None:
     """Step 4: split-KV paged decode; o_lat_out [B,H,L], optional lse_out float32 [B,H]."""
-    import torch
     _check_int32_table(block_table, seq_lens)
     if lse_out is not None and (lse_out.dtype != torch.float32 or not lse_out.is_contiguous()):
         raise MlaError(MLA_ERR_INVALID_ARG, "lse_out must be contiguous float32")
@@ -289,7 +284,6 @@ def mla_decode_fp8(o_lat_out, q_cat, cache, block_table, seq_lens, kv_lora_rank:
                    softmax_scale: float, descale_q=None, descale_k=None, lse_out=None, num_splits: int = 0,
                    workspace=None, stream=None) -> None:
     """Step 4 over an e4m3 cache: mla_decode with cache values = code * descale_k and q * descale_q."""
-    import torch
     _check_int32_table(block_table, seq_lens)
     if lse_out is not None and (lse_out.dtype != torch.float32 or not lse_out.is_contiguous()):
         raise MlaError(MLA_ERR_INVALID_ARG, "lse_out must be contiguous float32")
@@ -317,7 +311,6 @@ def mla_decode_sparse_fp8(o_lat_out, q_cat, cache, indices, softmax_scale: float
     """Sparse top-k decode over an fp8 ds_mla cache: query b attends the slots indices[b]
     (int32 [B, topk] or [B, 1, topk], -1 = padding) of a uint8 [num_blocks, page, 656]
     (or [num_blocks, page, 1, 656]) cache; o_lat_out [B,H,512], q_cat [B,H,576]."""
-    import torch
     if cache.dtype != torch.uint8:
         raise MlaError(MLA_ERR_INVALID_ARG, "a ds_mla cache is uint8 bytes")
     if cache.dim() == 4 and cache.shape[2] == 1:
@@ -347,7 +340,6 @@ def mla_decode_v_up(out, q_cat, cache, block_table, seq_lens, kv_lora_rank: int,
                     softmax_scale: float, w_uv, lse_out=None, num_splits: int = 0, workspace=None,
                     stream=None) -> None:
     """Steps 4 and 5 as one call: out[b,h,:] = decode(q_cat)[b,h,:] @ w_uv[h]; out [B,H,V], w_uv [H,L,V]."""
-    import torch
     _check_int32_table(block_table, seq_lens)
     if lse_out is not None and (lse_out.dtype != torch.float32 or not lse_out.is_contiguous()):
         raise MlaError(MLA_ERR_INVALID_ARG, "lse_out must be contiguous float32")
@@ -370,7 +362,6 @@ def mla_prefill(o_lat_out, q_cat, cache, block_table, cu_seqlens_q, seq_lens_kv,
                 kv_lora_rank: int, rope_dim: int, softmax_scale: float, lse_out=None, workspace=None,
                 stream=None) -> None:
     """Step 4 (prefill): causal attention of many queries per sequence over the paged cache."""
-    import torch
     _check_int32_table(block_table, seq_lens_kv)
     if cu_seqlens_q.dtype != torch.int32 or not cu_seqlens_q.is_contiguous():
         raise MlaError(MLA_ERR_INVALID_ARG, "cu_seqlens_q must be contiguous int32")
@@ -399,7 +390,6 @@ def mla_decode_noalloc(o_lat_out, q_cat, cache, block_table, seq_lens, kv_lora_r
     """mla_decode for callers that cannot allocate device memory: no workspace, the
     scratch is a fixed array inside the library (shared by all calls; do not overlap
     calls on the GPU)."""
-    import torch
     _check_int32_table(block_table, seq_lens)
     if lse_out is not None and (lse_out.dtype != torch.float32 or not lse_out.is_contiguous()):
         raise MlaError(MLA_ERR_INVALID_ARG, "lse_out must be contiguous float32")
@@ -412,7 +402,6 @@ def mla_decode_noalloc(o_lat_out, q_cat, cache, block_table, seq_lens, kv_lora_r
 
 def _check_device(*tensors) -> int:
     """Every tensor on one CUDA device, and that the current one: the library launches there. Its index."""
-    import torch
     device = tensors[0].get_device()
     for t in tensors:
         if t is not None and (t.get_device() != device or device < 0):
@@ -426,7 +415,6 @@ def _check_device(*tensors) -> int:
 def _stream_on(stream, device: int) -> Optional[int]:
     """The stream a call runs on; without one, the device's current stream (asked for directly where torch
     allows it: the stream object costs more than the rest of a small call)."""
-    import torch
     if stream is not None:
         return _stream(stream)
     direct = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -434,7 +422,6 @@ def _stream_on(stream, device: int) -> Optional[int]:
 
 
 def _check_slots(slot_mapping) -> None:
-    import torch
     if slot_mapping.dtype != torch.int64 or slot_mapping.dim() != 1:
         raise MlaError(MLA_ERR_INVALID_ARG, "slot_mapping must be int64 [T]")
     if slot_mapping.numel() and not slot_mapping.is_contiguous():
@@ -442,13 +429,11 @@ def _check_slots(slot_mapping) -> None:
 
 
 def _check_counts(t, n: int, name: str) -> None:
-    import torch
     if t.dtype != torch.int32 or t.dim() != 1 or t.numel() != n or not t.is_contiguous():
         raise MlaError(MLA_ERR_INVALID_ARG, f"{name} must be contiguous int32 [{n}]")
 
 
 def _check_table(block_table, batch: int) -> None:
-    import torch
     shape = block_table.shape
     if block_table.dtype != torch.int32 or len(shape) != 2 or shape[0] != batch:
         raise MlaError(MLA_ERR_INVALID_ARG, f"block_table must be int32 [{batch}, max_blocks]")
@@ -476,7 +461,6 @@ def _rows_and_heads(q_cat):
 
 
 def _check_lse(lse_out, q_cat) -> None:
-    import torch
     if lse_out is None:
         return
     shape, rows = lse_out.shape, q_cat.shape
@@ -488,7 +472,6 @@ def _check_lse(lse_out, q_cat) -> None:
 def _scratch(need: int, device: int, stream):
     """A workspace allocated on the stream the call runs on, so that its memory is reused only behind
     the call's work."""
-    import torch
     if stream is None:
         return torch.empty(need, dtype=torch.uint8, device=f"cuda:{device}")
     with torch.cuda.stream(torch.cuda.ExternalStream(_stream(stream), device=device)):
@@ -502,7 +485,6 @@ def _workspace_args(workspace):
 
 
 def _ds_mla_cache(cache):
-    import torch
     if cache.dtype != torch.uint8:
         raise MlaError(MLA_ERR_INVALID_ARG, "a ds_mla cache is uint8 bytes")
     return cache[:, :, 0] if cache.dim() == 4 and cache.shape[2] == 1 else cache
@@ -605,7 +587,6 @@ def mla_prefill_window(o_lat_out, q_cat, cache, block_table, cu_seqlens_q, seq_l
 
 def _angle_args(positions, cos_sin, tokens: int, eps: float):
     """eps, positions, table, its row stride, its rows."""
-    import torch
     if positions.dtype != torch.int64 or positions.dim() != 1 or positions.numel() != tokens or not positions.is_contiguous():
         raise MlaError(MLA_ERR_INVALID_ARG, f"positions must be contiguous int64 [{tokens}]")
     shape = cos_sin.shape
@@ -695,7 +676,6 @@ def mla_norm_rope_q_cache_write(q_nope_out, q_pe_out, q, q_weight, cache, kv, kv
 
 
 def _check_mass(mass, batch: int, name: str = "mass") -> None:
-    import torch
     shape = mass.shape
     if mass.dtype != torch.float32 or len(shape) != 2 or shape[0] != batch or (mass.stride(1) != 1 and mass.numel()):
         raise MlaError(MLA_ERR_INVALID_ARG, f"{name} must be float32 [{batch}, rows] with unit row stride")
@@ -750,7 +730,6 @@ def mla_cache_evict(cache, mass, block_table, seq_lens, budget: int, seq_lens_ou
     become rows 0, 1, .. in their order, in their pages or in those of block_table_out; masses move along (mass_out, or
     in place), seq_lens_out int32 [B] gets the lengths, kept_out int32 [B, budget] the old rows (-1 behind the last).
     cache: a plain, an e4m3 or a ds_mla cache."""
-    import torch
     batch = seq_lens.numel()
     if cache.dim() == 4 and cache.shape[2] == 1:
         cache = cache[:, :, 0]
