@@ -432,7 +432,8 @@ size_t mla_prefill_window_workspace_size(int32_t tokens, int32_t batch, int32_t 
  *   table [num_positions, R] with row stride cos_sin_stride, positions device int64 [T]. R is even;
  *   with R = 0 both may be NULL.
  *   Sums (of squares among them), norms and rotations are float32; a value is rounded once, as it
- *   is stored. A token whose position lies outside the table leaves its outputs and its row as
+ *   is stored. A sum of squares beyond float32 is infinite: its finite columns become 0, infinite
+ *   ones NaN. A token whose position lies outside the table leaves its outputs and its row as
  *   they were and is reported by mla_device_error (MLA_ERR_DEVICE_DATA). Slots, padding and
  *   out-of-range slots: as mla_cache_write; a padding token's queries are computed all the same. */
 mla_status mla_norm_rope_q(mla_dtype dtype, mla_tensor q_nope_out, mla_tensor q_pe_out, mla_tensor q,

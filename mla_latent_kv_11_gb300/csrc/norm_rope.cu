@@ -205,10 +205,12 @@ __device__ __forceinline__ int64_t row_offset(const RowPart& p, int64_t s, int l
 
 // 1 / sqrt(sum / n + eps), inv = 1 / n: a quotient and a root each mended by a step with its remainder (a division,
 // a root and another division took a head a fifth of its instructions). It enters every value of the row, and a
-// quantised value next to the middle of two codes tells its last bit.
+// quantised value next to the middle of two codes tells its last bit. A sum beyond float32 is infinite, and its factor 0:
+// it leaves no remainder to mend the quotient with (infinity minus infinity).
 __device__ __forceinline__ float norm_factor(float sum, float n, float inv, float eps) {
   float v = sum * inv;
-  v = fmaf(fmaf(-v, n, sum), inv, v) + eps;
+  if (v <= FLT_MAX) v = fmaf(fmaf(-v, n, sum), inv, v);
+  v += eps;
   const float y = rsqrtf(v);
   const float p = v * y, low = fmaf(v, y, -p);               // v y = p + low
   const float t = fmaf(-low, y, fmaf(-p, y, 1.f));           // 1 - v y^2

@@ -346,3 +346,69 @@ def test_many_rows_side_by_side(mla, form, interleaved, rope, latent, pad):
     flat = whole.view(7200, -1)
     assert (flat[~written] == 7).all() and (flat[:, latent + rope:] == 7).all()
     assert (flat[written] != 7).any(1).all()
+
+
+BIG = [1e20, float("inf"), float("-inf"), float("nan")]
+
+
+def by_nothing(x):
+    """A row's values by the factor 0 of a sum of squares beyond float32 (of NaN: NaN)."""
+    x = x.double().cpu()
+    return x * float("nan") if torch.isnan(x).any() else x * 0.0
+
+
+def same(a, b):
+    return torch.equal(torch.nan_to_num(a.double().cpu(), nan=7e77), torch.nan_to_num(b.double().cpu(), nan=7e77))
+
+
+@pytest.mark.parametrize("big", BIG)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("dims,offset", [(LITE, 0), (NOPE, 0), ((4, 448, 64, 512), 0), ((2, 960, 64, 512), 0), (ODD, 0), (LITE, 1)])
+@pytest.mark.parametrize("interleaved", [True, False])
+def test_heads_whose_squares_overflow(mla, big, dtype, dims, offset, interleaved):
+    # the factor is 0: finite columns become 0, an infinite one NaN; the heads beside it do not change
+    heads, nope, rope, latent = dims
+    q, _, w, _, pos, cs = inputs(11, 5, dims, dtype)
+    loud = q.clone()
+    loud[1, 1, 3], loud[3, 0, nope + rope - 1] = big, big
+    got = []
+    for x in (q, loud):
+        n, r = (torch.full((5, heads, c), 7.0, dtype=dtype, device="cuda") for c in (nope, rope))
+        mla.mla_norm_rope_q(n, r, gpu(x, offset), w.cuda(), pos.cuda(), cs.cuda(), eps=EPS, interleaved=interleaved)
+        got.append(torch.cat([n, r], 2).cpu())
+    mla.mla_device_error()
+    for t, h in ((1, 1), (3, 0)):
+        x = by_nothing(loud[t, h])
+        pe = ref.rotated(x[None, nope:], cs[pos[t]][None], interleaved, 0.0)[0][0]
+        assert same(got[1][t, h], torch.cat([x[:nope], pe]))
+        got[1][t, h] = got[0][t, h]
+    assert torch.equal(*got)
+
+
+@pytest.mark.parametrize("big", BIG)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("form", ["", "_fp8", "_ds_mla"])
+@pytest.mark.parametrize("tokens,offset", [(6, 0), (6, 1), (7001, 0)])
+def test_rows_whose_squares_overflow(mla, big, dtype, form, tokens, offset):
+    _, kv, _, w, pos, cs = inputs(12, tokens, LITE, dtype)
+    loud = kv.clone()
+    rows = (2, 5)
+    loud[rows[0], 7], loud[rows[1], 511] = big, big
+    more = [torch.tensor([0.01], device="cuda")] if form == "_fp8" else []
+    got = []
+    for x in (kv, loud):
+        cache = torch.zeros(1, tokens, 656 if form == "_ds_mla" else 576, dtype=torch.uint8 if form else dtype, device="cuda")
+        getattr(mla, "mla_norm_rope_cache_write" + form)(cache, gpu(x, offset), w.cuda(), pos.cuda(), cs.cuda(),
+                                                         torch.arange(tokens, device="cuda"), *more, eps=EPS)
+        got.append(cache[0].cpu())
+    mla.mla_device_error()
+    for t in rows:
+        latents = got[1][t, :512]
+        if form:
+            latents = latents.view(ref.E4M3)
+        assert same(latents.float(), by_nothing(loud[t, :512]))
+        if form == "_ds_mla":       # groups of zeros (a NaN does not count)
+            assert (got[1][t, 512:528].view(F32) == 2.0 ** -126).all()
+            got[1][t, :528] = got[0][t, :528]
+        got[1][t, :512] = got[0][t, :512]
+    assert torch.equal(*got)
