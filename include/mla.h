@@ -483,7 +483,7 @@ mla_status mla_norm_rope_q_cache_write(mla_dtype dtype, mla_tensor q_nope_out, m
  *   (decay 1 sums up; decay 0 never reads what was there). A decode's query attends every row, a
  *   prefill's the rows up to its own position, as in mla_prefill. Sums are float32 and their order
  *   does not change from run to run on a device. A query whose lse is -inf (it attended
- *   nothing) gives nothing. Masses behind a sequence's rows, and those of sequences without a query
+ *   nothing) gives nothing, whatever it holds. Masses behind a sequence's rows, and those of sequences without a query
  *   or without rows, are left as they were; so are masses of rows whose block id lies outside the
  *   cache, and of sequences whose cu_seqlens_q decrease or leave [0, T], which mla_device_error
  *   reports (MLA_ERR_DEVICE_DATA), as it does a length beyond the table or mass_rows (which counts

@@ -41,11 +41,13 @@
 // Every wait is bounded; one that gives up winds both CTAs down and is reported.
 #include <cuda.h>
 #include <cuda_bf16.h>
-#include <math_constants.h>
 
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
+#include <limits>
 #include <mutex>
+#include <type_traits>
 #include <vector>
 
 #include "mass.cuh"
@@ -94,6 +96,7 @@ struct Shared {
   Place found;
   long long wide[12];
   float neg_lse[2][256];     // -lse * log2(e) of a tile's columns, in turn in two places
+  int none[2];               // the tile (of this CTA's, in order) whose columns those are, if one of them is without a query
 };
 static_assert(sizeof(Shared) <= kMiscBytes, "barrier block overflows its slot");
 
@@ -440,11 +443,21 @@ __device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
   return d;
 }
 
-// e^(scale s - lse) summed over columns [lo, hi) of 32 scores.
+// A column's -lse log2(e) where its query attended nothing (lse -inf). No other column has it: one of a finite lse is
+// cut to the largest float32, whose weight is infinite all the same.
+constexpr float kNoQuery = std::numeric_limits<float>::infinity();
+__device__ __forceinline__ float neg_lse_of(float lse) {
+  const float v = -lse * kLog2e;
+  return v > FLT_MAX && lse != -kNoQuery ? FLT_MAX : v;
+}
+
+// e^(scale s - lse) summed over columns [lo, hi) of 32 scores. kSome: columns without a query among them. (With their
+// choice in the ordinary sum too, a prefill's tiles took 2 to 7% longer.)
+template <bool kSome>
 __device__ __forceinline__ float sum_weights(const float (&v)[32], const float* neg_lse, float scale_log2, int lo, int hi) {
   const uint64_t by = pair_f32(scale_log2, scale_log2);
   uint64_t sum[2] = {0, 0};
-  if (__all_sync(0xffffffffu, lo <= 0 && hi >= 32)) {
+  if (!kSome && __all_sync(0xffffffffu, lo <= 0 && hi >= 32)) {
 #pragma unroll
     for (int k = 0; k < 32; k += 4) {
       const float4 l = *reinterpret_cast<const float4*>(neg_lse + k);
@@ -455,10 +468,11 @@ __device__ __forceinline__ float sum_weights(const float (&v)[32], const float* 
     }
   } else {
 #pragma unroll
-    for (int k = 0; k < 32; k += 2) {   // a column outside may hold anything: chosen, not multiplied, away
-      const uint64_t x = fma_pair(pair_f32(v[k], v[k + 1]), by, pair_f32(neg_lse[k], neg_lse[k + 1]));
-      const float e0 = k >= lo && k < hi ? ex2_approx(low(x)) : 0.f, e1 = k + 1 >= lo && k + 1 < hi ? ex2_approx(high(x)) : 0.f;
-      sum[(k >> 1) & 1] = add_pair(sum[(k >> 1) & 1], pair_f32(e0, e1));
+    for (int k = 0; k < 32; k += 2) {   // a column that does not count may hold anything: chosen, not multiplied, away
+      const float l0 = neg_lse[k], l1 = neg_lse[k + 1];
+      const uint64_t x = fma_pair(pair_f32(v[k], v[k + 1]), by, pair_f32(l0, l1));
+      const bool c0 = k >= lo && k < hi && (!kSome || l0 != kNoQuery), c1 = k + 1 >= lo && k + 1 < hi && (!kSome || l1 != kNoQuery);
+      sum[(k >> 1) & 1] = add_pair(sum[(k >> 1) & 1], pair_f32(c0 ? ex2_approx(low(x)) : 0.f, c1 ? ex2_approx(high(x)) : 0.f));
     }
   }
   const uint64_t all = add_pair(sum[0], sum[1]);
@@ -522,6 +536,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kPrefill>, 
     }
     mbar_init(&sh.fin, 1);
     sh.abort_flag = 0;
+    sh.none[0] = sh.none[1] = -1;
     fence_mbar_init();
   }
   if (warp == 2) alloc_pair(&sh.tmem_base, 512);
@@ -558,8 +573,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kPrefill>, 
     const float scale_log2 = a.m.scale * kLog2e;
     const bool two = a.chunks > 1;
     const uint32_t d_empty = map_to_rank(&sh.d_empty[0], 0);
-    // -lse log2(e) of head h of token tok; a query that attended nothing (lse -inf) gives e^-inf
-    auto neg_lse = [&](float lse) { return lse == -CUDART_INF_F ? lse : -lse * kLog2e; };
+    volatile int* const none = sh.none;   // written before a tile's barrier and read behind it, as -lse
     bool ok = true, mine = true;   // ok: the group's decision; mine: this thread's waits so far
     int x = 0, place = 0;
     int4 ending = make_int4(-1, 0, 0, 0), beginning = ending;   // this unit's pieces of rows that are cut
@@ -577,7 +591,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kPrefill>, 
         return a.m.mass + wk.b * a.m.mass_stride + t;
       };
       if (!kPrefill) {
-        sh.neg_lse[place][e] = e < a.m.H ? neg_lse(a.m.lse[(int64_t)wk.t.s.q0 * a.m.H + e]) : 0.f;
+        const float mark = e < a.m.H ? neg_lse_of(a.m.lse[(int64_t)wk.t.s.q0 * a.m.H + e]) : 0.f;
+        const int tag = x;
+        sh.neg_lse[place][e] = mark;
+        if (mark == kNoQuery) none[place] = tag;
         for (int i = sg.i0; i < sg.i1; ++i, ++x) {
           const int buf = x & 1;
           float* const to = row_mass(row_of(i));
@@ -586,6 +603,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kPrefill>, 
           ok = named_bar_and(kEpiBar, kEpiThreads<kPrefill>, mine);
           if (!ok) break;
           tc_fence_after();
+          const bool some = none[place] == tag;
           float sum = 0.f;
 #pragma unroll 1
           for (int c = 0; c < a.m.H; c += 32) {
@@ -594,7 +612,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kPrefill>, 
             tmem_ld_wait();
             loaded(v);
             if (two) add_second(tmem + lane_addr + 256 * buf + kSecond<kPrefill> + c, v);
-            sum += sum_weights(v, &sh.neg_lse[place][c], scale_log2, 0, a.m.H - c);
+            const float* const l = &sh.neg_lse[place][c];
+            sum += some ? sum_weights<true>(v, l, scale_log2, 0, a.m.H - c) : sum_weights<false>(v, l, scale_log2, 0, a.m.H - c);
           }
           tc_fence_before();
           __syncwarp();
@@ -616,7 +635,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kPrefill>, 
         ask(sg.i0);
         float sum = 0.f;
         for (int i = sg.i0; i < sg.i1; ++i, ++x, place ^= 1) {
-          sh.neg_lse[place][et] = neg_lse(l);
+          const float mark = neg_lse_of(l);
+          sh.neg_lse[place][et] = mark;
+          if (mark == kNoQuery) none[place] = x;
           if (i + 1 < sg.i1) ask(i + 1);   // used a tile later
           mine = mine && wait_for(&sh.d_full[0], x & 1, abort);
           ok = named_bar_and(kEpiBar, kEpiThreads<kPrefill>, mine);
@@ -648,10 +669,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<kPrefill>, 
             __syncwarp();
             if (lane == 0) mbar_arrive_smem_released(d_empty + 8);
           }
+          auto add = [&](auto some) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (counts(c))
-              sum += sum_weights(v[c], &sh.neg_lse[place][128 * half + 32 * c], scale_log2, seen - 32 * c, there - 32 * c);
+            for (int c = 0; c < 4; ++c)
+              if (counts(c))
+                sum += sum_weights<decltype(some)::value>(v[c], &sh.neg_lse[place][128 * half + 32 * c], scale_log2,
+                                                          seen - 32 * c, there - 32 * c);
+          };
+          if (none[place] != x)
+            add(std::false_type{});
+          else
+            add(std::true_type{});
         }
         if (!ok) break;
         // the row's two sums, by way of the place that the next tile's -lse take: its thread there is the one that

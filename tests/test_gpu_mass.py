@@ -249,3 +249,45 @@ def test_far_more_sequences_than_a_block_has_threads(mla, batch, prefill, dtype)
     c.check(got, 0.5)
     assert torch.equal(got, c.run(mla, 0.5))
     mla.mla_device_error()
+
+
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("dtype,heads,page", [(BF16, 16, 64), (BF16, 128, 64), (BF16, 70, 16), (F32, 16, 64), (BF16, 16, 5)])
+@pytest.mark.parametrize("kv,q", [([300, 90], None), ([300, 90], [5, 6]), ([700, 40], [300, 64]), ([9000], [40])])
+def test_whatever_a_query_without_attention_holds(mla, value, dtype, heads, page, kv, q):
+    # lse -inf: a padded query, say, of values that nobody wrote; on the tensor cores and on the CUDA cores
+    c = Case(53, dtype, heads, 576, page, kv, q)
+    r = torch.Generator().manual_seed(heads)
+    off = (torch.rand(c.tokens, heads, generator=r) < 0.3).cuda()
+    off[-1, :] = True
+    c.lse[off] = -math.inf
+    want = c.want(0.5)
+    zeros, poisoned = c.q.clone(), c.q.clone()
+    zeros[off] = 0
+    poisoned[off] = value
+    c.q = zeros
+    clean = c.run(mla, 0.5)
+    c.q = poisoned
+    got = c.run(mla, 0.5)
+    mla.mla_device_error()
+    assert torch.equal(got, clean)
+    off = (got.double() - want[0]).abs() - want[1]
+    assert not torch.isnan(off).any() and off.max() <= 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("prefill", [False, True])
+def test_log_sum_exps_of_any_size(mla, dtype, prefill):
+    # weights beyond float32 are infinite, those of +inf nothing, of NaN NaN: each for the rows that its query attends
+    for lse, want in ((-3e38, math.inf), (-1e30, math.inf), (3e38, 0.0), (math.inf, 0.0), (math.nan, math.nan)):
+        c = Case(59, dtype, 16, 576, 64, [300, 90], [5, 6] if prefill else None)
+        clean = c.run(mla, 0.0)
+        c.lse[1 if not prefill else 7, 3] = lse     # in sequence 1: its only query, or the third of six
+        got = c.run(mla, 0.0)
+        n = 90 if not prefill else 87
+        assert torch.equal(got[0], clean[0]) and torch.equal(got[1, n:], clean[1, n:])
+        seen = got[1, :n]
+        if want == 0.0:
+            assert torch.isfinite(seen).all() and (seen <= clean[1, :n]).all()
+        else:
+            assert (torch.isnan(seen) if math.isnan(want) else torch.isinf(seen)).all()
