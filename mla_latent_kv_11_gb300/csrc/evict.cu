@@ -343,14 +343,14 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const MoveArgs
       const int j = j0 + sub + u * kRows, t = next[u];
       to[u] = -1;
       if (t < 0) continue;
-      const int pf = a.page_of(t), pt = a.page_of(j);
-      const int bf = table[pf], bt = pt < a.max_blocks_out ? table_out[pt] : -1;
+      const int pf = a.page_of(t), pt = a.page_of(j), rf = t - pf * a.page_of.page;
+      const bool there = pt < a.max_blocks_out;
+      const int bf = table[pf], bt = there ? table_out[pt] : -1;
+      if (there && bf == bt && rf == j - pt * a.page_of.page) continue;   // it stays where it is, whatever the id
       if (bf < 0 || bf >= a.num_blocks || bt < 0 || bt >= a.num_blocks) {
         atomicOr(&g_evict_err, kErrDeviceData);
         continue;
       }
-      const int rf = t - pf * a.page_of.page;
-      if (bf == bt && rf == j - pt * a.page_of.page) continue;
       to[u] = bt;
       const W* const from = cache + bf * a.s_blk + rf * a.s_row;
 #pragma unroll

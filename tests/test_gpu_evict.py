@@ -268,3 +268,26 @@ def test_clusters_captured_with_lengths_in_place(mla, several):
     assert n.tolist() == want[2]
     assert torch.equal(kept.cpu(), torch.where(torch.arange(budget) < torch.tensor(want[2])[:, None], torch.arange(budget), -1).int())
     assert torch.equal(bits(mass), bits(want[1])) and torch.equal(bits(c.whole), bits(want[0]))
+
+
+@pytest.mark.parametrize("bad", [-1, 10 ** 6])
+def test_rows_that_do_not_move_need_no_block(mla, bad):
+    # a copy of the table as block_table_out: rows whose place does not change are not looked at, as in place
+    c = Case(61, [200, 90, 130], 16, 64, torch.bfloat16, other=False)
+    c.mass[:, :40] = 1e6                      # the first pages' rows stay where they are
+    want = c.want(100, 0, 4, c.mass.clone(), torch.zeros(3, 100, dtype=torch.int32))
+    c.table[:, :2] = bad                      # 32 rows without blocks; of sequence 1 (90 rows) every row stays in place
+    c.table[1] = bad
+    for copy in (False, True):
+        table = torch.from_numpy(c.table).cuda()
+        whole, mass = c.whole.clone(), c.mass.cuda()
+        n = torch.tensor(c.lens, dtype=torch.int32, device="cuda")
+        mla.mla_cache_evict(whole[:, 0], mass, table, n, 100, n, recent=4, block_table_out=table.clone() if copy else None)
+        mla.mla_device_error()
+        assert n.tolist() == want[2] and torch.equal(mass.cpu(), want[1]) and torch.equal(bits(whole), bits(want[0]))
+    # a row whose new page lies outside the new table is one that cannot move
+    short = table[:, :4].clone()
+    mla.mla_cache_evict(c.whole[:, 0], c.mass.cuda(), table, torch.tensor(c.lens, dtype=torch.int32, device="cuda"), 100,
+                        torch.zeros(3, dtype=torch.int32, device="cuda"), recent=4, block_table_out=short)
+    with pytest.raises(mla.MlaError):
+        mla.mla_device_error()
