@@ -460,13 +460,12 @@ def _rows_and_heads(q_cat):
     return shape[0], shape[1]
 
 
-def _check_lse(lse_out, q_cat) -> None:
-    if lse_out is None:
+def _check_lse(lse, q_cat, name: str = "lse_out") -> None:
+    if lse is None:
         return
-    shape, rows = lse_out.shape, q_cat.shape
-    if (lse_out.dtype != torch.float32 or not lse_out.is_contiguous() or len(shape) != 2 or shape[0] != rows[0] or
-            shape[1] != rows[1]):
-        raise MlaError(MLA_ERR_INVALID_ARG, "lse_out must be contiguous float32 with q_cat's rows and heads")
+    shape, rows = lse.shape, q_cat.shape
+    if lse.dtype != torch.float32 or not lse.is_contiguous() or len(shape) != 2 or shape[0] != rows[0] or shape[1] != rows[1]:
+        raise MlaError(MLA_ERR_INVALID_ARG, f"{name} must be contiguous float32 with q_cat's rows and heads")
 
 
 def _scratch(need: int, device: int, stream):
@@ -689,7 +688,7 @@ def mla_decode_mass(mass, q_cat, cache, block_table, seq_lens, lse, softmax_scal
     _check_table(block_table, B)
     _check_counts(seq_lens, B, "seq_lens")
     _check_mass(mass, B)
-    _check_lse(lse, q_cat)
+    _check_lse(lse, q_cat, "lse")
     device = _check_device(mass, q_cat, cache, block_table, seq_lens, lse)
     _check(lib().mla_decode_mass(_dtype_code(q_cat, cache), _ptr(mass), _table_stride(mass), mass.shape[1],
                                  as_mla_tensor(q_cat), as_mla_tensor(cache), _ptr(block_table), _table_stride(block_table),
@@ -710,7 +709,7 @@ def mla_prefill_mass(mass, q_cat, cache, block_table, cu_seqlens_q, seq_lens_kv,
     _check_counts(seq_lens_kv, batch, "seq_lens_kv")
     _check_counts(cu_seqlens_q, batch + 1, "cu_seqlens_q")
     _check_mass(mass, batch)
-    _check_lse(lse, q_cat)
+    _check_lse(lse, q_cat, "lse")
     device = _check_device(mass, q_cat, cache, block_table, cu_seqlens_q, seq_lens_kv, lse, workspace)
     if workspace is None:
         workspace = _scratch(mla_prefill_mass_workspace_size(), device, stream)

@@ -1,11 +1,16 @@
 """Norms with rotations, row masses and eviction as seen from the host, without a GPU: malformed arguments are rejected
 before anything touches the device."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
 from test_abi import _contig, _view, mla  # noqa: F401  (the module's library fixture)
 from mla_latent_kv_11_gb300 import MlaTensor
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 P = 0x10000
 NONE = MlaTensor()
 
@@ -202,3 +207,14 @@ def test_the_binding_refuses(mla, which):  # noqa: F811
     with pytest.raises(mla.MlaError) as e:
         BAD[which](mla, torch.zeros)
     assert e.value.status == mla.MLA_ERR_INVALID_ARG and "on one CUDA device" not in str(e.value)
+
+
+def test_a_refused_lse_is_named(mla):  # noqa: F811
+    for which in (9 + 1, None):
+        with pytest.raises(mla.MlaError) as e:
+            if which is not None:
+                BAD[which](mla, torch.zeros)
+            else:
+                z, i32 = torch.zeros, dict(dtype=torch.int32)
+                mla.mla_prefill_mass(z(1, 16), z(3, 4, 576), z(2, 8, 576), z(1, 2, **i32), z(2, **i32), z(1, **i32), z(3, 4).double(), 0.1)
+        assert "lse must" in str(e.value)
