@@ -439,6 +439,7 @@ def _check_table(block_table, batch: int) -> None:
         raise MlaError(MLA_ERR_INVALID_ARG, f"block_table must be int32 [{batch}, max_blocks]")
     if block_table.stride(1) != 1 and block_table.numel():
         raise MlaError(MLA_ERR_INVALID_ARG, "block_table must have unit column stride")
+    _check_int32(shape[1], "block_table's width")
 
 
 def _table_stride(block_table) -> int:
@@ -678,6 +679,7 @@ def _check_mass(mass, batch: int, name: str = "mass") -> None:
     shape = mass.shape
     if mass.dtype != torch.float32 or len(shape) != 2 or shape[0] != batch or (mass.stride(1) != 1 and mass.numel()):
         raise MlaError(MLA_ERR_INVALID_ARG, f"{name} must be float32 [{batch}, rows] with unit row stride")
+    _check_int32(shape[1], f"{name}'s width")
 
 
 def mla_decode_mass(mass, q_cat, cache, block_table, seq_lens, lse, softmax_scale: float, decay: float = 1.0,

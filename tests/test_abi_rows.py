@@ -218,3 +218,16 @@ def test_a_refused_lse_is_named(mla):  # noqa: F811
                 z, i32 = torch.zeros, dict(dtype=torch.int32)
                 mla.mla_prefill_mass(z(1, 16), z(3, 4, 576), z(2, 8, 576), z(1, 2, **i32), z(2, **i32), z(1, **i32), z(3, 4).double(), 0.1)
         assert "lse must" in str(e.value)
+
+
+def test_widths_beyond_32_bits_are_refused(mla):  # noqa: F811
+    # passed on they would lose their upper bits: masses of 2^32 + 8 rows would be those of 8
+    z, i32 = torch.zeros, dict(dtype=torch.int32)
+    wide, table = (torch.empty(1, 2 ** 32 + 8, dtype=t, device="meta") for t in (torch.float32, torch.int32))
+    for mass, tab in ((wide, z(1, 2, **i32)), (z(1, 16), table)):
+        for call in (lambda: mla.mla_decode_mass(mass, z(1, 4, 576), z(2, 8, 576), tab, z(1, **i32), z(1, 4), 0.1),
+                     lambda: mla.mla_prefill_mass(mass, z(3, 4, 576), z(2, 8, 576), tab, z(2, **i32), z(1, **i32), z(3, 4), 0.1),
+                     lambda: mla.mla_cache_evict(z(2, 8, 576), mass, tab, z(1, **i32), 4, z(1, **i32))):
+            with pytest.raises(mla.MlaError) as e:
+                call()
+            assert e.value.status == mla.MLA_ERR_INVALID_ARG and "32 bits" in str(e.value)
