@@ -15,10 +15,18 @@ import os
 import struct
 from typing import Optional
 
-try:
-    import torch   # once: an import statement in each helper took a call of several tensors 1 us of 12
-except ImportError:   # (the build needs none)
-    torch = None
+
+class _Torch:
+    """torch until a call first needs it: a build, or a ctypes user of the library, imports none. From then on the name is
+    the module itself (an import statement in each helper took a call of several tensors 1 us of 12)."""
+
+    def __getattr__(self, name):
+        global torch
+        import torch
+        return getattr(torch, name)
+
+
+torch = _Torch()
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmla.so")

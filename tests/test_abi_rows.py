@@ -231,3 +231,13 @@ def test_widths_beyond_32_bits_are_refused(mla):  # noqa: F811
             with pytest.raises(mla.MlaError) as e:
                 call()
             assert e.value.status == mla.MLA_ERR_INVALID_ARG and "32 bits" in str(e.value)
+
+
+def test_importing_the_package_does_not_import_torch():
+    # a build, or a ctypes user of the library, needs none
+    code = ("import sys, mla_latent_kv_11_gb300 as m; assert 'torch' not in sys.modules; "
+            "m.lib(); assert 'torch' not in sys.modules; import torch; "
+            "\ntry: m.mla_norm_rope_q(*[torch.zeros(1, 1, 2)] * 4, torch.zeros(1), torch.zeros(1, 2))"
+            "\nexcept m.MlaError as e: print(e)")
+    got = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert got.returncode == 0 and "positions must be" in got.stdout, got.stderr
