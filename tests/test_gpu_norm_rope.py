@@ -412,3 +412,43 @@ def test_rows_whose_squares_overflow(mla, big, dtype, form, tokens, offset):
             got[1][t, :528] = got[0][t, :528]
         got[1][t, :512] = got[0][t, :512]
     assert torch.equal(*got)
+
+
+# scales of either side of where the quotients' short form ends, and ordinary ones
+QUOTIENTS = [0.0171, 1.0, -0.5, 2.0 ** -60, 1.0001 * 2.0 ** -60, 0.9999 * 2.0 ** 60, 2.0 ** 60, -1.37 * 2.0 ** 59, 1.7 * 2.0 ** -59]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("scale", QUOTIENTS)
+@pytest.mark.parametrize("rows", [300, 6000])
+@pytest.mark.parametrize("rope", [64, 128])
+def test_e4m3_quotients_value_by_value(mla, dtype, scale, rows, rope):
+    # ropes that the kernel of whole words takes, in rows of a warp and of half a warp; at position 0 the rotation leaves
+    # a value as it is where its partner is finite: all of those have mla_cache_write_fp8's codes
+    g = torch.Generator().manual_seed(6)
+    latent = 16
+    s = torch.tensor([scale])
+    x = torch.randn(rows, rope, generator=g) * torch.exp(6 * torch.randn(rows, 1, generator=g)) * abs(scale)
+    x[:20] = (torch.arange(20 * rope).view(20, rope) % 2048 - 1024) / 8 * s              # codes, middles of codes
+    x[20:60] = torch.nextafter(x[:20].repeat(2, 1), torch.tensor([1e38, -1e38])[:, None, None].expand(2, 20, rope).reshape(40, rope))
+    x[60:64] = torch.tensor([0.0, -0.0, 3.3e38, -3.3e38, 1e-45, -1e-45, 2.0 ** -126, 2.0 ** -120]).repeat(4, rope // 8)
+    odd = torch.tensor([float("inf"), -float("inf"), float("nan")])
+    x[64:128:2, 5] = odd.repeat(11)[:32]
+    x[65:128:2, rope // 2 + 8] = odd.repeat(11)[:32]
+    x = x.to(dtype)
+    kv = torch.cat([torch.ones(rows, latent, dtype=dtype), x], 1).cuda()
+    cs = torch.cat([torch.ones(1, rope // 2), torch.zeros(1, rope // 2)], 1).cuda()
+    slots, zero = torch.arange(rows, device="cuda"), torch.zeros(rows, dtype=torch.int64, device="cuda")
+    a, b = (torch.zeros(1, rows, latent + rope, dtype=torch.uint8, device="cuda") for _ in range(2))
+    for interleaved in (False, True):
+        mla.mla_norm_rope_cache_write_fp8(a, kv, torch.ones(latent, dtype=dtype, device="cuda"), zero, cs, slots, s.cuda(),
+                                          interleaved=interleaved)
+        mla.mla_cache_write_fp8(b, kv[:, :latent], kv[:, latent:], slots, s.cuda())
+        mla.mla_device_error()
+        u, v = (t[0, :, latent:].cpu() for t in (a, b))
+        partner = torch.arange(rope) ^ 1 if interleaved else (torch.arange(rope) + rope // 2) % rope
+        fine = torch.isfinite(x)[:, partner]
+        assert fine.sum() == rows * rope - 64 and (~torch.isfinite(x) & fine).sum() == 64
+        # x c - y 0 and y c + x 0 are x and y, but for the sign of a zero; a NaN has either sign
+        low = u & 0x7F
+        assert ((u == v) | (low == (v & 0x7F)) & ((low == 0) | (low == 0x7F)) | ~fine).all()
