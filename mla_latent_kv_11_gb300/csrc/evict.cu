@@ -96,11 +96,12 @@ __device__ __forceinline__ void together() {
     __syncthreads();
 }
 
-// Another block's copy of *p.
+// v added to rank's copy of *p.
 __device__ __forceinline__ void add_rank(int* p, int rank, int v) {
   asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(ptx::map_to_rank(p, rank)), "r"(v) : "memory");
 }
 
+// rank's copy of *p.
 __device__ __forceinline__ int ld_rank(const int* p, int rank) {
   int v;
   asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(ptx::map_to_rank(p, rank)) : "memory");

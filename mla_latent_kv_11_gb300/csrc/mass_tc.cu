@@ -20,7 +20,7 @@
 // Sums. The tensor cores' additions into an accumulator round toward zero, so that a score's error grows with the
 // length of the chain and does not average out over queries: with one accumulator for the 36 steps of a 576-wide
 // row, masses came out 1.4e-6 of themselves too small. So the first half of the chunks goes to one accumulator and
-// the rest to another, which the epilogue adds: 0.65e-6. A decode's two fit into tensor memory twice, so that
+// the rest to another, which the epilogue adds: 0.7e-6. A decode's two fit into tensor memory twice, so that
 // one tile is summed while the next is computed. A prefill's fill it (2 x 256 columns): there the epilogue's eight warps
 // take the first into registers (128 a thread, lent by the other warps) while the second is computed, and the second
 // while the next tile's first is: 6% slower than one accumulator in two places (12% at 32 tokens over 16K rows).
@@ -112,8 +112,8 @@ struct TcArgs {
   int4* piece;               // [unit][2] {sequence (-1: none), tile of 256 rows, whether it is the last piece, rows}
 };
 
-// Sum over i < n of (a i + b) / m, rounded down each: the integer points under a line, counted by Euclid's
-// steps. a, b >= 0, m > 0; a n + b below 2^31.
+// Sum over i < n of (a i + b) / m, rounded down each: the integer points under a line, by the well-known reduction with
+// Euclid's steps (whole parts apart, then axes exchanged). a, b >= 0, m > 0; a n + b below 2^31.
 __device__ long long points_below(int n, int m, int a, int b) {
   long long sum = 0;
   while (n > 0) {
@@ -492,7 +492,8 @@ __device__ __forceinline__ void loaded(float (&w)[32]) {
                  "+f"(w[16]), "+f"(w[17]), "+f"(w[18]), "+f"(w[19]), "+f"(w[20]), "+f"(w[21]), "+f"(w[22]), "+f"(w[23]),
                  "+f"(w[24]), "+f"(w[25]), "+f"(w[26]), "+f"(w[27]), "+f"(w[28]), "+f"(w[29]), "+f"(w[30]), "+f"(w[31]));
 }
-// The second accumulator's 32 columns added to the first's (in halves: 32 more registers would be spilled).
+// The second accumulator's 32 columns added to the first's, in halves: 32 more registers would be spilled. (The prefill spills
+// as it is: 664 bytes of stores, 372 of loads.)
 __device__ __forceinline__ void add_second(uint32_t taddr, float (&v)[32]) {
 #pragma unroll
   for (int h = 0; h < 32; h += 16) {

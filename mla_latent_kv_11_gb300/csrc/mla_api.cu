@@ -939,7 +939,7 @@ mla_status plan_norm_q(const mla_tensor& q_nope_out, const mla_tensor& q_pe_out,
   return MLA_OK;
 }
 
-// The rows' part: `width` is the cache's entry (0: L + R).
+// The rows' part; *R: the width of their rope.
 mla_status plan_norm_rows(const mla_tensor& cache, bool ds_mla, const mla_tensor& kv, const mla_tensor& weight,
                           const int64_t* slot_mapping, int64_t num_tokens, int64_t* R, NormRopeCall* c) {
   if (num_tokens < 0) return fail(MLA_ERR_INVALID_ARG, "num_tokens < 0");

@@ -15,9 +15,11 @@
 // parts share one launch: a decode step has 5 to 500 blocks of work in all.
 //
 // What it measured (device times): 4096 tokens of 128 normed heads of 192 and their rows, bf16: 73 us for 413 MB,
-// 5.6 TB/s, 0.83 of a copy's rate (halves rotated 79 us: a word's partner through eight exchanges); queries without a norm
-// 38 us for 145 MB: a rope's 128 bytes a head are read and written in separate lines. 20011 float32 rows into ds_mla entries
-// 14 us, 4.6 TB/s; 40000 bf16 rows plain 24 us, e4m3 29 (pairs side by side 21 and 23). A step of 64 tokens 3.5 us, of one 2.1.
+// 5.6 TB/s, 0.83 of a copy's rate (halves rotated 79 us: a word's partner through eight exchanges, and registers spilled for
+// them); the same with queries without a norm 38 us for 145 MB, 0.55 of it: a lane has one word of a head in flight and the next
+// one, behind its token's position (loads waited for 8 times an issue, DRAM at 34%). One head a token leaves most of a block
+// idle: 20000 heads of 512 bf16 columns 44 us for 41 MB. 20011 float32 rows into ds_mla entries 14 us, 4.6 TB/s; 40000 bf16
+// rows plain 24 us, e4m3 29 (pairs side by side 21 and 23). A step of 64 tokens 3.5 us, of one 2.1.
 #include <algorithm>
 
 #include "e4m3_codes.cuh"
